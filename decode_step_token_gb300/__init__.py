@@ -1,4 +1,4 @@
-"""GB300-native per-decode-step token sampler.
+"""GB300-native per-decode-step token sampler, with what trains on its tokens.
 
 The sampler itself is the CUDA library ``libsampler.so`` (C ABI in
 ``include/sampler.h``); this package is its thin Python binding. ``Sampler``
@@ -19,14 +19,21 @@ from ._binding import (EXPORTED, SAMPLER_CREATE_HOST_STAGING, SAMPLER_CREATE_SHO
                        load_library, sampler_abi_version, sampler_args_t, sampler_config_t, sampler_create,
                        sampler_destroy, sampler_ext_t, sampler_sample, sampler_sample_host,
                        sampler_sample_ex, sampler_sample_noalloc, sampler_status_string,
-                       sampler_get_stat)
+                       sampler_get_stat, SAMPLER_ERR_BAD_VALUE, sampler_rows_t, sampler_policy_t,
+                       sampler_preference_t, sampler_quantize_t, sampler_scaled_head_t, sampler_score,
+                       sampler_score_grad, sampler_policy_loss, sampler_preference_loss, sampler_quantize_blocks,
+                       sampler_lm_head_scaled, sampler_lm_head_scaled_sample)
 
 __all__ = ["Sampler", "SamplerError", "load_library", "sampler_create", "sampler_sample",
            "sampler_sample_host", "sampler_sample_noalloc", "sampler_sample_ex", "sampler_destroy",
            "sampler_status_string", "SAMPLER_NOALLOC_MAX_ROWS", "SAMPLER_MAX_TOP_N", "SAMPLER_MAX_BIAS",
            "SAMPLER_MAX_STOP", "sampler_ext_t", "sampler_lm_head_t", "sampler_lm_head_sample", "sampler_lm_head",
            "SAMPLER_LM_HEAD_MAX_ROWS", "SAMPLER_STAT_EXACT_ROWS", "SAMPLER_STAT_LM_HEAD_TIMEOUTS",
-           "sampler_abi_version", "sampler_args_t", "sampler_config_t", "EXPORTED"]
+           "sampler_abi_version", "sampler_args_t", "sampler_config_t", "EXPORTED",
+           "SAMPLER_ERR_BAD_VALUE", "sampler_rows_t", "sampler_policy_t", "sampler_preference_t",
+           "sampler_quantize_t", "sampler_scaled_head_t", "sampler_score", "sampler_score_grad",
+           "sampler_policy_loss", "sampler_preference_loss", "sampler_quantize_blocks", "sampler_lm_head_scaled",
+           "sampler_lm_head_scaled_sample"]
 
 
 def _make_ext(top_n: int = 0, unscaled: bool = False, out_token_logprob=None, out_top_ids=None,
@@ -53,6 +60,33 @@ def _ptr(t) -> Optional[int]:
     if hasattr(t, "data_ptr"):
         return t.data_ptr()
     return int(t)
+
+
+def _vector(name: str, t, n: int, dtype, device: int) -> Optional[int]:
+    """Address of a contiguous [n] tensor of the handle's device (None passes)."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector of {n} values, not {tuple(t.shape)}")
+    _on_device(name, t, device)
+    return t.data_ptr()
+
+
+def _matrix(name: str, t, dtypes, device: int) -> int:
+    """Row stride of a [rows, columns] tensor of the handle's device with unit inner stride."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {dtypes}, not {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be two-dimensional with contiguous rows")
+    _on_device(name, t, device)
+    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+
+
+def _on_device(name: str, t, device: int) -> None:
+    if t.device.type != "cuda" or t.device.index != device:
+        raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
 
 
 class Sampler:
@@ -189,6 +223,167 @@ class Sampler:
                              int(vocab if vocab is not None else weight.shape[0]), self._stream(stream))
         if rc != SAMPLER_OK:
             raise SamplerError(rc, "sampler_lm_head")
+
+    def _rows(self, logits, tokens, temperature, weight, out_logprob, out_entropy, out_status, out_grad,
+              vocab: Optional[int]) -> sampler_rows_t:
+        import torch
+
+        stride = _matrix("logits", logits, (torch.bfloat16, torch.float32), self.device)
+        n, V = logits.shape[0], int(vocab if vocab is not None else logits.shape[1])
+        if not 1 <= V <= logits.shape[1]:
+            raise ValueError(f"vocab {V} does not lie within the logits' {logits.shape[1]} columns")
+        grad_stride = 0
+        if out_grad is not None:
+            grad_stride = _matrix("out_grad", out_grad, (logits.dtype,), self.device)
+            if out_grad.shape[0] != n or out_grad.shape[1] < V:
+                raise ValueError(f"out_grad must be [{n}, {V}], not {tuple(out_grad.shape)}")
+        f32 = torch.float32
+        return sampler_rows_t(
+            _ptr(logits), SAMPLER_DTYPE_BF16 if logits.dtype == torch.bfloat16 else SAMPLER_DTYPE_F32, n, V, stride,
+            _vector("tokens", tokens, n, torch.int32, self.device),
+            _vector("temperature", temperature, n, f32, self.device),
+            _vector("weight", weight, n, f32, self.device),
+            _vector("out_logprob", out_logprob, n, f32, self.device),
+            _vector("out_entropy", out_entropy, n, f32, self.device),
+            _vector("out_status", out_status, n, torch.int32, self.device), _ptr(out_grad), grad_stride)
+
+    def _done(self, rc: int, what: str) -> None:
+        if rc != SAMPLER_OK:
+            raise SamplerError(rc, what)
+
+    def score(self, *, logits, tokens, out_logprob=None, out_entropy=None, out_status=None, temperature=None,
+              weight=None, vocab: Optional[int] = None, stream: Optional[int] = None) -> None:
+        """sampler_score: the logprob and the entropy of each row's token (int32
+        tokens [N]; fp32 temperature, weight and outputs [N]; a row of weight 0 is
+        left out)."""
+        rows = self._rows(logits, tokens, temperature, weight, out_logprob, out_entropy, out_status, None, vocab)
+        self._done(sampler_score(self._h, rows, self._stream(stream)), "sampler_score")
+
+    def score_grad(self, *, logits, tokens, grad_logprob, out_grad, grad_entropy=None, out_logprob=None,
+                   out_entropy=None, out_status=None, temperature=None, weight=None, vocab: Optional[int] = None,
+                   stream: Optional[int] = None) -> None:
+        """sampler_score_grad: the logits' gradient of sum(grad_logprob * logprob +
+        grad_entropy * entropy) into out_grad (the logits' type; it may be the logits),
+        with the outputs of ``score``."""
+        import torch
+
+        rows = self._rows(logits, tokens, temperature, weight, out_logprob, out_entropy, out_status, out_grad, vocab)
+        n = rows.n_rows
+        gl = _vector("grad_logprob", grad_logprob, n, torch.float32, self.device)
+        ge = _vector("grad_entropy", grad_entropy, n, torch.float32, self.device)
+        self._done(sampler_score_grad(self._h, rows, gl, ge, self._stream(stream)), "sampler_score_grad")
+
+    def policy_loss(self, *, logits, tokens, old_logprob, advantage, out_loss, ref_logprob=None, temperature=None,
+                    weight=None, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,
+                    entropy_coef: float = 0.0, grad_scale: float = 1.0, grad_scale_dev=None, out_grad=None,
+                    out_logprob=None, out_ratio=None, out_kl=None, out_entropy=None, out_status=None,
+                    vocab: Optional[int] = None, stream: Optional[int] = None) -> None:
+        """sampler_policy_loss: the clipped policy loss with its KL and entropy terms
+        (out_loss: one fp32), and with out_grad the logits' gradient in the same pass."""
+        import torch
+
+        rows = self._rows(logits, tokens, temperature, weight, out_logprob, out_entropy, out_status, out_grad, vocab)
+
+        def v(name, t, n=rows.n_rows):
+            return _vector(name, t, n, torch.float32, self.device)
+
+        q = sampler_policy_t(v("old_logprob", old_logprob), v("advantage", advantage), v("ref_logprob", ref_logprob),
+                             clip_low, clip_high, kl_coef, entropy_coef, grad_scale,
+                             v("grad_scale_dev", grad_scale_dev, 1), v("out_loss", out_loss, 1),
+                             v("out_ratio", out_ratio), v("out_kl", out_kl))
+        self._done(sampler_policy_loss(self._h, rows, q, self._stream(stream)), "sampler_policy_loss")
+
+    def preference_loss(self, *, logits, tokens, seq_offsets, out_loss, ref_logprob=None, temperature=None,
+                        weight=None, beta: float = 0.1, margin: float = 0.0, label_smoothing: float = 0.0,
+                        mean_over_tokens: bool = False, grad_scale: float = 1.0, grad_scale_dev=None, out_grad=None,
+                        out_logprob=None, out_reward=None, out_status=None, vocab: Optional[int] = None,
+                        stream: Optional[int] = None) -> None:
+        """sampler_preference_loss over (len(seq_offsets) - 1) / 2 pairs of answers
+        (int32 seq_offsets; out_loss: one fp32; out_reward: one for each answer), and
+        with out_grad the logits' gradient."""
+        import torch
+
+        rows = self._rows(logits, tokens, temperature, weight, out_logprob, None, out_status, out_grad, vocab)
+        ends = int(seq_offsets.shape[0])
+        if ends % 2 != 1:
+            raise ValueError(f"seq_offsets must have 2 * pairs + 1 entries, not {ends}")
+        n, f32 = rows.n_rows, torch.float32
+        q = sampler_preference_t(_vector("seq_offsets", seq_offsets, ends, torch.int32, self.device), ends // 2,
+                                 _vector("ref_logprob", ref_logprob, n, f32, self.device), beta, margin,
+                                 label_smoothing, 1 if mean_over_tokens else 0, grad_scale,
+                                 _vector("grad_scale_dev", grad_scale_dev, 1, f32, self.device),
+                                 _vector("out_loss", out_loss, 1, f32, self.device),
+                                 _vector("out_reward", out_reward, ends - 1, f32, self.device))
+        self._done(sampler_preference_loss(self._h, rows, q, self._stream(stream)), "sampler_preference_loss")
+
+    def quantize_blocks(self, *, src, out_values, out_scales, block_rows: int = 1,
+                        stream: Optional[int] = None) -> None:
+        """sampler_quantize_blocks: src [rows, cols] (bf16 or fp32) to out_values
+        (float8_e4m3fn, the same shape) with out_scales (fp32, [rows / block_rows,
+        cols / 128] rounded up)."""
+        import torch
+
+        stride = _matrix("src", src, (torch.bfloat16, torch.float32), self.device)
+        rows, cols = src.shape
+        vs = _matrix("out_values", out_values, (torch.float8_e4m3fn, torch.uint8), self.device)
+        ss = _matrix("out_scales", out_scales, (torch.float32,), self.device)
+        if tuple(out_values.shape) != (rows, cols):
+            raise ValueError(f"out_values must be [{rows}, {cols}], not {tuple(out_values.shape)}")
+        if block_rows > 0 and (out_scales.shape[0] < -(-rows // block_rows) or out_scales.shape[1] < -(-cols // 128)):
+            raise ValueError(f"out_scales {tuple(out_scales.shape)} is too small for {rows} x {cols}")
+        q = sampler_quantize_t(_ptr(src), SAMPLER_DTYPE_BF16 if src.dtype == torch.bfloat16 else SAMPLER_DTYPE_F32,
+                               rows, cols, stride, int(block_rows), _ptr(out_values), vs, _ptr(out_scales), ss)
+        self._done(sampler_quantize_blocks(self._h, q, self._stream(stream)), "sampler_quantize_blocks")
+
+    def _scaled_head(self, hidden, hidden_scale, weight, weight_scale) -> sampler_scaled_head_t:
+        import torch
+
+        eight, f32 = (torch.float8_e4m3fn, torch.uint8), (torch.float32,)
+        hs, ws = _matrix("hidden", hidden, eight, self.device), _matrix("weight", weight, eight, self.device)
+        if hidden.shape[1] != weight.shape[1]:
+            raise ValueError(f"hidden has {hidden.shape[1]} columns, weight {weight.shape[1]}")
+        hss = _matrix("hidden_scale", hidden_scale, f32, self.device)
+        wss = _matrix("weight_scale", weight_scale, f32, self.device)
+        groups = -(-hidden.shape[1] // 128)
+        for name, t, n in (("hidden_scale", hidden_scale, hidden.shape[0]),
+                           ("weight_scale", weight_scale, -(-weight.shape[0] // 128))):
+            if t.shape[0] < n or t.shape[1] < groups:
+                raise ValueError(f"{name} must be [{n}, {groups}], not {tuple(t.shape)}")
+        # the stride of a single row is not used, but has to be a legal one
+        if hidden.shape[0] <= 1:
+            hs = -(-hs // 16) * 16
+        if weight.shape[0] <= 1:
+            ws = -(-ws // 16) * 16
+        return sampler_scaled_head_t(_ptr(hidden), _ptr(hidden_scale), _ptr(weight), _ptr(weight_scale),
+                                     hidden.shape[1], hs, ws, hss, wss)
+
+    def lm_head_scaled(self, *, hidden, hidden_scale, weight, weight_scale, logits,
+                       stream: Optional[int] = None) -> None:
+        """sampler_lm_head_scaled: logits [rows, >= vocab] (bf16 or fp32) from e4m3
+        hidden [rows, K] and weight [vocab, K] with their scales as
+        ``quantize_blocks`` makes them (block_rows 1 and 128)."""
+        import torch
+
+        lm = self._scaled_head(hidden, hidden_scale, weight, weight_scale)
+        ldl = _matrix("logits", logits, (torch.bfloat16, torch.float32), self.device)
+        rows, V = hidden.shape[0], weight.shape[0]
+        if logits.shape[0] < rows or logits.shape[1] < V:
+            raise ValueError(f"logits must be [{rows}, {V}], not {tuple(logits.shape)}")
+        dtype = SAMPLER_DTYPE_BF16 if logits.dtype == torch.bfloat16 else SAMPLER_DTYPE_F32
+        self._done(sampler_lm_head_scaled(self._h, lm, _ptr(logits), dtype, ldl, rows, V, self._stream(stream)),
+                   "sampler_lm_head_scaled")
+
+    def lm_head_scaled_sample_args(self, args: sampler_args_t, *, hidden, hidden_scale, weight, weight_scale,
+                                   stream: Optional[int] = None, **ext_kw) -> None:
+        """sampler_lm_head_scaled_sample: the logits of ``lm_head_scaled`` written to
+        args.logits, then the step on them; ext_kw as for sample_ex_args."""
+        lm = self._scaled_head(hidden, hidden_scale, weight, weight_scale)
+        rows = args.n_logit_rows if args.n_logit_rows > 0 else args.n_rows
+        if hidden.shape[0] < rows or weight.shape[0] < args.vocab:
+            raise ValueError(f"hidden and weight must have {rows} and {args.vocab} rows")
+        ext = _make_ext(**ext_kw) if ext_kw else None
+        self._done(sampler_lm_head_scaled_sample(self._h, lm, args, ext, self._stream(stream)),
+                   "sampler_lm_head_scaled_sample")
 
     def _stream(self, stream: Optional[int]) -> int:
         if stream is None:

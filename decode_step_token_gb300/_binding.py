@@ -24,6 +24,7 @@ SAMPLER_ERR_CUDA = -5
 SAMPLER_ERR_NO_DEVICE = -6
 SAMPLER_ERR_NO_STAGING = -7
 SAMPLER_ERR_UNSUPPORTED = -8
+SAMPLER_ERR_BAD_VALUE = -9
 
 SAMPLER_ROW_OK = 0
 SAMPLER_ROW_NONFINITE = 1
@@ -38,7 +39,9 @@ SAMPLER_CREATE_SHORT_WAITS = 4
 
 EXPORTED = ("sampler_create", "sampler_sample", "sampler_sample_host", "sampler_destroy",
             "sampler_status_string", "sampler_abi_version", "sampler_get_stat",
-            "sampler_sample_noalloc", "sampler_sample_ex", "sampler_lm_head_sample", "sampler_lm_head")
+            "sampler_sample_noalloc", "sampler_sample_ex", "sampler_lm_head_sample", "sampler_lm_head",
+            "sampler_score", "sampler_score_grad", "sampler_policy_loss", "sampler_preference_loss",
+            "sampler_quantize_blocks", "sampler_lm_head_scaled", "sampler_lm_head_scaled_sample")
 SAMPLER_STAT_EXACT_ROWS = 0
 SAMPLER_STAT_LM_HEAD_TIMEOUTS = 1
 SAMPLER_LM_HEAD_MAX_ROWS = 256
@@ -121,6 +124,86 @@ class sampler_lm_head_t(ctypes.Structure):
     ]
 
 
+class sampler_rows_t(ctypes.Structure):
+    _fields_ = [
+        ("logits", _P),
+        ("dtype", ctypes.c_int32),
+        ("n_rows", ctypes.c_int64),
+        ("vocab", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+        ("tokens", _P),
+        ("temperature", _P),
+        ("weight", _P),
+        ("out_logprob", _P),
+        ("out_entropy", _P),
+        ("out_status", _P),
+        ("out_grad", _P),
+        ("grad_stride", ctypes.c_int64),
+    ]
+
+
+class sampler_policy_t(ctypes.Structure):
+    _fields_ = [
+        ("old_logprob", _P),
+        ("advantage", _P),
+        ("ref_logprob", _P),
+        ("clip_low", ctypes.c_float),
+        ("clip_high", ctypes.c_float),
+        ("kl_coef", ctypes.c_float),
+        ("entropy_coef", ctypes.c_float),
+        ("grad_scale", ctypes.c_float),
+        ("grad_scale_dev", _P),
+        ("out_loss", _P),
+        ("out_ratio", _P),
+        ("out_kl", _P),
+    ]
+
+
+class sampler_preference_t(ctypes.Structure):
+    _fields_ = [
+        ("seq_offsets", _P),
+        ("n_pairs", ctypes.c_int64),
+        ("ref_logprob", _P),
+        ("beta", ctypes.c_float),
+        ("margin", ctypes.c_float),
+        ("label_smoothing", ctypes.c_float),
+        ("mean_over_tokens", ctypes.c_int32),
+        ("grad_scale", ctypes.c_float),
+        ("grad_scale_dev", _P),
+        ("out_loss", _P),
+        ("out_reward", _P),
+    ]
+
+
+class sampler_quantize_t(ctypes.Structure):
+    _fields_ = [
+        ("src", _P),
+        ("dtype", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("src_stride", ctypes.c_int64),
+        ("block_rows", ctypes.c_int32),
+        ("values", _P),
+        ("values_stride", ctypes.c_int64),
+        ("scales", _P),
+        ("scale_stride", ctypes.c_int64),
+    ]
+
+
+class sampler_scaled_head_t(ctypes.Structure):
+    _fields_ = [
+        ("hidden", _P),
+        ("hidden_scale", _P),
+        ("weight", _P),
+        ("weight_scale", _P),
+        ("hidden_dim", ctypes.c_int64),
+        ("hidden_stride", ctypes.c_int64),
+        ("weight_stride", ctypes.c_int64),
+        ("hidden_scale_stride", ctypes.c_int64),
+        ("weight_scale_stride", ctypes.c_int64),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -157,6 +240,25 @@ def load_library(path: str = LIB):
             lib.sampler_lm_head.argtypes = [_P, ctypes.POINTER(sampler_lm_head_t), _P, ctypes.c_int64,
                                             ctypes.c_int64, ctypes.c_int64, _P]
             lib.sampler_lm_head.restype = ctypes.c_int
+            lib.sampler_score.argtypes = [_P, ctypes.POINTER(sampler_rows_t), _P]
+            lib.sampler_score.restype = ctypes.c_int
+            lib.sampler_score_grad.argtypes = [_P, ctypes.POINTER(sampler_rows_t), _P, _P, _P]
+            lib.sampler_score_grad.restype = ctypes.c_int
+            lib.sampler_policy_loss.argtypes = [_P, ctypes.POINTER(sampler_rows_t),
+                                                ctypes.POINTER(sampler_policy_t), _P]
+            lib.sampler_policy_loss.restype = ctypes.c_int
+            lib.sampler_preference_loss.argtypes = [_P, ctypes.POINTER(sampler_rows_t),
+                                                    ctypes.POINTER(sampler_preference_t), _P]
+            lib.sampler_preference_loss.restype = ctypes.c_int
+            lib.sampler_quantize_blocks.argtypes = [_P, ctypes.POINTER(sampler_quantize_t), _P]
+            lib.sampler_quantize_blocks.restype = ctypes.c_int
+            lib.sampler_lm_head_scaled.argtypes = [_P, ctypes.POINTER(sampler_scaled_head_t), _P, ctypes.c_int32,
+                                                   ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P]
+            lib.sampler_lm_head_scaled.restype = ctypes.c_int
+            lib.sampler_lm_head_scaled_sample.argtypes = [_P, ctypes.POINTER(sampler_scaled_head_t),
+                                                          ctypes.POINTER(sampler_args_t),
+                                                          ctypes.POINTER(sampler_ext_t), _P]
+            lib.sampler_lm_head_scaled_sample.restype = ctypes.c_int
             lib.sampler_abi_version.argtypes = []
             lib.sampler_abi_version.restype = ctypes.c_uint32
             _lib = lib
@@ -215,3 +317,35 @@ def sampler_get_stat(h, which: int, reset: bool = False):
     v = ctypes.c_uint64(0)
     rc = load_library().sampler_get_stat(h, which, ctypes.byref(v), 1 if reset else 0)
     return rc, int(v.value)
+
+
+def sampler_score(h, rows: sampler_rows_t, stream: int) -> int:
+    return load_library().sampler_score(h, ctypes.byref(rows), _P(stream))
+
+
+def sampler_score_grad(h, rows: sampler_rows_t, grad_logprob, grad_entropy, stream: int) -> int:
+    return load_library().sampler_score_grad(h, ctypes.byref(rows), _P(grad_logprob), _P(grad_entropy), _P(stream))
+
+
+def sampler_policy_loss(h, rows: sampler_rows_t, policy: sampler_policy_t, stream: int) -> int:
+    return load_library().sampler_policy_loss(h, ctypes.byref(rows), ctypes.byref(policy), _P(stream))
+
+
+def sampler_preference_loss(h, rows: sampler_rows_t, pref: sampler_preference_t, stream: int) -> int:
+    return load_library().sampler_preference_loss(h, ctypes.byref(rows), ctypes.byref(pref), _P(stream))
+
+
+def sampler_quantize_blocks(h, q: sampler_quantize_t, stream: int) -> int:
+    return load_library().sampler_quantize_blocks(h, ctypes.byref(q), _P(stream))
+
+
+def sampler_lm_head_scaled(h, lm: sampler_scaled_head_t, logits: int, dtype: int, logits_stride: int, rows: int,
+                           vocab: int, stream: int) -> int:
+    return load_library().sampler_lm_head_scaled(h, ctypes.byref(lm), _P(logits), dtype, logits_stride, rows, vocab,
+                                                 _P(stream))
+
+
+def sampler_lm_head_scaled_sample(h, lm: sampler_scaled_head_t, args: sampler_args_t, ext, stream: int) -> int:
+    """ext: a sampler_ext_t or None."""
+    return load_library().sampler_lm_head_scaled_sample(h, ctypes.byref(lm), ctypes.byref(args),
+                                                        ctypes.byref(ext) if ext is not None else None, _P(stream))

@@ -1,8 +1,9 @@
 """Build libsampler.so in-tree with nvcc for sm_103a (GB300).
 
-The library has five translation units (the C ABI's host code, the slice
+The library has nine translation units (the C ABI's host code in two, the slice
 kernel and its variant with the extensions, the fork-group kernel, the LM-head
-GEMM); they compile in parallel and link into one shared object.
+GEMM, its 8-bit counterpart, the block quantiser, scoring and the losses); they
+compile in parallel and link into one shared object.
 """
 from __future__ import annotations
 
@@ -20,7 +21,8 @@ OBJ_DIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [*ARCH, "-lineinfo", "-O3", "-std=c++17", "-Xcompiler", "-fPIC"]
-UNITS = ("sampler_api.cu", "slice_kernel.cu", "slice_kernel_ext.cu", "group_kernel.cu", "lm_head_kernel.cu")
+UNITS = ("sampler_api.cu", "slice_kernel.cu", "slice_kernel_ext.cu", "group_kernel.cu", "lm_head_kernel.cu",
+         "train_api.cu", "row_loss_kernel.cu", "quantize_kernel.cu", "scaled_head_kernel.cu")
 
 
 def sources() -> list:

@@ -104,4 +104,50 @@ int group_prepare(int dtype, bool pen, size_t smem);
 // work: two zeroed counters of the handle (the kernel leaves them zeroed)
 int group_launch(const sampler_args_t* a, const GroupGeometry& g, int clusters, uint32_t* work, cudaStream_t stream);
 
+// ---------------------------------------------------------------- scoring and losses
+// One row's record: its share of the logits' gradient, with u = (x_v - ref) * c
+// d loss / d x_v = 2^u * (k0 + k1 * u) + (v == token ? at_token : 0).
+struct RowRecord {
+    float c;         // log2(e) / T
+    float ref;       // the row's largest logit
+    float k0, k1;
+    float at_token;
+    int32_t token;   // -1: the row is written as zeros (left out)
+    float inv_s, inv_t;  // 1 / the row's sum of exponentials; 1 / T
+};
+constexpr size_t kRowRecordBytes = sizeof(RowRecord);
+
+struct RowWorkspace {
+    RowRecord* records;  // [max_rows]
+    double* terms;       // [max_rows] each row's share of the loss (pairs: its logprob)
+    double* pair_terms;  // [max_rows] each pair's share of the loss
+    uint32_t* ticket;    // blocks that have ended; zero between launches
+};
+
+enum RowMode : int { kModeScore = 0, kModeScoreGrad = 1, kModePolicy = 2, kModePairs = 3 };
+
+struct LossParams {
+    sampler_rows_t rows;
+    int mode;
+    const float* grad_logprob;  // kModeScoreGrad
+    const float* grad_entropy;
+    sampler_policy_t policy;    // kModePolicy
+    RowWorkspace ws;
+};
+
+// Statistics of every row, what the mode makes of them, and (kModeScoreGrad,
+// kModePolicy with out_grad) the logits' gradient.
+int rows_launch(const LossParams& p, int sms, cudaStream_t stream);
+// The pairs' loss from the rows' logprobs, and each row's record for pairs_grad_launch.
+int pairs_launch(const sampler_rows_t& rows, const sampler_preference_t& pref, const RowWorkspace& ws,
+                 cudaStream_t stream);
+int pairs_grad_launch(const sampler_rows_t& rows, const RowWorkspace& ws, int sms, cudaStream_t stream);
+
+// ---------------------------------------------------------------- 8-bit LM head
+int quantize_launch(const sampler_quantize_t& q, int sms, cudaStream_t stream);
+
+// dtype: the logits' type
+int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, int64_t ldl, int64_t rows,
+                       int64_t vocab, int sms, unsigned long long* timeouts, cudaStream_t stream);
+
 }  // namespace dst

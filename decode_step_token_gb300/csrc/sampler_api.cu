@@ -2,7 +2,8 @@
 // argument checks, the choice of kernel, the handle's workspace, the
 // allocation-free entry point, the host-buffer entry that stages through the
 // handle's device buffers, and the LM-head entry. The kernels live in
-// slice_kernel.cu, group_kernel.cu and lm_head_kernel.cu.
+// slice_kernel.cu, group_kernel.cu and lm_head_kernel.cu; scoring, the losses
+// and the 8-bit LM head have their host code in train_api.cu.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -12,8 +13,11 @@
 #include <mutex>
 #include <new>
 
+#include "handle.h"
 #include "launch.h"
 #include "sampler.h"
+
+using dst::DeviceGuard;
 
 namespace {
 
@@ -25,39 +29,7 @@ size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
 
 int kernel_slot(int dtype, bool pen) { return (dtype == SAMPLER_DTYPE_BF16 ? 2 : 0) + (pen ? 1 : 0); }
 
-// Restores the calling thread's current device when it goes out of scope.
-struct DeviceGuard {
-    int prev = -1;
-    DeviceGuard() { cudaGetDevice(&prev); }
-    ~DeviceGuard()
-    {
-        if (prev >= 0) cudaSetDevice(prev);
-    }
-};
-
 }  // namespace
-
-struct sampler_s {
-    int device;
-    int num_sms;
-    int64_t max_rows, max_vocab, max_history;
-    uint32_t flags;
-    uint32_t max_polls;
-    // slice kernel: per-(row, slice) records and per-row arrival counters
-    dst::SliceWorkspace slice_ws;
-    int slice_rows;
-    size_t slice_smem_set[2];  // dynamic shared memory already granted per dtype
-    // fork-group kernel
-    size_t grp_smem_set[4];
-    size_t lmh_smem_set;     // LM-head GEMM
-    size_t grp_occ_smem[4];  // shared memory of the cached cluster occupancy below
-    int grp_occ[4];          // co-resident clusters of the fork-group kernel
-    uint32_t* grp_work;      // the fork-group kernel's chunk counters (zero between launches)
-    unsigned long long* stats;  // device counters (diagnostics)
-    // staging for sampler_sample_host
-    unsigned char* stage_base;
-    size_t stage_bytes;
-};
 
 namespace {
 
@@ -136,6 +108,10 @@ void free_handle(sampler_s* h)
     cudaFree(h->slice_ws.cnt);
     cudaFree(h->stats);
     cudaFree(h->grp_work);
+    cudaFree(h->row_ws.records);
+    cudaFree(h->row_ws.terms);
+    cudaFree(h->row_ws.pair_terms);
+    cudaFree(h->row_ws.ticket);
     cudaFree(h->stage_base);
     delete h;
 }
@@ -210,7 +186,7 @@ int noalloc_grant_smem(int dev, int dtype, size_t smem)
 
 extern "C" {
 
-uint32_t sampler_abi_version(void) { return (1u << 16) | 3u; }
+uint32_t sampler_abi_version(void) { return (1u << 16) | 4u; }
 
 int sampler_get_stat(sampler_t h, int which, uint64_t* value, int reset)
 {
@@ -238,6 +214,7 @@ const char* sampler_status_string(int code)
         case SAMPLER_ERR_NO_DEVICE: return "no usable sm_103 device";
         case SAMPLER_ERR_NO_STAGING: return "handle has no host staging buffers";
         case SAMPLER_ERR_UNSUPPORTED: return "not supported by this entry point";
+        case SAMPLER_ERR_BAD_VALUE: return "a scalar argument is out of range";
         case SAMPLER_ROW_NONFINITE: return "row: NaN or +inf logit";
         case SAMPLER_ROW_ALL_NEG_INF: return "row: every logit is -inf";
         case SAMPLER_ROW_BAD_PARAM: return "row: parameter out of range";
@@ -284,6 +261,11 @@ int sampler_create(sampler_t* out, const sampler_config_t* cfg)
             cudaMemset(h->stats, 0, kNumStats * sizeof(unsigned long long)) != cudaSuccess ||
             cudaMalloc(&h->grp_work, 2 * sizeof(uint32_t)) != cudaSuccess ||
             cudaMemset(h->grp_work, 0, 2 * sizeof(uint32_t)) != cudaSuccess ||
+            cudaMalloc(&h->row_ws.records, size_t(h->max_rows) * dst::kRowRecordBytes) != cudaSuccess ||
+            cudaMalloc(&h->row_ws.terms, size_t(h->max_rows) * sizeof(double)) != cudaSuccess ||
+            cudaMalloc(&h->row_ws.pair_terms, size_t(h->max_rows) * sizeof(double)) != cudaSuccess ||
+            cudaMalloc(&h->row_ws.ticket, sizeof(uint32_t)) != cudaSuccess ||
+            cudaMemset(h->row_ws.ticket, 0, sizeof(uint32_t)) != cudaSuccess ||
             cudaDeviceSynchronize() != cudaSuccess) {
             free_handle(h);
             return SAMPLER_ERR_CUDA;
@@ -545,3 +527,24 @@ int sampler_sample_host(sampler_t h, const sampler_args_t* a, sampler_stream_t s
 }
 
 }  // extern "C"
+
+namespace dst {
+
+int sample_check(sampler_t h, const sampler_args_t* a, const sampler_ext_t* ext_in)
+{
+    int rc = check_args(h, a);
+    if (rc != SAMPLER_OK) return rc;
+    const sampler_ext_t* ext = nullptr;
+    rc = check_ext(a, ext_in, &ext);
+    if (rc != SAMPLER_OK || a->n_rows == 0) return rc;
+    return ext && !slice_would_take(h, a) ? SAMPLER_ERR_UNSUPPORTED : SAMPLER_OK;
+}
+
+int sample_launch(sampler_t h, const sampler_args_t* a, const sampler_ext_t* ext_in, bool pdl, cudaStream_t stream)
+{
+    const sampler_ext_t* ext = nullptr;
+    const int rc = check_ext(a, ext_in, &ext);
+    return rc != SAMPLER_OK ? rc : launch(h, a, stream, ext, pdl);
+}
+
+}  // namespace dst

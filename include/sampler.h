@@ -80,8 +80,9 @@ enum {
     SAMPLER_ERR_CUDA = -5,         /* a CUDA call failed (launch, copy, set-up) */
     SAMPLER_ERR_NO_DEVICE = -6,    /* no usable sm_100-family device */
     SAMPLER_ERR_NO_STAGING = -7,   /* sampler_sample_host on a handle made without staging */
-    SAMPLER_ERR_UNSUPPORTED = -8   /* a feature sampler_sample_noalloc or sampler_sample_ex
+    SAMPLER_ERR_UNSUPPORTED = -8,  /* a feature sampler_sample_noalloc or sampler_sample_ex
                                       does not offer on these arguments */
+    SAMPLER_ERR_BAD_VALUE = -9     /* a scalar argument is out of its range */
 };
 
 /* Per-row status codes written to out_status (when given). A row with a
@@ -349,6 +350,182 @@ int sampler_lm_head_sample(sampler_t h, const sampler_lm_head_t* lm, const sampl
  * max_vocab (SAMPLER_ERR_TOO_LARGE); lm checked as above. */
 int sampler_lm_head(sampler_t h, const sampler_lm_head_t* lm, void* logits, int64_t logits_stride, int64_t rows,
                     int64_t vocab, sampler_stream_t stream);
+
+/*
+ * Scoring and losses over the logits of given tokens.
+ *
+ * After sampling, a user trains on the tokens or scores them under another
+ * model. The calls below take one logits row per token. With x a row's logits,
+ * T its temperature and t its token,
+ *     p_v     = exp(x_v / T) / sum_u exp(x_u / T)
+ *     logprob = ln p_t             entropy = -sum_v p_v ln p_v   (0 ln 0 = 0)
+ * in fp32 with fp32 sums. This is the logprob that sampler_sample_ex reports of
+ * a row without truncation, with the same reading of T: below 1e-5 (a greedy
+ * row) T = 1.
+ *
+ * A row of weight 0 is left out: its logits are not read (they may hold
+ * anything), its outputs and its gradient are zeros, its status is
+ * SAMPLER_ROW_OK. The statuses of the other rows, in the order reported:
+ * SAMPLER_ROW_BAD_PARAM (T < 0, NaN or inf; a token outside [0, vocab)),
+ * SAMPLER_ROW_NONFINITE (a NaN or +inf logit), SAMPLER_ROW_ALL_NEG_INF. The
+ * outputs and the gradient of such a row are NaN, and so are a loss that it
+ * belongs to and the gradients of its pair's rows; other rows keep theirs. A
+ * -inf logit is a token of no mass: its gradient is 0, and the logprob of a
+ * token t with one is -inf.
+ *
+ * The gradient of the logits, where asked, has the logits' type, each value
+ * rounded once. out_grad may be the logits themselves (with the same stride):
+ * they are then overwritten; any other overlap of the two is not allowed.
+ * Gradients take all inputs but the logits as constants, and are multiplied by
+ * grad_scale and by *grad_scale_dev (a device float, NULL: 1), the gradient
+ * that arrives at the loss.
+ *
+ * n_rows is at most the handle's max_rows, vocab at most its max_vocab. The
+ * calls enqueue on `stream`, allocate nothing, read no device memory on the
+ * host and can be captured in a CUDA graph. Their results do not depend on the
+ * order in which the GPU's blocks run: the same inputs give the same bits.
+ */
+typedef struct {
+    const void* logits;         /* row i from element i * row_stride */
+    int32_t dtype;              /* SAMPLER_DTYPE_* */
+    int64_t n_rows;             /* N */
+    int64_t vocab;              /* V */
+    int64_t row_stride;         /* >= V */
+    const int32_t* tokens;      /* [N] */
+    const float* temperature;   /* [N] NULL = 1 */
+    const float* weight;        /* [N] NULL = 1; 0 leaves the row out; the losses multiply
+                                   each row's share by it */
+    float* out_logprob;         /* [N] NULL = not reported */
+    float* out_entropy;         /* [N] NULL = not reported (sampler_preference_loss has none) */
+    int32_t* out_status;        /* [N] NULL = not reported */
+    void* out_grad;             /* [N, grad_stride] NULL = no gradient */
+    int64_t grad_stride;        /* >= V */
+} sampler_rows_t;
+
+/* Logprob and entropy of each row's token; rows->out_grad must be NULL
+ * (SAMPLER_ERR_UNSUPPORTED). */
+int sampler_score(sampler_t h, const sampler_rows_t* rows, sampler_stream_t stream);
+
+/* The gradient of sum_i grad_logprob[i] * logprob_i + grad_entropy[i] * entropy_i
+ * over the rows with a weight other than 0 (whose value is not used) into
+ * rows->out_grad, and the outputs of sampler_score in the same pass over the
+ * logits. grad_logprob, grad_entropy: [N]; grad_entropy may be NULL (0). */
+int sampler_score_grad(sampler_t h, const sampler_rows_t* rows, const float* grad_logprob,
+                       const float* grad_entropy, sampler_stream_t stream);
+
+/*
+ * The clipped policy loss with a KL term and an entropy bonus: with
+ * ratio = exp(logprob - old_logprob), A = advantage, d = ref_logprob - logprob,
+ *     loss = sum_i weight_i * ( -min(ratio A, clip(ratio, 1 - clip_low, 1 + clip_high) A)
+ *                               + kl_coef * (exp(d) - d - 1) - entropy_coef * entropy )_i
+ * The weights hold the normalisation (1 / number of tokens, say). No gradient
+ * flows through a term that the clip decides. exp(d) - d - 1 is the
+ * non-negative one-sample estimate of KL(policy || reference).
+ */
+typedef struct {
+    const float* old_logprob;   /* [N] of the policy that sampled the tokens */
+    const float* advantage;     /* [N] */
+    const float* ref_logprob;   /* [N] of the reference model; NULL = no KL term (kl_coef 0, no out_kl) */
+    float clip_low;             /* in [0, 1] */
+    float clip_high;            /* >= 0 */
+    float kl_coef;
+    float entropy_coef;
+    float grad_scale;
+    const float* grad_scale_dev;  /* one device float, NULL = 1 */
+    float* out_loss;            /* one float */
+    float* out_ratio;           /* [N] NULL = not reported */
+    float* out_kl;              /* [N] exp(d) - d - 1; NULL = not reported */
+} sampler_policy_t;
+
+int sampler_policy_loss(sampler_t h, const sampler_rows_t* rows, const sampler_policy_t* policy,
+                        sampler_stream_t stream);
+
+/*
+ * The preference loss over pairs of answers. Answer s is the rows
+ * [seq_offsets[s], seq_offsets[s + 1]); answers 2i and 2i + 1 are the preferred
+ * and the other one of pair i. With
+ *     S_s      = sum_{rows i of s} weight_i * (logprob_i - ref_logprob_i)
+ *                (divided by sum weight_i with mean_over_tokens; 0 where that sum is 0)
+ *     reward_s = beta * S_s,   z_i = reward_2i - reward_2i+1 - margin,
+ *     loss     = mean over pairs of -(1 - label_smoothing) ln sigmoid(z_i)
+ *                                   - label_smoothing ln sigmoid(-z_i)
+ * (0 for no pairs). The weights mask prompts (0) or weigh tokens. A NULL
+ * ref_logprob is a loss without a reference model. Rows in no answer get a
+ * gradient of zeros. An answer whose offsets do not lie in 0 <= begin <= end
+ * <= n_rows has no rows and a NaN reward; the loss and the gradient of its
+ * pair's other answer are then NaN. n_pairs is at most the handle's max_rows.
+ */
+typedef struct {
+    const int32_t* seq_offsets; /* [2 * n_pairs + 1] */
+    int64_t n_pairs;
+    const float* ref_logprob;   /* [N] NULL = 0 */
+    float beta;
+    float margin;
+    float label_smoothing;      /* in [0, 1] */
+    int32_t mean_over_tokens;
+    float grad_scale;
+    const float* grad_scale_dev;  /* one device float, NULL = 1 */
+    float* out_loss;            /* one float */
+    float* out_reward;          /* [2 * n_pairs] NULL = not reported */
+} sampler_preference_t;
+
+int sampler_preference_loss(sampler_t h, const sampler_rows_t* rows, const sampler_preference_t* pref,
+                            sampler_stream_t stream);
+
+/*
+ * The LM head in 8 bits: e4m3 values (4-bit exponent, 3-bit mantissa, largest
+ * 448, no infinities) with one fp32 scale for each block of 128.
+ *
+ * sampler_quantize_blocks makes them. Columns go in blocks of 128, rows in
+ * blocks of block_rows: 1 (hidden rows: one scale for 128 values) or 128 (a
+ * weight: one scale for 128 x 128 values); the last blocks may be smaller. With
+ * m = max(largest |x| of the block, 2^-100),
+ *     scale = m / 448,   value = e4m3(x * (448 / m)),
+ * each operation one IEEE fp32 operation, the last a rounding to nearest even.
+ * A block with a NaN or an infinity has a NaN scale and zero values, so that
+ * what is computed from it is NaN.
+ */
+typedef struct {
+    const void* src;         /* [rows, src_stride] */
+    int32_t dtype;           /* SAMPLER_DTYPE_* */
+    int64_t rows, cols;
+    int64_t src_stride;      /* elements, >= cols */
+    int32_t block_rows;      /* 1 or 128 */
+    void* values;            /* [rows, values_stride] e4m3 */
+    int64_t values_stride;   /* >= cols */
+    float* scales;           /* [ceil(rows / block_rows), scale_stride] */
+    int64_t scale_stride;    /* >= ceil(cols / 128) */
+} sampler_quantize_t;
+
+int sampler_quantize_blocks(sampler_t h, const sampler_quantize_t* q, sampler_stream_t stream);
+
+/* logits[i, v] = sum_b hidden_scale[i, b] * weight_scale[v / 128, b]
+ *                      * sum_{k in block b} hidden[i, k] * weight[v, k]
+ * for i < rows, v < vocab, in fp32 sums, rounded once to `dtype`. hidden:
+ * [rows, hidden_stride] e4m3 with scales for 1 x 128 blocks, weight:
+ * [vocab, weight_stride] e4m3 with scales for 128 x 128 blocks. Both 16-byte
+ * aligned, strides multiples of 16 and >= hidden_dim, else
+ * SAMPLER_ERR_BAD_SHAPE; vocab is at most the handle's max_vocab. */
+typedef struct {
+    const void* hidden;
+    const float* hidden_scale;    /* [rows, hidden_scale_stride] */
+    const void* weight;
+    const float* weight_scale;    /* [ceil(vocab / 128), weight_scale_stride] */
+    int64_t hidden_dim;           /* K >= 1 */
+    int64_t hidden_stride;
+    int64_t weight_stride;
+    int64_t hidden_scale_stride;  /* >= ceil(K / 128) */
+    int64_t weight_scale_stride;  /* >= ceil(K / 128) */
+} sampler_scaled_head_t;
+
+int sampler_lm_head_scaled(sampler_t h, const sampler_scaled_head_t* lm, void* logits, int32_t dtype,
+                           int64_t logits_stride, int64_t rows, int64_t vocab, sampler_stream_t stream);
+
+/* sampler_lm_head_scaled into args->logits (n_logit_rows rows, n_rows when 0;
+ * args->dtype, row_stride apart), then the step of sampler_sample_ex on them,
+ * as sampler_lm_head_sample does with a bf16 head. */
+int sampler_lm_head_scaled_sample(sampler_t h, const sampler_scaled_head_t* lm, const sampler_args_t* args,
+                                  const sampler_ext_t* ext, sampler_stream_t stream);
 
 /* Release the handle and its device memory. NULL is a no-op. */
 void sampler_destroy(sampler_t h);

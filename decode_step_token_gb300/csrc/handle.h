@@ -28,6 +28,7 @@ struct sampler_s {
     uint32_t* grp_work;      // the fork-group kernel's chunk counters (zero between launches)
     unsigned long long* stats;  // device counters (diagnostics)
     dst::RowWorkspace row_ws;  // scoring and the losses: one record per row, and a launch's ticket
+    dst::RowOccupancy row_occ;
     // staging for sampler_sample_host
     unsigned char* stage_base;
     size_t stage_bytes;

@@ -121,7 +121,7 @@ struct RowWorkspace {
     RowRecord* records;  // [max_rows]
     double* terms;       // [max_rows] each row's share of the loss (pairs: its logprob)
     double* pair_terms;  // [max_rows] each pair's share of the loss
-    uint32_t* ticket;    // blocks that have ended; zero between launches
+    uint32_t* ticket;    // blocks (or clusters) that have ended; zero between launches
 };
 
 enum RowMode : int { kModeScore = 0, kModeScoreGrad = 1, kModePolicy = 2, kModePairs = 3 };
@@ -135,13 +135,19 @@ struct LossParams {
     RowWorkspace ws;
 };
 
+// Clusters that the device holds at once, by the logits' type, gradient, entropy
+// and cluster size (1, 2, 4, 8, 16); 0 = not asked yet.
+struct RowOccupancy {
+    int clusters[2][2][2][5];
+};
+
 // Statistics of every row, what the mode makes of them, and (kModeScoreGrad,
 // kModePolicy with out_grad) the logits' gradient.
-int rows_launch(const LossParams& p, int sms, cudaStream_t stream);
+int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t stream);
 // The pairs' loss from the rows' logprobs, and each row's record for pairs_grad_launch.
 int pairs_launch(const sampler_rows_t& rows, const sampler_preference_t& pref, const RowWorkspace& ws,
                  cudaStream_t stream);
-int pairs_grad_launch(const sampler_rows_t& rows, const RowWorkspace& ws, int sms, cudaStream_t stream);
+int pairs_grad_launch(const sampler_rows_t& rows, const RowWorkspace& ws, cudaStream_t stream);
 
 // ---------------------------------------------------------------- 8-bit LM head
 int quantize_launch(const sampler_quantize_t& q, int sms, cudaStream_t stream);

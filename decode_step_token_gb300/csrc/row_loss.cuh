@@ -24,15 +24,15 @@
 namespace dst {
 namespace rows {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr double kLn2 = 0.6931471805599453;
+constexpr double kLog2e = 1.4426950408889634;
+constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGreedyT = 1e-5f;  // below it a row is greedy and its outputs use T = 1
 constexpr int32_t kNoToken = 0x7fffffff;  // of a row with an error status: matches no element
 constexpr float kLowest = -3e4f;   // exponents are not taken below this where they are multiplied by 2^u (= 0)
+constexpr float kFloatMax = 3.402823466e38f;
 
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
 __device__ __forceinline__ float pos_inf() { return __int_as_float(0x7f800000); }
-__device__ __forceinline__ float neg_inf() { return __int_as_float(int(0xff800000u)); }
 
 __device__ __forceinline__ float exp2_fast(float x)
 {
@@ -46,59 +46,100 @@ __device__ __forceinline__ float load_logit(const uint16_t* p) { return __uint_a
 __device__ __forceinline__ void store_grad(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_grad(uint16_t* p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
-// Sum of exponentials relative to a reference of its own. ref = -inf: nothing
-// has been added (s = t = 0). bad: a NaN or +inf was met.
+// Sums of a part of a row relative to a reference of its own, which is at least
+// the lowest float: a -inf logit is then infinitely far below it and adds
+// nothing. A part with a NaN or +inf logit has s = NaN, an empty one s = 0.
 struct Stats {
     float ref, s, t;
-    uint32_t bad;
 };
 
-__device__ __forceinline__ Stats stats_empty() { return Stats{neg_inf(), 0.f, 0.f, 0u}; }
+__device__ __forceinline__ Stats stats_empty() { return Stats{-kFloatMax, 0.f, 0.f}; }
 
-// a and b, relative to the larger reference.
-__device__ __forceinline__ Stats stats_join(const Stats& a, const Stats& b, float c)
+// `a` relative to a reference that is at least its own.
+__device__ __forceinline__ void stats_move(Stats& a, float ref, float c)
 {
-    const float ref = fmaxf(a.ref, b.ref);
-    Stats r;
-    r.ref = ref;
-    r.bad = a.bad | b.bad;
-    if (ref == neg_inf()) {
-        r.s = r.t = 0.f;
-        return r;
-    }
-    const float da = fmaxf((a.ref - ref) * c, kLowest), db = fmaxf((b.ref - ref) * c, kLowest);
-    const float fa = exp2_fast(da), fb = exp2_fast(db);
-    r.s = a.s * fa + b.s * fb;
-    r.t = fa * fmaf(a.s, da, a.t) + fb * fmaf(b.s, db, b.t);
-    return r;
+    const float d = fmaxf((a.ref - ref) * c, kLowest), f = exp2_fast(d);
+    a.t = f * fmaf(a.s, d, a.t);
+    a.s *= f;
+    a.ref = ref;
 }
 
-// A row's parameters.
-struct RowHead {
-    float c, inv_t;
-    float weight;
+// The statistics of all lanes' parts, in every lane.
+__device__ __forceinline__ void stats_warp(Stats& a, float c)
+{
+    float ref = a.ref;
+    for (int o = 16; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+    stats_move(a, ref, c);
+    for (int o = 16; o > 0; o >>= 1) {
+        a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
+        a.t += __shfl_xor_sync(0xffffffffu, a.t, o);
+    }
+}
+
+// A row as the kernels take it up: its parameters and what its mode reads of it.
+struct RowJob {
+    int32_t row;      // -1: no more rows
     int32_t token;
-    bool live;       // false: left out
-    bool bad_param;
+    int32_t live;     // 0: left out
+    int32_t bad_param;
+    float weight;
+    float c, c_hi, c_lo;    // log2(e) / T, rounded, and as a pair: c_lo > 0
+    float inv_t, inv_t_lo;  // 1 / T as a pair
+    float in0, in1, in2;    // kModeScoreGrad: the gradients by logprob and entropy; kModePolicy: advantage,
+                            // old_logprob, ref_logprob
 };
 
-__device__ __forceinline__ RowHead row_open(const sampler_rows_t& a, int64_t r)
+// The pair c_hi + c_lo matters where sums are taken: c alone is off by up to
+// 2^-24 of itself in every exponent the same way, which is an error of the
+// logprob of that times the row's mean depth, and does not average out over a
+// sequence. c_lo > 0 keeps -inf * c_lo = -inf.
+__device__ __forceinline__ RowJob row_open(const LossParams& P, int64_t r)
 {
-    RowHead h;
+    const sampler_rows_t& a = P.rows;
+    RowJob h;
+    h.row = int32_t(r);
+    h.token = a.tokens[r];
     h.weight = a.weight ? a.weight[r] : 1.f;
     h.live = h.weight != 0.f;
-    h.token = a.tokens[r];
     const float T = a.temperature ? a.temperature[r] : 1.f;
+    h.in0 = h.in1 = h.in2 = 0.f;
+    if (P.mode == kModeScoreGrad) {
+        h.in0 = P.grad_logprob[r];
+        if (P.grad_entropy) h.in1 = P.grad_entropy[r];
+    } else if (P.mode == kModePolicy) {
+        h.in0 = P.policy.advantage[r];
+        h.in1 = P.policy.old_logprob[r];
+        if (P.policy.ref_logprob) h.in2 = P.policy.ref_logprob[r];
+    }
     h.bad_param = !(T >= 0.f) || isinf(T) || h.token < 0 || int64_t(h.token) >= a.vocab;
-    const float Te = T < kGreedyT ? 1.f : T;
-    h.inv_t = __fdiv_rn(1.f, Te);
-    h.c = __fdiv_rn(kLog2e, Te);
+    double c = kLog2e, inv = 1.0;
+    if (T >= kGreedyT && T != 1.f) {
+        inv = 1.0 / double(T);
+        c = kLog2e * inv;
+    }
+    h.c = float(c);
+    h.c_hi = __double2float_rd(c);
+    h.c_lo = fmaxf(float(c - double(h.c_hi)), 1e-30f);
+    h.inv_t = float(inv);
+    h.inv_t_lo = float(inv - double(h.inv_t));
     return h;
 }
 
-// ln s to about 3e-8: the exponent's part in double, the mantissa's (within
-// [1/sqrt 2, sqrt 2], so of magnitude below 0.35) by logf.
-__device__ __forceinline__ double log_of(float s)
+// Sums and products of two floats without rounding, as pairs (Dekker, Knuth).
+struct Pair {
+    float hi, lo;
+};
+
+__device__ __forceinline__ Pair two_sum(float a, float b)
+{
+    const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
+    return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z))};
+}
+
+// ln s, off by about 3e-8: the exponent's part exactly (ln 2 = 355/512 less a
+// small rest, after Cody and Waite), the mantissa's (within [1/sqrt 2, sqrt 2],
+// so of magnitude below 0.35) by logf.
+__device__ __forceinline__ Pair log_of(float s)
 {
     int e;
     float f = frexpf(s, &e);  // [0.5, 1)
@@ -106,7 +147,21 @@ __device__ __forceinline__ double log_of(float s)
         f *= 2.f;
         --e;
     }
-    return double(e) * kLn2 + double(logf(f));
+    const float n = float(e);
+    const Pair p = two_sum(n * 0.693359375f, logf(f));
+    return two_sum(p.hi, p.lo - n * 2.1219444005469058e-4f);
+}
+
+// ln p of the token with logit x_t.
+__device__ __forceinline__ Pair logprob_of(const RowJob& h, const Stats& st, float x_t, const Pair& ln_s)
+{
+    const Pair d = two_sum(x_t, -st.ref);
+    const float y = d.hi * h.inv_t;
+    if (!(y >= -kFloatMax)) return Pair{y, 0.f};  // no mass
+    const float rest = fmaf(d.hi, h.inv_t, -y) + fmaf(d.hi, h.inv_t_lo, d.lo * h.inv_t);
+    const Pair p = two_sum(y, -ln_s.hi);
+    const Pair q = two_sum(p.hi, p.lo + (rest - ln_s.lo));
+    return q;
 }
 
 // exp(d) - d - 1. Near 0 its Taylor series (to d^9: the next term is below 1e-8
@@ -124,7 +179,7 @@ __device__ __forceinline__ float exp_less_linear(float d)
         p = fmaf(p, d, 0.5f);
         return d * d * p;
     }
-    return expm1f(d) - d;
+    return isinf(d) ? pos_inf() : expm1f(d) - d;
 }
 
 __device__ __forceinline__ float scale_of_grad(float scale, const float* dev) { return dev ? scale * *dev : scale; }
@@ -134,107 +189,112 @@ __device__ __forceinline__ void set_factors(RowRecord& rec, float a, float b, fl
 {
     const float q = rec.inv_s * rec.inv_t;
     rec.k0 = -(b != 0.f ? fmaf(b, entropy - ln_s, a) : a) * q;
-    rec.k1 = -b * float(kLn2) * q;
+    rec.k1 = -b * kLn2 * q;
     rec.at_token = a * rec.inv_t;
 }
 
-// One thread's work once a row's statistics are known (x_t: the token's logit):
-// the row's outputs (where `write`), its share of the loss, and its record.
-__device__ __forceinline__ void row_close(const LossParams& P, int64_t r, const RowHead& h, const Stats& st, float x_t,
-                                          bool write, RowRecord& rec)
+// What becomes of a row once its statistics are known (x_t: the token's logit;
+// grad_scale: the whole factor of the gradient): its record, and where `write`
+// its outputs and its share of the loss.
+__device__ __forceinline__ void row_close(const LossParams& P, const RowJob& h, const Stats& st, float x_t,
+                                          float grad_scale, bool write, RowRecord& rec)
 {
     const sampler_rows_t& a = P.rows;
+    const int64_t r = h.row;
     rec.c = h.c;
     rec.ref = st.ref;
     rec.token = h.token;
     rec.inv_s = rec.inv_t = rec.k0 = rec.k1 = rec.at_token = 0.f;
-    float logprob = 0.f, entropy = 0.f, ratio = 0.f, kl = 0.f;
-    double term = 0.0;
+    Pair lp = {0.f, 0.f};
+    float entropy = 0.f, ratio = 0.f, kl = 0.f, term = 0.f;
     int status = SAMPLER_ROW_OK;
     if (!h.live) {
         rec.token = -1;
     } else {
-        status = h.bad_param ? SAMPLER_ROW_BAD_PARAM
-                 : st.bad    ? SAMPLER_ROW_NONFINITE
-                 : st.ref == neg_inf() ? SAMPLER_ROW_ALL_NEG_INF
-                                       : SAMPLER_ROW_OK;
+        status = h.bad_param   ? SAMPLER_ROW_BAD_PARAM
+                 : isnan(st.s) ? SAMPLER_ROW_NONFINITE
+                 : st.s == 0.f ? SAMPLER_ROW_ALL_NEG_INF
+                               : SAMPLER_ROW_OK;
         if (status != SAMPLER_ROW_OK) {
             // every value of the gradient becomes a multiple of NaN
             rec.c = rec.ref = 0.f;
             rec.token = kNoToken;
             rec.inv_s = rec.k0 = rec.at_token = quiet_nan();
-            logprob = entropy = ratio = kl = quiet_nan();
-            term = double(quiet_nan());
+            lp.hi = entropy = ratio = kl = term = quiet_nan();
         } else {
             rec.inv_s = __fdiv_rn(1.f, st.s);
             rec.inv_t = h.inv_t;
-            const double ln_s = log_of(st.s);
-            const double lp = (double(x_t) - double(st.ref)) * double(h.inv_t) - ln_s;
-            logprob = float(lp);
-            entropy = float(ln_s - kLn2 * double(__fdiv_rn(st.t, st.s)));
+            const Pair ln_s = log_of(st.s);
+            lp = logprob_of(h, st, x_t, ln_s);
+            entropy = ln_s.hi + fmaf(-kLn2, st.t * rec.inv_s, ln_s.lo);
             if (P.mode == kModeScoreGrad) {
-                set_factors(rec, P.grad_logprob[r], P.grad_entropy ? P.grad_entropy[r] : 0.f, entropy, float(ln_s));
+                set_factors(rec, h.in0, h.in1, entropy, ln_s.hi);
             } else if (P.mode == kModePolicy) {
                 const sampler_policy_t& q = P.policy;
-                const float A = q.advantage[r];
-                ratio = expf(float(lp - double(q.old_logprob[r])));
+                const float A = h.in0;
+                Pair d = two_sum(lp.hi, -h.in1);
+                ratio = expf(isinf(d.hi) ? d.hi : d.hi + (d.lo + lp.lo));
                 const float lo = 1.f - q.clip_low, hi = 1.f + q.clip_high;
                 const float plain = ratio * A;
                 const float cut = fminf(fmaxf(ratio, lo), hi) * A;
                 const float gain = plain < cut ? plain : plain >= cut ? cut : quiet_nan();
                 const bool decided = (A > 0.f && ratio > hi) || (A < 0.f && ratio < lo);  // by the clip
                 float by_lp = decided ? 0.f : -plain;
-                term = -double(gain);
+                term = -gain;
                 if (q.ref_logprob) {
-                    const float d = float(double(q.ref_logprob[r]) - lp);
-                    kl = exp_less_linear(d);
+                    d = two_sum(h.in2, -lp.hi);
+                    const float e = isinf(d.hi) ? d.hi : d.hi + (d.lo - lp.lo);
+                    kl = exp_less_linear(e);
                     if (q.kl_coef != 0.f) {
-                        term += double(q.kl_coef) * double(kl);
-                        by_lp = fmaf(-q.kl_coef, expm1f(d), by_lp);
+                        term = fmaf(q.kl_coef, kl, term);
+                        by_lp = fmaf(-q.kl_coef, expm1f(e), by_lp);
                     }
                 }
-                if (q.entropy_coef != 0.f) term -= double(q.entropy_coef) * double(entropy);
-                term *= double(h.weight);
+                if (q.entropy_coef != 0.f) term = fmaf(-q.entropy_coef, entropy, term);
                 if (a.out_grad) {
-                    const float g = h.weight * scale_of_grad(q.grad_scale, q.grad_scale_dev);
-                    set_factors(rec, g * by_lp, -g * q.entropy_coef, entropy, float(ln_s));
+                    const float g = h.weight * grad_scale;
+                    set_factors(rec, g * by_lp, -g * q.entropy_coef, entropy, ln_s.hi);
                 }
             }
         }
     }
     if (!write) return;
-    if (a.out_logprob) a.out_logprob[r] = logprob;
+    if (a.out_logprob) a.out_logprob[r] = lp.hi;
     if (a.out_entropy) a.out_entropy[r] = entropy;
     if (a.out_status) a.out_status[r] = status;
     if (P.mode == kModePolicy) {
         if (P.policy.out_ratio) P.policy.out_ratio[r] = ratio;
         if (P.policy.out_kl) P.policy.out_kl[r] = kl;
-        P.ws.terms[r] = term;
+        P.ws.terms[r] = h.live ? double(h.weight) * double(term) : 0.0;
     }
     if (P.mode == kModePairs) {
         // the pairs' kernel takes the logprob from here and puts the gradient's factors in
-        P.ws.terms[r] = double(logprob);
+        P.ws.terms[r] = double(lp.hi) + double(lp.lo);
         P.ws.records[r] = rec;
     }
 }
 
-// Whether this block is the last of the launch to get here; what the others
-// wrote before is then visible. Clears the ticket for the next launch. Called by
-// every thread of a block; `flag` is a word of its shared memory.
-__device__ __forceinline__ bool last_block(uint32_t* ticket, uint32_t blocks, uint32_t* flag)
+constexpr uint32_t kGaveUp = 0x80000000u;  // in the ticket: a wait of this launch gave up
+
+// Not 0 in the last of `blocks` blocks to get here (with kGaveUp as the ticket
+// has it); what the others wrote before is then visible. Clears the ticket for
+// the next launch. Called by every thread of a block; `flag` is a word of its
+// shared memory.
+__device__ __forceinline__ uint32_t last_block(uint32_t* ticket, uint32_t blocks, uint32_t* flag)
 {
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
         const uint32_t got = atomicAdd(ticket, 1u);
-        *flag = got + 1u == blocks;
-        if (*flag) {
+        *flag = 0u;
+        if ((got & ~kGaveUp) + 1u == blocks) {
+            *flag = 1u | (got & kGaveUp);
             *ticket = 0u;
             __threadfence();
         }
     }
     __syncthreads();
-    return *flag != 0u;
+    return *flag;
 }
 
 // Sum of terms[0 .. n) in double by one block of kThreads threads, in an order

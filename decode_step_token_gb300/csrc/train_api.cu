@@ -28,7 +28,7 @@ int check_rows(sampler_t h, const sampler_rows_t* a)
     if (!h || !a) return SAMPLER_ERR_NULL_ARG;
     if (a->n_rows < 0 || a->vocab < 1 || a->row_stride < a->vocab) return SAMPLER_ERR_BAD_SHAPE;
     if (!known(a->dtype)) return SAMPLER_ERR_BAD_DTYPE;
-    if (a->n_rows > h->max_rows || a->vocab > h->max_vocab) return SAMPLER_ERR_TOO_LARGE;
+    if (a->n_rows > h->max_rows || a->n_rows > INT_MAX || a->vocab > h->max_vocab) return SAMPLER_ERR_TOO_LARGE;
     if (a->n_rows == 0) return SAMPLER_OK;
     if (!a->logits || !a->tokens) return SAMPLER_ERR_NULL_ARG;
     const size_t es = bytes_of(a->dtype);
@@ -84,7 +84,7 @@ int sampler_score(sampler_t h, const sampler_rows_t* rows, sampler_stream_t stre
     p.rows = *rows;
     p.mode = dst::kModeScore;
     p.ws = h->row_ws;
-    return dst::rows_launch(p, h->num_sms, cuda_stream(stream));
+    return dst::rows_launch(p, h->num_sms, &h->row_occ, cuda_stream(stream));
 }
 
 int sampler_score_grad(sampler_t h, const sampler_rows_t* rows, const float* grad_logprob, const float* grad_entropy,
@@ -104,7 +104,7 @@ int sampler_score_grad(sampler_t h, const sampler_rows_t* rows, const float* gra
     p.grad_logprob = grad_logprob;
     p.grad_entropy = grad_entropy;
     p.ws = h->row_ws;
-    return dst::rows_launch(p, h->num_sms, cuda_stream(stream));
+    return dst::rows_launch(p, h->num_sms, &h->row_occ, cuda_stream(stream));
 }
 
 int sampler_policy_loss(sampler_t h, const sampler_rows_t* rows, const sampler_policy_t* q, sampler_stream_t stream)
@@ -130,7 +130,7 @@ int sampler_policy_loss(sampler_t h, const sampler_rows_t* rows, const sampler_p
     p.mode = dst::kModePolicy;
     p.policy = *q;
     p.ws = h->row_ws;
-    return dst::rows_launch(p, h->num_sms, cuda_stream(stream));
+    return dst::rows_launch(p, h->num_sms, &h->row_occ, cuda_stream(stream));
 }
 
 int sampler_preference_loss(sampler_t h, const sampler_rows_t* rows, const sampler_preference_t* q,
@@ -158,12 +158,12 @@ int sampler_preference_loss(sampler_t h, const sampler_rows_t* rows, const sampl
         p.rows = *rows;
         p.mode = dst::kModePairs;
         p.ws = h->row_ws;
-        rc = dst::rows_launch(p, h->num_sms, s);
+        rc = dst::rows_launch(p, h->num_sms, &h->row_occ, s);
         if (rc != SAMPLER_OK) return rc;
     }
     rc = q->n_pairs > 0 ? dst::pairs_launch(*rows, *q, h->row_ws, s) : write_zero(q->out_loss, s);
     if (rc != SAMPLER_OK || !rows->out_grad || rows->n_rows == 0) return rc;
-    return dst::pairs_grad_launch(*rows, h->row_ws, h->num_sms, s);
+    return dst::pairs_grad_launch(*rows, h->row_ws, s);
 }
 
 int sampler_quantize_blocks(sampler_t h, const sampler_quantize_t* q, sampler_stream_t stream)

@@ -86,7 +86,7 @@ def policy(logits, tokens, old, advantage, ref=None, temperature=None, weight=No
         kl = np.zeros(n)
         if ref is not None:
             d = ref - got["logprob"]
-            kl = np.expm1(d) - d
+            kl = np.where(np.isinf(d), np.inf, np.expm1(d) - d)
             if kl_coef != 0:
                 term = term + kl_coef * kl
                 by_lp = by_lp - kl_coef * np.expm1(d)

@@ -215,7 +215,7 @@ int sampler_lm_head_scaled_sample(sampler_t h, const sampler_scaled_head_t* lm, 
     rc = launch_scaled(h, lm, const_cast<void*>(a->logits), a->dtype, a->row_stride, rows, a->vocab,
                        cuda_stream(stream));
     if (rc != SAMPLER_OK) return rc;
-    return dst::sample_launch(h, a, ext, false, cuda_stream(stream));
+    return dst::sample_launch(h, a, ext, true, cuda_stream(stream));
 }
 
 }  // extern "C"

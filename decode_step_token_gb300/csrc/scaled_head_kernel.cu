@@ -30,9 +30,9 @@
 // Persistent, one CTA an SM; warp roles:
 //   warps 0-7  the epilogue: two groups of four warps, each a half of the tile's
 //              columns, a warp 32 of its lanes;
-//   warp 8     one thread issues the TMA loads of the operand ring;
-//   warp 9     owns the tensor memory, and one thread issues the MMAs (of a pair:
-//              the first CTA's).
+//   warp 8     issues the TMA loads of the operand ring;
+//   warp 9     owns the tensor memory and issues the MMAs (of a pair: the first
+//              CTA's).
 // Warps 10 and 11 fill up the third warpgroup, which gives its registers to the
 // epilogue's (a thread there holds up to 128 sums).
 // Every wait is bounded in time; a CTA whose wait gives up counts itself in the
@@ -227,6 +227,18 @@ __device__ __forceinline__ void fma2(float2& a, uint32_t x, uint32_t y, float p,
         : "r"(x), "r"(y), "f"(p), "f"(q));
 }
 
+// True in one lane of a warp whose lanes are together. The warps that issue TMA
+// loads and MMAs run as a whole, with this around the issuing instructions: their
+// operands are then known to be the same for all lanes, which those instructions
+// need. (Inside `if (lane == 0)` an MMA took about 65 cycles to issue and a commit
+// about 100, together more than the tensor cores took for a block.)
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ uint64_t now_ns()
 {
     uint64_t t;
@@ -337,7 +349,7 @@ __device__ __forceinline__ void end(const Params& P, Control& C, uint32_t tmem)
     if (threadIdx.x == 0 && C.gave_up && P.timeouts) atomicAdd(P.timeouts, 1ull);
 }
 
-// The TMA thread of a CTA that works alone.
+// The TMA warp of a CTA that works alone.
 __device__ __forceinline__ void produce(const Params& P, Control& C, unsigned char* sa, unsigned char* sb)
 {
     const uint32_t S = uint32_t(P.stages), b_bytes = uint32_t(P.NT) * kBK;
@@ -348,9 +360,12 @@ __device__ __forceinline__ void produce(const Params& P, Control& C, unsigned ch
         for (int b = 0; b < P.blocks; ++b) {
             ok = wait(&C.empty[s.at], s.phase ^ 1u);
             if (!ok) break;
-            mbar_arrive_expect_tx(&C.full[s.at], kABytes + b_bytes);
-            tma_load_2d(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, t * kBM, smem_addr(&C.full[s.at]));
-            tma_load_2d(smem_addr(sb + s.at * b_bytes), &P.tn, b * kBK, 0, smem_addr(&C.full[s.at]));
+            if (elect_one()) {
+                mbar_arrive_expect_tx(&C.full[s.at], kABytes + b_bytes);
+                tma_load_2d(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, t * kBM, smem_addr(&C.full[s.at]));
+                tma_load_2d(smem_addr(sb + s.at * b_bytes), &P.tn, b * kBK, 0, smem_addr(&C.full[s.at]));
+            }
+            __syncwarp();
             s.next(S);
             ++issued;
         }
@@ -360,7 +375,7 @@ __device__ __forceinline__ void produce(const Params& P, Control& C, unsigned ch
     for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j) wait(&C.full[j % S], j / S & 1u);
 }
 
-// The MMA thread: each block of K into the next accumulator.
+// The MMA warp: each block of K into the next accumulator.
 __device__ __forceinline__ void multiply(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
                                          uint32_t tmem)
 {
@@ -369,23 +384,27 @@ __device__ __forceinline__ void multiply(const Params& P, Control& C, unsigned c
     bool ok = true;
     for (int t = int(blockIdx.x); ok && t < P.tiles; t += int(gridDim.x)) {
         for (int b = 0; b < P.blocks; ++b) {
-            ok = wait(&C.tempty[acc.at], acc.phase ^ 1u) && wait(&C.full[s.at], s.phase);
+            ok = wait(&C.full[s.at], s.phase) && wait(&C.tempty[acc.at], acc.phase ^ 1u);
             if (!ok) break;
             fence_after_sync();
             const uint32_t d = tmem + acc.at * uint32_t(P.NT);
             const uint64_t da = desc_sw128(smem_addr(sa + s.at * kABytes));
             const uint64_t db = desc_sw128(smem_addr(sb + s.at * b_bytes));
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kBK / kUK; ++k)  // +32 bytes inside the 128-byte rows
-                mma_e4m3(d, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, uint32_t(k));
-            mma_commit(&C.empty[s.at]);
-            mma_commit(&C.tfull[acc.at]);
+                for (int k = 0; k < kBK / kUK; ++k)  // +32 bytes inside the 128-byte rows
+                    mma_e4m3(d, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, uint32_t(k));
+                mma_commit(&C.tfull[acc.at]);
+                mma_commit(&C.empty[s.at]);
+            }
+            __syncwarp();
             s.next(uint32_t(P.stages));
             acc.next(uint32_t(P.accs));
         }
     }
     if (!ok) C.gave_up = 1;
-    mma_commit(&C.drained);
+    if (elect_one()) mma_commit(&C.drained);
+    __syncwarp();
     wait(&C.drained, 0);
 }
 
@@ -421,9 +440,9 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     if (warp == 8) {
-        if (lane == 0) produce(P, C, sa, sb);
+        produce(P, C, sa, sb);
     } else if (warp == 9) {
-        if (lane == 0) multiply(P, C, sa, sb, tmem);
+        multiply(P, C, sa, sb, tmem);
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         const int group = warp >> 2, quarter = warp & 3;  // quarter: the tensor-memory lanes a warp may read
@@ -546,7 +565,7 @@ __device__ __forceinline__ void pair_tile(const Params& P, int t, int& m, int& n
 // The same barrier of the pair's first CTA, in the cluster's shared memory.
 __device__ __forceinline__ uint32_t of_first(uint64_t* bar) { return dsmem_map(smem_addr(bar), 0); }
 
-// The TMA thread of each CTA of a pair: its half of both operands. The first
+// The TMA warp of each CTA of a pair: its half of both operands. The first
 // CTA's barrier counts the bytes of both.
 __device__ __forceinline__ void pair_produce(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
                                              uint32_t rank, int first, int step)
@@ -563,10 +582,13 @@ __device__ __forceinline__ void pair_produce(const Params& P, Control& C, unsign
         for (int b = 0; b < P.blocks; ++b) {
             ok = wait(&C.empty[s.at], s.phase ^ 1u);
             if (!ok) break;
-            if (rank == 0) mbar_arrive_expect_tx(&C.full[s.at], 4 * kABytes);
             const uint32_t bar = of_first(&C.full[s.at]);
-            tma_load_2d_pair(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, m, bar);
-            tma_load_2d_pair(smem_addr(sb + s.at * kABytes), &P.tn, b * kBK, n, bar);
+            if (elect_one()) {
+                if (rank == 0) mbar_arrive_expect_tx(&C.full[s.at], 4 * kABytes);
+                tma_load_2d_pair(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, m, bar);
+                tma_load_2d_pair(smem_addr(sb + s.at * kABytes), &P.tn, b * kBK, n, bar);
+            }
+            __syncwarp();
             s.next(S);
             ++issued;
         }
@@ -577,7 +599,7 @@ __device__ __forceinline__ void pair_produce(const Params& P, Control& C, unsign
         for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j) wait(&C.full[j % S], j / S & 1u);
 }
 
-// The MMA thread of the pair.
+// The MMA warp of the pair.
 __device__ __forceinline__ void pair_multiply(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
                                               uint32_t tmem, int first, int step)
 {
@@ -586,23 +608,27 @@ __device__ __forceinline__ void pair_multiply(const Params& P, Control& C, unsig
     bool ok = true;
     for (int t = first; ok && t < P.tiles; t += step) {
         for (int b = 0; b < P.blocks; ++b) {
-            ok = wait(&C.tempty[acc.at], acc.phase ^ 1u) && wait(&C.full[s.at], s.phase);
+            ok = wait(&C.full[s.at], s.phase) && wait(&C.tempty[acc.at], acc.phase ^ 1u);
             if (!ok) break;
             fence_after_sync();
             const uint32_t d = tmem + acc.at * uint32_t(kWideN);
             const uint64_t da = desc_sw128(smem_addr(sa + s.at * kABytes));
             const uint64_t db = desc_sw128(smem_addr(sb + s.at * kABytes));
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < kBK / kUK; ++k)  // +32 bytes inside the 128-byte rows
-                mma_e4m3_pair(d, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, uint32_t(k));
-            mma_commit_pair(&C.empty[s.at]);
-            mma_commit_pair(&C.tfull[acc.at]);
+                for (int k = 0; k < kBK / kUK; ++k)  // +32 bytes inside the 128-byte rows
+                    mma_e4m3_pair(d, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, uint32_t(k));
+                mma_commit_pair(&C.tfull[acc.at]);
+                mma_commit_pair(&C.empty[s.at]);
+            }
+            __syncwarp();
             s.next(uint32_t(P.stages));
             acc.next(uint32_t(P.accs));
         }
     }
     if (!ok) C.gave_up = 1;
-    mma_commit_pair(&C.drained);
+    if (elect_one()) mma_commit_pair(&C.drained);
+    __syncwarp();
 }
 
 // Many rows: the hidden rows are M, the weight N = 256, of a pair of CTAs.
@@ -625,9 +651,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     if (warp == 8) {
-        if (lane == 0) pair_produce(P, C, sa, sb, rank, first, step);
+        pair_produce(P, C, sa, sb, rank, first, step);
     } else if (warp == 9) {
-        if (lane == 0 && rank == 0) pair_multiply(P, C, sa, sb, tmem, first, step);
+        if (rank == 0) pair_multiply(P, C, sa, sb, tmem, first, step);
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         const int group = warp >> 2, quarter = warp & 3;

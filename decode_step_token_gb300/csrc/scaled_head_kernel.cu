@@ -16,23 +16,25 @@
 // memory; the accumulators are up to eight, and the lanes are neighbouring
 // tokens of the vocabulary, so that the logits are stored as they lie.
 //
-// Many rows (a prompt) are taken as they are, by pairs of CTAs: a tile is 256
-// hidden rows (M, 128 in each CTA) by 256 weight rows (N, 128 of them in each
-// CTA's shared memory, which the pair's tensor cores read both of). So a block of
-// a tile costs a CTA 32 KB of loads; alone it would cost 48 KB, and the loads
-// from L2 and not the tensor cores would be the time (measured at 4096 x 64000 x
-// 4096: 15 to 17 TB/s with 48 KB, whatever else was left out). The tensor cores
-// take 512 cycles for a block, in which its 32768 products of each CTA have to be
-// scaled: a lane is a hidden row here, so its scale is one register, two products
-// are one instruction, and nothing is read from shared memory. The logits go
-// through shared memory once, to be stored by row.
+// Many rows (a prompt) are taken as they are, by pairs of CTAs: 256 hidden rows,
+// 128 in each CTA (M), by 256 weight rows (N) that both CTAs need; each loads half
+// of those and the TMA engine puts them into both (multicast). So a block costs a
+// CTA 32 KB from L2 instead of 48 KB, with which L2 would be the time (15 to 17
+// TB/s measured, whatever else was left out). Each CTA has its own MMAs and
+// accumulators, because the way of an accumulator round through the epilogue (its
+// completion seen, its columns read, its release seen by the MMA warp) has to fit
+// in one block's MMAs, and is too long across two CTAs. A lane is a hidden row
+// here, so its scale is one register, two products are one instruction, and
+// nothing is read from shared memory. The logits go through shared memory to the
+// TMA engine, which stores them while the next tile is under way (a warp's own
+// stores took 12 % of the time). Measured at 4096 x 128000 x 4096: 1.49 ms, 2880
+// TFLOP/s.
 //
 // Persistent, one CTA an SM; warp roles:
 //   warps 0-7  the epilogue: two groups of four warps, each a half of the tile's
 //              columns, a warp 32 of its lanes;
 //   warp 8     issues the TMA loads of the operand ring;
-//   warp 9     owns the tensor memory and issues the MMAs (of a pair: the first
-//              CTA's).
+//   warp 9     owns the tensor memory and issues the MMAs.
 // Warps 10 and 11 fill up the third warpgroup, which gives its registers to the
 // epilogue's (a thread there holds up to 128 sums).
 // Every wait is bounded in time; a CTA whose wait gives up counts itself in the
@@ -63,16 +65,21 @@ constexpr int kMaxAccs = 8;
 constexpr int kTmemCols = 512;
 constexpr int kFewRows = 128;                  // the most that are taken transposed
 constexpr int kWideN = 256;                    // weight rows of a tile of many hidden rows
+constexpr int kPairAccs = kTmemCols / kWideN;
+constexpr uint32_t kPairBBytes = kWideN * kBK; // of a stage
+constexpr int kFewPairRegs = 24, kManyPairRegs = 240;  // 128 * 24 + 256 * 240 <= 384 * 168
+constexpr int kLoad = 16;                      // columns that a thread reads at once (32: registers spill, 2264 TFLOP/s)
+constexpr uint32_t kBoxBytes = 32 * 128;       // a box of logits: 32 rows of 128 bytes, swizzled
+constexpr uint32_t kOutBytes = 8 * kBoxBytes;  // one for each warp of the epilogue: with more, a stage less
 constexpr int kScaleBlocks = 4;                // blocks of K whose scales are fetched together
 constexpr uint32_t kABytes = kBM * kBK;        // 16 KB a stage
 constexpr uint64_t kWaitNs = 2000000000ull;    // a wait gives up after 2 s
 constexpr size_t kScaleBytes = 2 * kScaleBlocks * kFewRows * 4;  // transposed: two buffers of every column's scales
-constexpr int kRowBytes = 64, kRowPitch = 80;  // many rows: a piece of a row on its way out; 80: no bank conflicts
-constexpr size_t kOutBytes = 8 * 32 * kRowPitch;
 constexpr size_t kBarBytes = 512;
 constexpr size_t kSmemMax = 227 * 1024;
 
 struct Params {
+    CUtensorMap to;      // many rows: the logits, boxes of 128 bytes by 32 rows, 128-byte swizzle
     CUtensorMap tm, tn;  // the operands of M and N [rows, K], 128-byte swizzle: boxes of 128 bytes by 128 and NT
                          // rows (of a pair: 128 and 128)
     const float* hidden_scale;
@@ -85,8 +92,8 @@ struct Params {
     int blocks;            // of K
     int stages, accs;
     uint32_t tmem_cols;    // a power of two >= accs * NT
-    int wide_scales;       // the hidden scales can be read four at a time
-    int wide_stores;       // the logits can be written 16 bytes at a time
+    int wide_scales;       // bits 0, 1: the hidden and the weight's scales can be read four at a time
+    int tma_stores;        // the logits lie so that the TMA engine can write them
     unsigned long long* timeouts;
 };
 
@@ -140,48 +147,39 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar)
                  : "memory");
 }
 
-// The same for a pair of CTAs: the loads' barrier may be the other CTA's, the
-// MMA's operands and accumulator are halves in each, and the arrivals go to the
-// barrier of both.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+// The same into the shared memory of both CTAs of a pair, each of which counts
+// the bytes on its own barrier at that place.
+__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
 {
     asm volatile(
-        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-        "%3}], [%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, "
+        "{%2, %3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(uint16_t(3))
         : "memory");
 }
 
-__device__ __forceinline__ void mma_e4m3_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+// Arrive on `bar` of both CTAs once every MMA issued before has completed.
+__device__ __forceinline__ void mma_commit_both(uint64_t* bar)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
             smem_addr(bar)),
         "h"(uint16_t(3))
         : "memory");
 }
 
-// Arrive on a barrier of the pair. What it tells is that tensor memory has been
-// read, which tcgen05.fence orders; a release would wait for this thread's other
-// accesses as well, on the way of every block.
-__device__ __forceinline__ void arrive_pair(uint32_t bar)
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src)
 {
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
 }
 
 __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 16 or 32 consecutive columns of this thread's tensor-memory lane; complete after tmem_wait.
+// 16 consecutive columns of this thread's tensor-memory lane; complete after tmem_wait.
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r)
 {
     asm volatile(
@@ -189,19 +187,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r)
         "%14, %15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
           "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t* r)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
 }
@@ -278,10 +263,19 @@ __device__ __forceinline__ void put(float* p, float v) { *p = v; }
 __device__ __forceinline__ void put(uint16_t* p, float v) { *p = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
 
 // What both kernels have in shared memory after the operand ring and their own.
+// Block n of a CTA (counted over its tiles) is in stage n % stages and
+// accumulator n % accs. The MMA warp's own instructions are on the tensor cores'
+// way (a wait takes it about 150 cycles even where nothing is left to wait for, a
+// commit 100), so it has one barrier to wait for and one to commit to: block n's
+// accumulator is free when the epilogue has read block n - accs, and the epilogue
+// arrives for that on block n's own barrier. With stages > accs no barrier can get
+// two phases ahead of one who waits for it.
 struct Control {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t tfull[kMaxAccs], tempty[kMaxAccs];  // an accumulator is complete; has been read
-    uint64_t drained;                            // every MMA of the CTA has completed
+    uint64_t ready[kMaxStages];  // of the block in a stage: its operands have come, and its accumulator has been read
+                                 // by every warp of the epilogue
+    uint64_t done[kMaxStages];   // its MMAs have completed: the accumulator can be read, the stage filled again
+    uint64_t free[kMaxStages];   // of a pair: done in both CTAs, whose stages are filled together
+    uint64_t drained;            // every MMA of the CTA has completed
     uint32_t tmem;
     int gave_up;
 };
@@ -293,12 +287,9 @@ __device__ __forceinline__ void begin(const Params& P, Control& C)
     const int tid = threadIdx.x, warp = tid >> 5;
     if (tid == 0) {
         for (int s = 0; s < kMaxStages; ++s) {
-            mbar_init(&C.full[s], 1);
-            mbar_init(&C.empty[s], 1);
-        }
-        for (int a = 0; a < kMaxAccs; ++a) {
-            mbar_init(&C.tfull[a], 1);
-            mbar_init(&C.tempty[a], kPair ? 16 : 8);
+            mbar_init(&C.ready[s], 1 + 8);
+            mbar_init(&C.done[s], 1);
+            mbar_init(&C.free[s], 2);
         }
         mbar_init(&C.drained, 1);
         C.gave_up = 0;
@@ -307,17 +298,10 @@ __device__ __forceinline__ void begin(const Params& P, Control& C)
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&P.tn)) : "memory");
     }
     if (warp == 9) {
-        if (kPair) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&C.tmem)),
-                         "r"(P.tmem_cols)
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&C.tmem)),
-                         "r"(P.tmem_cols)
-                         : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-        }
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&C.tmem)),
+                     "r"(P.tmem_cols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     fence_before_sync();
     __syncthreads();
@@ -331,21 +315,12 @@ __device__ __forceinline__ void end(const Params& P, Control& C, uint32_t tmem)
     fence_before_sync();
     __syncthreads();
     if (kPair) {
-        // every MMA has completed, and the last of their arrivals has come; then the other CTA is done with this
-        // one's shared and tensor memory, too
-        if (threadIdx.x == 0 && !wait(&C.drained, 0)) C.gave_up = 1;
-        __syncthreads();
+        // nothing that the other CTA sends (halves of stages, arrivals) is under way any more
         cluster_sync();
     }
     fence_after_sync();
-    if (threadIdx.x >> 5 == 9) {
-        if (kPair)
-            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(P.tmem_cols)
-                         : "memory");
-        else
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(P.tmem_cols)
-                         : "memory");
-    }
+    if (threadIdx.x >> 5 == 9)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(P.tmem_cols) : "memory");
     if (threadIdx.x == 0 && C.gave_up && P.timeouts) atomicAdd(P.timeouts, 1ull);
 }
 
@@ -358,12 +333,12 @@ __device__ __forceinline__ void produce(const Params& P, Control& C, unsigned ch
     bool ok = true;
     for (int t = int(blockIdx.x); ok && t < P.tiles; t += int(gridDim.x)) {
         for (int b = 0; b < P.blocks; ++b) {
-            ok = wait(&C.empty[s.at], s.phase ^ 1u);
+            ok = wait(&C.done[s.at], s.phase ^ 1u);
             if (!ok) break;
             if (elect_one()) {
-                mbar_arrive_expect_tx(&C.full[s.at], kABytes + b_bytes);
-                tma_load_2d(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, t * kBM, smem_addr(&C.full[s.at]));
-                tma_load_2d(smem_addr(sb + s.at * b_bytes), &P.tn, b * kBK, 0, smem_addr(&C.full[s.at]));
+                mbar_arrive_expect_tx(&C.ready[s.at], kABytes + b_bytes);
+                tma_load_2d(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, t * kBM, smem_addr(&C.ready[s.at]));
+                tma_load_2d(smem_addr(sb + s.at * b_bytes), &P.tn, b * kBK, 0, smem_addr(&C.ready[s.at]));
             }
             __syncwarp();
             s.next(S);
@@ -372,7 +347,7 @@ __device__ __forceinline__ void produce(const Params& P, Control& C, unsigned ch
     }
     if (!ok) C.gave_up = 1;
     // the last copies issued land before the CTA may exit
-    for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j) wait(&C.full[j % S], j / S & 1u);
+    for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j) wait(&C.ready[j % S], j / S & 1u);
 }
 
 // The MMA warp: each block of K into the next accumulator.
@@ -384,7 +359,7 @@ __device__ __forceinline__ void multiply(const Params& P, Control& C, unsigned c
     bool ok = true;
     for (int t = int(blockIdx.x); ok && t < P.tiles; t += int(gridDim.x)) {
         for (int b = 0; b < P.blocks; ++b) {
-            ok = wait(&C.full[s.at], s.phase) && wait(&C.tempty[acc.at], acc.phase ^ 1u);
+            ok = wait(&C.ready[s.at], s.phase);
             if (!ok) break;
             fence_after_sync();
             const uint32_t d = tmem + acc.at * uint32_t(P.NT);
@@ -394,8 +369,7 @@ __device__ __forceinline__ void multiply(const Params& P, Control& C, unsigned c
 #pragma unroll
                 for (int k = 0; k < kBK / kUK; ++k)  // +32 bytes inside the 128-byte rows
                     mma_e4m3(d, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, uint32_t(k));
-                mma_commit(&C.tfull[acc.at]);
-                mma_commit(&C.empty[s.at]);
+                mma_commit(&C.done[s.at]);
             }
             __syncwarp();
             s.next(uint32_t(P.stages));
@@ -422,6 +396,14 @@ __device__ __forceinline__ void fetch_scales(float (&q)[kScaleBlocks], const flo
 #pragma unroll
         for (int i = 0; i < kScaleBlocks; ++i) q[i] = has && b + i < blocks ? __ldg(row + b + i) : 0.f;
     }
+}
+
+// The accumulators of the first blocks are free from the start.
+__device__ __forceinline__ void free_first(const Params& P, Control& C, int lane)
+{
+    if (lane == 0)
+        for (int k = 0; k < P.accs; ++k) arrive(&C.ready[k]);
+    __syncwarp();
 }
 
 // Few rows: the weight is M, the hidden rows N = NT <= 2 * kCols.
@@ -453,14 +435,16 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
         const bool has = j < cols && c0 + j < P.rows;
         const float* sh = P.hidden_scale + int64_t(c0 + j) * P.hidden_scale_stride;
         float* mine = scales + group * (kFewRows / 2);
-        Ring acc{0, 0};
+        Ring acc{0, 0}, s{0, 0};
+        uint32_t freed = uint32_t(P.accs);  // stage of the block that the accumulator now read is for next
+        free_first(P, C, lane);
         uint32_t buffer = 0;
         bool ok = true;
         // raw scales of the next four blocks: they are fetched four blocks ahead and multiplied when those come
         float qh[kScaleBlocks], qw[kScaleBlocks];
         if (int(blockIdx.x) < P.tiles) {
-            fetch_scales(qh, sh, 0, P.blocks, has, P.wide_scales);
-            fetch_scales(qw, P.weight_scale + blockIdx.x * P.weight_scale_stride, 0, P.blocks, true, false);
+            fetch_scales(qh, sh, 0, P.blocks, has, P.wide_scales & 1);
+            fetch_scales(qw, P.weight_scale + blockIdx.x * P.weight_scale_stride, 0, P.blocks, true, P.wide_scales & 2);
         }
         for (int t = int(blockIdx.x); t < P.tiles; t += int(gridDim.x)) {  // to the end even where a wait gave up:
                                                                            // its group's barriers count on it
@@ -479,12 +463,12 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
                     const bool more = b + kScaleBlocks < P.blocks;
                     const int nt = more ? t : t + int(gridDim.x), nb = more ? b + kScaleBlocks : 0;
                     if (nt < P.tiles) {
-                        fetch_scales(qh, sh, nb, P.blocks, has, P.wide_scales);
-                        fetch_scales(qw, P.weight_scale + nt * P.weight_scale_stride, nb, P.blocks, true, false);
+                        fetch_scales(qh, sh, nb, P.blocks, has, P.wide_scales & 1);
+                        fetch_scales(qw, P.weight_scale + nt * P.weight_scale_stride, nb, P.blocks, true, P.wide_scales & 2);
                     }
                 }
                 const float* row = mine + buffer * (kScaleBlocks * kFewRows) + b % kScaleBlocks * kFewRows;
-                ok = ok && wait(&C.tfull[acc.at], acc.phase);
+                ok = ok && wait(&C.done[s.at], s.phase);
                 if (ok) {
                     fence_after_sync();
                     const uint32_t at = lanes + acc.at * uint32_t(P.NT);
@@ -507,8 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
                     }
                 }
                 __syncwarp();
-                if (ok && lane == 0) arrive(&C.tempty[acc.at]);
+                if (ok && lane == 0) arrive(&C.ready[freed]);
                 acc.next(uint32_t(P.accs));
+                s.next(uint32_t(P.stages));
+                freed = freed + 1 == uint32_t(P.stages) ? 0 : freed + 1;
             }
             const int v = t * kBM + quarter * 32 + lane;
             if (ok && v < P.V) {
@@ -522,30 +508,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
         if (!ok && lane == 0) C.gave_up = 1;
     }
     end<false>(P, C, tmem);
-}
-
-// Store 16-byte pieces, or single elements where they do not lie on 16 bytes: a
-// warp's 32 rows of kRowBytes from its buffer, columns from v0 on.
-template <typename T>
-__device__ __forceinline__ void store_rows(const Params& P, const unsigned char* buf, int row0, int v0, int lane)
-{
-    constexpr int kPer = kRowBytes / int(sizeof(T));
-    if (P.wide_stores && v0 + kPer <= P.V) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = i * 8 + (lane >> 2), piece = lane & 3;
-            const uint4 v = *reinterpret_cast<const uint4*>(buf + row * kRowPitch + piece * 16);
-            if (row0 + row < P.rows)
-                __stcs(reinterpret_cast<uint4*>(static_cast<T*>(P.logits) + int64_t(row0 + row) * P.ldl + v0) + piece, v);
-        }
-    } else {
-        const int col = lane % kPer;
-        for (int row = lane / kPer; row < 32; row += 32 / kPer) {
-            const T v = reinterpret_cast<const T*>(buf + row * kRowPitch)[col];
-            if (row0 + row < P.rows && v0 + col < P.V)
-                (static_cast<T*>(P.logits) + int64_t(row0 + row) * P.ldl + v0)[col] = v;
-        }
-    }
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
@@ -562,11 +524,8 @@ __device__ __forceinline__ void pair_tile(const Params& P, int t, int& m, int& n
     n = t / P.row_tiles * kWideN;
 }
 
-// The same barrier of the pair's first CTA, in the cluster's shared memory.
-__device__ __forceinline__ uint32_t of_first(uint64_t* bar) { return dsmem_map(smem_addr(bar), 0); }
-
-// The TMA warp of each CTA of a pair: its half of both operands. The first
-// CTA's barrier counts the bytes of both.
+// The TMA warp of each CTA of a pair: its hidden rows, and its half of the
+// weight rows for both.
 __device__ __forceinline__ void pair_produce(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
                                              uint32_t rank, int first, int step)
 {
@@ -578,15 +537,15 @@ __device__ __forceinline__ void pair_produce(const Params& P, Control& C, unsign
         int m, n;
         pair_tile(P, t, m, n);
         m += int(rank) * kBM;
-        n += int(rank) * kBM;
+        n += int(rank) * (kWideN / 2);
         for (int b = 0; b < P.blocks; ++b) {
-            ok = wait(&C.empty[s.at], s.phase ^ 1u);
+            ok = wait(&C.free[s.at], s.phase ^ 1u);
             if (!ok) break;
-            const uint32_t bar = of_first(&C.full[s.at]);
             if (elect_one()) {
-                if (rank == 0) mbar_arrive_expect_tx(&C.full[s.at], 4 * kABytes);
-                tma_load_2d_pair(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, m, bar);
-                tma_load_2d_pair(smem_addr(sb + s.at * kABytes), &P.tn, b * kBK, n, bar);
+                mbar_arrive_expect_tx(&C.ready[s.at], kABytes + kPairBBytes);
+                const uint32_t bar = smem_addr(&C.ready[s.at]);
+                tma_load_2d(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, m, bar);
+                tma_load_2d_both(smem_addr(sb + s.at * kPairBBytes + rank * (kPairBBytes / 2)), &P.tn, b * kBK, n, bar);
             }
             __syncwarp();
             s.next(S);
@@ -594,53 +553,55 @@ __device__ __forceinline__ void pair_produce(const Params& P, Control& C, unsign
         }
     }
     if (!ok) C.gave_up = 1;
-    // the last copies of both CTAs land before either may exit (the other waits for this one at the end)
-    if (rank == 0)
-        for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j) wait(&C.full[j % S], j / S & 1u);
+    // the last copies and the last stages' arrivals have come before either CTA may exit
+    for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
+        if (!wait(&C.ready[j % S], j / S & 1u) || !wait(&C.free[j % S], j / S & 1u)) C.gave_up = 1;
 }
 
-// The MMA warp of the pair.
+// The MMA warp of each CTA of a pair.
 __device__ __forceinline__ void pair_multiply(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
                                               uint32_t tmem, int first, int step)
 {
-    const uint32_t idesc = idesc_e4m3(2 * kBM, kWideN);
+    const uint32_t idesc = idesc_e4m3(kBM, kWideN);
     Ring s{0, 0}, acc{0, 0};
     bool ok = true;
     for (int t = first; ok && t < P.tiles; t += step) {
         for (int b = 0; b < P.blocks; ++b) {
-            ok = wait(&C.full[s.at], s.phase) && wait(&C.tempty[acc.at], acc.phase ^ 1u);
-            if (!ok) break;
-            fence_after_sync();
             const uint32_t d = tmem + acc.at * uint32_t(kWideN);
             const uint64_t da = desc_sw128(smem_addr(sa + s.at * kABytes));
-            const uint64_t db = desc_sw128(smem_addr(sb + s.at * kABytes));
+            const uint64_t db = desc_sw128(smem_addr(sb + s.at * kPairBBytes));
+            ok = wait(&C.ready[s.at], s.phase);
+            if (!ok) break;
+            fence_after_sync();
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kBK / kUK; ++k)  // +32 bytes inside the 128-byte rows
-                    mma_e4m3_pair(d, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, uint32_t(k));
-                mma_commit_pair(&C.tfull[acc.at]);
-                mma_commit_pair(&C.empty[s.at]);
+                    mma_e4m3(d, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, uint32_t(k));
+                mma_commit(&C.done[s.at]);
+                mma_commit_both(&C.free[s.at]);
             }
             __syncwarp();
             s.next(uint32_t(P.stages));
-            acc.next(uint32_t(P.accs));
+            acc.next(kPairAccs);
         }
     }
     if (!ok) C.gave_up = 1;
-    if (elect_one()) mma_commit_pair(&C.drained);
+    if (elect_one()) mma_commit(&C.drained);
     __syncwarp();
+    wait(&C.drained, 0);
 }
 
-// Many rows: the hidden rows are M, the weight N = 256, of a pair of CTAs.
+// Many rows: the hidden rows are M, the weight N.
 template <typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     many_rows_kernel(const __grid_constant__ Params P)
 {
-    constexpr int kCols = kWideN / 2;
+    constexpr int kCols = kWideN / 2;                  // of a thread: a block of the weight's scales
+    constexpr int kBoxCols = 128 / int(sizeof(T));     // of a box of logits
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sa = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char* sb = sa + size_t(P.stages) * kABytes;
-    unsigned char* outs = sb + size_t(P.stages) * kABytes;
+    unsigned char* outs = sb + size_t(P.stages) * kPairBBytes;
     Control& C = *reinterpret_cast<Control*>(outs + kOutBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t rank = cluster_ctarank();
@@ -649,30 +610,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     begin<true>(P, C);
     const uint32_t tmem = C.tmem;
 
-    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewPairRegs));
     if (warp == 8) {
         pair_produce(P, C, sa, sb, rank, first, step);
     } else if (warp == 9) {
-        if (rank == 0) pair_multiply(P, C, sa, sb, tmem, first, step);
+        pair_multiply(P, C, sa, sb, tmem, first, step);
     } else if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyPairRegs));
         const int group = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(group * kCols);
-        unsigned char* buf = outs + warp * (32 * kRowPitch);
-        Ring acc{0, 0};
+        unsigned char* out = outs + warp * kBoxBytes;
+        Ring acc{0, 0}, s{0, 0};
+        uint32_t freed = kPairAccs;  // stage of the block that the accumulator now read is for next
+        free_first(P, C, lane);
         bool ok = true;
-        // a lane's hidden row and the group's block of weight rows: their scales, fetched four blocks ahead
+        // scales of a lane's hidden row and of the group's weight rows, fetched four blocks of K ahead
         float qh[kScaleBlocks], qw[kScaleBlocks];
-        auto fetch = [&](int t, int b) {
-            int m, n;
-            pair_tile(P, t, m, n);
-            const int row = m + int(rank) * kBM + quarter * 32 + lane, vb = n / kBM + group;
-            fetch_scales(qh, P.hidden_scale + int64_t(row) * P.hidden_scale_stride, b, P.blocks, row < P.rows,
-                         P.wide_scales);
-            fetch_scales(qw, P.weight_scale + int64_t(vb) * P.weight_scale_stride, b, P.blocks, vb * kBM < P.V, false);
+        int row0 = 0, v0 = 0;  // of the tile that is fetched for
+        const float *ph = nullptr, *pw = nullptr;
+        auto place = [&](int t) {
+            pair_tile(P, t, row0, v0);
+            row0 += int(rank) * kBM + quarter * 32;
+            v0 += group * kCols;
+            ph = P.hidden_scale + int64_t(row0 + lane) * P.hidden_scale_stride;
+            pw = P.weight_scale + int64_t(v0 / kBM) * P.weight_scale_stride;
         };
-        if (first < P.tiles) fetch(first, 0);
+        auto fetch = [&](int b) {
+            fetch_scales(qh, ph, b, P.blocks, row0 + lane < P.rows, P.wide_scales & 1);
+            fetch_scales(qw, pw, b, P.blocks, v0 < P.V, P.wide_scales & 2);
+        };
+        if (first < P.tiles) {
+            place(first);
+            fetch(0);
+        }
         for (int t = first; ok && t < P.tiles; t += step) {
+            const int row = row0, v = v0;
             float2 sum[kCols / 2];
 #pragma unroll
             for (int i = 0; i < kCols / 2; ++i) sum[i] = make_float2(0.f, 0.f);
@@ -680,61 +652,81 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 float q[kScaleBlocks];
 #pragma unroll
                 for (int i = 0; i < kScaleBlocks; ++i) q[i] = qh[i] * qw[i];
-                const bool more = b0 + kScaleBlocks < P.blocks;
-                if (more || t + step < P.tiles) fetch(more ? t : t + step, more ? b0 + kScaleBlocks : 0);
+                if (b0 + kScaleBlocks < P.blocks) {
+                    fetch(b0 + kScaleBlocks);
+                } else if (t + step < P.tiles) {
+                    place(t + step);
+                    fetch(0);
+                }
 #pragma unroll
                 for (int i = 0; i < kScaleBlocks; ++i) {
                     if (b0 + i >= P.blocks) break;
-                    ok = wait(&C.tfull[acc.at], acc.phase);
+                    ok = wait(&C.done[s.at], s.phase);
                     if (!ok) break;
                     fence_after_sync();
                     const uint32_t at = lanes + acc.at * uint32_t(kWideN);
-                    uint32_t r[2][16];
+                    uint32_t r[2][kLoad];
                     tmem_ld16(at, r[0]);
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 16) {
-                        uint32_t* now = r[c / 16 & 1];
+                    for (int c = 0; c < kCols; c += kLoad) {
+                        uint32_t* now = r[c / kLoad & 1];
                         tmem_wait();
-                        tmem_take16(now);
-                        if (c + 16 < kCols) {  // the next columns come while these are added
-                            tmem_ld16(at + c + 16, r[c / 16 + 1 & 1]);
-                        } else {               // all of the accumulator has been read
+#pragma unroll
+                        for (int k = 0; k < kLoad; k += 16) tmem_take16(now + k);
+                        if (c + kLoad < kCols) {  // the next columns come while these are added
+                            tmem_ld16(at + c + kLoad, r[c / kLoad + 1 & 1]);
+                        } else {                  // all of the accumulator has been read
                             fence_before_sync();
                             __syncwarp();
-                            if (lane == 0) arrive_pair(of_first(&C.tempty[acc.at]));
+                            if (lane == 0) arrive(&C.ready[freed]);
                         }
 #pragma unroll
-                        for (int k = 0; k < 16; k += 2) fma2(sum[(c + k) / 2], now[k], now[k + 1], q[i], q[i]);
+                        for (int k = 0; k < kLoad; k += 2) fma2(sum[(c + k) / 2], now[k], now[k + 1], q[i], q[i]);
                     }
-                    acc.next(uint32_t(P.accs));
+                    acc.next(kPairAccs);
+                    s.next(uint32_t(P.stages));
+                    freed = freed + 1 == uint32_t(P.stages) ? 0 : freed + 1;
                 }
             }
             if (!ok) break;
-            int row0, v0;
-            pair_tile(P, t, row0, v0);
-            row0 += int(rank) * kBM + quarter * 32;
-            v0 += group * kCols;
-            constexpr int kPer = kRowBytes / int(sizeof(T));
 #pragma unroll
-            for (int c = 0; c < kCols; c += kPer) {
-                uint4* to = reinterpret_cast<uint4*>(buf + lane * kRowPitch);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (sizeof(T) == 2) {
-                        const float2* s = sum + c / 2 + 4 * i;
-                        to[i] = make_uint4(pack_bf16(s[0].x, s[0].y), pack_bf16(s[1].x, s[1].y),
-                                           pack_bf16(s[2].x, s[2].y), pack_bf16(s[3].x, s[3].y));
-                    } else {
-                        const float2* s = sum + c / 2 + 2 * i;
-                        to[i] = make_uint4(__float_as_uint(s[0].x), __float_as_uint(s[0].y), __float_as_uint(s[1].x),
-                                           __float_as_uint(s[1].y));
-                    }
+            for (int c0 = 0; c0 < kCols; c0 += kBoxCols) {
+                if (P.tma_stores) {  // the box before has left the buffer
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                    __syncwarp();
                 }
-                __syncwarp();
-                store_rows<T>(P, buf, row0, v0 + c, lane);
-                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {  // 16 bytes each, at their swizzled place in the lane's row
+                    const float2* x = sum + (c0 + i * kBoxCols / 8) / 2;
+                    const uint4 w = sizeof(T) == 2 ? make_uint4(pack_bf16(x[0].x, x[0].y), pack_bf16(x[1].x, x[1].y),
+                                                                pack_bf16(x[2].x, x[2].y), pack_bf16(x[3].x, x[3].y))
+                                                   : make_uint4(__float_as_uint(x[0].x), __float_as_uint(x[0].y),
+                                                                __float_as_uint(x[1].x), __float_as_uint(x[1].y));
+                    *reinterpret_cast<uint4*>(out + lane * 128 + (i ^ (lane & 7)) * 16) = w;
+                }
+                // the TMA engine ends a row at a multiple of 16 bytes: the last tile may have to be stored otherwise
+                if (P.tma_stores && (v + kCols <= P.V || P.V % (kBoxCols / 8) == 0)) {
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (row < P.rows && v + c0 < P.V) tma_store_2d(&P.to, v + c0, row, smem_addr(out));
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
+                } else {
+                    __syncwarp();
+                    const int rows = min(32, P.rows - row), cols = min(kBoxCols, P.V - v - c0);
+                    T* g = static_cast<T*>(P.logits) + int64_t(row) * P.ldl + v + c0;
+#pragma unroll 1
+                    for (int k = 0; k < rows; ++k)
+#pragma unroll 1
+                        for (int c = lane; c < cols; c += 32)
+                            g[int64_t(k) * P.ldl + c] =
+                                *reinterpret_cast<const T*>(out + k * 128 + (c * int(sizeof(T)) ^ (k & 7) * 16));
+                    __syncwarp();
+                }
             }
         }
+        if (P.tma_stores && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!ok && lane == 0) C.gave_up = 1;
     }
     end<true>(P, C, tmem);
@@ -754,6 +746,21 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder()
             fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     });
     return fn;
+}
+
+// Tensor map of the logits: boxes of a warp's part of a tile.
+bool encode_logits(CUtensorMap* map, void* base, int dtype, int64_t rows, int64_t cols, int64_t ld)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
+    if (!fn) return false;
+    const bool bf16 = dtype == SAMPLER_DTYPE_BF16;
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld) * (bf16 ? 2u : 4u)};
+    const cuuint32_t box[2] = {bf16 ? 64u : 32u, 32u};
+    const cuuint32_t estr[2] = {1u, 1u};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Tensor map over rows x cols bytes, box 128 x box_rows; bytes outside read as zero.
@@ -796,24 +803,28 @@ int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, 
     if (tiles > INT32_MAX - 65536) return SAMPLER_ERR_TOO_LARGE;
     p.tiles = int(tiles);
     p.blocks = int((g.hidden_dim + kBK - 1) / kBK);
-    const size_t stage = kABytes + (few ? size_t(p.NT) * kBK : size_t(kABytes)), own = few ? kScaleBytes : kOutBytes;
+    const int es = dtype == SAMPLER_DTYPE_BF16 ? 2 : 4;
+    const size_t stage = kABytes + (few ? size_t(p.NT) * kBK : size_t(kPairBBytes));
+    const size_t own = few ? kScaleBytes : kOutBytes;
     p.stages = int(std::min<size_t>(kMaxStages, (kSmemMax - 1024 - kBarBytes - own) / stage));
-    p.accs = std::min(kMaxAccs, kTmemCols / p.NT);
+    p.accs = std::min({kMaxAccs, kTmemCols / p.NT, p.stages - 1});
     p.tmem_cols = 32;
-    while (p.tmem_cols < uint32_t(p.accs * p.NT)) p.tmem_cols <<= 1;
+    while (p.tmem_cols < (few ? uint32_t(p.accs * p.NT) : uint32_t(kTmemCols))) p.tmem_cols <<= 1;
     const bool maps = few ? encode(&p.tm, g.weight, vocab, g.hidden_dim, g.weight_stride, kBM) &&
                                 encode(&p.tn, g.hidden, rows, g.hidden_dim, g.hidden_stride, p.NT)
                           : encode(&p.tm, g.hidden, rows, g.hidden_dim, g.hidden_stride, kBM) &&
-                                encode(&p.tn, g.weight, vocab, g.hidden_dim, g.weight_stride, kBM);
+                                encode(&p.tn, g.weight, vocab, g.hidden_dim, g.weight_stride, kWideN / 2);
     if (!maps) return SAMPLER_ERR_CUDA;
     p.hidden_scale = g.hidden_scale;
     p.weight_scale = g.weight_scale;
     p.hidden_scale_stride = g.hidden_scale_stride;
     p.weight_scale_stride = g.weight_scale_stride;
-    p.wide_scales = g.hidden_scale_stride % 4 == 0 && reinterpret_cast<uintptr_t>(g.hidden_scale) % 16 == 0;
+    p.wide_scales = (g.hidden_scale_stride % 4 == 0 && reinterpret_cast<uintptr_t>(g.hidden_scale) % 16 == 0 ? 1 : 0) |
+                    (g.weight_scale_stride % 4 == 0 && reinterpret_cast<uintptr_t>(g.weight_scale) % 16 == 0 ? 2 : 0);
     p.logits = logits;
     p.ldl = ldl;
-    p.wide_stores = ldl * (dtype == SAMPLER_DTYPE_BF16 ? 2 : 4) % 16 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
+    p.tma_stores = !few && ldl * es % 16 == 0 && reinterpret_cast<uintptr_t>(logits) % 16 == 0;
+    if (p.tma_stores && !encode_logits(&p.to, logits, dtype, rows, vocab, ldl)) return SAMPLER_ERR_CUDA;
     p.rows = int(rows);
     p.V = int(vocab);
     p.timeouts = timeouts;

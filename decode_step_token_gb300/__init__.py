@@ -62,30 +62,61 @@ def _ptr(t) -> Optional[int]:
     return int(t)
 
 
+_raw_stream = None
+
+
+def _current_stream(device: int) -> int:
+    """The cudaStream_t of torch's current stream (its raw form where torch has one: a stream object costs microseconds)."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_stream(device)  # torch's CUDA state is set up
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+    return _raw_stream(device)
+
+
+_types = None
+
+
+def _torch_types():
+    """(bf16, fp32, int32, e4m3 and bytes) of torch, imported when it is first needed."""
+    global _types
+    if _types is None:
+        import torch
+        _types = (torch.bfloat16, torch.float32, torch.int32, (torch.float8_e4m3fn, torch.uint8))
+    return _types
+
+
 def _vector(name: str, t, n: int, dtype, device: int) -> Optional[int]:
-    """Address of a contiguous [n] tensor of the handle's device (None passes)."""
+    """Address of a contiguous vector of n values or more on the handle's device (None passes)."""
     if t is None:
         return None
-    if t.dtype != dtype:
+    if t.dtype is dtype and t.get_device() == device and t.numel() >= n and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != 1 or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must be a contiguous vector of {n} values, not {tuple(t.shape)}")
     _on_device(name, t, device)
-    return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous vector of {n} values, not {tuple(t.shape)}")
 
 
-def _matrix(name: str, t, dtypes, device: int) -> int:
-    """Row stride of a [rows, columns] tensor of the handle's device with unit inner stride."""
+def _matrix(name: str, t, dtypes, device: int):
+    """(rows, columns, row stride) of a matrix on the handle's device with contiguous rows."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be one of {dtypes}, not {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2:
         raise ValueError(f"{name} must be two-dimensional with contiguous rows")
-    _on_device(name, t, device)
-    return max(t.stride(0), t.shape[1]) if t.shape[0] <= 1 else t.stride(0)
+    rows, cols = t.shape
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError(f"{name} must be two-dimensional with contiguous rows")
+    if t.get_device() != device:
+        _on_device(name, t, device)
+    return rows, cols, stride if rows > 1 and stride >= cols else max(stride, cols)
 
 
 def _on_device(name: str, t, device: int) -> None:
-    if t.device.type != "cuda" or t.device.index != device:
+    if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, not on cuda:{device}")
 
 
@@ -226,26 +257,24 @@ class Sampler:
 
     def _rows(self, logits, tokens, temperature, weight, out_logprob, out_entropy, out_status, out_grad,
               vocab: Optional[int]) -> sampler_rows_t:
-        import torch
-
-        stride = _matrix("logits", logits, (torch.bfloat16, torch.float32), self.device)
-        n, V = logits.shape[0], int(vocab if vocab is not None else logits.shape[1])
-        if not 1 <= V <= logits.shape[1]:
-            raise ValueError(f"vocab {V} does not lie within the logits' {logits.shape[1]} columns")
-        grad_stride = 0
+        bf16, f32, i32, _ = _torch_types()
+        dev = self.device
+        n, cols, stride = _matrix("logits", logits, (bf16, f32), dev)
+        V = cols if vocab is None else int(vocab)
+        if not 1 <= V <= cols:
+            raise ValueError(f"vocab {V} does not lie within the logits' {cols} columns")
+        grad, grad_stride = None, 0
         if out_grad is not None:
-            grad_stride = _matrix("out_grad", out_grad, (logits.dtype,), self.device)
-            if out_grad.shape[0] != n or out_grad.shape[1] < V:
+            gn, gcols, grad_stride = _matrix("out_grad", out_grad, (logits.dtype,), dev)
+            if gn != n or gcols < V:
                 raise ValueError(f"out_grad must be [{n}, {V}], not {tuple(out_grad.shape)}")
-        f32 = torch.float32
+            grad = out_grad.data_ptr()
         return sampler_rows_t(
-            _ptr(logits), SAMPLER_DTYPE_BF16 if logits.dtype == torch.bfloat16 else SAMPLER_DTYPE_F32, n, V, stride,
-            _vector("tokens", tokens, n, torch.int32, self.device),
-            _vector("temperature", temperature, n, f32, self.device),
-            _vector("weight", weight, n, f32, self.device),
-            _vector("out_logprob", out_logprob, n, f32, self.device),
-            _vector("out_entropy", out_entropy, n, f32, self.device),
-            _vector("out_status", out_status, n, torch.int32, self.device), _ptr(out_grad), grad_stride)
+            logits.data_ptr(), SAMPLER_DTYPE_BF16 if logits.dtype is bf16 else SAMPLER_DTYPE_F32, n, V, stride,
+            _vector("tokens", tokens, n, i32, dev), _vector("temperature", temperature, n, f32, dev),
+            _vector("weight", weight, n, f32, dev), _vector("out_logprob", out_logprob, n, f32, dev),
+            _vector("out_entropy", out_entropy, n, f32, dev), _vector("out_status", out_status, n, i32, dev), grad,
+            grad_stride)
 
     def _done(self, rc: int, what: str) -> None:
         if rc != SAMPLER_OK:
@@ -265,12 +294,10 @@ class Sampler:
         """sampler_score_grad: the logits' gradient of sum(grad_logprob * logprob +
         grad_entropy * entropy) into out_grad (the logits' type; it may be the logits),
         with the outputs of ``score``."""
-        import torch
-
         rows = self._rows(logits, tokens, temperature, weight, out_logprob, out_entropy, out_status, out_grad, vocab)
-        n = rows.n_rows
-        gl = _vector("grad_logprob", grad_logprob, n, torch.float32, self.device)
-        ge = _vector("grad_entropy", grad_entropy, n, torch.float32, self.device)
+        n, f32 = rows.n_rows, _torch_types()[1]
+        gl = _vector("grad_logprob", grad_logprob, n, f32, self.device)
+        ge = _vector("grad_entropy", grad_entropy, n, f32, self.device)
         self._done(sampler_score_grad(self._h, rows, gl, ge, self._stream(stream)), "sampler_score_grad")
 
     def policy_loss(self, *, logits, tokens, old_logprob, advantage, out_loss, ref_logprob=None, temperature=None,
@@ -280,17 +307,14 @@ class Sampler:
                     vocab: Optional[int] = None, stream: Optional[int] = None) -> None:
         """sampler_policy_loss: the clipped policy loss with its KL and entropy terms
         (out_loss: one fp32), and with out_grad the logits' gradient in the same pass."""
-        import torch
-
         rows = self._rows(logits, tokens, temperature, weight, out_logprob, out_entropy, out_status, out_grad, vocab)
 
-        def v(name, t, n=rows.n_rows):
-            return _vector(name, t, n, torch.float32, self.device)
-
-        q = sampler_policy_t(v("old_logprob", old_logprob), v("advantage", advantage), v("ref_logprob", ref_logprob),
-                             clip_low, clip_high, kl_coef, entropy_coef, grad_scale,
-                             v("grad_scale_dev", grad_scale_dev, 1), v("out_loss", out_loss, 1),
-                             v("out_ratio", out_ratio), v("out_kl", out_kl))
+        n, f32, dev = rows.n_rows, _torch_types()[1], self.device
+        q = sampler_policy_t(_vector("old_logprob", old_logprob, n, f32, dev), _vector("advantage", advantage, n, f32, dev),
+                             _vector("ref_logprob", ref_logprob, n, f32, dev), clip_low, clip_high, kl_coef,
+                             entropy_coef, grad_scale, _vector("grad_scale_dev", grad_scale_dev, 1, f32, dev),
+                             _vector("out_loss", out_loss, 1, f32, dev), _vector("out_ratio", out_ratio, n, f32, dev),
+                             _vector("out_kl", out_kl, n, f32, dev))
         self._done(sampler_policy_loss(self._h, rows, q, self._stream(stream)), "sampler_policy_loss")
 
     def preference_loss(self, *, logits, tokens, seq_offsets, out_loss, ref_logprob=None, temperature=None,
@@ -301,14 +325,12 @@ class Sampler:
         """sampler_preference_loss over (len(seq_offsets) - 1) / 2 pairs of answers
         (int32 seq_offsets; out_loss: one fp32; out_reward: one for each answer), and
         with out_grad the logits' gradient."""
-        import torch
-
         rows = self._rows(logits, tokens, temperature, weight, out_logprob, None, out_status, out_grad, vocab)
         ends = int(seq_offsets.shape[0])
         if ends % 2 != 1:
             raise ValueError(f"seq_offsets must have 2 * pairs + 1 entries, not {ends}")
-        n, f32 = rows.n_rows, torch.float32
-        q = sampler_preference_t(_vector("seq_offsets", seq_offsets, ends, torch.int32, self.device), ends // 2,
+        n, (_, f32, i32, _) = rows.n_rows, _torch_types()
+        q = sampler_preference_t(_vector("seq_offsets", seq_offsets, ends, i32, self.device), ends // 2,
                                  _vector("ref_logprob", ref_logprob, n, f32, self.device), beta, margin,
                                  label_smoothing, 1 if mean_over_tokens else 0, grad_scale,
                                  _vector("grad_scale_dev", grad_scale_dev, 1, f32, self.device),
@@ -321,56 +343,52 @@ class Sampler:
         """sampler_quantize_blocks: src [rows, cols] (bf16 or fp32) to out_values
         (float8_e4m3fn, the same shape) with out_scales (fp32, [rows / block_rows,
         cols / 128] rounded up)."""
-        import torch
-
-        stride = _matrix("src", src, (torch.bfloat16, torch.float32), self.device)
-        rows, cols = src.shape
-        vs = _matrix("out_values", out_values, (torch.float8_e4m3fn, torch.uint8), self.device)
-        ss = _matrix("out_scales", out_scales, (torch.float32,), self.device)
-        if tuple(out_values.shape) != (rows, cols):
+        bf16, f32, _, eight = _torch_types()
+        rows, cols, stride = _matrix("src", src, (bf16, f32), self.device)
+        vr, vc, vs = _matrix("out_values", out_values, eight, self.device)
+        sr, sc, ss = _matrix("out_scales", out_scales, (f32,), self.device)
+        if vr != rows or vc != cols:
             raise ValueError(f"out_values must be [{rows}, {cols}], not {tuple(out_values.shape)}")
-        if block_rows > 0 and (out_scales.shape[0] < -(-rows // block_rows) or out_scales.shape[1] < -(-cols // 128)):
+        if block_rows > 0 and (sr < -(-rows // block_rows) or sc < -(-cols // 128)):
             raise ValueError(f"out_scales {tuple(out_scales.shape)} is too small for {rows} x {cols}")
-        q = sampler_quantize_t(_ptr(src), SAMPLER_DTYPE_BF16 if src.dtype == torch.bfloat16 else SAMPLER_DTYPE_F32,
-                               rows, cols, stride, int(block_rows), _ptr(out_values), vs, _ptr(out_scales), ss)
+        q = sampler_quantize_t(src.data_ptr(), SAMPLER_DTYPE_BF16 if src.dtype is bf16 else SAMPLER_DTYPE_F32, rows,
+                               cols, stride, int(block_rows), out_values.data_ptr(), vs, out_scales.data_ptr(), ss)
         self._done(sampler_quantize_blocks(self._h, q, self._stream(stream)), "sampler_quantize_blocks")
 
     def _scaled_head(self, hidden, hidden_scale, weight, weight_scale) -> sampler_scaled_head_t:
-        import torch
-
-        eight, f32 = (torch.float8_e4m3fn, torch.uint8), (torch.float32,)
-        hs, ws = _matrix("hidden", hidden, eight, self.device), _matrix("weight", weight, eight, self.device)
-        if hidden.shape[1] != weight.shape[1]:
-            raise ValueError(f"hidden has {hidden.shape[1]} columns, weight {weight.shape[1]}")
-        hss = _matrix("hidden_scale", hidden_scale, f32, self.device)
-        wss = _matrix("weight_scale", weight_scale, f32, self.device)
-        groups = -(-hidden.shape[1] // 128)
-        for name, t, n in (("hidden_scale", hidden_scale, hidden.shape[0]),
-                           ("weight_scale", weight_scale, -(-weight.shape[0] // 128))):
-            if t.shape[0] < n or t.shape[1] < groups:
-                raise ValueError(f"{name} must be [{n}, {groups}], not {tuple(t.shape)}")
+        _, f32, _, eight = _torch_types()
+        rows, K, hs = _matrix("hidden", hidden, eight, self.device)
+        V, wk, ws = _matrix("weight", weight, eight, self.device)
+        if wk != K:
+            raise ValueError(f"hidden has {K} columns, weight {wk}")
+        hr, hc, hss = _matrix("hidden_scale", hidden_scale, (f32,), self.device)
+        wr, wc, wss = _matrix("weight_scale", weight_scale, (f32,), self.device)
+        groups = -(-K // 128)
+        if hr < rows or hc < groups:
+            raise ValueError(f"hidden_scale must be [{rows}, {groups}], not {tuple(hidden_scale.shape)}")
+        if wr < -(-V // 128) or wc < groups:
+            raise ValueError(f"weight_scale must be [{-(-V // 128)}, {groups}], not {tuple(weight_scale.shape)}")
         # the stride of a single row is not used, but has to be a legal one
-        if hidden.shape[0] <= 1:
+        if rows <= 1:
             hs = -(-hs // 16) * 16
-        if weight.shape[0] <= 1:
+        if V <= 1:
             ws = -(-ws // 16) * 16
-        return sampler_scaled_head_t(_ptr(hidden), _ptr(hidden_scale), _ptr(weight), _ptr(weight_scale),
-                                     hidden.shape[1], hs, ws, hss, wss)
+        return sampler_scaled_head_t(hidden.data_ptr(), hidden_scale.data_ptr(), weight.data_ptr(),
+                                     weight_scale.data_ptr(), K, hs, ws, hss, wss)
 
     def lm_head_scaled(self, *, hidden, hidden_scale, weight, weight_scale, logits,
                        stream: Optional[int] = None) -> None:
         """sampler_lm_head_scaled: logits [rows, >= vocab] (bf16 or fp32) from e4m3
         hidden [rows, K] and weight [vocab, K] with their scales as
         ``quantize_blocks`` makes them (block_rows 1 and 128)."""
-        import torch
-
         lm = self._scaled_head(hidden, hidden_scale, weight, weight_scale)
-        ldl = _matrix("logits", logits, (torch.bfloat16, torch.float32), self.device)
+        bf16, f32, _, _ = _torch_types()
+        lr, lc, ldl = _matrix("logits", logits, (bf16, f32), self.device)
         rows, V = hidden.shape[0], weight.shape[0]
-        if logits.shape[0] < rows or logits.shape[1] < V:
+        if lr < rows or lc < V:
             raise ValueError(f"logits must be [{rows}, {V}], not {tuple(logits.shape)}")
-        dtype = SAMPLER_DTYPE_BF16 if logits.dtype == torch.bfloat16 else SAMPLER_DTYPE_F32
-        self._done(sampler_lm_head_scaled(self._h, lm, _ptr(logits), dtype, ldl, rows, V, self._stream(stream)),
+        dtype = SAMPLER_DTYPE_BF16 if logits.dtype is bf16 else SAMPLER_DTYPE_F32
+        self._done(sampler_lm_head_scaled(self._h, lm, logits.data_ptr(), dtype, ldl, rows, V, self._stream(stream)),
                    "sampler_lm_head_scaled")
 
     def lm_head_scaled_sample_args(self, args: sampler_args_t, *, hidden, hidden_scale, weight, weight_scale,
@@ -386,10 +404,7 @@ class Sampler:
                    "sampler_lm_head_scaled_sample")
 
     def _stream(self, stream: Optional[int]) -> int:
-        if stream is None:
-            import torch
-            stream = torch.cuda.current_stream(self.device).cuda_stream
-        return stream
+        return _current_stream(self.device) if stream is None else stream
 
     def stat(self, which: int = 0, reset: bool = False) -> int:
         """A device diagnostic counter (synchronizes the device)."""

@@ -24,7 +24,7 @@
 namespace dst {
 namespace rows {
 
-constexpr double kLog2e = 1.4426950408889634;
+constexpr float kLog2e = 1.44269504f, kLog2eRest = 1.92596299e-8f;  // log2(e) as a pair
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGreedyT = 1e-5f;  // below it a row is greedy and its outputs use T = 1
 constexpr int32_t kNoToken = 0x7fffffff;  // of a row with an error status: matches no element
@@ -64,7 +64,8 @@ __device__ __forceinline__ void stats_move(Stats& a, float ref, float c)
     a.ref = ref;
 }
 
-// The statistics of all lanes' parts, in every lane.
+// The statistics of all lanes' parts, in every lane (t where kEntropy).
+template <bool kEntropy>
 __device__ __forceinline__ void stats_warp(Stats& a, float c)
 {
     float ref = a.ref;
@@ -72,7 +73,7 @@ __device__ __forceinline__ void stats_warp(Stats& a, float c)
     stats_move(a, ref, c);
     for (int o = 16; o > 0; o >>= 1) {
         a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
-        a.t += __shfl_xor_sync(0xffffffffu, a.t, o);
+        if (kEntropy) a.t += __shfl_xor_sync(0xffffffffu, a.t, o);
     }
 }
 
@@ -83,47 +84,12 @@ struct RowJob {
     int32_t live;     // 0: left out
     int32_t bad_param;
     float weight;
+    float x_t;        // the token's logit
     float c, c_hi, c_lo;    // log2(e) / T, rounded, and as a pair: c_lo > 0
     float inv_t, inv_t_lo;  // 1 / T as a pair
     float in0, in1, in2;    // kModeScoreGrad: the gradients by logprob and entropy; kModePolicy: advantage,
                             // old_logprob, ref_logprob
 };
-
-// The pair c_hi + c_lo matters where sums are taken: c alone is off by up to
-// 2^-24 of itself in every exponent the same way, which is an error of the
-// logprob of that times the row's mean depth, and does not average out over a
-// sequence. c_lo > 0 keeps -inf * c_lo = -inf.
-__device__ __forceinline__ RowJob row_open(const LossParams& P, int64_t r)
-{
-    const sampler_rows_t& a = P.rows;
-    RowJob h;
-    h.row = int32_t(r);
-    h.token = a.tokens[r];
-    h.weight = a.weight ? a.weight[r] : 1.f;
-    h.live = h.weight != 0.f;
-    const float T = a.temperature ? a.temperature[r] : 1.f;
-    h.in0 = h.in1 = h.in2 = 0.f;
-    if (P.mode == kModeScoreGrad) {
-        h.in0 = P.grad_logprob[r];
-        if (P.grad_entropy) h.in1 = P.grad_entropy[r];
-    } else if (P.mode == kModePolicy) {
-        h.in0 = P.policy.advantage[r];
-        h.in1 = P.policy.old_logprob[r];
-        if (P.policy.ref_logprob) h.in2 = P.policy.ref_logprob[r];
-    }
-    h.bad_param = !(T >= 0.f) || isinf(T) || h.token < 0 || int64_t(h.token) >= a.vocab;
-    double c = kLog2e, inv = 1.0;
-    if (T >= kGreedyT && T != 1.f) {
-        inv = 1.0 / double(T);
-        c = kLog2e * inv;
-    }
-    h.c = float(c);
-    h.c_hi = __double2float_rd(c);
-    h.c_lo = fmaxf(float(c - double(h.c_hi)), 1e-30f);
-    h.inv_t = float(inv);
-    h.inv_t_lo = float(inv - double(h.inv_t));
-    return h;
-}
 
 // Sums and products of two floats without rounding, as pairs (Dekker, Knuth).
 struct Pair {
@@ -134,6 +100,22 @@ __device__ __forceinline__ Pair two_sum(float a, float b)
 {
     const float s = __fadd_rn(a, b), z = __fsub_rn(s, a);
     return Pair{s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, z)), __fsub_rn(b, z))};
+}
+
+// What follows of a row from its temperature. The pair c_hi + c_lo matters where
+// sums are taken: c alone is off by up to 2^-24 of itself in every exponent the
+// same way, which is an error of the logprob of that times the row's mean depth,
+// and does not average out over a sequence. c_lo > 0 keeps -inf * c_lo = -inf.
+__device__ __forceinline__ void row_scale(RowJob& h, const sampler_rows_t& a, float T)
+{
+    h.bad_param = !(T >= 0.f) || isinf(T) || h.token < 0 || int64_t(h.token) >= a.vocab;
+    const float Te = T >= kGreedyT ? T : 1.f;  // a NaN or a negative T: the row is not used
+    h.inv_t = __fdiv_rn(1.f, Te);
+    h.inv_t_lo = fmaf(-Te, h.inv_t, 1.f) * h.inv_t;
+    h.c = kLog2e * h.inv_t;
+    const float rest = fmaf(kLog2e, h.inv_t, -h.c) + fmaf(kLog2e, h.inv_t_lo, kLog2eRest * h.inv_t);
+    h.c_hi = __int_as_float(__float_as_int(h.c) - 1);
+    h.c_lo = (h.c - h.c_hi) + rest;
 }
 
 // ln s, off by about 3e-8: the exponent's part exactly (ln 2 = 355/512 less a
@@ -193,14 +175,20 @@ __device__ __forceinline__ void set_factors(RowRecord& rec, float a, float b, fl
     rec.at_token = a * rec.inv_t;
 }
 
-// What becomes of a row once its statistics are known (x_t: the token's logit;
-// grad_scale: the whole factor of the gradient): its record, and where `write`
-// its outputs and its share of the loss.
-__device__ __forceinline__ void row_close(const LossParams& P, const RowJob& h, const Stats& st, float x_t,
-                                          float grad_scale, bool write, RowRecord& rec)
+// A row's outputs and its share of the loss.
+struct RowOut {
+    Pair lp;
+    float entropy, ratio, kl;
+    double term;
+    int status;
+};
+
+// What becomes of a row once its statistics are known (grad_scale: the whole
+// factor of the gradient).
+__device__ __forceinline__ void row_close(const LossParams& P, const RowJob& h, const Stats& st, float grad_scale,
+                                          RowRecord& rec, RowOut& out)
 {
     const sampler_rows_t& a = P.rows;
-    const int64_t r = h.row;
     rec.c = h.c;
     rec.ref = st.ref;
     rec.token = h.token;
@@ -225,7 +213,7 @@ __device__ __forceinline__ void row_close(const LossParams& P, const RowJob& h, 
             rec.inv_s = __fdiv_rn(1.f, st.s);
             rec.inv_t = h.inv_t;
             const Pair ln_s = log_of(st.s);
-            lp = logprob_of(h, st, x_t, ln_s);
+            lp = logprob_of(h, st, h.x_t, ln_s);
             entropy = ln_s.hi + fmaf(-kLn2, st.t * rec.inv_s, ln_s.lo);
             if (P.mode == kModeScoreGrad) {
                 set_factors(rec, h.in0, h.in1, entropy, ln_s.hi);
@@ -258,18 +246,28 @@ __device__ __forceinline__ void row_close(const LossParams& P, const RowJob& h, 
             }
         }
     }
-    if (!write) return;
-    if (a.out_logprob) a.out_logprob[r] = lp.hi;
-    if (a.out_entropy) a.out_entropy[r] = entropy;
-    if (a.out_status) a.out_status[r] = status;
+    out.lp = lp;
+    out.entropy = entropy;
+    out.ratio = ratio;
+    out.kl = kl;
+    out.term = h.live ? double(h.weight) * double(term) : 0.0;
+    out.status = status;
+}
+
+__device__ __forceinline__ void row_write(const LossParams& P, int64_t r, const RowRecord& rec, const RowOut& out)
+{
+    const sampler_rows_t& a = P.rows;
+    if (a.out_logprob) a.out_logprob[r] = out.lp.hi;
+    if (a.out_entropy) a.out_entropy[r] = out.entropy;
+    if (a.out_status) a.out_status[r] = out.status;
     if (P.mode == kModePolicy) {
-        if (P.policy.out_ratio) P.policy.out_ratio[r] = ratio;
-        if (P.policy.out_kl) P.policy.out_kl[r] = kl;
-        P.ws.terms[r] = h.live ? double(h.weight) * double(term) : 0.0;
+        if (P.policy.out_ratio) P.policy.out_ratio[r] = out.ratio;
+        if (P.policy.out_kl) P.policy.out_kl[r] = out.kl;
+        P.ws.terms[r] = out.term;
     }
     if (P.mode == kModePairs) {
         // the pairs' kernel takes the logprob from here and puts the gradient's factors in
-        P.ws.terms[r] = double(lp.hi) + double(lp.lo);
+        P.ws.terms[r] = double(out.lp.hi) + double(out.lp.lo);
         P.ws.records[r] = rec;
     }
 }

@@ -4,17 +4,19 @@
 //
 // A row's gradient needs the row's sums, so a row is wanted twice, and is read
 // from memory once: a cluster of C CTAs takes a row, each CTA a part of it in
-// shared memory, where the second pass finds it. One warp of a CTA (the
-// producer) goes ahead over the cluster's rows and brings their parts in with
-// bulk copies through a ring of 8 KB chunks; sixteen (the consumers) take
-//   pass 1   a vector of each chunk in every thread: the running reference and
-//            the sums of exponentials;
-//   join     each warp puts its sums into every CTA of the cluster (distributed
-//            shared memory) and arrives there on a barrier; one warp of each CTA
-//            combines all of them and works out the gradient's factors;
-//   pass 2   (with a gradient) the same vectors again from the ring: 16-byte
-//            stores of the gradient, and each chunk's slot goes back to the
-//            producer, which fills it for the next row.
+// shared memory, where the second pass finds it. Warp roles of a CTA:
+//   producer   goes ahead over the cluster's rows: it reads their parameters and
+//              brings their parts in with bulk copies, through a ring of 16 KB chunks;
+//   consumers  (sixteen) pass 1, two vectors of each chunk in every thread: the
+//              running reference and the sums of exponentials, which each warp puts
+//              into every CTA of the cluster (distributed shared memory);
+//   closer     combines the cluster's sums, works out the gradient's factors and
+//              writes the row's outputs;
+//   consumers  pass 2, with a gradient: the same vectors again from the ring,
+//              16-byte stores, and each chunk's slot goes back to the producer.
+// Where two parts fit in the ring, the consumers take pass 1 of a row before pass 2
+// of the row before it, so that the join and the closer's work (3 to 4 us a row,
+// most of it latency) run under pass 1.
 // The rows that count are dealt to the clusters evenly whatever rows are left
 // out: each producer counts them, 32 weights at a time.
 #include <cuda_runtime.h>
@@ -30,24 +32,59 @@ namespace rows {
 
 constexpr int kWarps = 16;                       // consumers
 constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 32;
-constexpr int kChunkVecs = kConsumers;           // 16-byte vectors of a chunk: one for each consumer
+constexpr int kProducer = kWarps, kCloser = kWarps + 1;
+constexpr int kThreads = kConsumers + 64;
+constexpr int kVecs = 2;                         // 16-byte vectors of a chunk in each consumer
+constexpr int kChunkVecs = kConsumers * kVecs;
 constexpr int kChunkBytes = kChunkVecs * 16;
-constexpr int kSlots = 12;
+constexpr int kMaxSlots = 6;
+constexpr int kPartChunks = 6;                   // of a row in a CTA, where the row allows it
 constexpr int kMaxParts = 16;                    // CTAs of a cluster
-constexpr int kJobs = 4;                         // rows that the producer may be ahead, in shared memory
+constexpr int kJobs = 4;                         // rows that a CTA has in hand
+constexpr int kSums = 4;                         // rows whose sums are in shared memory
+constexpr int kSmemMax = 113 * 1024;             // of a CTA: two on an SM
 constexpr uint64_t kWaitNs = 2000000000ull;      // a wait gives up after 2 s
 
+// The ring (slots * kChunkBytes), the sums [kSums][parts * kWarps] and this.
 struct Shared {
-    alignas(128) unsigned char ring[kSlots][kChunkBytes];
-    float4 sums[2][kMaxParts * kWarps];          // ref, s, t of each warp of the cluster, x_t of a CTA's first
-    uint64_t full[kSlots], empty[kSlots];
+    uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t job_full[kJobs], job_empty[kJobs];
-    uint64_t join[2], closed[2];
+    uint64_t join[kSums], closed[kSums];
     RowJob jobs[kJobs];
-    RowRecord rec[2];
+    RowRecord rec[kSums];
     double scratch[kThreads / 32];
     uint32_t flag, failed;  // failed: a wait of this CTA gave up
+};
+
+constexpr int smem_of(int slots, int parts)
+{
+    return slots * kChunkBytes + kSums * parts * kWarps * int(sizeof(float4)) + int(sizeof(Shared));
+}
+
+constexpr int slots_for(int parts)
+{
+    int slots = kMaxSlots;
+    while (smem_of(slots, parts) > kSmemMax) --slots;
+    return slots;
+}
+
+// How the rows of a call are cut.
+struct RowPlan {
+    int part_vecs;  // vectors of a row in each CTA
+    int slots;
+    int deep;       // two parts fit in the ring
+};
+
+// A ring's place and the parity of its phase.
+struct Place {
+    uint32_t at, phase;
+    __device__ __forceinline__ void next(uint32_t n)
+    {
+        if (++at == n) {
+            at = 0;
+            phase ^= 1u;
+        }
+    }
 };
 
 __device__ __forceinline__ uint64_t now_ns()
@@ -57,20 +94,21 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
-// Wait for the phase of `bar` with the given parity, for kWaitNs at most.
+// A whole warp waits for the phase of `bar` with the given parity, for kWaitNs at
+// most; all of its lanes get the same answer.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity)
 {
     const uint64_t until = now_ns() + kWaitNs;
     for (uint32_t i = 0; i < (1u << 30); ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63u) == 63u && now_ns() > until) return false;
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        if ((i & 63u) == 63u && __any_sync(0xffffffffu, now_ns() > until)) return false;
     }
     return false;
 }
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity)
 {
-    return mbar_try_wait(bar, parity) || wait_slow(bar, parity);
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_slow(bar, parity);
 }
 
 __device__ __forceinline__ void arrive(uint64_t* bar)
@@ -78,38 +116,14 @@ __device__ __forceinline__ void arrive(uint64_t* bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// The same wait with the cluster's writes before the arrivals made visible.
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity)
+// Put 16 bytes into a CTA of the cluster and count them on its barrier. (Ordinary
+// stores and a release of the cluster would wait for all that the thread has
+// stored, the last row's gradient included.)
+__device__ __forceinline__ void put_sums(uint32_t addr, uint32_t bar, float a, float b, float c, float d)
 {
-    uint64_t until = 0;
-    for (uint32_t i = 0; i < (1u << 30); ++i) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(smem_addr(bar)), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if ((i & 63u) == 63u) {
-            const uint64_t now = now_ns();
-            if (until == 0) until = now + kWaitNs;
-            if (now > until) return false;
-        }
-    }
-    return false;
-}
-
-__device__ __forceinline__ void put_sums(uint32_t addr, float a, float b, float c, float d)
-{
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+                 "f"(a), "f"(b), "f"(c), "f"(d), "r"(bar)
                  : "memory");
-}
-
-__device__ __forceinline__ void arrive_cluster(uint32_t addr)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
 // A wait for row r (-1: for no row yet) gave up: the row says so, and the loss
@@ -220,39 +234,74 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return y;
 }
 
-// Pass 1 over kVecs vectors. The reference moves only when a vector holds a
-// larger element, which is rare after the first few.
-template <typename T, bool kEntropy, int kVecs>
-__device__ __forceinline__ void fold(Stats& st, bool& bad, const uint4 (&v)[kVecs], float c_hi, float c_lo)
+// Two fp32 operations in one instruction: both passes are bound by the number of
+// instructions before they are by memory.
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 y;
+    asm("{\n\t.reg .b64 s, t;\n\tmov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %5};\n\tadd.rn.f32x2 s, s, t;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t}"
+        : "=f"(y.x), "=f"(y.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return y;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 y;
+    asm("{\n\t.reg .b64 s, t;\n\tmov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %5};\n\tmul.rn.f32x2 s, s, t;\n\t"
+        "mov.b64 {%0, %1}, s;\n\t}"
+        : "=f"(y.x), "=f"(y.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return y;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 y;
+    asm("{\n\t.reg .b64 s, t, u;\n\tmov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %5};\n\tmov.b64 u, {%6, %7};\n\t"
+        "fma.rn.f32x2 s, s, t, u;\n\tmov.b64 {%0, %1}, s;\n\t}"
+        : "=f"(y.x), "=f"(y.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return y;
+}
+
+// Pass 1 over N vectors. The reference moves only when one holds a larger
+// element, which is rare after the first few.
+template <typename T, bool kEntropy, int N>
+__device__ __forceinline__ void fold(Stats& st, bool& bad, const uint4 (&v)[N], float c_hi, float c_lo)
 {
     constexpr int kPer = Elems<T>::kPer;
     float m = Elems<T>::largest(v[0]);
 #pragma unroll
-    for (int k = 1; k < kVecs; ++k) m = max_nan(m, Elems<T>::largest(v[k]));
+    for (int k = 1; k < N; ++k) m = max_nan(m, Elems<T>::largest(v[k]));
     if (!(m <= st.ref)) {
         if (m < pos_inf())
             stats_move(st, m, c_hi);
         else
             bad = true;
     }
-    float s0 = 0.f, s1 = 0.f;
+    const float2 ref = make_float2(-st.ref, -st.ref), hi = make_float2(c_hi, c_hi), lo = make_float2(c_lo, c_lo);
+    float2 s = make_float2(st.s, 0.f), t = make_float2(st.t, 0.f);
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
+    for (int k = 0; k < N; ++k) {
         float x[kPer];
         Elems<T>::widen(v[k], x);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const float d = x[j] - st.ref;
-            const float u = fmaf(d, c_hi, d * c_lo);
-            const float e = exp2_fast(u);
-            if (j & 1)
-                s1 += e;
-            else
-                s0 += e;
-            if (kEntropy) st.t = fmaf(e, fmaxf(u, kLowest), st.t);
+        for (int j = 0; j < kPer; j += 2) {
+            const float2 d = add2(make_float2(x[j], x[j + 1]), ref);
+            float2 u = fma2(d, hi, mul2(d, lo));
+            const float2 e = make_float2(exp2_fast(u.x), exp2_fast(u.y));
+            s = add2(s, e);
+            if (kEntropy) {
+                u.x = fmaxf(u.x, kLowest);
+                u.y = fmaxf(u.y, kLowest);
+                t = fma2(e, u, t);
+            }
         }
     }
-    st.s += s0 + s1;
+    st.s = s.x + s.y;
+    if (kEntropy) st.t = t.x + t.y;
 }
 
 // Pass 2 of one vector; `at` is the token's place in it (outside [0, kPer): not in it).
@@ -260,17 +309,23 @@ template <typename T, bool kEntropy>
 __device__ __forceinline__ uint4 gradient(const uint4& v, const RowRecord& rec, int at)
 {
     constexpr int kPer = Elems<T>::kPer;
+    const float2 ref = make_float2(-rec.ref, -rec.ref), c = make_float2(rec.c, rec.c);
+    const float2 k0 = make_float2(rec.k0, rec.k0), k1 = make_float2(rec.k1, rec.k1);
     float x[kPer];
     Elems<T>::widen(v, x);
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        const float d = x[j] - rec.ref;
+    for (int j = 0; j < kPer; j += 2) {
+        float2 u = mul2(add2(make_float2(x[j], x[j + 1]), ref), c);
+        float2 y;
         if (kEntropy) {
-            const float u = fmaxf(d * rec.c, kLowest);
-            x[j] = exp2_fast(u) * fmaf(rec.k1, u, rec.k0);
+            u.x = fmaxf(u.x, kLowest);
+            u.y = fmaxf(u.y, kLowest);
+            y = mul2(make_float2(exp2_fast(u.x), exp2_fast(u.y)), fma2(k1, u, k0));
         } else {
-            x[j] = exp2_fast(d * rec.c) * rec.k0;
+            y = mul2(make_float2(exp2_fast(u.x), exp2_fast(u.y)), k0);
         }
+        x[j] = y.x;
+        x[j + 1] = y.y;
     }
     if (unsigned(at) < unsigned(kPer)) {
 #pragma unroll
@@ -281,12 +336,13 @@ __device__ __forceinline__ uint4 gradient(const uint4& v, const RowRecord& rec, 
 }
 
 // Store vector `i` of a row's span to the gradient: as one where it lies wholly
-// inside the row and the gradient's vectors lie as the logits' do, else by element.
+// inside the row and the gradient's vectors lie as the logits' do (`whole`), else
+// by element.
 template <typename T>
-__device__ __forceinline__ void put_vector(T* g, int64_t vocab, int head, int64_t i, bool whole, const uint4& y)
+__device__ __forceinline__ void put_vector(T* g, int vocab, const RowSpan& span, int i, bool whole, const uint4& y)
 {
     constexpr int kPer = Elems<T>::kPer;
-    const int64_t first = i * kPer - head;
+    const int first = i * kPer - span.head;
     if (whole && first >= 0 && first + kPer <= vocab) {
         __stcs(reinterpret_cast<uint4*>(g + first), y);
     } else {
@@ -297,77 +353,148 @@ __device__ __forceinline__ void put_vector(T* g, int64_t vocab, int head, int64_
     }
 }
 
-// A CTA's part of a row's gradient, all the same value (zeros, or NaN).
-template <typename T>
-__device__ __forceinline__ void fill(T* g, const RowSpan& span, int64_t vocab, int first, int last, int tid, bool whole,
-                                     bool nan)
-{
-    const uint32_t w = !nan ? 0u : sizeof(T) == 2 ? 0x7fc07fc0u : 0x7fc00000u;
-    for (int i = first + tid; i < last; i += kConsumers)
-        put_vector(g, vocab, span.head, i, whole, make_uint4(w, w, w, w));
-}
-
 // ---------------------------------------------------------------- the kernel
 // The rows of cluster `q` of `n_clusters`, in order: every n_clusters-th of those
 // that count, and every n_clusters-th of those that are left out. One warp.
 struct RowDealer {
-    int64_t base;            // first row of the 32 in `mine`
+    int64_t base;            // first row of the 32 in `mine`; without weights: the next row
     uint32_t mine;           // those of them that are this cluster's and have not been given out
     uint32_t live, dead;     // rows of either kind before `base`, modulo n_clusters
-    float weight;            // this lane's row of the next 32
+    uint32_t group;          // of the four in `counts`
+    uint32_t counts;         // bit k: this lane's row of group k of 32 has a weight
+    float ahead[4];          // weights of the next 128 rows
 };
 
 __device__ __forceinline__ void dealer_load(RowDealer& d, const sampler_rows_t& a, int64_t base)
 {
-    const int64_t r = base + (threadIdx.x & 31);
-    d.weight = a.weight && r < a.n_rows ? a.weight[r] : 1.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int64_t r = base + 32 * k + (threadIdx.x & 31);
+        d.ahead[k] = r < a.n_rows ? a.weight[r] : 1.f;
+    }
+}
+
+__device__ __forceinline__ void dealer_open(RowDealer& d, const sampler_rows_t& a, uint32_t q)
+{
+    d.base = a.weight ? -32 : int64_t(q);
+    d.mine = d.live = d.dead = d.counts = 0;
+    d.group = 3;
+    if (a.weight) dealer_load(d, a, 0);
 }
 
 // The next row, -1 at the end.
 __device__ __forceinline__ int64_t dealer_next(RowDealer& d, const sampler_rows_t& a, uint32_t q, uint32_t n_clusters)
 {
+    if (!a.weight) {
+        const int64_t r = d.base;
+        d.base += n_clusters;
+        return r < a.n_rows ? r : -1;
+    }
     const uint32_t lane = threadIdx.x & 31;
     while (d.mine == 0) {
         d.base += 32;
         if (d.base >= a.n_rows) return -1;
-        const bool in = d.base + lane < a.n_rows;
-        const bool counts = d.weight != 0.f;
+        if (++d.group == 4) {
+            d.group = 0;
+            d.counts = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) d.counts |= d.ahead[k] != 0.f ? 1u << k : 0u;
+            dealer_load(d, a, d.base + 128);
+        }
+        const bool in = d.base + lane < a.n_rows, counts = d.counts >> d.group & 1u;
         const uint32_t live = __ballot_sync(0xffffffffu, in && counts), dead = __ballot_sync(0xffffffffu, in && !counts);
         const uint32_t before = (1u << lane) - 1u;
-        const uint32_t rank = counts ? d.live + __popc(live & before) : d.dead + __popc(dead & before);
-        d.mine = __ballot_sync(0xffffffffu, in && rank % n_clusters == q);
+        uint32_t rank = counts ? d.live + __popc(live & before) : d.dead + __popc(dead & before);
+        rank %= n_clusters;
+        d.mine = __ballot_sync(0xffffffffu, in && rank == q);
         d.live = (d.live + __popc(live)) % n_clusters;
         d.dead = (d.dead + __popc(dead)) % n_clusters;
-        dealer_load(d, a, d.base + 32);
     }
     const int bit = __ffs(d.mine) - 1;
     d.mine &= d.mine - 1u;
     return d.base + bit;
 }
 
-// kGrad: with the logits' gradient. kEntropy: with the sum t. The grid is whole
-// clusters of `parts` CTAs; part_vecs: vectors of a row in each CTA.
-template <typename T, bool kGrad, bool kEntropy>
-__global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant__ LossParams P, int part_vecs)
+// What a producer reads of a row ahead of its turn.
+struct RowAhead {
+    int64_t row;     // -1: none
+    int32_t token;
+    float weight, T, in0, in1, in2;
+    float x_t;
+};
+
+__device__ __forceinline__ void ahead_load(RowAhead& h, const LossParams& P, int64_t r)
 {
-    extern __shared__ __align__(128) unsigned char smem_raw[];
-    Shared& S = *reinterpret_cast<Shared*>(smem_raw);
+    const sampler_rows_t& a = P.rows;
+    h.row = r;
+    if (r < 0) return;
+    h.token = a.tokens[r];
+    h.weight = a.weight ? a.weight[r] : 1.f;
+    h.T = a.temperature ? a.temperature[r] : 1.f;
+    h.in0 = h.in1 = h.in2 = 0.f;
+    if (P.mode == kModeScoreGrad) {
+        h.in0 = P.grad_logprob[r];
+        if (P.grad_entropy) h.in1 = P.grad_entropy[r];
+    } else if (P.mode == kModePolicy) {
+        h.in0 = P.policy.advantage[r];
+        h.in1 = P.policy.old_logprob[r];
+        if (P.policy.ref_logprob) h.in2 = P.policy.ref_logprob[r];
+    }
+}
+
+// The token's logit. It is read before the row is taken up, and so before any
+// CTA can write the row's gradient in the logits' place.
+template <typename T>
+__device__ __forceinline__ void ahead_token(RowAhead& h, const sampler_rows_t& a)
+{
+    h.x_t = 0.f;
+    if (h.row >= 0 && h.weight != 0.f && h.token >= 0 && int64_t(h.token) < a.vocab)
+        h.x_t = load_logit(static_cast<const T*>(a.logits) + h.row * a.row_stride + h.token);
+}
+
+// A CTA's part of a row: vectors first .. last, in chunks that end at `end`
+// (counted for the consumer: every one of them takes part in each chunk).
+struct RowPart {
+    RowSpan span;
+    int first, last, end;
+};
+
+template <typename T>
+__device__ __forceinline__ RowPart row_part(const T* x, int64_t vocab, uint32_t rank, int part_vecs)
+{
+    RowPart p;
+    p.span = row_span(x, vocab);
+    p.first = int(rank) * part_vecs;
+    p.last = max(p.first, min(p.first + part_vecs, p.span.count));
+    p.end = p.first + (p.last - p.first + kChunkVecs - 1) / kChunkVecs * kChunkVecs;
+    return p;
+}
+
+// kGrad: with the logits' gradient. kEntropy: with the sum t. The grid is whole
+// clusters.
+template <typename T, bool kGrad, bool kEntropy>
+__global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant__ LossParams P, const RowPlan plan)
+{
+    extern __shared__ __align__(128) unsigned char ring[];
     const sampler_rows_t& a = P.rows;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t parts = cluster_nctarank(), rank = cluster_ctarank();
     const uint32_t q = blockIdx.x / parts, n_clusters = gridDim.x / parts;
+    const uint32_t slots = uint32_t(plan.slots);
+    float4* sums = reinterpret_cast<float4*>(ring + slots * kChunkBytes);
+    Shared& S = *reinterpret_cast<Shared*>(sums + kSums * parts * kWarps);
 
     if (tid == 0) {
-        for (int i = 0; i < kSlots; ++i) {
+        for (int i = 0; i < kMaxSlots; ++i) {
             mbar_init(&S.full[i], 1);
             mbar_init(&S.empty[i], kWarps);
         }
         for (int i = 0; i < kJobs; ++i) {
             mbar_init(&S.job_full[i], 1);
-            mbar_init(&S.job_empty[i], kWarps);
+            mbar_init(&S.job_empty[i], kWarps + 1);
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&S.join[i], kWarps * parts);
+        for (int i = 0; i < kSums; ++i) {
+            mbar_init(&S.join[i], 1);
             mbar_init(&S.closed[i], 1);
         }
         S.failed = 0;
@@ -375,169 +502,238 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     }
     cluster_sync();
 
-    if (warp == kWarps) {  // producer
-        RowDealer d{-32, 0, 0, 0, 1.f};
-        dealer_load(d, a, 0);
-        uint32_t chunk = 0;  // of all rows
+    if (warp == kProducer) {
+        RowDealer d;
+        dealer_open(d, a, q);
+        Place slot{0, 0}, job{0, 0};
+        uint32_t issued = 0;
         bool ok = true;
-        for (uint32_t n = 0; ok; ++n) {
-            const int64_t r = dealer_next(d, a, q, n_clusters);
-            RowJob job;
-            if (r >= 0)
-                job = row_open(P, r);
-            else
-                job.row = -1;
-            const uint32_t slot = n % kJobs;
-            ok = wait(&S.job_empty[slot], (n / kJobs & 1u) ^ 1u);
-            if (lane == 0) {
-                S.jobs[slot] = job;
-                arrive(&S.job_full[slot]);
-            }
-            __syncwarp();
-            if (!ok || r < 0) break;
-            if (!job.live || job.bad_param) continue;
-            const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
-            const RowSpan span = row_span(x, a.vocab);
-            const int first = int(rank) * part_vecs, last = min(first + part_vecs, span.count);
-            const unsigned char* from = reinterpret_cast<const unsigned char*>(x - span.head);
-            for (int v = first; ok && v < last; v += kChunkVecs, ++chunk) {
-                const uint32_t s = chunk % kSlots;
-                ok = wait(&S.empty[s], (chunk / kSlots & 1u) ^ 1u);
+        auto copy_in = [&](const RowAhead& h) {
+            const T* x = static_cast<const T*>(a.logits) + h.row * a.row_stride;
+            const RowPart part = row_part(x, a.vocab, rank, plan.part_vecs);
+            const unsigned char* from = reinterpret_cast<const unsigned char*>(x - part.span.head);
+            for (int v = part.first; ok && v < part.last; v += kChunkVecs) {
+                ok = wait(&S.empty[slot.at], slot.phase ^ 1u);
                 if (ok && lane == 0) {
-                    const uint32_t bytes = uint32_t(min(kChunkVecs, last - v)) * 16u;
-                    mbar_arrive_expect_tx(&S.full[s], bytes);
-                    bulk_copy_g2s(S.ring[s], from + size_t(v) * 16, bytes, &S.full[s]);
+                    const uint32_t bytes = uint32_t(min(kChunkVecs, part.last - v)) * 16u;
+                    mbar_arrive_expect_tx(&S.full[slot.at], bytes);
+                    bulk_copy_g2s(ring + slot.at * kChunkBytes, from + size_t(v) * 16, bytes, &S.full[slot.at]);
                 }
                 __syncwarp();
+                slot.next(slots);
+                ++issued;
             }
+        };
+        RowAhead now, next;
+        ahead_load(now, P, dealer_next(d, a, q, n_clusters));
+        if (now.row >= 0 && now.weight != 0.f) copy_in(now);
+        ahead_token<T>(now, a);
+        ahead_load(next, P, now.row < 0 ? -1 : dealer_next(d, a, q, n_clusters));
+        for (bool first = true; ok; first = false) {
+            ahead_token<T>(next, a);
+            RowAhead after;
+            ahead_load(after, P, next.row < 0 ? -1 : dealer_next(d, a, q, n_clusters));
+            ok = wait(&S.job_empty[job.at], job.phase ^ 1u);
+            if (!ok) break;
+            if (lane == 0) {
+                RowJob& j = S.jobs[job.at];
+                j.row = int32_t(now.row);
+                if (now.row >= 0) {
+                    j.token = now.token;
+                    j.live = now.weight != 0.f;
+                    j.weight = now.weight;
+                    j.x_t = now.x_t;
+                    j.in0 = now.in0;
+                    j.in1 = now.in1;
+                    j.in2 = now.in2;
+                    row_scale(j, a, now.T);
+                }
+                arrive(&S.job_full[job.at]);
+            }
+            __syncwarp();
+            job.next(kJobs);
+            if (now.row < 0) break;
+            if (!first && now.weight != 0.f) copy_in(now);
+            now = next;
+            next = after;
         }
         if (!ok) {
             gave_up(S, P, -1);
             // copies in flight land before the CTA may exit
-            for (uint32_t j = chunk > kSlots ? chunk - kSlots : 0; j < chunk; ++j)
-                wait(&S.full[j % kSlots], j / kSlots & 1u);
+            for (uint32_t j = issued > slots ? issued - slots : 0; j < issued; ++j) wait(&S.full[j % slots], j / slots & 1u);
         }
-    } else {
-        uint32_t chunk = 0, joins = 0;
+    } else if (warp == kCloser) {
         const float grad_scale =
             kGrad && P.mode == kModePolicy ? scale_of_grad(P.policy.grad_scale, P.policy.grad_scale_dev) : 1.f;
-        for (uint32_t n = 0;; ++n) {
-            const uint32_t slot = n % kJobs;
-            if (!wait(&S.job_full[slot], n / kJobs & 1u)) {
+        Place jp{0, 0}, sp{0, 0};
+        for (;;) {
+            if (!wait(&S.job_full[jp.at], jp.phase)) {
                 gave_up(S, P, -1);
                 break;
             }
-            const RowJob job = S.jobs[slot];
-            __syncwarp();
-            if (lane == 0) arrive(&S.job_empty[slot]);
+            const RowJob job = S.jobs[jp.at];
             if (job.row < 0) break;
+            Stats st = stats_empty();
+            if (job.live) {
+                if (lane == 0) mbar_arrive_expect_tx(&S.join[sp.at], kWarps * parts * 16u);
+                __syncwarp();
+                if (!wait(&S.join[sp.at], sp.phase)) {
+                    gave_up(S, P, job.row);
+                    break;
+                }
+                const float4* in = sums + sp.at * parts * kWarps;
+                for (uint32_t i = lane; i < parts * kWarps; i += 32) {
+                    const float4 p = in[i];
+                    Stats o{p.x, p.y, p.z};
+                    const float ref = fmaxf(st.ref, o.ref);
+                    stats_move(st, ref, job.c);
+                    stats_move(o, ref, job.c);
+                    st.s += o.s;
+                    st.t += o.t;
+                }
+                stats_warp<kEntropy>(st, job.c);
+            }
+            RowRecord rec;
+            RowOut out;
+            row_close(P, job, st, grad_scale, rec, out);
+            if (job.live) {
+                if (lane == 0) {
+                    if (kGrad) S.rec[sp.at] = rec;
+                    arrive(&S.closed[sp.at]);
+                }
+                sp.next(kSums);
+            }
+            if (rank == 0 && lane == 0) row_write(P, job.row, rec, out);
+            __syncwarp();
+            if (lane == 0) arrive(&S.job_empty[jp.at]);
+            jp.next(kJobs);
+        }
+    } else {
+        // pass 1's row, pass 2's row (the same, or the one before), and what has been waited for of `closed`
+        Place jp{0, 0}, slot1{0, 0}, slot2{0, 0}, sp{0, 0}, cp{0, 0};
+        uint32_t behind = 0;  // rows taken in pass 1 and not finished
+        int32_t prev = -1;    // job of the row before, where it waits for pass 2
+        uint32_t prev_at = 0;
+        bool ok = true;
+        // pass 2 of a job's row, or its fill where it is left out
+        auto finish = [&](uint32_t at) {
+            const RowJob& job = S.jobs[at];
             const int64_t r = job.row;
             const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
-            T* g = kGrad ? static_cast<T*>(a.out_grad) + r * a.grad_stride : nullptr;
-            const RowSpan span = row_span(x, a.vocab);
-            const bool whole = kGrad && ((reinterpret_cast<uintptr_t>(g) - reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
-            const int first = int(rank) * part_vecs, last = max(first, min(first + part_vecs, span.count));
-            const bool closes = warp == 0;
-            const bool writes = rank == 0 && warp == 0 && lane == 0;
-            RowRecord rec;
-            if (!job.live || job.bad_param) {
-                if (closes) row_close(P, job, stats_empty(), 0.f, grad_scale, writes, rec);
-                if (kGrad) fill(g, span, a.vocab, first, last, tid, whole, job.live != 0);
-                continue;
+            T* g = static_cast<T*>(a.out_grad) + r * a.grad_stride;
+            const RowPart part = row_part(x, a.vocab, rank, plan.part_vecs);
+            const bool whole = ((reinterpret_cast<uintptr_t>(g) - reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
+            if (!job.live) {
+                for (int i = part.first + tid; i < part.last; i += kConsumers)
+                    put_vector(g, int(a.vocab), part.span, i, whole, make_uint4(0u, 0u, 0u, 0u));
+                return true;
             }
-            const float x_t = closes ? load_logit(x + job.token) : 0.f;
-            // pass 1
-            Stats st = stats_empty();
-            bool bad = false, ok = true;
-            const int mine = last - first - tid;  // this thread has vectors first + tid + kChunkVecs * j
-            const int chunks = (last - first + kChunkVecs - 1) / kChunkVecs;
-            const int edge_lo = 0, edge_hi = span.count - 1;
-            for (int j = 0; j < chunks; j += 2) {
-                const uint32_t c0 = chunk + j, s0 = c0 % kSlots, c1 = c0 + 1, s1 = c1 % kSlots;
-                const bool two = j + 1 < chunks;
-                ok = ok && wait(&S.full[s0], c0 / kSlots & 1u);
-                if (two) ok = ok && wait(&S.full[s1], c1 / kSlots & 1u);
-                if (!ok) break;
-                uint4 v[2];
-                const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
-                v[0] = v[1] = make_uint4(none, none, none, none);
-                const int i0 = first + tid + kChunkVecs * j, i1 = i0 + kChunkVecs;
-                if (mine > kChunkVecs * j) v[0] = reinterpret_cast<const uint4*>(S.ring[s0])[tid];
-                if (mine > kChunkVecs * (j + 1)) v[1] = reinterpret_cast<const uint4*>(S.ring[s1])[tid];
-                if (i0 == edge_lo || i0 == edge_hi || i1 == edge_hi) {
-                    constexpr int kPer = Elems<T>::kPer;
-                    const int hi = int(a.vocab) + span.head;
-                    Elems<T>::mask(v[0], span.head - i0 * kPer, hi - i0 * kPer);
-                    Elems<T>::mask(v[1], span.head - i1 * kPer, hi - i1 * kPer);
+            if (!wait(&S.closed[cp.at], cp.phase)) return false;
+            const RowRecord rec = S.rec[cp.at];
+            cp.next(kSums);
+            const int tok = rec.token < kNoToken ? rec.token + part.span.head : -1;
+            for (int i = part.first + tid; i < part.end; i += kChunkVecs) {
+                const uint4* in = reinterpret_cast<const uint4*>(ring + slot2.at * kChunkBytes) + tid;
+#pragma unroll
+                for (int k = 0; k < kVecs; ++k) {
+                    const int ik = i + k * kConsumers;
+                    if (ik < part.last)
+                        put_vector(g, int(a.vocab), part.span, ik, whole,
+                                   gradient<T, kEntropy>(in[k * kConsumers], rec, tok - ik * Elems<T>::kPer));
                 }
-                fold<T, kEntropy, 2>(st, bad, v, job.c_hi, job.c_lo);
+                __syncwarp();
+                if (lane == 0) arrive(&S.empty[slot2.at]);
+                slot2.next(slots);
+            }
+            return true;
+        };
+        for (;;) {
+            if (!wait(&S.job_full[jp.at], jp.phase)) {
+                gave_up(S, P, -1);
+                break;
+            }
+            const RowJob& job = S.jobs[jp.at];
+            const int32_t row = job.row;
+            if (row >= 0 && job.live) {
+                const T* x = static_cast<const T*>(a.logits) + int64_t(row) * a.row_stride;
+                const RowPart part = row_part(x, a.vocab, rank, plan.part_vecs);
+                const float c_hi = job.c_hi, c_lo = job.c_lo;
+                Stats st = stats_empty();
+                bool bad = false;
+                for (int i = part.first + tid; i < part.end; i += kChunkVecs) {
+                    ok = wait(&S.full[slot1.at], slot1.phase);
+                    if (!ok) break;
+                    const uint4* in = reinterpret_cast<const uint4*>(ring + slot1.at * kChunkBytes) + tid;
+                    const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+                    uint4 v[kVecs];
+                    bool edge = i == 0;
+#pragma unroll
+                    for (int k = 0; k < kVecs; ++k) {
+                        const int ik = i + k * kConsumers;
+                        v[k] = make_uint4(none, none, none, none);
+                        if (ik < part.last) v[k] = in[k * kConsumers];
+                        edge = edge || ik == part.span.count - 1;
+                    }
+                    if (edge) {
+                        constexpr int kPer = Elems<T>::kPer;
+                        const int hi = int(a.vocab) + part.span.head;
+#pragma unroll
+                        for (int k = 0; k < kVecs; ++k) {
+                            const int at = (i + k * kConsumers) * kPer;
+                            Elems<T>::mask(v[k], part.span.head - at, hi - at);
+                        }
+                    }
+                    fold<T, kEntropy, kVecs>(st, bad, v, c_hi, c_lo);
+                    if (!kGrad) {
+                        __syncwarp();
+                        if (lane == 0) arrive(&S.empty[slot1.at]);
+                    }
+                    slot1.next(slots);
+                }
+                if (bad) st.s = quiet_nan();
+                stats_warp<kEntropy>(st, job.c);
+                // A buffer of sums is written again four rows later. By then this CTA has closed the row two
+                // before this one, so every warp of the cluster had come to that row's join, and each had
+                // seen the row two before that closed in its own CTA: all closers are done with the buffer.
+                // (With a gradient, finish() has waited for it.)
                 if (!kGrad) {
-                    __syncwarp();
-                    if (lane == 0) {
-                        arrive(&S.empty[s0]);
-                        if (two) arrive(&S.empty[s1]);
+                    if (behind == 2) {
+                        ok = ok && wait(&S.closed[cp.at], cp.phase);
+                        cp.next(kSums);
+                    } else {
+                        ++behind;
                     }
                 }
-            }
-            if (!ok) {
-                gave_up(S, P, r);
-                break;
-            }
-            if (bad) st.s = quiet_nan();
-            stats_warp(st, job.c);
-            // join
-            const uint32_t buf = joins & 1u;
-            // a buffer is written again once every warp of the cluster has come to the join after its last
-            // use (with a gradient, the wait for `closed` below has seen to that)
-            if (!kGrad && joins > 0) ok = wait_cluster(&S.join[buf ^ 1u], (joins - 1u) >> 1 & 1u);
-            if (ok && uint32_t(lane) < parts) {
-                put_sums(dsmem_map(smem_addr(&S.sums[buf][rank * kWarps + warp]), lane), st.ref, st.s, st.t, x_t);
-                arrive_cluster(dsmem_map(smem_addr(&S.join[buf]), lane));
-            }
-            if (ok && closes) {
-                ok = wait_cluster(&S.join[buf], joins >> 1 & 1u);
-                if (ok) {
-                    st = stats_empty();
-                    for (uint32_t i = lane; i < parts * kWarps; i += 32) {
-                        const float4 p = S.sums[buf][i];
-                        Stats o{p.x, p.y, p.z};
-                        const float ref = fmaxf(st.ref, o.ref);
-                        stats_move(st, ref, job.c);
-                        stats_move(o, ref, job.c);
-                        st.s += o.s;
-                        st.t += o.t;
-                    }
-                    stats_warp(st, job.c);
-                    row_close(P, job, st, x_t, grad_scale, writes, rec);
-                    if (kGrad && lane == 0) {
-                        S.rec[buf] = rec;
-                        arrive(&S.closed[buf]);
-                    }
+                if (!ok) {
+                    gave_up(S, P, row);
+                    break;
                 }
+                if (uint32_t(lane) < parts)
+                    put_sums(dsmem_map(smem_addr(sums + (sp.at * parts + rank) * kWarps + warp), lane),
+                             dsmem_map(smem_addr(&S.join[sp.at]), lane), st.ref, st.s, st.t, 0.f);
+                sp.next(kSums);
             }
-            if (kGrad) ok = ok && wait(&S.closed[buf], joins >> 1 & 1u);
-            if (!ok) {
-                gave_up(S, P, r);
-                break;
-            }
-            ++joins;
+            const uint32_t at = jp.at;
+            jp.next(kJobs);
             if (kGrad) {
-                rec = S.rec[buf];
-                // pass 2
-                const int tok = rec.token < kNoToken ? rec.token + span.head : -1;
-                for (int j = 0; j < chunks; ++j) {
-                    const uint32_t s = (chunk + j) % kSlots;
-                    if (mine > kChunkVecs * j) {
-                        const int64_t i = first + tid + kChunkVecs * j;
-                        const uint4 v = reinterpret_cast<const uint4*>(S.ring[s])[tid];
-                        put_vector(g, a.vocab, span.head, i, whole,
-                                   gradient<T, kEntropy>(v, rec, tok - int(i) * Elems<T>::kPer));
+                const bool held = plan.deep != 0;
+                const int32_t target = held ? prev : row;
+                const uint32_t target_at = held ? prev_at : at;
+                prev = row;
+                prev_at = at;
+                if (target >= 0) {
+                    if (!finish(target_at)) {
+                        gave_up(S, P, target);
+                        break;
                     }
                     __syncwarp();
-                    if (lane == 0) arrive(&S.empty[s]);
+                    if (lane == 0) arrive(&S.job_empty[target_at]);
                 }
+            } else if (row >= 0) {
+                __syncwarp();
+                if (lane == 0) arrive(&S.job_empty[at]);
             }
-            chunk += chunks;
+            if (row < 0) break;
         }
     }
     // no CTA leaves while another may still write to its shared memory
@@ -664,7 +860,7 @@ __global__ void __launch_bounds__(kGradThreads) pairs_grad_kernel(const sampler_
     for (int k = 0; k < kGradVecs; ++k) {
         const int i = first + k * kGradThreads;
         if (i < span.count)
-            put_vector(g, a.vocab, span.head, i, whole,
+            put_vector(g, int(a.vocab), span, i, whole,
                        zero ? v[k] : gradient<T, false>(v[k], rec, tok - i * Elems<T>::kPer));
     }
 }
@@ -673,7 +869,7 @@ __global__ void __launch_bounds__(kGradThreads) pairs_grad_kernel(const sampler_
 
 namespace {
 
-using RowsKernel = void (*)(const LossParams, int);
+using RowsKernel = void (*)(const LossParams, const rows::RowPlan);
 
 template <typename T>
 RowsKernel rows_kernel_for(bool grad, bool entropy)
@@ -694,14 +890,20 @@ int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t st
     const RowsKernel kernel = es == 2 ? rows_kernel_for<uint16_t>(grad, entropy) : rows_kernel_for<float>(grad, entropy);
     // vectors of a row that starts anywhere
     const int64_t vecs = (p.rows.vocab + 2 * (16 / es - 1)) * es / 16 + 1;
+    // parts of at most kPartChunks chunks, of which two fit in the ring; smaller ones while few rows leave the
+    // device unfilled
     int parts = 1;
-    while (parts < rows::kMaxParts &&
-           ((vecs + parts - 1) / parts > 8 * rows::kChunkVecs || p.rows.n_rows * parts * 2 <= sms))
+    while (parts < rows::kMaxParts && ((vecs + parts - 1) / parts > rows::kPartChunks * rows::kChunkVecs ||
+                                       p.rows.n_rows * parts * 2 <= sms))
         parts *= 2;
-    const int part_vecs = int((vecs + parts - 1) / parts);
+    rows::RowPlan plan;
+    plan.part_vecs = int((vecs + parts - 1) / parts);
+    plan.slots = rows::slots_for(parts);
+    plan.deep = 2 * ((plan.part_vecs + rows::kChunkVecs - 1) / rows::kChunkVecs) <= plan.slots;
+    const int smem = rows::smem_of(plan.slots, parts);
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(rows::kThreads);
-    cfg.dynamicSmemBytes = sizeof(rows::Shared);
+    cfg.dynamicSmemBytes = size_t(smem);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -711,7 +913,7 @@ int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t st
     int& resident = occ->clusters[es == 2][grad][entropy][parts == 1 ? 0 : parts == 2 ? 1 : parts == 4 ? 2 : parts == 8 ? 3 : 4];
     if (resident < 1) {  // once for each kernel and cluster size of a handle
         const void* k = reinterpret_cast<const void*>(kernel);
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, int(sizeof(rows::Shared))) !=
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, rows::kSmemMax) !=
                 cudaSuccess ||
             (parts > 8 && cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
             return SAMPLER_ERR_CUDA;
@@ -722,7 +924,7 @@ int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t st
     }
     const int clusters = int(std::min<int64_t>(p.rows.n_rows, resident));
     cfg.gridDim = dim3(unsigned(clusters * parts));
-    return cudaLaunchKernelEx(&cfg, kernel, p, part_vecs) == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, kernel, p, plan) == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
 }
 
 int pairs_launch(const sampler_rows_t& rows, const sampler_preference_t& pref, const RowWorkspace& ws,

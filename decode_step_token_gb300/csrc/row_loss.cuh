@@ -64,25 +64,48 @@ __device__ __forceinline__ void stats_move(Stats& a, float ref, float c)
     a.ref = ref;
 }
 
-// The statistics of all lanes' parts, in every lane (t where kEntropy).
-template <bool kEntropy>
-__device__ __forceinline__ void stats_warp(Stats& a, float c)
+// The largest of all lanes' values, in every lane.
+__device__ __forceinline__ float max_warp(float x)
 {
-    float ref = a.ref;
-    for (int o = 16; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-    stats_move(a, ref, c);
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool kEntropy>
+__device__ __forceinline__ void sum_warp(Stats& a)
+{
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         a.s += __shfl_xor_sync(0xffffffffu, a.s, o);
         if (kEntropy) a.t += __shfl_xor_sync(0xffffffffu, a.t, o);
     }
 }
 
+// The statistics of all lanes' parts, in every lane (t where kEntropy).
+template <bool kEntropy>
+__device__ __forceinline__ void stats_warp(Stats& a, float c)
+{
+    stats_move(a, max_warp(a.ref), c);
+    sum_warp<kEntropy>(a);
+}
+
+// A CTA's part of a row: vectors first .. last of the `count` 16-byte vectors that
+// cover it, the first of which begins `head` elements before the row.
+struct RowPart {
+    int32_t head, count, first, last;
+    int32_t whole;   // the gradient's vectors lie as the logits' do
+    void* grad;      // the row's gradient
+};
+
 // A row as the kernels take it up: its parameters and what its mode reads of it.
 struct RowJob {
+    RowPart part;
     int32_t row;      // -1: no more rows
     int32_t token;
     int32_t live;     // 0: left out
     int32_t bad_param;
+    int32_t last;     // of its batch
     float weight;
     float x_t;        // the token's logit
     float c, c_hi, c_lo;    // log2(e) / T, rounded, and as a pair: c_lo > 0
@@ -146,9 +169,10 @@ __device__ __forceinline__ Pair logprob_of(const RowJob& h, const Stats& st, flo
     return q;
 }
 
-// exp(d) - d - 1. Near 0 its Taylor series (to d^9: the next term is below 1e-8
-// of the sum at |d| = 0.5), where the difference would lose digits.
-__device__ __forceinline__ float exp_less_linear(float d)
+// exp(d) - d - 1 and exp(d) - 1, given exp(d). Near 0 the former is its Taylor
+// series (to d^9: the next term is below 1e-8 of the sum at |d| = 0.5), where the
+// differences would lose digits.
+__device__ __forceinline__ float exp_less_linear(float d, float exp_d, float& expm1_d)
 {
     if (fabsf(d) < 0.5f) {
         float p = 1.f / 362880.f;
@@ -159,9 +183,12 @@ __device__ __forceinline__ float exp_less_linear(float d)
         p = fmaf(p, d, 1.f / 24.f);
         p = fmaf(p, d, 1.f / 6.f);
         p = fmaf(p, d, 0.5f);
-        return d * d * p;
+        const float k = d * d * p;
+        expm1_d = d + k;
+        return k;
     }
-    return isinf(d) ? pos_inf() : expm1f(d) - d;
+    expm1_d = exp_d - 1.f;
+    return isinf(d) ? pos_inf() : expm1_d - d;
 }
 
 __device__ __forceinline__ float scale_of_grad(float scale, const float* dev) { return dev ? scale * *dev : scale; }
@@ -184,7 +211,8 @@ struct RowOut {
 };
 
 // What becomes of a row once its statistics are known (grad_scale: the whole
-// factor of the gradient).
+// factor of the gradient). A whole warp works on one row: where two exponentials
+// are wanted, its halves take one each.
 __device__ __forceinline__ void row_close(const LossParams& P, const RowJob& h, const Stats& st, float grad_scale,
                                           RowRecord& rec, RowOut& out)
 {
@@ -220,8 +248,12 @@ __device__ __forceinline__ void row_close(const LossParams& P, const RowJob& h, 
             } else if (P.mode == kModePolicy) {
                 const sampler_policy_t& q = P.policy;
                 const float A = h.in0;
-                Pair d = two_sum(lp.hi, -h.in1);
-                ratio = expf(isinf(d.hi) ? d.hi : d.hi + (d.lo + lp.lo));
+                // the exponential of lp - old in the warp's lower half, of ref - lp in its upper
+                const bool upper = threadIdx.x & 16;
+                const Pair d = upper ? two_sum(h.in2, -lp.hi) : two_sum(lp.hi, -h.in1);
+                const float e = isinf(d.hi) ? d.hi : d.hi + (upper ? d.lo - lp.lo : d.lo + lp.lo);
+                const float E = expf(e);
+                ratio = __shfl_sync(0xffffffffu, E, 0);
                 const float lo = 1.f - q.clip_low, hi = 1.f + q.clip_high;
                 const float plain = ratio * A;
                 const float cut = fminf(fmaxf(ratio, lo), hi) * A;
@@ -230,12 +262,11 @@ __device__ __forceinline__ void row_close(const LossParams& P, const RowJob& h, 
                 float by_lp = decided ? 0.f : -plain;
                 term = -gain;
                 if (q.ref_logprob) {
-                    d = two_sum(h.in2, -lp.hi);
-                    const float e = isinf(d.hi) ? d.hi : d.hi + (d.lo - lp.lo);
-                    kl = exp_less_linear(e);
+                    float em;
+                    kl = exp_less_linear(__shfl_sync(0xffffffffu, e, 16), __shfl_sync(0xffffffffu, E, 16), em);
                     if (q.kl_coef != 0.f) {
                         term = fmaf(q.kl_coef, kl, term);
-                        by_lp = fmaf(-q.kl_coef, expm1f(e), by_lp);
+                        by_lp = fmaf(-q.kl_coef, em, by_lp);
                     }
                 }
                 if (q.entropy_coef != 0.f) term = fmaf(-q.entropy_coef, entropy, term);

@@ -7,7 +7,7 @@
 // shared memory, where the second pass finds it. Warp roles of a CTA:
 //   producer   goes ahead over the cluster's rows: it reads their parameters and
 //              brings their parts in with bulk copies, through a ring of 16 KB chunks;
-//   consumers  (sixteen) pass 1, two vectors of each chunk in every thread: the
+//   consumers  (eight) pass 1, four vectors of each chunk in every thread: the
 //              running reference and the sums of exponentials, which each warp puts
 //              into every CTA of the cluster (distributed shared memory);
 //   closer     combines the cluster's sums, works out the gradient's factors and
@@ -30,17 +30,18 @@
 namespace dst {
 namespace rows {
 
-constexpr int kWarps = 16;                       // consumers
+constexpr int kWarps = 8;                        // consumers: few, with much in hand (see below)
 constexpr int kConsumers = kWarps * 32;
 constexpr int kProducer = kWarps, kCloser = kWarps + 1;
 constexpr int kThreads = kConsumers + 64;
-constexpr int kVecs = 2;                         // 16-byte vectors of a chunk in each consumer
+constexpr int kVecs = 4;                         // 16-byte vectors of a chunk in each consumer
 constexpr int kChunkVecs = kConsumers * kVecs;
 constexpr int kChunkBytes = kChunkVecs * 16;
 constexpr int kMaxSlots = 6;
 constexpr int kPartChunks = 6;                   // of a row in a CTA, where the row allows it
 constexpr int kMaxParts = 16;                    // CTAs of a cluster
-constexpr int kJobs = 4;                         // rows that a CTA has in hand
+constexpr int kBatch = 8;                        // rows whose parameters are fetched together
+constexpr int kFirstBatch = 2;                   // the first time, when all wait for them
 constexpr int kSums = 4;                         // rows whose sums are in shared memory
 constexpr int kSmemMax = 113 * 1024;             // of a CTA: two on an SM
 constexpr uint64_t kWaitNs = 2000000000ull;      // a wait gives up after 2 s
@@ -48,9 +49,9 @@ constexpr uint64_t kWaitNs = 2000000000ull;      // a wait gives up after 2 s
 // The ring (slots * kChunkBytes), the sums [kSums][parts * kWarps] and this.
 struct Shared {
     uint64_t full[kMaxSlots], empty[kMaxSlots];
-    uint64_t job_full[kJobs], job_empty[kJobs];
+    uint64_t job_full[2], job_empty[2];
     uint64_t join[kSums], closed[kSums];
-    RowJob jobs[kJobs];
+    RowJob jobs[2][kBatch];
     RowRecord rec[kSums];
     double scratch[kThreads / 32];
     uint32_t flag, failed;  // failed: a wait of this CTA gave up
@@ -111,6 +112,14 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity)
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_slow(bar, parity);
 }
 
+// True in one lane of a warp whose lanes are together.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 __device__ __forceinline__ void arrive(uint64_t* bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -154,17 +163,68 @@ __device__ __forceinline__ RowSpan row_span(const T* x, int64_t vocab)
     return s;
 }
 
+// Two fp32 values in a register pair, and two operations in one instruction:
+// both passes are bound by the number of instructions before they are by memory.
+// (The pairs are kept as 64-bit values: put together for each operation they
+// cost as many moves as the operations save.)
+using Two = unsigned long long;
+
+__device__ __forceinline__ Two two(float a, float b)
+{
+    Two y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+__device__ __forceinline__ void split(Two x, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+
+__device__ __forceinline__ Two add2(Two a, Two b)
+{
+    Two y;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+
+__device__ __forceinline__ Two mul2(Two a, Two b)
+{
+    Two y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c)
+{
+    Two y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+
+__device__ __forceinline__ Two exp2_two(Two u)
+{
+    float a, b;
+    split(u, a, b);
+    return two(exp2_fast(a), exp2_fast(b));
+}
+
+__device__ __forceinline__ Two clamp2(Two u)
+{
+    float a, b;
+    split(u, a, b);
+    return two(fmaxf(a, kLowest), fmaxf(b, kLowest));
+}
+
 template <typename T>
 struct Elems;
 template <>
 struct Elems<float> {
     static constexpr int kPer = 4;
-    static __device__ __forceinline__ void widen(const uint4& v, float (&x)[4])
+    static __device__ __forceinline__ void widen(const uint4& v, Two (&x)[2])
     {
-        x[0] = __uint_as_float(v.x);
-        x[1] = __uint_as_float(v.y);
-        x[2] = __uint_as_float(v.z);
-        x[3] = __uint_as_float(v.w);
+        x[0] = two(__uint_as_float(v.x), __uint_as_float(v.y));
+        x[1] = two(__uint_as_float(v.z), __uint_as_float(v.w));
     }
     static __device__ __forceinline__ float largest(const uint4& v)  // NaN where there is one
     {
@@ -174,9 +234,9 @@ struct Elems<float> {
         asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(b));
         return a;
     }
-    static __device__ __forceinline__ uint4 round(const float (&y)[4])
+    static __device__ __forceinline__ uint4 round(const Two (&y)[2])
     {
-        return make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+        return make_uint4(uint32_t(y[0]), uint32_t(y[0] >> 32), uint32_t(y[1]), uint32_t(y[1] >> 32));
     }
     // elements before `lo` and from `hi` on become -inf
     static __device__ __forceinline__ void mask(uint4& v, int lo, int hi)
@@ -190,14 +250,11 @@ struct Elems<float> {
 template <>
 struct Elems<uint16_t> {
     static constexpr int kPer = 8;
-    static __device__ __forceinline__ void widen(const uint4& v, float (&x)[8])
+    static __device__ __forceinline__ void widen(const uint4& v, Two (&x)[4])
     {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[2 * j] = __uint_as_float(w[j] << 16);
-            x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
+        for (int j = 0; j < 4; ++j) x[j] = two(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
     }
     static __device__ __forceinline__ float largest(const uint4& v)
     {
@@ -209,12 +266,15 @@ struct Elems<uint16_t> {
         asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(__uint_as_float(a << 16)), "f"(__uint_as_float(a & 0xffff0000u)));
         return m;
     }
-    static __device__ __forceinline__ uint4 round(const float (&y)[8])
+    static __device__ __forceinline__ uint4 round(const Two (&y)[4])
     {
         uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(y[2 * j + 1]), "f"(y[2 * j]));
+        for (int j = 0; j < 4; ++j) {
+            float a, b;
+            split(y[j], a, b);
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(b), "f"(a));
+        }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
     static __device__ __forceinline__ void mask(uint4& v, int lo, int hi)
@@ -234,42 +294,10 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return y;
 }
 
-// Two fp32 operations in one instruction: both passes are bound by the number of
-// instructions before they are by memory.
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 y;
-    asm("{\n\t.reg .b64 s, t;\n\tmov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %5};\n\tadd.rn.f32x2 s, s, t;\n\t"
-        "mov.b64 {%0, %1}, s;\n\t}"
-        : "=f"(y.x), "=f"(y.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return y;
-}
-
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    float2 y;
-    asm("{\n\t.reg .b64 s, t;\n\tmov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %5};\n\tmul.rn.f32x2 s, s, t;\n\t"
-        "mov.b64 {%0, %1}, s;\n\t}"
-        : "=f"(y.x), "=f"(y.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return y;
-}
-
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 y;
-    asm("{\n\t.reg .b64 s, t, u;\n\tmov.b64 s, {%2, %3};\n\tmov.b64 t, {%4, %5};\n\tmov.b64 u, {%6, %7};\n\t"
-        "fma.rn.f32x2 s, s, t, u;\n\tmov.b64 {%0, %1}, s;\n\t}"
-        : "=f"(y.x), "=f"(y.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return y;
-}
-
 // Pass 1 over N vectors. The reference moves only when one holds a larger
 // element, which is rare after the first few.
 template <typename T, bool kEntropy, int N>
-__device__ __forceinline__ void fold(Stats& st, bool& bad, const uint4 (&v)[N], float c_hi, float c_lo)
+__device__ __forceinline__ void fold(Stats& st, bool& bad, const uint4 (&v)[N], Two c_hi, Two c_lo, float c)
 {
     constexpr int kPer = Elems<T>::kPer;
     float m = Elems<T>::largest(v[0]);
@@ -277,72 +305,92 @@ __device__ __forceinline__ void fold(Stats& st, bool& bad, const uint4 (&v)[N], 
     for (int k = 1; k < N; ++k) m = max_nan(m, Elems<T>::largest(v[k]));
     if (!(m <= st.ref)) {
         if (m < pos_inf())
-            stats_move(st, m, c_hi);
+            stats_move(st, m, c);
         else
             bad = true;
     }
-    const float2 ref = make_float2(-st.ref, -st.ref), hi = make_float2(c_hi, c_hi), lo = make_float2(c_lo, c_lo);
-    float2 s = make_float2(st.s, 0.f), t = make_float2(st.t, 0.f);
+    const Two ref = two(-st.ref, -st.ref);
+    Two s = two(st.s, 0.f), t = two(st.t, 0.f);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-        float x[kPer];
+        Two x[kPer / 2];
         Elems<T>::widen(v[k], x);
 #pragma unroll
-        for (int j = 0; j < kPer; j += 2) {
-            const float2 d = add2(make_float2(x[j], x[j + 1]), ref);
-            float2 u = fma2(d, hi, mul2(d, lo));
-            const float2 e = make_float2(exp2_fast(u.x), exp2_fast(u.y));
+        for (int j = 0; j < kPer / 2; ++j) {
+            const Two d = add2(x[j], ref);
+            const Two u = fma2(d, c_hi, mul2(d, c_lo));
+            const Two e = exp2_two(u);
             s = add2(s, e);
-            if (kEntropy) {
-                u.x = fmaxf(u.x, kLowest);
-                u.y = fmaxf(u.y, kLowest);
-                t = fma2(e, u, t);
-            }
+            if (kEntropy) t = fma2(e, clamp2(u), t);
         }
     }
-    st.s = s.x + s.y;
-    if (kEntropy) st.t = t.x + t.y;
+    float a, b;
+    split(s, a, b);
+    st.s = a + b;
+    if (kEntropy) {
+        split(t, a, b);
+        st.t = a + b;
+    }
 }
 
-// Pass 2 of one vector; `at` is the token's place in it (outside [0, kPer): not in it).
-template <typename T, bool kEntropy>
-__device__ __forceinline__ uint4 gradient(const uint4& v, const RowRecord& rec, int at)
+// A row's record as pass 2 uses it.
+struct Factors {
+    Two ref, c, k0, k1;
+};
+
+__device__ __forceinline__ Factors factors(const RowRecord& rec)
 {
-    constexpr int kPer = Elems<T>::kPer;
-    const float2 ref = make_float2(-rec.ref, -rec.ref), c = make_float2(rec.c, rec.c);
-    const float2 k0 = make_float2(rec.k0, rec.k0), k1 = make_float2(rec.k1, rec.k1);
-    float x[kPer];
-    Elems<T>::widen(v, x);
+    return Factors{two(-rec.ref, -rec.ref), two(rec.c, rec.c), two(rec.k0, rec.k0), two(rec.k1, rec.k1)};
+}
+
+// Pass 2 of one vector.
+template <typename T, bool kEntropy>
+__device__ __forceinline__ void gradient(const uint4& v, const Factors& f, Two (&y)[Elems<T>::kPer / 2])
+{
+    Elems<T>::widen(v, y);
 #pragma unroll
-    for (int j = 0; j < kPer; j += 2) {
-        float2 u = mul2(add2(make_float2(x[j], x[j + 1]), ref), c);
-        float2 y;
+    for (int j = 0; j < Elems<T>::kPer / 2; ++j) {
+        Two u = mul2(add2(y[j], f.ref), f.c);
         if (kEntropy) {
-            u.x = fmaxf(u.x, kLowest);
-            u.y = fmaxf(u.y, kLowest);
-            y = mul2(make_float2(exp2_fast(u.x), exp2_fast(u.y)), fma2(k1, u, k0));
+            u = clamp2(u);
+            y[j] = mul2(exp2_two(u), fma2(f.k1, u, f.k0));
         } else {
-            y = mul2(make_float2(exp2_fast(u.x), exp2_fast(u.y)), k0);
+            y[j] = mul2(exp2_two(u), f.k0);
         }
-        x[j] = y.x;
-        x[j + 1] = y.y;
     }
-    if (unsigned(at) < unsigned(kPer)) {
+}
+
+template <typename T, bool kEntropy>
+__device__ __forceinline__ uint4 gradient(const uint4& v, const Factors& f)
+{
+    Two y[Elems<T>::kPer / 2];
+    gradient<T, kEntropy>(v, f, y);
+    return Elems<T>::round(y);
+}
+
+// The same with the token at place `at` of the vector (kPer or more, or below 0: not in it).
+template <typename T, bool kEntropy>
+__device__ __forceinline__ uint4 gradient_token(const uint4& v, const Factors& f, int at, float at_token)
+{
+    Two y[Elems<T>::kPer / 2];
+    gradient<T, kEntropy>(v, f, y);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-            if (j == at) x[j] += rec.at_token;
+    for (int j = 0; j < Elems<T>::kPer / 2; ++j) {
+        float a, b;
+        split(y[j], a, b);
+        y[j] = two(2 * j == at ? a + at_token : a, 2 * j + 1 == at ? b + at_token : b);
     }
-    return Elems<T>::round(x);
+    return Elems<T>::round(y);
 }
 
 // Store vector `i` of a row's span to the gradient: as one where it lies wholly
 // inside the row and the gradient's vectors lie as the logits' do (`whole`), else
 // by element.
 template <typename T>
-__device__ __forceinline__ void put_vector(T* g, int vocab, const RowSpan& span, int i, bool whole, const uint4& y)
+__device__ __forceinline__ void put_vector(T* g, int vocab, int head, int i, bool whole, const uint4& y)
 {
     constexpr int kPer = Elems<T>::kPer;
-    const int first = i * kPer - span.head;
+    const int first = i * kPer - head;
     if (whole && first >= 0 && first + kPer <= vocab) {
         __stcs(reinterpret_cast<uint4*>(g + first), y);
     } else {
@@ -359,6 +407,7 @@ __device__ __forceinline__ void put_vector(T* g, int vocab, const RowSpan& span,
 struct RowDealer {
     int64_t base;            // first row of the 32 in `mine`; without weights: the next row
     uint32_t mine;           // those of them that are this cluster's and have not been given out
+    uint32_t is_live;        // those that count
     uint32_t live, dead;     // rows of either kind before `base`, modulo n_clusters
     uint32_t group;          // of the four in `counts`
     uint32_t counts;         // bit k: this lane's row of group k of 32 has a weight
@@ -377,15 +426,17 @@ __device__ __forceinline__ void dealer_load(RowDealer& d, const sampler_rows_t& 
 __device__ __forceinline__ void dealer_open(RowDealer& d, const sampler_rows_t& a, uint32_t q)
 {
     d.base = a.weight ? -32 : int64_t(q);
-    d.mine = d.live = d.dead = d.counts = 0;
+    d.mine = d.is_live = d.live = d.dead = d.counts = 0;
     d.group = 3;
     if (a.weight) dealer_load(d, a, 0);
 }
 
-// The next row, -1 at the end.
-__device__ __forceinline__ int64_t dealer_next(RowDealer& d, const sampler_rows_t& a, uint32_t q, uint32_t n_clusters)
+// The next row, -1 at the end; whether it counts.
+__device__ __forceinline__ int64_t dealer_next(RowDealer& d, const sampler_rows_t& a, uint32_t q, uint32_t n_clusters,
+                                               bool& counting)
 {
     if (!a.weight) {
+        counting = true;
         const int64_t r = d.base;
         d.base += n_clusters;
         return r < a.n_rows ? r : -1;
@@ -403,6 +454,7 @@ __device__ __forceinline__ int64_t dealer_next(RowDealer& d, const sampler_rows_
         }
         const bool in = d.base + lane < a.n_rows, counts = d.counts >> d.group & 1u;
         const uint32_t live = __ballot_sync(0xffffffffu, in && counts), dead = __ballot_sync(0xffffffffu, in && !counts);
+        d.is_live = live;
         const uint32_t before = (1u << lane) - 1u;
         uint32_t rank = counts ? d.live + __popc(live & before) : d.dead + __popc(dead & before);
         rank %= n_clusters;
@@ -412,61 +464,52 @@ __device__ __forceinline__ int64_t dealer_next(RowDealer& d, const sampler_rows_
     }
     const int bit = __ffs(d.mine) - 1;
     d.mine &= d.mine - 1u;
+    counting = d.is_live >> bit & 1u;
     return d.base + bit;
 }
 
-// What a producer reads of a row ahead of its turn.
-struct RowAhead {
-    int64_t row;     // -1: none
-    int32_t token;
-    float weight, T, in0, in1, in2;
-    float x_t;
-};
-
-__device__ __forceinline__ void ahead_load(RowAhead& h, const LossParams& P, int64_t r)
+// What a row needs besides its logits and its weight, one row in each lane.
+__device__ __forceinline__ void job_load(RowJob& j, float& temperature, const LossParams& P, int64_t r)
 {
     const sampler_rows_t& a = P.rows;
-    h.row = r;
-    if (r < 0) return;
-    h.token = a.tokens[r];
-    h.weight = a.weight ? a.weight[r] : 1.f;
-    h.T = a.temperature ? a.temperature[r] : 1.f;
-    h.in0 = h.in1 = h.in2 = 0.f;
+    j.token = a.tokens[r];
+    j.weight = a.weight ? a.weight[r] : 1.f;
+    temperature = a.temperature ? a.temperature[r] : 1.f;
+    j.in0 = j.in1 = j.in2 = 0.f;
     if (P.mode == kModeScoreGrad) {
-        h.in0 = P.grad_logprob[r];
-        if (P.grad_entropy) h.in1 = P.grad_entropy[r];
+        j.in0 = P.grad_logprob[r];
+        if (P.grad_entropy) j.in1 = P.grad_entropy[r];
     } else if (P.mode == kModePolicy) {
-        h.in0 = P.policy.advantage[r];
-        h.in1 = P.policy.old_logprob[r];
-        if (P.policy.ref_logprob) h.in2 = P.policy.ref_logprob[r];
+        j.in0 = P.policy.advantage[r];
+        j.in1 = P.policy.old_logprob[r];
+        if (P.policy.ref_logprob) j.in2 = P.policy.ref_logprob[r];
     }
 }
 
-// The token's logit. It is read before the row is taken up, and so before any
+// Its token's logit. It is read before the row is taken up, and so before any
 // CTA can write the row's gradient in the logits' place.
 template <typename T>
-__device__ __forceinline__ void ahead_token(RowAhead& h, const sampler_rows_t& a)
+__device__ __forceinline__ void job_token(RowJob& j, const sampler_rows_t& a, int64_t r, bool live)
 {
-    h.x_t = 0.f;
-    if (h.row >= 0 && h.weight != 0.f && h.token >= 0 && int64_t(h.token) < a.vocab)
-        h.x_t = load_logit(static_cast<const T*>(a.logits) + h.row * a.row_stride + h.token);
+    j.x_t = 0.f;
+    if (live && j.token >= 0 && int64_t(j.token) < a.vocab)
+        j.x_t = load_logit(static_cast<const T*>(a.logits) + r * a.row_stride + j.token);
 }
 
-// A CTA's part of a row: vectors first .. last, in chunks that end at `end`
-// (counted for the consumer: every one of them takes part in each chunk).
-struct RowPart {
-    RowSpan span;
-    int first, last, end;
-};
-
+// A CTA's part of row r, worked out once by the producer.
 template <typename T>
-__device__ __forceinline__ RowPart row_part(const T* x, int64_t vocab, uint32_t rank, int part_vecs)
+__device__ __forceinline__ RowPart row_part(const sampler_rows_t& a, int64_t r, uint32_t rank, const RowPlan& plan)
 {
+    const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
+    const RowSpan span = row_span(x, a.vocab);
     RowPart p;
-    p.span = row_span(x, vocab);
-    p.first = int(rank) * part_vecs;
-    p.last = max(p.first, min(p.first + part_vecs, p.span.count));
-    p.end = p.first + (p.last - p.first + kChunkVecs - 1) / kChunkVecs * kChunkVecs;
+    p.head = span.head;
+    p.count = span.count;
+    p.first = int(rank) * plan.part_vecs;
+    p.last = max(p.first, min(p.first + plan.part_vecs, span.count));
+    T* g = a.out_grad ? static_cast<T*>(a.out_grad) + r * a.grad_stride : nullptr;
+    p.whole = ((reinterpret_cast<uintptr_t>(g) - reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
+    p.grad = g;
     return p;
 }
 
@@ -489,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
             mbar_init(&S.full[i], 1);
             mbar_init(&S.empty[i], kWarps);
         }
-        for (int i = 0; i < kJobs; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&S.job_full[i], 1);
             mbar_init(&S.job_empty[i], kWarps + 1);
         }
@@ -505,17 +548,18 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     if (warp == kProducer) {
         RowDealer d;
         dealer_open(d, a, q);
-        Place slot{0, 0}, job{0, 0};
+        Place slot{0, 0}, batch{0, 0};
         uint32_t issued = 0;
-        bool ok = true;
-        auto copy_in = [&](const RowAhead& h) {
-            const T* x = static_cast<const T*>(a.logits) + h.row * a.row_stride;
-            const RowPart part = row_part(x, a.vocab, rank, plan.part_vecs);
-            const unsigned char* from = reinterpret_cast<const unsigned char*>(x - part.span.head);
+        bool ok = true, end = false;
+        auto copy_in = [&](int64_t row) {
+            const RowPart part = row_part<T>(a, row, rank, plan);
+            const unsigned char* from = reinterpret_cast<const unsigned char*>(static_cast<const T*>(a.logits) +
+                                                                               row * a.row_stride - part.head);
             for (int v = part.first; ok && v < part.last; v += kChunkVecs) {
                 ok = wait(&S.empty[slot.at], slot.phase ^ 1u);
-                if (ok && lane == 0) {
-                    const uint32_t bytes = uint32_t(min(kChunkVecs, part.last - v)) * 16u;
+                if (!ok) break;
+                const uint32_t bytes = uint32_t(min(kChunkVecs, part.last - v)) * 16u;
+                if (elect_one()) {
                     mbar_arrive_expect_tx(&S.full[slot.at], bytes);
                     bulk_copy_g2s(ring + slot.at * kChunkBytes, from + size_t(v) * 16, bytes, &S.full[slot.at]);
                 }
@@ -524,38 +568,69 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
                 ++issued;
             }
         };
-        RowAhead now, next;
-        ahead_load(now, P, dealer_next(d, a, q, n_clusters));
-        if (now.row >= 0 && now.weight != 0.f) copy_in(now);
-        ahead_token<T>(now, a);
-        ahead_load(next, P, now.row < 0 ? -1 : dealer_next(d, a, q, n_clusters));
-        for (bool first = true; ok; first = false) {
-            ahead_token<T>(next, a);
-            RowAhead after;
-            ahead_load(after, P, next.row < 0 ? -1 : dealer_next(d, a, q, n_clusters));
-            ok = wait(&S.job_empty[job.at], job.phase ^ 1u);
-            if (!ok) break;
-            if (lane == 0) {
-                RowJob& j = S.jobs[job.at];
-                j.row = int32_t(now.row);
-                if (now.row >= 0) {
-                    j.token = now.token;
-                    j.live = now.weight != 0.f;
-                    j.weight = now.weight;
-                    j.x_t = now.x_t;
-                    j.in0 = now.in0;
-                    j.in1 = now.in1;
-                    j.in2 = now.in2;
-                    row_scale(j, a, now.T);
+        // The next `most` rows at most, the k-th in lane k (row -1: the end); which of them count. Their number.
+        auto deal = [&](int most, int64_t& mine, uint32_t& live) {
+            int count = 0;
+            mine = -1;
+            live = 0;
+            while (count < most && !end) {
+                bool counts;
+                const int64_t r = dealer_next(d, a, q, n_clusters, counts);
+                if (lane == count) mine = r;
+                if (r < 0)
+                    end = true;
+                else if (counts)
+                    live |= 1u << count;
+                ++count;
+            }
+            return count;
+        };
+        auto publish = [&](RowJob& job, float temperature, int count, int64_t mine, uint32_t live) {
+            ok = ok && wait(&S.job_empty[batch.at], batch.phase ^ 1u);
+            if (!ok) return;
+            if (lane < count) {
+                job.row = int32_t(mine);
+                job.live = live >> lane & 1u;
+                job.last = lane == count - 1;
+                if (mine >= 0) {
+                    row_scale(job, a, temperature);
+                    job.part = row_part<T>(a, mine, rank, plan);
                 }
-                arrive(&S.job_full[job.at]);
+                S.jobs[batch.at][lane] = job;
             }
             __syncwarp();
-            job.next(kJobs);
-            if (now.row < 0) break;
-            if (!first && now.weight != 0.f) copy_in(now);
-            now = next;
-            next = after;
+            if (lane == 0) arrive(&S.job_full[batch.at]);
+            batch.next(2);
+        };
+        int64_t mine;
+        uint32_t live;
+        int count = deal(kFirstBatch, mine, live);
+        {
+            RowJob job;
+            float temperature;
+            if (mine >= 0) job_load(job, temperature, P, mine);
+            if (live & 1u) copy_in(__shfl_sync(0xffffffffu, mine, 0));
+            if (mine >= 0) job_token<T>(job, a, mine, live >> lane & 1u);
+            publish(job, temperature, count, mine, live);
+        }
+        // a batch's copies, and on their way the parameters of the next
+        for (int k0 = 1; ok; k0 = 0) {
+            int64_t mine_next;
+            uint32_t live_next;
+            const int count_next = deal(kBatch, mine_next, live_next);
+            RowJob job;
+            float temperature;
+            if (mine_next >= 0) job_load(job, temperature, P, mine_next);
+            for (int k = k0; ok && k < count; ++k) {
+                if (live >> k & 1u) copy_in(__shfl_sync(0xffffffffu, mine, k));
+                if (k == k0 && mine_next >= 0) job_token<T>(job, a, mine_next, live_next >> lane & 1u);
+            }
+            if (k0 >= count && mine_next >= 0) job_token<T>(job, a, mine_next, live_next >> lane & 1u);
+            if (count_next == 0) break;
+            publish(job, temperature, count_next, mine_next, live_next);
+            mine = mine_next;
+            live = live_next;
+            count = count_next;
         }
         if (!ok) {
             gave_up(S, P, -1);
@@ -565,13 +640,13 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     } else if (warp == kCloser) {
         const float grad_scale =
             kGrad && P.mode == kModePolicy ? scale_of_grad(P.policy.grad_scale, P.policy.grad_scale_dev) : 1.f;
-        Place jp{0, 0}, sp{0, 0};
-        for (;;) {
-            if (!wait(&S.job_full[jp.at], jp.phase)) {
+        Place batch{0, 0}, sp{0, 0};
+        for (int k = 0;; ++k) {
+            if (k == 0 && !wait(&S.job_full[batch.at], batch.phase)) {
                 gave_up(S, P, -1);
                 break;
             }
-            const RowJob job = S.jobs[jp.at];
+            const RowJob job = S.jobs[batch.at][k];
             if (job.row < 0) break;
             Stats st = stats_empty();
             if (job.live) {
@@ -582,16 +657,17 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
                     break;
                 }
                 const float4* in = sums + sp.at * parts * kWarps;
+                float ref = -kFloatMax;
+                for (uint32_t i = lane; i < parts * kWarps; i += 32) ref = fmaxf(ref, in[i].x);
+                st.ref = max_warp(ref);
                 for (uint32_t i = lane; i < parts * kWarps; i += 32) {
                     const float4 p = in[i];
                     Stats o{p.x, p.y, p.z};
-                    const float ref = fmaxf(st.ref, o.ref);
-                    stats_move(st, ref, job.c);
-                    stats_move(o, ref, job.c);
+                    stats_move(o, st.ref, job.c);
                     st.s += o.s;
                     st.t += o.t;
                 }
-                stats_warp<kEntropy>(st, job.c);
+                sum_warp<kEntropy>(st);
             }
             RowRecord rec;
             RowOut out;
@@ -605,41 +681,51 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
             }
             if (rank == 0 && lane == 0) row_write(P, job.row, rec, out);
             __syncwarp();
-            if (lane == 0) arrive(&S.job_empty[jp.at]);
-            jp.next(kJobs);
+            if (job.last) {
+                if (lane == 0) arrive(&S.job_empty[batch.at]);
+                batch.next(2);
+                k = -1;
+            }
         }
     } else {
+        constexpr int kPer = Elems<T>::kPer;
         // pass 1's row, pass 2's row (the same, or the one before), and what has been waited for of `closed`
-        Place jp{0, 0}, slot1{0, 0}, slot2{0, 0}, sp{0, 0}, cp{0, 0};
+        Place batch{0, 0}, slot1{0, 0}, slot2{0, 0}, sp{0, 0}, cp{0, 0};
         uint32_t behind = 0;  // rows taken in pass 1 and not finished
-        int32_t prev = -1;    // job of the row before, where it waits for pass 2
-        uint32_t prev_at = 0;
+        const RowJob* before = nullptr;  // the row before, where it waits for pass 2
         bool ok = true;
         // pass 2 of a job's row, or its fill where it is left out
-        auto finish = [&](uint32_t at) {
-            const RowJob& job = S.jobs[at];
-            const int64_t r = job.row;
-            const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
-            T* g = static_cast<T*>(a.out_grad) + r * a.grad_stride;
-            const RowPart part = row_part(x, a.vocab, rank, plan.part_vecs);
-            const bool whole = ((reinterpret_cast<uintptr_t>(g) - reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
+        const int vocab = int(a.vocab);
+        auto finish = [&](const RowJob& job) {
+            const RowPart part = job.part;
+            T* g = static_cast<T*>(part.grad);
             if (!job.live) {
                 for (int i = part.first + tid; i < part.last; i += kConsumers)
-                    put_vector(g, int(a.vocab), part.span, i, whole, make_uint4(0u, 0u, 0u, 0u));
+                    put_vector(g, vocab, part.head, i, part.whole, make_uint4(0u, 0u, 0u, 0u));
                 return true;
             }
             if (!wait(&S.closed[cp.at], cp.phase)) return false;
             const RowRecord rec = S.rec[cp.at];
             cp.next(kSums);
-            const int tok = rec.token < kNoToken ? rec.token + part.span.head : -1;
-            for (int i = part.first + tid; i < part.end; i += kChunkVecs) {
+            const Factors f = factors(rec);
+            const int tok = rec.token < kNoToken ? rec.token + part.head : -1;
+            const int inner_end = min(part.last, part.count - 1) - kChunkVecs;
+            for (int i0 = part.first; i0 < part.last; i0 += kChunkVecs) {
                 const uint4* in = reinterpret_cast<const uint4*>(ring + slot2.at * kChunkBytes) + tid;
+                const int i = i0 + tid;
+                // a whole chunk without a vector that the row's ends may lie inside, and without the token
+                if (part.whole && i0 > 0 && i0 <= inner_end && unsigned(tok - i0 * kPer) >= unsigned(kChunkVecs * kPer)) {
+                    uint4* out = reinterpret_cast<uint4*>(g + (i * kPer - part.head));
 #pragma unroll
-                for (int k = 0; k < kVecs; ++k) {
-                    const int ik = i + k * kConsumers;
-                    if (ik < part.last)
-                        put_vector(g, int(a.vocab), part.span, ik, whole,
-                                   gradient<T, kEntropy>(in[k * kConsumers], rec, tok - ik * Elems<T>::kPer));
+                    for (int k = 0; k < kVecs; ++k)
+                        __stcs(out + k * kConsumers, gradient<T, kEntropy>(in[k * kConsumers], f));
+                } else {
+#pragma unroll 1
+                    for (int ik = i, k = 0; k < kVecs && ik < part.last; ++k, ik += kConsumers) {
+                        const uint4 v = in[k * kConsumers];
+                        put_vector(g, vocab, part.head, ik, part.whole,
+                                   gradient_token<T, kEntropy>(v, f, tok - ik * kPer, rec.at_token));
+                    }
                 }
                 __syncwarp();
                 if (lane == 0) arrive(&S.empty[slot2.at]);
@@ -647,43 +733,45 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
             }
             return true;
         };
-        for (;;) {
-            if (!wait(&S.job_full[jp.at], jp.phase)) {
+        // a job that has been done with gives its batch back if it is the batch's last
+        auto leave = [&](const RowJob& job) {
+            __syncwarp();
+            if (job.last && lane == 0) arrive(&S.job_empty[(&job - S.jobs[0]) / kBatch]);
+        };
+        for (int k = 0;; ++k) {
+            if (k == 0 && !wait(&S.job_full[batch.at], batch.phase)) {
                 gave_up(S, P, -1);
                 break;
             }
-            const RowJob& job = S.jobs[jp.at];
+            const RowJob& job = S.jobs[batch.at][k];
             const int32_t row = job.row;
+            const bool last = job.last != 0;
             if (row >= 0 && job.live) {
-                const T* x = static_cast<const T*>(a.logits) + int64_t(row) * a.row_stride;
-                const RowPart part = row_part(x, a.vocab, rank, plan.part_vecs);
-                const float c_hi = job.c_hi, c_lo = job.c_lo;
+                const RowPart part = job.part;
+                const int inner_end = min(part.last, part.count - 1) - kChunkVecs;
+                const Two c_hi = two(job.c_hi, job.c_hi), c_lo = two(job.c_lo, job.c_lo);
+                const float c = job.c;
                 Stats st = stats_empty();
                 bool bad = false;
-                for (int i = part.first + tid; i < part.end; i += kChunkVecs) {
+                for (int i0 = part.first; i0 < part.last; i0 += kChunkVecs) {
                     ok = wait(&S.full[slot1.at], slot1.phase);
                     if (!ok) break;
                     const uint4* in = reinterpret_cast<const uint4*>(ring + slot1.at * kChunkBytes) + tid;
-                    const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
-                    uint4 v[kVecs];
-                    bool edge = i == 0;
+                    if (i0 > 0 && i0 <= inner_end) {
+                        uint4 v[kVecs];
 #pragma unroll
-                    for (int k = 0; k < kVecs; ++k) {
-                        const int ik = i + k * kConsumers;
-                        v[k] = make_uint4(none, none, none, none);
-                        if (ik < part.last) v[k] = in[k * kConsumers];
-                        edge = edge || ik == part.span.count - 1;
-                    }
-                    if (edge) {
-                        constexpr int kPer = Elems<T>::kPer;
-                        const int hi = int(a.vocab) + part.span.head;
-#pragma unroll
-                        for (int k = 0; k < kVecs; ++k) {
-                            const int at = (i + k * kConsumers) * kPer;
-                            Elems<T>::mask(v[k], part.span.head - at, hi - at);
+                        for (int k = 0; k < kVecs; ++k) v[k] = in[k * kConsumers];
+                        fold<T, kEntropy, kVecs>(st, bad, v, c_hi, c_lo, c);
+                    } else {
+                        const int hi = vocab + part.head;
+#pragma unroll 1
+                        for (int ik = i0 + tid, k = 0; k < kVecs && ik < part.last; ++k, ik += kConsumers) {
+                            uint4 v[1] = {in[k * kConsumers]};
+                            if (ik == 0 || ik == part.count - 1)
+                                Elems<T>::mask(v[0], part.head - ik * kPer, hi - ik * kPer);
+                            fold<T, kEntropy, 1>(st, bad, v, c_hi, c_lo, c);
                         }
                     }
-                    fold<T, kEntropy, kVecs>(st, bad, v, c_hi, c_lo);
                     if (!kGrad) {
                         __syncwarp();
                         if (lane == 0) arrive(&S.empty[slot1.at]);
@@ -691,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
                     slot1.next(slots);
                 }
                 if (bad) st.s = quiet_nan();
-                stats_warp<kEntropy>(st, job.c);
+                stats_warp<kEntropy>(st, c);
                 // A buffer of sums is written again four rows later. By then this CTA has closed the row two
                 // before this one, so every warp of the cluster had come to that row's join, and each had
                 // seen the row two before that closed in its own CTA: all closers are done with the buffer.
@@ -713,27 +801,24 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
                              dsmem_map(smem_addr(&S.join[sp.at]), lane), st.ref, st.s, st.t, 0.f);
                 sp.next(kSums);
             }
-            const uint32_t at = jp.at;
-            jp.next(kJobs);
             if (kGrad) {
-                const bool held = plan.deep != 0;
-                const int32_t target = held ? prev : row;
-                const uint32_t target_at = held ? prev_at : at;
-                prev = row;
-                prev_at = at;
-                if (target >= 0) {
-                    if (!finish(target_at)) {
-                        gave_up(S, P, target);
+                const RowJob* target = plan.deep ? before : row >= 0 ? &job : nullptr;
+                before = row >= 0 ? &job : nullptr;
+                if (target) {
+                    if (!finish(*target)) {
+                        gave_up(S, P, target->row);
                         break;
                     }
-                    __syncwarp();
-                    if (lane == 0) arrive(&S.job_empty[target_at]);
+                    leave(*target);
                 }
             } else if (row >= 0) {
-                __syncwarp();
-                if (lane == 0) arrive(&S.job_empty[at]);
+                leave(job);
             }
             if (row < 0) break;
+            if (last) {
+                batch.next(2);
+                k = -1;
+            }
         }
     }
     // no CTA leaves while another may still write to its shared memory
@@ -847,6 +932,7 @@ __global__ void __launch_bounds__(kGradThreads) pairs_grad_kernel(const sampler_
     const bool whole = ((reinterpret_cast<uintptr_t>(g) - reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
     const uint4* from = reinterpret_cast<const uint4*>(x - span.head);
     const int first = int(blockIdx.x) * kGradThreads * kGradVecs + threadIdx.x;
+    const Factors f = factors(rec);
     const bool zero = rec.token < 0 || (rec.k0 == 0.f && rec.at_token == 0.f);
     const int tok = rec.token < kNoToken ? rec.token + span.head : -1;
     uint4 v[kGradVecs];
@@ -860,8 +946,8 @@ __global__ void __launch_bounds__(kGradThreads) pairs_grad_kernel(const sampler_
     for (int k = 0; k < kGradVecs; ++k) {
         const int i = first + k * kGradThreads;
         if (i < span.count)
-            put_vector(g, int(a.vocab), span, i, whole,
-                       zero ? v[k] : gradient<T, false>(v[k], rec, tok - i * Elems<T>::kPer));
+            put_vector(g, int(a.vocab), span.head, i, whole,
+                       zero ? v[k] : gradient_token<T, false>(v[k], f, tok - i * Elems<T>::kPer, rec.at_token));
     }
 }
 

@@ -94,8 +94,11 @@ __device__ __forceinline__ void stats_warp(Stats& a, float c)
 // cover it, the first of which begins `head` elements before the row.
 struct RowPart {
     int32_t head, count, first, last;
+    int32_t inner_first, inner_last;  // first vectors of the chunks that are whole and lie wholly inside the row
     int32_t whole;   // the gradient's vectors lie as the logits' do
     void* grad;      // the row's gradient
+    // whether the chunk from vector i on is whole and lies wholly inside the row
+    __device__ __forceinline__ bool inner(int i) const { return i >= inner_first && i <= inner_last; }
 };
 
 // A row as the kernels take it up: its parameters and what its mode reads of it.

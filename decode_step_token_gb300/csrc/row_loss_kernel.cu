@@ -14,9 +14,9 @@
 //              writes the row's outputs;
 //   consumers  pass 2, with a gradient: the same vectors again from the ring,
 //              16-byte stores, and each chunk's slot goes back to the producer.
-// Where two parts fit in the ring, the consumers take pass 1 of a row before pass 2
-// of the row before it, so that the join and the closer's work (3 to 4 us a row,
-// most of it latency) run under pass 1.
+// Before pass 2 of a row the consumers take pass 1 of the next as far as the ring
+// holds it, so that the join and the closer's work (about 2 us a row, most of it
+// latency) run under it.
 // The rows that count are dealt to the clusters evenly whatever rows are left
 // out: each producer counts them, 32 weights at a time.
 #include <cuda_runtime.h>
@@ -73,8 +73,9 @@ constexpr int slots_for(int parts)
 struct RowPlan {
     int part_vecs;  // vectors of a row in each CTA
     int slots;
-    int deep;       // two parts fit in the ring
 };
+
+constexpr int kPut = 0x7fffffff;  // in the place of the next vector: the row's sums have been put
 
 // A ring's place and the parity of its phase.
 struct Place {
@@ -507,6 +508,8 @@ __device__ __forceinline__ RowPart row_part(const sampler_rows_t& a, int64_t r, 
     p.count = span.count;
     p.first = int(rank) * plan.part_vecs;
     p.last = max(p.first, min(p.first + plan.part_vecs, span.count));
+    p.inner_first = span.head ? 1 : 0;
+    p.inner_last = min(p.last, int((span.head + a.vocab) / (16 / int(sizeof(T))))) - kChunkVecs;
     T* g = a.out_grad ? static_cast<T*>(a.out_grad) + r * a.grad_stride : nullptr;
     p.whole = ((reinterpret_cast<uintptr_t>(g) - reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
     p.grad = g;
@@ -689,32 +692,105 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
         }
     } else {
         constexpr int kPer = Elems<T>::kPer;
-        // pass 1's row, pass 2's row (the same, or the one before), and what has been waited for of `closed`
-        Place batch{0, 0}, slot1{0, 0}, slot2{0, 0}, sp{0, 0}, cp{0, 0};
-        uint32_t behind = 0;  // rows taken in pass 1 and not finished
-        const RowJob* before = nullptr;  // the row before, where it waits for pass 2
-        bool ok = true;
-        // pass 2 of a job's row, or its fill where it is left out
         const int vocab = int(a.vocab);
-        auto finish = [&](const RowJob& job) {
-            const RowPart part = job.part;
-            T* g = static_cast<T*>(part.grad);
-            if (!job.live) {
-                for (int i = part.first + tid; i < part.last; i += kConsumers)
-                    put_vector(g, vocab, part.head, i, part.whole, make_uint4(0u, 0u, 0u, 0u));
-                return true;
+        Place batch{0, 0}, slot1{0, 0}, slot2{0, 0}, sp{0, 0}, cp{0, 0};
+        uint32_t behind = 0;  // rows put into the join whose closing has not been waited for
+        int at = 0;           // of the batch
+        bool ok = true;
+        // The next job; its row is -1 at the end.
+        auto next_job = [&]() -> const RowJob* {
+            if (at < 0) {
+                batch.next(2);
+                at = 0;
             }
-            if (!wait(&S.closed[cp.at], cp.phase)) return false;
+            if (at == 0 && !wait(&S.job_full[batch.at], batch.phase)) {
+                gave_up(S, P, -1);
+                ok = false;
+                return nullptr;
+            }
+            const RowJob* job = &S.jobs[batch.at][at];
+            at = job->last ? -1 : at + 1;
+            return job;
+        };
+        // a job that has been done with gives its batch back if it is the batch's last
+        auto leave = [&](const RowJob* job) {
+            __syncwarp();
+            if (job->last && lane == 0) arrive(&S.job_empty[(job - S.jobs[0]) / kBatch]);
+        };
+        // pass 1 of a row, as far as it has come
+        Stats st;
+        bool bad;
+        int i1;
+        auto open1 = [&](const RowJob* job) {
+            st = stats_empty();
+            bad = false;
+            i1 = job->part.first;
+        };
+        // goes on for `most` chunks at most; at the row's end puts the sums into the cluster's join
+        auto pass1 = [&](const RowJob* job, int most) {
+            const RowPart part = job->part;
+            const Two c_hi = two(job->c_hi, job->c_hi), c_lo = two(job->c_lo, job->c_lo);
+            const float c = job->c;
+            for (; i1 < part.last && most > 0; i1 += kChunkVecs, --most) {
+                ok = wait(&S.full[slot1.at], slot1.phase);
+                if (!ok) break;
+                const uint4* in = reinterpret_cast<const uint4*>(ring + slot1.at * kChunkBytes) + tid;
+                if (part.inner(i1)) {
+                    uint4 v[kVecs];
+#pragma unroll
+                    for (int k = 0; k < kVecs; ++k) v[k] = in[k * kConsumers];
+                    fold<T, kEntropy, kVecs>(st, bad, v, c_hi, c_lo, c);
+                } else {
+                    const int hi = vocab + part.head;
+#pragma unroll 1
+                    for (int ik = i1 + tid, k = 0; k < kVecs && ik < part.last; ++k, ik += kConsumers) {
+                        uint4 v[1] = {in[k * kConsumers]};
+                        if (ik == 0 || ik == part.count - 1)
+                            Elems<T>::mask(v[0], part.head - ik * kPer, hi - ik * kPer);
+                        fold<T, kEntropy, 1>(st, bad, v, c_hi, c_lo, c);
+                    }
+                }
+                if (!kGrad) {
+                    __syncwarp();
+                    if (lane == 0) arrive(&S.empty[slot1.at]);
+                }
+                slot1.next(slots);
+            }
+            if (!ok || i1 < part.last || i1 == kPut) return;
+            i1 = kPut;
+            if (bad) st.s = quiet_nan();
+            stats_warp<kEntropy>(st, c);
+            // A buffer of sums is written again four rows later. By then this CTA has closed the row two before
+            // this one, so every warp of the cluster had come to that row's join, and each had seen the row two
+            // before that closed in its own CTA: all closers are done with the buffer. (With a gradient, pass 2
+            // has waited for it.)
+            if (!kGrad) {
+                if (behind == 2) {
+                    ok = wait(&S.closed[cp.at], cp.phase);
+                    if (!ok) return;
+                    cp.next(kSums);
+                } else {
+                    ++behind;
+                }
+            }
+            if (uint32_t(lane) < parts)
+                put_sums(dsmem_map(smem_addr(sums + (sp.at * parts + rank) * kWarps + warp), lane),
+                         dsmem_map(smem_addr(&S.join[sp.at]), lane), st.ref, st.s, st.t, 0.f);
+            sp.next(kSums);
+        };
+        auto pass2 = [&](const RowJob* job) {
+            const RowPart part = job->part;
+            T* g = static_cast<T*>(part.grad);
+            ok = wait(&S.closed[cp.at], cp.phase);
+            if (!ok) return;
             const RowRecord rec = S.rec[cp.at];
             cp.next(kSums);
             const Factors f = factors(rec);
             const int tok = rec.token < kNoToken ? rec.token + part.head : -1;
-            const int inner_end = min(part.last, part.count - 1) - kChunkVecs;
             for (int i0 = part.first; i0 < part.last; i0 += kChunkVecs) {
                 const uint4* in = reinterpret_cast<const uint4*>(ring + slot2.at * kChunkBytes) + tid;
                 const int i = i0 + tid;
-                // a whole chunk without a vector that the row's ends may lie inside, and without the token
-                if (part.whole && i0 > 0 && i0 <= inner_end && unsigned(tok - i0 * kPer) >= unsigned(kChunkVecs * kPer)) {
+                if (part.whole && part.inner(i0) && unsigned(tok - i0 * kPer) >= unsigned(kChunkVecs * kPer)) {
                     uint4* out = reinterpret_cast<uint4*>(g + (i * kPer - part.head));
 #pragma unroll
                     for (int k = 0; k < kVecs; ++k)
@@ -731,94 +807,35 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
                 if (lane == 0) arrive(&S.empty[slot2.at]);
                 slot2.next(slots);
             }
-            return true;
         };
-        // a job that has been done with gives its batch back if it is the batch's last
-        auto leave = [&](const RowJob& job) {
-            __syncwarp();
-            if (job.last && lane == 0) arrive(&S.job_empty[(&job - S.jobs[0]) / kBatch]);
-        };
-        for (int k = 0;; ++k) {
-            if (k == 0 && !wait(&S.job_full[batch.at], batch.phase)) {
-                gave_up(S, P, -1);
-                break;
-            }
-            const RowJob& job = S.jobs[batch.at][k];
-            const int32_t row = job.row;
-            const bool last = job.last != 0;
-            if (row >= 0 && job.live) {
-                const RowPart part = job.part;
-                const int inner_end = min(part.last, part.count - 1) - kChunkVecs;
-                const Two c_hi = two(job.c_hi, job.c_hi), c_lo = two(job.c_lo, job.c_lo);
-                const float c = job.c;
-                Stats st = stats_empty();
-                bool bad = false;
-                for (int i0 = part.first; i0 < part.last; i0 += kChunkVecs) {
-                    ok = wait(&S.full[slot1.at], slot1.phase);
-                    if (!ok) break;
-                    const uint4* in = reinterpret_cast<const uint4*>(ring + slot1.at * kChunkBytes) + tid;
-                    if (i0 > 0 && i0 <= inner_end) {
-                        uint4 v[kVecs];
-#pragma unroll
-                        for (int k = 0; k < kVecs; ++k) v[k] = in[k * kConsumers];
-                        fold<T, kEntropy, kVecs>(st, bad, v, c_hi, c_lo, c);
-                    } else {
-                        const int hi = vocab + part.head;
-#pragma unroll 1
-                        for (int ik = i0 + tid, k = 0; k < kVecs && ik < part.last; ++k, ik += kConsumers) {
-                            uint4 v[1] = {in[k * kConsumers]};
-                            if (ik == 0 || ik == part.count - 1)
-                                Elems<T>::mask(v[0], part.head - ik * kPer, hi - ik * kPer);
-                            fold<T, kEntropy, 1>(st, bad, v, c_hi, c_lo, c);
-                        }
-                    }
-                    if (!kGrad) {
-                        __syncwarp();
-                        if (lane == 0) arrive(&S.empty[slot1.at]);
-                    }
-                    slot1.next(slots);
+        const RowJob* job = next_job();
+        if (ok) open1(job);
+        while (ok && job->row >= 0) {
+            const RowJob* next = nullptr;
+            if (job->live) {
+                pass1(job, kMaxSlots);
+                if (ok && kGrad) {
+                    // pass 1 of the next row as far as the ring holds it beside this one
+                    next = next_job();
+                    if (ok) open1(next);
+                    if (ok && next->row >= 0 && next->live)
+                        pass1(next, int(slots) - (job->part.last - job->part.first + kChunkVecs - 1) / kChunkVecs);
+                    if (ok) pass2(job);
                 }
-                if (bad) st.s = quiet_nan();
-                stats_warp<kEntropy>(st, c);
-                // A buffer of sums is written again four rows later. By then this CTA has closed the row two
-                // before this one, so every warp of the cluster had come to that row's join, and each had
-                // seen the row two before that closed in its own CTA: all closers are done with the buffer.
-                // (With a gradient, finish() has waited for it.)
-                if (!kGrad) {
-                    if (behind == 2) {
-                        ok = ok && wait(&S.closed[cp.at], cp.phase);
-                        cp.next(kSums);
-                    } else {
-                        ++behind;
-                    }
-                }
-                if (!ok) {
-                    gave_up(S, P, row);
-                    break;
-                }
-                if (uint32_t(lane) < parts)
-                    put_sums(dsmem_map(smem_addr(sums + (sp.at * parts + rank) * kWarps + warp), lane),
-                             dsmem_map(smem_addr(&S.join[sp.at]), lane), st.ref, st.s, st.t, 0.f);
-                sp.next(kSums);
+                if (!ok) gave_up(S, P, job->row);
+            } else if (kGrad) {
+                const RowPart part = job->part;
+                for (int i = part.first + tid; i < part.last; i += kConsumers)
+                    put_vector(static_cast<T*>(part.grad), vocab, part.head, i, part.whole, make_uint4(0u, 0u, 0u, 0u));
             }
-            if (kGrad) {
-                const RowJob* target = plan.deep ? before : row >= 0 ? &job : nullptr;
-                before = row >= 0 ? &job : nullptr;
-                if (target) {
-                    if (!finish(*target)) {
-                        gave_up(S, P, target->row);
-                        break;
-                    }
-                    leave(*target);
-                }
-            } else if (row >= 0) {
-                leave(job);
+            if (!ok) break;
+            leave(job);
+            if (!next) {
+                next = next_job();
+                if (!ok) break;
+                open1(next);
             }
-            if (row < 0) break;
-            if (last) {
-                batch.next(2);
-                k = -1;
-            }
+            job = next;
         }
     }
     // no CTA leaves while another may still write to its shared memory
@@ -983,9 +1000,12 @@ int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t st
                                        p.rows.n_rows * parts * 2 <= sms))
         parts *= 2;
     rows::RowPlan plan;
-    plan.part_vecs = int((vecs + parts - 1) / parts);
+    // whole vectors for every consumer, and whole chunks where that makes the largest part little larger
+    const int64_t part = (vecs + parts - 1) / parts;
+    const int64_t even = (part + rows::kConsumers - 1) / rows::kConsumers * rows::kConsumers;
+    const int64_t chunks = (part + rows::kChunkVecs - 1) / rows::kChunkVecs * rows::kChunkVecs;
+    plan.part_vecs = int(chunks * 20 <= even * 21 ? chunks : even);
     plan.slots = rows::slots_for(parts);
-    plan.deep = 2 * ((plan.part_vecs + rows::kChunkVecs - 1) / rows::kChunkVecs) <= plan.slots;
     const int smem = rows::smem_of(plan.slots, parts);
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(rows::kThreads);

@@ -850,6 +850,103 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     }
 }
 
+// ---------------------------------------------------------------- small rows
+// Rows of up to kSmallVecs vectors for each thread of kGroup warps stay in
+// registers from pass 1 to pass 2, and a row is a group's whole work: what such
+// rows cost is latency, and with no roles and no ring many of them are under way
+// on an SM at once.
+constexpr int kSmallVecs = 8;
+constexpr int kSmallBlock = 4;  // rows of one warp that share a block
+
+template <typename T, bool kGrad, bool kEntropy, int kGroup>
+__global__ void __launch_bounds__(kGroup == 1 ? 32 * kSmallBlock : 32 * kGroup)
+    small_rows_kernel(const __grid_constant__ LossParams P)
+{
+    constexpr int kPer = Elems<T>::kPer, kStep = 32 * kGroup;
+    __shared__ float4 sums[kGroup];
+    __shared__ RowRecord shared_rec;
+    __shared__ double scratch[kGroup == 1 ? kSmallBlock : kGroup];
+    __shared__ uint32_t flag;
+    const sampler_rows_t& a = P.rows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = kGroup == 1 ? lane : int(threadIdx.x);
+    const int64_t r = kGroup == 1 ? int64_t(blockIdx.x) * kSmallBlock + warp : int64_t(blockIdx.x);
+    if (kGroup > 1 || r < a.n_rows) {
+        RowJob job;
+        float temperature;
+        job.row = int32_t(r);
+        job_load(job, temperature, P, r);
+        job.live = job.weight != 0.f;
+        const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
+        const RowSpan span = row_span(x, a.vocab);
+        const uint4* from = reinterpret_cast<const uint4*>(x - span.head);
+        const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;  // -inf
+        const int vocab = int(a.vocab), hi = vocab + span.head;
+        uint4 v[kSmallVecs];
+#pragma unroll
+        for (int k = 0; k < kSmallVecs; ++k) {
+            const int i = tid + k * kStep;
+            v[k] = make_uint4(none, none, none, none);
+            if (job.live && i < span.count) v[k] = __ldcs(from + i);
+        }
+        job_token<T>(job, a, r, job.live);
+        row_scale(job, a, temperature);
+#pragma unroll
+        for (int k = 0; k < kSmallVecs; ++k) {
+            const int i = tid + k * kStep;
+            if (i == 0 || i == span.count - 1) Elems<T>::mask(v[k], span.head - i * kPer, hi - i * kPer);
+        }
+        Stats st = stats_empty();
+        bool bad = false;
+        fold<T, kEntropy, kSmallVecs>(st, bad, v, two(job.c_hi, job.c_hi), two(job.c_lo, job.c_lo), job.c);
+        if (bad) st.s = quiet_nan();
+        stats_warp<kEntropy>(st, job.c);
+        if (kGroup > 1) {
+            if (lane == 0) sums[warp] = make_float4(st.ref, st.s, st.t, 0.f);
+            __syncthreads();
+            if (warp == 0) {
+                st = stats_empty();
+                if (lane < kGroup) st = Stats{sums[lane].x, sums[lane].y, sums[lane].z};
+                stats_warp<kEntropy>(st, job.c);
+            }
+        }
+        RowRecord rec;
+        if (kGroup == 1 || warp == 0) {
+            RowOut out;
+            row_close(P, job, st,
+                      kGrad && P.mode == kModePolicy ? scale_of_grad(P.policy.grad_scale, P.policy.grad_scale_dev) : 1.f,
+                      rec, out);
+            if (kGroup > 1 && lane == 0) shared_rec = rec;
+            if (lane == 0) row_write(P, r, rec, out);
+        }
+        if (kGrad) {
+            if (kGroup > 1) {
+                __syncthreads();
+                rec = shared_rec;
+            }
+            T* g = static_cast<T*>(a.out_grad) + r * a.grad_stride;
+            const bool whole = ((reinterpret_cast<uintptr_t>(g) - reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
+            const Factors f = factors(rec);
+            const int tok = rec.token >= 0 && rec.token < kNoToken ? rec.token + span.head : -kPer;
+#pragma unroll
+            for (int k = 0; k < kSmallVecs; ++k) {
+                const int i = tid + k * kStep;
+                if (i < span.count)
+                    put_vector(g, vocab, span.head, i, whole,
+                               rec.token < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                                             : gradient_token<T, kEntropy>(v[k], f, tok - i * kPer, rec.at_token));
+            }
+        }
+    }
+    if (P.mode == kModePolicy) {
+        const uint32_t end = last_block(P.ws.ticket, gridDim.x, &flag);
+        if (end) {
+            const double loss = sum_terms<kGroup == 1 ? 32 * kSmallBlock : kStep>(P.ws.terms, a.n_rows, scratch);
+            if (threadIdx.x == 0) *P.policy.out_loss = end & kGaveUp ? quiet_nan() : float(loss);
+        }
+    }
+}
+
 // ---------------------------------------------------------------- pairs
 constexpr int kPairThreads = 256;
 
@@ -982,6 +1079,24 @@ RowsKernel rows_kernel_for(bool grad, bool entropy)
                      : rows::rows_kernel<T, false, false>;
 }
 
+using SmallKernel = void (*)(const LossParams);
+
+template <typename T, int kGroup>
+SmallKernel small_kernel_for(bool grad, bool entropy)
+{
+    return grad ? entropy ? rows::small_rows_kernel<T, true, true, kGroup> : rows::small_rows_kernel<T, true, false, kGroup>
+           : entropy ? rows::small_rows_kernel<T, false, true, kGroup>
+                     : rows::small_rows_kernel<T, false, false, kGroup>;
+}
+
+template <typename T>
+SmallKernel small_kernel(int group, bool grad, bool entropy)
+{
+    return group == 1   ? small_kernel_for<T, 1>(grad, entropy)
+           : group == 2 ? small_kernel_for<T, 2>(grad, entropy)
+                        : small_kernel_for<T, 4>(grad, entropy);
+}
+
 }  // namespace
 
 int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t stream)
@@ -993,6 +1108,14 @@ int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t st
     const RowsKernel kernel = es == 2 ? rows_kernel_for<uint16_t>(grad, entropy) : rows_kernel_for<float>(grad, entropy);
     // vectors of a row that starts anywhere
     const int64_t vecs = (p.rows.vocab + 2 * (16 / es - 1)) * es / 16 + 1;
+    // rows of up to 16 KB: a group of 1, 2 or 4 warps each
+    if (vecs <= 4 * 32 * rows::kSmallVecs) {
+        const int group = vecs <= 32 * rows::kSmallVecs ? 1 : vecs <= 64 * rows::kSmallVecs ? 2 : 4;
+        const SmallKernel small = es == 2 ? small_kernel<uint16_t>(group, grad, entropy) : small_kernel<float>(group, grad, entropy);
+        const int64_t blocks = group == 1 ? (p.rows.n_rows + rows::kSmallBlock - 1) / rows::kSmallBlock : p.rows.n_rows;
+        small<<<unsigned(blocks), group == 1 ? 32 * rows::kSmallBlock : 32 * group, 0, stream>>>(p);
+        return cudaGetLastError() == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
+    }
     // parts of at most kPartChunks chunks, of which two fit in the ring; smaller ones while few rows leave the
     // device unfilled
     int parts = 1;

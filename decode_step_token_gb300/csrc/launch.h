@@ -147,7 +147,8 @@ int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t st
 // The pairs' loss from the rows' logprobs, and each row's record for pairs_grad_launch.
 int pairs_launch(const sampler_rows_t& rows, const sampler_preference_t& pref, const RowWorkspace& ws,
                  cudaStream_t stream);
-int pairs_grad_launch(const sampler_rows_t& rows, const RowWorkspace& ws, cudaStream_t stream);
+// dependent: pairs_launch has been called just before on the stream.
+int pairs_grad_launch(const sampler_rows_t& rows, const RowWorkspace& ws, bool dependent, cudaStream_t stream);
 
 // ---------------------------------------------------------------- 8-bit LM head
 int quantize_launch(const sampler_quantize_t& q, int sms, cudaStream_t stream);

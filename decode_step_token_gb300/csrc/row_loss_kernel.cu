@@ -136,6 +136,11 @@ __device__ __forceinline__ void put_sums(uint32_t addr, uint32_t bar, float a, f
                  : "memory");
 }
 
+// The two kernels after the rows' are launched as programmatic dependents: their
+// blocks come up while the grid before ends, and wait for it here.
+__device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependent_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // A wait for row r (-1: for no row yet) gave up: the row says so, and the loss
 // becomes NaN.
 __device__ __noinline__ void gave_up(Shared& S, const LossParams& P, int64_t r)
@@ -530,6 +535,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     float4* sums = reinterpret_cast<float4*>(ring + slots * kChunkBytes);
     Shared& S = *reinterpret_cast<Shared*>(sums + kSums * parts * kWarps);
 
+    if (P.mode == kModePairs) dependent_launch();
     if (tid == 0) {
         for (int i = 0; i < kMaxSlots; ++i) {
             mbar_init(&S.full[i], 1);
@@ -871,6 +877,7 @@ __global__ void __launch_bounds__(kGroup == 1 ? 32 * kSmallBlock : 32 * kGroup)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int tid = kGroup == 1 ? lane : int(threadIdx.x);
     const int64_t r = kGroup == 1 ? int64_t(blockIdx.x) * kSmallBlock + warp : int64_t(blockIdx.x);
+    if (P.mode == kModePairs) dependent_launch();
     if (kGroup > 1 || r < a.n_rows) {
         RowJob job;
         float temperature;
@@ -950,78 +957,73 @@ __global__ void __launch_bounds__(kGroup == 1 ? 32 * kSmallBlock : 32 * kGroup)
 // ---------------------------------------------------------------- pairs
 constexpr int kPairThreads = 256;
 
-// Sums of one answer's rows: weight * (logprob - ref_logprob), and weight.
-__device__ __forceinline__ void answer_sums(const sampler_rows_t& a, const sampler_preference_t& q, const double* lp,
-                                            int64_t begin, int64_t end, double* scratch, double* sum, double* count)
+// One block for a pair, a half of it for an answer: the answer's sums, the
+// pair's share of the loss, and the gradient's factors of the rows. The sums are
+// in double (a reward is a small difference of long sums); what follows from the
+// margin is in fp32, in forms that lose nothing where a sigmoid is near 0 or 1.
+__global__ void __launch_bounds__(kPairThreads) pairs_kernel(const sampler_rows_t a, const sampler_preference_t q,
+                                                             const RowWorkspace ws)
 {
+    constexpr int kHalf = kPairThreads / 2, kWarpsHalf = kHalf / 32;
+    __shared__ double part[2][2 * kWarpsHalf];
+    __shared__ double scratch[kPairThreads / 32];
+    __shared__ double rewards[2];
+    __shared__ uint32_t flag;
+    const int64_t i = blockIdx.x;
+    const int k = threadIdx.x / kHalf, t = threadIdx.x % kHalf;
+    const int64_t b = q.seq_offsets[2 * i + k], e = q.seq_offsets[2 * i + k + 1];
+    const bool ok = b >= 0 && b <= e && e <= a.n_rows;
+    const int64_t begin = ok ? b : 0, end = ok ? e : 0;
+    dependent_wait();
+    dependent_launch();  // not before: the gradient's blocks would take the rows' kernel's place on the SMs
     double s = 0.0, n = 0.0;
-    for (int64_t r = begin + threadIdx.x; r < end; r += kPairThreads) {
+    for (int64_t r = begin + t; r < end; r += kHalf) {
         const float w = a.weight ? a.weight[r] : 1.f;
         if (w == 0.f) continue;
-        s += double(w) * (lp[r] - (q.ref_logprob ? double(q.ref_logprob[r]) : 0.0));
+        s += double(w) * (ws.terms[r] - (q.ref_logprob ? double(q.ref_logprob[r]) : 0.0));
         n += double(w);
     }
     for (int o = 16; o > 0; o >>= 1) {
         s += __shfl_xor_sync(0xffffffffu, s, o);
         n += __shfl_xor_sync(0xffffffffu, n, o);
     }
-    const int warp = threadIdx.x >> 5;
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
-        scratch[warp] = s;
-        scratch[kPairThreads / 32 + warp] = n;
+    if ((t & 31) == 0) {
+        part[k][t >> 5] = s;
+        part[k][kWarpsHalf + (t >> 5)] = n;
     }
     __syncthreads();
     s = n = 0.0;
-    for (int w = 0; w < kPairThreads / 32; ++w) {
-        s += scratch[w];
-        n += scratch[kPairThreads / 32 + w];
+    for (int w = 0; w < kWarpsHalf; ++w) {
+        s += part[k][w];
+        n += part[k][kWarpsHalf + w];
     }
-    *sum = s;
-    *count = n;
-}
-
-// One block for a pair: the two answers' sums, the pair's share of the loss,
-// and the gradient's factors of their rows.
-__global__ void __launch_bounds__(kPairThreads) pairs_kernel(const sampler_rows_t a, const sampler_preference_t q,
-                                                             const RowWorkspace ws)
-{
-    __shared__ double scratch[2 * kPairThreads / 32];
-    __shared__ uint32_t flag;
-    const int64_t i = blockIdx.x;
-    int64_t at[2][2];
-    double sum[2], share[2], reward[2];
-    for (int k = 0; k < 2; ++k) {
-        const int64_t b = q.seq_offsets[2 * i + k], e = q.seq_offsets[2 * i + k + 1];
-        const bool ok = b >= 0 && b <= e && e <= a.n_rows;
-        at[k][0] = ok ? b : 0;
-        at[k][1] = ok ? e : 0;
-        double count;
-        answer_sums(a, q, ws.terms, at[k][0], at[k][1], scratch, &sum[k], &count);
-        share[k] = !q.mean_over_tokens ? 1.0 : count != 0.0 ? 1.0 / count : 0.0;
-        reward[k] = ok ? double(q.beta) * (sum[k] * share[k]) : double(quiet_nan());
-        if (threadIdx.x == 0 && q.out_reward) q.out_reward[2 * i + k] = float(reward[k]);
+    const double share = !q.mean_over_tokens ? 1.0 : n != 0.0 ? 1.0 / n : 0.0;
+    const double reward = ok ? double(q.beta) * (s * share) : double(quiet_nan());
+    if (t == 0) {
+        rewards[k] = reward;
+        if (q.out_reward) q.out_reward[2 * i + k] = float(reward);
     }
-    const double z = reward[0] - reward[1] - double(q.margin);
-    const double eps = double(q.label_smoothing);
+    __syncthreads();
+    const float z = float(rewards[0] - rewards[1] - double(q.margin));
+    const float eps = q.label_smoothing, small = expf(-fabsf(z));  // exp of the negative magnitude
     if (threadIdx.x == 0) {
         // -ln sigmoid(z) = max(-z, 0) + ln(1 + exp(-|z|)); a share of 0 takes no part, even of an infinity
-        const double tail = log1p(exp(-fabs(z)));
-        const double chosen = eps != 1.0 ? (1.0 - eps) * (fmax(-z, 0.0) + tail) : 0.0;
-        const double other = eps != 0.0 ? eps * (fmax(z, 0.0) + tail) : 0.0;
-        ws.pair_terms[i] = isnan(z) ? z : chosen + other;
+        const float tail = log1pf(small);
+        const float chosen = eps != 1.f ? (1.f - eps) * (fmaxf(-z, 0.f) + tail) : 0.f;
+        const float other = eps != 0.f ? eps * (fmaxf(z, 0.f) + tail) : 0.f;
+        ws.pair_terms[i] = double(isnan(z) ? z : chosen + other);
     }
     if (a.out_grad) {
-        const double by_z = 1.0 / (1.0 + exp(-z)) - (1.0 - eps);
-        const float scale = scale_of_grad(q.grad_scale, q.grad_scale_dev);
-        for (int k = 0; k < 2; ++k) {
-            const float by_sum = float((k ? -by_z : by_z) * double(q.beta) * share[k] / double(q.n_pairs)) * scale;
-            for (int64_t r = at[k][0] + threadIdx.x; r < at[k][1]; r += kPairThreads) {
-                RowRecord rec = ws.records[r];
-                if (rec.token < 0) continue;
-                set_factors(rec, (a.weight ? a.weight[r] : 1.f) * by_sum, 0.f, 0.f, 0.f);
-                ws.records[r] = rec;
-            }
+        // d loss / d z = eps - sigmoid(-z)
+        const float by_z = eps - __fdiv_rn(z > 0.f ? small : 1.f, 1.f + small);
+        const float by_sum =
+            float(double(k ? -by_z : by_z) * (double(q.beta) * share / double(q.n_pairs))) *
+            scale_of_grad(q.grad_scale, q.grad_scale_dev);
+        for (int64_t r = begin + t; r < end; r += kHalf) {
+            RowRecord rec = ws.records[r];
+            if (rec.token < 0) continue;
+            set_factors(rec, (a.weight ? a.weight[r] : 1.f) * by_sum, 0.f, 0.f, 0.f);
+            ws.records[r] = rec;
         }
     }
     if (last_block(ws.ticket, gridDim.x, &flag) != 0u) {
@@ -1039,6 +1041,7 @@ template <typename T>
 __global__ void __launch_bounds__(kGradThreads) pairs_grad_kernel(const sampler_rows_t a, const RowWorkspace ws)
 {
     const int64_t r = a.n_rows - 1 - int64_t(blockIdx.y);
+    dependent_wait();
     const RowRecord rec = ws.records[r];
     const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
     T* g = static_cast<T*>(a.out_grad) + r * a.grad_stride;
@@ -1156,14 +1159,38 @@ int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t st
     return cudaLaunchKernelEx(&cfg, kernel, p, plan) == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
 }
 
+namespace {
+
+// As the programmatic dependent of the kernel enqueued before, or (not first)
+// after it.
+template <typename... Args>
+bool launch_dependent(void (*kernel)(Args...), dim3 grid, int threads, bool dependent, cudaStream_t stream, Args... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+}  // namespace
+
 int pairs_launch(const sampler_rows_t& rows, const sampler_preference_t& pref, const RowWorkspace& ws,
                  cudaStream_t stream)
 {
-    rows::pairs_kernel<<<unsigned(pref.n_pairs), rows::kPairThreads, 0, stream>>>(rows, pref, ws);
-    return cudaGetLastError() == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
+    // (with no rows there is no kernel of this call before it)
+    return launch_dependent(rows::pairs_kernel, dim3(unsigned(pref.n_pairs)), rows::kPairThreads, rows.n_rows > 0,
+                            stream, rows, pref, ws)
+               ? SAMPLER_OK
+               : SAMPLER_ERR_CUDA;
 }
 
-int pairs_grad_launch(const sampler_rows_t& rows, const RowWorkspace& ws, cudaStream_t stream)
+int pairs_grad_launch(const sampler_rows_t& rows, const RowWorkspace& ws, bool dependent, cudaStream_t stream)
 {
     const int es = rows.dtype == SAMPLER_DTYPE_BF16 ? 2 : 4;
     const int64_t vecs = (rows.vocab + 2 * (16 / es - 1)) * es / 16 + 1;
@@ -1177,12 +1204,13 @@ int pairs_grad_launch(const sampler_rows_t& rows, const RowWorkspace& ws, cudaSt
         some.out_grad = static_cast<char*>(rows.out_grad) + base * rows.grad_stride * es;
         at.records = ws.records + base;
         const dim3 grid(unsigned((vecs + kPer - 1) / kPer), unsigned(some.n_rows));
-        if (es == 2)
-            rows::pairs_grad_kernel<uint16_t><<<grid, rows::kGradThreads, 0, stream>>>(some, at);
-        else
-            rows::pairs_grad_kernel<float><<<grid, rows::kGradThreads, 0, stream>>>(some, at);
+        const bool ok = es == 2 ? launch_dependent(rows::pairs_grad_kernel<uint16_t>, grid, rows::kGradThreads,
+                                                   dependent && done == 0, stream, some, at)
+                                : launch_dependent(rows::pairs_grad_kernel<float>, grid, rows::kGradThreads,
+                                                   dependent && done == 0, stream, some, at);
+        if (!ok) return SAMPLER_ERR_CUDA;
     }
-    return cudaGetLastError() == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
+    return SAMPLER_OK;
 }
 
 }  // namespace dst

@@ -163,7 +163,7 @@ int sampler_preference_loss(sampler_t h, const sampler_rows_t* rows, const sampl
     }
     rc = q->n_pairs > 0 ? dst::pairs_launch(*rows, *q, h->row_ws, s) : write_zero(q->out_loss, s);
     if (rc != SAMPLER_OK || !rows->out_grad || rows->n_rows == 0) return rc;
-    return dst::pairs_grad_launch(*rows, h->row_ws, s);
+    return dst::pairs_grad_launch(*rows, h->row_ws, q->n_pairs > 0, s);
 }
 
 int sampler_quantize_blocks(sampler_t h, const sampler_quantize_t* q, sampler_stream_t stream)

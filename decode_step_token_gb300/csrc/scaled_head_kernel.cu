@@ -27,7 +27,8 @@
 // here, so its scale is one register, two products are one instruction, and
 // nothing is read from shared memory. The logits go through shared memory to the
 // TMA engine, which stores them while the next tile is under way (a warp's own
-// stores took 12 % of the time). Measured at 4096 x 128000 x 4096: 1.49 ms, 2880
+// stores took 12 % of the time). CTAs work alone (kPair false) where that takes
+// fewer rounds over the SMs: 333 rows are three tiles of 128, but two of 256. Measured at 4096 x 128000 x 4096: 1.49 ms, 2880
 // TFLOP/s.
 //
 // Persistent, one CTA an SM; warp roles:
@@ -81,7 +82,7 @@ constexpr size_t kSmemMax = 227 * 1024;
 struct Params {
     CUtensorMap to;      // many rows: the logits, boxes of 128 bytes by 32 rows, 128-byte swizzle
     CUtensorMap tm, tn;  // the operands of M and N [rows, K], 128-byte swizzle: boxes of 128 bytes by 128 and NT
-                         // rows (of a pair: 128 and 128)
+                         // rows (of many rows: 128 and 128)
     const float* hidden_scale;
     const float* weight_scale;
     int64_t hidden_scale_stride, weight_scale_stride;
@@ -517,16 +518,18 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return w;
 }
 
-// A pair's tile t: its first hidden and weight rows.
-__device__ __forceinline__ void pair_tile(const Params& P, int t, int& m, int& n)
+// Tile t of a pair or of a CTA alone: its first hidden and weight rows.
+template <bool kPair>
+__device__ __forceinline__ void wide_tile(const Params& P, int t, int& m, int& n)
 {
-    m = t % P.row_tiles * (2 * kBM);
+    m = t % P.row_tiles * (kPair ? 2 * kBM : kBM);
     n = t / P.row_tiles * kWideN;
 }
 
-// The TMA warp of each CTA of a pair: its hidden rows, and its half of the
-// weight rows for both.
-__device__ __forceinline__ void pair_produce(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
+// The TMA warp: the CTA's hidden rows, and of the weight rows its half for both
+// CTAs of a pair, or all.
+template <bool kPair>
+__device__ __forceinline__ void wide_produce(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
                                              uint32_t rank, int first, int step)
 {
     const uint32_t S = uint32_t(P.stages);
@@ -535,17 +538,23 @@ __device__ __forceinline__ void pair_produce(const Params& P, Control& C, unsign
     bool ok = true;
     for (int t = first; ok && t < P.tiles; t += step) {
         int m, n;
-        pair_tile(P, t, m, n);
+        wide_tile<kPair>(P, t, m, n);
         m += int(rank) * kBM;
         n += int(rank) * (kWideN / 2);
         for (int b = 0; b < P.blocks; ++b) {
-            ok = wait(&C.free[s.at], s.phase ^ 1u);
+            ok = wait(kPair ? &C.free[s.at] : &C.done[s.at], s.phase ^ 1u);
             if (!ok) break;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&C.ready[s.at], kABytes + kPairBBytes);
                 const uint32_t bar = smem_addr(&C.ready[s.at]);
                 tma_load_2d(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, m, bar);
-                tma_load_2d_both(smem_addr(sb + s.at * kPairBBytes + rank * (kPairBBytes / 2)), &P.tn, b * kBK, n, bar);
+                const uint32_t to = smem_addr(sb + s.at * kPairBBytes + rank * (kPairBBytes / 2));
+                if (kPair) {
+                    tma_load_2d_both(to, &P.tn, b * kBK, n, bar);
+                } else {
+                    tma_load_2d(to, &P.tn, b * kBK, n, bar);
+                    tma_load_2d(to + kPairBBytes / 2, &P.tn, b * kBK, n + kWideN / 2, bar);
+                }
             }
             __syncwarp();
             s.next(S);
@@ -555,11 +564,12 @@ __device__ __forceinline__ void pair_produce(const Params& P, Control& C, unsign
     if (!ok) C.gave_up = 1;
     // the last copies and the last stages' arrivals have come before either CTA may exit
     for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
-        if (!wait(&C.ready[j % S], j / S & 1u) || !wait(&C.free[j % S], j / S & 1u)) C.gave_up = 1;
+        if (!wait(&C.ready[j % S], j / S & 1u) || !wait(kPair ? &C.free[j % S] : &C.done[j % S], j / S & 1u)) C.gave_up = 1;
 }
 
-// The MMA warp of each CTA of a pair.
-__device__ __forceinline__ void pair_multiply(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
+// The MMA warp of a CTA of many rows.
+template <bool kPair>
+__device__ __forceinline__ void wide_multiply(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
                                               uint32_t tmem, int first, int step)
 {
     const uint32_t idesc = idesc_e4m3(kBM, kWideN);
@@ -578,7 +588,7 @@ __device__ __forceinline__ void pair_multiply(const Params& P, Control& C, unsig
                 for (int k = 0; k < kBK / kUK; ++k)  // +32 bytes inside the 128-byte rows
                     mma_e4m3(d, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, uint32_t(k));
                 mma_commit(&C.done[s.at]);
-                mma_commit_both(&C.free[s.at]);
+                if (kPair) mma_commit_both(&C.free[s.at]);
             }
             __syncwarp();
             s.next(uint32_t(P.stages));
@@ -592,9 +602,8 @@ __device__ __forceinline__ void pair_multiply(const Params& P, Control& C, unsig
 }
 
 // Many rows: the hidden rows are M, the weight N.
-template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    many_rows_kernel(const __grid_constant__ Params P)
+template <typename T, bool kPair>
+__global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_constant__ Params P)
 {
     constexpr int kCols = kWideN / 2;                  // of a thread: a block of the weight's scales
     constexpr int kBoxCols = 128 / int(sizeof(T));     // of a box of logits
@@ -604,17 +613,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     unsigned char* outs = sb + size_t(P.stages) * kPairBBytes;
     Control& C = *reinterpret_cast<Control*>(outs + kOutBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t rank = cluster_ctarank();
-    const int first = int(blockIdx.x >> 1), step = int(gridDim.x >> 1);
+    const uint32_t rank = kPair ? cluster_ctarank() : 0u;
+    const int first = int(kPair ? blockIdx.x >> 1 : blockIdx.x), step = int(kPair ? gridDim.x >> 1 : gridDim.x);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    begin<true>(P, C);
+    begin<kPair>(P, C);
     const uint32_t tmem = C.tmem;
 
     if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewPairRegs));
     if (warp == 8) {
-        pair_produce(P, C, sa, sb, rank, first, step);
+        wide_produce<kPair>(P, C, sa, sb, rank, first, step);
     } else if (warp == 9) {
-        pair_multiply(P, C, sa, sb, tmem, first, step);
+        wide_multiply<kPair>(P, C, sa, sb, tmem, first, step);
     } else if (warp < 8) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyPairRegs));
         const int group = warp >> 2, quarter = warp & 3;
@@ -629,7 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int row0 = 0, v0 = 0;  // of the tile that is fetched for
         const float *ph = nullptr, *pw = nullptr;
         auto place = [&](int t) {
-            pair_tile(P, t, row0, v0);
+            wide_tile<kPair>(P, t, row0, v0);
             row0 += int(rank) * kBM + quarter * 32;
             v0 += group * kCols;
             ph = P.hidden_scale + int64_t(row0 + lane) * P.hidden_scale_stride;
@@ -729,7 +738,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (P.tma_stores && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!ok && lane == 0) C.gave_up = 1;
     }
-    end<true>(P, C, tmem);
+    end<kPair>(P, C, tmem);
 }
 
 // ---------------------------------------------------------------- host side
@@ -780,9 +789,9 @@ bool encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int6
 using Kernel = void (*)(const Params);
 
 template <typename T>
-Kernel kernel_for(bool few, int NT)
+Kernel kernel_for(bool few, bool pair, int NT)
 {
-    return !few       ? many_rows_kernel<T>
+    return !few       ? pair ? many_rows_kernel<T, true> : many_rows_kernel<T, false>
            : NT <= 32 ? few_rows_kernel<T, 16>
            : NT <= 64 ? few_rows_kernel<T, 32>
                       : few_rows_kernel<T, 64>;
@@ -797,7 +806,12 @@ int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, 
     Params p;
     std::memset(&p, 0, sizeof p);
     const bool few = rows <= kFewRows;
-    p.row_tiles = few ? 1 : int((rows + 2 * kBM - 1) / (2 * kBM));
+    // rounds over the SMs of either way; a CTA alone loads half as much again for a tile, about 15 % of its time
+    const int64_t wide = (vocab + kWideN - 1) / kWideN;
+    const int64_t rounds_pair = ((rows + 2 * kBM - 1) / (2 * kBM) * wide + sms / 2 - 1) / std::max(sms / 2, 1);
+    const int64_t rounds_alone = ((rows + kBM - 1) / kBM * wide + sms - 1) / sms;
+    const bool pair = !few && sms >= 2 && rounds_alone * 115 >= rounds_pair * 100;
+    p.row_tiles = few ? 1 : int((rows + (pair ? 2 : 1) * kBM - 1) / ((pair ? 2 : 1) * kBM));
     p.NT = few ? int((rows + 15) / 16 * 16) : kWideN;
     const int64_t tiles = (vocab + (few ? kBM : kWideN) - 1) / (few ? kBM : kWideN) * p.row_tiles;
     if (tiles > INT32_MAX - 65536) return SAMPLER_ERR_TOO_LARGE;
@@ -828,13 +842,18 @@ int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, 
     p.rows = int(rows);
     p.V = int(vocab);
     p.timeouts = timeouts;
-    const Kernel kernel = dtype == SAMPLER_DTYPE_BF16 ? kernel_for<uint16_t>(few, p.NT) : kernel_for<float>(few, p.NT);
+    const Kernel kernel = dtype == SAMPLER_DTYPE_BF16 ? kernel_for<uint16_t>(few, pair, p.NT) : kernel_for<float>(few, pair, p.NT);
     const size_t smem = 1024 + size_t(p.stages) * stage + own + kBarBytes;
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(smem)) != cudaSuccess)
         return SAMPLER_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(few ? std::min(sms, p.tiles) : 2 * std::min(sms / 2, p.tiles)));
+    cfg.gridDim = dim3(unsigned(pair ? 2 * std::min(sms / 2, p.tiles) : std::min(sms, p.tiles)));
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {2u, 1u, 1u};
+    cfg.attrs = &attr;
+    cfg.numAttrs = pair ? 1 : 0;
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

@@ -173,6 +173,14 @@ SHAPES = [
     dict(n=20, V=151936, kind="bf16", heat=True), dict(n=2, V=262144, heat=True), dict(n=2, V=262144, kind="bf16"),
     dict(n=700, V=3000, kind="bf16", kept=0.9), dict(n=320, V=20011, kind="bf16", heat=True, kept=0.9, pad=5),
 ]
+# several rows for each cluster, at every way of cutting a row: one CTA a row and more, parts of which two fit in
+# the ring and parts of which one does, rows in registers
+MANY = [
+    dict(n=650, V=9001, kind="bf16", kept=0.6), dict(n=330, V=32000, kind="bf16"),
+    dict(n=170, V=64000, kind="bf16", kept=0.5, heat=True), dict(n=100, V=128000, kind="bf16", kept=0.8),
+    dict(n=90, V=151936, kind="bf16", pad=3, shift=1), dict(n=50, V=128000, kept=0.9), dict(n=40, V=200003, pad=1),
+    dict(n=900, V=1500, kept=0.5), dict(n=300, V=5000, kind="bf16", banned=0.3), dict(n=300, V=4001, shift=3),
+]
 
 
 def _id(s):
@@ -198,6 +206,27 @@ def test_score_grad(sampler, shape, entropy):
                        grad_entropy=torch.from_numpy(b).cuda() if entropy else None, **c.kw())
     got = L.score(c.x, c.tokens, c.T, c.weight)
     tol = c.check_rows(got)
+    got["grad"] = L.logits_grad(got, c.tokens, a.astype(np.float64), b, c.T, c.weight)
+    c.check_grad(got, tol, a, np.zeros(c.n), b)
+
+
+@pytest.mark.parametrize("shape", MANY, ids=_id)
+@pytest.mark.parametrize("mode", ["score", "clip", "entropy"])
+def test_many_rows(sampler, shape, mode):
+    import torch
+
+    c = Rows(12, grad=mode != "score", **shape)
+    if mode == "score":
+        sampler.score(**c.kw())
+        c.check_rows(L.score(c.x, c.tokens, c.T, c.weight), entropy=False)
+        return
+    a = c.rng.standard_normal(c.n).astype(np.float32)
+    b = c.rng.standard_normal(c.n).astype(np.float32) if mode == "entropy" else None
+    sampler.score_grad(grad_logprob=torch.from_numpy(a).cuda(), out_grad=c.grad,
+                       out_entropy=c.out["entropy"] if b is not None else None,
+                       grad_entropy=torch.from_numpy(b).cuda() if b is not None else None, **c.kw())
+    got = L.score(c.x, c.tokens, c.T, c.weight)
+    tol = c.check_rows(got, entropy=b is not None)
     got["grad"] = L.logits_grad(got, c.tokens, a.astype(np.float64), b, c.T, c.weight)
     c.check_grad(got, tol, a, np.zeros(c.n), b)
 

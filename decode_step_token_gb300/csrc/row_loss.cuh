@@ -140,7 +140,9 @@ __device__ __forceinline__ void row_scale(RowJob& h, const sampler_rows_t& a, fl
     h.inv_t_lo = fmaf(-Te, h.inv_t, 1.f) * h.inv_t;
     h.c = kLog2e * h.inv_t;
     const float rest = fmaf(kLog2e, h.inv_t, -h.c) + fmaf(kLog2e, h.inv_t_lo, kLog2eRest * h.inv_t);
-    h.c_hi = __int_as_float(__float_as_int(h.c) - 1);
+    // `rest` is above -1.8 units of c's last place (half of one, one by inv_t's rounding, and kLog2eRest's): four
+    // steps down, which are two of them just above a power of two
+    h.c_hi = __int_as_float(__float_as_int(h.c) - 4);
     h.c_lo = (h.c - h.c_hi) + rest;
 }
 

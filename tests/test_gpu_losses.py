@@ -419,6 +419,27 @@ def test_gradient_in_place(sampler, kind, n, V):
     assert torch.equal(c.logits, apart)
 
 
+@pytest.mark.parametrize("V,kind", [(33, "bf16"), (70, "f32"), (20011, "bf16")])
+def test_forbidden_tokens_at_many_temperatures(sampler, V, kind):
+    """-inf logits (and the elements of a row's neighbours that its first and last vectors hold) stay without
+    mass at every temperature: the factor log2(e) / T is a pair, whose parts have to have the same sign."""
+    import torch
+
+    n = 2048
+    gen = torch.Generator(device="cuda:0").manual_seed(2)
+    x = torch.randn((n, V), generator=gen, device="cuda:0").to(torch.bfloat16 if kind == "bf16" else torch.float32)
+    x[:, 1::3] = -torch.inf
+    T = 10.0 ** (6.0 * torch.rand(n, generator=gen, device="cuda:0") - 2.0)
+    tok = torch.zeros(n, dtype=torch.int32, device="cuda:0")
+    lp, ent = torch.empty(n, device="cuda:0"), torch.empty(n, device="cuda:0")
+    sampler.score(logits=x, tokens=tok, temperature=T, out_logprob=lp, out_entropy=ent)
+    want = torch.log_softmax(x.double() / T.double()[:, None], 1)[:, 0]
+    # see the tolerances above: the depth of a token at T = 0.01 is up to 800 nats
+    tol = 2.0 ** -22 + 3 * EPS * want.abs() * 2 + 4 * (V / 256 + 64) ** 0.5 * EPS + EPS * want.abs() + 2 * EPS
+    assert torch.isfinite(lp).all() and torch.isfinite(ent).all()
+    assert ((lp.double() - want).abs() <= tol).all()
+
+
 def test_same_bits_each_time_and_in_a_graph(sampler):
     import torch
 

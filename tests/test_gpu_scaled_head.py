@@ -113,6 +113,9 @@ def _close(got, want, mag, K, kind):
 SHAPES = [(1, 1, 1), (1, 128, 128), (2, 129, 130), (3, 1000, 64), (16, 4096, 256), (17, 300, 1000), (31, 5003, 96),
           (64, 2000, 512), (65, 257, 129), (127, 640, 384), (128, 1024, 1024), (129, 1025, 300), (200, 3001, 256),
           (255, 511, 200), (256, 256, 4096), (257, 1300, 640), (513, 900, 16), (700, 1111, 1000),
+          # few tiles with many blocks of K
+          (1, 1, 600), (16, 1000, 4096), (32, 2000, 3000), (8, 2000, 8192), (5, 4000, 2500), (20, 9001, 1024),
+          (40, 3000, 4100), (64, 500, 1900), (100, 5000, 2048), (128, 130, 1030), (33, 1921, 4096),
           # several tiles for each CTA and pair, with more than one ring's blocks
           (140, 42000, 1300), (300, 21000, 640), (600, 20003, 384), (40, 40011, 2100)]
 

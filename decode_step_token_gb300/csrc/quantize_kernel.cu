@@ -9,6 +9,8 @@
 // shuffle among those lanes, blocks of 128 rows the whole thread block.
 // Magnitudes are compared as the integers of their bits, in which an infinity
 // and a NaN are the largest.
+// Measured: a weight of 128000 x 4096 bf16 in blocks of 128 x 128 in 226 us, 6.9
+// TB/s (the copy rate); 64 hidden rows of 4096 in 1.9 us, which is the launch.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -180,7 +182,9 @@ bool launch(sampler_quantize_t q, int sms, cudaStream_t stream)
     const bool vec_out = reinterpret_cast<uintptr_t>(q.values) % Elems<T>::kPer == 0 && q.values_stride % Elems<T>::kPer == 0;
     const int64_t across = (q.cols + 127) / 128;
     const bool square = q.block_rows == 128;
-    // one row a thread while that leaves the device unfilled, for its latency; else several loads in flight
+    // one row a thread while that leaves the device unfilled, for its latency; else several loads in flight (bf16,
+    // x 4096, one / several: 64 rows 1.5 / 2.5 us, 600 rows 3.2 / 4.2, 1200 rows 5.0 / 5.3, 4096 rows 13.0 / 12.3,
+    // 32768 rows 88 / 72)
     const bool few = !square && (q.rows + kRows - 1) / kRows * across <= int64_t(sms) * 8;
     const int rows = square ? 128 : few ? kRows : 64;
     // the grid's second dimension is limited: taller matrices go in several launches

@@ -31,7 +31,8 @@ constexpr int32_t kNoToken = 0x7fffffff;  // of a row with an error status: matc
 constexpr float kLowest = -3e4f;   // exponents are not taken below this where they are multiplied by 2^u (= 0)
 // ex2.approx is on average this much too small, of its value (means of -2.5e-8 to -5.0e-8 over ranges of length 0.5
 // to 20 below 0; at most 1.5e-7). A row's sum is, too, but for the exact 1 of its largest element, and so would be
-// all logprobs of a sequence the same way.
+// all logprobs of a sequence the same way. The mean error of 2048 logprobs against 64 bits, without and with this:
+// 4.4e-8 and 1.0e-8 (128000 bf16), 4.7e-8 and 0.8e-8 (1024 fp32), 7.5e-8 and 4.0e-8 (151936 fp32).
 constexpr float kExp2Short = 4e-8f;
 constexpr float kFloatMax = 3.402823466e38f;
 

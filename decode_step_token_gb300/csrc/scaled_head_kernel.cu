@@ -9,27 +9,32 @@
 // of tensor memory; there are two accumulators or more, so that the tensor cores
 // fill one while the threads empty another.
 //
-// Few rows (a decode step; up to kFewRows) are taken transposed: a tile is 128
-// weight rows (M: one block of the weight's scales, so that scale is one number
-// for a tile and block) by all hidden rows (N). The weight's bytes are all the
-// time then. A column's scale is the same for all lanes and comes from shared
-// memory; the accumulators are up to eight, and the lanes are neighbouring
-// tokens of the vocabulary, so that the logits are stored as they lie.
+// Few rows (a small decode step; up to kFewRows) are taken transposed: a tile is
+// 128 weight rows (M: one block of the weight's scales, so that scale is one
+// number for a tile and block) by all hidden rows (N). The weight's bytes are all
+// the time then. A column's scale is the same for all lanes and comes from shared
+// memory; the accumulators are up to eight, and the lanes are neighbouring tokens
+// of the vocabulary, so that the logits are stored as they lie.
 //
-// Many rows (a prompt) are taken as they are, by pairs of CTAs: 256 hidden rows,
-// 128 in each CTA (M), by 256 weight rows (N) that both CTAs need; each loads half
-// of those and the TMA engine puts them into both (multicast). So a block costs a
-// CTA 32 KB from L2 instead of 48 KB, with which L2 would be the time (15 to 17
-// TB/s measured, whatever else was left out). Each CTA has its own MMAs and
-// accumulators, because the way of an accumulator round through the epilogue (its
+// More rows are taken as they are: 128 hidden rows (M) by 256 weight rows (N). A
+// lane is a hidden row here, so its scale is one register, two products are one
+// instruction, and nothing is read from shared memory. The logits go through
+// shared memory to the TMA engine, which stores them while the next tile is under
+// way (a warp's own stores took 12 % of the time). N is as wide as two accumulators
+// of tensor memory allow: the way of an accumulator round through the epilogue (its
 // completion seen, its columns read, its release seen by the MMA warp) has to fit
-// in one block's MMAs, and is too long across two CTAs. A lane is a hidden row
-// here, so its scale is one register, two products are one instruction, and
-// nothing is read from shared memory. The logits go through shared memory to the
-// TMA engine, which stores them while the next tile is under way (a warp's own
-// stores took 12 % of the time). CTAs work alone (kPair false) where that takes
-// fewer rounds over the SMs: 333 rows are three tiles of 128, but two of 256. Measured at 4096 x 128000 x 4096: 1.49 ms, 2880
-// TFLOP/s.
+// in one block's MMAs, and wider tiles load less from L2. Pairs of CTAs that share
+// their weight tile by multicast load a third less, but wait for each other: 1.49
+// against 1.46 ms at 4096 x 128000 x 4096, and one tile of 256 rows where CTAs
+// alone have two (333 x 20011 x 1000: 41 against 30 us).
+//
+// Where the two meet (x 4096 where nothing is said, transposed / not): 16 x 128000
+// 86 / 107 us, 32 x 64000 53 / 49, 32 x 40000 x 1024 15 / 16, 33 x 128000 92 / 94,
+// 64 x 128000 94 / 95.5, 64 x 64000 57 / 51, 64 x 256000 x 1024 60 / 51, 96 x 128000
+// 121 / 97.
+//
+// Measured: 16 x 128000 x 4096 86 us (6.1 TB/s, 91 % of the copy rate); 4096 x
+// 128000 x 4096 1.46 ms, 2940 TFLOP/s.
 //
 // Persistent, one CTA an SM; warp roles:
 //   warps 0-7  the epilogue: two groups of four warps, each a half of the tile's
@@ -37,7 +42,7 @@
 //   warp 8     issues the TMA loads of the operand ring;
 //   warp 9     owns the tensor memory and issues the MMAs.
 // Warps 10 and 11 fill up the third warpgroup, which gives its registers to the
-// epilogue's (a thread there holds up to 128 sums).
+// epilogue's where those hold 128 sums a thread (more rows).
 // Every wait is bounded in time; a CTA whose wait gives up counts itself in the
 // handle's statistics and leaves its logits unwritten.
 #include <cuda.h>
@@ -59,16 +64,15 @@ constexpr int kBM = 128;                       // MMA M, and a block of the weig
 constexpr int kBK = 128;                       // K of a stage: a block of scales, one 128-byte swizzled row
 constexpr int kUK = 32;                        // K of one tcgen05.mma of 8-bit operands
 constexpr int kThreads = 384;
-constexpr int kFewRegs = 40, kManyRegs = 224;  // 128 * 40 + 256 * 224 <= 384 * 168
+constexpr int kFewRegs = 24, kManyRegs = 240;  // many rows: 128 * 24 + 256 * 240 <= 384 * 168
 constexpr int kGroupThreads = 128;             // of one half of the columns
 constexpr int kMaxStages = 8;
 constexpr int kMaxAccs = 8;
 constexpr int kTmemCols = 512;
-constexpr int kFewRows = 128;                  // the most that are taken transposed
+constexpr int kFewRows = 32;                   // the most that are taken transposed (see above)
 constexpr int kWideN = 256;                    // weight rows of a tile of many hidden rows
-constexpr int kPairAccs = kTmemCols / kWideN;
-constexpr uint32_t kPairBBytes = kWideN * kBK; // of a stage
-constexpr int kFewPairRegs = 24, kManyPairRegs = 240;  // 128 * 24 + 256 * 240 <= 384 * 168
+constexpr int kWideAccs = kTmemCols / kWideN;
+constexpr uint32_t kWideBytes = kWideN * kBK; // of a stage
 constexpr int kLoad = 16;                      // columns that a thread reads at once (32: registers spill, 2264 TFLOP/s)
 constexpr uint32_t kBoxBytes = 32 * 128;       // a box of logits: 32 rows of 128 bytes, swizzled
 constexpr uint32_t kOutBytes = 8 * kBoxBytes;  // one for each warp of the epilogue: with more, a stage less
@@ -82,7 +86,7 @@ constexpr size_t kSmemMax = 227 * 1024;
 struct Params {
     CUtensorMap to;      // many rows: the logits, boxes of 128 bytes by 32 rows, 128-byte swizzle
     CUtensorMap tm, tn;  // the operands of M and N [rows, K], 128-byte swizzle: boxes of 128 bytes by 128 and NT
-                         // rows (of many rows: 128 and 128)
+                         // rows
     const float* hidden_scale;
     const float* weight_scale;
     int64_t hidden_scale_stride, weight_scale_stride;
@@ -146,27 +150,6 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar)
 {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
                  : "memory");
-}
-
-// The same into the shared memory of both CTAs of a pair, each of which counts
-// the bytes on its own barrier at that place.
-__device__ __forceinline__ void tma_load_2d_both(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, "
-        "{%2, %3}], [%4], %5;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "h"(uint16_t(3))
-        : "memory");
-}
-
-// Arrive on `bar` of both CTAs once every MMA issued before has completed.
-__device__ __forceinline__ void mma_commit_both(uint64_t* bar)
-{
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_addr(bar)),
-        "h"(uint16_t(3))
-        : "memory");
 }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src)
@@ -275,14 +258,12 @@ struct Control {
     uint64_t ready[kMaxStages];  // of the block in a stage: its operands have come, and its accumulator has been read
                                  // by every warp of the epilogue
     uint64_t done[kMaxStages];   // its MMAs have completed: the accumulator can be read, the stage filled again
-    uint64_t free[kMaxStages];   // of a pair: done in both CTAs, whose stages are filled together
     uint64_t drained;            // every MMA of the CTA has completed
     uint32_t tmem;
     int gave_up;
 };
 static_assert(sizeof(Control) <= kBarBytes, "");
 
-template <bool kPair>
 __device__ __forceinline__ void begin(const Params& P, Control& C)
 {
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -290,7 +271,6 @@ __device__ __forceinline__ void begin(const Params& P, Control& C)
         for (int s = 0; s < kMaxStages; ++s) {
             mbar_init(&C.ready[s], 1 + 8);
             mbar_init(&C.done[s], 1);
-            mbar_init(&C.free[s], 2);
         }
         mbar_init(&C.drained, 1);
         C.gave_up = 0;
@@ -306,40 +286,46 @@ __device__ __forceinline__ void begin(const Params& P, Control& C)
     }
     fence_before_sync();
     __syncthreads();
-    if (kPair) cluster_sync();
     fence_after_sync();
 }
 
-template <bool kPair>
 __device__ __forceinline__ void end(const Params& P, Control& C, uint32_t tmem)
 {
     fence_before_sync();
     __syncthreads();
-    if (kPair) {
-        // nothing that the other CTA sends (halves of stages, arrivals) is under way any more
-        cluster_sync();
-    }
     fence_after_sync();
     if (threadIdx.x >> 5 == 9)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(P.tmem_cols) : "memory");
     if (threadIdx.x == 0 && C.gave_up && P.timeouts) atomicAdd(P.timeouts, 1ull);
 }
 
-// The TMA warp of a CTA that works alone.
+// Tile t: its first rows of M and of N. (Of many rows, tiles that follow one
+// another have the same weight rows, which are then in L2.)
+template <bool kFew>
+__device__ __forceinline__ void tile_at(const Params& P, int t, int& m, int& n)
+{
+    m = kFew ? t * kBM : t % P.row_tiles * kBM;
+    n = kFew ? 0 : t / P.row_tiles * kWideN;
+}
+
+// The TMA warp.
+template <bool kFew>
 __device__ __forceinline__ void produce(const Params& P, Control& C, unsigned char* sa, unsigned char* sb)
 {
-    const uint32_t S = uint32_t(P.stages), b_bytes = uint32_t(P.NT) * kBK;
+    const uint32_t S = uint32_t(P.stages), b_bytes = kFew ? uint32_t(P.NT) * kBK : kWideBytes;
     Ring s{0, 0};
     uint32_t issued = 0;
     bool ok = true;
     for (int t = int(blockIdx.x); ok && t < P.tiles; t += int(gridDim.x)) {
+        int m, n;
+        tile_at<kFew>(P, t, m, n);
         for (int b = 0; b < P.blocks; ++b) {
             ok = wait(&C.done[s.at], s.phase ^ 1u);
             if (!ok) break;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&C.ready[s.at], kABytes + b_bytes);
-                tma_load_2d(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, t * kBM, smem_addr(&C.ready[s.at]));
-                tma_load_2d(smem_addr(sb + s.at * b_bytes), &P.tn, b * kBK, 0, smem_addr(&C.ready[s.at]));
+                tma_load_2d(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, m, smem_addr(&C.ready[s.at]));
+                tma_load_2d(smem_addr(sb + s.at * b_bytes), &P.tn, b * kBK, n, smem_addr(&C.ready[s.at]));
             }
             __syncwarp();
             s.next(S);
@@ -352,20 +338,22 @@ __device__ __forceinline__ void produce(const Params& P, Control& C, unsigned ch
 }
 
 // The MMA warp: each block of K into the next accumulator.
+template <bool kFew>
 __device__ __forceinline__ void multiply(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
                                          uint32_t tmem)
 {
-    const uint32_t idesc = idesc_e4m3(kBM, P.NT), b_bytes = uint32_t(P.NT) * kBK;
+    const uint32_t cols = kFew ? uint32_t(P.NT) : uint32_t(kWideN), b_bytes = cols * kBK;
+    const uint32_t idesc = idesc_e4m3(kBM, int(cols)), accs = kFew ? uint32_t(P.accs) : uint32_t(kWideAccs);
     Ring s{0, 0}, acc{0, 0};
     bool ok = true;
     for (int t = int(blockIdx.x); ok && t < P.tiles; t += int(gridDim.x)) {
         for (int b = 0; b < P.blocks; ++b) {
+            const uint32_t d = tmem + acc.at * cols;
+            const uint64_t da = desc_sw128(smem_addr(sa + s.at * kABytes));
+            const uint64_t db = desc_sw128(smem_addr(sb + s.at * b_bytes));
             ok = wait(&C.ready[s.at], s.phase);
             if (!ok) break;
             fence_after_sync();
-            const uint32_t d = tmem + acc.at * uint32_t(P.NT);
-            const uint64_t da = desc_sw128(smem_addr(sa + s.at * kABytes));
-            const uint64_t db = desc_sw128(smem_addr(sb + s.at * b_bytes));
             if (elect_one()) {
 #pragma unroll
                 for (int k = 0; k < kBK / kUK; ++k)  // +32 bytes inside the 128-byte rows
@@ -374,7 +362,7 @@ __device__ __forceinline__ void multiply(const Params& P, Control& C, unsigned c
             }
             __syncwarp();
             s.next(uint32_t(P.stages));
-            acc.next(uint32_t(P.accs));
+            acc.next(accs);
         }
     }
     if (!ok) C.gave_up = 1;
@@ -407,10 +395,11 @@ __device__ __forceinline__ void free_first(const Params& P, Control& C, int lane
     __syncwarp();
 }
 
-// Few rows: the weight is M, the hidden rows N = NT <= 2 * kCols.
-template <typename T, int kCols>
+// Few rows: the weight is M, the hidden rows N = NT, 16 or 32.
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_constant__ Params P)
 {
+    constexpr int kCols = kFewRows / 2;  // of a thread
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sa = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char* sb = sa + size_t(P.stages) * kABytes;
@@ -418,20 +407,17 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
     Control& C = *reinterpret_cast<Control*>(reinterpret_cast<unsigned char*>(scales) + kScaleBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    begin<false>(P, C);
+    begin(P, C);
     const uint32_t tmem = C.tmem;
 
-    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     if (warp == 8) {
-        produce(P, C, sa, sb);
+        produce<true>(P, C, sa, sb);
     } else if (warp == 9) {
-        multiply(P, C, sa, sb, tmem);
+        multiply<true>(P, C, sa, sb, tmem);
     } else if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         const int group = warp >> 2, quarter = warp & 3;  // quarter: the tensor-memory lanes a warp may read
         const int j = quarter * 32 + lane;                // thread of the group: it fetches column j's scales
-        const int half = ((P.NT >> 1) + 15) & ~15;
-        const int c0 = group * half, cols = max(0, min(half, P.NT - c0));
+        const int c0 = group * kCols, cols = max(0, min(kCols, P.NT - c0));  // 0 or kCols
         const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(c0);
         const bool has = j < cols && c0 + j < P.rows;
         const float* sh = P.hidden_scale + int64_t(c0 + j) * P.hidden_scale_stride;
@@ -474,22 +460,18 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
                     fence_after_sync();
                     const uint32_t at = lanes + acc.at * uint32_t(P.NT);
                     uint32_t r[kCols];
+                    if (cols > 0) {
+                        tmem_ld16(at, r);
+                        tmem_wait();
+                        tmem_take16(r);
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 16)
-                        if (c < cols) tmem_ld16(at + c, r + c);
-                    tmem_wait();
-                    fence_before_sync();
-#pragma unroll
-                    for (int c = 0; c < kCols; c += 16) {
-                        tmem_take16(r + c);
-                        if (c < cols)
-#pragma unroll
-                            for (int i = c; i < c + 16; i += 4) {
-                                const float4 s = *reinterpret_cast<const float4*>(row + i);
-                                fma2(sum[i / 2], r[i], r[i + 1], s.x, s.y);
-                                fma2(sum[i / 2 + 1], r[i + 2], r[i + 3], s.z, s.w);
-                            }
+                        for (int i = 0; i < kCols; i += 4) {
+                            const float4 s = *reinterpret_cast<const float4*>(row + i);
+                            fma2(sum[i / 2], r[i], r[i + 1], s.x, s.y);
+                            fma2(sum[i / 2 + 1], r[i + 2], r[i + 3], s.z, s.w);
+                        }
                     }
+                    fence_before_sync();
                 }
                 __syncwarp();
                 if (ok && lane == 0) arrive(&C.ready[freed]);
@@ -508,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
         }
         if (!ok && lane == 0) C.gave_up = 1;
     }
-    end<false>(P, C, tmem);
+    end(P, C, tmem);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
@@ -518,91 +500,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return w;
 }
 
-// Tile t of a pair or of a CTA alone: its first hidden and weight rows.
-template <bool kPair>
-__device__ __forceinline__ void wide_tile(const Params& P, int t, int& m, int& n)
-{
-    m = t % P.row_tiles * (kPair ? 2 * kBM : kBM);
-    n = t / P.row_tiles * kWideN;
-}
-
-// The TMA warp: the CTA's hidden rows, and of the weight rows its half for both
-// CTAs of a pair, or all.
-template <bool kPair>
-__device__ __forceinline__ void wide_produce(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
-                                             uint32_t rank, int first, int step)
-{
-    const uint32_t S = uint32_t(P.stages);
-    Ring s{0, 0};
-    uint32_t issued = 0;
-    bool ok = true;
-    for (int t = first; ok && t < P.tiles; t += step) {
-        int m, n;
-        wide_tile<kPair>(P, t, m, n);
-        m += int(rank) * kBM;
-        n += int(rank) * (kWideN / 2);
-        for (int b = 0; b < P.blocks; ++b) {
-            ok = wait(kPair ? &C.free[s.at] : &C.done[s.at], s.phase ^ 1u);
-            if (!ok) break;
-            if (elect_one()) {
-                mbar_arrive_expect_tx(&C.ready[s.at], kABytes + kPairBBytes);
-                const uint32_t bar = smem_addr(&C.ready[s.at]);
-                tma_load_2d(smem_addr(sa + s.at * kABytes), &P.tm, b * kBK, m, bar);
-                const uint32_t to = smem_addr(sb + s.at * kPairBBytes + rank * (kPairBBytes / 2));
-                if (kPair) {
-                    tma_load_2d_both(to, &P.tn, b * kBK, n, bar);
-                } else {
-                    tma_load_2d(to, &P.tn, b * kBK, n, bar);
-                    tma_load_2d(to + kPairBBytes / 2, &P.tn, b * kBK, n + kWideN / 2, bar);
-                }
-            }
-            __syncwarp();
-            s.next(S);
-            ++issued;
-        }
-    }
-    if (!ok) C.gave_up = 1;
-    // the last copies and the last stages' arrivals have come before either CTA may exit
-    for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j)
-        if (!wait(&C.ready[j % S], j / S & 1u) || !wait(kPair ? &C.free[j % S] : &C.done[j % S], j / S & 1u)) C.gave_up = 1;
-}
-
-// The MMA warp of a CTA of many rows.
-template <bool kPair>
-__device__ __forceinline__ void wide_multiply(const Params& P, Control& C, unsigned char* sa, unsigned char* sb,
-                                              uint32_t tmem, int first, int step)
-{
-    const uint32_t idesc = idesc_e4m3(kBM, kWideN);
-    Ring s{0, 0}, acc{0, 0};
-    bool ok = true;
-    for (int t = first; ok && t < P.tiles; t += step) {
-        for (int b = 0; b < P.blocks; ++b) {
-            const uint32_t d = tmem + acc.at * uint32_t(kWideN);
-            const uint64_t da = desc_sw128(smem_addr(sa + s.at * kABytes));
-            const uint64_t db = desc_sw128(smem_addr(sb + s.at * kPairBBytes));
-            ok = wait(&C.ready[s.at], s.phase);
-            if (!ok) break;
-            fence_after_sync();
-            if (elect_one()) {
-#pragma unroll
-                for (int k = 0; k < kBK / kUK; ++k)  // +32 bytes inside the 128-byte rows
-                    mma_e4m3(d, da + uint64_t(2 * k), db + uint64_t(2 * k), idesc, uint32_t(k));
-                mma_commit(&C.done[s.at]);
-                if (kPair) mma_commit_both(&C.free[s.at]);
-            }
-            __syncwarp();
-            s.next(uint32_t(P.stages));
-            acc.next(kPairAccs);
-        }
-    }
-    if (!ok) C.gave_up = 1;
-    if (elect_one()) mma_commit(&C.drained);
-    __syncwarp();
-    wait(&C.drained, 0);
-}
-
 // Many rows: the hidden rows are M, the weight N.
-template <typename T, bool kPair>
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_constant__ Params P)
 {
     constexpr int kCols = kWideN / 2;                  // of a thread: a block of the weight's scales
@@ -610,27 +509,26 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sa = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char* sb = sa + size_t(P.stages) * kABytes;
-    unsigned char* outs = sb + size_t(P.stages) * kPairBBytes;
+    unsigned char* outs = sb + size_t(P.stages) * kWideBytes;
     Control& C = *reinterpret_cast<Control*>(outs + kOutBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const uint32_t rank = kPair ? cluster_ctarank() : 0u;
-    const int first = int(kPair ? blockIdx.x >> 1 : blockIdx.x), step = int(kPair ? gridDim.x >> 1 : gridDim.x);
+    const int first = int(blockIdx.x), step = int(gridDim.x);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    begin<kPair>(P, C);
+    begin(P, C);
     const uint32_t tmem = C.tmem;
 
-    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewPairRegs));
+    if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     if (warp == 8) {
-        wide_produce<kPair>(P, C, sa, sb, rank, first, step);
+        produce<false>(P, C, sa, sb);
     } else if (warp == 9) {
-        wide_multiply<kPair>(P, C, sa, sb, tmem, first, step);
+        multiply<false>(P, C, sa, sb, tmem);
     } else if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyPairRegs));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         const int group = warp >> 2, quarter = warp & 3;
         const uint32_t lanes = tmem + (uint32_t(quarter * 32) << 16) + uint32_t(group * kCols);
         unsigned char* out = outs + warp * kBoxBytes;
         Ring acc{0, 0}, s{0, 0};
-        uint32_t freed = kPairAccs;  // stage of the block that the accumulator now read is for next
+        uint32_t freed = kWideAccs;  // stage of the block that the accumulator now read is for next
         free_first(P, C, lane);
         bool ok = true;
         // scales of a lane's hidden row and of the group's weight rows, fetched four blocks of K ahead
@@ -638,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
         int row0 = 0, v0 = 0;  // of the tile that is fetched for
         const float *ph = nullptr, *pw = nullptr;
         auto place = [&](int t) {
-            wide_tile<kPair>(P, t, row0, v0);
-            row0 += int(rank) * kBM + quarter * 32;
+            tile_at<false>(P, t, row0, v0);
+            row0 += quarter * 32;
             v0 += group * kCols;
             ph = P.hidden_scale + int64_t(row0 + lane) * P.hidden_scale_stride;
             pw = P.weight_scale + int64_t(v0 / kBM) * P.weight_scale_stride;
@@ -692,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
 #pragma unroll
                         for (int k = 0; k < kLoad; k += 2) fma2(sum[(c + k) / 2], now[k], now[k + 1], q[i], q[i]);
                     }
-                    acc.next(kPairAccs);
+                    acc.next(kWideAccs);
                     s.next(uint32_t(P.stages));
                     freed = freed + 1 == uint32_t(P.stages) ? 0 : freed + 1;
                 }
@@ -738,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
         if (P.tma_stores && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if (!ok && lane == 0) C.gave_up = 1;
     }
-    end<kPair>(P, C, tmem);
+    end(P, C, tmem);
 }
 
 // ---------------------------------------------------------------- host side
@@ -788,15 +686,6 @@ bool encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int6
 
 using Kernel = void (*)(const Params);
 
-template <typename T>
-Kernel kernel_for(bool few, bool pair, int NT)
-{
-    return !few       ? pair ? many_rows_kernel<T, true> : many_rows_kernel<T, false>
-           : NT <= 32 ? few_rows_kernel<T, 16>
-           : NT <= 64 ? few_rows_kernel<T, 32>
-                      : few_rows_kernel<T, 64>;
-}
-
 }  // namespace scaled
 
 int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, int64_t ldl, int64_t rows,
@@ -806,19 +695,14 @@ int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, 
     Params p;
     std::memset(&p, 0, sizeof p);
     const bool few = rows <= kFewRows;
-    // rounds over the SMs of either way; a CTA alone loads half as much again for a tile, about 15 % of its time
-    const int64_t wide = (vocab + kWideN - 1) / kWideN;
-    const int64_t rounds_pair = ((rows + 2 * kBM - 1) / (2 * kBM) * wide + sms / 2 - 1) / std::max(sms / 2, 1);
-    const int64_t rounds_alone = ((rows + kBM - 1) / kBM * wide + sms - 1) / sms;
-    const bool pair = !few && sms >= 2 && rounds_alone * 115 >= rounds_pair * 100;
-    p.row_tiles = few ? 1 : int((rows + (pair ? 2 : 1) * kBM - 1) / ((pair ? 2 : 1) * kBM));
+    p.row_tiles = few ? 1 : int((rows + kBM - 1) / kBM);
     p.NT = few ? int((rows + 15) / 16 * 16) : kWideN;
     const int64_t tiles = (vocab + (few ? kBM : kWideN) - 1) / (few ? kBM : kWideN) * p.row_tiles;
     if (tiles > INT32_MAX - 65536) return SAMPLER_ERR_TOO_LARGE;
     p.tiles = int(tiles);
     p.blocks = int((g.hidden_dim + kBK - 1) / kBK);
     const int es = dtype == SAMPLER_DTYPE_BF16 ? 2 : 4;
-    const size_t stage = kABytes + (few ? size_t(p.NT) * kBK : size_t(kPairBBytes));
+    const size_t stage = kABytes + (few ? size_t(p.NT) * kBK : size_t(kWideBytes));
     const size_t own = few ? kScaleBytes : kOutBytes;
     p.stages = int(std::min<size_t>(kMaxStages, (kSmemMax - 1024 - kBarBytes - own) / stage));
     p.accs = std::min({kMaxAccs, kTmemCols / p.NT, p.stages - 1});
@@ -827,7 +711,7 @@ int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, 
     const bool maps = few ? encode(&p.tm, g.weight, vocab, g.hidden_dim, g.weight_stride, kBM) &&
                                 encode(&p.tn, g.hidden, rows, g.hidden_dim, g.hidden_stride, p.NT)
                           : encode(&p.tm, g.hidden, rows, g.hidden_dim, g.hidden_stride, kBM) &&
-                                encode(&p.tn, g.weight, vocab, g.hidden_dim, g.weight_stride, kWideN / 2);
+                                encode(&p.tn, g.weight, vocab, g.hidden_dim, g.weight_stride, kWideN);
     if (!maps) return SAMPLER_ERR_CUDA;
     p.hidden_scale = g.hidden_scale;
     p.weight_scale = g.weight_scale;
@@ -842,18 +726,15 @@ int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, 
     p.rows = int(rows);
     p.V = int(vocab);
     p.timeouts = timeouts;
-    const Kernel kernel = dtype == SAMPLER_DTYPE_BF16 ? kernel_for<uint16_t>(few, pair, p.NT) : kernel_for<float>(few, pair, p.NT);
+    const bool bf16 = dtype == SAMPLER_DTYPE_BF16;
+    const Kernel kernel = few    ? bf16 ? few_rows_kernel<uint16_t> : few_rows_kernel<float>
+                          : bf16 ? many_rows_kernel<uint16_t> : many_rows_kernel<float>;
     const size_t smem = 1024 + size_t(p.stages) * stage + own + kBarBytes;
     if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              int(smem)) != cudaSuccess)
         return SAMPLER_ERR_CUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned(pair ? 2 * std::min(sms / 2, p.tiles) : std::min(sms, p.tiles)));
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim = {2u, 1u, 1u};
-    cfg.attrs = &attr;
-    cfg.numAttrs = pair ? 1 : 0;
+    cfg.gridDim = dim3(unsigned(std::min(sms, p.tiles)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;

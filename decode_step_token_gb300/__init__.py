@@ -112,7 +112,11 @@ def _matrix(name: str, t, dtypes, device: int):
         raise ValueError(f"{name} must be two-dimensional with contiguous rows")
     if t.get_device() != device:
         _on_device(name, t, device)
-    return rows, cols, stride if rows > 1 and stride >= cols else max(stride, cols)
+    if stride < cols:
+        if rows > 1:
+            raise ValueError(f"{name}'s rows overlap: {stride} apart, {cols} wide")
+        stride = cols
+    return rows, cols, stride
 
 
 def _on_device(name: str, t, device: int) -> None:

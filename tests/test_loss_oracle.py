@@ -220,3 +220,19 @@ def test_binding_refuses_what_it_can_see(lib):
         s.quantize_blocks(src=x.half(), out_values=x, out_scales=x)
     with pytest.raises(TypeError, match="hidden"):
         s.lm_head_scaled(hidden=x, hidden_scale=x, weight=x, weight_scale=x, logits=x)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_binding_refuses_rows_that_overlap(dtype):
+    """A row stride below the width (a broadcast row, a sliding window) is no matrix: its rows do not lie where
+    cols * row would put them."""
+    from decode_step_token_gb300 import _matrix
+
+    x = torch.zeros(64, dtype=dtype)
+    for t in (x[:8].expand(5, 8), x.as_strided((5, 8), (3, 1)), x.as_strided((2, 8), (7, 1))):
+        with pytest.raises(ValueError):
+            _matrix("x", t, (dtype,), -1)
+    assert _matrix("x", x[:8].expand(1, 8), (dtype,), -1) == (1, 8, 8)
+    assert _matrix("x", x.as_strided((5, 8), (9, 1)), (dtype,), -1) == (5, 8, 9)
+    assert _matrix("x", x.as_strided((1, 8), (0, 1)), (dtype,), -1) == (1, 8, 8)
+    assert _matrix("x", x.view(8, 8)[:0], (dtype,), -1)[:2] == (0, 8)

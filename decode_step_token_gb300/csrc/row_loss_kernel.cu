@@ -748,10 +748,21 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
                 ok = wait(&S.full[slot1.at], slot1.phase);
                 if (!ok) break;
                 const uint4* in = reinterpret_cast<const uint4*>(ring + slot1.at * kChunkBytes) + tid;
-                if (part.inner(i1)) {
+                // whole chunks at the row's ends, too: 2048 x 50257 bf16 scored in 43 us (47 without), 100001 fp32 126 (137),
+                // 128000 bf16 91 (90); with a gradient that gains nothing
+                if (kGrad ? part.inner(i1) : i1 + kChunkVecs <= part.last) {
                     uint4 v[kVecs];
 #pragma unroll
                     for (int k = 0; k < kVecs; ++k) v[k] = in[k * kConsumers];
+                    if (!kGrad && !part.inner(i1)) {
+                        const int hi = vocab + part.head;
+#pragma unroll
+                        for (int k = 0; k < kVecs; ++k) {
+                            const int ik = i1 + tid + k * kConsumers;
+                            if (ik == 0 || ik == part.count - 1)
+                                Elems<T>::mask(v[k], part.head - ik * kPer, hi - ik * kPer);
+                        }
+                    }
                     fold<T, kEntropy, kVecs>(st, bad, v, c_hi, c_lo, c);
                 } else {
                     const int hi = vocab + part.head;
@@ -871,8 +882,11 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
 constexpr int kSmallVecs = 8;
 constexpr int kSmallBlock = 4;  // rows of one warp that share a block
 
+constexpr int small_threads(int group) { return 32 * (group == 1 ? kSmallBlock : group); }
+constexpr int kSmallResident = 896;  // threads of an SM, with a gradient (1024: registers spill, 4096 x 4000 fp32 30 / 29 us)
+
 template <typename T, bool kGrad, bool kEntropy, int kGroup>
-__global__ void __launch_bounds__(kGroup == 1 ? 32 * kSmallBlock : 32 * kGroup)
+__global__ void __launch_bounds__(small_threads(kGroup), kGrad ? kSmallResident / small_threads(kGroup) : 0)
     small_rows_kernel(const __grid_constant__ LossParams P)
 {
     constexpr int kPer = Elems<T>::kPer, kStep = 32 * kGroup;
@@ -945,6 +959,9 @@ __global__ void __launch_bounds__(kGroup == 1 ? 32 * kSmallBlock : 32 * kGroup)
 #pragma unroll
             for (int k = 0; k < kSmallVecs; ++k) {
                 const int i = tid + k * kStep;
+                // the vector is widened again: pass 1's wide values, kept till here, take half of the registers (16384 x
+                // 8000 bf16 145 us, so 106)
+                asm volatile("" : "+r"(v[k].x), "+r"(v[k].y), "+r"(v[k].z), "+r"(v[k].w));
                 if (i < span.count)
                     put_vector(g, vocab, span.head, i, whole,
                                rec.token < 0 ? make_uint4(0u, 0u, 0u, 0u)
@@ -1119,12 +1136,12 @@ int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t st
     // vectors of a row that starts anywhere
     const int64_t vecs = (p.rows.vocab + 2 * (16 / es - 1)) * es / 16 + 1;
     // rows of up to 16 KB: a group of 1, 2 or 4 warps each (policy with its gradient, against clusters: 4096 x 2000 bf16
-    // 16 / 29 us, 4096 x 4000 fp32 29 / 38, 4096 x 8000 bf16 41 / 43, 16 x 1024 fp32 5.2 / 7.4)
+    // 13.5 / 29 us, 4096 x 4000 fp32 29 / 38, 4096 x 8000 bf16 32 / 43, 16 x 1024 fp32 5.2 / 7.4)
     if (vecs <= 4 * 32 * rows::kSmallVecs) {
         const int group = vecs <= 32 * rows::kSmallVecs ? 1 : vecs <= 64 * rows::kSmallVecs ? 2 : 4;
         const SmallKernel small = es == 2 ? small_kernel<uint16_t>(group, grad, entropy) : small_kernel<float>(group, grad, entropy);
         const int64_t blocks = group == 1 ? (p.rows.n_rows + rows::kSmallBlock - 1) / rows::kSmallBlock : p.rows.n_rows;
-        small<<<unsigned(blocks), group == 1 ? 32 * rows::kSmallBlock : 32 * group, 0, stream>>>(p);
+        small<<<unsigned(blocks), unsigned(rows::small_threads(group)), 0, stream>>>(p);
         return cudaGetLastError() == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
     }
     // parts of at most kPartChunks chunks; smaller ones while few rows leave the device unfilled (policy with its

@@ -878,7 +878,9 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
 // Rows of up to kSmallVecs vectors for each thread of kGroup warps stay in
 // registers from pass 1 to pass 2, and a row is a group's whole work: what such
 // rows cost is latency, and with no roles and no ring many of them are under way
-// on an SM at once.
+// on an SM at once, or few are done with sooner. (Clusters of such blocks, for few
+// longer rows, gained nothing with a gradient, and without one took 12 us against
+// the ring's 7.8 for 32 x 151936 bf16.)
 constexpr int kSmallVecs = 8;
 constexpr int kSmallBlock = 4;  // rows of one warp that share a block
 
@@ -1121,7 +1123,24 @@ SmallKernel small_kernel(int group, bool grad, bool entropy)
 {
     return group == 1   ? small_kernel_for<T, 1>(grad, entropy)
            : group == 2 ? small_kernel_for<T, 2>(grad, entropy)
-                        : small_kernel_for<T, 4>(grad, entropy);
+           : group == 4 ? small_kernel_for<T, 4>(grad, entropy)
+           : group == 8 ? small_kernel_for<T, 8>(grad, entropy)
+                        : small_kernel_for<T, 16>(grad, entropy);
+}
+
+// Warps whose registers a row stays in; 0 for the kernel with a ring. Rows of up to 16 KB (four warps) always do
+// (policy with its gradient, against the ring: 4096 x 2000 bf16 13.5 / 29 us, 4096 x 4000 fp32 29 / 38, 4096 x 8000
+// bf16 32 / 43, 16 x 1024 fp32 5.2 / 7.4). Larger groups are too few on an SM for the way from a row's loads to its
+// stores, so they are taken where rows are few, or without a gradient: eight warps with a gradient 400 x 16000 bf16
+// 10.3 / 12.8 us, 600 x 16000 15.8 / 15.7, 4096 x 16000 61 / 58; without 64 x 8000 fp32 3.1 / 5.3, 4096 x 16000 26 / 34;
+// sixteen with 150 x 32000 bf16 8.6 / 11.4, 300 x 32000 17 / 16; without 64 x 32000 3.8 / 6.0, 600 x 32000 11 / 14,
+// 4096 x 32000 53 / 50.
+int small_group(int64_t vecs, int64_t n_rows, int sms, bool grad)
+{
+    int group = 1;
+    while (group <= 16 && vecs > group * 32 * rows::kSmallVecs) group *= 2;
+    const int64_t most = group <= 4 ? INT64_MAX : group == 8 ? (grad ? 3 * sms : INT64_MAX) : grad ? sms : 4 * sms;
+    return group <= 16 && n_rows <= most ? group : 0;
 }
 
 }  // namespace
@@ -1135,10 +1154,8 @@ int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t st
     const RowsKernel kernel = es == 2 ? rows_kernel_for<uint16_t>(grad, entropy) : rows_kernel_for<float>(grad, entropy);
     // vectors of a row that starts anywhere
     const int64_t vecs = (p.rows.vocab + 2 * (16 / es - 1)) * es / 16 + 1;
-    // rows of up to 16 KB: a group of 1, 2 or 4 warps each (policy with its gradient, against clusters: 4096 x 2000 bf16
-    // 13.5 / 29 us, 4096 x 4000 fp32 29 / 38, 4096 x 8000 bf16 32 / 43, 16 x 1024 fp32 5.2 / 7.4)
-    if (vecs <= 4 * 32 * rows::kSmallVecs) {
-        const int group = vecs <= 32 * rows::kSmallVecs ? 1 : vecs <= 64 * rows::kSmallVecs ? 2 : 4;
+    const int group = small_group(vecs, p.rows.n_rows, sms, grad);
+    if (group) {
         const SmallKernel small = es == 2 ? small_kernel<uint16_t>(group, grad, entropy) : small_kernel<float>(group, grad, entropy);
         const int64_t blocks = group == 1 ? (p.rows.n_rows + rows::kSmallBlock - 1) / rows::kSmallBlock : p.rows.n_rows;
         small<<<unsigned(blocks), unsigned(rows::small_threads(group)), 0, stream>>>(p);

@@ -171,7 +171,11 @@ SHAPES = [
     dict(n=40, V=17001, heat=True, banned=0.5), dict(n=3, V=40961, kind="bf16", pad=7, heat=True),
     dict(n=1, V=128000, kind="bf16"), dict(n=9, V=128000, heat=True, kept=0.8, shift=2),
     dict(n=20, V=151936, kind="bf16", heat=True), dict(n=2, V=262144, heat=True), dict(n=2, V=262144, kind="bf16"),
-    dict(n=700, V=3000, kind="bf16", kept=0.9), dict(n=320, V=20011, kind="bf16", heat=True, kept=0.9, pad=5),
+    dict(n=700, V=3000, kind="bf16", kept=0.9), dict(n=320, V=20011, kind="bf16", heat=True, kept=0.9, pad=5),    # few rows in the registers of a block of 8 and 16 warps, and few longer ones
+    dict(n=5, V=9001, kind="bf16", pad=3, shift=1), dict(n=150, V=32000, kind="bf16", kept=0.8, heat=True),
+    dict(n=60, V=16001, kept=0.5, banned=0.3), dict(n=13, V=151936, kind="bf16", pad=3, shift=1, kept=0.7, heat=True),
+    dict(n=7, V=100003, banned=0.5, pad=1, grad_pad=2), dict(n=50, V=40961, kind="bf16", heat=True),
+    dict(n=14, V=65537, kind="bf16", grad_shift=3, kept=0.6),
 ]
 # several rows for each cluster, at every way of cutting a row: one CTA a row and more, parts of which two fit in
 # the ring and parts of which one does, rows in registers

@@ -26,7 +26,7 @@
 // in one block's MMAs, and wider tiles load less from L2. Pairs of CTAs that share
 // their weight tile by multicast load a third less, but wait for each other: 1.49
 // against 1.46 ms at 4096 x 128000 x 4096, and one tile of 256 rows where CTAs
-// alone have two (333 x 20011 x 1000: 41 against 30 us).
+// alone have two (333 x 20011 x 1000: 41 against 30 us, with the stores as they were).
 //
 // Where the two meet (x 4096 where nothing is said, transposed / not): 16 x 128000
 // 86 / 107 us, 32 x 64000 53 / 49, 32 x 40000 x 1024 15 / 16, 33 x 128000 92 / 94,
@@ -621,14 +621,17 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
                     }
                 } else {
                     __syncwarp();
+                    // eight rows' elements under way at once (one: 333 x 20011 x 1000 fp32 26.1 us, so 18.7)
                     const int rows = min(32, P.rows - row), cols = min(kBoxCols, P.V - v - c0);
                     T* g = static_cast<T*>(P.logits) + int64_t(row) * P.ldl + v + c0;
-#pragma unroll 1
-                    for (int k = 0; k < rows; ++k)
-#pragma unroll 1
-                        for (int c = lane; c < cols; c += 32)
-                            g[int64_t(k) * P.ldl + c] =
-                                *reinterpret_cast<const T*>(out + k * 128 + (c * int(sizeof(T)) ^ (k & 7) * 16));
+#pragma unroll 8
+                    for (int k = 0; k < 32; ++k) {
+#pragma unroll
+                        for (int c = lane; c < kBoxCols; c += 32)
+                            if (k < rows && c < cols)
+                                g[c] = *reinterpret_cast<const T*>(out + k * 128 + (c * int(sizeof(T)) ^ (k & 7) * 16));
+                        g += P.ldl;
+                    }
                     __syncwarp();
                 }
             }

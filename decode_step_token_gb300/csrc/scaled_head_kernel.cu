@@ -621,7 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
                     }
                 } else {
                     __syncwarp();
-                    // eight rows' elements under way at once (one: 333 x 20011 x 1000 fp32 26.1 us, so 18.7)
+                    // eight rows' elements under way at once (one: 333 x 20011 x 1000 fp32 26.1 us, so 18.7;
+                    // two bf16 columns a lane on their 4-byte boundaries: 28 us where this takes 16.6, for the branches)
                     const int rows = min(32, P.rows - row), cols = min(kBoxCols, P.V - v - c0);
                     T* g = static_cast<T*>(P.logits) + int64_t(row) * P.ldl + v + c0;
 #pragma unroll 8

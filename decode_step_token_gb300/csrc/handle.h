@@ -15,7 +15,8 @@ struct sampler_s {
     int num_sms;
     int64_t max_rows, max_vocab, max_history;
     uint32_t flags;
-    uint32_t max_polls;
+    uint32_t max_polls;  // of a wait on a staging copy
+    uint64_t wait_ns;    // of a wait inside the kernels of scoring and the losses
     // slice kernel: per-(row, slice) records and per-row arrival counters
     dst::SliceWorkspace slice_ws;
     int slice_rows;

@@ -105,6 +105,8 @@ int group_prepare(int dtype, bool pen, size_t smem);
 int group_launch(const sampler_args_t* a, const GroupGeometry& g, int clusters, uint32_t* work, cudaStream_t stream);
 
 // ---------------------------------------------------------------- scoring and losses
+constexpr uint64_t kWaitNs = 2000000000ull;  // a wait inside a kernel gives up after 2 s
+
 // One row's record: its share of the logits' gradient, with u = (x_v - ref) * c
 // d loss / d x_v = 2^u * (k0 + k1 * u) + (v == token ? at_token : 0).
 struct RowRecord {
@@ -133,6 +135,7 @@ struct LossParams {
     const float* grad_entropy;
     sampler_policy_t policy;    // kModePolicy
     RowWorkspace ws;
+    uint64_t wait_ns;           // kWaitNs, or 0: every wait gives up
 };
 
 // Clusters that the device holds at once, by the logits' type, gradient, entropy

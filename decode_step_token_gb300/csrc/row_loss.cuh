@@ -314,27 +314,35 @@ __device__ __forceinline__ void row_write(const LossParams& P, int64_t r, const 
     }
 }
 
-constexpr uint32_t kGaveUp = 0x80000000u;  // in the ticket: a wait of this launch gave up
+// What is written of a row whose cluster gave up (see abandon): nothing of it is
+// known, so its outputs, its share of the loss and all of its gradient are NaN.
+// A row that is left out has its zeros as ever.
+__device__ __forceinline__ void row_give_up(const LossParams& P, int64_t r, bool counts)
+{
+    const float x = counts ? quiet_nan() : 0.f;
+    const RowRecord rec{0.f, 0.f, x, 0.f, x, counts ? kNoToken : -1, x, 0.f};
+    const RowOut out{Pair{x, 0.f}, x, x, x, double(x), counts ? SAMPLER_ROW_TIMEOUT : SAMPLER_ROW_OK};
+    row_write(P, r, rec, out);
+}
 
-// Not 0 in the last of `blocks` blocks to get here (with kGaveUp as the ticket
-// has it); what the others wrote before is then visible. Clears the ticket for
-// the next launch. Called by every thread of a block; `flag` is a word of its
-// shared memory.
-__device__ __forceinline__ uint32_t last_block(uint32_t* ticket, uint32_t blocks, uint32_t* flag)
+// True in the last of `blocks` blocks to get here; what the others wrote before
+// is then visible. Clears the ticket for the next launch. Called by every thread
+// of a block; `flag` is a word of its shared memory.
+__device__ __forceinline__ bool last_block(uint32_t* ticket, uint32_t blocks, uint32_t* flag)
 {
     __syncthreads();
     if (threadIdx.x == 0) {
         __threadfence();
         const uint32_t got = atomicAdd(ticket, 1u);
         *flag = 0u;
-        if ((got & ~kGaveUp) + 1u == blocks) {
-            *flag = 1u | (got & kGaveUp);
+        if (got + 1u == blocks) {
+            *flag = 1u;
             *ticket = 0u;
             __threadfence();
         }
     }
     __syncthreads();
-    return *flag;
+    return *flag != 0u;
 }
 
 // Sum of terms[0 .. n) in double by one block of kThreads threads, in an order

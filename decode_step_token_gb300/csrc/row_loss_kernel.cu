@@ -51,7 +51,7 @@ constexpr int kBatch = 8;                        // rows whose parameters are fe
 constexpr int kFirstBatch = 2;                   // the first time, when all wait for them
 constexpr int kSums = 4;                         // rows whose sums are in shared memory
 constexpr int kSmemMax = 113 * 1024;             // of a CTA: two on an SM
-constexpr uint64_t kWaitNs = 2000000000ull;      // a wait gives up after 2 s
+constexpr uint64_t kSettleNs = 100000;           // in which what is on its way to shared memory lands
 
 // The ring (slots * kChunkBytes), the sums [kSums][parts * kWarps] and this.
 struct Shared {
@@ -61,7 +61,7 @@ struct Shared {
     RowJob jobs[2][kBatch];
     RowRecord rec[kSums];
     double scratch[kThreads / 32];
-    uint32_t flag, failed;  // failed: a wait of this CTA gave up
+    uint32_t flag, failed;  // failed: a wait of this cluster gave up
 };
 
 constexpr int smem_of(int slots, int parts)
@@ -103,11 +103,11 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
-// A whole warp waits for the phase of `bar` with the given parity, for kWaitNs at
+// A whole warp waits for the phase of `bar` with the given parity, for `ns` at
 // most; all of its lanes get the same answer.
-__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity)
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint64_t ns)
 {
-    const uint64_t until = now_ns() + kWaitNs;
+    const uint64_t until = now_ns() + ns;
     for (uint32_t i = 0; i < (1u << 30); ++i) {
         if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
         if ((i & 63u) == 63u && __any_sync(0xffffffffu, now_ns() > until)) return false;
@@ -115,9 +115,9 @@ __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity)
     return false;
 }
 
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity)
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint64_t ns)
 {
-    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_slow(bar, parity);
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_slow(bar, parity, ns);
 }
 
 // True in one lane of a warp whose lanes are together.
@@ -148,14 +148,12 @@ __device__ __forceinline__ void put_sums(uint32_t addr, uint32_t bar, float a, f
 __device__ __forceinline__ void dependent_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dependent_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// A wait for row r (-1: for no row yet) gave up: the row says so, and the loss
-// becomes NaN.
-__device__ __noinline__ void gave_up(Shared& S, const LossParams& P, int64_t r)
+// A wait of this warp gave up: every CTA of the cluster is told, and abandons the
+// cluster's rows once all have come to their end.
+__device__ __noinline__ void gave_up(Shared& S)
 {
-    if ((threadIdx.x & 31) != 0) return;
-    S.failed = 1;
-    if (r >= 0 && P.rows.out_status) P.rows.out_status[r] = SAMPLER_ROW_TIMEOUT;
-    if (P.mode == kModePolicy) atomicOr(P.ws.ticket, kGaveUp);
+    const uint32_t cta = threadIdx.x & 31;
+    if (cta < cluster_nctarank()) dsmem_st_u32(dsmem_map(smem_addr(&S.failed), cta), 1u);
 }
 
 // ---------------------------------------------------------------- vectors
@@ -481,6 +479,34 @@ __device__ __forceinline__ int64_t dealer_next(RowDealer& d, const sampler_rows_
     return d.base + bit;
 }
 
+// A wait of this cluster gave up. Which of its rows were done with is not known,
+// so all of them are written again, by all CTAs after the last of them has come to
+// its end: those that count as TIMEOUT with NaN, the others as ever. Otherwise a
+// loss, or the pairs' kernel after this one, would go on with what an earlier call
+// has left in the workspace.
+template <typename T, bool kGrad>
+__device__ __noinline__ void abandon(const LossParams& P, uint32_t q, uint32_t n_clusters, uint32_t parts, uint32_t rank)
+{
+    // copies, and sums put into this CTA, that nobody has waited for land before it may exit
+    const uint64_t until = now_ns() + kSettleNs;
+    for (uint32_t i = 0; i < (1u << 20) && now_ns() < until; ++i) {
+    }
+    const sampler_rows_t& a = P.rows;
+    RowDealer d;
+    dealer_open(d, a, q);
+    for (;;) {
+        bool counts;
+        const int64_t r = dealer_next(d, a, q, n_clusters, counts);
+        if (r < 0) return;
+        if (rank == 0 && threadIdx.x == 0) row_give_up(P, r, counts);
+        if (kGrad) {
+            T* g = static_cast<T*>(a.out_grad) + r * a.grad_stride;
+            for (int64_t v = rank * kThreads + threadIdx.x; v < a.vocab; v += parts * kThreads)
+                store_grad(g + v, counts ? quiet_nan() : 0.f);
+        }
+    }
+}
+
 // What a row needs besides its logits and its weight, one row in each lane.
 __device__ __forceinline__ void job_load(RowJob& j, float& temperature, const LossParams& P, int64_t r)
 {
@@ -566,13 +592,13 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
         dealer_open(d, a, q);
         Place slot{0, 0}, batch{0, 0};
         uint32_t issued = 0;
-        bool ok = true, end = false;
+        bool ok = P.wait_ns != 0, end = false;  // 0: nothing begins, and every other wait of the cluster gives up
         auto copy_in = [&](int64_t row) {
             const RowPart part = row_part<T>(a, row, rank, plan);
             const unsigned char* from = reinterpret_cast<const unsigned char*>(static_cast<const T*>(a.logits) +
                                                                                row * a.row_stride - part.head);
             for (int v = part.first; ok && v < part.last; v += kChunkVecs) {
-                ok = wait(&S.empty[slot.at], slot.phase ^ 1u);
+                ok = wait(&S.empty[slot.at], slot.phase ^ 1u, P.wait_ns);
                 if (!ok) break;
                 const uint32_t bytes = uint32_t(min(kChunkVecs, part.last - v)) * 16u;
                 if (elect_one()) {
@@ -602,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
             return count;
         };
         auto publish = [&](RowJob& job, float temperature, int count, int64_t mine, uint32_t live) {
-            ok = ok && wait(&S.job_empty[batch.at], batch.phase ^ 1u);
+            ok = ok && wait(&S.job_empty[batch.at], batch.phase ^ 1u, P.wait_ns);
             if (!ok) return;
             if (lane < count) {
                 job.row = int32_t(mine);
@@ -649,17 +675,18 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
             count = count_next;
         }
         if (!ok) {
-            gave_up(S, P, -1);
+            gave_up(S);
             // copies in flight land before the CTA may exit
-            for (uint32_t j = issued > slots ? issued - slots : 0; j < issued; ++j) wait(&S.full[j % slots], j / slots & 1u);
+            for (uint32_t j = issued > slots ? issued - slots : 0; j < issued; ++j)
+                wait(&S.full[j % slots], j / slots & 1u, kWaitNs);
         }
     } else if (warp == kCloser) {
         const float grad_scale =
             kGrad && P.mode == kModePolicy ? scale_of_grad(P.policy.grad_scale, P.policy.grad_scale_dev) : 1.f;
         Place batch{0, 0}, sp{0, 0};
         for (int k = 0;; ++k) {
-            if (k == 0 && !wait(&S.job_full[batch.at], batch.phase)) {
-                gave_up(S, P, -1);
+            if (k == 0 && !wait(&S.job_full[batch.at], batch.phase, P.wait_ns)) {
+                gave_up(S);
                 break;
             }
             const RowJob job = S.jobs[batch.at][k];
@@ -668,8 +695,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
             if (job.live) {
                 if (lane == 0) mbar_arrive_expect_tx(&S.join[sp.at], kWarps * parts * 16u);
                 __syncwarp();
-                if (!wait(&S.join[sp.at], sp.phase)) {
-                    gave_up(S, P, job.row);
+                if (!wait(&S.join[sp.at], sp.phase, P.wait_ns)) {
+                    gave_up(S);
                     break;
                 }
                 const float4* in = sums + sp.at * parts * kWarps;
@@ -716,8 +743,8 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
                 batch.next(2);
                 at = 0;
             }
-            if (at == 0 && !wait(&S.job_full[batch.at], batch.phase)) {
-                gave_up(S, P, -1);
+            if (at == 0 && !wait(&S.job_full[batch.at], batch.phase, P.wait_ns)) {
+                gave_up(S);
                 ok = false;
                 return nullptr;
             }
@@ -745,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
             const Two c_hi = two(job->c_hi, job->c_hi), c_lo = two(job->c_lo, job->c_lo);
             const float c = job->c;
             for (; i1 < part.last && most > 0; i1 += kChunkVecs, --most) {
-                ok = wait(&S.full[slot1.at], slot1.phase);
+                ok = wait(&S.full[slot1.at], slot1.phase, P.wait_ns);
                 if (!ok) break;
                 const uint4* in = reinterpret_cast<const uint4*>(ring + slot1.at * kChunkBytes) + tid;
                 // whole chunks at the row's ends, too: 2048 x 50257 bf16 scored in 43 us (47 without), 100001 fp32 126 (137),
@@ -790,7 +817,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
             // has waited for it.)
             if (!kGrad) {
                 if (behind == 2) {
-                    ok = wait(&S.closed[cp.at], cp.phase);
+                    ok = wait(&S.closed[cp.at], cp.phase, P.wait_ns);
                     if (!ok) return;
                     cp.next(kSums);
                 } else {
@@ -805,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
         auto pass2 = [&](const RowJob* job) {
             const RowPart part = job->part;
             T* g = static_cast<T*>(part.grad);
-            ok = wait(&S.closed[cp.at], cp.phase);
+            ok = wait(&S.closed[cp.at], cp.phase, P.wait_ns);
             if (!ok) return;
             const RowRecord rec = S.rec[cp.at];
             cp.next(kSums);
@@ -846,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
                         pass1(next, int(slots) - (job->part.last - job->part.first + kChunkVecs - 1) / kChunkVecs);
                     if (ok) pass2(job);
                 }
-                if (!ok) gave_up(S, P, job->row);
+                if (!ok) gave_up(S);
             } else if (kGrad) {
                 const RowPart part = job->part;
                 for (int i = part.first + tid; i < part.last; i += kConsumers)
@@ -865,12 +892,11 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
     // no CTA leaves while another may still write to its shared memory
     __syncwarp();
     cluster_sync();
-    if (P.mode == kModePolicy && rank == 0) {  // the first CTAs have written the rows' shares
-        const uint32_t end = last_block(P.ws.ticket, n_clusters, &S.flag);
-        if (end) {
-            const double loss = sum_terms<kThreads>(P.ws.terms, a.n_rows, S.scratch);
-            if (tid == 0) *P.policy.out_loss = end & kGaveUp ? quiet_nan() : float(loss);
-        }
+    if (S.failed) abandon<T, kGrad>(P, q, n_clusters, parts, rank);
+    if (P.mode == kModePolicy && rank == 0 &&  // the first CTAs have written the rows' shares
+        last_block(P.ws.ticket, n_clusters, &S.flag)) {
+        const double loss = sum_terms<kThreads>(P.ws.terms, a.n_rows, S.scratch);
+        if (tid == 0) *P.policy.out_loss = float(loss);
     }
 }
 
@@ -971,12 +997,9 @@ __global__ void __launch_bounds__(small_threads(kGroup), kGrad ? kSmallResident 
             }
         }
     }
-    if (P.mode == kModePolicy) {
-        const uint32_t end = last_block(P.ws.ticket, gridDim.x, &flag);
-        if (end) {
-            const double loss = sum_terms<kGroup == 1 ? 32 * kSmallBlock : kStep>(P.ws.terms, a.n_rows, scratch);
-            if (threadIdx.x == 0) *P.policy.out_loss = end & kGaveUp ? quiet_nan() : float(loss);
-        }
+    if (P.mode == kModePolicy && last_block(P.ws.ticket, gridDim.x, &flag)) {
+        const double loss = sum_terms<kGroup == 1 ? 32 * kSmallBlock : kStep>(P.ws.terms, a.n_rows, scratch);
+        if (threadIdx.x == 0) *P.policy.out_loss = float(loss);
     }
 }
 
@@ -1052,7 +1075,7 @@ __global__ void __launch_bounds__(kPairThreads) pairs_kernel(const sampler_rows_
             ws.records[r] = rec;
         }
     }
-    if (last_block(ws.ticket, gridDim.x, &flag) != 0u) {
+    if (last_block(ws.ticket, gridDim.x, &flag)) {
         const double loss = sum_terms<kPairThreads>(ws.pair_terms, q.n_pairs, scratch);
         if (threadIdx.x == 0) *q.out_loss = float(loss / double(q.n_pairs));
     }

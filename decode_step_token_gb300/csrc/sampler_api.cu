@@ -248,6 +248,7 @@ int sampler_create(sampler_t* out, const sampler_config_t* cfg)
     h->max_history = cfg->max_history;
     h->flags = cfg->flags;
     h->max_polls = (cfg->flags & SAMPLER_CREATE_SHORT_WAITS) ? 0u : kMaxPolls;
+    h->wait_ns = (cfg->flags & SAMPLER_CREATE_SHORT_WAITS) ? 0u : dst::kWaitNs;
     cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, cfg->device);
     h->slice_rows = int(std::min<int64_t>(cfg->max_rows, dst::kSliceMaxRows));
     {

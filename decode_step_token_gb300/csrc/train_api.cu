@@ -84,6 +84,7 @@ int sampler_score(sampler_t h, const sampler_rows_t* rows, sampler_stream_t stre
     p.rows = *rows;
     p.mode = dst::kModeScore;
     p.ws = h->row_ws;
+    p.wait_ns = h->wait_ns;
     return dst::rows_launch(p, h->num_sms, &h->row_occ, cuda_stream(stream));
 }
 
@@ -104,6 +105,7 @@ int sampler_score_grad(sampler_t h, const sampler_rows_t* rows, const float* gra
     p.grad_logprob = grad_logprob;
     p.grad_entropy = grad_entropy;
     p.ws = h->row_ws;
+    p.wait_ns = h->wait_ns;
     return dst::rows_launch(p, h->num_sms, &h->row_occ, cuda_stream(stream));
 }
 
@@ -130,6 +132,7 @@ int sampler_policy_loss(sampler_t h, const sampler_rows_t* rows, const sampler_p
     p.mode = dst::kModePolicy;
     p.policy = *q;
     p.ws = h->row_ws;
+    p.wait_ns = h->wait_ns;
     return dst::rows_launch(p, h->num_sms, &h->row_occ, cuda_stream(stream));
 }
 
@@ -158,6 +161,7 @@ int sampler_preference_loss(sampler_t h, const sampler_rows_t* rows, const sampl
         p.rows = *rows;
         p.mode = dst::kModePairs;
         p.ws = h->row_ws;
+        p.wait_ns = h->wait_ns;
         rc = dst::rows_launch(p, h->num_sms, &h->row_occ, s);
         if (rc != SAMPLER_OK) return rc;
     }

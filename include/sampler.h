@@ -123,7 +123,9 @@ typedef struct {
  * up at once, so each row it samples reports SAMPLER_ROW_TIMEOUT (token -1).
  * The kernel still lets each copy land before it reuses or releases the
  * buffer, so nothing faults and nothing hangs; later calls are unaffected
- * (no state survives a call). Lets a test observe the timeout status. */
+ * (no state survives a call). Scoring and the losses give up likewise where
+ * their rows take a kernel with waits (rows above 16 KB may). Lets a test
+ * observe the timeout status. */
 #define SAMPLER_CREATE_SHORT_WAITS 4u
 
 /*
@@ -367,10 +369,11 @@ int sampler_lm_head(sampler_t h, const sampler_lm_head_t* lm, void* logits, int6
  * anything), its outputs and its gradient are zeros, its status is
  * SAMPLER_ROW_OK. The statuses of the other rows, in the order reported:
  * SAMPLER_ROW_BAD_PARAM (T < 0, NaN or inf; a token outside [0, vocab)),
- * SAMPLER_ROW_NONFINITE (a NaN or +inf logit), SAMPLER_ROW_ALL_NEG_INF. The
- * outputs and the gradient of such a row are NaN, and so are a loss that it
- * belongs to and the gradients of its pair's rows; other rows keep theirs. A
- * -inf logit is a token of no mass: its gradient is 0, and the logprob of a
+ * SAMPLER_ROW_NONFINITE (a NaN or +inf logit), SAMPLER_ROW_ALL_NEG_INF; and in
+ * their place SAMPLER_ROW_TIMEOUT for all rows of a part of the batch in which
+ * an internal wait gave up. The outputs and the gradient of a row with one of
+ * these are NaN, and so are a loss that it belongs to and the gradients of its
+ * pair's rows; other rows keep theirs. A -inf logit is a token of no mass: its gradient is 0, and the logprob of a
  * token t with one is -inf.
  *
  * The gradient of the logits, where asked, has the logits' type, each value

@@ -567,3 +567,57 @@ def test_agrees_with_the_sampler(sampler):
     sampler.score(logits=x, tokens=tok, temperature=T, out_logprob=ours)
     # the sampler's logprobs are within 1e-6 + 1e-5 |lp| of the exact ones, ours within about 1e-5
     assert ((said - ours).abs() <= 2e-5 + 1e-5 * ours.abs()).all()
+
+
+@pytest.mark.parametrize("kind,n,V", [("f32", 300, 40961), ("bf16", 40, 151936)])
+def test_waits_that_give_up(sampler, kind, n, V):
+    """On a handle whose waits give up at once, every row that counts says so and nothing looks like a result:
+    outputs, rewards, losses and gradients are NaN, also where an earlier call has left sums in the workspace."""
+    import torch
+    import decode_step_token_gb300 as d
+
+    old, ends = torch.zeros(n, device="cuda:0"), torch.tensor([0, n // 3, n - 1], dtype=torch.int32, device="cuda:0")
+    reward = torch.full((2,), -7.0, device="cuda:0")
+    ones = torch.ones(n, device="cuda:0")
+
+    def calls(s, c):
+        yield "score", lambda: s.score(out_entropy=c.out["entropy"], **c.kw())
+        yield "grad", lambda: s.score_grad(grad_logprob=ones, grad_entropy=ones, out_grad=c.grad, **c.kw())
+        yield "policy", lambda: s.policy_loss(old_logprob=old, advantage=ones, ref_logprob=old, kl_coef=0.1,
+                                              out_kl=c.out["kl"], out_ratio=c.out["ratio"], out_loss=c.loss,
+                                              out_grad=c.grad, **c.kw())
+        yield "forward", lambda: s.policy_loss(old_logprob=old, advantage=ones, out_loss=c.loss, **c.kw())
+        yield "pairs", lambda: s.preference_loss(seq_offsets=ends, out_loss=c.loss, out_reward=reward, out_grad=c.grad,
+                                                 **c.kw())
+        yield "pairs forward", lambda: s.preference_loss(seq_offsets=ends, out_loss=c.loss, out_reward=reward, **c.kw())
+
+    with d.Sampler(max_rows=n, max_vocab=V, short_waits=True) as short:
+        # rows that stay in registers have no waits: this call leaves its sums and records behind
+        few = Rows(13, n, 900, kind)
+        short.preference_loss(seq_offsets=ends, out_loss=few.loss, out_reward=reward, out_grad=few.grad, **few.kw())
+        assert torch.isfinite(few.loss).all() and torch.isfinite(few.grad).all() and (few.status == 0).all()
+        c = Rows(14, n, V, kind, pad=1, kept=0.8)
+        live = torch.from_numpy(c.live()).cuda()
+        for name, call in calls(short, c):
+            for t in (c.loss, c.gflat, *c.out.values(), reward):
+                t.fill_(-7.0)
+            c.status.fill_(-7)
+            call()
+            assert torch.equal(c.status, torch.where(live, 5, 0).int()), name
+            for k, t in c.out.items():
+                if not bool((t == -7).all()):  # not asked of this call
+                    assert torch.isnan(t[live]).all() and (t[~live] == 0).all(), (name, k)
+            assert torch.isnan(c.out["logprob"][live]).all(), name
+            if name != "score" and name != "grad":
+                assert torch.isnan(c.loss).all(), name
+            if name.startswith("pairs"):
+                assert torch.isnan(reward).all(), name
+            if name in ("grad", "policy", "pairs"):
+                assert torch.isnan(c.grad[live]).all() and (c.grad[~live] == 0).all(), name
+                c.grad.fill_(-7.0)
+            assert (c.gflat == -7).all(), name
+    # another handle is not affected
+    for name, call in calls(sampler, c):
+        call()
+        assert (c.status == 0).all() and torch.isfinite(c.out["logprob"]).all(), name
+        assert name in ("score", "grad") or torch.isfinite(c.loss).all(), name

@@ -112,7 +112,11 @@ constexpr uint64_t kWaitNs = 2000000000ull;  // a wait inside a kernel gives up 
 struct RowRecord {
     float c;         // log2(e) / T
     float ref;       // the row's largest logit
-    float k0, k1;
+    float k0;
+    union {
+        float k1;
+        uint32_t answers;  // pairs (whose k1 is 0): the answers that the row lies in
+    };
     float at_token;
     int32_t token;   // -1: the row is written as zeros (left out)
     float inv_s, inv_t;  // 1 / the row's sum of exponentials; 1 / T

@@ -1010,6 +1010,10 @@ constexpr int kPairThreads = 256;
 // pair's share of the loss, and the gradient's factors of the rows. The sums are
 // in double (a reward is a small difference of long sums); what follows from the
 // margin is in fp32, in forms that lose nothing where a sigmoid is near 0 or 1.
+// The host cannot look at the offsets, and where they decrease a row may lie in
+// several answers: each counts itself in the row's record, the first to come
+// there alone writes the factors, and a row with a count above one gets NaN in
+// the next kernel, whichever came first.
 __global__ void __launch_bounds__(kPairThreads) pairs_kernel(const sampler_rows_t a, const sampler_preference_t q,
                                                              const RowWorkspace ws)
 {
@@ -1069,10 +1073,13 @@ __global__ void __launch_bounds__(kPairThreads) pairs_kernel(const sampler_rows_
             float(double(k ? -by_z : by_z) * (double(q.beta) * share / double(q.n_pairs))) *
             scale_of_grad(q.grad_scale, q.grad_scale_dev);
         for (int64_t r = begin + t; r < end; r += kHalf) {
-            RowRecord rec = ws.records[r];
-            if (rec.token < 0) continue;
+            RowRecord& to = ws.records[r];
+            const uint32_t before = atomicAdd(&to.answers, 1u);
+            RowRecord rec = to;
+            if (rec.token < 0 || before != 0u) continue;
             set_factors(rec, (a.weight ? a.weight[r] : 1.f) * by_sum, 0.f, 0.f, 0.f);
-            ws.records[r] = rec;
+            to.k0 = rec.k0;
+            to.at_token = rec.at_token;
         }
     }
     if (last_block(ws.ticket, gridDim.x, &flag)) {
@@ -1091,7 +1098,8 @@ __global__ void __launch_bounds__(kGradThreads) pairs_grad_kernel(const sampler_
 {
     const int64_t r = a.n_rows - 1 - int64_t(blockIdx.y);
     dependent_wait();
-    const RowRecord rec = ws.records[r];
+    RowRecord rec = ws.records[r];
+    if (rec.answers > 1u) rec.k0 = rec.at_token = quiet_nan();
     const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
     T* g = static_cast<T*>(a.out_grad) + r * a.grad_stride;
     const RowSpan span = row_span(x, a.vocab);

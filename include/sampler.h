@@ -456,7 +456,8 @@ int sampler_policy_loss(sampler_t h, const sampler_rows_t* rows, const sampler_p
  * ref_logprob is a loss without a reference model. Rows in no answer get a
  * gradient of zeros. An answer whose offsets do not lie in 0 <= begin <= end
  * <= n_rows has no rows and a NaN reward; the loss and the gradient of its
- * pair's other answer are then NaN. n_pairs is at most the handle's max_rows.
+ * pair's other answer are then NaN. (Offsets that decrease have such an answer.
+ * Rows that they put into more than one answer get a NaN gradient.) n_pairs is at most the handle's max_rows.
  */
 typedef struct {
     const int32_t* seq_offsets; /* [2 * n_pairs + 1] */

@@ -133,6 +133,10 @@ def preference(logits, tokens, offsets, ref=None, temperature=None, weight=None,
         for k in range(2):
             b, e = spans[2 * i + k]
             by_lp[b:e] = (by_z if k == 0 else -by_z) * beta * share[2 * i + k] / pairs * w[b:e] * grad_scale
+    inside = np.zeros(n, int)
+    for b, e in spans:
+        inside[b:e] += 1
+    by_lp[inside > 1] = np.nan  # in more than one answer
     got["by_logprob"] = by_lp
     got["reward"], got["loss"] = reward, loss / pairs if pairs else 0.0
     got["grad"] = logits_grad(got, tokens, by_lp, None, temperature, weight)

@@ -621,3 +621,45 @@ def test_waits_that_give_up(sampler, kind, n, V):
         call()
         assert (c.status == 0).all() and torch.isfinite(c.out["logprob"]).all(), name
         assert name in ("score", "grad") or torch.isfinite(c.loss).all(), name
+
+
+@pytest.mark.parametrize("bad", [[0, 3, 9, 5, 10], [0, 6, 9, 0, 4, 5, 7], [4, 10, 4, 10, 4, 10, 4, 10, 4], [9, 3, 0],
+                                 [0, 8, 2, 6, 10], [0, 3, 5, 8, 11], [2, 5, -4, 7, 9]])
+@pytest.mark.parametrize("kind,V,scale", [("f32", 301, 1), ("bf16", 301, 60)])
+def test_answers_that_overlap(sampler, bad, kind, V, scale):
+    """Offsets that decrease or leave the rows: defined rewards and gradients, the same bits each time, and nothing
+    written beside the gradient. Offsets `scale` times as long have each answer's rows in several threads."""
+    import torch
+
+    c = Rows(15, 10 * scale, V, kind, kept=0.9, pad=3)
+    offsets = np.array(bad, np.int32) * scale
+    pairs = len(bad) // 2
+    reward = torch.full((2 * pairs,), -7.0, device="cuda:0")
+    call = lambda: sampler.preference_loss(  # noqa: E731
+        seq_offsets=torch.from_numpy(offsets).cuda(), out_loss=c.loss, out_reward=reward, out_grad=c.grad, **c.kw())
+    call()
+    got = L.preference(c.x, c.tokens, offsets, None, c.T, c.weight)
+    tol = c.check_rows(got, entropy=False)
+    assert torch.isnan(c.loss).item()
+    np.testing.assert_array_equal(np.isnan(reward.cpu().numpy()), np.isnan(got["reward"]))
+    # as in test_preference_loss: the sigmoid has a slope of at most 1/4, in the margin's error
+    w = c.weight.astype(np.float64)
+    t_by = np.zeros(c.n)
+    for i in range(pairs):
+        if np.isnan(got["reward"][2 * i:2 * i + 2]).any():
+            continue
+        t_z = 0.0
+        for s in (2 * i, 2 * i + 1):
+            at = slice(offsets[s], offsets[s + 1])
+            t_z += 0.1 * ((w * tol["logprob"])[at]).sum() + 3 * EPS * (abs(got["reward"][s]) + 1)
+        for s in (2 * i, 2 * i + 1):
+            at = slice(offsets[s], offsets[s + 1])
+            t_by[at] = w[at] * 0.1 / pairs * (t_z / 4 + EPS)
+    c.check_grad(got, tol, got["by_logprob"], t_by + 8 * EPS * np.abs(got["by_logprob"]))
+    first = c.grad.clone(), reward.clone()
+    for _ in range(20):
+        c.grad.fill_(-7.0)
+        call()
+        for a, b in zip(first, (c.grad, reward)):
+            assert torch.equal(a.view(torch.int16 if a.dtype == torch.bfloat16 else torch.int32),
+                               b.view(torch.int16 if b.dtype == torch.bfloat16 else torch.int32))

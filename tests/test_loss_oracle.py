@@ -236,3 +236,18 @@ def test_binding_refuses_rows_that_overlap(dtype):
     assert _matrix("x", x.as_strided((5, 8), (9, 1)), (dtype,), -1) == (5, 8, 9)
     assert _matrix("x", x.as_strided((1, 8), (0, 1)), (dtype,), -1) == (1, 8, 8)
     assert _matrix("x", x.view(8, 8)[:0], (dtype,), -1)[:2] == (0, 8)
+
+
+def test_preference_rows_in_several_answers():
+    """Offsets that decrease: the answer with its end before its begin and its pair are NaN, and so is the gradient of
+    rows in more than one answer; the other rows keep theirs."""
+    rng = np.random.default_rng(8)
+    x, tok = rng.standard_normal((10, 30)), rng.integers(0, 30, 10)
+    got = L.preference(x, tok, [0, 6, 9, 0, 4, 5, 7])
+    # answers [0, 6) [6, 9) | [9, 0) [0, 4) | [4, 5) [5, 7)
+    assert np.isnan(got["reward"]).tolist() == [False, False, True, False, False, False] and np.isnan(got["loss"])
+    nan = np.isnan(got["grad"]).all(1)
+    assert nan.tolist() == [True] * 7 + [False] * 3 and np.isfinite(got["grad"][~nan]).all()
+    alone = L.preference(x, tok, [0, 6, 9])
+    np.testing.assert_allclose(got["grad"][7:9], alone["grad"][7:9] / 3, rtol=1e-14)
+    assert (got["grad"][9] == 0).all()

@@ -16,7 +16,7 @@ struct sampler_s {
     int64_t max_rows, max_vocab, max_history;
     uint32_t flags;
     uint32_t max_polls;  // of a wait on a staging copy
-    uint64_t wait_ns;    // of a wait inside the kernels of scoring and the losses
+    uint64_t wait_ns;    // of a wait inside the kernels of scoring, the losses and the 8-bit LM head
     // slice kernel: per-(row, slice) records and per-row arrival counters
     dst::SliceWorkspace slice_ws;
     int slice_rows;

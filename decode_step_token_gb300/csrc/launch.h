@@ -104,9 +104,9 @@ int group_prepare(int dtype, bool pen, size_t smem);
 // work: two zeroed counters of the handle (the kernel leaves them zeroed)
 int group_launch(const sampler_args_t* a, const GroupGeometry& g, int clusters, uint32_t* work, cudaStream_t stream);
 
-// ---------------------------------------------------------------- scoring and losses
-constexpr uint64_t kWaitNs = 2000000000ull;  // a wait inside a kernel gives up after 2 s
+constexpr uint64_t kWaitNs = 2000000000ull;  // a wait inside the kernels below gives up after 2 s
 
+// ---------------------------------------------------------------- scoring and losses
 // One row's record: its share of the logits' gradient, with u = (x_v - ref) * c
 // d loss / d x_v = 2^u * (k0 + k1 * u) + (v == token ? at_token : 0).
 struct RowRecord {
@@ -162,6 +162,6 @@ int quantize_launch(const sampler_quantize_t& q, int sms, cudaStream_t stream);
 
 // dtype: the logits' type
 int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, int64_t ldl, int64_t rows,
-                       int64_t vocab, int sms, unsigned long long* timeouts, cudaStream_t stream);
+                       int64_t vocab, int sms, uint64_t wait_ns, unsigned long long* timeouts, cudaStream_t stream);
 
 }  // namespace dst

@@ -84,53 +84,18 @@ struct RowPlan {
 
 constexpr int kPut = 0x7fffffff;  // in the place of the next vector: the row's sums have been put
 
-// A ring's place and the parity of its phase.
-struct Place {
-    uint32_t at, phase;
-    __device__ __forceinline__ void next(uint32_t n)
-    {
-        if (++at == n) {
-            at = 0;
-            phase ^= 1u;
-        }
-    }
-};
-
-__device__ __forceinline__ uint64_t now_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
+using Place = RingPlace;
 
 // A whole warp waits for the phase of `bar` with the given parity, for `ns` at
 // most; all of its lanes get the same answer.
 __device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, uint64_t ns)
 {
-    const uint64_t until = now_ns() + ns;
-    for (uint32_t i = 0; i < (1u << 30); ++i) {
-        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-        if ((i & 63u) == 63u && __any_sync(0xffffffffu, now_ns() > until)) return false;
-    }
-    return false;
+    return mbar_wait_warp(bar, parity, now_ns() + ns);
 }
 
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint64_t ns)
 {
     return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_slow(bar, parity, ns);
-}
-
-// True in one lane of a warp whose lanes are together.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-__device__ __forceinline__ void arrive(uint64_t* bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // Put 16 bytes into a CTA of the cluster and count them on its barrier. (Ordinary
@@ -641,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
                 S.jobs[batch.at][lane] = job;
             }
             __syncwarp();
-            if (lane == 0) arrive(&S.job_full[batch.at]);
+            if (lane == 0) mbar_arrive(&S.job_full[batch.at]);
             batch.next(2);
         };
         int64_t mine;
@@ -718,14 +683,14 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
             if (job.live) {
                 if (lane == 0) {
                     if (kGrad) S.rec[sp.at] = rec;
-                    arrive(&S.closed[sp.at]);
+                    mbar_arrive(&S.closed[sp.at]);
                 }
                 sp.next(kSums);
             }
             if (rank == 0 && lane == 0) row_write(P, job.row, rec, out);
             __syncwarp();
             if (job.last) {
-                if (lane == 0) arrive(&S.job_empty[batch.at]);
+                if (lane == 0) mbar_arrive(&S.job_empty[batch.at]);
                 batch.next(2);
                 k = -1;
             }
@@ -755,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
         // a job that has been done with gives its batch back if it is the batch's last
         auto leave = [&](const RowJob* job) {
             __syncwarp();
-            if (job->last && lane == 0) arrive(&S.job_empty[(job - S.jobs[0]) / kBatch]);
+            if (job->last && lane == 0) mbar_arrive(&S.job_empty[(job - S.jobs[0]) / kBatch]);
         };
         // pass 1 of a row, as far as it has come
         Stats st;
@@ -803,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
                 }
                 if (!kGrad) {
                     __syncwarp();
-                    if (lane == 0) arrive(&S.empty[slot1.at]);
+                    if (lane == 0) mbar_arrive(&S.empty[slot1.at]);
                 }
                 slot1.next(slots);
             }
@@ -855,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 2) rows_kernel(const __grid_constant
                     }
                 }
                 __syncwarp();
-                if (lane == 0) arrive(&S.empty[slot2.at]);
+                if (lane == 0) mbar_arrive(&S.empty[slot2.at]);
                 slot2.next(slots);
             }
         };

@@ -43,7 +43,7 @@
 //   warp 9     owns the tensor memory and issues the MMAs.
 // Warps 10 and 11 fill up the third warpgroup, which gives its registers to the
 // epilogue's where those hold 128 sums a thread (more rows).
-// Every wait is bounded in time; a CTA whose wait gives up counts itself in the
+// Every wait is bounded in time, with one answer for a warp; a CTA whose wait gives up counts itself in the
 // handle's statistics and leaves its logits unwritten.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -78,7 +78,6 @@ constexpr uint32_t kBoxBytes = 32 * 128;       // a box of logits: 32 rows of 12
 constexpr uint32_t kOutBytes = 8 * kBoxBytes;  // one for each warp of the epilogue: with more, a stage less
 constexpr int kScaleBlocks = 4;                // blocks of K whose scales are fetched together
 constexpr uint32_t kABytes = kBM * kBK;        // 16 KB a stage
-constexpr uint64_t kWaitNs = 2000000000ull;    // a wait gives up after 2 s
 constexpr size_t kScaleBytes = 2 * kScaleBlocks * kFewRows * 4;  // transposed: two buffers of every column's scales
 constexpr size_t kBarBytes = 512;
 constexpr size_t kSmemMax = 227 * 1024;
@@ -99,20 +98,11 @@ struct Params {
     uint32_t tmem_cols;    // a power of two >= accs * NT
     int wide_scales;       // bits 0, 1: the hidden and the weight's scales can be read four at a time
     int tma_stores;        // the logits lie so that the TMA engine can write them
+    uint64_t wait_ns;      // kWaitNs, or 0: every wait gives up
     unsigned long long* timeouts;
 };
 
-// A ring's place and the parity of its phase.
-struct Ring {
-    uint32_t at, phase;
-    __device__ __forceinline__ void next(uint32_t n)
-    {
-        if (++at == n) {
-            at = 0;
-            phase ^= 1u;
-        }
-    }
-};
+using Ring = RingPlace;
 
 // K-major tile in the 128-byte swizzled layout that the TMA engine writes: 8-row
 // atoms 1024 bytes apart.
@@ -196,43 +186,10 @@ __device__ __forceinline__ void fma2(float2& a, uint32_t x, uint32_t y, float p,
         : "r"(x), "r"(y), "f"(p), "f"(q));
 }
 
-// True in one lane of a warp whose lanes are together. The warps that issue TMA
-// loads and MMAs run as a whole, with this around the issuing instructions: their
-// operands are then known to be the same for all lanes, which those instructions
-// need. (Inside `if (lane == 0)` an MMA took about 65 cycles to issue and a commit
-// about 100, together more than the tensor cores took for a block.)
-__device__ __forceinline__ bool elect_one()
+// A whole warp waits for the phase of `bar` with the given parity, for `ns` at most.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, uint64_t ns)
 {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-__device__ __forceinline__ uint64_t now_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Wait for the phase of `bar` with the given parity, for kWaitNs at most.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity)
-{
-    uint64_t until = 0;
-    for (uint32_t i = 0; i < (1u << 30); ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63u) == 63u) {
-            const uint64_t now = now_ns();
-            if (until == 0) until = now + kWaitNs;
-            if (now > until) return false;
-        }
-    }
-    return false;
-}
-
-__device__ __forceinline__ void arrive(uint64_t* bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || mbar_wait_warp(bar, parity, now_ns() + ns);
 }
 
 __device__ __forceinline__ void group_sync(int group)
@@ -308,19 +265,23 @@ __device__ __forceinline__ void tile_at(const Params& P, int t, int& m, int& n)
     n = kFew ? 0 : t / P.row_tiles * kWideN;
 }
 
-// The TMA warp.
+// The TMA warp. It and the MMA warp run as a whole, with elect_one around the
+// issuing instructions: their operands are then known to be the same for all
+// lanes, which those instructions need. (Inside `if (lane == 0)` an MMA took about
+// 65 cycles to issue and a commit about 100, together more than the tensor cores
+// took for a block.)
 template <bool kFew>
 __device__ __forceinline__ void produce(const Params& P, Control& C, unsigned char* sa, unsigned char* sb)
 {
     const uint32_t S = uint32_t(P.stages), b_bytes = kFew ? uint32_t(P.NT) * kBK : kWideBytes;
     Ring s{0, 0};
     uint32_t issued = 0;
-    bool ok = true;
+    bool ok = P.wait_ns != 0;  // 0: nothing is loaded, and the other warps' waits give up
     for (int t = int(blockIdx.x); ok && t < P.tiles; t += int(gridDim.x)) {
         int m, n;
         tile_at<kFew>(P, t, m, n);
         for (int b = 0; b < P.blocks; ++b) {
-            ok = wait(&C.done[s.at], s.phase ^ 1u);
+            ok = wait(&C.done[s.at], s.phase ^ 1u, P.wait_ns);
             if (!ok) break;
             if (elect_one()) {
                 mbar_arrive_expect_tx(&C.ready[s.at], kABytes + b_bytes);
@@ -334,7 +295,7 @@ __device__ __forceinline__ void produce(const Params& P, Control& C, unsigned ch
     }
     if (!ok) C.gave_up = 1;
     // the last copies issued land before the CTA may exit
-    for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j) wait(&C.ready[j % S], j / S & 1u);
+    for (uint32_t j = issued > S ? issued - S : 0; j < issued; ++j) wait(&C.ready[j % S], j / S & 1u, kWaitNs);
 }
 
 // The MMA warp: each block of K into the next accumulator.
@@ -351,7 +312,7 @@ __device__ __forceinline__ void multiply(const Params& P, Control& C, unsigned c
             const uint32_t d = tmem + acc.at * cols;
             const uint64_t da = desc_sw128(smem_addr(sa + s.at * kABytes));
             const uint64_t db = desc_sw128(smem_addr(sb + s.at * b_bytes));
-            ok = wait(&C.ready[s.at], s.phase);
+            ok = wait(&C.ready[s.at], s.phase, P.wait_ns);
             if (!ok) break;
             fence_after_sync();
             if (elect_one()) {
@@ -368,7 +329,7 @@ __device__ __forceinline__ void multiply(const Params& P, Control& C, unsigned c
     if (!ok) C.gave_up = 1;
     if (elect_one()) mma_commit(&C.drained);
     __syncwarp();
-    wait(&C.drained, 0);
+    wait(&C.drained, 0, kWaitNs);
 }
 
 // Scales of blocks b .. b + 3 from one row of them; 0 past the row's end and where there is none.
@@ -391,7 +352,7 @@ __device__ __forceinline__ void fetch_scales(float (&q)[kScaleBlocks], const flo
 __device__ __forceinline__ void free_first(const Params& P, Control& C, int lane)
 {
     if (lane == 0)
-        for (int k = 0; k < P.accs; ++k) arrive(&C.ready[k]);
+        for (int k = 0; k < P.accs; ++k) mbar_arrive(&C.ready[k]);
     __syncwarp();
 }
 
@@ -455,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
                     }
                 }
                 const float* row = mine + buffer * (kScaleBlocks * kFewRows) + b % kScaleBlocks * kFewRows;
-                ok = ok && wait(&C.done[s.at], s.phase);
+                ok = ok && wait(&C.done[s.at], s.phase, P.wait_ns);
                 if (ok) {
                     fence_after_sync();
                     const uint32_t at = lanes + acc.at * uint32_t(P.NT);
@@ -474,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
                     fence_before_sync();
                 }
                 __syncwarp();
-                if (ok && lane == 0) arrive(&C.ready[freed]);
+                if (ok && lane == 0) mbar_arrive(&C.ready[freed]);
                 acc.next(uint32_t(P.accs));
                 s.next(uint32_t(P.stages));
                 freed = freed + 1 == uint32_t(P.stages) ? 0 : freed + 1;
@@ -568,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
 #pragma unroll
                 for (int i = 0; i < kScaleBlocks; ++i) {
                     if (b0 + i >= P.blocks) break;
-                    ok = wait(&C.done[s.at], s.phase);
+                    ok = wait(&C.done[s.at], s.phase, P.wait_ns);
                     if (!ok) break;
                     fence_after_sync();
                     const uint32_t at = lanes + acc.at * uint32_t(kWideN);
@@ -585,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
                         } else {                  // all of the accumulator has been read
                             fence_before_sync();
                             __syncwarp();
-                            if (lane == 0) arrive(&C.ready[freed]);
+                            if (lane == 0) mbar_arrive(&C.ready[freed]);
                         }
 #pragma unroll
                         for (int k = 0; k < kLoad; k += 2) fma2(sum[(c + k) / 2], now[k], now[k + 1], q[i], q[i]);
@@ -693,7 +654,7 @@ using Kernel = void (*)(const Params);
 }  // namespace scaled
 
 int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, int64_t ldl, int64_t rows,
-                       int64_t vocab, int sms, unsigned long long* timeouts, cudaStream_t stream)
+                       int64_t vocab, int sms, uint64_t wait_ns, unsigned long long* timeouts, cudaStream_t stream)
 {
     using namespace scaled;
     Params p;
@@ -729,6 +690,7 @@ int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, 
     if (p.tma_stores && !encode_logits(&p.to, logits, dtype, rows, vocab, ldl)) return SAMPLER_ERR_CUDA;
     p.rows = int(rows);
     p.V = int(vocab);
+    p.wait_ns = wait_ns;
     p.timeouts = timeouts;
     const bool bf16 = dtype == SAMPLER_DTYPE_BF16;
     const Kernel kernel = few    ? bf16 ? few_rows_kernel<uint16_t> : few_rows_kernel<float>

@@ -63,7 +63,7 @@ int check_scaled(const sampler_scaled_head_t* g)
 int launch_scaled(sampler_t h, const sampler_scaled_head_t* g, void* logits, int dtype, int64_t ldl, int64_t rows,
                   int64_t vocab, cudaStream_t stream)
 {
-    return dst::scaled_head_launch(*g, logits, dtype, ldl, rows, vocab, h->num_sms,
+    return dst::scaled_head_launch(*g, logits, dtype, ldl, rows, vocab, h->num_sms, h->wait_ns,
                                    h->stats + SAMPLER_STAT_LM_HEAD_TIMEOUTS, stream);
 }
 

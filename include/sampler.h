@@ -124,8 +124,9 @@ typedef struct {
  * The kernel still lets each copy land before it reuses or releases the
  * buffer, so nothing faults and nothing hangs; later calls are unaffected
  * (no state survives a call). Scoring and the losses give up likewise where
- * their rows take a kernel with waits (rows above 16 KB may). Lets a test
- * observe the timeout status. */
+ * their rows take a kernel with waits (rows above 16 KB may), and so does the
+ * 8-bit LM head, which leaves its logits as they were and counts its blocks in
+ * SAMPLER_STAT_LM_HEAD_TIMEOUTS. Lets a test observe the timeout status. */
 #define SAMPLER_CREATE_SHORT_WAITS 4u
 
 /*

@@ -260,3 +260,27 @@ def test_refusals(sampler):
     empty = _up(np.zeros((0, 64), np.uint8))
     sampler.lm_head_scaled(**{**op, "hidden": empty, "hidden_scale": torch.empty((0, 1), device="cuda:0"),
                               "logits": out})
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V,K", [(7, 900, 300), (32, 30000, 4096), (33, 900, 300), (300, 20000, 640)])
+def test_waits_that_give_up(sampler, rows, V, K, kind):
+    """On a handle whose waits give up at once the head ends, counts every block and writes nothing; another handle
+    is not affected."""
+    import torch
+    import decode_step_token_gb300 as d
+
+    h, sh, w, sw = _head(21, rows, V, K)
+    op = dict(hidden=_up(h), hidden_scale=torch.from_numpy(sh).cuda(), weight=_up(w),
+              weight_scale=torch.from_numpy(sw).cuda())
+    out = torch.full((rows, V), -7.0, dtype=torch.bfloat16 if kind == "bf16" else torch.float32, device="cuda:0")
+    tiles = -(-V // 128) if rows <= 32 else -(-V // 256) * -(-rows // 128)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    with d.Sampler(max_rows=64, max_vocab=V, short_waits=True) as short:
+        short.lm_head_scaled(logits=out, **op)
+        assert short.stat(d.SAMPLER_STAT_LM_HEAD_TIMEOUTS, reset=True) == min(tiles, sms)
+    assert (out == -7).all()
+    sampler.lm_head_scaled(logits=out, **op)
+    assert sampler.stat(d.SAMPLER_STAT_LM_HEAD_TIMEOUTS) == 0
+    want, mag = L.scaled_head(h, sh, w, sw)
+    _close(out.double().cpu().numpy(), want, mag, K, kind)

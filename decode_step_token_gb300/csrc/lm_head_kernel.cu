@@ -117,15 +117,8 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16])
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ uint64_t now_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
 // Wait for the phase of `bar` with the given parity, giving up at `deadline`
-// (global timer, ns); returns success.
+// (global timer, ns); returns success. One thread's wait.
 __device__ __forceinline__ bool wait_until(uint64_t* bar, uint32_t parity, uint64_t deadline)
 {
     for (uint32_t i = 0; i < (1u << 30); ++i) {
@@ -133,11 +126,6 @@ __device__ __forceinline__ bool wait_until(uint64_t* bar, uint32_t parity, uint6
         if ((i & 63u) == 63u && now_ns() > deadline) return false;
     }
     return false;
-}
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 __global__ void __launch_bounds__(kThreads, 1) lm_head_kernel(const __grid_constant__ Params P)
@@ -253,7 +241,8 @@ __global__ void __launch_bounds__(kThreads, 1) lm_head_kernel(const __grid_const
         bool ok = true;
         for (int t = 0; t < my_tiles; ++t) {
             const int acc = t & 1;
-            if (!wait_until(&tfull[acc], uint32_t(t >> 1) & 1u, deadline)) {
+            // one answer for the warp: its loads from tensor memory are the whole warp's
+            if (!mbar_wait_warp(&tfull[acc], uint32_t(t >> 1) & 1u, deadline)) {
                 ok = false;
                 break;
             }

@@ -56,6 +56,7 @@
 
 #include "launch.h"
 #include "ptx.cuh"
+#include "warp_wait.cuh"
 
 namespace dst {
 namespace scaled {

@@ -30,6 +30,7 @@ struct sampler_s {
     unsigned long long* stats;  // device counters (diagnostics)
     dst::RowWorkspace row_ws;  // scoring and the losses: one record per row, and a launch's ticket
     dst::RowOccupancy row_occ;
+    dst::ScaledHeadGrants head_grants;
     // staging for sampler_sample_host
     unsigned char* stage_base;
     size_t stage_bytes;

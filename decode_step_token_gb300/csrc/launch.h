@@ -160,8 +160,15 @@ int pairs_grad_launch(const sampler_rows_t& rows, const RowWorkspace& ws, bool d
 // ---------------------------------------------------------------- 8-bit LM head
 int quantize_launch(const sampler_quantize_t& q, int sms, cudaStream_t stream);
 
+// Whether a handle has granted the head's kernels their shared memory, by few or
+// many rows and the logits' type.
+struct ScaledHeadGrants {
+    bool granted[2][2];
+};
+
 // dtype: the logits' type
 int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, int64_t ldl, int64_t rows,
-                       int64_t vocab, int sms, uint64_t wait_ns, unsigned long long* timeouts, cudaStream_t stream);
+                       int64_t vocab, int sms, uint64_t wait_ns, unsigned long long* timeouts,
+                       ScaledHeadGrants* grants, cudaStream_t stream);
 
 }  // namespace dst

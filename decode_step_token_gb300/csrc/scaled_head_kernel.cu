@@ -655,7 +655,8 @@ using Kernel = void (*)(const Params);
 }  // namespace scaled
 
 int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, int64_t ldl, int64_t rows,
-                       int64_t vocab, int sms, uint64_t wait_ns, unsigned long long* timeouts, cudaStream_t stream)
+                       int64_t vocab, int sms, uint64_t wait_ns, unsigned long long* timeouts,
+                       ScaledHeadGrants* grants, cudaStream_t stream)
 {
     using namespace scaled;
     Params p;
@@ -697,9 +698,13 @@ int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, 
     const Kernel kernel = few    ? bf16 ? few_rows_kernel<uint16_t> : few_rows_kernel<float>
                           : bf16 ? many_rows_kernel<uint16_t> : many_rows_kernel<float>;
     const size_t smem = 1024 + size_t(p.stages) * stage + own + kBarBytes;
-    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(smem)) != cudaSuccess)
+    // the limit belongs to the function, for all handles and threads: always the same one, so that no call takes
+    // from another what it has been granted and not yet launched with
+    bool& granted = grants->granted[few][bf16];
+    if (!granted && cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmemMax)) != cudaSuccess)
         return SAMPLER_ERR_CUDA;
+    granted = true;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned(std::min(sms, p.tiles)));
     cfg.blockDim = dim3(kThreads);

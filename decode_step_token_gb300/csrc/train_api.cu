@@ -64,7 +64,7 @@ int launch_scaled(sampler_t h, const sampler_scaled_head_t* g, void* logits, int
                   int64_t vocab, cudaStream_t stream)
 {
     return dst::scaled_head_launch(*g, logits, dtype, ldl, rows, vocab, h->num_sms, h->wait_ns,
-                                   h->stats + SAMPLER_STAT_LM_HEAD_TIMEOUTS, stream);
+                                   h->stats + SAMPLER_STAT_LM_HEAD_TIMEOUTS, &h->head_grants, stream);
 }
 
 }  // namespace

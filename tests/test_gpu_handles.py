@@ -1,0 +1,56 @@
+"""Several handles in one process: what one of them does takes nothing from another. Needs a GB300."""
+import threading
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def pkg():
+    from decode_step_token_gb300 import build
+    build.build_library()
+    import decode_step_token_gb300 as d
+    return d
+
+
+def _codes(rng, rows, K):
+    import torch
+
+    return torch.from_numpy(rng.integers(0, 0x70, (rows, K)).astype(np.uint8)).cuda()
+
+
+def test_8bit_heads_of_two_threads(pkg):
+    """A head of 16 rows needs less shared memory than one of 32: two threads that call them in turn, each with its
+    handle and stream, do not refuse each other's launches."""
+    import torch
+
+    rng = np.random.default_rng(1)
+    K, V, calls = 128, 300, 3000
+    w, ws = _codes(rng, V, K), torch.ones((3, 1), device="cuda:0")
+    failed, start = [], threading.Barrier(2)
+
+    def work(rows):
+        try:
+            torch.cuda.set_device(0)
+            stream = torch.cuda.Stream()
+            h, hs = ops[rows]
+            with pkg.Sampler(max_rows=64, max_vocab=V) as s:
+                start.wait()
+                for _ in range(calls):
+                    s.lm_head_scaled(hidden=h, hidden_scale=hs, weight=w, weight_scale=ws, logits=out[rows],
+                                     stream=stream.cuda_stream)
+                stream.synchronize()
+        except Exception as e:  # noqa: BLE001 - seen by the test below
+            failed.append((rows, e))
+
+    ops = {rows: (_codes(rng, rows, K), torch.ones((rows, 1), device="cuda:0")) for rows in (16, 32)}
+    out = {rows: torch.empty((rows, V), device="cuda:0") for rows in ops}
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(rows,)) for rows in ops]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed

@@ -24,6 +24,11 @@ namespace {
 constexpr int64_t kMaxVocabLimit = 262144;  // a row always fits one cluster's shared memory
 constexpr int kNumStats = 4;
 constexpr uint32_t kMaxPolls = 1u << 24;  // bound of each wait on a staging copy
+// Shared memory that the fork-group kernel and the LM-head GEMM are granted: the
+// most that any call takes, and always that, as a function's limit belongs to all
+// handles (a handle that set its own smaller one would take it from the others).
+constexpr size_t kGroupSmem = 226 * 1024;
+constexpr size_t kLmHeadSmem = 227 * 1024;
 
 size_t align16(size_t x) { return (x + 15) & ~size_t(15); }
 
@@ -47,8 +52,8 @@ int launch_group(sampler_t h, const sampler_args_t* a, cudaStream_t stream)
     if (!dst::group_geometry(a->vocab, esize_of(a->dtype), pen, &gg)) return SAMPLER_ERR_TOO_LARGE;
     const int slot = kernel_slot(a->dtype, pen);
     if (h->grp_smem_set[slot] < gg.smem) {
-        if (dst::group_prepare(a->dtype, pen, gg.smem) != SAMPLER_OK) return SAMPLER_ERR_CUDA;
-        h->grp_smem_set[slot] = gg.smem;
+        if (dst::group_prepare(a->dtype, pen, kGroupSmem) != SAMPLER_OK) return SAMPLER_ERR_CUDA;
+        h->grp_smem_set[slot] = kGroupSmem;
     }
     if (h->grp_occ_smem[slot] != gg.smem || h->grp_occ[slot] < 1) {
         const int nc = dst::group_occupancy(a->dtype, pen, gg);
@@ -360,8 +365,8 @@ int launch_lm_head(sampler_t h, const sampler_lm_head_t* lm, void* logits, int64
     dst::LmHeadPlan plan;
     if (!dst::lm_head_plan(rows, vocab, lm->hidden_dim, h->num_sms, &plan)) return SAMPLER_ERR_TOO_LARGE;
     if (h->lmh_smem_set < plan.smem) {
-        if (dst::lm_head_prepare(plan.smem) != SAMPLER_OK) return SAMPLER_ERR_CUDA;
-        h->lmh_smem_set = plan.smem;
+        if (dst::lm_head_prepare(kLmHeadSmem) != SAMPLER_OK) return SAMPLER_ERR_CUDA;
+        h->lmh_smem_set = kLmHeadSmem;
     }
     return dst::lm_head_launch(lm, logits, ldl, rows, vocab, plan, h->stats + SAMPLER_STAT_LM_HEAD_TIMEOUTS, stream);
 }

@@ -54,3 +54,44 @@ def test_8bit_heads_of_two_threads(pkg):
     for t in threads:
         t.join()
     assert not failed, failed
+
+
+def test_group_kernels_of_two_handles(pkg):
+    """The fork-group kernel's shared memory follows the vocabulary: a small call of one handle leaves another's large
+    one possible."""
+    import torch
+
+    def call(s, V, kind):
+        x = torch.zeros((2, V), dtype=kind, device="cuda:0")
+        x[:, 7] = 9.0
+        tok = torch.empty(2, dtype=torch.int32, device="cuda:0")
+        lp = torch.empty((2, V), device="cuda:0")
+        s.sample(logits=x, temperature=torch.zeros(2, device="cuda:0"), out_tokens=tok, out_logprobs=lp)
+        assert tok.tolist() == [7, 7]
+
+    for kind in (torch.bfloat16, torch.float32):
+        with pkg.Sampler(max_rows=4, max_vocab=262144) as a, pkg.Sampler(max_rows=4, max_vocab=262144) as b:
+            call(a, 262144, kind)
+            call(b, 100, kind)
+            call(a, 262144, kind)
+
+
+def test_lm_heads_of_two_handles(pkg):
+    """So does the bf16 head's, with the rows."""
+    import torch
+
+    w = torch.eye(64, device="cuda:0").to(torch.bfloat16)
+
+    def call(s, rows):
+        h = w[torch.arange(rows, device="cuda:0") % 64]
+        out = torch.empty((rows, 64), dtype=torch.bfloat16, device="cuda:0")
+        s.lm_head(hidden=h, weight=w, logits=out)
+        assert torch.equal(out, h)
+
+    with pkg.Sampler(max_rows=256, max_vocab=64) as a, pkg.Sampler(max_rows=256, max_vocab=64) as b:
+        sizes = (240, 16, 176, 256)
+        for rows in sizes:
+            call(a, rows)
+        for rows in sizes[1:] + sizes:
+            call(b, 16)
+            call(a, rows)

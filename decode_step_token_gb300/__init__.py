@@ -19,7 +19,7 @@ from ._binding import (EXPORTED, SAMPLER_CREATE_HOST_STAGING, SAMPLER_CREATE_SHO
                        load_library, sampler_abi_version, sampler_args_t, sampler_config_t, sampler_create,
                        sampler_destroy, sampler_ext_t, sampler_sample, sampler_sample_host,
                        sampler_sample_ex, sampler_sample_noalloc, sampler_status_string,
-                       sampler_get_stat, SAMPLER_ERR_BAD_VALUE, sampler_rows_t, sampler_policy_t,
+                       sampler_get_stat, SAMPLER_ERR_BAD_VALUE, SAMPLER_LOSS_MAX_ROWS, sampler_rows_t, sampler_policy_t,
                        sampler_preference_t, sampler_quantize_t, sampler_scaled_head_t, sampler_score,
                        sampler_score_grad, sampler_policy_loss, sampler_preference_loss, sampler_quantize_blocks,
                        sampler_lm_head_scaled, sampler_lm_head_scaled_sample)
@@ -30,7 +30,7 @@ __all__ = ["Sampler", "SamplerError", "load_library", "sampler_create", "sampler
            "SAMPLER_MAX_STOP", "sampler_ext_t", "sampler_lm_head_t", "sampler_lm_head_sample", "sampler_lm_head",
            "SAMPLER_LM_HEAD_MAX_ROWS", "SAMPLER_STAT_EXACT_ROWS", "SAMPLER_STAT_LM_HEAD_TIMEOUTS",
            "sampler_abi_version", "sampler_args_t", "sampler_config_t", "EXPORTED",
-           "SAMPLER_ERR_BAD_VALUE", "sampler_rows_t", "sampler_policy_t", "sampler_preference_t",
+           "SAMPLER_ERR_BAD_VALUE", "SAMPLER_LOSS_MAX_ROWS", "sampler_rows_t", "sampler_policy_t", "sampler_preference_t",
            "sampler_quantize_t", "sampler_scaled_head_t", "sampler_score", "sampler_score_grad",
            "sampler_policy_loss", "sampler_preference_loss", "sampler_quantize_blocks", "sampler_lm_head_scaled",
            "sampler_lm_head_scaled_sample"]

@@ -46,6 +46,7 @@ SAMPLER_STAT_EXACT_ROWS = 0
 SAMPLER_STAT_LM_HEAD_TIMEOUTS = 1
 SAMPLER_LM_HEAD_MAX_ROWS = 256
 SAMPLER_NOALLOC_MAX_ROWS = 64
+SAMPLER_LOSS_MAX_ROWS = 16777216
 SAMPLER_MAX_TOP_N = 16
 SAMPLER_MAX_BIAS = 64
 SAMPLER_MAX_STOP = 16

@@ -28,7 +28,7 @@ struct sampler_s {
     int grp_occ[4];          // co-resident clusters of the fork-group kernel
     uint32_t* grp_work;      // the fork-group kernel's chunk counters (zero between launches)
     unsigned long long* stats;  // device counters (diagnostics)
-    dst::RowWorkspace row_ws;  // scoring and the losses: one record per row, and a launch's ticket
+    dst::RowWorkspace row_ws;  // the losses: one record per row, and a launch's ticket
     dst::RowOccupancy row_occ;
     dst::ScaledHeadGrants head_grants;
     // staging for sampler_sample_host

@@ -124,9 +124,10 @@ struct RowRecord {
 constexpr size_t kRowRecordBytes = sizeof(RowRecord);
 
 struct RowWorkspace {
-    RowRecord* records;  // [max_rows]
-    double* terms;       // [max_rows] each row's share of the loss (pairs: its logprob)
-    double* pair_terms;  // [max_rows] each pair's share of the loss
+    RowRecord* records;  // [rows]
+    double* terms;       // [rows] each row's share of the loss (pairs: its logprob)
+    double* pair_terms;  // [rows] each pair's share of the loss
+    int64_t rows;        // min(the handle's max_rows, SAMPLER_LOSS_MAX_ROWS)
     uint32_t* ticket;    // blocks (or clusters) that have ended; zero between launches
 };
 

@@ -259,6 +259,9 @@ int sampler_create(sampler_t* out, const sampler_config_t* cfg)
     {
         const size_t recs = size_t(h->slice_rows) * dst::kSliceMaxSlices;
         const size_t cnt_bytes = size_t(h->slice_rows) * dst::kSliceCntStride * sizeof(uint32_t);
+        // the losses' records; what else a handle does needs nothing for a row
+        h->row_ws.rows = std::min<int64_t>(cfg->max_rows, SAMPLER_LOSS_MAX_ROWS);
+        const size_t loss_rows = size_t(h->row_ws.rows);
         if (cudaMalloc(&h->slice_ws.hdr, recs * dst::kSliceHdrBytes) != cudaSuccess ||
             cudaMalloc(&h->slice_ws.body, recs * dst::kSliceBodyBytes) != cudaSuccess ||
             cudaMalloc(&h->slice_ws.cnt, cnt_bytes) != cudaSuccess ||
@@ -267,9 +270,9 @@ int sampler_create(sampler_t* out, const sampler_config_t* cfg)
             cudaMemset(h->stats, 0, kNumStats * sizeof(unsigned long long)) != cudaSuccess ||
             cudaMalloc(&h->grp_work, 2 * sizeof(uint32_t)) != cudaSuccess ||
             cudaMemset(h->grp_work, 0, 2 * sizeof(uint32_t)) != cudaSuccess ||
-            cudaMalloc(&h->row_ws.records, size_t(h->max_rows) * dst::kRowRecordBytes) != cudaSuccess ||
-            cudaMalloc(&h->row_ws.terms, size_t(h->max_rows) * sizeof(double)) != cudaSuccess ||
-            cudaMalloc(&h->row_ws.pair_terms, size_t(h->max_rows) * sizeof(double)) != cudaSuccess ||
+            cudaMalloc(&h->row_ws.records, loss_rows * dst::kRowRecordBytes) != cudaSuccess ||
+            cudaMalloc(&h->row_ws.terms, loss_rows * sizeof(double)) != cudaSuccess ||
+            cudaMalloc(&h->row_ws.pair_terms, loss_rows * sizeof(double)) != cudaSuccess ||
             cudaMalloc(&h->row_ws.ticket, sizeof(uint32_t)) != cudaSuccess ||
             cudaMemset(h->row_ws.ticket, 0, sizeof(uint32_t)) != cudaSuccess ||
             cudaDeviceSynchronize() != cudaSuccess) {

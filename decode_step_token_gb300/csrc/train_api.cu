@@ -113,6 +113,7 @@ int sampler_policy_loss(sampler_t h, const sampler_rows_t* rows, const sampler_p
 {
     const int rc = check_rows(h, rows);
     if (rc != SAMPLER_OK) return rc;
+    if (rows->n_rows > h->row_ws.rows) return SAMPLER_ERR_TOO_LARGE;
     if (!q || !q->out_loss) return SAMPLER_ERR_NULL_ARG;
     if (!(q->clip_low >= 0.f && q->clip_low <= 1.f) || !(q->clip_high >= 0.f) || !std::isfinite(q->clip_high) ||
         !std::isfinite(q->kl_coef) || !std::isfinite(q->entropy_coef) || !std::isfinite(q->grad_scale))
@@ -141,10 +142,11 @@ int sampler_preference_loss(sampler_t h, const sampler_rows_t* rows, const sampl
 {
     int rc = check_rows(h, rows);
     if (rc != SAMPLER_OK) return rc;
+    if (rows->n_rows > h->row_ws.rows) return SAMPLER_ERR_TOO_LARGE;
     if (!q || !q->out_loss) return SAMPLER_ERR_NULL_ARG;
     if (rows->out_entropy) return SAMPLER_ERR_UNSUPPORTED;
     if (q->n_pairs < 0) return SAMPLER_ERR_BAD_SHAPE;
-    if (q->n_pairs > h->max_rows || q->n_pairs > INT_MAX) return SAMPLER_ERR_TOO_LARGE;
+    if (q->n_pairs > h->row_ws.rows) return SAMPLER_ERR_TOO_LARGE;
     if (!std::isfinite(q->beta) || !std::isfinite(q->margin) || !std::isfinite(q->grad_scale) ||
         !(q->label_smoothing >= 0.f && q->label_smoothing <= 1.f))
         return SAMPLER_ERR_BAD_VALUE;

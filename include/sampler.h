@@ -384,11 +384,14 @@ int sampler_lm_head(sampler_t h, const sampler_lm_head_t* lm, void* logits, int6
  * grad_scale and by *grad_scale_dev (a device float, NULL: 1), the gradient
  * that arrives at the loss.
  *
- * n_rows is at most the handle's max_rows, vocab at most its max_vocab. The
- * calls enqueue on `stream`, allocate nothing, read no device memory on the
- * host and can be captured in a CUDA graph. Their results do not depend on the
- * order in which the GPU's blocks run: the same inputs give the same bits.
+ * n_rows is at most the handle's max_rows, and in the two losses at most
+ * SAMPLER_LOSS_MAX_ROWS; vocab is at most its max_vocab. The calls enqueue on
+ * `stream`, allocate nothing, read no device memory on the host and can be
+ * captured in a CUDA graph. Their results do not depend on the order in which
+ * the GPU's blocks run: the same inputs give the same bits.
  */
+#define SAMPLER_LOSS_MAX_ROWS 16777216 /* a handle keeps 48 bytes for each row up to these */
+
 typedef struct {
     const void* logits;         /* row i from element i * row_stride */
     int32_t dtype;              /* SAMPLER_DTYPE_* */
@@ -458,7 +461,8 @@ int sampler_policy_loss(sampler_t h, const sampler_rows_t* rows, const sampler_p
  * gradient of zeros. An answer whose offsets do not lie in 0 <= begin <= end
  * <= n_rows has no rows and a NaN reward; the loss and the gradient of its
  * pair's other answer are then NaN. (Offsets that decrease have such an answer.
- * Rows that they put into more than one answer get a NaN gradient.) n_pairs is at most the handle's max_rows.
+ * Rows that they put into more than one answer get a NaN gradient.) n_pairs has
+ * the same limits as n_rows.
  */
 typedef struct {
     const int32_t* seq_offsets; /* [2 * n_pairs + 1] */

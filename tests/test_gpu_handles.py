@@ -95,3 +95,33 @@ def test_lm_heads_of_two_handles(pkg):
         for rows in sizes[1:] + sizes:
             call(b, 16)
             call(a, rows)
+
+
+def test_handle_for_any_number_of_rows(pkg):
+    """max_rows only bounds the calls: a handle with a large one holds no memory for rows beyond what a loss takes."""
+    import torch
+
+    most = pkg.SAMPLER_LOSS_MAX_ROWS
+    with pkg.Sampler(max_rows=1 << 40, max_vocab=1000) as s:
+        x = torch.zeros((3, 1000), device="cuda:0")
+        x[:, 5] = 60.0
+        tok = torch.empty(3, dtype=torch.int32, device="cuda:0")
+        s.sample(logits=x, temperature=torch.ones(3, device="cuda:0"), out_tokens=tok)
+        assert tok.tolist() == [5, 5, 5]
+        loss, one = torch.empty(1, device="cuda:0"), torch.ones(3, device="cuda:0")
+        s.policy_loss(logits=x, tokens=tok, old_logprob=one - 1, advantage=one, out_loss=loss)
+        assert abs(loss.item() + 3.0) < 1e-6
+        # scoring takes more rows than the losses
+        n = most + 5
+        x = torch.zeros((n, 1), dtype=torch.bfloat16, device="cuda:0")
+        tok, lp = torch.zeros(n, dtype=torch.int32, device="cuda:0"), torch.full((n,), -7.0, device="cuda:0")
+        s.score(logits=x, tokens=tok, out_logprob=lp)
+        assert (lp == 0).all()
+        ends = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda:0")
+        for call in (lambda: s.policy_loss(logits=x, tokens=tok, old_logprob=lp, advantage=lp, out_loss=loss),
+                     lambda: s.preference_loss(logits=x, tokens=tok, seq_offsets=ends, out_loss=loss)):
+            with pytest.raises(pkg.SamplerError) as e:
+                call()
+            assert e.value.code == -3
+        s.policy_loss(logits=x[:most], tokens=tok, old_logprob=lp, advantage=lp, out_loss=loss)
+        assert loss.item() == 0.0

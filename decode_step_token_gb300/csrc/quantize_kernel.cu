@@ -198,15 +198,17 @@ bool launch(sampler_quantize_t q, int sms, cudaStream_t stream)
         q.src = src + done * q.src_stride * int64_t(sizeof(T));
         q.values = values + done * q.values_stride;
         q.scales = scales + done / q.block_rows * q.scale_stride;
-        const dim3 grid(unsigned(across), unsigned((q.rows + rows - 1) / rows));
-        if (square)
-            quantize_kernel<T, kAll, true><<<grid, kThreads, 0, stream>>>(q, vec_in, vec_out);
-        else if (few)
-            quantize_kernel<T, 1, false><<<grid, kThreads, 0, stream>>>(q, vec_in, vec_out);
-        else
-            quantize_kernel<T, kMany, false><<<grid, kThreads, 0, stream>>>(q, vec_in, vec_out);
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(unsigned(across), unsigned((q.rows + rows - 1) / rows));
+        cfg.blockDim = dim3(kThreads);
+        cfg.stream = stream;
+        const auto kernel = square ? quantize_kernel<T, kAll, true>
+                            : few  ? quantize_kernel<T, 1, false>
+                                   : quantize_kernel<T, kMany, false>;
+        // (the launch's own status: cudaGetLastError would also report what an earlier call has left)
+        if (cudaLaunchKernelEx(&cfg, kernel, q, vec_in, vec_out) != cudaSuccess) return false;
     }
-    return cudaGetLastError() == cudaSuccess;
+    return true;
 }
 
 }  // namespace quant

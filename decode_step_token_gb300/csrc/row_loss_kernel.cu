@@ -1155,8 +1155,11 @@ int rows_launch(const LossParams& p, int sms, RowOccupancy* occ, cudaStream_t st
     if (group) {
         const SmallKernel small = es == 2 ? small_kernel<uint16_t>(group, grad, entropy) : small_kernel<float>(group, grad, entropy);
         const int64_t blocks = group == 1 ? (p.rows.n_rows + rows::kSmallBlock - 1) / rows::kSmallBlock : p.rows.n_rows;
-        small<<<unsigned(blocks), unsigned(rows::small_threads(group)), 0, stream>>>(p);
-        return cudaGetLastError() == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(unsigned(blocks));
+        cfg.blockDim = dim3(unsigned(rows::small_threads(group)));
+        cfg.stream = stream;
+        return cudaLaunchKernelEx(&cfg, small, p) == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
     }
     // parts of at most kPartChunks chunks; smaller ones while few rows leave the device unfilled (policy with its
     // gradient, against parts of kPartChunks: 1 x 151936 bf16 8.9 / 11.0 us, 8 x 128000 8.9 / 10.7, 32 x 32000 8.8 / 11)

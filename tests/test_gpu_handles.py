@@ -125,3 +125,21 @@ def test_handle_for_any_number_of_rows(pkg):
             assert e.value.code == -3
         s.policy_loss(logits=x[:most], tokens=tok, old_logprob=lp, advantage=lp, out_loss=loss)
         assert loss.item() == 0.0
+
+
+def test_an_earlier_error_is_not_a_calls_own(pkg):
+    """A handle that could not be had (its staging buffers are far larger than the memory) does not make the next
+    calls of another report an error."""
+    import torch
+
+    x = torch.zeros((4, 256), device="cuda:0")
+    codes, scales = torch.empty((4, 256), dtype=torch.float8_e4m3fn, device="cuda:0"), torch.empty((4, 2), device="cuda:0")
+    tok, lp = torch.zeros(4, dtype=torch.int32, device="cuda:0"), torch.empty(4, device="cuda:0")
+    with pkg.Sampler(max_rows=4, max_vocab=256) as s:
+        for call in (lambda: s.score(logits=x, tokens=tok, out_logprob=lp),
+                     lambda: s.quantize_blocks(src=x, out_values=codes, out_scales=scales)):
+            with pytest.raises(pkg.SamplerError) as e:
+                pkg.Sampler(max_rows=1 << 24, max_vocab=262144, host_staging=True)
+            assert e.value.code == -5
+            call()
+    np.testing.assert_allclose(lp.cpu().numpy(), -np.log(256), rtol=1e-6)

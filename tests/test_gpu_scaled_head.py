@@ -284,3 +284,25 @@ def test_waits_that_give_up(sampler, rows, V, K, kind):
     assert sampler.stat(d.SAMPLER_STAT_LM_HEAD_TIMEOUTS) == 0
     want, mag = L.scaled_head(h, sh, w, sw)
     _close(out.double().cpu().numpy(), want, mag, K, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("pad", ["none", "padded"])
+@pytest.mark.parametrize("rows,V,K", [(33, 1000, 200), (65, 1032, 130), (129, 4104, 128), (300, 20000, 200),
+                                      (64, 256, 300), (200, 264, 64), (45, 8, 128), (128, 513, 140), (333, 20011, 96),
+                                      (160, 50257, 64), (513, 30004, 32)])
+def test_logits_on_16_bytes(sampler, rows, V, K, pad, kind):
+    """Rows of logits that lie on 16 bytes are stored by the TMA engine, whose boxes end where the logits do: at a last
+    tile of the vocabulary that is cut off, or stored otherwise, and at the last rows. Nothing is written beside."""
+    import torch
+
+    h, sh, w, sw = _head(rows + V, rows, V, K)
+    ldl = -(-V // 8) * 8 + (8 if pad == "padded" else 0)
+    guard = 140  # rows after the last: more than a tile's
+    out = torch.full((rows + guard, ldl), -7.0, dtype=torch.bfloat16 if kind == "bf16" else torch.float32, device="cuda:0")
+    assert out.data_ptr() % 16 == 0 and ldl * out.element_size() % 16 == 0
+    sampler.lm_head_scaled(hidden=_up(h), hidden_scale=torch.from_numpy(sh).cuda(), weight=_up(w),
+                           weight_scale=torch.from_numpy(sw).cuda(), logits=out[:rows])
+    assert (out[:, V:] == -7).all() and (out[rows:] == -7).all(), "written beside the logits"
+    want, mag = L.scaled_head(h, sh, w, sw)
+    _close(out[:rows, :V].double().cpu().numpy(), want, mag, K, kind)

@@ -663,3 +663,44 @@ def test_answers_that_overlap(sampler, bad, kind, V, scale):
         for a, b in zip(first, (c.grad, reward)):
             assert torch.equal(a.view(torch.int16 if a.dtype == torch.bfloat16 else torch.int32),
                                b.view(torch.int16 if b.dtype == torch.bfloat16 else torch.int32))
+
+
+@pytest.mark.parametrize("shape", [dict(n=9, V=7, kind="bf16", pad=1), dict(n=40, V=1000, kept=0.6, heat=True),
+                                   dict(n=300, V=3001, kind="bf16", kept=0.7, shift=3), dict(n=60, V=16001, banned=0.3),
+                                   dict(n=24, V=128000, kind="bf16", kept=0.8), dict(n=160, V=40961, kept=0.9, pad=1)],
+                         ids=_id)
+@pytest.mark.parametrize("mean", [False, True])
+def test_preference_loss_without_the_gradient(sampler, shape, mean):
+    """The outputs of the form with the gradient, bit for bit, and what the definition says."""
+    import torch
+
+    c = Rows(16, **shape)
+    lp = L.score(c.x, c.tokens, c.T, c.weight)["logprob"]
+    ref = (lp + 0.3 * c.rng.standard_normal(c.n)).astype(np.float32)
+    offsets = np.array([0, c.n // 3, c.n // 2, c.n // 2, c.n], np.int32)
+    reward = torch.full((4,), -7.0, device="cuda:0")
+    kw = dict(beta=0.4, margin=0.25, label_smoothing=0.1, mean_over_tokens=mean)
+    ins = dict(seq_offsets=torch.from_numpy(offsets).cuda(), ref_logprob=torch.from_numpy(ref).cuda(), out_loss=c.loss,
+               out_reward=reward, **kw, **c.kw())
+    sampler.preference_loss(out_grad=c.grad, **ins)
+    first = [t.clone() for t in (c.loss, reward, c.out["logprob"], c.status)]
+    for t in (c.loss, reward, c.out["logprob"]):
+        t.fill_(-7.0)
+    c.status.fill_(-7)
+    c.gflat.fill_(-7.0)
+    sampler.preference_loss(**ins)
+    for a, b in zip(first, (c.loss, reward, c.out["logprob"], c.status)):
+        assert torch.equal(a, b)
+    assert (c.gflat == -7.0).all()
+    got = L.preference(c.x, c.tokens, offsets, ref.astype(np.float64), c.T, c.weight, **kw)
+    tol = c.check_rows(got, entropy=False)
+    w = np.ones(c.n) if c.weight is None else c.weight.astype(np.float64)
+    t_reward = np.zeros(4)
+    for s in range(4):
+        at = slice(offsets[s], offsets[s + 1])
+        share = 1.0 / w[at].sum() if mean and w[at].sum() else 1.0
+        t_reward[s] = 0.4 * share * ((w * tol["logprob"])[at]).sum() + 2 * EPS * abs(got["reward"][s])
+    assert (np.abs(reward.double().cpu().numpy() - got["reward"]) <= t_reward).all()
+    # beta, the margin and the smoothing are floats; the loss has a slope of at most 1 in a margin
+    t_z = t_reward[0::2] + t_reward[1::2] + EPS * (np.abs(got["reward"]).max() + 1.25)
+    assert abs(c.loss.item() - got["loss"]) <= t_z.sum() / 2 + 4 * EPS * (1 + abs(got["loss"]))

@@ -83,3 +83,39 @@ def test_product_path_does_not_touch_the_oracle():
             if f.endswith((".py", ".cu", ".cuh", ".h", ".cpp")):
                 text = open(os.path.join(dirpath, f)).read()
                 assert "oracle" not in text.lower().replace("oracle-free", ""), f
+
+
+def test_struct_layouts_of_scoring_and_the_8bit_head(tmp_path):
+    import decode_step_token_gb300 as d
+    structs = [(name, getattr(d, name)) for name in ("sampler_rows_t", "sampler_policy_t", "sampler_preference_t",
+                                                     "sampler_quantize_t", "sampler_scaled_head_t")]
+    body = ["#include <stdio.h>", "#include <stddef.h>", '#include "sampler.h"', "int main(void){"]
+    want = []
+    for name, st in structs:
+        body.append(f'printf("%zu\\n", sizeof({name}));')
+        want.append(ctypes.sizeof(st))
+        for f in st._fields_:
+            body.append(f'printf("%zu\\n", offsetof({name}, {f[0]}));')
+            want.append(getattr(st, f[0]).offset)
+    body.append('printf("%d\\n%d\\n", SAMPLER_LOSS_MAX_ROWS, SAMPLER_ERR_BAD_VALUE);return 0;}')
+    want += [d.SAMPLER_LOSS_MAX_ROWS, d.SAMPLER_ERR_BAD_VALUE]
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text("\n".join(body))
+    subprocess.run(["gcc", f"-I{os.path.dirname(HEADER)}", str(src), "-o", str(exe)], check=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout
+    assert [int(x) for x in out.split()] == want
+
+
+def test_host_checks_of_scoring_and_the_8bit_head_without_a_gpu(lib):
+    """A NULL handle or argument is refused before any CUDA call."""
+    import decode_step_token_gb300 as d
+    b = d._binding
+    rows, none = d.sampler_rows_t(), None
+    assert b.sampler_score(none, rows, 0) == b.SAMPLER_ERR_NULL_ARG
+    assert b.sampler_score_grad(none, rows, 0, 0, 0) == b.SAMPLER_ERR_NULL_ARG
+    assert b.sampler_policy_loss(none, rows, d.sampler_policy_t(), 0) == b.SAMPLER_ERR_NULL_ARG
+    assert b.sampler_preference_loss(none, rows, d.sampler_preference_t(), 0) == b.SAMPLER_ERR_NULL_ARG
+    assert b.sampler_quantize_blocks(none, d.sampler_quantize_t(), 0) == b.SAMPLER_ERR_NULL_ARG
+    assert b.sampler_lm_head_scaled(none, d.sampler_scaled_head_t(), 0, 0, 1, 1, 1, 0) == b.SAMPLER_ERR_NULL_ARG
+    assert (b.sampler_lm_head_scaled_sample(none, d.sampler_scaled_head_t(), d.sampler_args_t(), none, 0)
+            == b.SAMPLER_ERR_NULL_ARG)

@@ -182,10 +182,13 @@ bool launch(sampler_quantize_t q, int sms, cudaStream_t stream)
     const bool vec_out = reinterpret_cast<uintptr_t>(q.values) % Elems<T>::kPer == 0 && q.values_stride % Elems<T>::kPer == 0;
     const int64_t across = (q.cols + 127) / 128;
     const bool square = q.block_rows == 128;
-    // one row a thread while that leaves the device unfilled, for its latency; else several loads in flight (bf16,
-    // x 4096, one / several: 64 rows 1.5 / 2.5 us, 600 rows 3.2 / 4.2, 1200 rows 5.0 / 5.3, 4096 rows 13.0 / 12.3,
-    // 32768 rows 88 / 72)
-    const bool few = !square && (q.rows + kRows - 1) / kRows * across <= int64_t(sms) * 8;
+    // one row a thread up to so many blocks of threads for each SM, for its latency; else several loads in flight. One
+    // row / several, from inputs not in L2: bf16 x 4096 64 rows 2.5 / 3.4 us, 600 3.7 / 4.7, 1200 5.5 / 5.9, 2400 9.2 /
+    // 9.2 (4800 blocks, 32 an SM), 3600 12.8 / 11.9, 8192 25.6 / 23.3; x 16384 300 rows 5.6 / 6.2, 600 9.2 / 9.2 (4864),
+    // 1200 15.9 / 14.7; fp32 x 4096 600 rows 5.1 / 6.3, 2400 13.9 / 15.1, 3600 19.9 / 20.3 (14400 blocks, 95 an SM),
+    // 4800 25.4 / 24.9; x 16384 900 rows 19.9 / 20.7 (14464), 1800 36.6 / 34.5
+    constexpr int kFewBlocks = sizeof(T) == 2 ? 32 : 96;
+    const bool few = !square && (q.rows + kRows - 1) / kRows * across <= int64_t(sms) * kFewBlocks;
     const int rows = square ? 128 : few ? kRows : 64;
     // the grid's second dimension is limited: taller matrices go in several launches
     const int64_t most = 65535LL * rows;

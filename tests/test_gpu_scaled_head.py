@@ -306,3 +306,25 @@ def test_logits_on_16_bytes(sampler, rows, V, K, pad, kind):
     assert (out[:, V:] == -7).all() and (out[rows:] == -7).all(), "written beside the logits"
     want, mag = L.scaled_head(h, sh, w, sw)
     _close(out[:rows, :V].double().cpu().numpy(), want, mag, K, kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols,pad", [(2500, 4100, 4), (4801, 4200, 0), (20000, 1000, 1)])
+def test_quantize_many_rows(sampler, rows, cols, pad, kind):
+    """Rows for which a thread takes several; a block is one row here, so some of the rows are compared."""
+    import torch
+
+    gen = torch.Generator(device="cuda:0").manual_seed(rows)
+    dt = torch.bfloat16 if kind == "bf16" else torch.float32
+    src = torch.randn((rows, cols + pad), generator=gen, device="cuda:0", dtype=dt)[:, :cols]
+    src[rows // 2, 300] = float("inf")
+    values = torch.full((rows, cols + pad), 0x55, dtype=torch.uint8, device="cuda:0")
+    scales = torch.empty((rows, -(-cols // 128)), device="cuda:0")
+    sampler.quantize_blocks(src=src, block_rows=1, out_values=values[:, :cols].view(torch.float8_e4m3fn),
+                            out_scales=scales)
+    at = np.unique(np.concatenate([np.arange(5), [rows // 2], np.arange(rows - 70, rows),
+                                   np.random.default_rng(0).integers(0, rows, 200)]))
+    codes, want = L.quantize(src[torch.from_numpy(at).cuda()].float().cpu().numpy(), 1)
+    np.testing.assert_array_equal(scales.cpu().numpy()[at], want)
+    np.testing.assert_array_equal(values[:, :cols].cpu().numpy()[at], codes)
+    assert (values[:, cols:] == 0x55).all(), "written beside the values"

@@ -19,7 +19,7 @@
 // latency) run under it.
 // Measured, policy loss with its gradient in bf16: 2048 x 128000 in 176 us, 5.9 TB/s
 // of logits and gradients (88 % of the copy rate); 2048 x 151936 in 210 us; one row
-// of 151936 in 8.9 us, which is launch, one part's way through memory and the join.
+// of 151936 in 8.6 us, which is launch, one part's way through memory and the join.
 // At 1024 x 128000 the DRAM is 62 % busy from cold caches and 58 % of the issue
 // slots are taken: the arithmetic of the two passes and the memory's latency share
 // the time. (fp32 rows, with half the elements to a byte, take 322 us at 2048 x

@@ -28,13 +28,18 @@
 // against 1.46 ms at 4096 x 128000 x 4096, and one tile of 256 rows where CTAs
 // alone have two (333 x 20011 x 1000: 41 against 30 us, with the stores as they were).
 //
-// Where the two meet (x 4096 where nothing is said, transposed / not): 16 x 128000
-// 86 / 107 us, 32 x 64000 53 / 49, 32 x 40000 x 1024 15 / 16, 33 x 128000 92 / 94,
-// 64 x 128000 94 / 95.5, 64 x 64000 57 / 51, 64 x 256000 x 1024 60 / 51, 96 x 128000
-// 121 / 97.
+// Where the two meet, transposed / not, a call at a time after 268 MB of writes: over 1 to 32 rows, seven
+// vocabularies of 4000 to 151936 and a K of 1024 and 4096, transposed is faster at
+// 81 of 84 sizes (17 x 4000 x 1024 6.1 / 7.6 us, 16 x 64000 x 4096 57 / 63, 32 x
+// 128000 x 4096 103 / 108) and up to 6 % slower at the others, all of 32 rows x 4096
+// (64000 56.9 / 53.8, 100000 90.2 / 86.2, 151936 116.9 / 115.8). Beyond, with a form
+// for up to 96 rows, call after call: 33 x 128000 x 4096 92 / 94, 64 x 128000 94 /
+// 95.5, 64 x 64000 57 / 51, 64 x 256000 x 1024 60 / 51, 96 x 128000 121 / 97. (What
+// decides at 32 rows and more is how the tiles fill the SMs in their last round.)
 //
-// Measured: 16 x 128000 x 4096 86 us (6.1 TB/s, 91 % of the copy rate); 4096 x
-// 128000 x 4096 1.46 ms, 2940 TFLOP/s.
+// Measured: 16 x 128000 x 4096 83-86 us (6.1-6.4 TB/s, 91-94 % of the copy rate); 4096 x
+// 128000 x 4096 1.46-1.49 ms call after call (2880-2940 TFLOP/s), 1.66-1.70 ms where
+// each call has inputs of its own that are not in L2 (2530-2590).
 //
 // Persistent, one CTA an SM; warp roles:
 //   warps 0-7  the epilogue: two groups of four warps, each a half of the tile's
@@ -583,8 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
                     }
                 } else {
                     __syncwarp();
-                    // eight rows' elements under way at once (one: 333 x 20011 x 1000 fp32 26.1 us, so 18.7;
-                    // two bf16 columns a lane on their 4-byte boundaries: 28 us where this takes 16.6, for the branches)
+                    // eight rows' elements under way at once (one: 333 x 20011 x 1000 fp32 26.1 us, so 18.7
+                    // from inputs in L2, 20.2 from others; two bf16 columns a lane on their 4-byte boundaries: 28 us
+                    // where this takes 16.6, for the branches)
                     const int rows = min(32, P.rows - row), cols = min(kBoxCols, P.V - v - c0);
                     T* g = static_cast<T*>(P.logits) + int64_t(row) * P.ldl + v + c0;
 #pragma unroll 8

@@ -374,8 +374,9 @@ int sampler_lm_head(sampler_t h, const sampler_lm_head_t* lm, void* logits, int6
  * their place SAMPLER_ROW_TIMEOUT for all rows of a part of the batch in which
  * an internal wait gave up. The outputs and the gradient of a row with one of
  * these are NaN, and so are a loss that it belongs to and the gradients of its
- * pair's rows; other rows keep theirs. A -inf logit is a token of no mass: its gradient is 0, and the logprob of a
- * token t with one is -inf.
+ * pair's rows; other rows keep theirs. A -inf logit is a token of no mass: it
+ * has a gradient of 0 where it is not t, and a logprob of -inf where it is (whose
+ * gradient is the one by the logprob, over T).
  *
  * The gradient of the logits, where asked, has the logits' type, each value
  * rounded once. out_grad may be the logits themselves (with the same stride):
@@ -547,7 +548,7 @@ const char* sampler_status_string(int code);
  *                            per-slice candidate lists could not settle (top-k
  *                            above 128, a top-p cut past the lists, too many
  *                            candidates), finished by its slower exact path.
- *   SAMPLER_STAT_LM_HEAD_TIMEOUTS  CTAs of the LM-head GEMM whose bounded wait
+ *   SAMPLER_STAT_LM_HEAD_TIMEOUTS  CTAs of an LM-head GEMM whose bounded wait
  *                            gave up (their logits were left unwritten).
  * Writes the count to *value and clears it when reset != 0. */
 enum { SAMPLER_STAT_EXACT_ROWS = 0, SAMPLER_STAT_LM_HEAD_TIMEOUTS = 1 };

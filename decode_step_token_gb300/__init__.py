@@ -22,7 +22,9 @@ from ._binding import (EXPORTED, SAMPLER_CREATE_HOST_STAGING, SAMPLER_CREATE_SHO
                        sampler_get_stat, SAMPLER_ERR_BAD_VALUE, SAMPLER_LOSS_MAX_ROWS, sampler_rows_t, sampler_policy_t,
                        sampler_preference_t, sampler_quantize_t, sampler_scaled_head_t, sampler_score,
                        sampler_score_grad, sampler_policy_loss, sampler_preference_loss, sampler_quantize_blocks,
-                       sampler_lm_head_scaled, sampler_lm_head_scaled_sample)
+                       sampler_lm_head_scaled, sampler_lm_head_scaled_sample, sampler_micro_t, sampler_micro_rows_t,
+                       sampler_micro_head_t, sampler_micro_scale_bytes, sampler_quantize_micro, sampler_micro_rows,
+                       sampler_lm_head_micro, sampler_lm_head_micro_sample)
 
 __all__ = ["Sampler", "SamplerError", "load_library", "sampler_create", "sampler_sample",
            "sampler_sample_host", "sampler_sample_noalloc", "sampler_sample_ex", "sampler_destroy",
@@ -33,7 +35,9 @@ __all__ = ["Sampler", "SamplerError", "load_library", "sampler_create", "sampler
            "SAMPLER_ERR_BAD_VALUE", "SAMPLER_LOSS_MAX_ROWS", "sampler_rows_t", "sampler_policy_t", "sampler_preference_t",
            "sampler_quantize_t", "sampler_scaled_head_t", "sampler_score", "sampler_score_grad",
            "sampler_policy_loss", "sampler_preference_loss", "sampler_quantize_blocks", "sampler_lm_head_scaled",
-           "sampler_lm_head_scaled_sample"]
+           "sampler_lm_head_scaled_sample", "sampler_micro_t", "sampler_micro_rows_t", "sampler_micro_head_t",
+           "sampler_micro_scale_bytes", "sampler_quantize_micro", "sampler_micro_rows", "sampler_lm_head_micro",
+           "sampler_lm_head_micro_sample"]
 
 
 def _make_ext(top_n: int = 0, unscaled: bool = False, out_token_logprob=None, out_top_ids=None,
@@ -86,6 +90,32 @@ def _torch_types():
         import torch
         _types = (torch.bfloat16, torch.float32, torch.int32, (torch.float8_e4m3fn, torch.uint8))
     return _types
+
+
+_micro = None
+
+
+def _micro_types():
+    """(those of two 4-bit values, those of their blocks' scales) of torch, as far as it has them, and bytes."""
+    global _micro
+    if _micro is None:
+        import torch
+        named = lambda *names: tuple(getattr(torch, n) for n in names if hasattr(torch, n))  # noqa: E731
+        _micro = (named("uint8", "float4_e2m1fn_x2"), named("uint8", "float8_e4m3fn", "float8_e8m0fnu"))
+    return _micro
+
+
+def _scales(name: str, t, rows: int, cols: int, block: int, device: int) -> int:
+    """Address of the scales of a matrix in 4 bits."""
+    need = sampler_micro_scale_bytes(rows, cols, block)
+    if need < 0:
+        raise ValueError(f"{name}: no scales for blocks of {block} in {rows} x {cols}")
+    if t.dtype not in _micro_types()[1]:
+        raise TypeError(f"{name} must be one of {_micro_types()[1]}, not {t.dtype}")
+    _on_device(name, t, device)
+    if not t.is_contiguous() or t.numel() < need:
+        raise ValueError(f"{name} must be {need} contiguous bytes, not {tuple(t.shape)}")
+    return t.data_ptr()
 
 
 def _vector(name: str, t, n: int, dtype, device: int) -> Optional[int]:
@@ -406,6 +436,97 @@ class Sampler:
         ext = _make_ext(**ext_kw) if ext_kw else None
         self._done(sampler_lm_head_scaled_sample(self._h, lm, args, ext, self._stream(stream)),
                    "sampler_lm_head_scaled_sample")
+
+    @staticmethod
+    def micro_scale_bytes(rows: int, cols: int, block: int = 16) -> int:
+        """Bytes of the scales of a [rows, cols] matrix in 4 bits."""
+        n = sampler_micro_scale_bytes(rows, cols, block)
+        if n < 0:
+            raise ValueError(f"no scales for blocks of {block} in {rows} x {cols}")
+        return n
+
+    def quantize_micro(self, *, src, out_values, out_scales, out_row_scale, block: int = 16,
+                       stream: Optional[int] = None) -> None:
+        """sampler_quantize_micro: src [rows, cols] (bf16 or fp32) to out_values (bytes
+        of two 4-bit values, [rows, cols / 2] rounded up) with out_scales
+        (``micro_scale_bytes``) and out_row_scale (fp32 [rows])."""
+        bf16, f32, _, _ = _torch_types()
+        dev = self.device
+        rows, cols, stride = _matrix("src", src, (bf16, f32), dev)
+        vr, vc, vs = _matrix("out_values", out_values, _micro_types()[0], dev)
+        if vr != rows or vc != (cols + 1) // 2:
+            raise ValueError(f"out_values must be [{rows}, {(cols + 1) // 2}], not {tuple(out_values.shape)}")
+        q = sampler_micro_t(src.data_ptr(), SAMPLER_DTYPE_BF16 if src.dtype is bf16 else SAMPLER_DTYPE_F32, rows, cols,
+                            stride, block, out_values.data_ptr(), vs,
+                            _scales("out_scales", out_scales, rows, cols, block, dev),
+                            _vector("out_row_scale", out_row_scale, rows, f32, dev))
+        self._done(sampler_quantize_micro(self._h, q, self._stream(stream)), "sampler_quantize_micro")
+
+    def micro_rows(self, *, values, scales, out, row_scale=None, ids=None, block: int = 16,
+                   stream: Optional[int] = None) -> None:
+        """sampler_micro_rows: rows of a matrix that ``quantize_micro`` has laid out back
+        into out [n, cols] (bf16 or fp32): the rows that ids (int32 [n]) names, or the
+        first n."""
+        bf16, f32, i32, _ = _torch_types()
+        dev = self.device
+        rows, vc, vs = _matrix("values", values, _micro_types()[0], dev)
+        n, cols, stride = _matrix("out", out, (bf16, f32), dev)
+        if vc != (cols + 1) // 2:
+            raise ValueError(f"out has {cols} columns, values has bytes for {2 * vc}")
+        q = sampler_micro_rows_t(values.data_ptr(), vs, _scales("scales", scales, rows, cols, block, dev),
+                                 _vector("row_scale", row_scale, rows, f32, dev), rows, cols, block,
+                                 _vector("ids", ids, n, i32, dev), n, out.data_ptr(),
+                                 SAMPLER_DTYPE_BF16 if out.dtype is bf16 else SAMPLER_DTYPE_F32, stride)
+        self._done(sampler_micro_rows(self._h, q, self._stream(stream)), "sampler_micro_rows")
+
+    def _micro_head(self, hidden, hidden_scale, weight, weight_scale, hidden_dim, hidden_row_scale, weight_row_scale,
+                    block) -> sampler_micro_head_t:
+        dev, f32, four = self.device, _torch_types()[1], _micro_types()[0]
+        rows, hb, hs = _matrix("hidden", hidden, four, dev)
+        V, wb, ws = _matrix("weight", weight, four, dev)
+        K = 2 * hb if hidden_dim is None else int(hidden_dim)
+        if hb != (K + 1) // 2 or wb != (K + 1) // 2:
+            raise ValueError(f"hidden and weight must have {(K + 1) // 2} bytes a row, not {hb} and {wb}")
+        # the stride of a single row is not used, but has to be a legal one
+        if rows <= 1:
+            hs = -(-hs // 16) * 16
+        if V <= 1:
+            ws = -(-ws // 16) * 16
+        return sampler_micro_head_t(hidden.data_ptr(), _scales("hidden_scale", hidden_scale, rows, K, block, dev),
+                                    _vector("hidden_row_scale", hidden_row_scale, rows, f32, dev), weight.data_ptr(),
+                                    _scales("weight_scale", weight_scale, V, K, block, dev),
+                                    _vector("weight_row_scale", weight_row_scale, V, f32, dev), K, hs, ws, block)
+
+    def lm_head_micro(self, *, hidden, hidden_scale, weight, weight_scale, logits, hidden_dim: Optional[int] = None,
+                      hidden_row_scale=None, weight_row_scale=None, block: int = 16,
+                      stream: Optional[int] = None) -> None:
+        """sampler_lm_head_micro: logits [rows, >= vocab] (bf16 or fp32) from hidden [rows,
+        K / 2] and weight [vocab, K / 2] in 4 bits with their scales, as
+        ``quantize_micro`` makes them. hidden_dim: K, where it is odd."""
+        lm = self._micro_head(hidden, hidden_scale, weight, weight_scale, hidden_dim, hidden_row_scale, weight_row_scale,
+                              block)
+        bf16, f32, _, _ = _torch_types()
+        lr, lc, ldl = _matrix("logits", logits, (bf16, f32), self.device)
+        rows, V = hidden.shape[0], weight.shape[0]
+        if lr < rows or lc < V:
+            raise ValueError(f"logits must be [{rows}, {V}], not {tuple(logits.shape)}")
+        dtype = SAMPLER_DTYPE_BF16 if logits.dtype is bf16 else SAMPLER_DTYPE_F32
+        self._done(sampler_lm_head_micro(self._h, lm, logits.data_ptr(), dtype, ldl, rows, V, self._stream(stream)),
+                   "sampler_lm_head_micro")
+
+    def lm_head_micro_sample_args(self, args: sampler_args_t, *, hidden, hidden_scale, weight, weight_scale,
+                                  hidden_dim: Optional[int] = None, hidden_row_scale=None, weight_row_scale=None,
+                                  block: int = 16, stream: Optional[int] = None, **ext_kw) -> None:
+        """sampler_lm_head_micro_sample: the logits of ``lm_head_micro`` written to
+        args.logits, then the step on them; ext_kw as for sample_ex_args."""
+        lm = self._micro_head(hidden, hidden_scale, weight, weight_scale, hidden_dim, hidden_row_scale, weight_row_scale,
+                              block)
+        rows = args.n_logit_rows if args.n_logit_rows > 0 else args.n_rows
+        if hidden.shape[0] < rows or weight.shape[0] < args.vocab:
+            raise ValueError(f"hidden and weight must have {rows} and {args.vocab} rows")
+        ext = _make_ext(**ext_kw) if ext_kw else None
+        self._done(sampler_lm_head_micro_sample(self._h, lm, args, ext, self._stream(stream)),
+                   "sampler_lm_head_micro_sample")
 
     def _stream(self, stream: Optional[int]) -> int:
         return _current_stream(self.device) if stream is None else stream

@@ -41,7 +41,9 @@ EXPORTED = ("sampler_create", "sampler_sample", "sampler_sample_host", "sampler_
             "sampler_status_string", "sampler_abi_version", "sampler_get_stat",
             "sampler_sample_noalloc", "sampler_sample_ex", "sampler_lm_head_sample", "sampler_lm_head",
             "sampler_score", "sampler_score_grad", "sampler_policy_loss", "sampler_preference_loss",
-            "sampler_quantize_blocks", "sampler_lm_head_scaled", "sampler_lm_head_scaled_sample")
+            "sampler_quantize_blocks", "sampler_lm_head_scaled", "sampler_lm_head_scaled_sample",
+            "sampler_micro_scale_bytes", "sampler_quantize_micro", "sampler_micro_rows", "sampler_lm_head_micro",
+            "sampler_lm_head_micro_sample")
 SAMPLER_STAT_EXACT_ROWS = 0
 SAMPLER_STAT_LM_HEAD_TIMEOUTS = 1
 SAMPLER_LM_HEAD_MAX_ROWS = 256
@@ -205,6 +207,53 @@ class sampler_scaled_head_t(ctypes.Structure):
     ]
 
 
+class sampler_micro_t(ctypes.Structure):
+    _fields_ = [
+        ("src", _P),
+        ("dtype", ctypes.c_int32),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("src_stride", ctypes.c_int64),
+        ("block", ctypes.c_int32),
+        ("values", _P),
+        ("values_stride", ctypes.c_int64),
+        ("scales", _P),
+        ("row_scale", _P),
+    ]
+
+
+class sampler_micro_rows_t(ctypes.Structure):
+    _fields_ = [
+        ("values", _P),
+        ("values_stride", ctypes.c_int64),
+        ("scales", _P),
+        ("row_scale", _P),
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("block", ctypes.c_int32),
+        ("ids", _P),
+        ("n", ctypes.c_int64),
+        ("out", _P),
+        ("dtype", ctypes.c_int32),
+        ("out_stride", ctypes.c_int64),
+    ]
+
+
+class sampler_micro_head_t(ctypes.Structure):
+    _fields_ = [
+        ("hidden", _P),
+        ("hidden_scale", _P),
+        ("hidden_row_scale", _P),
+        ("weight", _P),
+        ("weight_scale", _P),
+        ("weight_row_scale", _P),
+        ("hidden_dim", ctypes.c_int64),
+        ("hidden_stride", ctypes.c_int64),
+        ("weight_stride", ctypes.c_int64),
+        ("block", ctypes.c_int32),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -260,6 +309,19 @@ def load_library(path: str = LIB):
                                                           ctypes.POINTER(sampler_args_t),
                                                           ctypes.POINTER(sampler_ext_t), _P]
             lib.sampler_lm_head_scaled_sample.restype = ctypes.c_int
+            lib.sampler_micro_scale_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32]
+            lib.sampler_micro_scale_bytes.restype = ctypes.c_int64
+            lib.sampler_quantize_micro.argtypes = [_P, ctypes.POINTER(sampler_micro_t), _P]
+            lib.sampler_quantize_micro.restype = ctypes.c_int
+            lib.sampler_micro_rows.argtypes = [_P, ctypes.POINTER(sampler_micro_rows_t), _P]
+            lib.sampler_micro_rows.restype = ctypes.c_int
+            lib.sampler_lm_head_micro.argtypes = [_P, ctypes.POINTER(sampler_micro_head_t), _P, ctypes.c_int32,
+                                                  ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, _P]
+            lib.sampler_lm_head_micro.restype = ctypes.c_int
+            lib.sampler_lm_head_micro_sample.argtypes = [_P, ctypes.POINTER(sampler_micro_head_t),
+                                                         ctypes.POINTER(sampler_args_t),
+                                                         ctypes.POINTER(sampler_ext_t), _P]
+            lib.sampler_lm_head_micro_sample.restype = ctypes.c_int
             lib.sampler_abi_version.argtypes = []
             lib.sampler_abi_version.restype = ctypes.c_uint32
             _lib = lib
@@ -350,3 +412,27 @@ def sampler_lm_head_scaled_sample(h, lm: sampler_scaled_head_t, args: sampler_ar
     """ext: a sampler_ext_t or None."""
     return load_library().sampler_lm_head_scaled_sample(h, ctypes.byref(lm), ctypes.byref(args),
                                                         ctypes.byref(ext) if ext is not None else None, _P(stream))
+
+
+def sampler_micro_scale_bytes(rows: int, cols: int, block: int) -> int:
+    return int(load_library().sampler_micro_scale_bytes(rows, cols, block))
+
+
+def sampler_quantize_micro(h, q: sampler_micro_t, stream: int) -> int:
+    return load_library().sampler_quantize_micro(h, ctypes.byref(q), _P(stream))
+
+
+def sampler_micro_rows(h, q: sampler_micro_rows_t, stream: int) -> int:
+    return load_library().sampler_micro_rows(h, ctypes.byref(q), _P(stream))
+
+
+def sampler_lm_head_micro(h, lm: sampler_micro_head_t, logits: int, dtype: int, logits_stride: int, rows: int, vocab: int,
+                          stream: int) -> int:
+    return load_library().sampler_lm_head_micro(h, ctypes.byref(lm), _P(logits), dtype, logits_stride, rows, vocab,
+                                                _P(stream))
+
+
+def sampler_lm_head_micro_sample(h, lm: sampler_micro_head_t, args: sampler_args_t, ext, stream: int) -> int:
+    """ext: a sampler_ext_t or None."""
+    return load_library().sampler_lm_head_micro_sample(h, ctypes.byref(lm), ctypes.byref(args),
+                                                       ctypes.byref(ext) if ext is not None else None, _P(stream))

@@ -31,6 +31,7 @@ struct sampler_s {
     dst::RowWorkspace row_ws;  // the losses: one record per row, and a launch's ticket
     dst::RowOccupancy row_occ;
     dst::ScaledHeadGrants head_grants;
+    dst::MicroHeadGrants micro_grants;
     // staging for sampler_sample_host
     unsigned char* stage_base;
     size_t stage_bytes;

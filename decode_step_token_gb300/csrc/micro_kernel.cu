@@ -1,0 +1,415 @@
+// micro_kernel.cu -- rows to microscaled 4 bits (e2m1 values with a scale for each
+// block of 16 or 32) and back.
+//
+// Every step is exact or one rounding, so that the codes follow from the
+// definition bit for bit: the row's scale is a power of two, a block's scale has
+// at most four digits, and a quotient is the correctly rounded one. (A product
+// with the rounded reciprocal would put many of the quotients that lie halfway
+// between two codes on the wrong side: bf16 values over a scale of four digits
+// often do.)
+//
+// A block's codes need the block's largest magnitude and, for blocks of 16, the
+// row's, so a row stays in registers: 16 neighbouring values in each thread, one
+// to four times, 4 to 256 threads to a row. Rows of more than 16384 values are
+// read twice where the row's largest is needed.
+// Scales are laid out as the tensor cores take them: 512 bytes for 128 rows by 4
+// blocks, (row % 32) * 16 + (row / 32 % 4) * 4 + block % 4. The four bytes of a
+// row are stored as one word.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "launch.h"
+
+namespace dst {
+namespace micro {
+
+constexpr int kThreads = 256;
+constexpr int kPer = 16;                     // values of a thread
+constexpr float kLeast = 7.888609052e-31f;   // 2^-100: keeps a row's scale and its quotients normal
+constexpr uint32_t kInf = 0x7f800000u;
+
+__device__ __forceinline__ float power(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+// The exponent of the least power of two p with m <= f p, from the bits of m, for an f of 1 to 2 with the mantissa
+// bits `f`.
+__device__ __forceinline__ int least_power(uint32_t m, uint32_t f)
+{
+    return int(m >> 23) - 127 + ((m & 0x7fffffu) > f ? 1 : 0);
+}
+
+// Eight values to eight codes, the first in the lowest four bits; ties to even, beyond 6 to 6.
+__device__ __forceinline__ uint32_t codes8(const float* x)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+
+// A value to its e4m3 code, and that code's value.
+__device__ __forceinline__ uint32_t e4m3_code(float x)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(0.f), "f"(x));
+    return r & 0xffu;
+}
+
+__device__ __forceinline__ float e4m3_value(uint32_t code)
+{
+    float y;
+    asm("{\n\t.reg .b32 w;\n\t.reg .b16 lo, hi;\n\tcvt.rn.f16x2.e4m3x2 w, %1;\n\tmov.b32 {lo, hi}, w;\n\t"
+        "cvt.f32.f16 %0, lo;\n\t}"
+        : "=f"(y)
+        : "h"(uint16_t(code)));
+    return y;
+}
+
+// The value of a block's scale; the codes 0x7f (blocks of 16) and 0xff (of 32) are NaN.
+template <int kBlock>
+__device__ __forceinline__ float scale_value(uint32_t code)
+{
+    if (kBlock == 16) return e4m3_value(code);
+    if (code == 0xffu) return __int_as_float(0x7fc00000);
+    return code == 0u ? __int_as_float(0x00400000) : __int_as_float(code << 23);
+}
+
+template <typename T>
+__device__ __forceinline__ void load16(float (&x)[kPer], const T* p, int count, bool vec);
+
+template <>
+__device__ __forceinline__ void load16<float>(float (&x)[kPer], const float* p, int count, bool vec)
+{
+    if (vec && count == kPer) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 v = __ldg(reinterpret_cast<const float4*>(p) + j);
+            x[4 * j] = v.x;
+            x[4 * j + 1] = v.y;
+            x[4 * j + 2] = v.z;
+            x[4 * j + 3] = v.w;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) x[j] = j < count ? p[j] : 0.f;
+    }
+}
+
+template <>
+__device__ __forceinline__ void load16<uint16_t>(float (&x)[kPer], const uint16_t* p, int count, bool vec)
+{
+    if (vec && count == kPer) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + j);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[8 * j + 2 * k] = __uint_as_float(w[k] << 16);
+                x[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) x[j] = j < count ? __uint_as_float(uint32_t(p[j]) << 16) : 0.f;
+    }
+}
+
+// The largest magnitude of 16 values as bits: kInf or more where one is not finite.
+__device__ __forceinline__ uint32_t largest(const float (&x)[kPer])
+{
+    uint32_t m = 0u;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
+    return m;
+}
+
+// What a call's shape makes of it. group: threads to a row.
+struct Plan {
+    int group, chunks, tiles;  // chunks of 16 values, and tiles of scales, in a row
+    int64_t padded;            // rows, rounded up to whole tiles
+    bool vec_in, vec_out;
+};
+
+// The codes of one chunk and its block's scale code, given the block's largest magnitude and (blocks of 16) the row's
+// scale 2^g.
+template <int kBlock>
+__device__ __forceinline__ uint2 encode(const float (&x)[kPer], uint32_t most, int g, uint32_t& code)
+{
+    float q[kPer];
+    const bool finite = most < kInf;
+    if (kBlock == 32) {
+        const int e = max(least_power(most, 0x400000u) - 2, -127);  // m <= 1.5 * 4 * 2^e
+        code = finite ? uint32_t(e + 127) : 0xffu;
+        const float up = power(-max(min(e, 126), -127));  // its reciprocal: a product with it is exact
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) q[j] = x[j] * up;
+    } else {
+        code = finite ? e4m3_code(__fdiv_rn(__uint_as_float(most), 6.f) * power(-g)) : 0x7fu;
+        const float unit = (finite ? e4m3_value(code) : 0.f) * power(g);
+        const float inv = unit > 0.f ? __fdiv_rn(1.f, unit) : 0.f;
+        // the quotient, correctly rounded: the product with the rounded reciprocal and one step on its remainder
+        // (Markstein)
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const float y = x[j] * inv;
+            q[j] = fmaf(fmaf(-y, unit, x[j]), inv, y);
+        }
+    }
+    const uint32_t keep = finite ? 0xffffffffu : 0u;
+    return make_uint2(codes8(q) & keep, codes8(q + 8) & keep);
+}
+
+// Store a chunk's codes: 8 bytes where they lie so, else the `bytes` that belong to the row.
+__device__ __forceinline__ void put_codes(uint8_t* to, uint2 c, int bytes, bool vec)
+{
+    if (vec && bytes == 8) {
+        *reinterpret_cast<uint2*>(to) = c;
+    } else {
+        const uint64_t w = uint64_t(c.y) << 32 | c.x;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < bytes) to[j] = uint8_t(w >> 8 * j);
+    }
+}
+
+__device__ __forceinline__ int64_t scale_word(int64_t row, int tile, int tiles)
+{
+    return (row / 128 * tiles + tile) * 128 + (row % 32) * 4 + row / 32 % 4;
+}
+
+// kChunks: of a thread, in registers; 0: any number, read twice where blocks are of 16.
+template <typename T, int kBlock, int kChunks>
+__global__ void __launch_bounds__(kThreads) quantize_kernel(const sampler_micro_t q, const Plan plan)
+{
+    constexpr int kHeld = kChunks ? kChunks : 1;
+    constexpr int kOfTile = 4 * kBlock / kPer;  // chunks that one word of scales belongs to
+    const int group = plan.group, t = threadIdx.x & (group - 1);
+    const int64_t row = int64_t(blockIdx.x) * (kThreads / group) + threadIdx.x / group;
+    const bool in = row < q.rows;
+    const T* src = static_cast<const T*>(q.src) + (in ? row * q.src_stride : 0);
+    uint32_t* words = static_cast<uint32_t*>(q.scales);
+    float x[kHeld][kPer];
+    auto load = [&](int k, int chunk) {
+        const int64_t left = in ? q.cols - int64_t(chunk) * kPer : 0;
+        load16<T>(x[k], src + int64_t(chunk) * kPer, int(max(int64_t(0), min(int64_t(kPer), left))), plan.vec_in);
+    };
+    int g = 0;
+    uint32_t most[kHeld];
+    if (kChunks) {
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) load(k, t + k * group);
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) {
+            most[k] = largest(x[k]);
+            if (kBlock == 32) most[k] = max(most[k], __shfl_xor_sync(0xffffffffu, most[k], 1));
+        }
+    }
+    if (kBlock == 16) {
+        // the row's largest, of its blocks without a NaN or an infinity
+        __shared__ uint32_t part[kThreads / 32];
+        uint32_t m = __float_as_uint(kLeast);
+        if (kChunks) {
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) m = max(m, most[k] < kInf ? most[k] : 0u);
+        } else {
+            for (int chunk = t; chunk < plan.chunks; chunk += group) {
+                load(0, chunk);
+                const uint32_t n = largest(x[0]);
+                m = max(m, n < kInf ? n : 0u);
+            }
+        }
+        for (int o = min(group, 32) / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (group > 32) {
+            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+            __syncthreads();
+            const int first = threadIdx.x / group * (group / 32);
+            for (int w = 0; w < group / 32; ++w) m = max(m, part[first + w]);
+        }
+        g = least_power(m, 0x280000u) - 11;  // m <= 448 * 6 * 2^g = 1.3125 * 2^11 * 2^g
+        if (in && t == 0) q.row_scale[row] = power(g);
+    } else if (in && t == 0) {
+        q.row_scale[row] = 1.f;
+    }
+    auto finish = [&](int k, int chunk, uint32_t m) {
+        uint32_t code;
+        const uint2 c = encode<kBlock>(x[k], m, g, code);
+        const bool there = in && chunk < plan.chunks;
+        if (there) {
+            const int64_t bytes = (q.cols + 1) / 2 - int64_t(chunk) * 8;
+            put_codes(static_cast<uint8_t*>(q.values) + row * q.values_stride + int64_t(chunk) * 8, c,
+                      int(min(int64_t(8), bytes)), plan.vec_out);
+        }
+        // the word of a row's four blocks, from the threads that have them; scales that belong to no block are 0
+        uint32_t w = there ? code << 8 * (chunk * kPer / kBlock & 3) : 0u;
+#pragma unroll
+        for (int o = kOfTile / 2; o > 0; o >>= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
+        const int tile = chunk / kOfTile;
+        if (t % kOfTile == 0 && tile < plan.tiles && row < plan.padded) words[scale_word(row, tile, plan.tiles)] = w;
+    };
+    if (kChunks) {
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k) finish(k, t + k * group, most[k]);
+    } else {
+        // all threads of a row (256) take as many turns
+        for (int first = 0; first < plan.chunks; first += group) {
+            load(0, first + t);
+            uint32_t m = largest(x[0]);
+            if (kBlock == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            finish(0, first + t, m);
+        }
+    }
+}
+
+template <typename T, int kBlock>
+cudaError_t launch_quantize(const sampler_micro_t& q, cudaStream_t stream)
+{
+    Plan p;
+    const int64_t chunks = (q.cols + kPer - 1) / kPer;
+    p.chunks = int(chunks);
+    p.tiles = int(((q.cols + kBlock - 1) / kBlock + 3) / 4);
+    p.padded = (q.rows + 127) / 128 * 128;
+    p.vec_in = reinterpret_cast<uintptr_t>(q.src) % 16 == 0 && q.src_stride * int64_t(sizeof(T)) % 16 == 0;
+    p.vec_out = reinterpret_cast<uintptr_t>(q.values) % 8 == 0 && q.values_stride % 8 == 0;
+    p.group = 8;
+    while (p.group < kThreads && p.group < chunks) p.group *= 2;
+    const int held = chunks <= p.group ? 1 : chunks <= 2 * kThreads ? 2 : chunks <= 4 * kThreads ? 4 : 0;
+    const int64_t per = kThreads / p.group;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned((p.padded + per - 1) / per));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    const auto kernel = held == 1   ? quantize_kernel<T, kBlock, 1>
+                        : held == 2 ? quantize_kernel<T, kBlock, 2>
+                        : held == 4 ? quantize_kernel<T, kBlock, 4>
+                                    : quantize_kernel<T, kBlock, 0>;
+    return cudaLaunchKernelEx(&cfg, kernel, q, p);
+}
+
+// ---------------------------------------------------------------- reading back
+// Two codes of a byte to two values, exactly.
+__device__ __forceinline__ float2 values2(uint32_t byte)
+{
+    float2 y;
+    asm("{\n\t.reg .b8 c;\n\t.reg .b32 w;\n\t.reg .b16 lo, hi, s;\n\tcvt.u16.u32 s, %2;\n\tcvt.u8.u16 c, s;\n\t"
+        "cvt.rn.f16x2.e2m1x2 w, c;\n\tmov.b32 {lo, hi}, w;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+        : "=f"(y.x), "=f"(y.y)
+        : "r"(byte));
+    return y;
+}
+
+template <typename T>
+struct Out;
+template <>
+struct Out<float> {
+    static constexpr int kVec = 4;
+    static __device__ __forceinline__ uint4 pack(const float* x)
+    {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+};
+template <>
+struct Out<uint16_t> {
+    static constexpr int kVec = 8;
+    static __device__ __forceinline__ uint4 pack(const float* x)
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[j]) : "f"(x[2 * j + 1]), "f"(x[2 * j]));
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+
+// One 16-byte vector of a row in each thread, `group` of them side by side.
+template <typename T, int kBlock>
+__global__ void __launch_bounds__(kThreads) rows_kernel(const sampler_micro_rows_t q, int group, int vectors, int tiles,
+                                                        bool vec_in, bool vec_out)
+{
+    constexpr int kVec = Out<T>::kVec;
+    const int64_t r = int64_t(blockIdx.x) * (kThreads / group) + threadIdx.x / group;
+    const int i = int(blockIdx.y) * group + (threadIdx.x & (group - 1));
+    if (r >= q.n || i >= vectors) return;
+    const int64_t row = q.ids ? int64_t(q.ids[r]) : r;
+    const int64_t col = int64_t(i) * kVec;
+    const int count = int(min(int64_t(kVec), q.cols - col));
+    float x[kVec];
+    if (row < 0 || row >= q.rows) {
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) x[j] = __int_as_float(0x7fc00000);
+    } else {
+        const uint8_t* v = static_cast<const uint8_t*>(q.values) + row * q.values_stride + col / 2;
+        uint32_t codes = 0u;
+        if (vec_in && count == kVec) {
+            codes = kVec == 8 ? *reinterpret_cast<const uint32_t*>(v) : *reinterpret_cast<const uint16_t*>(v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVec / 2; ++j)
+                if (2 * j < count) codes |= uint32_t(v[j]) << 8 * j;
+        }
+        const int b = int(col / kBlock);
+        const uint32_t code = static_cast<const uint8_t*>(q.scales)[scale_word(row, b / 4, tiles) * 4 + b % 4];
+        const float unit = scale_value<kBlock>(code) * (q.row_scale ? q.row_scale[row] : 1.f);
+#pragma unroll
+        for (int j = 0; j < kVec; j += 2) {
+            const float2 y = values2(codes >> 4 * j & 0xffu);
+            x[j] = y.x * unit;
+            x[j + 1] = y.y * unit;
+        }
+    }
+    T* to = static_cast<T*>(q.out) + r * q.out_stride + col;
+    const uint4 y = Out<T>::pack(x);
+    if (vec_out && count == kVec) {
+        *reinterpret_cast<uint4*>(to) = y;
+    } else {
+        const T* e = reinterpret_cast<const T*>(&y);
+#pragma unroll
+        for (int j = 0; j < kVec; ++j)
+            if (j < count) to[j] = e[j];
+    }
+}
+
+template <typename T, int kBlock>
+cudaError_t launch_rows(const sampler_micro_rows_t& q, cudaStream_t stream)
+{
+    constexpr int kVec = Out<T>::kVec;
+    const int64_t vectors = (q.cols + kVec - 1) / kVec;
+    int group = 8;
+    while (group < kThreads && group < vectors) group *= 2;
+    const bool vec_in = reinterpret_cast<uintptr_t>(q.values) % (kVec / 2) == 0 && q.values_stride % (kVec / 2) == 0;
+    const bool vec_out = reinterpret_cast<uintptr_t>(q.out) % 16 == 0 && q.out_stride * int64_t(sizeof(T)) % 16 == 0;
+    const int64_t per = kThreads / group;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(unsigned((q.n + per - 1) / per), unsigned((vectors + group - 1) / group));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    const int tiles = int(((q.cols + kBlock - 1) / kBlock + 3) / 4);
+    return cudaLaunchKernelEx(&cfg, rows_kernel<T, kBlock>, q, group, int(vectors), tiles, vec_in, vec_out);
+}
+
+}  // namespace micro
+
+int micro_quantize_launch(const sampler_micro_t& q, cudaStream_t stream)
+{
+    using namespace micro;
+    const bool bf16 = q.dtype == SAMPLER_DTYPE_BF16;
+    const cudaError_t e = q.block == 16 ? bf16 ? launch_quantize<uint16_t, 16>(q, stream) : launch_quantize<float, 16>(q, stream)
+                          : bf16        ? launch_quantize<uint16_t, 32>(q, stream)
+                                        : launch_quantize<float, 32>(q, stream);
+    return e == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
+}
+
+int micro_rows_launch(const sampler_micro_rows_t& q, cudaStream_t stream)
+{
+    using namespace micro;
+    const bool bf16 = q.dtype == SAMPLER_DTYPE_BF16;
+    const cudaError_t e = q.block == 16 ? bf16 ? launch_rows<uint16_t, 16>(q, stream) : launch_rows<float, 16>(q, stream)
+                          : bf16        ? launch_rows<uint16_t, 32>(q, stream)
+                                        : launch_rows<float, 32>(q, stream);
+    return e == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
+}
+
+}  // namespace dst

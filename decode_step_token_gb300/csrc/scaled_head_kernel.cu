@@ -50,17 +50,15 @@
 // epilogue's where those hold 128 sums a thread (more rows).
 // Every wait is bounded in time, with one answer for a warp; a CTA whose wait gives up counts itself in the
 // handle's statistics and leaves its logits unwritten.
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cstring>
-#include <mutex>
 
 #include "launch.h"
 #include "ptx.cuh"
+#include "tensor_core.cuh"
 #include "warp_wait.cuh"
 
 namespace dst {
@@ -80,7 +78,6 @@ constexpr int kWideN = 256;                    // weight rows of a tile of many 
 constexpr int kWideAccs = kTmemCols / kWideN;
 constexpr uint32_t kWideBytes = kWideN * kBK; // of a stage
 constexpr int kLoad = 16;                      // columns that a thread reads at once (32: registers spill, 2264 TFLOP/s)
-constexpr uint32_t kBoxBytes = 32 * 128;       // a box of logits: 32 rows of 128 bytes, swizzled
 constexpr uint32_t kOutBytes = 8 * kBoxBytes;  // one for each warp of the epilogue: with more, a stage less
 constexpr int kScaleBlocks = 4;                // blocks of K whose scales are fetched together
 constexpr uint32_t kABytes = kBM * kBK;        // 16 KB a stage
@@ -110,27 +107,10 @@ struct Params {
 
 using Ring = RingPlace;
 
-// K-major tile in the 128-byte swizzled layout that the TMA engine writes: 8-row
-// atoms 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_sw128(uint32_t addr)
-{
-    return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
-           (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-
 // kind::f8f6f4, fp32 accumulator, e4m3 A and B (type 0 each), both K-major.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N)
 {
     return (1u << 4) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
-        "[%4];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
-        : "memory");
 }
 
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
@@ -140,47 +120,6 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
         "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
         : "memory");
-}
-
-__device__ __forceinline__ void mma_commit(uint64_t* bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src)
-{
-    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(x), "r"(y), "r"(src)
-                 : "memory");
-}
-
-__device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 16 consecutive columns of this thread's tensor-memory lane; complete after tmem_wait.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
-
-__device__ __forceinline__ void tmem_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-// Passes 16 loaded registers through, after tmem_wait: what uses them is not moved ahead of it.
-__device__ __forceinline__ void tmem_take16(uint32_t* r)
-{
-    asm volatile(""
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
 }
 
 // (a, b) += (x, y) * (p, q), two fp32 operations in one.
@@ -460,13 +399,6 @@ __global__ void __launch_bounds__(kThreads, 1) few_rows_kernel(const __grid_cons
     end(P, C, tmem);
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
-{
-    uint32_t w;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-    return w;
-}
-
 // Many rows: the hidden rows are M, the weight N.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_constant__ Params P)
@@ -563,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
                 }
             }
             if (!ok) break;
+            // (as store_logits does: called here, it spills registers of the fp32 form)
 #pragma unroll
             for (int c0 = 0; c0 < kCols; c0 += kBoxCols) {
                 if (P.tma_stores) {  // the box before has left the buffer
@@ -611,51 +544,6 @@ __global__ void __launch_bounds__(kThreads, 1) many_rows_kernel(const __grid_con
     end(P, C, tmem);
 }
 
-// ---------------------------------------------------------------- host side
-PFN_cuTensorMapEncodeTiled_v12000 encoder()
-{
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
-    return fn;
-}
-
-// Tensor map of the logits: boxes of a warp's part of a tile.
-bool encode_logits(CUtensorMap* map, void* base, int dtype, int64_t rows, int64_t cols, int64_t ld)
-{
-    PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
-    if (!fn) return false;
-    const bool bf16 = dtype == SAMPLER_DTYPE_BF16;
-    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(ld) * (bf16 ? 2u : 4u)};
-    const cuuint32_t box[2] = {bf16 ? 64u : 32u, 32u};
-    const cuuint32_t estr[2] = {1u, 1u};
-    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// Tensor map over rows x cols bytes, box 128 x box_rows; bytes outside read as zero.
-bool encode(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_rows)
-{
-    PFN_cuTensorMapEncodeTiled_v12000 fn = encoder();
-    if (!fn) return false;
-    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
-    const cuuint64_t strides[1] = {cuuint64_t(ld)};
-    const cuuint32_t box[2] = {cuuint32_t(kBK), cuuint32_t(box_rows)};
-    const cuuint32_t estr[2] = {1u, 1u};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 using Kernel = void (*)(const Params);
 
 }  // namespace scaled
@@ -681,10 +569,10 @@ int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, 
     p.accs = std::min({kMaxAccs, kTmemCols / p.NT, p.stages - 1});
     p.tmem_cols = 32;
     while (p.tmem_cols < (few ? uint32_t(p.accs * p.NT) : uint32_t(kTmemCols))) p.tmem_cols <<= 1;
-    const bool maps = few ? encode(&p.tm, g.weight, vocab, g.hidden_dim, g.weight_stride, kBM) &&
-                                encode(&p.tn, g.hidden, rows, g.hidden_dim, g.hidden_stride, p.NT)
-                          : encode(&p.tm, g.hidden, rows, g.hidden_dim, g.hidden_stride, kBM) &&
-                                encode(&p.tn, g.weight, vocab, g.hidden_dim, g.weight_stride, kWideN);
+    const bool maps = few ? encode_bytes(&p.tm, g.weight, vocab, g.hidden_dim, g.weight_stride, kBM) &&
+                                encode_bytes(&p.tn, g.hidden, rows, g.hidden_dim, g.hidden_stride, p.NT)
+                          : encode_bytes(&p.tm, g.hidden, rows, g.hidden_dim, g.hidden_stride, kBM) &&
+                                encode_bytes(&p.tn, g.weight, vocab, g.hidden_dim, g.weight_stride, kWideN);
     if (!maps) return SAMPLER_ERR_CUDA;
     p.hidden_scale = g.hidden_scale;
     p.weight_scale = g.weight_scale;

@@ -1,5 +1,5 @@
-// train_api.cu -- the C ABI's entries for scoring, the losses and the 8-bit LM
-// head (declared in include/sampler.h): argument checks and launches.
+// train_api.cu -- the C ABI's entries for scoring, the losses and the LM heads in
+// 8 and 4 bits (declared in include/sampler.h): argument checks and launches.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -65,6 +65,30 @@ int launch_scaled(sampler_t h, const sampler_scaled_head_t* g, void* logits, int
 {
     return dst::scaled_head_launch(*g, logits, dtype, ldl, rows, vocab, h->num_sms, h->wait_ns,
                                    h->stats + SAMPLER_STAT_LM_HEAD_TIMEOUTS, &h->head_grants, stream);
+}
+
+constexpr int64_t kMicroMaxCols = 1 << 24;
+
+bool micro_block(int block) { return block == 16 || block == 32; }
+
+int check_micro_head(const sampler_micro_head_t* g)
+{
+    if (!g || !g->hidden || !g->hidden_scale || !g->weight || !g->weight_scale) return SAMPLER_ERR_NULL_ARG;
+    if (!micro_block(g->block)) return SAMPLER_ERR_BAD_VALUE;
+    const int64_t bytes = (g->hidden_dim + 1) / 2;
+    if (g->hidden_dim < 1 || g->hidden_dim > kMicroMaxCols || g->hidden_stride < bytes || g->weight_stride < bytes ||
+        g->hidden_stride % 16 != 0 || g->weight_stride % 16 != 0 || !aligned(g->hidden, 16) || !aligned(g->weight, 16) ||
+        !aligned(g->hidden_scale, 16) || !aligned(g->weight_scale, 16) || !aligned(g->hidden_row_scale, 4) ||
+        !aligned(g->weight_row_scale, 4))
+        return SAMPLER_ERR_BAD_SHAPE;
+    return SAMPLER_OK;
+}
+
+int launch_micro(sampler_t h, const sampler_micro_head_t* g, void* logits, int dtype, int64_t ldl, int64_t rows,
+                 int64_t vocab, cudaStream_t stream)
+{
+    return dst::micro_head_launch(*g, logits, dtype, ldl, rows, vocab, h->num_sms, h->wait_ns,
+                                  h->stats + SAMPLER_STAT_LM_HEAD_TIMEOUTS, &h->micro_grants, stream);
 }
 
 }  // namespace
@@ -220,6 +244,81 @@ int sampler_lm_head_scaled_sample(sampler_t h, const sampler_scaled_head_t* lm, 
     if (cudaSetDevice(h->device) != cudaSuccess) return SAMPLER_ERR_CUDA;
     rc = launch_scaled(h, lm, const_cast<void*>(a->logits), a->dtype, a->row_stride, rows, a->vocab,
                        cuda_stream(stream));
+    if (rc != SAMPLER_OK) return rc;
+    return dst::sample_launch(h, a, ext, true, cuda_stream(stream));
+}
+
+int64_t sampler_micro_scale_bytes(int64_t rows, int64_t cols, int32_t block)
+{
+    if (!micro_block(block) || rows < 0 || rows > INT_MAX - 127 || cols < 1 || cols > kMicroMaxCols) return -1;
+    return (rows + 127) / 128 * (((cols + block - 1) / block + 3) / 4) * 512;
+}
+
+int sampler_quantize_micro(sampler_t h, const sampler_micro_t* q, sampler_stream_t stream)
+{
+    if (!h || !q) return SAMPLER_ERR_NULL_ARG;
+    if (!micro_block(q->block)) return SAMPLER_ERR_BAD_VALUE;
+    if (sampler_micro_scale_bytes(q->rows, q->cols, q->block) < 0 || q->src_stride < q->cols ||
+        q->values_stride < (q->cols + 1) / 2)
+        return SAMPLER_ERR_BAD_SHAPE;
+    if (!known(q->dtype)) return SAMPLER_ERR_BAD_DTYPE;
+    if (q->rows == 0) return SAMPLER_OK;
+    if (!q->src || !q->values || !q->scales || !q->row_scale) return SAMPLER_ERR_NULL_ARG;
+    if (!aligned(q->src, bytes_of(q->dtype)) || !aligned(q->scales, 16) || !aligned(q->row_scale, 4))
+        return SAMPLER_ERR_BAD_SHAPE;
+    DeviceGuard guard;
+    if (cudaSetDevice(h->device) != cudaSuccess) return SAMPLER_ERR_CUDA;
+    return dst::micro_quantize_launch(*q, cuda_stream(stream));
+}
+
+int sampler_micro_rows(sampler_t h, const sampler_micro_rows_t* q, sampler_stream_t stream)
+{
+    if (!h || !q) return SAMPLER_ERR_NULL_ARG;
+    if (!micro_block(q->block)) return SAMPLER_ERR_BAD_VALUE;
+    if (sampler_micro_scale_bytes(q->rows, q->cols, q->block) < 0 || q->values_stride < (q->cols + 1) / 2 || q->n < 0 ||
+        q->n > INT_MAX || q->out_stride < q->cols || (!q->ids && q->n > q->rows))
+        return SAMPLER_ERR_BAD_SHAPE;
+    if (!known(q->dtype)) return SAMPLER_ERR_BAD_DTYPE;
+    if (q->n == 0) return SAMPLER_OK;
+    if (!q->out || (q->rows > 0 && (!q->values || !q->scales))) return SAMPLER_ERR_NULL_ARG;
+    if (!aligned(q->out, bytes_of(q->dtype)) || !aligned(q->scales, 16) || !aligned(q->row_scale, 4) || !aligned(q->ids, 4))
+        return SAMPLER_ERR_BAD_SHAPE;
+    DeviceGuard guard;
+    if (cudaSetDevice(h->device) != cudaSuccess) return SAMPLER_ERR_CUDA;
+    return dst::micro_rows_launch(*q, cuda_stream(stream));
+}
+
+int sampler_lm_head_micro(sampler_t h, const sampler_micro_head_t* lm, void* logits, int32_t dtype, int64_t ldl,
+                          int64_t rows, int64_t vocab, sampler_stream_t stream)
+{
+    if (!h || !lm) return SAMPLER_ERR_NULL_ARG;
+    if (!known(dtype)) return SAMPLER_ERR_BAD_DTYPE;
+    if (rows < 0 || vocab < 1 || ldl < vocab || !aligned(logits, bytes_of(dtype))) return SAMPLER_ERR_BAD_SHAPE;
+    if (rows > INT_MAX - 255 || vocab > h->max_vocab) return SAMPLER_ERR_TOO_LARGE;
+    if (rows == 0) return SAMPLER_OK;
+    if (!logits) return SAMPLER_ERR_NULL_ARG;
+    const int rc = check_micro_head(lm);
+    if (rc != SAMPLER_OK) return rc;
+    DeviceGuard guard;
+    if (cudaSetDevice(h->device) != cudaSuccess) return SAMPLER_ERR_CUDA;
+    return launch_micro(h, lm, logits, dtype, ldl, rows, vocab, cuda_stream(stream));
+}
+
+int sampler_lm_head_micro_sample(sampler_t h, const sampler_micro_head_t* lm, const sampler_args_t* a,
+                                 const sampler_ext_t* ext, sampler_stream_t stream)
+{
+    if (!h || !a || !lm) return SAMPLER_ERR_NULL_ARG;
+    // the sampler's own checks, before anything is enqueued
+    int rc = dst::sample_check(h, a, ext);
+    if (rc != SAMPLER_OK || a->n_rows == 0) return rc;
+    rc = check_micro_head(lm);
+    if (rc != SAMPLER_OK) return rc;
+    const int64_t rows = a->n_logit_rows > 0 ? a->n_logit_rows : a->n_rows;
+    if (rows > INT_MAX - 255) return SAMPLER_ERR_TOO_LARGE;
+    if (!aligned(a->logits, bytes_of(a->dtype))) return SAMPLER_ERR_BAD_SHAPE;
+    DeviceGuard guard;
+    if (cudaSetDevice(h->device) != cudaSuccess) return SAMPLER_ERR_CUDA;
+    rc = launch_micro(h, lm, const_cast<void*>(a->logits), a->dtype, a->row_stride, rows, a->vocab, cuda_stream(stream));
     if (rc != SAMPLER_OK) return rc;
     return dst::sample_launch(h, a, ext, true, cuda_stream(stream));
 }

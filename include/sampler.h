@@ -124,9 +124,9 @@ typedef struct {
  * The kernel still lets each copy land before it reuses or releases the
  * buffer, so nothing faults and nothing hangs; later calls are unaffected
  * (no state survives a call). Scoring and the losses give up likewise where
- * their rows take a kernel with waits (rows above 16 KB may), and so does the
- * 8-bit LM head, which leaves its logits as they were and counts its blocks in
- * SAMPLER_STAT_LM_HEAD_TIMEOUTS. Lets a test observe the timeout status. */
+ * their rows take a kernel with waits (rows above 16 KB may), and so do the
+ * 8-bit and the 4-bit LM head, which leave their logits as they were and count
+ * their blocks in SAMPLER_STAT_LM_HEAD_TIMEOUTS. Lets a test observe the timeout status. */
 #define SAMPLER_CREATE_SHORT_WAITS 4u
 
 /*
@@ -536,6 +536,95 @@ int sampler_lm_head_scaled(sampler_t h, const sampler_scaled_head_t* lm, void* l
  * as sampler_lm_head_sample does with a bf16 head. */
 int sampler_lm_head_scaled_sample(sampler_t h, const sampler_scaled_head_t* lm, const sampler_args_t* args,
                                   const sampler_ext_t* ext, sampler_stream_t stream);
+
+/*
+ * The LM head in 4 bits: e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4 and 6 with a sign),
+ * two to a byte, the one of the lower column in the lower four bits, with a scale of
+ * 8 bits for each block of `block` neighbouring columns of a row:
+ *   block 16: scales in e4m3 (NaN: 0x7f), and one fp32 scale for each row;
+ *   block 32: scales that are powers of two, 2^(byte - 127) (NaN: 0xff).
+ * A value is code * (block scale * row scale), each product one fp32 operation.
+ *
+ * Scales lie as the tensor cores take them, in tiles of 128 rows by 4 blocks: the
+ * scale of row r and block b is byte
+ *   ((r / 128) * tiles + b / 4) * 512 + (r % 32) * 16 + (r / 32 % 4) * 4 + b % 4
+ * with tiles = ceil(ceil(cols / block) / 4). Those of rows and blocks that are not
+ * there are 0 (sampler_quantize_micro writes them so; what is in the place of a
+ * block that is not there takes part in products with zeros and must not be NaN).
+ * sampler_micro_scale_bytes gives their size, ceil(rows / 128) * tiles * 512 (-1 for
+ * sizes that the calls refuse).
+ *
+ * sampler_quantize_micro lays a matrix out so. With m the largest magnitude of a
+ * block and M the one of a row's finite blocks:
+ *   block 32: scale = 2^e, e >= -127 the least with m <= 6 * 2^e; row scales 1;
+ *   block 16: row scale = 2^g, g the least with max(M, 2^-100) <= 448 * 6 * 2^g,
+ *             scale = e4m3((m / 6) / 2^g);
+ *   code = e2m1(x / (scale * row scale)), beyond 6 as 6 (0 where that scale is 0),
+ * each rounding to nearest even, of the exact quotient. A block with a NaN or an
+ * infinity has a NaN scale and zero codes, so that what is computed from it is NaN.
+ */
+typedef struct {
+    const void* src;         /* [rows, src_stride] */
+    int32_t dtype;           /* SAMPLER_DTYPE_* */
+    int64_t rows, cols;      /* cols at most 2^24 */
+    int64_t src_stride;      /* elements, >= cols */
+    int32_t block;           /* 16 or 32 */
+    void* values;            /* [rows, values_stride]: ceil(cols / 2) bytes of a row are written (the upper four
+                                bits of the last byte are 0 where cols is odd) */
+    int64_t values_stride;   /* bytes, >= ceil(cols / 2) */
+    void* scales;            /* sampler_micro_scale_bytes(rows, cols, block), 16-byte aligned */
+    float* row_scale;        /* [rows] */
+} sampler_micro_t;
+
+int64_t sampler_micro_scale_bytes(int64_t rows, int64_t cols, int32_t block);
+int sampler_quantize_micro(sampler_t h, const sampler_micro_t* q, sampler_stream_t stream);
+
+/* Rows of such a matrix back to numbers, each rounded once to `dtype`: out[i] = row
+ * ids[i] (an embedding's rows, say), or row i without ids. A row for an id outside
+ * [0, rows) is NaN. */
+typedef struct {
+    const void* values;       /* [rows, values_stride] */
+    int64_t values_stride;    /* bytes, >= ceil(cols / 2) */
+    const void* scales;       /* 16-byte aligned */
+    const float* row_scale;   /* [rows] NULL = 1 */
+    int64_t rows, cols;
+    int32_t block;
+    const int32_t* ids;       /* [n] NULL = 0 .. n - 1 (n <= rows) */
+    int64_t n;
+    void* out;                /* [n, out_stride] */
+    int32_t dtype;
+    int64_t out_stride;       /* elements, >= cols */
+} sampler_micro_rows_t;
+
+int sampler_micro_rows(sampler_t h, const sampler_micro_rows_t* q, sampler_stream_t stream);
+
+/* logits[i, v] = hidden_row_scale[i] * weight_row_scale[v] * sum_k (code * block scale of hidden[i, k])
+ *                                                               * (code * block scale of weight[v, k])
+ * for i < rows, v < vocab, in fp32 sums, rounded once to `dtype`. Both operands
+ * 16-byte aligned with strides multiples of 16 bytes and >= ceil(hidden_dim / 2),
+ * else SAMPLER_ERR_BAD_SHAPE; where hidden_dim is odd the upper four bits of a row's
+ * last byte are 0. vocab is at most the handle's max_vocab. Waits and
+ * SAMPLER_STAT_LM_HEAD_TIMEOUTS as in the other heads. */
+typedef struct {
+    const void* hidden;             /* [rows, hidden_stride] */
+    const void* hidden_scale;       /* 16-byte aligned */
+    const float* hidden_row_scale;  /* [rows] NULL = 1 */
+    const void* weight;             /* [vocab, weight_stride] */
+    const void* weight_scale;
+    const float* weight_row_scale;  /* [vocab] NULL = 1 */
+    int64_t hidden_dim;             /* K >= 1, at most 2^24 */
+    int64_t hidden_stride;          /* bytes */
+    int64_t weight_stride;
+    int32_t block;                  /* 16 or 32, of both */
+} sampler_micro_head_t;
+
+int sampler_lm_head_micro(sampler_t h, const sampler_micro_head_t* lm, void* logits, int32_t dtype,
+                          int64_t logits_stride, int64_t rows, int64_t vocab, sampler_stream_t stream);
+
+/* sampler_lm_head_micro into args->logits, then the step of sampler_sample_ex on
+ * them, as sampler_lm_head_scaled_sample does with an 8-bit head. */
+int sampler_lm_head_micro_sample(sampler_t h, const sampler_micro_head_t* lm, const sampler_args_t* args,
+                                 const sampler_ext_t* ext, sampler_stream_t stream);
 
 /* Release the handle and its device memory. NULL is a no-op. */
 void sampler_destroy(sampler_t h);

@@ -24,7 +24,8 @@ from ._binding import (EXPORTED, SAMPLER_CREATE_HOST_STAGING, SAMPLER_CREATE_SHO
                        sampler_score_grad, sampler_policy_loss, sampler_preference_loss, sampler_quantize_blocks,
                        sampler_lm_head_scaled, sampler_lm_head_scaled_sample, sampler_micro_t, sampler_micro_rows_t,
                        sampler_micro_head_t, sampler_micro_scale_bytes, sampler_quantize_micro, sampler_micro_rows,
-                       sampler_lm_head_micro, sampler_lm_head_micro_sample)
+                       sampler_lm_head_micro, sampler_lm_head_micro_sample, SAMPLER_MAX_ALTERNATIVES, sampler_top_t,
+                       sampler_distill_t, sampler_score_top, sampler_distill_loss)
 
 __all__ = ["Sampler", "SamplerError", "load_library", "sampler_create", "sampler_sample",
            "sampler_sample_host", "sampler_sample_noalloc", "sampler_sample_ex", "sampler_destroy",
@@ -37,7 +38,8 @@ __all__ = ["Sampler", "SamplerError", "load_library", "sampler_create", "sampler
            "sampler_policy_loss", "sampler_preference_loss", "sampler_quantize_blocks", "sampler_lm_head_scaled",
            "sampler_lm_head_scaled_sample", "sampler_micro_t", "sampler_micro_rows_t", "sampler_micro_head_t",
            "sampler_micro_scale_bytes", "sampler_quantize_micro", "sampler_micro_rows", "sampler_lm_head_micro",
-           "sampler_lm_head_micro_sample"]
+           "sampler_lm_head_micro_sample", "SAMPLER_MAX_ALTERNATIVES", "sampler_top_t", "sampler_distill_t",
+           "sampler_score_top", "sampler_distill_loss"]
 
 
 def _make_ext(top_n: int = 0, unscaled: bool = False, out_token_logprob=None, out_top_ids=None,
@@ -333,6 +335,41 @@ class Sampler:
         gl = _vector("grad_logprob", grad_logprob, n, f32, self.device)
         ge = _vector("grad_entropy", grad_entropy, n, f32, self.device)
         self._done(sampler_score_grad(self._h, rows, gl, ge, self._stream(stream)), "sampler_score_grad")
+
+    def score_top(self, *, logits, top_n: int, out_top_ids, out_top_logprobs, out_rest_logprob=None, tokens=None,
+                  out_logprob=None, out_entropy=None, out_status=None, temperature=None, weight=None,
+                  vocab: Optional[int] = None, stream: Optional[int] = None) -> None:
+        """sampler_score_top: the top_n most likely tokens of each row (int32 out_top_ids,
+        fp32 out_top_logprobs, [N, top_n]) and the logprob of all others together
+        (fp32 out_rest_logprob [N]), with the outputs of ``score`` for tokens, where
+        they are given."""
+        rows = self._rows(logits, tokens, temperature, weight, out_logprob, out_entropy, out_status, None, vocab)
+        n, (_, f32, i32, _), dev = rows.n_rows, _torch_types(), self.device
+        q = sampler_top_t(top_n, _vector("out_top_ids", out_top_ids, n * max(0, top_n), i32, dev),
+                          _vector("out_top_logprobs", out_top_logprobs, n * max(0, top_n), f32, dev),
+                          _vector("out_rest_logprob", out_rest_logprob, n, f32, dev))
+        self._done(sampler_score_top(self._h, rows, q, self._stream(stream)), "sampler_score_top")
+
+    def distill_loss(self, *, logits, teacher_ids, teacher_logprobs, out_loss, teacher_rest=None, tokens=None,
+                     token_coef: float = 0.0, temperature=None, weight=None, grad_scale: float = 1.0,
+                     grad_scale_dev=None, out_grad=None, out_kl=None, out_logprob=None, out_status=None,
+                     vocab: Optional[int] = None, stream: Optional[int] = None) -> None:
+        """sampler_distill_loss against the lists that ``score_top`` gives of a teacher's
+        rows (int32 teacher_ids and fp32 teacher_logprobs [N, n], fp32 teacher_rest
+        [N]), with token_coef times the loss of tokens (out_loss: one fp32), and with
+        out_grad the logits' gradient."""
+        rows = self._rows(logits, tokens, temperature, weight, out_logprob, None, out_status, out_grad, vocab)
+        n, (_, f32, i32, _), dev = rows.n_rows, _torch_types(), self.device
+        if teacher_ids.dim() != 2 or teacher_ids.shape != teacher_logprobs.shape or teacher_ids.shape[0] != n:
+            raise ValueError(f"teacher_ids and teacher_logprobs must be [{n}, top_n], not {tuple(teacher_ids.shape)} and "
+                             f"{tuple(teacher_logprobs.shape)}")
+        top_n = teacher_ids.shape[1]
+        q = sampler_distill_t(top_n, _vector("teacher_ids", teacher_ids, n * top_n, i32, dev),
+                              _vector("teacher_logprobs", teacher_logprobs, n * top_n, f32, dev),
+                              _vector("teacher_rest", teacher_rest, n, f32, dev), token_coef, grad_scale,
+                              _vector("grad_scale_dev", grad_scale_dev, 1, f32, dev),
+                              _vector("out_loss", out_loss, 1, f32, dev), _vector("out_kl", out_kl, n, f32, dev))
+        self._done(sampler_distill_loss(self._h, rows, q, self._stream(stream)), "sampler_distill_loss")
 
     def policy_loss(self, *, logits, tokens, old_logprob, advantage, out_loss, ref_logprob=None, temperature=None,
                     weight=None, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0,

@@ -43,13 +43,14 @@ EXPORTED = ("sampler_create", "sampler_sample", "sampler_sample_host", "sampler_
             "sampler_score", "sampler_score_grad", "sampler_policy_loss", "sampler_preference_loss",
             "sampler_quantize_blocks", "sampler_lm_head_scaled", "sampler_lm_head_scaled_sample",
             "sampler_micro_scale_bytes", "sampler_quantize_micro", "sampler_micro_rows", "sampler_lm_head_micro",
-            "sampler_lm_head_micro_sample")
+            "sampler_lm_head_micro_sample", "sampler_score_top", "sampler_distill_loss")
 SAMPLER_STAT_EXACT_ROWS = 0
 SAMPLER_STAT_LM_HEAD_TIMEOUTS = 1
 SAMPLER_LM_HEAD_MAX_ROWS = 256
 SAMPLER_NOALLOC_MAX_ROWS = 64
 SAMPLER_LOSS_MAX_ROWS = 16777216
 SAMPLER_MAX_TOP_N = 16
+SAMPLER_MAX_ALTERNATIVES = 128
 SAMPLER_MAX_BIAS = 64
 SAMPLER_MAX_STOP = 16
 
@@ -207,6 +208,29 @@ class sampler_scaled_head_t(ctypes.Structure):
     ]
 
 
+class sampler_top_t(ctypes.Structure):
+    _fields_ = [
+        ("top_n", ctypes.c_int32),
+        ("out_top_ids", _P),
+        ("out_top_logprobs", _P),
+        ("out_rest_logprob", _P),
+    ]
+
+
+class sampler_distill_t(ctypes.Structure):
+    _fields_ = [
+        ("top_n", ctypes.c_int32),
+        ("teacher_ids", _P),
+        ("teacher_logprobs", _P),
+        ("teacher_rest", _P),
+        ("token_coef", ctypes.c_float),
+        ("grad_scale", ctypes.c_float),
+        ("grad_scale_dev", _P),
+        ("out_loss", _P),
+        ("out_kl", _P),
+    ]
+
+
 class sampler_micro_t(ctypes.Structure):
     _fields_ = [
         ("src", _P),
@@ -309,6 +333,11 @@ def load_library(path: str = LIB):
                                                           ctypes.POINTER(sampler_args_t),
                                                           ctypes.POINTER(sampler_ext_t), _P]
             lib.sampler_lm_head_scaled_sample.restype = ctypes.c_int
+            lib.sampler_score_top.argtypes = [_P, ctypes.POINTER(sampler_rows_t), ctypes.POINTER(sampler_top_t), _P]
+            lib.sampler_score_top.restype = ctypes.c_int
+            lib.sampler_distill_loss.argtypes = [_P, ctypes.POINTER(sampler_rows_t),
+                                                 ctypes.POINTER(sampler_distill_t), _P]
+            lib.sampler_distill_loss.restype = ctypes.c_int
             lib.sampler_micro_scale_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int32]
             lib.sampler_micro_scale_bytes.restype = ctypes.c_int64
             lib.sampler_quantize_micro.argtypes = [_P, ctypes.POINTER(sampler_micro_t), _P]
@@ -412,6 +441,14 @@ def sampler_lm_head_scaled_sample(h, lm: sampler_scaled_head_t, args: sampler_ar
     """ext: a sampler_ext_t or None."""
     return load_library().sampler_lm_head_scaled_sample(h, ctypes.byref(lm), ctypes.byref(args),
                                                         ctypes.byref(ext) if ext is not None else None, _P(stream))
+
+
+def sampler_score_top(h, rows: sampler_rows_t, top: sampler_top_t, stream: int) -> int:
+    return load_library().sampler_score_top(h, ctypes.byref(rows), ctypes.byref(top), _P(stream))
+
+
+def sampler_distill_loss(h, rows: sampler_rows_t, distill: sampler_distill_t, stream: int) -> int:
+    return load_library().sampler_distill_loss(h, ctypes.byref(rows), ctypes.byref(distill), _P(stream))
 
 
 def sampler_micro_scale_bytes(rows: int, cols: int, block: int) -> int:

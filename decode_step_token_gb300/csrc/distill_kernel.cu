@@ -1,0 +1,635 @@
+// distill_kernel.cu -- distillation from a teacher's most likely tokens: the loss of
+// rows of logits against lists of tokens with logprobs, and the logits' gradient.
+//
+// With S a row's list, q_j = exp(l_j) its masses, q_r the mass outside, W = sum q_j + q_r, h = token_coef
+// and p_r = sum_{v not in S} p_v,
+//     KL = sum_j q_j (l_j - ln p_j) + q_r (ln q_r - ln p_r),
+//     T d loss / d x_v = (p_v / p_r) ((W + h) p_r - q_r)  outside the list,
+//                        (W + h) p_j - q_j                inside,     and -h at the row's token.
+// The two sides of the list are kept apart from the start: the sums of the tokens outside have their own reference, so
+// that p_r is a sum and not a difference, however little it is, and an element outside is one exponential times one
+// factor of the row. The list's own terms are taken one by one, with the accurate exponential, and added up in double:
+// a divergence is a small difference of logprobs.
+//
+// As in the other losses (row_loss_kernel.cu) a cluster of C CTAs takes a row, each CTA a part of it in shared memory
+// between the two passes, so that each logit is read once and each gradient written once. Here a part is one buffer,
+// of which a CTA has two to four. Warp roles of a CTA:
+//   producer   goes ahead over the cluster's rows and brings their parts in with bulk copies;
+//   closer     marks the list's tokens of a part in a map of bits, a byte for each vector, before pass 1; takes their
+//              logits from the buffer and puts its share of the list's sums into all CTAs of the cluster; combines what
+//              all have put, works out the row's factors, writes the row's outputs, and puts the list's own gradients
+//              into the buffer in their logits' place;
+//   consumers  (eight) pass 1: the running reference and sum of what is not marked; pass 2: the gradient, marked elements
+//              as they now are in the buffer. A row's pass 1 comes before the pass 2 of the row before it, so that the
+//              join and the closer's work run under it.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "launch.h"
+#include "ptx.cuh"
+#include "row_loss.cuh"
+#include "row_queue.cuh"
+#include "row_vectors.cuh"
+#include "warp_wait.cuh"
+
+namespace dst {
+namespace distill {
+
+using namespace rows;
+
+constexpr int kWarps = 8;
+constexpr int kConsumers = kWarps * 32;
+constexpr int kProducer = kWarps, kCloser = kWarps + 1;
+constexpr int kThreads = kConsumers + 64;
+constexpr int kVecs = 4;                     // vectors that a consumer folds at once
+constexpr int kStep = kConsumers * kVecs;
+constexpr int kMaxBuffers = 4;
+constexpr int kMaxParts = 16;                // CTAs of a cluster
+constexpr int kMaps = 3;                     // rows whose tokens are marked
+constexpr int kSums = 4;                     // rows whose sums are in shared memory
+constexpr int kHeld = SAMPLER_MAX_ALTERNATIVES / 32;  // of a list in each of the closer's lanes
+constexpr int kSmemTwo = 113 * 1024, kSmemOne = 226 * 1024;  // of a CTA: two on an SM, and one
+constexpr uint64_t kSettleNs = 100000;       // in which what is on its way to shared memory lands
+
+// What a CTA's closer puts into all CTAs: sums of the list's tokens in its part.
+struct ListSums {
+    float ref, s;   // exponentials
+    double a, q;    // q_j (l_j - x_j / T) and q_j
+    uint32_t flags, pad;
+};
+static_assert(sizeof(ListSums) == 32, "two stores of 16 bytes");
+constexpr uint32_t kBadList = 1, kBadLogit = 2;
+
+// A row's factors for pass 2.
+struct Factor {
+    float ref, c, k, at_token;
+    int token;  // kNoToken: none
+};
+
+struct Shared {
+    uint64_t full[kMaxBuffers], empty[kMaxBuffers];
+    uint64_t marked[kMaps], unmarked[kMaps];
+    uint64_t join[kSums], closed[kSums];
+    RowQueue queue;
+    Factor factor[kSums];
+    double scratch[kThreads / 32];
+    uint32_t flag, failed;  // failed: a wait of this cluster gave up
+};
+
+// The buffers, the consumers' sums [kSums][parts * kWarps], the closers' [kSums][parts], the maps [kMaps][part_vecs] and
+// Shared.
+__host__ __device__ constexpr int map_bytes(int part_vecs) { return (part_vecs + 15) / 16 * 16; }
+constexpr int smem_of(int part_vecs, int buffers, int parts)
+{
+    return buffers * part_vecs * 16 + kSums * parts * (kWarps * 16 + int(sizeof(ListSums))) + kMaps * map_bytes(part_vecs) +
+           int(sizeof(Shared));
+}
+
+__device__ __noinline__ void gave_up(Shared& S)
+{
+    const uint32_t cta = threadIdx.x & 31;
+    if (cta < cluster_nctarank()) dsmem_st_u32(dsmem_map(smem_addr(&S.failed), cta), 1u);
+}
+
+__device__ __forceinline__ void write_row(const DistillParams& P, int64_t r, float kl, float logprob, int status, double term)
+{
+    if (P.distill.out_kl) P.distill.out_kl[r] = kl;
+    if (P.rows.out_logprob) P.rows.out_logprob[r] = logprob;
+    if (P.rows.out_status) P.rows.out_status[r] = status;
+    P.ws.terms[r] = term;
+}
+
+// A wait of this cluster gave up. Which of its rows were done with is not known, so all of them are written again, by all
+// CTAs after the last of them has come to its end: those that count as TIMEOUT with NaN, the others as ever.
+template <typename T, bool kGrad>
+__device__ __noinline__ void abandon(const DistillParams& P, uint32_t q, uint32_t n_clusters, uint32_t parts, uint32_t rank)
+{
+    // copies, and sums put into this CTA, that nobody has waited for land before it may exit
+    const uint64_t until = now_ns() + kSettleNs;
+    for (uint32_t i = 0; i < (1u << 20) && now_ns() < until; ++i) {
+    }
+    const sampler_rows_t& a = P.rows;
+    RowDealer d;
+    dealer_open(d, a, q);
+    for (;;) {
+        bool counts;
+        const int64_t r = dealer_next(d, a, q, n_clusters, counts);
+        if (r < 0) return;
+        const float x = counts ? quiet_nan() : 0.f;
+        if (rank == 0 && threadIdx.x == 0) write_row(P, r, x, x, counts ? SAMPLER_ROW_TIMEOUT : SAMPLER_ROW_OK, x);
+        if (kGrad) {
+            T* g = static_cast<T*>(a.out_grad) + r * a.grad_stride;
+            for (int64_t v = rank * kThreads + threadIdx.x; v < a.vocab; v += parts * kThreads) store_grad(g + v, x);
+        }
+    }
+}
+
+// Marked elements of a vector become -inf, or those of `from`.
+template <typename T>
+__device__ __forceinline__ void blend(uint4& v, const uint4& from, uint32_t bits);
+template <>
+__device__ __forceinline__ void blend<float>(uint4& v, const uint4& from, uint32_t bits)
+{
+    if (bits & 1u) v.x = from.x;
+    if (bits & 2u) v.y = from.y;
+    if (bits & 4u) v.z = from.z;
+    if (bits & 8u) v.w = from.w;
+}
+template <>
+__device__ __forceinline__ void blend<uint16_t>(uint4& v, const uint4& from, uint32_t bits)
+{
+    auto word = [&](uint32_t& w, uint32_t f, uint32_t b) {
+        const uint32_t m = (b & 1u ? 0xffffu : 0u) | (b & 2u ? 0xffff0000u : 0u);
+        w = (w & ~m) | (f & m);
+    };
+    word(v.x, from.x, bits);
+    word(v.y, from.y, bits >> 2);
+    word(v.z, from.z, bits >> 4);
+    word(v.w, from.w, bits >> 6);
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 nothing()
+{
+    const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    return make_uint4(w, w, w, w);
+}
+
+// A list's token in this CTA's part, as a lane of the closer has it.
+struct Entry {
+    int at;      // element of the part's buffer; -1: not in it
+    float x, q;
+};
+
+template <typename T, bool kGrad>
+__global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_constant__ DistillParams P)
+{
+    constexpr int kPer = Elems<T>::kPer;
+    extern __shared__ __align__(128) unsigned char smem[];
+    const sampler_rows_t& a = P.rows;
+    const sampler_distill_t& D = P.distill;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const uint32_t parts = cluster_nctarank(), rank = cluster_ctarank();
+    const uint32_t q = blockIdx.x / parts, n_clusters = gridDim.x / parts;
+    const uint32_t buffers = uint32_t(P.buffers);
+    const int buffer_bytes = P.part_vecs * 16;
+    float4* sums = reinterpret_cast<float4*>(smem + buffers * buffer_bytes);
+    ListSums* lists = reinterpret_cast<ListSums*>(sums + kSums * parts * kWarps);
+    unsigned char* maps = reinterpret_cast<unsigned char*>(lists + kSums * parts);
+    Shared& S = *reinterpret_cast<Shared*>(maps + kMaps * map_bytes(P.part_vecs));
+
+    if (tid == 0) {
+        for (int i = 0; i < kMaxBuffers; ++i) {
+            mbar_init(&S.full[i], 1);
+            mbar_init(&S.empty[i], kWarps + 1);
+        }
+        for (int i = 0; i < kMaps; ++i) {
+            mbar_init(&S.marked[i], 1);
+            mbar_init(&S.unmarked[i], kWarps);
+        }
+        for (int i = 0; i < kSums; ++i) {
+            mbar_init(&S.join[i], 1);
+            mbar_init(&S.closed[i], 1);
+        }
+        queue_open(S.queue, kWarps + 1);
+        S.failed = 0;
+        fence_mbar_init();
+    }
+    for (int i = tid; i < kMaps * map_bytes(P.part_vecs) / 4; i += kThreads) reinterpret_cast<uint32_t*>(maps)[i] = 0;
+    cluster_sync();
+
+    const int first_vec = int(rank) * P.part_vecs;
+    if (warp == kProducer) {
+        RingPlace buf{0, 0};
+        uint32_t issued = 0;
+        // (wait_ns 0: nothing begins, and every other wait of the cluster gives up)
+        const bool ok = P.wait_ns != 0 && queue_fill<T>(S.queue, a, q, n_clusters, a.tokens != nullptr, P.wait_ns, [&](int64_t r) {
+            const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
+            const RowSpan span = row_span(x, a.vocab);
+            const int n = min(first_vec + P.part_vecs, span.count) - first_vec;
+            if (!wait(&S.empty[buf.at], buf.phase ^ 1u, P.wait_ns)) return false;
+            if (elect_one()) {
+                if (n > 0) {
+                    mbar_arrive_expect_tx(&S.full[buf.at], uint32_t(n) * 16u);
+                    bulk_copy_g2s(smem + buf.at * buffer_bytes,
+                                  reinterpret_cast<const unsigned char*>(x - span.head) + size_t(first_vec) * 16, uint32_t(n) * 16u,
+                                  &S.full[buf.at]);
+                } else {
+                    mbar_arrive(&S.full[buf.at]);  // the row ends before this part
+                }
+            }
+            __syncwarp();
+            buf.next(buffers);
+            ++issued;
+            return true;
+        });
+        if (!ok) {
+            gave_up(S);
+            // copies in flight land before the CTA may exit
+            for (uint32_t j = issued > buffers ? issued - buffers : 0; j < issued; ++j)
+                wait(&S.full[j % buffers], j / buffers & 1u, kWaitNs);
+        }
+    } else if (warp == kCloser) {
+        QueuePlace place{{0, 0}, 0};
+        RingPlace buf{0, 0}, map{0, 0}, put{0, 0}, taken{0, 0};
+        const float scale = kGrad ? scale_of_grad(D.grad_scale, D.grad_scale_dev) : 1.f;
+        const int k = D.top_n;
+        // A row whose list has been put, until it is closed.
+        struct Open {
+            RowItem item;
+            RowJob h;
+            Entry list[kHeld];
+            uint32_t buffer;
+            float rest;  // teacher's logprob outside the list
+        };
+        // The next row: marks its tokens, and puts its share of the sums. 1: done; 0: no more rows; -1: a wait gave up.
+        auto open = [&](Open& o) {
+            do {
+                if (!queue_next(S.queue, place, P.wait_ns, o.item)) return -1;
+                if (o.item.row >= 0 && !o.item.live && rank == 0 && lane == 0)
+                    write_row(P, o.item.row, 0.f, 0.f, SAMPLER_ROW_OK, 0.0);
+            } while (o.item.row >= 0 && !o.item.live);
+            if (o.item.row < 0) return 0;
+            const int64_t r = o.item.row;
+            const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
+            const RowSpan span = row_span(x, a.vocab);
+            const int n = min(first_vec + P.part_vecs, span.count) - first_vec;  // vectors here
+            o.h.token = o.item.token;
+            row_scale(o.h, a, o.item.temperature);
+            o.rest = D.teacher_rest ? D.teacher_rest[r] : -pos_inf();
+            float l[kHeld];
+            uint32_t flags = o.rest < pos_inf() ? 0 : kBadList;
+#pragma unroll
+            for (int e = 0; e < kHeld; ++e) {
+                const int j = lane + 32 * e;
+                int id = -1;
+                l[e] = -pos_inf();
+                if (j < k) {
+                    id = D.teacher_ids[r * k + j];
+                    if (id != -1) l[e] = D.teacher_logprobs[r * k + j];
+                }
+                if (id < -1 || int64_t(id) >= a.vocab || !(l[e] < pos_inf())) {
+                    flags |= kBadList;
+                    id = -1;
+                }
+                const int at = id + span.head - first_vec * kPer;
+                o.list[e].at = id >= 0 && at >= 0 && at < n * kPer ? at : -1;
+                o.list[e].q = o.list[e].at >= 0 ? expf(l[e]) : 0.f;
+            }
+            if (!wait(&S.unmarked[map.at], map.phase ^ 1u, P.wait_ns)) return -1;
+            unsigned char* bits = maps + map.at * map_bytes(P.part_vecs);
+#pragma unroll
+            for (int e = 0; e < kHeld; ++e) {
+                const int at = o.list[e].at;
+                if (at >= 0) {
+                    const int byte = at / kPer;
+                    const uint32_t bit = 1u << (8 * (byte & 3) + at % kPer);
+                    if (atomicOr(reinterpret_cast<uint32_t*>(bits) + byte / 4, bit) & bit) flags |= kBadList;  // twice
+                }
+            }
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&S.marked[map.at]);
+                mbar_arrive_expect_tx(&S.join[put.at], parts * uint32_t(kWarps * 16 + sizeof(ListSums)));
+            }
+            map.next(kMaps);
+            __syncwarp();
+            if (!wait(&S.full[buf.at], buf.phase, P.wait_ns)) return -1;
+            o.buffer = buf.at;
+            const T* in = reinterpret_cast<const T*>(smem + buf.at * buffer_bytes);
+            float ref = -kFloatMax;
+#pragma unroll
+            for (int e = 0; e < kHeld; ++e) {
+                o.list[e].x = o.list[e].at >= 0 ? load_logit(in + o.list[e].at) : -pos_inf();
+                if (!(o.list[e].x < pos_inf())) flags |= kBadLogit;
+                ref = fmaxf(ref, o.list[e].x);
+            }
+            ref = max_warp(ref);
+            float s = 0.f;
+            double sa = 0.0, sq = 0.0;
+            const double inv_t = double(o.h.inv_t) + double(o.h.inv_t_lo);
+#pragma unroll
+            for (int e = 0; e < kHeld; ++e) {
+                if (o.list[e].at < 0) continue;
+                const float d = o.list[e].x - ref;
+                s += exp2f(fmaxf(fmaf(d, o.h.c_hi, d * o.h.c_lo), kLowest));
+                if (o.list[e].q > 0.f) {
+                    sa += double(o.list[e].q) * (double(l[e]) - double(o.list[e].x) * inv_t);
+                    sq += double(o.list[e].q);
+                }
+            }
+#pragma unroll
+            for (int i = 16; i > 0; i >>= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, i);
+                sa += __shfl_xor_sync(0xffffffffu, sa, i);
+                sq += __shfl_xor_sync(0xffffffffu, sq, i);
+            }
+            flags = __reduce_or_sync(0xffffffffu, flags);
+            if (uint32_t(lane) < parts) {
+                const uint32_t to = dsmem_map(smem_addr(lists + put.at * parts + rank), lane),
+                               bar = dsmem_map(smem_addr(&S.join[put.at]), lane);
+                put_sums(to, bar, ref, s, __int_as_float(__double2loint(sa)), __int_as_float(__double2hiint(sa)));
+                put_sums(to + 16, bar, __int_as_float(__double2loint(sq)), __int_as_float(__double2hiint(sq)),
+                         __uint_as_float(flags), 0.f);
+            }
+            __syncwarp();
+            if (!kGrad && lane == 0) mbar_arrive(&S.empty[buf.at]);
+            buf.next(buffers);
+            put.next(kSums);
+            return 1;
+        };
+        // Closes a row; false where a wait gave up.
+        auto close = [&](const Open& o) {
+            if (!wait(&S.join[taken.at], taken.phase, P.wait_ns)) return false;
+            const RowJob& h = o.h;
+            // outside the list
+            const float4* in = sums + taken.at * parts * kWarps;
+            Stats out = stats_empty();
+            for (uint32_t i = lane; i < parts * kWarps; i += 32) out.ref = fmaxf(out.ref, in[i].x);
+            out.ref = max_warp(out.ref);
+            for (uint32_t i = lane; i < parts * kWarps; i += 32) {
+                Stats p{in[i].x, in[i].y, 0.f};
+                stats_move(p, out.ref, h.c);
+                out.s += p.s;
+            }
+            sum_warp<false>(out);
+            // inside
+            Stats list = stats_empty();
+            double sa = 0.0, sq = 0.0;
+            uint32_t flags = 0;
+            if (uint32_t(lane) < parts) {
+                const ListSums& p = lists[taken.at * parts + lane];
+                list.ref = p.ref;
+                list.s = p.s;
+                sa = p.a;
+                sq = p.q;
+                flags = p.flags;
+            }
+            stats_warp<false>(list, h.c);
+#pragma unroll
+            for (int i = 16; i > 0; i >>= 1) {
+                sa += __shfl_xor_sync(0xffffffffu, sa, i);
+                sq += __shfl_xor_sync(0xffffffffu, sq, i);
+            }
+            flags = __reduce_or_sync(0xffffffffu, flags);
+
+            const float most = fmaxf(out.ref, list.ref);
+            auto lift = [&](float ref) {
+                const float d = ref - most;
+                return exp2f(fmaxf(fmaf(d, h.c_hi, d * h.c_lo), kLowest));
+            };
+            const float f_out = lift(out.ref);
+            const float s = out.s * f_out + list.s * lift(list.ref);
+            const int status = h.bad_param || (flags & kBadList)        ? SAMPLER_ROW_BAD_PARAM
+                               : isnan(out.s) || (flags & kBadLogit) ? SAMPLER_ROW_NONFINITE
+                               : s == 0.f                            ? SAMPLER_ROW_ALL_NEG_INF
+                                                                     : SAMPLER_ROW_OK;
+            const float inv_s = __fdiv_rn(1.f, s), p_out = out.s * f_out * inv_s;
+            const float q_out = o.rest > -pos_inf() ? expf(o.rest) : 0.f;
+            const float coef = a.tokens ? D.token_coef : 0.f;
+            const float w = float(sq) + q_out + coef;
+            const float g = o.item.weight * scale * h.inv_t;
+            const bool fine = status == SAMPLER_ROW_OK;
+            if (kGrad) {
+                // the list's own gradients, in their logits' place
+                T* to = reinterpret_cast<T*>(smem + o.buffer * buffer_bytes);
+                const T* x = static_cast<const T*>(a.logits) + int64_t(o.item.row) * a.row_stride;
+                const int head = row_span(x, a.vocab).head - first_vec * kPer;
+#pragma unroll
+                for (int e = 0; e < kHeld; ++e) {
+                    const Entry& t = o.list[e];
+                    if (t.at < 0) continue;
+                    float y = fmaf(w, lift(t.x) * inv_s, -t.q);
+                    if (a.tokens && t.at == o.item.token + head) y -= coef;
+                    store_grad(to + t.at, fine ? y * g : quiet_nan());
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (lane == 0) {
+                    Factor& f = S.factor[taken.at];
+                    f.ref = fine ? out.ref : 0.f;
+                    f.c = fine ? h.c : 0.f;
+                    f.k = !fine ? quiet_nan() : out.s > 0.f ? __fdiv_rn(fmaf(w, p_out, -q_out), out.s) * g : 0.f;
+                    f.at_token = -coef * g;
+                    f.token = fine && coef != 0.f ? o.item.token : kNoToken;
+                }
+                __syncwarp();
+            }
+            if (lane == 0) {
+                mbar_arrive(&S.closed[taken.at]);
+                if (kGrad) mbar_arrive(&S.empty[o.buffer]);
+            }
+            if (rank == 0) {
+                Pair ln_s = log_of(s);
+                ln_s.lo = fmaf(kExp2Short, p_out, ln_s.lo);
+                const Stats all{most, s, 0.f};
+                const double inv_t = double(h.inv_t) + double(h.inv_t_lo);
+                const double lse = double(most) * inv_t + (double(ln_s.hi) + double(ln_s.lo));
+                double kl = sa + sq * lse;
+                if (q_out > 0.f) {
+                    const Pair ln_out = log_of(out.s);
+                    kl += out.s > 0.f ? double(q_out) * (double(o.rest) - (double(out.ref) * inv_t + (double(ln_out.hi) + double(ln_out.lo) +
+                                                                                                       double(kExp2Short)) - lse))
+                                      : double(pos_inf());
+                }
+                const Pair lp = logprob_of(h, all, o.item.x_t, ln_s);
+                double each = kl;
+                if (coef != 0.f) each -= double(coef) * (double(lp.hi) + double(lp.lo));
+                if (lane == 0)
+                    write_row(P, o.item.row, fine ? float(kl) : quiet_nan(), fine ? lp.hi : quiet_nan(), status,
+                              fine ? double(o.item.weight) * each : double(quiet_nan()));
+            }
+            __syncwarp();
+            taken.next(kSums);
+            return true;
+        };
+        Open now, next;
+        int more = open(now);
+        while (more == 1) {
+            more = open(next);
+            if (more < 0 || !close(now)) {
+                more = -1;
+                break;
+            }
+            now = next;
+        }
+        if (more < 0) gave_up(S);
+    } else {
+        QueuePlace place{{0, 0}, 0};
+        RingPlace buf1{0, 0}, buf2{0, 0}, map1{0, 0}, map2{0, 0}, put{0, 0}, closed{0, 0};
+        const int vocab = int(a.vocab);
+        // The next row that counts, and its pass 1. 1: done; 0: no more rows; -1: a wait gave up.
+        auto pass1 = [&](RowItem& item) {
+            for (;;) {
+                if (!queue_next(S.queue, place, P.wait_ns, item)) return -1;
+                if (item.row < 0) return 0;
+                if (item.live) break;
+                if (kGrad) {
+                    T* g = static_cast<T*>(a.out_grad) + int64_t(item.row) * a.grad_stride;
+                    const RowSpan span = row_span(g, a.vocab);
+                    // (the gradient's own vectors, dealt to the cluster's CTAs)
+                    for (int i = int(rank) * kConsumers + tid; i < span.count; i += int(parts) * kConsumers)
+                        put_vector<T>(g, vocab, span.head, i, true, make_uint4(0u, 0u, 0u, 0u));
+                }
+            }
+            RowJob h;
+            h.token = item.token;
+            row_scale(h, a, item.temperature);
+            const T* x = static_cast<const T*>(a.logits) + int64_t(item.row) * a.row_stride;
+            const RowSpan span = row_span(x, a.vocab);
+            const int n = min(first_vec + P.part_vecs, span.count) - first_vec;
+            const int end = span.head + vocab;
+            const Two c_hi = two(h.c_hi, h.c_hi), c_lo = two(h.c_lo, h.c_lo);
+            if (!wait(&S.marked[map1.at], map1.phase, P.wait_ns) || !wait(&S.full[buf1.at], buf1.phase, P.wait_ns)) return -1;
+            const uint4* in = reinterpret_cast<const uint4*>(smem + buf1.at * buffer_bytes);
+            unsigned char* bits = maps + map1.at * map_bytes(P.part_vecs);
+            Stats st = stats_empty();
+            bool bad = false;
+            for (int i0 = 0; i0 < n; i0 += kStep) {
+                uint4 v[kVecs];
+#pragma unroll
+                for (int k = 0; k < kVecs; ++k) {
+                    const int i = i0 + k * kConsumers + tid;
+                    v[k] = nothing<T>();
+                    if (i < n) {
+                        v[k] = in[i];
+                        const int at = (first_vec + i) * kPer;
+                        if (at < span.head || at + kPer > end) Elems<T>::mask(v[k], span.head - at, end - at);
+                        const uint32_t b = bits[i];
+                        if (b) {
+                            blend<T>(v[k], nothing<T>(), b);
+                            if (!kGrad) bits[i] = 0;
+                        }
+                    }
+                }
+                fold<T, false, kVecs>(st, bad, v, c_hi, c_lo, h.c);
+            }
+            if (bad) st.s = quiet_nan();
+            stats_warp<false>(st, h.c);
+            // (A buffer of sums is written again four rows later: by then every closer of the cluster is done with it, as
+            // each puts a row's list sums after closing the row two before, and a warp puts a row's after that two before
+            // is closed.)
+            if (uint32_t(lane) < parts)
+                put_sums(dsmem_map(smem_addr(sums + (put.at * parts + rank) * kWarps + warp), lane),
+                         dsmem_map(smem_addr(&S.join[put.at]), lane), st.ref, st.s, 0.f, 0.f);
+            __syncwarp();
+            if (!kGrad && lane == 0) {
+                mbar_arrive(&S.empty[buf1.at]);
+                mbar_arrive(&S.unmarked[map1.at]);
+            }
+            buf1.next(buffers);
+            map1.next(kMaps);
+            put.next(kSums);
+            return 1;
+        };
+        // Its pass 2, once it is closed; false where the wait gave up.
+        auto pass2 = [&](const RowItem& item) {
+            if (!wait(&S.closed[closed.at], closed.phase, P.wait_ns)) return false;
+            if (kGrad) {
+                const Factor f = S.factor[closed.at];
+                const Factors fs{two(-f.ref, -f.ref), two(f.c, f.c), two(f.k, f.k), 0};
+                const T* x = static_cast<const T*>(a.logits) + int64_t(item.row) * a.row_stride;
+                T* g = static_cast<T*>(a.out_grad) + int64_t(item.row) * a.grad_stride;
+                const RowSpan span = row_span(x, a.vocab);
+                const int n = min(first_vec + P.part_vecs, span.count) - first_vec;
+                const bool whole = ((reinterpret_cast<uintptr_t>(g) - reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
+                const int token_vec = f.token == kNoToken ? -1 : (f.token + span.head) / kPer - first_vec;
+                const uint4* in = reinterpret_cast<const uint4*>(smem + buf2.at * buffer_bytes);
+                unsigned char* bits = maps + map2.at * map_bytes(P.part_vecs);
+#pragma unroll 4
+                for (int i = tid; i < n; i += kConsumers) {
+                    const uint4 v = in[i];
+                    const uint32_t b = bits[i];
+                    uint4 y;
+                    if (i == token_vec)
+                        y = gradient_token<T, false>(v, fs, f.token + span.head - (first_vec + i) * kPer, f.at_token);
+                    else
+                        y = gradient<T, false>(v, fs);
+                    if (b) {
+                        blend<T>(y, v, b);
+                        bits[i] = 0;
+                    }
+                    put_vector<T>(g, vocab, span.head, first_vec + i, whole, y);
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&S.empty[buf2.at]);
+                    mbar_arrive(&S.unmarked[map2.at]);
+                }
+                buf2.next(buffers);
+                map2.next(kMaps);
+            }
+            closed.next(kSums);
+            return true;
+        };
+        RowItem now, next;
+        int more = pass1(now);
+        while (more == 1) {
+            more = pass1(next);
+            if (more < 0 || !pass2(now)) {
+                more = -1;
+                break;
+            }
+            now = next;
+        }
+        if (more < 0) gave_up(S);
+    }
+    __syncwarp();
+    cluster_sync();
+    if (S.failed) abandon<T, kGrad>(P, q, n_clusters, parts, rank);
+    if (rank == 0 && last_block(P.ws.ticket, n_clusters, &S.flag)) {
+        const double loss = sum_terms<kThreads>(P.ws.terms, a.n_rows, S.scratch);
+        if (tid == 0) D.out_loss[0] = float(loss);
+    }
+}
+
+}  // namespace distill
+
+int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, cudaStream_t stream)
+{
+    using namespace distill;
+    DistillParams p = params;
+    const bool bf16 = p.rows.dtype == SAMPLER_DTYPE_BF16, grad = p.rows.out_grad != nullptr;
+    const int per = bf16 ? 8 : 4;
+    const int64_t vecs = (p.rows.vocab + 2 * per - 2) / per;  // the most that a row touches, wherever it starts
+    // CTAs of a cluster: so many that two on an SM have three buffers each, and more where rows are few; one CTA on an SM
+    // where a row is too long for that
+    auto part_of = [&](int parts) { return int((vecs + parts - 1) / parts); };
+    auto fits = [&](int parts, int buffers, int smem) { return smem_of(part_of(parts), buffers, parts) <= smem; };
+    int parts = 1;
+    while (parts < kMaxParts && !fits(parts, 3, kSmemTwo)) parts *= 2;
+    const bool two = fits(parts, 2, kSmemTwo);
+    while (parts < kMaxParts && p.rows.n_rows * parts < 2 * sms && part_of(2 * parts) >= 256) parts *= 2;
+    const int budget = two ? kSmemTwo : kSmemOne;
+    p.part_vecs = part_of(parts);
+    p.buffers = 2;
+    while (p.buffers < kMaxBuffers && fits(parts, p.buffers + 1, budget)) ++p.buffers;
+    if (!fits(parts, 2, budget)) return SAMPLER_ERR_TOO_LARGE;  // (no row of the vocabularies that handles take)
+    const auto kernel = bf16 ? grad ? distill_kernel<uint16_t, true> : distill_kernel<uint16_t, false>
+                             : grad ? distill_kernel<float, true> : distill_kernel<float, false>;
+    cudaLaunchConfig_t cfg{};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = size_t(budget);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim = {unsigned(parts), 1u, 1u};
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    const int size = parts == 1 ? 0 : parts == 2 ? 1 : parts == 4 ? 2 : parts == 8 ? 3 : 4;
+    int& resident = occ->clusters[bf16][grad][size][two];
+    if (resident < 1) {  // once for each kernel and shape of the launch of a handle
+        const void* k = reinterpret_cast<const void*>(kernel);
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne) != cudaSuccess ||
+            (parts > 8 && cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
+            return SAMPLER_ERR_CUDA;
+        cfg.gridDim = dim3(unsigned(parts));
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return SAMPLER_ERR_CUDA;
+        resident = n;
+    }
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(p.rows.n_rows, resident) * parts));
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
+}
+
+}  // namespace dst

@@ -32,6 +32,9 @@ struct sampler_s {
     dst::RowOccupancy row_occ;
     dst::ScaledHeadGrants head_grants;
     dst::MicroHeadGrants micro_grants;
+    dst::TopWorkspace top_ws;  // parts of rows of sampler_score_top
+    dst::TopGrants top_grants;
+    dst::DistillOccupancy distill_occ;
     // staging for sampler_sample_host
     unsigned char* stage_base;
     size_t stage_bytes;

@@ -158,6 +158,51 @@ int pairs_launch(const sampler_rows_t& rows, const sampler_preference_t& pref, c
 // dependent: pairs_launch has been called just before on the stream.
 int pairs_grad_launch(const sampler_rows_t& rows, const RowWorkspace& ws, bool dependent, cudaStream_t stream);
 
+// ---------------------------------------------------------------- the most likely tokens
+// What a part of a row leaves: sums of what is not among its largest, and those.
+struct TopPart {
+    float ref, s, t;
+    int32_t count, bad, failed;  // bad: a NaN or +inf logit; failed: a wait gave up
+};
+constexpr int kTopUnits = 1024;  // parts of rows that a call may have, where it cuts rows
+
+struct TopWorkspace {
+    TopPart* parts;     // [kTopUnits]
+    uint64_t* keys;     // [kTopUnits][SAMPLER_MAX_ALTERNATIVES]
+    uint32_t* tickets;  // [kTopUnits] parts of a row that are done; zero between launches
+};
+
+struct TopParams {
+    sampler_rows_t rows;
+    sampler_top_t top;
+    TopWorkspace ws;
+    int parts, part_vecs;  // of a row, worked out by the launch
+    uint64_t wait_ns;
+};
+
+// Whether a handle has granted the kernel its shared memory, by the logits' type and entropy.
+struct TopGrants {
+    bool granted[2][2];
+};
+
+int top_launch(const TopParams& params, int sms, TopGrants* grants, cudaStream_t stream);
+
+// ---------------------------------------------------------------- distillation
+struct DistillParams {
+    sampler_rows_t rows;
+    sampler_distill_t distill;
+    RowWorkspace ws;  // its terms and ticket
+    int part_vecs, buffers;  // worked out by the launch
+    uint64_t wait_ns;
+};
+
+// Clusters that the device holds at once, by the logits' type, gradient and shape of the launch; 0 = not asked yet.
+struct DistillOccupancy {
+    int clusters[2][2][5][4];
+};
+
+int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, cudaStream_t stream);
+
 // ---------------------------------------------------------------- 8-bit LM head
 int quantize_launch(const sampler_quantize_t& q, int sms, cudaStream_t stream);
 

@@ -117,6 +117,9 @@ void free_handle(sampler_s* h)
     cudaFree(h->row_ws.terms);
     cudaFree(h->row_ws.pair_terms);
     cudaFree(h->row_ws.ticket);
+    cudaFree(h->top_ws.parts);
+    cudaFree(h->top_ws.keys);
+    cudaFree(h->top_ws.tickets);
     cudaFree(h->stage_base);
     delete h;
 }
@@ -191,7 +194,7 @@ int noalloc_grant_smem(int dev, int dtype, size_t smem)
 
 extern "C" {
 
-uint32_t sampler_abi_version(void) { return (1u << 16) | 4u; }
+uint32_t sampler_abi_version(void) { return (1u << 16) | 5u; }
 
 int sampler_get_stat(sampler_t h, int which, uint64_t* value, int reset)
 {
@@ -275,6 +278,10 @@ int sampler_create(sampler_t* out, const sampler_config_t* cfg)
             cudaMalloc(&h->row_ws.pair_terms, loss_rows * sizeof(double)) != cudaSuccess ||
             cudaMalloc(&h->row_ws.ticket, sizeof(uint32_t)) != cudaSuccess ||
             cudaMemset(h->row_ws.ticket, 0, sizeof(uint32_t)) != cudaSuccess ||
+            cudaMalloc(&h->top_ws.parts, dst::kTopUnits * sizeof(dst::TopPart)) != cudaSuccess ||
+            cudaMalloc(&h->top_ws.keys, dst::kTopUnits * SAMPLER_MAX_ALTERNATIVES * sizeof(uint64_t)) != cudaSuccess ||
+            cudaMalloc(&h->top_ws.tickets, dst::kTopUnits * sizeof(uint32_t)) != cudaSuccess ||
+            cudaMemset(h->top_ws.tickets, 0, dst::kTopUnits * sizeof(uint32_t)) != cudaSuccess ||
             cudaDeviceSynchronize() != cudaSuccess) {
             free_handle(h);
             return SAMPLER_ERR_CUDA;

@@ -23,14 +23,15 @@ size_t bytes_of(int dtype) { return dtype == SAMPLER_DTYPE_BF16 ? 2 : 4; }
 
 cudaStream_t cuda_stream(sampler_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
-int check_rows(sampler_t h, const sampler_rows_t* a)
+// need_tokens: the call cannot do without them (others: where out_logprob is asked for).
+int check_rows(sampler_t h, const sampler_rows_t* a, bool need_tokens = true)
 {
     if (!h || !a) return SAMPLER_ERR_NULL_ARG;
     if (a->n_rows < 0 || a->vocab < 1 || a->row_stride < a->vocab) return SAMPLER_ERR_BAD_SHAPE;
     if (!known(a->dtype)) return SAMPLER_ERR_BAD_DTYPE;
     if (a->n_rows > h->max_rows || a->n_rows > INT_MAX || a->vocab > h->max_vocab) return SAMPLER_ERR_TOO_LARGE;
     if (a->n_rows == 0) return SAMPLER_OK;
-    if (!a->logits || !a->tokens) return SAMPLER_ERR_NULL_ARG;
+    if (!a->logits || (!a->tokens && (need_tokens || a->out_logprob))) return SAMPLER_ERR_NULL_ARG;
     const size_t es = bytes_of(a->dtype);
     if (!aligned(a->logits, es) || !aligned(a->tokens, 4) || !aligned(a->temperature, 4) || !aligned(a->weight, 4) ||
         !aligned(a->out_logprob, 4) || !aligned(a->out_entropy, 4) || !aligned(a->out_status, 4))
@@ -194,6 +195,55 @@ int sampler_preference_loss(sampler_t h, const sampler_rows_t* rows, const sampl
     rc = q->n_pairs > 0 ? dst::pairs_launch(*rows, *q, h->row_ws, s) : write_zero(q->out_loss, s);
     if (rc != SAMPLER_OK || !rows->out_grad || rows->n_rows == 0) return rc;
     return dst::pairs_grad_launch(*rows, h->row_ws, q->n_pairs > 0, s);
+}
+
+int sampler_score_top(sampler_t h, const sampler_rows_t* rows, const sampler_top_t* top, sampler_stream_t stream)
+{
+    const int rc = check_rows(h, rows, false);
+    if (rc != SAMPLER_OK) return rc;
+    if (!top) return SAMPLER_ERR_NULL_ARG;
+    if (rows->out_grad) return SAMPLER_ERR_UNSUPPORTED;
+    if (top->top_n < 1 || top->top_n > SAMPLER_MAX_ALTERNATIVES) return SAMPLER_ERR_BAD_VALUE;
+    if (rows->n_rows == 0) return SAMPLER_OK;
+    if (!top->out_top_ids || !top->out_top_logprobs) return SAMPLER_ERR_NULL_ARG;
+    if (!aligned(top->out_top_ids, 4) || !aligned(top->out_top_logprobs, 4) || !aligned(top->out_rest_logprob, 4))
+        return SAMPLER_ERR_BAD_SHAPE;
+    DeviceGuard guard;
+    if (cudaSetDevice(h->device) != cudaSuccess) return SAMPLER_ERR_CUDA;
+    dst::TopParams p;
+    std::memset(&p, 0, sizeof p);
+    p.rows = *rows;
+    p.top = *top;
+    p.ws = h->top_ws;
+    p.wait_ns = h->wait_ns;
+    return dst::top_launch(p, h->num_sms, &h->top_grants, cuda_stream(stream));
+}
+
+int sampler_distill_loss(sampler_t h, const sampler_rows_t* rows, const sampler_distill_t* q, sampler_stream_t stream)
+{
+    const int rc = check_rows(h, rows, false);
+    if (rc != SAMPLER_OK) return rc;
+    if (rows->n_rows > h->row_ws.rows) return SAMPLER_ERR_TOO_LARGE;
+    if (!q || !q->out_loss) return SAMPLER_ERR_NULL_ARG;
+    if (rows->out_entropy) return SAMPLER_ERR_UNSUPPORTED;
+    if (q->top_n < 1 || q->top_n > SAMPLER_MAX_ALTERNATIVES || !(q->token_coef >= 0.f) || !std::isfinite(q->token_coef) ||
+        !std::isfinite(q->grad_scale))
+        return SAMPLER_ERR_BAD_VALUE;
+    if (rows->n_rows > 0 && (!q->teacher_ids || !q->teacher_logprobs || (q->token_coef != 0.f && !rows->tokens)))
+        return SAMPLER_ERR_NULL_ARG;
+    if (!aligned(q->teacher_ids, 4) || !aligned(q->teacher_logprobs, 4) || !aligned(q->teacher_rest, 4) ||
+        !aligned(q->grad_scale_dev, 4) || !aligned(q->out_loss, 4) || !aligned(q->out_kl, 4))
+        return SAMPLER_ERR_BAD_SHAPE;
+    DeviceGuard guard;
+    if (cudaSetDevice(h->device) != cudaSuccess) return SAMPLER_ERR_CUDA;
+    if (rows->n_rows == 0) return write_zero(q->out_loss, cuda_stream(stream));
+    dst::DistillParams p;
+    std::memset(&p, 0, sizeof p);
+    p.rows = *rows;
+    p.distill = *q;
+    p.ws = h->row_ws;
+    p.wait_ns = h->wait_ns;
+    return dst::distill_launch(p, h->num_sms, &h->distill_occ, cuda_stream(stream));
 }
 
 int sampler_quantize_blocks(sampler_t h, const sampler_quantize_t* q, sampler_stream_t stream)

@@ -483,6 +483,56 @@ int sampler_preference_loss(sampler_t h, const sampler_rows_t* rows, const sampl
                             sampler_stream_t stream);
 
 /*
+ * Each row's most likely tokens: the top_n of largest logit, by value desc, index asc,
+ * with their logprobs, and the logprob of all other tokens together (ln of their
+ * mass, taken as a sum of its own; -inf where there is none). Past the tokens with
+ * a logit above -inf, ids are -1 and logprobs -inf. Rows that are left out get ids
+ * -1 and zeros, rows with a status ids -1 and NaN. rows->tokens may be NULL, with
+ * rows->out_logprob NULL; rows->out_logprob and out_entropy are as in sampler_score;
+ * rows->out_grad must be NULL (SAMPLER_ERR_UNSUPPORTED).
+ */
+#define SAMPLER_MAX_ALTERNATIVES 128
+typedef struct {
+    int32_t top_n;             /* 1 .. SAMPLER_MAX_ALTERNATIVES */
+    int32_t* out_top_ids;      /* [N * top_n] */
+    float* out_top_logprobs;   /* [N * top_n] */
+    float* out_rest_logprob;   /* [N] NULL = not reported */
+} sampler_top_t;
+
+int sampler_score_top(sampler_t h, const sampler_rows_t* rows, const sampler_top_t* top, sampler_stream_t stream);
+
+/*
+ * Distillation from a teacher's most likely tokens. Row i has a list of tokens id_j
+ * with the teacher's logprobs l_j, as sampler_score_top gives them (entries with id
+ * -1 are not there), and, with teacher_rest, the teacher's logprob r of all other
+ * tokens together. With p the student's probabilities at the row's temperature,
+ *     KL_i = sum_j e^l_j (l_j - ln p_id_j) + e^r (r - ln sum_{v not in the list} p_v)
+ *     loss = sum_i weight_i * (KL_i - token_coef * ln p_t)
+ * (0 times an infinity is 0). Without teacher_rest the second term is not there: the
+ * loss is then the list's share. token_coef (>= 0) mixes in the row's own token t;
+ * rows->tokens may be NULL where it is 0 and out_logprob is NULL.
+ * A list with a token twice or outside [0, vocab), or with a logprob (r among them)
+ * that is NaN or +inf, makes its row SAMPLER_ROW_BAD_PARAM. rows->out_entropy must be
+ * NULL (SAMPLER_ERR_UNSUPPORTED).
+ * A token that has no mass in the student gets the gradient of its logprob's limit,
+ * as in sampler_score_grad; where the loss is infinite for that, it is reported so.
+ */
+typedef struct {
+    int32_t top_n;                  /* 1 .. SAMPLER_MAX_ALTERNATIVES */
+    const int32_t* teacher_ids;     /* [N * top_n] */
+    const float* teacher_logprobs;  /* [N * top_n] */
+    const float* teacher_rest;      /* [N] NULL = not used */
+    float token_coef;
+    float grad_scale;
+    const float* grad_scale_dev;    /* one device float, NULL = 1 */
+    float* out_loss;                /* one float */
+    float* out_kl;                  /* [N] NULL = not reported */
+} sampler_distill_t;
+
+int sampler_distill_loss(sampler_t h, const sampler_rows_t* rows, const sampler_distill_t* distill,
+                         sampler_stream_t stream);
+
+/*
  * The LM head in 8 bits: e4m3 values (4-bit exponent, 3-bit mantissa, largest
  * 448, no infinities) with one fp32 scale for each block of 128.
  *

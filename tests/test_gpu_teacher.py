@@ -1,0 +1,546 @@
+"""The most likely tokens of rows and distillation from them, on the GPU against their
+definitions in double precision (oracle/teacher.py). Needs a GB300.
+
+Tokens are equal. Tolerances of the other outputs, from the kernels' fp32 arithmetic (EPS =
+2^-24, one rounding; depths in nats below the row's largest):
+ - an exponential: 2^-22 of itself (ex2.approx; exp2f and expf are within that), and three
+   roundings of its argument;
+ - a sum of A terms one after another: 4 sqrt(A) EPS of itself (Higham and Mary, lambda = 4),
+   A at most V / 256 + 64 in a thread and the joins after it;
+ - a row's sum S and the sum outside the list, each of the two; a logprob adds the roundings
+   of its own two terms and of the output;
+ - a divergence is added up in double from logprobs that share ln S, masses q within 4 EPS;
+ - the gradient is p W - q from p and q with these errors (outside the list p_v / p_out times
+   W p_out - q_out), and half a step of its type.
+"""
+import numpy as np
+import pytest
+
+import oracle.teacher as O
+import workloads
+
+pytestmark = pytest.mark.gpu
+EPS, EXP = 2.0 ** -24, 2.0 ** -22
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+TINY = 2.0 ** -125  # below it fp32 has fewer digits, and exponentials are 0
+
+
+@pytest.fixture(scope="module")
+def sampler():
+    from decode_step_token_gb300 import build
+    build.build_library()
+    import decode_step_token_gb300 as d
+    s = d.Sampler(max_rows=2048, max_vocab=262144)
+    yield s
+    s.close()
+
+
+def _round(x, kind):
+    if kind == "f32":
+        return x.astype(np.float32)
+    return workloads.bf16_bits_to_f32(workloads.to_bf16_bits(x.astype(np.float32))).reshape(x.shape)
+
+
+def _dev(a):
+    import torch
+
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).to("cuda:0")
+
+
+def _buffer(n, V, kind, pad, shift, fill):
+    """(whole buffer, its [n, V] part with rows V + pad apart)."""
+    import torch
+
+    t = torch.bfloat16 if kind == "bf16" else torch.float32
+    flat = torch.full((n * (V + pad) + shift + 64,), fill, dtype=t, device="cuda:0")
+    return flat, flat[shift:shift + n * (V + pad)].view(n, V + pad)[:, :V]
+
+
+def _logits(x, kind, pad=0, shift=0):
+    import torch
+
+    flat, view = _buffer(*x.shape, kind, pad, shift, float("nan"))
+    view.copy_(torch.from_numpy(x))
+    return view
+
+
+def _depths(logp):
+    return np.where(np.isfinite(logp), logp.max() - logp, 0.0)
+
+
+def _sum_error(p, depth, V):
+    """Relative error of the sum of p's exponentials."""
+    total = p.sum()
+    return EXP + 3 * EPS * ((p * depth).sum() / total if total > 0 else 0) + 4.0 * np.sqrt(V / 256 + 64) * EPS
+
+
+def _same(a, b, tol, what):
+    assert np.array_equal(np.isnan(a), np.isnan(b)), what
+    fine = np.isfinite(b)
+    assert np.array_equal(a[~fine & ~np.isnan(b)], b[~fine & ~np.isnan(b)]), what
+    bad = ~(np.abs(a[fine] - b[fine]) <= np.broadcast_to(tol, b.shape)[fine])
+    assert not bad.any(), (what, np.argwhere(fine)[bad][:5], a[fine][bad][:5], b[fine][bad][:5])
+
+
+# ------------------------------------------------------------------------------- the most likely tokens
+def _run_top(sampler, x, kind, n, pad=0, shift=0, tokens=None, T=None, weight=None, entropy=True, stream=None):
+    import torch
+
+    rows = x.shape[0]
+    out = dict(ids=torch.full((rows, n), -7, dtype=torch.int32, device="cuda:0"),
+               logprobs=torch.full((rows, n), -7.0, device="cuda:0"), rest=torch.full((rows,), -7.0, device="cuda:0"),
+               status=torch.full((rows,), -7, dtype=torch.int32, device="cuda:0"))
+    if tokens is not None:
+        out["logprob"] = torch.full((rows,), -7.0, device="cuda:0")
+    if entropy:
+        out["entropy"] = torch.full((rows,), -7.0, device="cuda:0")
+    sampler.score_top(logits=_logits(x, kind, pad, shift), top_n=n, tokens=_dev(tokens), temperature=_dev(T),
+                      weight=_dev(weight), out_top_ids=out["ids"], out_top_logprobs=out["logprobs"],
+                      out_rest_logprob=out["rest"], out_logprob=out.get("logprob"), out_entropy=out.get("entropy"),
+                      out_status=out["status"])
+    return {k: v.cpu().numpy() if v.dtype == torch.int32 else v.double().cpu().numpy() for k, v in out.items()}
+
+
+def _check_top(got, x, n, tokens=None, T=None, weight=None):
+    rows, V = x.shape
+    want = O.top(x, n, tokens, T, weight)
+    np.testing.assert_array_equal(got["status"], want["status"])
+    np.testing.assert_array_equal(got["ids"], want["ids"])
+    for r in range(rows):
+        if want["status"][r] != 0 or (weight is not None and weight[r] == 0):
+            for k in ("logprobs", "rest", "logprob", "entropy"):
+                if k in got:
+                    np.testing.assert_array_equal(got[k][r], want[k][r])
+            continue
+        y = x[r].astype(np.float64) / (1.0 if T is None or T[r] < np.float32(1e-5) else float(T[r]))
+        logp = y - y.max()
+        logp = logp - O.log_sum(logp)
+        p, depth = np.exp(logp), _depths(logp)
+        s = _sum_error(p, depth, V)
+        ids = want["ids"][r][want["ids"][r] >= 0]
+        m = len(ids)
+        _same(got["logprobs"][r, :m], want["logprobs"][r, :m], s + 2 * EPS + 3 * EPS * depth[ids] + EPS * np.abs(logp[ids]), "logprobs")
+        assert (got["logprobs"][r, m:] == -np.inf).all()
+        outside = np.ones(V, bool)
+        outside[ids] = False
+        if want["rest"][r] > -80:
+            # the exponentials are relative to the list's least, which is within the row
+            near = depth[ids].max() if m else 0
+            s_out = _sum_error(p[outside], depth[outside], V) + 3 * EPS * near
+            _same(got["rest"][r:r + 1], want["rest"][r:r + 1], s + s_out + 4 * EPS + EPS * abs(want["rest"][r]), "rest")
+        else:
+            assert got["rest"][r] < -79
+        if "logprob" in got:
+            t = tokens[r]
+            _same(got["logprob"][r:r + 1], np.maximum(want["logprob"][r:r + 1], -np.inf),
+                  s + 2 * EPS + 3 * EPS * depth[t] + EPS * np.abs(want["logprob"][r]), "logprob")
+        if "entropy" in got:
+            far = (p * depth).sum() + depth[ids].max()
+            tol = s * (1 + far) + far * (EXP + s) + 6 * EPS * ((p * depth ** 2).sum() + far ** 2) + EPS * abs(want["entropy"][r])
+            _same(got["entropy"][r:r + 1], want["entropy"][r:r + 1], tol + 2 * EPS, "entropy")
+
+
+TOPS = [  # rows, vocabulary, n, type, pad, shift, heat, kept, banned, entropy
+    (1, 1, 1, "f32", 0, 0, False, 1.0, 0.0, True), (3, 2, 5, "bf16", 0, 1, True, 1.0, 0.0, True),
+    (2, 7, 128, "f32", 3, 1, False, 1.0, 0.3, True), (5, 100, 20, "bf16", 5, 3, True, 1.0, 0.0, False),
+    (4, 1000, 128, "f32", 0, 0, False, 1.0, 0.0, True), (9, 1023, 1, "bf16", 1, 0, True, 0.6, 0.2, True),
+    (70, 2051, 64, "bf16", 0, 5, True, 0.8, 0.0, True), (33, 8191, 100, "f32", 2, 2, True, 0.7, 0.5, True),
+    (1, 50257, 128, "bf16", 0, 0, False, 1.0, 0.0, True), (1, 151936, 20, "bf16", 0, 0, True, 1.0, 0.0, False),
+    (32, 151936, 20, "bf16", 0, 0, True, 1.0, 0.0, False), (7, 128000, 128, "f32", 1, 1, True, 1.0, 0.1, True),
+    (2, 262144, 17, "f32", 0, 0, False, 1.0, 0.0, True), (3, 262143, 128, "bf16", 1, 7, True, 1.0, 0.9, True),
+    (310, 9001, 40, "bf16", 0, 0, True, 0.9, 0.0, False), (1500, 700, 64, "f32", 1, 0, False, 0.9, 0.0, True),
+    (400, 33000, 64, "bf16", 8, 0, False, 0.5, 0.0, False), (200, 20000, 128, "f32", 0, 0, True, 1.0, 0.999, True)]
+
+
+@pytest.mark.parametrize("shape", TOPS)
+def test_top(sampler, shape):
+    rows, V, n, kind, pad, shift, heat, kept, banned, entropy = shape
+    rng = np.random.default_rng(rows * 31 + V)
+    x = 2.0 * rng.standard_normal((rows, V))
+    if banned:
+        x[rng.random((rows, V)) < banned] = -np.inf
+    tokens = rng.integers(0, V, rows).astype(np.int32)
+    x[np.arange(rows), tokens] = rng.uniform(0, 9, rows)
+    x = _round(x, kind)
+    T = rng.uniform(0.5, 1.6, rows).astype(np.float32) if heat else None
+    weight = None
+    if kept < 1:
+        weight = (rng.random(rows) < kept).astype(np.float32)
+        x[weight == 0] = np.nan
+    tokens = tokens if rows % 2 else None
+    got = _run_top(sampler, x, kind, n, pad, shift, tokens, T, weight, entropy)
+    _check_top(got, x, n, tokens, T, weight)
+
+
+@pytest.mark.parametrize("V,n", [(300, 128), (9000, 5), (40000, 128), (151936, 64)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [6, 700])
+def test_top_orders_and_ties(sampler, V, n, kind, rows):
+    """Rows in rising and falling order, flat ones, few different values, zeros of both signs, one finite token."""
+    if rows * V > 30_000_000:
+        rows = 320
+    rng = np.random.default_rng(V)
+    x = np.empty((rows, V))
+    up = np.sort(3 * rng.standard_normal(V))
+    for r in range(rows):
+        x[r] = [lambda: up, lambda: up[::-1], lambda: np.full(V, 1.5), lambda: rng.integers(0, 3, V),
+                lambda: np.where(rng.random(V) < 0.5, 0.0, -0.0), lambda: np.where(np.arange(V) == V - 2, 1.0, -np.inf)][r % 6]()
+    x = _round(x, kind)
+    if rows > 6:  # only some of the rows on the host
+        some = np.concatenate([np.arange(12), np.arange(rows - 6, rows)])
+        got = _run_top(sampler, x, kind, n)
+        got = {k: v[some] for k, v in got.items()}
+        x = x[some]
+    else:
+        got = _run_top(sampler, x, kind, n)
+    _check_top(got, x, n)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [200, 30000])
+def test_top_extreme_values(sampler, kind, V):
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((8, V))
+    x[0] *= 1e4  # one token has all the mass
+    x[1] = 3e38 * np.sign(x[1])
+    x[2] = -3e38
+    x[3] = np.where(np.arange(V) % 2 == 0, -3.38e38, -np.inf)
+    x[4] *= 1e-40 if kind == "f32" else 1e-30
+    x[5, 3] = 100.0
+    x = _round(x, kind)
+    T = np.array([1, 1, 1, 1, 1, 1, 0.02, 50], np.float32)
+    got = _run_top(sampler, x, kind, 16, T=T, entropy=False)
+    _check_top(got, x, 16, T=T)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V", [(9, 5000), (9, 100000), (640, 5000)])
+def test_top_status_rows(sampler, kind, rows, V):
+    rng = np.random.default_rng(6)
+    x = rng.standard_normal((rows, V))
+    T, tokens = np.ones(rows, np.float32), rng.integers(0, V, rows).astype(np.int32)
+    x[0, V // 2], x[1, 0], x[2] = np.nan, np.inf, -np.inf
+    T[3], T[4], T[5] = -1, np.nan, np.inf
+    tokens[6], tokens[7] = -1, V
+    T[8] = 1e-6  # greedy: T = 1
+    x = _round(x, kind)
+    _check_top(_run_top(sampler, x, kind, 8, tokens=tokens, T=T), x, 8, tokens, T)
+
+
+# ------------------------------------------------------------------------------- distillation
+class Batch:
+    def __init__(self, seed, rows, V, k, kind="f32", pad=0, shift=0, heat=False, kept=1.0, tail=True, coef=0.0, short=0.0,
+                 scale=2.0, noise=0.7):
+        rng = self.rng = np.random.default_rng(seed)
+        self.kind, self.pad, self.shift, self.coef, self.k = kind, pad, shift, coef, k
+        x = scale * rng.standard_normal((rows, V))
+        self.tokens = rng.integers(0, V, rows).astype(np.int32)
+        x[np.arange(rows), self.tokens] = rng.uniform(0, 9, rows)
+        self.x = _round(x, kind)
+        self.T = rng.uniform(0.5, 1.6, rows).astype(np.float32) if heat else None
+        z = (self.x + noise * rng.standard_normal((rows, V))) / (1.0 if self.T is None else self.T[:, None])
+        lp = z - z.max(1, keepdims=True)
+        lp -= np.log(np.exp(lp).sum(1, keepdims=True))
+        m = min(k, V)
+        best = np.argsort(-lp, 1, kind="stable")[:, :m]
+        self.ids, self.l = np.full((rows, k), -1, np.int32), np.full((rows, k), -np.inf, np.float32)
+        count = np.where(rng.random(rows) < short, rng.integers(0, m + 1, rows), m)
+        self.rest = np.empty(rows, np.float32)
+        for r in range(rows):
+            at = best[r, :count[r]]
+            self.ids[r, :count[r]], self.l[r, :count[r]] = at, lp[r, at]
+            self.rest[r] = O.log_sum(np.delete(lp[r], at))
+        if not tail:
+            self.rest = None
+        self.weight = rng.uniform(0.2, 1.0, rows).astype(np.float32)
+        if kept < 1:
+            self.weight[rng.random(rows) >= kept] = 0
+            self.x[self.weight == 0] = np.nan
+
+    def run(self, sampler, grad=True, in_place=False, scale=1.5, scale_dev=None, out=None):
+        import torch
+
+        rows, V = self.x.shape
+        self.logits = _logits(self.x, self.kind, self.pad, self.shift)
+        self.gflat = None
+        if grad:
+            self.gflat, g = _buffer(rows, V, self.kind, self.pad, self.shift, -7.0)
+            if in_place:
+                g = self.logits
+        else:
+            g = None
+        self.scale = scale * (1.0 if scale_dev is None else scale_dev)
+        o = dict(loss=torch.full((1,), -7.0, device="cuda:0"), kl=torch.full((rows,), -7.0, device="cuda:0"),
+                 logprob=torch.full((rows,), -7.0, device="cuda:0"),
+                 status=torch.full((rows,), -7, dtype=torch.int32, device="cuda:0"))
+        self.call = lambda: sampler.distill_loss(
+            logits=self.logits, teacher_ids=self.d[0], teacher_logprobs=self.d[1], teacher_rest=self.d[2], tokens=self.d[3],
+            token_coef=self.coef, temperature=self.d[4], weight=self.d[5], grad_scale=scale, grad_scale_dev=self.d[6],
+            out_loss=o["loss"], out_kl=o["kl"], out_logprob=o["logprob"], out_status=o["status"], out_grad=g)
+        self.d = [_dev(a) for a in (self.ids, self.l, self.rest, self.tokens, self.T, self.weight,
+                                    None if scale_dev is None else np.array([scale_dev], np.float32))]
+        self.call()
+        self.out, self.grad = o, g
+        return self
+
+    def check(self):
+        import torch
+
+        rows, V = self.x.shape
+        want = O.distill(self.x, self.ids, self.l, self.rest, self.tokens, self.coef, self.T, self.weight, self.scale)
+        got = {k: v.cpu().numpy() if v.dtype == torch.int32 else v.double().cpu().numpy() for k, v in self.out.items()}
+        np.testing.assert_array_equal(got["status"], want["status"])
+        g = None if self.grad is None else self.grad.double().cpu().numpy()
+        loss_tol = EPS * abs(want["loss"])
+        for r in range(rows):
+            w = float(self.weight[r])
+            if w == 0 or want["status"][r]:
+                for k in ("kl", "logprob"):
+                    np.testing.assert_array_equal(got[k][r], want[k][r])
+                if g is not None:
+                    np.testing.assert_array_equal(g[r], want["grad"][r])
+                continue
+            T = 1.0 if self.T is None or self.T[r] < np.float32(1e-5) else float(self.T[r])
+            y = self.x[r].astype(np.float64) / T
+            logp = y - y.max()
+            logp = logp - O.log_sum(logp)
+            p, depth = np.exp(logp), _depths(logp)
+            s = _sum_error(p, depth, V) + 2 * EPS
+            ids, l = self.ids[r][self.ids[r] >= 0], self.l[r][self.ids[r] >= 0].astype(np.float64)
+            q, tail = np.exp(l), -np.inf if self.rest is None else float(self.rest[r])
+            qr = np.exp(tail)
+            outside = np.ones(V, bool)
+            outside[ids] = False
+            s_out, ln_out, top_out = 0.0, -np.inf, 0.0
+            if p[outside].sum() > 0:
+                s_out = _sum_error(p[outside], depth[outside], V) + 2 * EPS
+                ln_out, top_out = O.log_sum(logp[outside]), depth[outside][np.isfinite(logp[outside])].min()
+            total = q.sum() + qr + self.coef
+            with np.errstate(invalid="ignore"):
+                terms = np.where(q > 0, q * np.abs(l - logp[ids]), 0.0)
+                tol = (q.sum() + qr) * s + 6 * EPS * terms.sum() + EPS * abs(want["kl"][r])
+                if qr > 0:
+                    tol += qr * (s_out + 6 * EPS * abs(tail - ln_out))
+            _same(got["kl"][r:r + 1], want["kl"][r:r + 1], tol, "kl")
+            t = self.tokens[r]
+            tol_lp = s + 2 * EPS + 3 * EPS * depth[t] + EPS * abs(want["logprob"][r])
+            _same(got["logprob"][r:r + 1], want["logprob"][r:r + 1], tol_lp, "logprob")
+            loss_tol += w * (tol + self.coef * tol_lp)
+            if g is None:
+                continue
+            gw = w * abs(self.scale) / T
+            err = np.empty(V)
+            each = EXP + s + s_out + 3 * EPS * (depth + 2 * top_out) + 16 * EPS
+            err = (total * p + (qr * np.exp(logp - ln_out) if ln_out > -np.inf else 0.0)) * each
+            err[ids] = total * p[ids] * (EXP + s + 3 * EPS * depth[ids] + 16 * EPS) + q * 16 * EPS
+            err[t] += self.coef * 16 * EPS
+            tol = gw * err * 1.01 + HALF[self.kind] * np.abs(want["grad"][r]) * 1.01 + TINY
+            bad = ~(np.abs(g[r] - want["grad"][r]) <= tol)
+            assert not bad.any(), (r, np.nonzero(bad)[0][:5], g[r][bad][:5], want["grad"][r][bad][:5], tol[bad][:5])
+        _same(got["loss"], np.array([want["loss"]]), loss_tol, "loss")
+        if self.gflat is not None and self.grad.data_ptr() != self.logits.data_ptr():
+            beside = torch.ones_like(self.gflat, dtype=torch.bool)
+            beside[self.shift:self.shift + rows * (V + self.pad)].view(rows, -1)[:, :V] = False
+            assert bool((self.gflat[beside] == -7.0).all()), "written beside the gradient"
+
+
+DISTILS = [  # rows, vocabulary, list, type, pad, shift, heat, kept, tail, coef, short
+    (1, 1, 1, "f32", 0, 0, False, 1.0, True, 0.0, 0.0), (3, 2, 5, "bf16", 0, 1, True, 1.0, True, 0.5, 0.5),
+    (2, 7, 128, "f32", 3, 1, False, 1.0, True, 0.0, 0.0), (5, 100, 20, "bf16", 5, 3, True, 1.0, False, 0.2, 0.0),
+    (4, 1024, 8, "f32", 0, 0, False, 1.0, True, 0.0, 0.0), (9, 1023, 1, "bf16", 1, 0, True, 0.6, True, 0.0, 0.0),
+    (70, 2051, 64, "bf16", 0, 5, True, 0.8, True, 0.1, 0.3), (33, 8191, 100, "f32", 2, 2, True, 0.7, False, 0.3, 0.5),
+    (1, 50257, 128, "bf16", 0, 0, False, 1.0, True, 0.0, 0.0), (1, 151936, 20, "bf16", 0, 0, True, 1.0, True, 1.0, 0.0),
+    (12, 151936, 64, "bf16", 8, 0, True, 1.0, True, 0.0, 0.0), (7, 128000, 100, "f32", 1, 1, True, 1.0, True, 0.1, 0.5),
+    (2, 262144, 17, "f32", 0, 0, False, 1.0, True, 0.0, 0.0), (3, 262143, 128, "bf16", 1, 7, True, 1.0, True, 0.2, 0.0),
+    (2, 262143, 64, "f32", 3, 2, True, 1.0, False, 0.2, 0.0), (310, 9001, 40, "bf16", 0, 0, True, 0.9, True, 0.0, 0.0),
+    (1500, 700, 64, "f32", 1, 0, False, 0.9, True, 0.3, 0.2), (400, 33000, 64, "bf16", 8, 0, False, 0.5, True, 0.1, 0.0),
+    (500, 20011, 128, "f32", 0, 0, True, 1.0, True, 0.0, 0.0)]
+
+
+@pytest.mark.parametrize("shape", DISTILS)
+@pytest.mark.parametrize("grad", [True, False])
+def test_distill(sampler, shape, grad):
+    rows, V, k, kind, pad, shift, heat, kept, tail, coef, short = shape
+    b = Batch(rows * 37 + V, rows, V, k, kind, pad, shift, heat, kept, tail, coef, short)
+    b.run(sampler, grad=grad).check()
+
+
+@pytest.mark.parametrize("V,kind", [(5003, "bf16"), (151937, "bf16"), (128000, "f32"), (300, "f32")])
+def test_distill_in_place_with_a_scale_on_the_device(sampler, V, kind):
+    Batch(V, 9, V, 30, kind, pad=1, heat=True, coef=0.2, kept=0.8).run(sampler, in_place=True, scale_dev=0.75).check()
+
+
+def test_gradient_against_differences(sampler):
+    """The loss itself, as the kernel computes it, moved along the gradient."""
+    b = Batch(3, 6, 900, 12, heat=True, coef=0.3)
+    b.run(sampler, scale=1.0)
+    g = b.grad.double().cpu().numpy()
+    d = b.rng.standard_normal(b.x.shape)
+    x, h = b.x.copy(), 0.05
+    vals = []
+    for sign in (1, -1):
+        b.x = (x + sign * h * d).astype(np.float32)
+        vals.append(b.run(sampler, grad=False, scale=1.0).out["loss"].item())
+    # third derivatives of a log-sum are below 1 along d's few units; the loss has 2^-24 of itself
+    np.testing.assert_allclose((g * d).sum(), (vals[0] - vals[1]) / (2 * h), rtol=2e-2, atol=2e-3)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [3000, 130000])
+def test_distill_status_rows(sampler, kind, V):
+    b = Batch(V, 16, V, 10, kind, coef=0.2)
+    b.T = np.ones(16, np.float32)
+    b.x[0, V // 2], b.x[1, b.ids[1, 4]], b.x[2, 0], b.x[3] = np.nan, np.inf, np.inf, -np.inf
+    b.T[4], b.T[5], b.T[6] = -1, np.nan, 1e-6
+    b.tokens[7], b.tokens[8] = -1, V
+    b.ids[9, 3], b.ids[10, 2], b.ids[11, 7] = V, -2, b.ids[11, 1]  # outside, outside, twice
+    b.l[12, 4], b.l[13, 0], b.rest[14] = np.nan, np.inf, np.nan
+    b.ids[15] = -1  # an empty list
+    b.run(sampler).check()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [400, 60000])
+def test_distill_without_mass(sampler, kind, V):
+    """Tokens of the list, and all tokens outside it, that the student forbids; masses that are far apart."""
+    b = Batch(V, 6, V, 10, kind)
+    b.x[0, b.ids[0, 3]] = -np.inf  # an infinite divergence, with a finite gradient
+    outside = np.ones(V, bool)
+    outside[b.ids[1]] = False
+    b.x[1, outside] = -np.inf
+    b.l[2, 5] = -np.inf            # a token of no mass in the teacher
+    b.x[2, b.ids[2, 5]] = -np.inf
+    b.x[3, b.ids[3]] = 60.0        # nothing is left outside, but for the logarithm
+    b.rest[4] = -np.inf
+    b.x[5, b.ids[5]] = -60.0
+    b.run(sampler).check()
+
+
+def test_teacher_to_student(sampler):
+    """The lists of score_top into distill_loss: the teacher's own rows have no divergence and no gradient."""
+    import torch
+
+    for kind in ("bf16", "f32"):
+        rng = np.random.default_rng(8)
+        x = _round(2 * rng.standard_normal((40, 30011)), kind)
+        T = rng.uniform(0.5, 1.5, 40).astype(np.float32)
+        logits = _logits(x, kind)
+        ids = torch.empty((40, 64), dtype=torch.int32, device="cuda:0")
+        lps, rest, kl = torch.empty((40, 64), device="cuda:0"), torch.empty(40, device="cuda:0"), torch.empty(40, device="cuda:0")
+        loss, grad = torch.empty(1, device="cuda:0"), torch.empty_like(logits)
+        sampler.score_top(logits=logits, top_n=64, temperature=_dev(T), out_top_ids=ids, out_top_logprobs=lps,
+                          out_rest_logprob=rest)
+        sampler.distill_loss(logits=logits, temperature=_dev(T), teacher_ids=ids, teacher_logprobs=lps, teacher_rest=rest,
+                             out_loss=loss, out_kl=kl, out_grad=grad)
+        # both have errors of a sum of 30011 exponentials, and logprobs of up to 15 in fp32
+        assert kl.abs().max().item() < 2 * (EXP + 4 * np.sqrt(30011 / 256 + 64) * EPS + 3 * EPS * 15 + 16 * EPS)
+        lp = torch.log_softmax(logits.double() / _dev(T).double()[:, None], 1).exp()
+        assert (grad.double().abs() * _dev(T).double()[:, None] <= lp * 1e-5 + 1e-30).all()
+
+
+@pytest.mark.parametrize("rows,V", [(3, 151936), (50, 3000), (700, 9001)])
+def test_same_bits_each_time_and_in_a_graph(sampler, rows, V):
+    """Also on another stream, and while an eager call's outputs live on."""
+    import torch
+
+    b = Batch(rows, rows, V, 50, "bf16", heat=True, coef=0.1, kept=0.9)
+    b.run(sampler)
+    top = [torch.empty((rows, 50), dtype=torch.int32, device="cuda:0"), torch.empty((rows, 50), device="cuda:0"),
+           torch.empty(rows, device="cuda:0"), torch.empty(rows, device="cuda:0")]
+
+    def both():
+        sampler.score_top(logits=b.logits, top_n=50, temperature=b.d[4], weight=b.d[5], out_top_ids=top[0],
+                          out_top_logprobs=top[1], out_rest_logprob=top[2], out_entropy=top[3])
+        b.call()
+
+    both()
+    outs = top + [b.out["loss"], b.out["kl"], b.grad]
+    first = [t.clone() for t in outs]
+
+    def same():
+        torch.cuda.synchronize()
+        for t, f in zip(outs, first):
+            assert torch.equal(t.view(torch.uint8), f.view(torch.uint8))
+            t.zero_()
+
+    same()
+    for _ in range(3):
+        both()
+        same()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        both()
+    same()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both()
+    for _ in range(3):
+        graph.replay()
+        same()
+
+
+def test_nothing_to_do(sampler):
+    import torch
+
+    x, f = torch.empty((0, 50), device="cuda:0"), torch.empty(0, device="cuda:0")
+    ids, lps = torch.empty((0, 4), dtype=torch.int32, device="cuda:0"), torch.empty((0, 4), device="cuda:0")
+    loss = torch.full((1,), -7.0, device="cuda:0")
+    sampler.score_top(logits=x, top_n=4, out_top_ids=ids, out_top_logprobs=lps)
+    sampler.distill_loss(logits=x, teacher_ids=ids, teacher_logprobs=lps, out_loss=loss, out_kl=f)
+    assert loss.item() == 0
+    # rows that are all left out
+    x = torch.full((5, 50), float("nan"), device="cuda:0")
+    ids, lps = torch.zeros((5, 4), dtype=torch.int32, device="cuda:0"), torch.zeros((5, 4), device="cuda:0")
+    w, grad = torch.zeros(5, device="cuda:0"), torch.full((5, 50), -7.0, device="cuda:0")
+    sampler.distill_loss(logits=x, teacher_ids=ids, teacher_logprobs=lps, weight=w, out_loss=loss, out_grad=grad)
+    assert loss.item() == 0 and (grad == 0).all()
+    sampler.score_top(logits=x, top_n=4, weight=w, out_top_ids=ids, out_top_logprobs=lps)
+    assert (ids == -1).all() and (lps == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V", [(3, 3000), (3, 151936), (400, 3000)])
+def test_waits_that_give_up(kind, rows, V):
+    import decode_step_token_gb300 as d
+
+    b = Batch(1, rows, V, 20, kind, kept=0.8)
+    with d.Sampler(max_rows=512, max_vocab=262144, short_waits=True) as s:
+        b.run(s)
+        live = b.weight != 0
+        assert (b.out["status"].cpu().numpy() == np.where(live, 5, 0)).all()
+        kl, g = b.out["kl"].cpu().numpy(), b.grad.float().cpu().numpy()
+        assert np.isnan(kl[live]).all() and (kl[~live] == 0).all() and np.isnan(b.out["loss"].item())
+        assert np.isnan(g[live]).all() and (g[~live] == 0).all()
+        got = _run_top(s, b.x, kind, 9, weight=b.weight)
+        assert (got["status"] == np.where(live, 5, 0)).all() and (got["ids"] == -1).all()
+        assert np.isnan(got["logprobs"][live]).all() and (got["logprobs"][~live] == 0).all()
+    with d.Sampler(max_rows=512, max_vocab=262144) as s:  # nothing is left over
+        if rows <= 3:
+            b.run(s).check()
+            _check_top(_run_top(s, b.x, kind, 9, weight=b.weight), b.x, 9, weight=b.weight)
+
+
+def test_argument_checks(sampler):
+    import torch
+
+    x = torch.randn((4, 50), device="cuda:0")
+    ids, lps = torch.zeros((4, 3), dtype=torch.int32, device="cuda:0"), torch.zeros((4, 3), device="cuda:0")
+    loss = torch.empty(1, device="cuda:0")
+    import decode_step_token_gb300 as d
+    top = dict(logits=x, top_n=3, out_top_ids=ids, out_top_logprobs=lps)
+    for change, error in [(dict(top_n=4), ValueError), (dict(top_n=0), d.SamplerError), (dict(out_top_ids=lps), TypeError),
+                          (dict(out_rest_logprob=loss), ValueError), (dict(out_logprob=lps[:, 0].contiguous()), d.SamplerError),
+                          (dict(logits=x.half()), TypeError), (dict(vocab=51), ValueError)]:
+        with pytest.raises(error):
+            sampler.score_top(**{**top, **change})
+    dis = dict(logits=x, teacher_ids=ids, teacher_logprobs=lps, out_loss=loss)
+    for change, error in [(dict(teacher_ids=ids[:3]), ValueError), (dict(teacher_logprobs=lps[:, :2]), ValueError),
+                          (dict(token_coef=0.5), d.SamplerError), (dict(token_coef=-1.0), d.SamplerError),
+                          (dict(teacher_rest=lps), None), (dict(teacher_rest=loss), ValueError),
+                          (dict(out_grad=x.bfloat16()), TypeError), (dict(out_grad=x[:3]), ValueError),
+                          (dict(teacher_ids=ids.t(), teacher_logprobs=lps.t()), ValueError)]:
+        if error is None:
+            continue
+        with pytest.raises(error):
+            sampler.distill_loss(**{**dis, **change})

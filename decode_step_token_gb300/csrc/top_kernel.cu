@@ -36,30 +36,56 @@ using namespace rows;
 
 constexpr int kWarps = 8;
 constexpr int kConsumers = kWarps * 32;
-constexpr int kThreads = kConsumers + 32;
+constexpr int kProducer = kWarps, kCloser = kWarps + 1;
+constexpr int kThreads = kConsumers + 64;
 constexpr int kVecs = 4;                        // of a chunk in each consumer
 constexpr int kChunkVecs = kConsumers * kVecs;
 constexpr int kChunkBytes = kChunkVecs * 16;
 constexpr int kSlots = 5;
 constexpr int kMost = SAMPLER_MAX_ALTERNATIVES;
-constexpr int kCap = 2048;                      // keys in the list
-constexpr int kHeld = kCap / kConsumers;        // of them to a thread
-constexpr double kLostUnit = 1099511627776.0;   // 2^40
+constexpr int kCap = 1024;                      // keys in a list
+constexpr int kMaxToken = 262143;
+constexpr int kMaxTopParts = 32;                // of a row: the lanes of a warp
+constexpr float kLostUnit = 1099511627776.f;    // 2^40
+
+// A row for the closer: its keys are in order, and these are the sums of the rest.
+struct Close {
+    int row;  // -1: no more rows
+    int count, token;
+    float ref, s, t;
+    float temperature, x_t;
+};
 
 struct Shared {
     uint64_t full[kSlots], empty[kSlots];
+    uint64_t ready[2], written[2];  // rows with the closer
     RowQueue queue;
-    uint64_t list[kCap];
-    uint64_t sorted[kMost];
-    float4 sums[kWarps];
+    __align__(16) uint64_t list[2][kCap];  // one is filled, the other is what it is cut into
+    uint64_t sorted[2][kMost];
+    Close close[2];
+    __align__(16) uint32_t largest[kConsumers];  // of a chunk, in each thread, as orders
+    float4 state[kConsumers];   // sums, on their way into functions out of line and back
+    float2 sums[kWarps];
+    uint32_t tops[kWarps];
     uint32_t tally[3];
-    uint32_t count;             // keys put into the list (more than kCap: the last of them are not there)
-    unsigned long long lost_s;  // what fell out of the list, relative to the largest of it, in multiples of 2^-40
-    long long lost_t;
-    uint32_t lost_most;         // its order
+    uint32_t count[2];          // keys put into a list (more than kCap: the last of them are not there)
+    unsigned long long lost_s[kWarps];  // what fell out of a list, relative to the largest of it, in multiples of 2^-40
+    long long lost_t[kWarps];
+    uint32_t lost_most;                 // its order; 0 between cuts
     uint32_t flag;
+    float part_ref[kMaxTopParts], part_s[kMaxTopParts], part_t[kMaxTopParts];
+    int part_count[kMaxTopParts], part_flags[kMaxTopParts];
 };
 constexpr int kSmem = kSlots * kChunkBytes + int(sizeof(Shared));
+
+__device__ __forceinline__ unsigned char* ring_of()
+{
+    extern __shared__ __align__(128) unsigned char ring[];
+    return ring;
+}
+
+// (Asked for wherever it is needed, so that functions that stay out of line know it to be in shared memory.)
+__device__ __forceinline__ Shared& shared() { return *reinterpret_cast<Shared*>(ring_of() + kSlots * kChunkBytes); }
 
 __device__ __forceinline__ void bar_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kConsumers) : "memory"); }
 
@@ -106,33 +132,58 @@ __device__ __forceinline__ uint64_t key_of(float x, int token) { return uint64_t
 __device__ __forceinline__ float key_value(uint64_t k) { return value_of(uint32_t(k >> 32)); }
 __device__ __forceinline__ int key_token(uint64_t k) { return int(~uint32_t(k)); }
 
+// A bar as vectors are compared with it: `x > bar` for every x of the type.
 template <typename T>
-__device__ __forceinline__ float element(const uint4& v, int j);
+__device__ __forceinline__ uint32_t packed_bar(float bar);
 template <>
-__device__ __forceinline__ float element<float>(const uint4& v, int j)
+__device__ __forceinline__ uint32_t packed_bar<float>(float bar)
 {
-    return __uint_as_float(j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w);
+    return __float_as_uint(bar);
 }
 template <>
-__device__ __forceinline__ float element<uint16_t>(const uint4& v, int j)
+__device__ __forceinline__ uint32_t packed_bar<uint16_t>(float bar)
 {
-    const uint32_t w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
-    return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+    uint32_t u = __float_as_uint(bar);  // rounded down: the same bf16 values are above it
+    if ((u >> 31) && (u & 0xffffu)) u += 0x10000u;
+    u >>= 16;
+    return u << 16 | u;
 }
 
-// Element j becomes -inf.
+// Which elements of a vector are above the bar (a bit for each); those become -inf.
 template <typename T>
-__device__ __forceinline__ void clear(uint4& v, int j);
+__device__ __forceinline__ uint32_t take_above(uint4& v, uint32_t bar);
 template <>
-__device__ __forceinline__ void clear<float>(uint4& v, int j)
+__device__ __forceinline__ uint32_t take_above<float>(uint4& v, uint32_t bar)
 {
-    (j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w) = 0xff800000u;
+    const float b = __uint_as_float(bar);
+    uint32_t bits = 0;
+    auto word = [&](uint32_t& w, uint32_t bit) {
+        if (__uint_as_float(w) > b) {
+            w = 0xff800000u;
+            bits |= bit;
+        }
+    };
+    word(v.x, 1u);
+    word(v.y, 2u);
+    word(v.z, 4u);
+    word(v.w, 8u);
+    return bits;
 }
 template <>
-__device__ __forceinline__ void clear<uint16_t>(uint4& v, int j)
+__device__ __forceinline__ uint32_t take_above<uint16_t>(uint4& v, uint32_t bar)
 {
-    uint32_t& w = j < 2 ? v.x : j < 4 ? v.y : j < 6 ? v.z : v.w;
-    w = j & 1 ? (w & 0xffffu) | 0xff800000u : (w & 0xffff0000u) | 0xff80u;
+    uint32_t bits = 0;
+    auto word = [&](uint32_t& w, int shift) {
+        uint32_t m;  // 0xffff in each half that is above
+        asm("set.gt.u32.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(w), "r"(bar));
+        w = (w & ~m) | (0xff80ff80u & m);
+        bits |= ((m & 1u) | (m >> 15 & 2u)) << shift;
+    };
+    word(v.x, 0);
+    word(v.y, 2);
+    word(v.z, 4);
+    word(v.w, 6);
+    return bits;
 }
 
 // What of a unit (a row, or a part of one) a thread keeps.
@@ -142,9 +193,11 @@ struct Sums {
     float s, t;
 };
 
-// Add four vectors to the sums.
+// Add four vectors to the sums. (The rounded log2(e) / T alone: its error is that of the product after it. A row of
+// 128000 takes a tenth of its instructions more with the pair that the other losses take, whose logprobs are of sums
+// that are not.)
 template <typename T, bool kEntropy>
-__device__ __forceinline__ void add(Sums& st, const uint4 (&v)[kVecs], Two c_hi, Two c_lo)
+__device__ __forceinline__ void add(Sums& st, const uint4 (&v)[kVecs], Two c)
 {
     const Two ref = two(-st.ref, -st.ref);
     Two s = two(st.s, 0.f), t = two(st.t, 0.f);
@@ -154,8 +207,7 @@ __device__ __forceinline__ void add(Sums& st, const uint4 (&v)[kVecs], Two c_hi,
         Elems<T>::widen(v[k], x);
 #pragma unroll
         for (int j = 0; j < Elems<T>::kPer / 2; ++j) {
-            const Two d = add2(x[j], ref);
-            const Two u = fma2(d, c_hi, mul2(d, c_lo));
+            const Two u = mul2(add2(x[j], ref), c);
             const Two e = exp2_two(u);
             s = add2(s, e);
             if (kEntropy) t = fma2(e, clamp2(u), t);
@@ -180,8 +232,9 @@ __device__ __forceinline__ void move(Sums& st, float ref, float c)
 }
 
 // The sum of all consumers' counts; `turn` goes round the three tallies, of which the one that it starts from is 0.
-__device__ __forceinline__ uint32_t count_all(Shared& S, uint32_t mine, uint32_t& turn)
+__device__ __forceinline__ uint32_t count_all(uint32_t mine, uint32_t& turn)
 {
+    Shared& S = shared();
     mine = __reduce_add_sync(0xffffffffu, mine);
     const uint32_t next = turn == 2 ? 0 : turn + 1;
     if ((threadIdx.x & 31) == 0 && mine) atomicAdd(&S.tally[turn], mine);
@@ -192,91 +245,281 @@ __device__ __forceinline__ uint32_t count_all(Shared& S, uint32_t mine, uint32_t
     return n;
 }
 
-// A key that n to `most` of the list's `count` keys reach; count > most.
-__device__ __noinline__ uint64_t select(Shared& S, uint32_t count, uint32_t n, uint32_t most)
+// A key that n to `most` of the first `count` keys of a list reach; count > most. A bisection, over the values first and,
+// where ties do not leave it a number in between, over the tokens of the value that it ends at. (Each step is a barrier
+// that counts, of a key in each thread; longer lists take the tallies.) What has been put into the list before is seen
+// by all after it.
+__device__ __forceinline__ uint64_t select(const uint64_t* list, uint32_t count, uint32_t n, uint32_t most)
 {
-    uint64_t lo = 0, hi = ~0ull;
-    uint32_t turn = 0;
-    if (threadIdx.x == 0) S.tally[0] = 0;
+    Shared& S = shared();
+    const int tid = threadIdx.x;
+    const bool single = count <= uint32_t(kConsumers);
+    const uint64_t mine = uint32_t(tid) < count ? list[tid] : 0;
+    uint32_t top = uint32_t(mine >> 32), turn = 0;
+    for (uint32_t i = tid + kConsumers; i < count; i += kConsumers) top = max(top, uint32_t(list[i] >> 32));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if ((tid & 31) == 0) S.tops[tid >> 5] = top;
+    if (tid == 0) S.tally[0] = 0;
     bar_sync();
-    while (hi - lo > 1) {
-        const uint64_t mid = lo + (hi - lo) / 2;
-        uint32_t mine = 0;
-        for (uint32_t i = threadIdx.x; i < count; i += kConsumers) mine += S.list[i] >= mid;
-        const uint32_t got = count_all(S, mine, turn);
-        if (got >= n) {
-            lo = mid;
-            if (got <= most) break;
-        } else {
-            hi = mid;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = max(top, S.tops[w]);
+    auto reach = [&](uint64_t key) {
+        if (single) return bar_count(mine >= key);
+        uint32_t c = 0;
+        for (uint32_t i = tid; i < count; i += kConsumers) c += list[i] >= key;
+        return count_all(c, turn);
+    };
+    uint64_t lo = uint64_t(order_of(-kFloatMax)) << 32, hi = (uint64_t(top) + 1) << 32, step = 1ull << (32 + 21);
+    bool found = false;  // a lower end that is near: steps down from the top, each four times the one before
+    for (int part = 0; part < 2; ++part) {
+        const uint64_t last = part == 0 ? 1ull << 32 : 1;
+#pragma unroll 1
+        while (hi - lo > last) {
+            uint64_t mid = lo + ((hi - lo) / 2 & ~(last - 1));
+            if (!found && step != 0 && step < hi - lo) mid = max(mid, hi - step);
+            step <<= 2;  // (0 at last: halves from then on)
+            const uint32_t got = reach(mid);
+            if (got >= n) {
+                lo = mid;
+                found = true;
+                if (got <= most) return mid;
+            } else {
+                hi = mid;
+            }
         }
+        if (part == 0) lo |= uint32_t(~uint32_t(kMaxToken));  // the lowest key of the value
     }
     return lo;
 }
 
-// A key below `least` becomes part of the sums, relative to `ref`.
-template <bool kEntropy>
-__device__ __forceinline__ void lose(Shared& S, uint64_t key, float ref, float c_hi, float c_lo)
+// log2(e) / T, rounded and as a pair, for keys one by one.
+struct Scale {
+    float c, c_hi, c_lo;
+};
+
+// The next place in a list for a lane by itself. (Written so that the lanes that want one, a few of a warp, are not put
+// together first.)
+__device__ __forceinline__ uint32_t next_place(uint32_t* count)
 {
-    const float d = key_value(key) - ref, u = fmaxf(fmaf(d, c_hi, d * c_lo), kLowest), e = exp2_fast(u);
-    atomicAdd(&S.lost_s, static_cast<unsigned long long>(double(e) * kLostUnit));
-    if (kEntropy) atomicAdd(reinterpret_cast<unsigned long long*>(&S.lost_t),
-                            static_cast<unsigned long long>(static_cast<long long>(double(e) * double(u) * kLostUnit)));
+    uint32_t at;
+    asm volatile("atom.shared.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(smem_addr(count)) : "memory");
+    return at;
 }
 
-// Keep the first `count` keys of the list that reach `least`; `before`: those of tokens before it (the others are not
-// looked at). The others become part of the sums. Their place is free for more, which `more` puts in.
-template <bool kEntropy, typename F>
-__device__ __forceinline__ void cut(Shared& S, Sums& st, uint32_t count, uint64_t least, int before, const RowJob& h, F more)
+// Places in a list for the lanes of a warp that want one (kCap and above: there is none); the warp is whole.
+__device__ __forceinline__ uint32_t places(uint32_t* count, bool want)
 {
-    uint64_t mine[kHeld];
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const uint32_t at = threadIdx.x + i * kConsumers;
-        mine[i] = at < count ? S.list[at] : 0;
-        if (key_token(mine[i]) >= before) mine[i] = 0;
-    }
-    bar_sync();
-    if (threadIdx.x == 0) {
-        S.count = 0;
-        S.lost_s = 0;
-        S.lost_t = 0;
-        S.lost_most = 0;
-    }
-    bar_sync();
-    uint32_t most = 0;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        if (mine[i] >= least) {
-            S.list[atomicAdd(&S.count, 1u)] = mine[i];
-            mine[i] = 0;
-        }
-        most = max(most, uint32_t(mine[i] >> 32));
-    }
-    most = __reduce_max_sync(0xffffffffu, most);
-    if ((threadIdx.x & 31) == 0 && most) atomicMax(&S.lost_most, most);
-    move(st, key_value(least), h.c);
-    st.bar = st.ref;
-    more();
-    bar_sync();
+    const uint32_t lanes = __ballot_sync(0xffffffffu, want), lane = threadIdx.x & 31;
+    uint32_t first = 0;
+    if (lane == 0 && lanes) first = atomicAdd(count, uint32_t(__popc(lanes)));
+    return __shfl_sync(0xffffffffu, first, 0) + __popc(lanes & ((1u << lane) - 1u));
+}
+
+// Those of the first `count` keys of a list for which goes(key, the place in turn) become part of thread 0's sums, as
+// whole multiples of 2^-40 of the largest of them, so that it does not matter in what order they are. S.lost_most is
+// their largest order, seen by all.
+template <bool kEntropy, typename F>
+__device__ __forceinline__ void lose(const uint64_t* from, uint32_t count, Sums& st, const Scale& q, F goes)
+{
+    Shared& S = shared();
+    const int tid = threadIdx.x;
     const uint32_t lost = S.lost_most;
     if (lost == 0) return;
     const float ref = value_of(lost);
+    unsigned long long s = 0;
+    long long t = 0;
+#pragma unroll 1
+    for (uint32_t i = tid; i < count; i += kConsumers) {
+        const uint64_t k = from[i];
+        if (!goes(k)) continue;
+        const float d = key_value(k) - ref, u = fmaxf(fmaf(d, q.c_hi, d * q.c_lo), kLowest), e = exp2_fast(u);
+        s += __float2ull_rn(e * kLostUnit);
+        if (kEntropy) t += __float2ll_rn(e * u * kLostUnit);
+    }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i)
-        if (mine[i] != 0) lose<kEntropy>(S, mine[i], ref, h.c_hi, h.c_lo);
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (kEntropy) t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    if ((tid & 31) == 0) {
+        S.lost_s[tid >> 5] = s;
+        S.lost_t[tid >> 5] = t;
+    }
     bar_sync();
-    if (threadIdx.x == 0) {
-        Sums one{0.f, ref, float(double(S.lost_s) * (1.0 / kLostUnit)), float(double(S.lost_t) * (1.0 / kLostUnit))};
-        move(one, st.ref, h.c);
+    if (tid == 0) {
+        s = 0;
+        t = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            s += S.lost_s[w];
+            t += S.lost_t[w];
+        }
+        Sums one{0.f, ref, __ull2float_rn(s) * (1.f / kLostUnit), __ll2float_rn(t) * (1.f / kLostUnit)};
+        move(one, st.ref, q.c);
         st.s += one.s;
         st.t += one.t;
+        S.lost_most = 0;
     }
 }
 
-// A part of row r is done; true (in all consumers) for the one that is last, which sees what the others have left.
-__device__ __forceinline__ bool leave(const TopParams& P, Shared& S, int64_t r, uint32_t part, const TopPart& q)
+// The n largest of a list's first `count` keys (as many as there are threads at most), in order, into `to`; the others
+// become part of thread 0's sums. Each thread counts the keys above its own. (Ends without a barrier for S.lost_most,
+// which the next use comes two barriers after.)
+template <bool kEntropy>
+__device__ __forceinline__ void rank(const uint64_t* from, uint32_t count, uint32_t n, uint64_t* to, Sums& st, const Scale& q)
 {
+    Shared& S = shared();
+    const uint32_t tid = threadIdx.x;
+    if ((tid & ~31u) < count) {
+        const uint64_t mine = tid < count ? from[tid] : 0;
+        const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(from);
+        uint32_t above = 0;
+#pragma unroll 8
+        for (uint32_t j = 0; j < count / 2; ++j) {
+            const ulonglong2 k = pairs[j];
+            above += k.x > mine;
+            above += k.y > mine;
+        }
+        if (count & 1) above += from[count - 1] > mine;
+        const bool stays = above < n;
+        if (tid < count && stays) to[above] = mine;
+        const uint32_t most = __reduce_max_sync(0xffffffffu, stays ? 0 : uint32_t(mine >> 32));
+        if ((tid & 31) == 0 && most) atomicMax(&S.lost_most, most);
+    }
+    bar_sync();
+    if (count <= n) return;
+    const uint64_t least = to[n - 1];
+    move(st, key_value(least), q.c);
+    st.bar = st.ref;
+    lose<kEntropy>(from, count, st, q, [&](uint64_t k) { return k < least; });
+}
+
+// Cuts the first `count` keys of list `at` into the other one, which is empty: those that reach `least`. The others
+// become part of thread 0's sums. List `at` is then empty, and the other one is seen by all. (Between two cuts there is
+// a select.)
+template <bool kEntropy>
+__device__ __forceinline__ void cut(uint32_t at, uint32_t count, uint64_t least, Sums& st, const Scale& q)
+{
+    Shared& S = shared();
+    const int tid = threadIdx.x;
+    const uint64_t* from = S.list[at];
+    uint32_t most = 0;
+#pragma unroll 1
+    for (uint32_t i0 = 0; i0 < count; i0 += kConsumers) {
+        const uint64_t k = i0 + tid < count ? from[i0 + tid] : 0;
+        const bool stays = k >= least;
+        const uint32_t to = places(&S.count[at ^ 1], stays);
+        if (stays)
+            S.list[at ^ 1][to] = k;
+        else
+            most = max(most, uint32_t(k >> 32));
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    if ((tid & 31) == 0 && most) atomicMax(&S.lost_most, most);
+    move(st, key_value(least), q.c);
+    st.bar = st.ref;
+    bar_sync();
+    lose<kEntropy>(from, count, st, q, [&](uint64_t k) { return k < least; });
+    if (tid == 0) S.count[at] = 0;
+}
+
+// A list that is longer than there are threads is cut down to n to `most` keys. Sums come and go in S.state; the list that
+// is filled in the end is returned.
+template <bool kEntropy>
+__device__ __noinline__ uint32_t cut_long(uint32_t at, uint32_t count, uint32_t n, uint32_t most, float c, float c_hi, float c_lo)
+{
+    Shared& S = shared();
+    const float4 in = S.state[threadIdx.x];
+    Sums st{in.x, in.y, in.z, in.w};
+    const uint64_t least = select(S.list[at], count, n, most);
+    cut<kEntropy>(at, count, least, st, Scale{c, c_hi, c_lo});
+    S.state[threadIdx.x] = make_float4(st.bar, st.ref, st.s, st.t);
+    bar_sync();
+    return at ^ 1;
+}
+
+// Where a chunk of a row is: its place in the ring, the first of its vectors in the span, the end of the part's, and the
+// span's elements that the row begins and ends at.
+struct Chunk {
+    int at, base, last, head, end;
+};
+
+template <typename T>
+__device__ __forceinline__ void load(uint4 (&v)[kVecs], const Chunk& p)
+{
+    constexpr int kPer = Elems<T>::kPer;
+    const uint4* in = reinterpret_cast<const uint4*>(ring_of() + p.at);
+    const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+#pragma unroll
+    for (int k = 0; k < kVecs; ++k) {
+        const int i = k * kConsumers + int(threadIdx.x);
+        v[k] = make_uint4(none, none, none, none);
+        if (p.base + i < p.last) {
+            v[k] = in[i];
+            const int at = (p.base + i) * kPer;
+            if (at < p.head || at + kPer > p.end) Elems<T>::mask(v[k], p.head - at, p.end - at);
+        }
+    }
+}
+
+// The list has had no place for all that a chunk put into it (rows that rise, ties in the first chunk). What it had
+// before is kept, and the chunk's elements are looked at again, one of each thread at a time, as keys. Sums come and go
+// in S.state (before the chunk; after it); the list that is filled in the end is returned.
+template <typename T, bool kEntropy>
+__device__ __noinline__ uint32_t slow_chunk(uint32_t at, int chunk_at, int base, int last, int head, int end, uint32_t n, float c,
+                                            float c_hi, float c_lo)
+{
+    constexpr int kPer = Elems<T>::kPer;
+    Shared& S = shared();
+    const int tid = threadIdx.x, before = base * kPer - head;
+    const Scale q{c, c_hi, c_lo};
+    const float4 in = S.state[tid];
+    Sums st{in.x, in.y, in.z, in.w};
+    bar_sync();
+#pragma unroll 1
+    for (uint32_t i0 = 0; i0 < uint32_t(kCap); i0 += kConsumers) {
+        const uint64_t k = S.list[at][i0 + tid];
+        const bool stays = key_token(k) < before;
+        const uint32_t to = places(&S.count[at ^ 1], stays);
+        if (stays) S.list[at ^ 1][to] = k;
+    }
+    bar_sync();
+    if (tid == 0) S.count[at] = 0;
+    at ^= 1;
+    uint64_t least = st.bar > -pos_inf() ? uint64_t(order_of(st.bar) + 1) << 32 : 0;  // (of the list, where it has n keys)
+    const T* x = reinterpret_cast<const T*>(ring_of() + chunk_at);
+#pragma unroll 1
+    for (int e = 0; e < kVecs * kPer; ++e) {
+        const int i = e / kPer * kConsumers + tid, j = (base + i) * kPer + e % kPer;
+        const bool there = base + i < last && j >= head && j < end;
+        const float y = there ? load_logit(x + i * kPer + e % kPer) : -pos_inf();
+        const uint64_t k = key_of(y, j - head);
+        const bool wants = y > -pos_inf() && k >= least;
+        const uint32_t to = places(&S.count[at], wants);
+        if (wants) {
+            S.list[at][to] = k;
+        } else {
+            const float u = (y - st.ref) * c, f = exp2_fast(u);
+            st.s += f;
+            if (kEntropy) st.t = fmaf(f, fmaxf(u, kLowest), st.t);
+        }
+        bar_sync();
+        const uint32_t count = S.count[at];
+        if (count >= uint32_t(kCap - kConsumers) || (e == kVecs * kPer - 1 && count > n)) {
+            least = select(S.list[at], count, n, n + n / 4 + 8 < count ? n + n / 4 + 8 : n);
+            cut<kEntropy>(at, count, least, st, q);
+            at ^= 1;
+        }
+        bar_sync();
+    }
+    S.state[tid] = make_float4(st.bar, st.ref, st.s, st.t);
+    return at;
+}
+
+// A part of row r is done; true (in all consumers) for the one that is last, which sees what the others have left.
+__device__ __forceinline__ bool leave(const TopParams& P, int64_t r, uint32_t part, const TopPart& q)
+{
+    Shared& S = shared();
     if (threadIdx.x == 0) P.ws.parts[r * P.parts + part] = q;
     bar_sync();
     if (threadIdx.x == 0) {
@@ -310,10 +553,10 @@ __device__ __forceinline__ void write_none(const TopParams& P, int64_t r, int st
     }
 }
 
-// Warp 0, with the row's `count` largest keys in order and the sums of the rest: its outputs.
+// The closer, with a row's `count` largest keys in order and the sums of the rest: its outputs.
 template <bool kEntropy>
-__device__ __forceinline__ void close_row(const TopParams& P, const uint64_t* sorted, int count, Sums st, const RowJob& h,
-                                          int64_t r)
+__device__ __forceinline__ void close_row(const TopParams& P, const uint64_t* sorted, int count, const Sums& st,
+                                          const RowJob& h, int64_t r)
 {
     const sampler_rows_t& a = P.rows;
     const int lane = threadIdx.x & 31, n = P.top.top_n;
@@ -357,12 +600,112 @@ __device__ __forceinline__ void close_row(const TopParams& P, const uint64_t* so
     }
 }
 
+// A row's keys in a list and the sums of the rest, each thread's own: the keys in order, and the sums of all, to the
+// closer. `turn`: rows that have gone to it. False where a wait gave up. (A row that has no statistics is written here.)
+template <bool kEntropy>
+__device__ __forceinline__ bool hand_over(const TopParams& P, const uint64_t* list, uint32_t count, Sums st, const RowJob& h,
+                                          float temperature, bool bad, int64_t r, uint32_t& turn)
+{
+    Shared& S = shared();
+    const int tid = threadIdx.x;
+    const uint32_t n = uint32_t(P.top.top_n), slot = turn & 1;
+    const bool ok = wait(&S.written[slot], (turn >> 1 & 1) ^ 1u, P.wait_ns);
+    if (bar_any(!ok)) return false;
+    rank<kEntropy>(list, count, n, S.sorted[slot], st, Scale{h.c, h.c_hi, h.c_lo});
+    count = min(count, n);
+    // the sums of all threads, in order
+    float s = st.s, t = st.t;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (kEntropy) t += __shfl_xor_sync(0xffffffffu, t, o);
+    }
+    if ((tid & 31) == 0) S.sums[tid >> 5] = make_float2(s, t);
+    bar_sync();
+    const int status = h.bad_param    ? SAMPLER_ROW_BAD_PARAM
+                       : bad          ? SAMPLER_ROW_NONFINITE
+                       : count == 0   ? SAMPLER_ROW_ALL_NEG_INF
+                                      : SAMPLER_ROW_OK;
+    if (status != SAMPLER_ROW_OK) {
+        write_none(P, r, status);
+        return true;
+    }
+    if (tid == 0) {
+        s = t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            s += S.sums[w].x;
+            t += S.sums[w].y;
+        }
+        S.close[slot] = Close{int(r), int(count), h.token, st.ref, s, t, temperature, h.x_t};
+        mbar_arrive(&S.ready[slot]);
+    }
+    ++turn;
+    return true;
+}
+
+// The last part of a row joins them all. One more than the rows that have gone to the closer then; 0 where a wait gave up.
+template <bool kEntropy>
+__device__ __noinline__ uint32_t join_parts(const TopParams& P, int64_t r, int32_t token, float temperature, float x_t,
+                                            uint32_t turn)
+{
+    Shared& S = shared();
+    const int tid = threadIdx.x, parts = P.parts;
+    const uint32_t n = uint32_t(P.top.top_n);
+    RowJob h;
+    h.token = token;
+    row_scale(h, P.rows, temperature);
+    h.x_t = x_t;
+    if (tid < 2) S.count[tid] = 0;
+    if (tid < parts) {
+        const volatile TopPart& from = P.ws.parts[r * parts + tid];
+        S.part_ref[tid] = from.ref;
+        S.part_s[tid] = from.s;
+        S.part_t[tid] = from.t;
+        S.part_count[tid] = from.count;
+        S.part_flags[tid] = (from.bad ? 1 : 0) | (from.failed ? 2 : 0);
+    }
+    bar_sync();
+    // keys into the list; the parts' sums, in order, are thread 0's
+    uint32_t count = 0;
+    int flags = 0;
+    Sums st{0.f, -kFloatMax, 0.f, 0.f};
+    for (int p = 0; p < parts; ++p) {
+        const uint32_t c = uint32_t(S.part_count[p]);
+        if (uint32_t(tid) < c)
+            S.list[0][count + tid] = __ldcg(reinterpret_cast<const unsigned long long*>(P.ws.keys + (r * parts + p) * kMost + tid));
+        count += c;
+        flags |= S.part_flags[p];
+        st.ref = fmaxf(st.ref, S.part_ref[p]);
+    }
+    for (int p = 0; p < parts; ++p) {
+        Sums one{0.f, S.part_ref[p], S.part_s[p], S.part_t[p]};
+        move(one, st.ref, h.c);
+        st.s += tid == 0 ? one.s : 0.f;
+        st.t += tid == 0 ? one.t : 0.f;
+    }
+    bar_sync();
+    if (flags & 2) {
+        write_none(P, r, SAMPLER_ROW_TIMEOUT);
+        return turn + 1;
+    }
+    uint32_t at = 0;
+    if (count > uint32_t(kConsumers)) {
+        S.state[tid] = make_float4(st.bar, st.ref, st.s, st.t);
+        at = cut_long<kEntropy>(0, count, n, n, h.c, h.c_hi, h.c_lo);
+        const float4 q = S.state[tid];
+        st = Sums{q.x, q.y, q.z, q.w};
+        count = n;
+    }
+    return hand_over<kEntropy>(P, S.list[at], count, st, h, temperature, flags & 1, r, turn) ? turn + 1 : 0;
+}
+
 template <typename T, bool kEntropy>
 __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant__ TopParams P)
 {
     constexpr int kPer = Elems<T>::kPer;
-    extern __shared__ __align__(128) unsigned char ring[];
-    Shared& S = *reinterpret_cast<Shared*>(ring + kSlots * kChunkBytes);
+    unsigned char* ring = ring_of();
+    Shared& S = shared();
     const sampler_rows_t& a = P.rows;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t part = blockIdx.x % P.parts, q = blockIdx.x / P.parts, n_clusters = gridDim.x / P.parts;
@@ -371,12 +714,17 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
             mbar_init(&S.full[i], 1);
             mbar_init(&S.empty[i], kWarps);
         }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&S.ready[i], 1);
+            mbar_init(&S.written[i], 1);
+        }
         queue_open(S.queue, kWarps);
+        S.lost_most = 0;
         fence_mbar_init();
     }
     __syncthreads();
 
-    if (warp == kWarps) {
+    if (warp == kProducer) {
         RingPlace slot{0, 0};
         uint32_t issued = 0;
         // (wait_ns 0: nothing begins, and the consumers' waits give up)
@@ -405,244 +753,182 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
         return;
     }
 
+    if (warp == kCloser) {
+        // (the consumers give up before it does, and say so)
+        for (uint32_t turn = 0;; ++turn) {
+            const uint32_t slot = turn & 1;
+            if (!wait(&S.ready[slot], turn >> 1 & 1, 8 * kWaitNs)) return;
+            const Close row = S.close[slot];
+            if (row.row < 0) return;
+            RowJob h;
+            h.token = row.token;
+            row_scale(h, a, row.temperature);
+            h.x_t = row.x_t;
+            close_row<kEntropy>(P, S.sorted[slot], row.count, Sums{0.f, row.ref, row.s, row.t}, h, row.row);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&S.written[slot]);
+        }
+    }
+
     const uint32_t n = uint32_t(P.top.top_n);
-    const uint32_t trigger = max(256u, 3 * n), about = n + n / 4 + 8;
+    const uint32_t trigger = n + 64, about = n + n / 4 + 8;
     RingPlace slot{0, 0};
     QueuePlace place{{0, 0}, 0};
-    int64_t done = 0;  // rows that this CTA has ended with
+    uint32_t turn = 0;  // rows that have gone to the closer
+    int64_t done = 0;   // rows that this CTA has ended with
+    bool failed = false;
     for (;; ++done) {
         RowItem row;
         // a wait that gives up gives up for all warps
-        if (bar_any(!queue_next(S.queue, place, P.wait_ns, row))) break;
-        if (row.row < 0) return;
+        failed = bar_any(!queue_next(S.queue, place, P.wait_ns, row));
+        if (failed || row.row < 0) break;
         const int64_t r = row.row;
         if (!row.live) {
             if (part == 0) write_none(P, r, SAMPLER_ROW_OK);
             continue;
         }
-        bool failed = false;
         RowJob h;
         h.token = row.token;
         row_scale(h, a, row.temperature);
-        const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
         h.x_t = row.x_t;
-        const RowSpan span = row_span(x, a.vocab);
+        const RowSpan span = row_span(static_cast<const T*>(a.logits) + r * a.row_stride, a.vocab);
         const int first = int(part) * P.part_vecs, last = min(first + P.part_vecs, span.count);
-        const int end = span.head + int(a.vocab);  // elements of the span up to the row's end
-        const Two c_hi = two(h.c_hi, h.c_hi), c_lo = two(h.c_lo, h.c_lo);
+        const Scale scale{h.c, h.c_hi, h.c_lo};
         Sums st{-pos_inf(), -kFloatMax, 0.f, 0.f};
         bool has_n = false, bad = false;
-        if (tid == 0) S.count = 0;
+        uint32_t at = 0, count = 0;  // the list that is filled, and, at the end, the keys in it
+        if (tid < 2) S.count[tid] = 0;
         bar_sync();
         for (int base = first; base < last; base += kChunkVecs) {
-            bool ok = wait(&S.full[slot.at], slot.phase, P.wait_ns);
-            const uint4* chunk = reinterpret_cast<const uint4*>(ring + slot.at * kChunkBytes);
+            const bool ok = wait(&S.full[slot.at], slot.phase, P.wait_ns);
+            const Chunk chunk{int(slot.at) * kChunkBytes, base, ok ? last : 0, span.head, span.head + int(a.vocab)};
             uint4 v[kVecs];
-            auto load = [&] {
-#pragma unroll
-                for (int k = 0; k < kVecs; ++k) {
-                    const int i = base + k * kConsumers + tid;
-                    v[k] = make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
-                    if (sizeof(T) == 2) v[k] = make_uint4(0xff80ff80u, 0xff80ff80u, 0xff80ff80u, 0xff80ff80u);
-                    if (ok && i < last) {
-                        v[k] = chunk[k * kConsumers + tid];
-                        const int at = i * kPer;
-                        if (at < span.head || at + kPer > end) Elems<T>::mask(v[k], span.head - at, end - at);
-                    }
-                }
-            };
-            load();
-            float m[kVecs];
-#pragma unroll
-            for (int k = 0; k < kVecs; ++k) m[k] = Elems<T>::largest(v[k]);
-            const float most = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
+            load<T>(v, chunk);
+            const float most = max_nan(max_nan(Elems<T>::largest(v[0]), Elems<T>::largest(v[1])),
+                                       max_nan(Elems<T>::largest(v[2]), Elems<T>::largest(v[3])));
             bad |= !(most < pos_inf());
+            bool first_bar = false;
             if (!has_n) {
-                // n of the threads' largest reach `lo`
-                uint32_t lo = order_of(-kFloatMax), hi = order_of(pos_inf());
+                // the n-th of the threads' largest; where fewer threads have any, all are taken
                 const uint32_t mine = order_of(most);
-                uint32_t got = bar_count(most >= -kFloatMax);
-                if (got >= n) {
-                    while (got > about && hi - lo > 1) {
-                        const uint32_t mid = lo + (hi - lo) / 2;
-                        const uint32_t c = bar_count(mine >= mid);
-                        if (c >= n) {
-                            lo = mid;
-                            got = c;
-                        } else {
-                            hi = mid;
-                        }
-                    }
-                    has_n = true;
+                S.largest[tid] = mine;
+                bar_sync();
+                uint32_t above = 0;
+                const uint4* all = reinterpret_cast<const uint4*>(S.largest);
+#pragma unroll 8
+                for (int j = 0; j < kConsumers / 4; ++j) {
+                    const uint4 o = all[j];
+                    above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+                }
+                // of equal ones all have the first's place: the least of those that come before the n-th or on it
+                const uint32_t least = __reduce_min_sync(0xffffffffu, above < n ? mine : 0xffffffffu);
+                if (lane == 0) S.tops[warp] = least;
+                first_bar = has_n = bar_count(above < n && most >= -kFloatMax) >= n;
+                if (has_n) {
+                    uint32_t lo = 0xffffffffu;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) lo = min(lo, S.tops[w]);
                     move(st, value_of(lo), h.c);
                     st.bar = below(lo);
                 }
             }
             const float s_before = st.s, t_before = st.t;
-            uint32_t top = 0;
+            uint32_t top = 0, above = 0;
+            if (!(most <= st.bar)) {
+                const uint32_t bar = packed_bar<T>(st.bar);
 #pragma unroll
-            for (int k = 0; k < kVecs; ++k) {
-                if (!(m[k] <= st.bar)) {
-                    const int at = (base + k * kConsumers + tid) * kPer - span.head;
-#pragma unroll
-                    for (int j = 0; j < kPer; ++j) {
-                        const float y = element<T>(v[k], j);
-                        if (y > st.bar) {
-                            top = atomicAdd(&S.count, 1u) + 1;
-                            if (top <= kCap) S.list[top - 1] = key_of(y, at + j);
-                            clear<T>(v[k], j);
-                        }
-                    }
-                }
+                for (int k = 0; k < kVecs; ++k) above |= take_above<T>(v[k], bar) << k * kPer;
             }
-            add<T, kEntropy>(st, v, c_hi, c_lo);
-            if (bar_any(top >= trigger || !ok)) {
-                failed = bar_any(!ok);
-                if (failed) break;
-                const uint32_t count = S.count;
-                if (count > kCap) {
-                    // the list has no place for this chunk: it is cut together with what the list had before
-                    st.s = s_before;
-                    st.t = t_before;
-                    load();
-                    const int before = base * kPer - span.head;
-                    uint64_t lo = 0, hi = ~0ull;
-                    uint32_t turn = 0;
-                    if (tid == 0) S.tally[0] = 0;
-                    bar_sync();
-                    while (hi - lo > 1) {
-                        const uint64_t mid = lo + (hi - lo) / 2;
-                        uint32_t c = 0;
-                        for (int i = tid; i < kCap; i += kConsumers) c += key_token(S.list[i]) < before && S.list[i] >= mid;
-#pragma unroll
-                        for (int k = 0; k < kVecs; ++k) {
-                            const int at = (base + k * kConsumers + tid) * kPer - span.head;
-#pragma unroll
-                            for (int j = 0; j < kPer; ++j) {
-                                const float y = element<T>(v[k], j);
-                                c += y > -pos_inf() && key_of(y, at + j) >= mid;
-                            }
-                        }
-                        const uint32_t got = count_all(S, c, turn);
-                        if (got >= n) {
-                            lo = mid;
-                            if (got <= about) break;
-                        } else {
-                            hi = mid;
-                        }
+            while (above) {
+                const int bit = __ffs(above) - 1, i = bit / kPer * kConsumers + tid, j = bit % kPer;
+                above &= above - 1;
+                const uint32_t to = next_place(&S.count[at]);
+                top = to + 1;
+                if (to < kCap)
+                    S.list[at][to] = key_of(load_logit(reinterpret_cast<const T*>(ring + chunk.at) + i * kPer + j),
+                                            (base + i) * kPer - span.head + j);
+            }
+            __syncwarp();
+            add<T, kEntropy>(st, v, two(h.c, h.c));
+            const bool any = bar_any(top >= (first_bar ? n + 1 : trigger) || !ok), end = base + kChunkVecs >= last;
+            if (any && bar_any(!ok)) {
+                failed = true;
+                break;
+            }
+            if (any || end) {
+                count = S.count[at];
+                if (count > uint32_t(kConsumers)) {
+                    const bool over = count > uint32_t(kCap);
+                    S.state[tid] = make_float4(st.bar, st.ref, over ? s_before : st.s, over ? t_before : st.t);
+                    at = over ? slow_chunk<T, kEntropy>(at, chunk.at, base, last, chunk.head, chunk.end, n, h.c, h.c_hi, h.c_lo)
+                              : cut_long<kEntropy>(at, count, n, about, h.c, h.c_hi, h.c_lo);
+                    const float4 q = S.state[tid];
+                    st = Sums{q.x, q.y, q.z, q.w};
+                    count = S.count[at];
+                    has_n = true;
+                } else if (any && !end) {
+                    rank<kEntropy>(S.list[at], count, n, S.list[at ^ 1], st, scale);
+                    if (tid == 0) {
+                        S.count[at] = 0;
+                        S.count[at ^ 1] = min(count, n);
                     }
-                    cut<kEntropy>(S, st, kCap, lo, before, h, [&] {
-#pragma unroll
-                        for (int k = 0; k < kVecs; ++k) {
-                            const int at = (base + k * kConsumers + tid) * kPer - span.head;
-#pragma unroll
-                            for (int j = 0; j < kPer; ++j) {
-                                const float y = element<T>(v[k], j);
-                                if (y > -pos_inf() && key_of(y, at + j) >= lo) {
-                                    S.list[atomicAdd(&S.count, 1u)] = key_of(y, at + j);
-                                    clear<T>(v[k], j);
-                                }
-                            }
-                        }
-                        add<T, kEntropy>(st, v, c_hi, c_lo);
-                    });
-                } else {
-                    const uint64_t least = select(S, count, n, about);
-                    cut<kEntropy>(S, st, count, least, 0x7fffffff, h, [] {});
+                    at ^= 1;
+                    has_n |= count >= n;
                 }
-                has_n = true;
                 bar_sync();
-            } else if (has_n) {
-                st.bar = st.ref;  // later tokens lose ties
             }
+            if (has_n) st.bar = st.ref;  // later tokens lose ties
             if (lane == 0) mbar_arrive(&S.empty[slot.at]);
             slot.next(kSlots);
         }
         if (failed) break;
         bad = bar_any(bad);
-        uint32_t count = S.count;
-        if (count > n) {
-            const uint64_t least = select(S, count, n, n);
-            cut<kEntropy>(S, st, count, least, 0x7fffffff, h, [] {});
-            bar_sync();
-            count = n;
-        }
-        // the sums of all threads, in order
-        {
-            float s = st.s, t = st.t;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                s += __shfl_xor_sync(0xffffffffu, s, o);
-                if (kEntropy) t += __shfl_xor_sync(0xffffffffu, t, o);
-            }
-            if (lane == 0) S.sums[warp] = make_float4(s, t, 0.f, 0.f);
-            bar_sync();
-            st.s = st.t = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                st.s += S.sums[w].x;
-                st.t += S.sums[w].y;
-            }
-        }
-        if (P.parts > 1) {
-            uint64_t* keys = P.ws.keys + (r * P.parts + part) * kMost;
-            if (uint32_t(tid) < count) __stcg(reinterpret_cast<unsigned long long*>(keys + tid), S.list[tid]);
-            const bool joins = leave(P, S, r, part, TopPart{st.ref, st.s, st.t, int(count), bad, 0});
-            if (!joins) continue;
-            // all parts: their keys into the list, their sums in order
-            count = 0;
-            bool some_failed = false;
-            Sums sum{0.f, -kFloatMax, 0.f, 0.f};
-            for (int p = 0; p < P.parts; ++p) {
-                const volatile TopPart& from = P.ws.parts[r * P.parts + p];
-                Sums one{0.f, from.ref, from.s, from.t};
-                const uint32_t c = uint32_t(from.count);
-                bad |= from.bad != 0;
-                some_failed |= from.failed != 0;
-                const float ref = fmaxf(sum.ref, one.ref);
-                move(sum, ref, h.c);
-                move(one, ref, h.c);
-                sum.s += one.s;
-                sum.t += one.t;
-                if (uint32_t(tid) < c)
-                    S.list[count + tid] = __ldcg(reinterpret_cast<const unsigned long long*>(P.ws.keys + (r * P.parts + p) * kMost + tid));
-                count += c;
-            }
-            st = sum;
-            if (some_failed) {
-                write_none(P, r, SAMPLER_ROW_TIMEOUT);
-                bar_sync();
-                continue;
-            }
-            bar_sync();
-            if (count > n) {
-                const uint64_t least = select(S, count, n, n);
-                cut<kEntropy>(S, st, count, least, 0x7fffffff, h, [] {});  // (thread 0 has the sums with what is lost)
-                count = n;
-                if (tid == 0) S.sums[0] = make_float4(st.s, st.t, 0.f, 0.f);
-                bar_sync();
-                st.s = S.sums[0].x;
-                st.t = S.sums[0].y;
-            }
-        }
-        const int status = h.bad_param    ? SAMPLER_ROW_BAD_PARAM
-                           : bad          ? SAMPLER_ROW_NONFINITE
-                           : count == 0   ? SAMPLER_ROW_ALL_NEG_INF
-                                          : SAMPLER_ROW_OK;
-        if (status != SAMPLER_ROW_OK) {
-            write_none(P, r, status);
-            bar_sync();
+        if (P.parts == 1) {
+            failed = !hand_over<kEntropy>(P, S.list[at], count, st, h, row.temperature, bad, r, turn);
+            if (failed) break;
             continue;
         }
-        if (uint32_t(tid) < count) {
-            const uint64_t k = S.list[tid];
-            uint32_t rank = 0;
-            for (uint32_t j = 0; j < count; ++j) rank += S.list[j] > k;
-            S.sorted[rank] = k;
+        // this part's n largest keys and sums go into the workspace, for the part of the row that ends last
+        rank<kEntropy>(S.list[at], count, n, S.list[at ^ 1], st, scale);
+        count = min(count, n);
+        float s = st.s, t = st.t;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (kEntropy) t += __shfl_xor_sync(0xffffffffu, t, o);
+        }
+        if (lane == 0) S.sums[warp] = make_float2(s, t);
+        if (uint32_t(tid) < count)
+            __stcg(reinterpret_cast<unsigned long long*>(P.ws.keys + (r * P.parts + part) * kMost + tid), S.list[at ^ 1][tid]);
+        bar_sync();
+        s = t = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            s += S.sums[w].x;
+            t += S.sums[w].y;
+        }
+        if (leave(P, r, part, TopPart{st.ref, s, t, int(count), bad, 0})) {
+            // (0: a wait gave up; a row with a status does not go to the closer)
+            const uint32_t to = join_parts<kEntropy>(P, r, row.token, row.temperature, row.x_t, turn);
+            if (to == 0) {
+                write_none(P, r, SAMPLER_ROW_TIMEOUT);
+                failed = true;
+                ++done;
+                break;
+            }
+            turn = to - 1;
         }
         bar_sync();
-        if (warp == 0) close_row<kEntropy>(P, S.sorted, int(count), st, h, r);
     }
+    if (warp == 0) {  // the closer's last
+        const uint32_t to = turn & 1;
+        if (wait(&S.written[to], (turn >> 1 & 1) ^ 1u, kWaitNs) && lane == 0) {
+            S.close[to].row = -1;
+            mbar_arrive(&S.ready[to]);
+        }
+        __syncwarp();
+    }
+    if (!failed) return;
 
     // A wait gave up. The rows that this CTA has not ended with are written as TIMEOUT, those that it shares with other
     // CTAs by the last of them.
@@ -655,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
         if (i < done) continue;
         if (!counts) {
             if (part == 0) write_none(P, r, SAMPLER_ROW_OK);
-        } else if (P.parts == 1 || leave(P, S, r, part, TopPart{0.f, 0.f, 0.f, 0, 0, 1})) {
+        } else if (P.parts == 1 || leave(P, r, part, TopPart{0.f, 0.f, 0.f, 0, 0, 1})) {
             write_none(P, r, SAMPLER_ROW_TIMEOUT);
         }
     }
@@ -674,7 +960,7 @@ int top_launch(const TopParams& params, int sms, TopGrants* grants, cudaStream_t
     // parts of a row: as many as give every place on the GPU one, where rows are few; not so small that their joining is
     // what takes the time, and so many that their keys fit the list
     int64_t parts = std::max<int64_t>(1, slots / p.rows.n_rows);
-    parts = std::min({parts, int64_t(kCap / p.top.top_n), std::max<int64_t>(1, vecs / 256)});
+    parts = std::min({parts, int64_t(kMaxTopParts), int64_t(kCap / p.top.top_n), std::max<int64_t>(1, vecs / 256)});
     if (p.rows.n_rows * parts > kTopUnits) parts = 1;
     p.part_vecs = int((vecs + parts - 1) / parts);
     p.parts = int((vecs + p.part_vecs - 1) / p.part_vecs);

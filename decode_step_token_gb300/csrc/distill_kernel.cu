@@ -55,7 +55,7 @@ constexpr uint64_t kSettleNs = 100000;       // in which what is on its way to s
 // What a CTA's closer puts into all CTAs: sums of the list's tokens in its part.
 struct ListSums {
     float ref, s;   // exponentials
-    double a, q;    // q_j (l_j - x_j / T) and q_j
+    Pair a, q;      // q_j (l_j - (x_j - ref) / T) and q_j
     uint32_t flags, pad;
 };
 static_assert(sizeof(ListSums) == 32, "two stores of 16 bytes");
@@ -79,7 +79,7 @@ struct Shared {
 
 // The buffers, the consumers' sums [kSums][parts * kWarps], the closers' [kSums][parts], the maps [kMaps][part_vecs] and
 // Shared.
-__host__ __device__ constexpr int map_bytes(int part_vecs) { return (part_vecs + 15) / 16 * 16; }
+__host__ __device__ constexpr int map_bytes(int part_vecs) { return (part_vecs + kStep - 1) / kStep * kStep; }
 constexpr int smem_of(int part_vecs, int buffers, int parts)
 {
     return buffers * part_vecs * 16 + kSums * parts * (kWarps * 16 + int(sizeof(ListSums))) + kMaps * map_bytes(part_vecs) +
@@ -124,6 +124,38 @@ __device__ __noinline__ void abandon(const DistillParams& P, uint32_t q, uint32_
         }
     }
 }
+
+// A divergence is a small difference of logprobs: its terms are pairs, and so are their sums.
+__device__ __forceinline__ Pair pair_add(const Pair& a, const Pair& b)
+{
+    const Pair s = two_sum(a.hi, b.hi);
+    return Pair{s.hi, s.lo + (a.lo + b.lo)};
+}
+
+__device__ __forceinline__ Pair pair_times(float q, const Pair& a)
+{
+    const float p = q * a.hi;
+    return Pair{p, fmaf(q, a.hi, -p) + q * a.lo};
+}
+
+// (x - ref) / T of a finite x
+__device__ __forceinline__ Pair scaled(const RowJob& h, float x, float ref)
+{
+    const Pair d = two_sum(x, -ref);
+    const float y = d.hi * h.inv_t;
+    return Pair{y, fmaf(d.hi, h.inv_t, -y) + fmaf(d.hi, h.inv_t_lo, d.lo * h.inv_t)};
+}
+
+// The sum over a warp, in every lane.
+__device__ __forceinline__ void pair_warp(Pair& a)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        a = pair_add(a, Pair{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)});
+}
+
+// Where the byte of a part's vector i is in a map: those of the vectors that a thread takes at once lie side by side.
+__device__ __forceinline__ int map_place(int i) { return (i & ~(kStep - 1)) | (i & (kConsumers - 1)) * kVecs | (i / kConsumers & (kVecs - 1)); }
 
 // Marked elements of a vector become -inf, or those of `from`.
 template <typename T>
@@ -235,55 +267,63 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
         RingPlace buf{0, 0}, map{0, 0}, put{0, 0}, taken{0, 0};
         const float scale = kGrad ? scale_of_grad(D.grad_scale, D.grad_scale_dev) : 1.f;
         const int k = D.top_n;
+        uint32_t writer = 0;  // whose turn it is to write a row's outputs
+        // A row and its list, as they are read ahead.
+        struct Fetched {
+            RowItem item;
+            int id[kHeld];
+            float l[kHeld];
+            float rest;  // the teacher's logprob outside the list
+        };
         // A row whose list has been put, until it is closed.
         struct Open {
             RowItem item;
             RowJob h;
             Entry list[kHeld];
             uint32_t buffer;
-            float rest;  // teacher's logprob outside the list
+            float rest;
         };
-        // The next row: marks its tokens, and puts its share of the sums. 1: done; 0: no more rows; -1: a wait gave up.
-        auto open = [&](Open& o) {
-            do {
-                if (!queue_next(S.queue, place, P.wait_ns, o.item)) return -1;
-                if (o.item.row >= 0 && !o.item.live && rank == 0 && lane == 0)
-                    write_row(P, o.item.row, 0.f, 0.f, SAMPLER_ROW_OK, 0.0);
-            } while (o.item.row >= 0 && !o.item.live);
-            if (o.item.row < 0) return 0;
-            const int64_t r = o.item.row;
-            const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
+        // The next row that counts. 1: done; 0: no more rows; -1: a wait gave up.
+        auto fetch = [&](Fetched& f) {
+            for (;;) {
+                if (!queue_next(S.queue, place, P.wait_ns, f.item)) return -1;
+                if (f.item.row < 0) return 0;
+                if (f.item.live) break;
+                if (rank == 0 && lane == 0) write_row(P, f.item.row, 0.f, 0.f, SAMPLER_ROW_OK, 0.0);
+            }
+            const int64_t r = f.item.row;
+            f.rest = D.teacher_rest ? __ldg(D.teacher_rest + r) : -pos_inf();
+#pragma unroll
+            for (int e = 0; e < kHeld; ++e) {
+                const int j = lane + 32 * e;
+                f.id[e] = j < k ? __ldg(D.teacher_ids + r * k + j) : -1;
+                f.l[e] = j < k ? __ldg(D.teacher_logprobs + r * k + j) : -pos_inf();
+            }
+            return 1;
+        };
+        // Marks a row's tokens, and puts its share of the sums; false where a wait gave up.
+        auto open = [&](const Fetched& f, Open& o) {
+            o.item = f.item;
+            o.rest = f.rest;
+            const T* x = static_cast<const T*>(a.logits) + int64_t(o.item.row) * a.row_stride;
             const RowSpan span = row_span(x, a.vocab);
             const int n = min(first_vec + P.part_vecs, span.count) - first_vec;  // vectors here
             o.h.token = o.item.token;
             row_scale(o.h, a, o.item.temperature);
-            o.rest = D.teacher_rest ? D.teacher_rest[r] : -pos_inf();
-            float l[kHeld];
             uint32_t flags = o.rest < pos_inf() ? 0 : kBadList;
+            if (!wait(&S.unmarked[map.at], map.phase ^ 1u, P.wait_ns)) return false;
+            unsigned char* bits = maps + map.at * map_bytes(P.part_vecs);
 #pragma unroll
             for (int e = 0; e < kHeld; ++e) {
-                const int j = lane + 32 * e;
-                int id = -1;
-                l[e] = -pos_inf();
-                if (j < k) {
-                    id = D.teacher_ids[r * k + j];
-                    if (id != -1) l[e] = D.teacher_logprobs[r * k + j];
-                }
-                if (id < -1 || int64_t(id) >= a.vocab || !(l[e] < pos_inf())) {
+                int id = f.id[e];
+                if (id < -1 || int64_t(id) >= a.vocab || (id != -1 && !(f.l[e] < pos_inf()))) {
                     flags |= kBadList;
                     id = -1;
                 }
                 const int at = id + span.head - first_vec * kPer;
                 o.list[e].at = id >= 0 && at >= 0 && at < n * kPer ? at : -1;
-                o.list[e].q = o.list[e].at >= 0 ? expf(l[e]) : 0.f;
-            }
-            if (!wait(&S.unmarked[map.at], map.phase ^ 1u, P.wait_ns)) return -1;
-            unsigned char* bits = maps + map.at * map_bytes(P.part_vecs);
-#pragma unroll
-            for (int e = 0; e < kHeld; ++e) {
-                const int at = o.list[e].at;
-                if (at >= 0) {
-                    const int byte = at / kPer;
+                if (o.list[e].at >= 0) {
+                    const int byte = map_place(at / kPer);
                     const uint32_t bit = 1u << (8 * (byte & 3) + at % kPer);
                     if (atomicOr(reinterpret_cast<uint32_t*>(bits) + byte / 4, bit) & bit) flags |= kBadList;  // twice
                 }
@@ -295,55 +335,59 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             }
             map.next(kMaps);
             __syncwarp();
-            if (!wait(&S.full[buf.at], buf.phase, P.wait_ns)) return -1;
+            if (!wait(&S.full[buf.at], buf.phase, P.wait_ns)) return false;
             o.buffer = buf.at;
             const T* in = reinterpret_cast<const T*>(smem + buf.at * buffer_bytes);
             float ref = -kFloatMax;
 #pragma unroll
             for (int e = 0; e < kHeld; ++e) {
                 o.list[e].x = o.list[e].at >= 0 ? load_logit(in + o.list[e].at) : -pos_inf();
+                o.list[e].q = o.list[e].at >= 0 ? expf(f.l[e]) : 0.f;
                 if (!(o.list[e].x < pos_inf())) flags |= kBadLogit;
                 ref = fmaxf(ref, o.list[e].x);
             }
             ref = max_warp(ref);
             float s = 0.f;
-            double sa = 0.0, sq = 0.0;
-            const double inv_t = double(o.h.inv_t) + double(o.h.inv_t_lo);
+            Pair sa{0.f, 0.f}, sq{0.f, 0.f};
 #pragma unroll
             for (int e = 0; e < kHeld; ++e) {
-                if (o.list[e].at < 0) continue;
-                const float d = o.list[e].x - ref;
+                const Entry& t = o.list[e];
+                if (t.at < 0) continue;
+                const float d = t.x - ref;
                 s += exp2f(fmaxf(fmaf(d, o.h.c_hi, d * o.h.c_lo), kLowest));
-                if (o.list[e].q > 0.f) {
-                    sa += double(o.list[e].q) * (double(l[e]) - double(o.list[e].x) * inv_t);
-                    sq += double(o.list[e].q);
+                if (t.q > 0.f) {
+                    sq = pair_add(sq, Pair{t.q, 0.f});
+                    Pair z{pos_inf(), 0.f};
+                    if (t.x > -pos_inf()) {
+                        const Pair y = scaled(o.h, t.x, ref);
+                        z = two_sum(f.l[e], -y.hi);
+                        z.lo -= y.lo;
+                    }
+                    sa = pair_add(sa, pair_times(t.q, z));
                 }
             }
 #pragma unroll
-            for (int i = 16; i > 0; i >>= 1) {
-                s += __shfl_xor_sync(0xffffffffu, s, i);
-                sa += __shfl_xor_sync(0xffffffffu, sa, i);
-                sq += __shfl_xor_sync(0xffffffffu, sq, i);
-            }
+            for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+            pair_warp(sa);
+            pair_warp(sq);
             flags = __reduce_or_sync(0xffffffffu, flags);
             if (uint32_t(lane) < parts) {
                 const uint32_t to = dsmem_map(smem_addr(lists + put.at * parts + rank), lane),
                                bar = dsmem_map(smem_addr(&S.join[put.at]), lane);
-                put_sums(to, bar, ref, s, __int_as_float(__double2loint(sa)), __int_as_float(__double2hiint(sa)));
-                put_sums(to + 16, bar, __int_as_float(__double2loint(sq)), __int_as_float(__double2hiint(sq)),
-                         __uint_as_float(flags), 0.f);
+                put_sums(to, bar, ref, s, sa.hi, sa.lo);
+                put_sums(to + 16, bar, sq.hi, sq.lo, __uint_as_float(flags), 0.f);
             }
             __syncwarp();
             if (!kGrad && lane == 0) mbar_arrive(&S.empty[buf.at]);
             buf.next(buffers);
             put.next(kSums);
-            return 1;
+            return true;
         };
         // Closes a row; false where a wait gave up.
         auto close = [&](const Open& o) {
             if (!wait(&S.join[taken.at], taken.phase, P.wait_ns)) return false;
             const RowJob& h = o.h;
-            // outside the list
+            // outside the list, and inside
             const float4* in = sums + taken.at * parts * kWarps;
             Stats out = stats_empty();
             for (uint32_t i = lane; i < parts * kWarps; i += 32) out.ref = fmaxf(out.ref, in[i].x);
@@ -353,26 +397,18 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
                 stats_move(p, out.ref, h.c);
                 out.s += p.s;
             }
-            sum_warp<false>(out);
-            // inside
-            Stats list = stats_empty();
-            double sa = 0.0, sq = 0.0;
-            uint32_t flags = 0;
-            if (uint32_t(lane) < parts) {
-                const ListSums& p = lists[taken.at * parts + lane];
-                list.ref = p.ref;
-                list.s = p.s;
-                sa = p.a;
-                sq = p.q;
-                flags = p.flags;
-            }
-            stats_warp<false>(list, h.c);
+            ListSums mine{-kFloatMax, 0.f, {0.f, 0.f}, {0.f, 0.f}, 0, 0};
+            if (uint32_t(lane) < parts) mine = lists[taken.at * parts + lane];
+            Stats list{mine.ref, mine.s, 0.f};
+            stats_move(list, max_warp(mine.ref), h.c);
+            float q_list = mine.q.hi;
 #pragma unroll
             for (int i = 16; i > 0; i >>= 1) {
-                sa += __shfl_xor_sync(0xffffffffu, sa, i);
-                sq += __shfl_xor_sync(0xffffffffu, sq, i);
+                out.s += __shfl_xor_sync(0xffffffffu, out.s, i);
+                list.s += __shfl_xor_sync(0xffffffffu, list.s, i);
+                q_list += __shfl_xor_sync(0xffffffffu, q_list, i);
             }
-            flags = __reduce_or_sync(0xffffffffu, flags);
+            const uint32_t flags = __reduce_or_sync(0xffffffffu, mine.flags);
 
             const float most = fmaxf(out.ref, list.ref);
             auto lift = [&](float ref) {
@@ -388,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             const float inv_s = __fdiv_rn(1.f, s), p_out = out.s * f_out * inv_s;
             const float q_out = o.rest > -pos_inf() ? expf(o.rest) : 0.f;
             const float coef = a.tokens ? D.token_coef : 0.f;
-            const float w = float(sq) + q_out + coef;
+            const float w = q_list + q_out + coef;
             const float g = o.item.weight * scale * h.inv_t;
             const bool fine = status == SAMPLER_ROW_OK;
             if (kGrad) {
@@ -419,41 +455,66 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
                 mbar_arrive(&S.closed[taken.at]);
                 if (kGrad) mbar_arrive(&S.empty[o.buffer]);
             }
-            if (rank == 0) {
+            // a row's outputs are the work of one of the cluster's closers in turn
+            if (writer == rank) {
                 Pair ln_s = log_of(s);
                 ln_s.lo = fmaf(kExp2Short, p_out, ln_s.lo);
                 const Stats all{most, s, 0.f};
-                const double inv_t = double(h.inv_t) + double(h.inv_t_lo);
-                const double lse = double(most) * inv_t + (double(ln_s.hi) + double(ln_s.lo));
-                double kl = sa + sq * lse;
+                // each part's tokens, from its reference to the row's: q_j (l_j - ln p_j) = q_j (l_j - (x_j - ref) / T)
+                // + q_j (ln s + (most - ref) / T)
+                Pair kl{0.f, 0.f};
+                if (mine.q.hi > 0.f) {
+                    const Pair y = scaled(h, most, mine.ref), z = pair_add(ln_s, y);
+                    kl = pair_add(mine.a, pair_add(pair_times(mine.q.hi, z), Pair{mine.q.lo * z.hi, 0.f}));
+                }
+                pair_warp(kl);
                 if (q_out > 0.f) {
-                    const Pair ln_out = log_of(out.s);
-                    kl += out.s > 0.f ? double(q_out) * (double(o.rest) - (double(out.ref) * inv_t + (double(ln_out.hi) + double(ln_out.lo) +
-                                                                                                       double(kExp2Short)) - lse))
-                                      : double(pos_inf());
+                    // ln p_out = (ref_out - most) / T - ln s + ln s_out
+                    Pair z{pos_inf(), 0.f};
+                    if (out.s > 0.f) {
+                        Pair l = log_of(out.s);
+                        l.lo += kExp2Short;
+                        l = pair_add(l, logprob_of(h, all, out.ref, ln_s));
+                        z = two_sum(o.rest, -l.hi);
+                        z.lo -= l.lo;
+                    }
+                    kl = pair_add(kl, pair_times(q_out, z));
                 }
                 const Pair lp = logprob_of(h, all, o.item.x_t, ln_s);
-                double each = kl;
-                if (coef != 0.f) each -= double(coef) * (double(lp.hi) + double(lp.lo));
-                if (lane == 0)
-                    write_row(P, o.item.row, fine ? float(kl) : quiet_nan(), fine ? lp.hi : quiet_nan(), status,
+                if (lane == 0) {
+                    const double divergence = isinf(kl.hi) ? double(kl.hi) : double(kl.hi) + double(kl.lo);
+                    double each = divergence;
+                    if (coef != 0.f) each -= double(coef) * (double(lp.hi) + double(lp.lo));
+                    write_row(P, o.item.row, fine ? float(divergence) : quiet_nan(), fine ? lp.hi : quiet_nan(), status,
                               fine ? double(o.item.weight) * each : double(quiet_nan()));
+                }
             }
+            writer = writer + 1 == parts ? 0 : writer + 1;
             __syncwarp();
             taken.next(kSums);
             return true;
         };
+        Fetched ahead;
         Open now, next;
-        int more = open(now);
-        while (more == 1) {
-            more = open(next);
-            if (more < 0 || !close(now)) {
-                more = -1;
-                break;
-            }
-            now = next;
+        int more = fetch(ahead);  // whether `ahead` is a row
+        bool have = more == 1, ok = more >= 0;
+        if (have) {
+            ok = open(ahead, now);
+            if (ok) more = fetch(ahead);
         }
-        if (more < 0) gave_up(S);
+        while (ok && have) {
+            ok = more >= 0;
+            if (!ok) break;
+            const bool have_next = more == 1;
+            if (have_next) {
+                ok = open(ahead, next);
+                if (ok) more = fetch(ahead);
+            }
+            ok = ok && close(now);
+            now = next;
+            have = have_next;
+        }
+        if (!ok) gave_up(S);
     } else {
         QueuePlace place{{0, 0}, 0};
         RingPlace buf1{0, 0}, buf2{0, 0}, map1{0, 0}, map2{0, 0}, put{0, 0}, closed{0, 0};
@@ -487,20 +548,25 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             bool bad = false;
             for (int i0 = 0; i0 < n; i0 += kStep) {
                 uint4 v[kVecs];
+                uint32_t* marks = reinterpret_cast<uint32_t*>(bits + i0) + tid;  // (a byte for each of the four vectors)
+                // whole, and inside the row
+                const bool inner = i0 + kStep <= n && (first_vec + i0) * kPer >= span.head && (first_vec + i0 + kStep) * kPer <= end;
 #pragma unroll
                 for (int k = 0; k < kVecs; ++k) {
                     const int i = i0 + k * kConsumers + tid;
                     v[k] = nothing<T>();
-                    if (i < n) {
-                        v[k] = in[i];
-                        const int at = (first_vec + i) * kPer;
+                    if (inner || i < n) v[k] = in[i];
+                }
+                if (!inner)
+#pragma unroll
+                    for (int k = 0; k < kVecs; ++k) {
+                        const int at = (first_vec + i0 + k * kConsumers + tid) * kPer;
                         if (at < span.head || at + kPer > end) Elems<T>::mask(v[k], span.head - at, end - at);
-                        const uint32_t b = bits[i];
-                        if (b) {
-                            blend<T>(v[k], nothing<T>(), b);
-                            if (!kGrad) bits[i] = 0;
-                        }
                     }
+                if (const uint32_t b = *marks) {
+#pragma unroll
+                    for (int k = 0; k < kVecs; ++k) blend<T>(v[k], nothing<T>(), b >> 8 * k & 0xffu);
+                    if (!kGrad) *marks = 0;
                 }
                 fold<T, false, kVecs>(st, bad, v, c_hi, c_lo, h.c);
             }
@@ -536,20 +602,37 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
                 const int token_vec = f.token == kNoToken ? -1 : (f.token + span.head) / kPer - first_vec;
                 const uint4* in = reinterpret_cast<const uint4*>(smem + buf2.at * buffer_bytes);
                 unsigned char* bits = maps + map2.at * map_bytes(P.part_vecs);
-#pragma unroll 4
-                for (int i = tid; i < n; i += kConsumers) {
-                    const uint4 v = in[i];
-                    const uint32_t b = bits[i];
-                    uint4 y;
-                    if (i == token_vec)
-                        y = gradient_token<T, false>(v, fs, f.token + span.head - (first_vec + i) * kPer, f.at_token);
-                    else
-                        y = gradient<T, false>(v, fs);
-                    if (b) {
-                        blend<T>(y, v, b);
-                        bits[i] = 0;
+                const int end = span.head + vocab;
+                for (int i0 = 0; i0 < n; i0 += kStep) {
+                    uint32_t* marks = reinterpret_cast<uint32_t*>(bits + i0) + tid;
+                    const uint32_t marked = *marks;
+                    const bool inner = whole && i0 + kStep <= n && (first_vec + i0) * kPer >= span.head &&
+                                       (first_vec + i0 + kStep) * kPer <= end && !(token_vec >= i0 && token_vec < i0 + kStep);
+                    if (inner) {
+                        uint4* to = reinterpret_cast<uint4*>(g - span.head) + first_vec + i0 + tid;
+                        uint4 v[kVecs], y[kVecs];
+#pragma unroll
+                        for (int k = 0; k < kVecs; ++k) v[k] = in[i0 + k * kConsumers + tid];
+#pragma unroll
+                        for (int k = 0; k < kVecs; ++k) y[k] = gradient<T, false>(v[k], fs);
+                        if (marked)
+#pragma unroll
+                            for (int k = 0; k < kVecs; ++k) blend<T>(y[k], v[k], marked >> 8 * k & 0xffu);
+#pragma unroll
+                        for (int k = 0; k < kVecs; ++k) __stcs(to + k * kConsumers, y[k]);
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < kVecs; ++k) {
+                            const int i = i0 + k * kConsumers + tid;
+                            if (i >= n) break;
+                            const uint4 v = in[i];
+                            uint4 y = gradient_token<T, false>(v, fs, i == token_vec ? f.token + span.head - (first_vec + i) * kPer : -1,
+                                                               f.at_token);
+                            blend<T>(y, v, marked >> 8 * k & 0xffu);
+                            put_vector<T>(g, vocab, span.head, first_vec + i, whole, y);
+                        }
                     }
-                    put_vector<T>(g, vocab, span.head, first_vec + i, whole, y);
+                    if (marked) *marks = 0;
                 }
                 __syncwarp();
                 if (lane == 0) {

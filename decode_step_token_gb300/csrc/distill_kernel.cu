@@ -15,9 +15,9 @@
 // between the two passes, so that each logit is read once and each gradient written once. Here a part is one buffer,
 // of which a CTA has two to four. Warp roles of a CTA:
 //   producer   goes ahead over the cluster's rows and brings their parts in with bulk copies;
-//   closer     marks the list's tokens of a part in a map of bits, a byte for each vector, before pass 1; takes their
-//              logits from the buffer and puts its share of the list's sums into all CTAs of the cluster; combines what
-//              all have put, works out the row's factors, writes the row's outputs, and puts the list's own gradients
+//   closers    (two, a row each in turn) mark the list's tokens of a part in a map of bits, a byte for each vector, before pass 1; take their
+//              logits from the buffer and put their share of the list's sums into all CTAs of the cluster; combine what
+//              all have put, work out the row's factors, write the row's outputs, and put the list's own gradients
 //              into the buffer in their logits' place;
 //   consumers  (eight) pass 1: the running reference and sum of what is not marked; pass 2: the gradient, marked elements
 //              as they now are in the buffer. A row's pass 1 comes before the pass 2 of the row before it, so that the
@@ -41,7 +41,8 @@ using namespace rows;
 constexpr int kWarps = 8;
 constexpr int kConsumers = kWarps * 32;
 constexpr int kProducer = kWarps, kCloser = kWarps + 1;
-constexpr int kThreads = kConsumers + 64;
+constexpr int kClosers = 2;                  // warps, of which each takes every other row
+constexpr int kThreads = kConsumers + 32 + 32 * kClosers;
 constexpr int kVecs = 4;                     // vectors that a consumer folds at once
 constexpr int kStep = kConsumers * kVecs;
 constexpr int kMaxBuffers = 4;
@@ -224,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             mbar_init(&S.join[i], 1);
             mbar_init(&S.closed[i], 1);
         }
-        queue_open(S.queue, kWarps + 1);
+        queue_open(S.queue, kWarps + kClosers);
         S.failed = 0;
         fence_mbar_init();
     }
@@ -262,12 +263,13 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             for (uint32_t j = issued > buffers ? issued - buffers : 0; j < issued; ++j)
                 wait(&S.full[j % buffers], j / buffers & 1u, kWaitNs);
         }
-    } else if (warp == kCloser) {
+    } else if (warp >= kCloser) {
         QueuePlace place{{0, 0}, 0};
         RingPlace buf{0, 0}, map{0, 0}, put{0, 0}, taken{0, 0};
         const float scale = kGrad ? scale_of_grad(D.grad_scale, D.grad_scale_dev) : 1.f;
         const int k = D.top_n;
-        uint32_t writer = 0;  // whose turn it is to write a row's outputs
+        uint32_t writer = uint32_t(warp - kCloser);  // whose turn it is to write a row's outputs, modulo `parts`
+        int before = warp - kCloser;                 // rows that the other closers take before this one's next
         // A row and its list, as they are read ahead.
         struct Fetched {
             RowItem item;
@@ -288,9 +290,10 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             for (;;) {
                 if (!queue_next(S.queue, place, P.wait_ns, f.item)) return -1;
                 if (f.item.row < 0) return 0;
-                if (f.item.live) break;
-                if (rank == 0 && lane == 0) write_row(P, f.item.row, 0.f, 0.f, SAMPLER_ROW_OK, 0.0);
+                if (f.item.live && before-- == 0) break;
+                if (!f.item.live && rank == 0 && lane == 0 && warp == kCloser) write_row(P, f.item.row, 0.f, 0.f, SAMPLER_ROW_OK, 0.0);
             }
+            before = kClosers - 1;
             const int64_t r = f.item.row;
             f.rest = D.teacher_rest ? __ldg(D.teacher_rest + r) : -pos_inf();
 #pragma unroll
@@ -333,7 +336,6 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
                 mbar_arrive(&S.marked[map.at]);
                 mbar_arrive_expect_tx(&S.join[put.at], parts * uint32_t(kWarps * 16 + sizeof(ListSums)));
             }
-            map.next(kMaps);
             __syncwarp();
             if (!wait(&S.full[buf.at], buf.phase, P.wait_ns)) return false;
             o.buffer = buf.at;
@@ -379,8 +381,6 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             }
             __syncwarp();
             if (!kGrad && lane == 0) mbar_arrive(&S.empty[buf.at]);
-            buf.next(buffers);
-            put.next(kSums);
             return true;
         };
         // Closes a row; false where a wait gave up.
@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
                 if (kGrad) mbar_arrive(&S.empty[o.buffer]);
             }
             // a row's outputs are the work of one of the cluster's closers in turn
-            if (writer == rank) {
+            if (writer % parts == rank) {
                 Pair ln_s = log_of(s);
                 ln_s.lo = fmaf(kExp2Short, p_out, ln_s.lo);
                 const Stats all{most, s, 0.f};
@@ -489,30 +489,28 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
                               fine ? double(o.item.weight) * each : double(quiet_nan()));
                 }
             }
-            writer = writer + 1 == parts ? 0 : writer + 1;
-            __syncwarp();
-            taken.next(kSums);
+            writer += kClosers;
             return true;
         };
-        Fetched ahead;
-        Open now, next;
-        int more = fetch(ahead);  // whether `ahead` is a row
-        bool have = more == 1, ok = more >= 0;
-        if (have) {
-            ok = open(ahead, now);
-            if (ok) more = fetch(ahead);
-        }
-        while (ok && have) {
-            ok = more >= 0;
-            if (!ok) break;
-            const bool have_next = more == 1;
-            if (have_next) {
-                ok = open(ahead, next);
-                if (ok) more = fetch(ahead);
+        auto skip = [&](int rows) {
+            for (; rows > 0; --rows) {
+                buf.next(buffers);
+                map.next(kMaps);
+                put.next(kSums);
+                taken.next(kSums);
             }
-            ok = ok && close(now);
-            now = next;
-            have = have_next;
+        };
+        skip(warp - kCloser);
+        Fetched ahead;
+        int more = fetch(ahead);  // whether `ahead` is a row
+        bool ok = more >= 0;
+        while (ok && more == 1) {
+            Open now;
+            ok = open(ahead, now);
+            if (!ok) break;
+            more = fetch(ahead);  // (on its way while the row is closed)
+            ok = more >= 0 && close(now);
+            skip(kClosers);
         }
         if (!ok) gave_up(S);
     } else {

@@ -68,9 +68,16 @@ struct Factor {
     int token;  // kNoToken: none
 };
 
+// A list's token that is in a CTA's part.
+struct Entry {
+    int at;     // element of the part's buffer
+    float l, x, q;
+};
+
 struct Shared {
+    Entry list[kClosers][SAMPLER_MAX_ALTERNATIVES];
     uint64_t full[kMaxBuffers], empty[kMaxBuffers];
-    uint64_t marked[kMaps], unmarked[kMaps];
+    uint64_t unmarked[kMaps];
     uint64_t join[kSums], closed[kSums];
     RowQueue queue;
     Factor factor[kSums];
@@ -182,18 +189,18 @@ __device__ __forceinline__ void blend<uint16_t>(uint4& v, const uint4& from, uin
     word(v.w, from.w, bits >> 6);
 }
 
+// Whether some of the kStep vectors from `at` on of a row's span are partly beside the row.
+__device__ __forceinline__ bool ragged(const RowSpan& span, int end, int at, int per)
+{
+    return (at == 0 && span.head != 0) || (at + kStep >= span.count && end % per != 0);
+}
+
 template <typename T>
 __device__ __forceinline__ uint4 nothing()
 {
     const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
     return make_uint4(w, w, w, w);
 }
-
-// A list's token in this CTA's part, as a lane of the closer has it.
-struct Entry {
-    int at;      // element of the part's buffer; -1: not in it
-    float x, q;
-};
 
 template <typename T, bool kGrad>
 __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_constant__ DistillParams P)
@@ -214,11 +221,10 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
 
     if (tid == 0) {
         for (int i = 0; i < kMaxBuffers; ++i) {
-            mbar_init(&S.full[i], 1);
+            mbar_init(&S.full[i], 2);  // its copy, and its row's marks
             mbar_init(&S.empty[i], kWarps + 1);
         }
         for (int i = 0; i < kMaps; ++i) {
-            mbar_init(&S.marked[i], 1);
             mbar_init(&S.unmarked[i], kWarps);
         }
         for (int i = 0; i < kSums; ++i) {
@@ -261,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             gave_up(S);
             // copies in flight land before the CTA may exit
             for (uint32_t j = issued > buffers ? issued - buffers : 0; j < issued; ++j)
-                wait(&S.full[j % buffers], j / buffers & 1u, kWaitNs);
+                wait(&S.full[j % buffers], j / buffers & 1u, kSettleNs);
         }
     } else if (warp >= kCloser) {
         QueuePlace place{{0, 0}, 0};
@@ -277,14 +283,15 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             float l[kHeld];
             float rest;  // the teacher's logprob outside the list
         };
-        // A row whose list has been put, until it is closed.
+        // A row whose list has been put, until it is closed. (Its tokens in this part are few of the list: they are moved
+        // together first, so that the closers' work, which all CTAs of a cluster have, is one token in each lane.)
         struct Open {
             RowItem item;
-            RowJob h;
-            Entry list[kHeld];
             uint32_t buffer;
+            int count;
             float rest;
         };
+        Entry* list = S.list[warp - kCloser];
         // The next row that counts. 1: done; 0: no more rows; -1: a wait gave up.
         auto fetch = [&](Fetched& f) {
             for (;;) {
@@ -308,70 +315,77 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
         auto open = [&](const Fetched& f, Open& o) {
             o.item = f.item;
             o.rest = f.rest;
-            const T* x = static_cast<const T*>(a.logits) + int64_t(o.item.row) * a.row_stride;
-            const RowSpan span = row_span(x, a.vocab);
-            const int n = min(first_vec + P.part_vecs, span.count) - first_vec;  // vectors here
-            o.h.token = o.item.token;
-            row_scale(o.h, a, o.item.temperature);
+            const int n = min(first_vec + P.part_vecs, o.item.count) - first_vec;  // vectors here
+            const int head = o.item.head - first_vec * kPer;
+            const RowJob h = job_of(o.item);
             uint32_t flags = o.rest < pos_inf() ? 0 : kBadList;
-            if (!wait(&S.unmarked[map.at], map.phase ^ 1u, P.wait_ns)) return false;
-            unsigned char* bits = maps + map.at * map_bytes(P.part_vecs);
+            o.count = 0;
 #pragma unroll
             for (int e = 0; e < kHeld; ++e) {
+                if (32 * e >= k) break;
                 int id = f.id[e];
                 if (id < -1 || int64_t(id) >= a.vocab || (id != -1 && !(f.l[e] < pos_inf()))) {
                     flags |= kBadList;
                     id = -1;
                 }
-                const int at = id + span.head - first_vec * kPer;
-                o.list[e].at = id >= 0 && at >= 0 && at < n * kPer ? at : -1;
-                if (o.list[e].at >= 0) {
-                    const int byte = map_place(at / kPer);
-                    const uint32_t bit = 1u << (8 * (byte & 3) + at % kPer);
-                    if (atomicOr(reinterpret_cast<uint32_t*>(bits) + byte / 4, bit) & bit) flags |= kBadList;  // twice
+                const int at = id + head;
+                const bool here = id >= 0 && at >= 0 && at < n * kPer;
+                const uint32_t lanes = __ballot_sync(0xffffffffu, here);
+                if (here) {
+                    Entry& t = list[o.count + __popc(lanes & ((1u << lane) - 1u))];
+                    t.at = at;
+                    t.l = f.l[e];
                 }
+                o.count += __popc(lanes);
+            }
+            __syncwarp();
+            if (!wait(&S.unmarked[map.at], map.phase ^ 1u, P.wait_ns)) return false;
+            unsigned char* bits = maps + map.at * map_bytes(P.part_vecs);
+            for (int i = lane; i < o.count; i += 32) {
+                const int at = list[i].at, byte = map_place(at / kPer);
+                const uint32_t bit = 1u << (8 * (byte & 3) + at % kPer);
+                if (atomicOr(reinterpret_cast<uint32_t*>(bits) + byte / 4, bit) & bit) flags |= kBadList;  // twice
             }
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&S.marked[map.at]);
+                mbar_arrive(&S.full[buf.at]);
                 mbar_arrive_expect_tx(&S.join[put.at], parts * uint32_t(kWarps * 16 + sizeof(ListSums)));
             }
             __syncwarp();
             if (!wait(&S.full[buf.at], buf.phase, P.wait_ns)) return false;
             o.buffer = buf.at;
             const T* in = reinterpret_cast<const T*>(smem + buf.at * buffer_bytes);
-            float ref = -kFloatMax;
-#pragma unroll
-            for (int e = 0; e < kHeld; ++e) {
-                o.list[e].x = o.list[e].at >= 0 ? load_logit(in + o.list[e].at) : -pos_inf();
-                o.list[e].q = o.list[e].at >= 0 ? expf(f.l[e]) : 0.f;
-                if (!(o.list[e].x < pos_inf())) flags |= kBadLogit;
-                ref = fmaxf(ref, o.list[e].x);
-            }
-            ref = max_warp(ref);
-            float s = 0.f;
+            float ref = -kFloatMax, s = 0.f;
             Pair sa{0.f, 0.f}, sq{0.f, 0.f};
-#pragma unroll
-            for (int e = 0; e < kHeld; ++e) {
-                const Entry& t = o.list[e];
-                if (t.at < 0) continue;
-                const float d = t.x - ref;
-                s += exp2f(fmaxf(fmaf(d, o.h.c_hi, d * o.h.c_lo), kLowest));
-                if (t.q > 0.f) {
-                    sq = pair_add(sq, Pair{t.q, 0.f});
-                    Pair z{pos_inf(), 0.f};
-                    if (t.x > -pos_inf()) {
-                        const Pair y = scaled(o.h, t.x, ref);
-                        z = two_sum(f.l[e], -y.hi);
-                        z.lo -= y.lo;
-                    }
-                    sa = pair_add(sa, pair_times(t.q, z));
+            if (o.count) {
+                for (int i = lane; i < o.count; i += 32) {
+                    const float y = load_logit(in + list[i].at);
+                    list[i].x = y;
+                    if (!(y < pos_inf())) flags |= kBadLogit;
+                    ref = fmaxf(ref, y);
                 }
-            }
+                ref = max_warp(ref);
+                for (int i = lane; i < o.count; i += 32) {
+                    const Entry t = list[i];
+                    const float q = expf(t.l), d = t.x - ref;
+                    list[i].q = q;
+                    s += exp2f(fmaxf(fmaf(d, h.c_hi, d * h.c_lo), kLowest));
+                    if (q > 0.f) {
+                        sq = pair_add(sq, Pair{q, 0.f});
+                        Pair z{pos_inf(), 0.f};
+                        if (t.x > -pos_inf()) {
+                            const Pair y = scaled(h, t.x, ref);
+                            z = two_sum(t.l, -y.hi);
+                            z.lo -= y.lo;
+                        }
+                        sa = pair_add(sa, pair_times(q, z));
+                    }
+                }
 #pragma unroll
-            for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
-            pair_warp(sa);
-            pair_warp(sq);
+                for (int i = 16; i > 0; i >>= 1) s += __shfl_xor_sync(0xffffffffu, s, i);
+                pair_warp(sa);
+                pair_warp(sq);
+            }
             flags = __reduce_or_sync(0xffffffffu, flags);
             if (uint32_t(lane) < parts) {
                 const uint32_t to = dsmem_map(smem_addr(lists + put.at * parts + rank), lane),
@@ -386,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
         // Closes a row; false where a wait gave up.
         auto close = [&](const Open& o) {
             if (!wait(&S.join[taken.at], taken.phase, P.wait_ns)) return false;
-            const RowJob& h = o.h;
+            const RowJob h = job_of(o.item);
             // outside the list, and inside
             const float4* in = sums + taken.at * parts * kWarps;
             Stats out = stats_empty();
@@ -399,24 +413,24 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             }
             ListSums mine{-kFloatMax, 0.f, {0.f, 0.f}, {0.f, 0.f}, 0, 0};
             if (uint32_t(lane) < parts) mine = lists[taken.at * parts + lane];
-            Stats list{mine.ref, mine.s, 0.f};
-            stats_move(list, max_warp(mine.ref), h.c);
+            Stats inside{mine.ref, mine.s, 0.f};
+            stats_move(inside, max_warp(mine.ref), h.c);
             float q_list = mine.q.hi;
 #pragma unroll
             for (int i = 16; i > 0; i >>= 1) {
                 out.s += __shfl_xor_sync(0xffffffffu, out.s, i);
-                list.s += __shfl_xor_sync(0xffffffffu, list.s, i);
+                inside.s += __shfl_xor_sync(0xffffffffu, inside.s, i);
                 q_list += __shfl_xor_sync(0xffffffffu, q_list, i);
             }
             const uint32_t flags = __reduce_or_sync(0xffffffffu, mine.flags);
 
-            const float most = fmaxf(out.ref, list.ref);
+            const float most = fmaxf(out.ref, inside.ref);
             auto lift = [&](float ref) {
                 const float d = ref - most;
                 return exp2f(fmaxf(fmaf(d, h.c_hi, d * h.c_lo), kLowest));
             };
             const float f_out = lift(out.ref);
-            const float s = out.s * f_out + list.s * lift(list.ref);
+            const float s = out.s * f_out + inside.s * lift(inside.ref);
             const int status = h.bad_param || (flags & kBadList)        ? SAMPLER_ROW_BAD_PARAM
                                : isnan(out.s) || (flags & kBadLogit) ? SAMPLER_ROW_NONFINITE
                                : s == 0.f                            ? SAMPLER_ROW_ALL_NEG_INF
@@ -430,12 +444,9 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             if (kGrad) {
                 // the list's own gradients, in their logits' place
                 T* to = reinterpret_cast<T*>(smem + o.buffer * buffer_bytes);
-                const T* x = static_cast<const T*>(a.logits) + int64_t(o.item.row) * a.row_stride;
-                const int head = row_span(x, a.vocab).head - first_vec * kPer;
-#pragma unroll
-                for (int e = 0; e < kHeld; ++e) {
-                    const Entry& t = o.list[e];
-                    if (t.at < 0) continue;
+                const int head = o.item.head - first_vec * kPer;
+                for (int i = lane; i < o.count; i += 32) {
+                    const Entry t = list[i];
                     float y = fmaf(w, lift(t.x) * inv_s, -t.q);
                     if (a.tokens && t.at == o.item.token + head) y -= coef;
                     store_grad(to + t.at, fine ? y * g : quiet_nan());
@@ -531,15 +542,12 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
                         put_vector<T>(g, vocab, span.head, i, true, make_uint4(0u, 0u, 0u, 0u));
                 }
             }
-            RowJob h;
-            h.token = item.token;
-            row_scale(h, a, item.temperature);
-            const T* x = static_cast<const T*>(a.logits) + int64_t(item.row) * a.row_stride;
-            const RowSpan span = row_span(x, a.vocab);
+            const RowSpan span{item.head, item.count};
             const int n = min(first_vec + P.part_vecs, span.count) - first_vec;
             const int end = span.head + vocab;
-            const Two c_hi = two(h.c_hi, h.c_hi), c_lo = two(h.c_lo, h.c_lo);
-            if (!wait(&S.marked[map1.at], map1.phase, P.wait_ns) || !wait(&S.full[buf1.at], buf1.phase, P.wait_ns)) return -1;
+            const Two c_hi = two(item.c_hi, item.c_hi), c_lo = two(item.c_lo, item.c_lo);
+            const float c = item.c;
+            if (!wait(&S.full[buf1.at], buf1.phase, P.wait_ns)) return -1;
             const uint4* in = reinterpret_cast<const uint4*>(smem + buf1.at * buffer_bytes);
             unsigned char* bits = maps + map1.at * map_bytes(P.part_vecs);
             Stats st = stats_empty();
@@ -547,15 +555,13 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
             for (int i0 = 0; i0 < n; i0 += kStep) {
                 uint4 v[kVecs];
                 uint32_t* marks = reinterpret_cast<uint32_t*>(bits + i0) + tid;  // (a byte for each of the four vectors)
-                // whole, and inside the row
-                const bool inner = i0 + kStep <= n && (first_vec + i0) * kPer >= span.head && (first_vec + i0 + kStep) * kPer <= end;
 #pragma unroll
                 for (int k = 0; k < kVecs; ++k) {
                     const int i = i0 + k * kConsumers + tid;
                     v[k] = nothing<T>();
-                    if (inner || i < n) v[k] = in[i];
+                    if (i < n) v[k] = in[i];
                 }
-                if (!inner)
+                if (ragged(span, end, first_vec + i0, kPer))
 #pragma unroll
                     for (int k = 0; k < kVecs; ++k) {
                         const int at = (first_vec + i0 + k * kConsumers + tid) * kPer;
@@ -563,13 +569,14 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
                     }
                 if (const uint32_t b = *marks) {
 #pragma unroll
-                    for (int k = 0; k < kVecs; ++k) blend<T>(v[k], nothing<T>(), b >> 8 * k & 0xffu);
+                    for (int k = 0; k < kVecs; ++k)
+                        if (b >> 8 * k & 0xffu) blend<T>(v[k], nothing<T>(), b >> 8 * k & 0xffu);
                     if (!kGrad) *marks = 0;
                 }
-                fold<T, false, kVecs>(st, bad, v, c_hi, c_lo, h.c);
+                fold<T, false, kVecs>(st, bad, v, c_hi, c_lo, c);
             }
             if (bad) st.s = quiet_nan();
-            stats_warp<false>(st, h.c);
+            stats_warp<false>(st, c);
             // (A buffer of sums is written again four rows later: by then every closer of the cluster is done with it, as
             // each puts a row's list sums after closing the row two before, and a warp puts a row's after that two before
             // is closed.)
@@ -594,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
                 const Factors fs{two(-f.ref, -f.ref), two(f.c, f.c), two(f.k, f.k), 0};
                 const T* x = static_cast<const T*>(a.logits) + int64_t(item.row) * a.row_stride;
                 T* g = static_cast<T*>(a.out_grad) + int64_t(item.row) * a.grad_stride;
-                const RowSpan span = row_span(x, a.vocab);
+                const RowSpan span{item.head, item.count};
                 const int n = min(first_vec + P.part_vecs, span.count) - first_vec;
                 const bool whole = ((reinterpret_cast<uintptr_t>(g) - reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
                 const int token_vec = f.token == kNoToken ? -1 : (f.token + span.head) / kPer - first_vec;
@@ -604,20 +611,20 @@ __global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_const
                 for (int i0 = 0; i0 < n; i0 += kStep) {
                     uint32_t* marks = reinterpret_cast<uint32_t*>(bits + i0) + tid;
                     const uint32_t marked = *marks;
-                    const bool inner = whole && i0 + kStep <= n && (first_vec + i0) * kPer >= span.head &&
-                                       (first_vec + i0 + kStep) * kPer <= end && !(token_vec >= i0 && token_vec < i0 + kStep);
-                    if (inner) {
+                    if (whole && !ragged(span, end, first_vec + i0, kPer) && !(token_vec >= i0 && token_vec < i0 + kStep)) {
                         uint4* to = reinterpret_cast<uint4*>(g - span.head) + first_vec + i0 + tid;
                         uint4 v[kVecs], y[kVecs];
 #pragma unroll
-                        for (int k = 0; k < kVecs; ++k) v[k] = in[i0 + k * kConsumers + tid];
+                        for (int k = 0; k < kVecs; ++k) v[k] = in[min(i0 + k * kConsumers + tid, n - 1)];
 #pragma unroll
                         for (int k = 0; k < kVecs; ++k) y[k] = gradient<T, false>(v[k], fs);
                         if (marked)
 #pragma unroll
-                            for (int k = 0; k < kVecs; ++k) blend<T>(y[k], v[k], marked >> 8 * k & 0xffu);
+                            for (int k = 0; k < kVecs; ++k)
+                                if (marked >> 8 * k & 0xffu) blend<T>(y[k], v[k], marked >> 8 * k & 0xffu);
 #pragma unroll
-                        for (int k = 0; k < kVecs; ++k) __stcs(to + k * kConsumers, y[k]);
+                        for (int k = 0; k < kVecs; ++k)
+                            if (i0 + k * kConsumers + tid < n) __stcs(to + k * kConsumers, y[k]);
                     } else {
 #pragma unroll 1
                         for (int k = 0; k < kVecs; ++k) {

@@ -79,15 +79,32 @@ __device__ __forceinline__ int64_t dealer_next(RowDealer& d, const sampler_rows_
     return d.base + bit;
 }
 
-// A row as it is handed over: what it needs besides its logits, read ahead.
+// A row as it is handed over: what it needs besides its logits, read ahead, and what follows from that.
 struct RowItem {
-    int32_t row;  // -1: no more rows
+    int32_t row;   // -1: no more rows
     int32_t live;  // 0: left out
     int32_t last;  // of its batch
-    int32_t token;
-    float temperature, weight;
-    float x_t;  // the token's logit (0 without one)
+    int32_t token, bad_param;
+    float weight, temperature;
+    float x_t;     // the token's logit (0 without one)
+    float c, c_hi, c_lo, inv_t, inv_t_lo;  // as in RowJob
+    int32_t head, count;                   // of its span of vectors
 };
+
+// What the functions of row_loss.cuh read of a row.
+__device__ __forceinline__ RowJob job_of(const RowItem& i)
+{
+    RowJob h;
+    h.token = i.token;
+    h.bad_param = i.bad_param;
+    h.x_t = i.x_t;
+    h.c = i.c;
+    h.c_hi = i.c_hi;
+    h.c_lo = i.c_lo;
+    h.inv_t = i.inv_t;
+    h.inv_t_lo = i.inv_t_lo;
+    return h;
+}
 
 constexpr int kQueueBatch = 8;  // rows whose parameters are fetched together
 constexpr int kQueueFirst = 2;  // the first time, when all wait for them
@@ -130,13 +147,32 @@ __device__ __forceinline__ bool queue_fill(RowQueue& S, const sampler_rows_t& a,
                 live |= 1u << count;
             ++count;
         }
-        RowItem item{int32_t(mine), int32_t(live >> lane & 1u), lane == count - 1, 0, 1.f, 1.f, 0.f};
+        RowItem item;
+        item.row = int32_t(mine);
+        item.live = int32_t(live >> lane & 1u);
+        item.last = lane == count - 1;
+        item.token = 0;
+        item.temperature = item.weight = 1.f;
+        item.x_t = 0.f;
         if (mine >= 0) {
             if (a.tokens) item.token = a.tokens[mine];
             if (a.temperature) item.temperature = a.temperature[mine];
             if (a.weight) item.weight = a.weight[mine];
+            const T* x = static_cast<const T*>(a.logits) + mine * a.row_stride;
             if (want_token && a.tokens && item.live && item.token >= 0 && int64_t(item.token) < a.vocab)
-                item.x_t = load_logit(static_cast<const T*>(a.logits) + mine * a.row_stride + item.token);
+                item.x_t = load_logit(x + item.token);
+            RowJob h;
+            h.token = item.token;
+            row_scale(h, a, item.temperature);
+            item.bad_param = h.bad_param;
+            item.c = h.c;
+            item.c_hi = h.c_hi;
+            item.c_lo = h.c_lo;
+            item.inv_t = h.inv_t;
+            item.inv_t_lo = h.inv_t_lo;
+            const RowSpan span = row_span(x, a.vocab);
+            item.head = span.head;
+            item.count = span.count;
         }
         if (!wait(&S.empty[batch.at], batch.phase ^ 1u, wait_ns)) return false;
         if (lane < count) S.items[batch.at][lane] = item;

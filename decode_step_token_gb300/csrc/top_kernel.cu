@@ -787,11 +787,8 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
             if (part == 0) write_none(P, r, SAMPLER_ROW_OK);
             continue;
         }
-        RowJob h;
-        h.token = row.token;
-        row_scale(h, a, row.temperature);
-        h.x_t = row.x_t;
-        const RowSpan span = row_span(static_cast<const T*>(a.logits) + r * a.row_stride, a.vocab);
+        const RowJob h = job_of(row);
+        const RowSpan span{row.head, row.count};
         const int first = int(part) * P.part_vecs, last = min(first + P.part_vecs, span.count);
         const Scale scale{h.c, h.c_hi, h.c_lo};
         Sums st{-pos_inf(), -kFloatMax, 0.f, 0.f};

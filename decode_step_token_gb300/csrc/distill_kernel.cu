@@ -38,7 +38,7 @@ namespace distill {
 
 using namespace rows;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 16;
 constexpr int kConsumers = kWarps * 32;
 constexpr int kProducer = kWarps, kCloser = kWarps + 1;
 constexpr int kClosers = 2;                  // warps, of which each takes every other row
@@ -203,7 +203,7 @@ __device__ __forceinline__ uint4 nothing()
 }
 
 template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kThreads, 2) distill_kernel(const __grid_constant__ DistillParams P)
+__global__ void __launch_bounds__(kThreads, 1) distill_kernel(const __grid_constant__ DistillParams P)
 {
     constexpr int kPer = Elems<T>::kPer;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -685,9 +685,9 @@ int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, 
     auto part_of = [&](int parts) { return int((vecs + parts - 1) / parts); };
     auto fits = [&](int parts, int buffers, int smem) { return smem_of(part_of(parts), buffers, parts) <= smem; };
     int parts = 1;
-    while (parts < kMaxParts && !fits(parts, 3, kSmemTwo)) parts *= 2;
-    const bool two = fits(parts, 2, kSmemTwo);
-    while (parts < kMaxParts && p.rows.n_rows * parts < 2 * sms && part_of(2 * parts) >= 256) parts *= 2;
+    while (parts < kMaxParts && !fits(parts, 3, kSmemOne)) parts *= 2;
+    const bool two = false;
+    while (parts < kMaxParts && p.rows.n_rows * parts < sms && part_of(2 * parts) >= 256) parts *= 2;
     const int budget = two ? kSmemTwo : kSmemOne;
     p.part_vecs = part_of(parts);
     p.buffers = 2;

@@ -63,7 +63,7 @@ struct Shared {
     __align__(16) uint64_t list[2][kCap];  // one is filled, the other is what it is cut into
     uint64_t sorted[2][kMost];
     Close close[2];
-    __align__(16) uint32_t largest[kConsumers];  // of a chunk, in each thread, as orders
+    __align__(16) uint16_t largest[kConsumers];  // of a chunk, in each thread, in bf16
     float4 state[kConsumers];   // sums, on their way into functions out of line and back
     float2 sums[kWarps];
     uint32_t tops[kWarps];
@@ -147,6 +147,47 @@ __device__ __forceinline__ uint32_t packed_bar<uint16_t>(float bar)
     if ((u >> 31) && (u & 0xffffu)) u += 0x10000u;
     u >>= 16;
     return u << 16 | u;
+}
+
+// The largest element of a vector, NaN where there is one, as it is compared: fp32 a float, bf16 those of the even and of
+// the odd elements.
+template <typename T>
+struct Peak;
+template <>
+struct Peak<float> {
+    static __device__ __forceinline__ uint32_t none() { return 0xff800000u; }
+    static __device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b)
+    {
+        return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+    }
+    static __device__ __forceinline__ bool above(uint32_t a, uint32_t bar) { return __uint_as_float(a) > __uint_as_float(bar); }
+    static __device__ __forceinline__ float value(uint32_t a) { return __uint_as_float(a); }
+};
+template <>
+struct Peak<uint16_t> {
+    static __device__ __forceinline__ uint32_t none() { return 0xff80ff80u; }
+    static __device__ __forceinline__ uint32_t join(uint32_t a, uint32_t b)
+    {
+        uint32_t y;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+        return y;
+    }
+    static __device__ __forceinline__ bool above(uint32_t a, uint32_t bar)
+    {
+        uint32_t m;
+        asm("set.gt.u32.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(bar));
+        return m != 0;
+    }
+    static __device__ __forceinline__ float value(uint32_t a)
+    {
+        return max_nan(__uint_as_float(a << 16), __uint_as_float(a & 0xffff0000u));
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ uint32_t peak(const uint4& v)
+{
+    return Peak<T>::join(Peak<T>::join(v.x, v.y), Peak<T>::join(v.z, v.w));
 }
 
 // Which elements of a vector are above the bar (a bit for each); those become -inf.
@@ -438,6 +479,14 @@ __device__ __noinline__ uint32_t cut_long(uint32_t at, uint32_t count, uint32_t 
     return at ^ 1;
 }
 
+// Adds 1 to each half of `count` (in bf16) whose value of `a` is above `b`'s.
+__device__ __forceinline__ void count_above(uint32_t& count, uint32_t a, uint32_t b)
+{
+    uint32_t one;
+    asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(one) : "r"(a), "r"(b));
+    asm("add.rn.bf16x2 %0, %0, %1;" : "+r"(count) : "r"(one));
+}
+
 // Where a chunk of a row is: its place in the ring, the first of its vectors in the span, the end of the part's, and the
 // span's elements that the row begins and ends at.
 struct Chunk {
@@ -448,14 +497,19 @@ template <typename T>
 __device__ __forceinline__ void load(uint4 (&v)[kVecs], const Chunk& p)
 {
     constexpr int kPer = Elems<T>::kPer;
-    const uint4* in = reinterpret_cast<const uint4*>(ring_of() + p.at);
-    const uint32_t none = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    const uint4* in = reinterpret_cast<const uint4*>(ring_of() + p.at) + threadIdx.x;
+    const uint32_t none = Peak<T>::none();
+    if (p.base + kChunkVecs <= p.last && p.base * kPer >= p.head && (p.base + kChunkVecs) * kPer <= p.end) {
+#pragma unroll
+        for (int k = 0; k < kVecs; ++k) v[k] = in[k * kConsumers];
+        return;
+    }
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
         const int i = k * kConsumers + int(threadIdx.x);
         v[k] = make_uint4(none, none, none, none);
         if (p.base + i < p.last) {
-            v[k] = in[i];
+            v[k] = in[k * kConsumers];
             const int at = (p.base + i) * kPer;
             if (at < p.head || at + kPer > p.end) Elems<T>::mask(v[k], p.head - at, p.end - at);
         }
@@ -792,7 +846,8 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
         const int first = int(part) * P.part_vecs, last = min(first + P.part_vecs, span.count);
         const Scale scale{h.c, h.c_hi, h.c_lo};
         Sums st{-pos_inf(), -kFloatMax, 0.f, 0.f};
-        bool has_n = false, bad = false;
+        bool has_n = false;
+        uint32_t worst = Peak<T>::none();  // NaN, or +inf, where the row has one
         uint32_t at = 0, count = 0;  // the list that is filled, and, at the end, the keys in it
         if (tid < 2) S.count[tid] = 0;
         bar_sync();
@@ -801,41 +856,52 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
             const Chunk chunk{int(slot.at) * kChunkBytes, base, ok ? last : 0, span.head, span.head + int(a.vocab)};
             uint4 v[kVecs];
             load<T>(v, chunk);
-            const float most = max_nan(max_nan(Elems<T>::largest(v[0]), Elems<T>::largest(v[1])),
-                                       max_nan(Elems<T>::largest(v[2]), Elems<T>::largest(v[3])));
-            bad |= !(most < pos_inf());
+            uint32_t peaks[kVecs];
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) peaks[k] = peak<T>(v[k]);
+            const uint32_t four = Peak<T>::join(Peak<T>::join(peaks[0], peaks[1]), Peak<T>::join(peaks[2], peaks[3]));
+            worst = Peak<T>::join(worst, four);
             bool first_bar = false;
             if (!has_n) {
-                // the n-th of the threads' largest; where fewer threads have any, all are taken
-                const uint32_t mine = order_of(most);
-                S.largest[tid] = mine;
+                // The n-th of the threads' largest, rounded down to bf16 (two to an instruction, whose counts are exact in
+                // bf16 up to 256); where fewer threads have any, all are taken.
+                const float most = Peak<T>::value(four);
+                const uint32_t mine = packed_bar<uint16_t>(most);
+                S.largest[tid] = uint16_t(mine);
                 bar_sync();
-                uint32_t above = 0;
+                uint32_t n0 = 0, n1 = 0;
                 const uint4* all = reinterpret_cast<const uint4*>(S.largest);
 #pragma unroll 8
-                for (int j = 0; j < kConsumers / 4; ++j) {
+                for (int j = 0; j < kConsumers / 8; ++j) {
                     const uint4 o = all[j];
-                    above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+                    count_above(n0, o.x, mine);
+                    count_above(n1, o.y, mine);
+                    count_above(n0, o.z, mine);
+                    count_above(n1, o.w, mine);
                 }
-                // of equal ones all have the first's place: the least of those that come before the n-th or on it
-                const uint32_t least = __reduce_min_sync(0xffffffffu, above < n ? mine : 0xffffffffu);
+                const float above = __uint_as_float(n0 << 16) + __uint_as_float(n0 & 0xffff0000u) + __uint_as_float(n1 << 16) +
+                                    __uint_as_float(n1 & 0xffff0000u);
+                // (of equal ones all have the first's place: the least of those that come before the n-th or on it)
+                const bool within = above < float(n);
+                const uint32_t order = order_of(__uint_as_float(mine << 16));
+                const uint32_t least = __reduce_min_sync(0xffffffffu, within ? order : 0xffffffffu);
                 if (lane == 0) S.tops[warp] = least;
-                first_bar = has_n = bar_count(above < n && most >= -kFloatMax) >= n;
+                first_bar = has_n = bar_count(within && most >= -kFloatMax) >= n;
                 if (has_n) {
                     uint32_t lo = 0xffffffffu;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) lo = min(lo, S.tops[w]);
+                    lo = max(lo, order_of(-kFloatMax));
                     move(st, value_of(lo), h.c);
                     st.bar = below(lo);
                 }
             }
             const float s_before = st.s, t_before = st.t;
             uint32_t top = 0, above = 0;
-            if (!(most <= st.bar)) {
-                const uint32_t bar = packed_bar<T>(st.bar);
+            const uint32_t bar = packed_bar<T>(st.bar);
 #pragma unroll
-                for (int k = 0; k < kVecs; ++k) above |= take_above<T>(v[k], bar) << k * kPer;
-            }
+            for (int k = 0; k < kVecs; ++k)
+                if (Peak<T>::above(peaks[k], bar)) above |= take_above<T>(v[k], bar) << k * kPer;
             while (above) {
                 const int bit = __ffs(above) - 1, i = bit / kPer * kConsumers + tid, j = bit % kPer;
                 above &= above - 1;
@@ -847,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
             }
             __syncwarp();
             add<T, kEntropy>(st, v, two(h.c, h.c));
-            const bool any = bar_any(top >= (first_bar ? n + 1 : trigger) || !ok), end = base + kChunkVecs >= last;
+            const bool any = bar_any(top >= (first_bar ? about : trigger) || !ok), end = base + kChunkVecs >= last;
             if (any && bar_any(!ok)) {
                 failed = true;
                 break;
@@ -879,7 +945,7 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
             slot.next(kSlots);
         }
         if (failed) break;
-        bad = bar_any(bad);
+        const bool bad = bar_any(!(Peak<T>::value(worst) < pos_inf()));
         if (P.parts == 1) {
             failed = !hand_over<kEntropy>(P, S.list[at], count, st, h, row.temperature, bad, r, turn);
             if (failed) break;

@@ -41,34 +41,46 @@ constexpr int kThreads = kConsumers + 64;
 constexpr int kVecs = 4;                        // of a chunk in each consumer
 constexpr int kChunkVecs = kConsumers * kVecs;
 constexpr int kChunkBytes = kChunkVecs * 16;
-constexpr int kSlots = 5;
+constexpr int kSlots = 4;
+constexpr int kJobs = 4;                         // of the closer
+constexpr int kLane = 8;                         // keys of a list in each of its lanes, at most
 constexpr int kMost = SAMPLER_MAX_ALTERNATIVES;
 constexpr int kCap = 1024;                      // keys in a list
 constexpr int kMaxToken = 262143;
 constexpr int kMaxTopParts = 32;                // of a row: the lanes of a warp
 constexpr float kLostUnit = 1099511627776.f;    // 2^40
 
-// A row for the closer: its keys are in order, and these are the sums of the rest.
-struct Close {
-    int row;  // -1: no more rows
-    int count, token;
-    float ref, s, t;
-    float temperature, x_t;
+// What the closer is asked for: to cut a list down, to close a row, or to end.
+enum JobKind : int { kCut, kClose, kEnd };
+struct Job {
+    int kind, list, count;
+    int ordered;  // kClose: the list is the row's, in order
+    int row, token;
+    float ref;    // of the sums of what is not in the list
+    float bar;    // the list's keys have values of that or above
+    float c, c_hi, c_lo, inv_t, inv_t_lo, x_t;
 };
 
 struct Shared {
     uint64_t full[kSlots], empty[kSlots];
-    uint64_t ready[2], written[2];  // rows with the closer
+    uint64_t ready[kJobs], ended[kJobs];
+    uint64_t closed[2];  // the rows that had a pair of lists
     RowQueue queue;
-    __align__(16) uint64_t list[2][kCap];  // one is filled, the other is what it is cut into
-    uint64_t sorted[2][kMost];
-    Close close[2];
+    // two for a row, whose successor has the other two: one is filled, the other is what it is cut into, or what is filled
+    // while the closer cuts it
+    __align__(16) uint64_t list[4][kCap];
+    uint64_t sorted[kMost];
+    Job jobs[kJobs];
+    uint64_t cut_least;   // what a cut has left: its least key, how many, and the sums of the others
+    uint32_t cut_count;
+    float cut_ref, cut_s, cut_t;
     __align__(16) uint16_t largest[kConsumers];  // of a chunk, in each thread, in bf16
     float4 state[kConsumers];   // sums, on their way into functions out of line and back
-    float2 sums[kWarps];
+    float2 sums[2][kWarps];     // of a row's consumers, for the closer
     uint32_t tops[kWarps];
     uint32_t tally[3];
-    uint32_t count[2];          // keys put into a list (more than kCap: the last of them are not there)
+    uint32_t count[4];          // keys put into a list (functions out of line)
+    uint32_t pushed[4];         // keys put into the row's list since it was last changed; used in turn
     unsigned long long lost_s[kWarps];  // what fell out of a list, relative to the largest of it, in multiples of 2^-40
     long long lost_t[kWarps];
     uint32_t lost_most;                 // its order; 0 between cuts
@@ -338,12 +350,12 @@ struct Scale {
     float c, c_hi, c_lo;
 };
 
-// The next place in a list for a lane by itself. (Written so that the lanes that want one, a few of a warp, are not put
-// together first.)
-__device__ __forceinline__ uint32_t next_place(uint32_t* count)
+// The next `want` places in a list for a lane by itself. (Written so that the lanes that want some, a few of a warp, are
+// not put together first.)
+__device__ __forceinline__ uint32_t next_places(uint32_t* count, uint32_t want)
 {
     uint32_t at;
-    asm volatile("atom.shared.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(smem_addr(count)) : "memory");
+    asm volatile("atom.shared.add.u32 %0, [%1], %2;" : "=r"(at) : "r"(smem_addr(count)), "r"(want) : "memory");
     return at;
 }
 
@@ -520,8 +532,8 @@ __device__ __forceinline__ void load(uint4 (&v)[kVecs], const Chunk& p)
 // before is kept, and the chunk's elements are looked at again, one of each thread at a time, as keys. Sums come and go
 // in S.state (before the chunk; after it); the list that is filled in the end is returned.
 template <typename T, bool kEntropy>
-__device__ __noinline__ uint32_t slow_chunk(uint32_t at, int chunk_at, int base, int last, int head, int end, uint32_t n, float c,
-                                            float c_hi, float c_lo)
+__device__ __noinline__ uint32_t slow_chunk(uint32_t at, uint32_t valid, int chunk_at, int base, int last, int head, int end,
+                                            uint32_t n, float c, float c_hi, float c_lo)
 {
     constexpr int kPer = Elems<T>::kPer;
     Shared& S = shared();
@@ -531,9 +543,9 @@ __device__ __noinline__ uint32_t slow_chunk(uint32_t at, int chunk_at, int base,
     Sums st{in.x, in.y, in.z, in.w};
     bar_sync();
 #pragma unroll 1
-    for (uint32_t i0 = 0; i0 < uint32_t(kCap); i0 += kConsumers) {
-        const uint64_t k = S.list[at][i0 + tid];
-        const bool stays = key_token(k) < before;
+    for (uint32_t i0 = 0; i0 < valid; i0 += kConsumers) {
+        const uint64_t k = i0 + tid < valid ? S.list[at][i0 + tid] : 0;
+        const bool stays = k != 0 && key_token(k) < before;
         const uint32_t to = places(&S.count[at ^ 1], stays);
         if (stays) S.list[at ^ 1][to] = k;
     }
@@ -607,7 +619,7 @@ __device__ __forceinline__ void write_none(const TopParams& P, int64_t r, int st
     }
 }
 
-// The closer, with a row's `count` largest keys in order and the sums of the rest: its outputs.
+// The closer (a warp), with a row's `count` largest keys in order and the sums of the rest: its outputs.
 template <bool kEntropy>
 __device__ __forceinline__ void close_row(const TopParams& P, const uint64_t* sorted, int count, const Sums& st,
                                           const RowJob& h, int64_t r)
@@ -654,63 +666,258 @@ __device__ __forceinline__ void close_row(const TopParams& P, const uint64_t* so
     }
 }
 
-// A row's keys in a list and the sums of the rest, each thread's own: the keys in order, and the sums of all, to the
-// closer. `turn`: rows that have gone to it. False where a wait gave up. (A row that has no statistics is written here.)
-template <bool kEntropy>
-__device__ __forceinline__ bool hand_over(const TopParams& P, const uint64_t* list, uint32_t count, Sums st, const RowJob& h,
-                                          float temperature, bool bad, int64_t r, uint32_t& turn)
+// ---------------------------------------------------------------- the closer
+// A list of up to 32 * kLane keys in a warp's lanes.
+struct Keys {
+    uint64_t k[kLane];
+};
+
+__device__ __forceinline__ void take_keys(Keys& a, const uint64_t* list, int count)
 {
-    Shared& S = shared();
-    const int tid = threadIdx.x;
-    const uint32_t n = uint32_t(P.top.top_n), slot = turn & 1;
-    const bool ok = wait(&S.written[slot], (turn >> 1 & 1) ^ 1u, P.wait_ns);
-    if (bar_any(!ok)) return false;
-    rank<kEntropy>(list, count, n, S.sorted[slot], st, Scale{h.c, h.c_hi, h.c_lo});
-    count = min(count, n);
-    // the sums of all threads, in order
-    float s = st.s, t = st.t;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (kEntropy) t += __shfl_xor_sync(0xffffffffu, t, o);
-    }
-    if ((tid & 31) == 0) S.sums[tid >> 5] = make_float2(s, t);
-    bar_sync();
-    const int status = h.bad_param    ? SAMPLER_ROW_BAD_PARAM
-                       : bad          ? SAMPLER_ROW_NONFINITE
-                       : count == 0   ? SAMPLER_ROW_ALL_NEG_INF
-                                      : SAMPLER_ROW_OK;
-    if (status != SAMPLER_ROW_OK) {
-        write_none(P, r, status);
-        return true;
-    }
-    if (tid == 0) {
-        s = t = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            s += S.sums[w].x;
-            t += S.sums[w].y;
-        }
-        S.close[slot] = Close{int(r), int(count), h.token, st.ref, s, t, temperature, h.x_t};
-        mbar_arrive(&S.ready[slot]);
-    }
-    ++turn;
-    return true;
+    for (int i = 0; i < kLane; ++i) a.k[i] = lane + 32 * i < count ? list[lane + 32 * i] : 0;
 }
 
-// The last part of a row joins them all. One more than the rows that have gone to the closer then; 0 where a wait gave up.
+__device__ __forceinline__ uint32_t reaching(const Keys& a, uint64_t key)
+{
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) c += a.k[i] >= key;
+    return __reduce_add_sync(0xffffffffu, c);
+}
+
+// How many reach each of three orders, ten bits for each.
+__device__ __forceinline__ uint32_t reaching(const Keys& a, uint32_t o1, uint32_t o2, uint32_t o3)
+{
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) {
+        const uint32_t o = uint32_t(a.k[i] >> 32);
+        c += (o >= o1 ? 1u : 0u) + (o >= o2 ? 1u << 10 : 0u) + (o >= o3 ? 1u << 20 : 0u);
+    }
+    return __reduce_add_sync(0xffffffffu, c);
+}
+
+// As select: a key that n to `most` of the lanes' keys reach (exact), or that at least n reach and no other value's with
+// fewer (not exact: more than `most` where ties are). There are more than `most` keys, all of order `lo` or above. The
+// values' steps cut the range in four.
+__device__ __forceinline__ uint64_t select_warp(const Keys& a, uint32_t n, uint32_t most, bool exact, uint32_t lo)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) top = max(top, uint32_t(a.k[i] >> 32));
+    uint32_t hi = __reduce_max_sync(0xffffffffu, top) + 1;
+#pragma unroll 1
+    while (hi - lo > 1) {
+        const uint32_t q = max((hi - lo) / 4, 1u), o1 = lo + q, o2 = min(o1 + q, hi), o3 = min(o2 + q, hi);
+        const uint32_t got = reaching(a, o1, o2, o3), c1 = got & 1023u, c2 = got >> 10 & 1023u, c3 = got >> 20;
+        uint32_t c;
+        if (c3 >= n) {
+            lo = o3;
+            c = c3;
+        } else if (c2 >= n) {
+            lo = o2;
+            hi = o3;
+            c = c2;
+        } else if (c1 >= n) {
+            lo = o1;
+            hi = o2;
+            c = c1;
+        } else {
+            hi = o1;
+            continue;
+        }
+        if (c <= most) return uint64_t(lo) << 32;
+    }
+    if (!exact) return uint64_t(lo) << 32;
+    // among the tokens of that value: the lowest n of them that are still wanted
+    uint64_t l = uint64_t(lo) << 32 | uint32_t(~uint32_t(kMaxToken)), h = uint64_t(lo + 1) << 32;
+#pragma unroll 1
+    while (h - l > 1) {
+        const uint64_t mid = l + (h - l) / 2;
+        const uint32_t got = reaching(a, mid);
+        if (got >= n) {
+            l = mid;
+            if (got <= most) break;
+        } else {
+            h = mid;
+        }
+    }
+    return l;
+}
+
+// The keys that reach `least` go to the front of the list; the sums of the others, relative to their largest, as whole
+// multiples of 2^-40. Their number.
 template <bool kEntropy>
-__device__ __noinline__ uint32_t join_parts(const TopParams& P, int64_t r, int32_t token, float temperature, float x_t,
-                                            uint32_t turn)
+__device__ __forceinline__ int split_keys(const Keys& a, uint64_t least, uint64_t* list, const Scale& q, Sums& lost)
+{
+    const int lane = threadIdx.x & 31;
+    int count = 0;
+    uint32_t most = 0;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kLane; ++i) {
+        const bool stays = a.k[i] >= least;
+        const uint32_t lanes = __ballot_sync(0xffffffffu, stays);
+        if (stays)
+            list[count + __popc(lanes & ((1u << lane) - 1u))] = a.k[i];
+        else
+            most = max(most, uint32_t(a.k[i] >> 32));
+        count += __popc(lanes);
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    lost = Sums{0.f, -kFloatMax, 0.f, 0.f};
+    if (most != 0) {
+        lost.ref = value_of(most);
+        unsigned long long s = 0;
+        long long t = 0;
+#pragma unroll
+        for (int i = 0; i < kLane; ++i) {
+            if (a.k[i] >= least || a.k[i] == 0) continue;
+            const float d = key_value(a.k[i]) - lost.ref, u = fmaxf(fmaf(d, q.c_hi, d * q.c_lo), kLowest), e = exp2_fast(u);
+            s += __float2ull_rn(e * kLostUnit);
+            if (kEntropy) t += __float2ll_rn(e * u * kLostUnit);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (kEntropy) t += __shfl_xor_sync(0xffffffffu, t, o);
+        }
+        lost.s = __ull2float_rn(s) * (1.f / kLostUnit);
+        lost.t = __ll2float_rn(t) * (1.f / kLostUnit);
+    }
+    __syncwarp();
+    return count;
+}
+
+// The keys at the front of a list in order.
+__device__ __forceinline__ void sort_keys(const uint64_t* list, int count, uint64_t* to)
+{
+    const int lane = threadIdx.x & 31;
+    uint64_t mine[kMost / 32];
+    int rank[kMost / 32];
+#pragma unroll
+    for (int i = 0; i < kMost / 32; ++i) {
+        mine[i] = lane + 32 * i < count ? list[lane + 32 * i] : 0;
+        rank[i] = 0;
+    }
+    if (count <= 32) {
+#pragma unroll 4
+        for (int j = 0; j < count; ++j) rank[0] += list[j] > mine[0];
+    } else {
+#pragma unroll 2
+        for (int j = 0; j < count; ++j) {
+            const uint64_t k = list[j];
+#pragma unroll
+            for (int i = 0; i < kMost / 32; ++i) rank[i] += k > mine[i];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kMost / 32; ++i)
+        if (lane + 32 * i < count) to[rank[i]] = mine[i];
+    __syncwarp();
+}
+
+template <bool kEntropy>
+__device__ __forceinline__ void run_closer(const TopParams& P)
+{
+    Shared& S = shared();
+    const int lane = threadIdx.x & 31;
+    const uint32_t n = uint32_t(P.top.top_n);
+    for (uint32_t j = 0;; ++j) {
+        const uint32_t slot = j % kJobs;
+        // (the consumers give up before it does, and say so)
+        if (!wait(&S.ready[slot], j / kJobs & 1u, 8 * kWaitNs)) return;
+        const Job job = S.jobs[slot];
+        if (job.kind == kEnd) return;
+        const Scale q{job.c, job.c_hi, job.c_lo};
+        uint64_t* list = S.list[job.list];
+        int count = job.count;
+        if (job.kind == kCut) {
+            Keys keys;
+            take_keys(keys, list, count);
+            const uint64_t least = select_warp(keys, n, n + n / 4 + 8, false, order_of(job.bar));
+            Sums lost;
+            count = split_keys<kEntropy>(keys, least, list, q, lost);
+            if (lane == 0) {
+                S.cut_least = least;
+                S.cut_count = uint32_t(count);
+                S.cut_ref = lost.ref;
+                S.cut_s = lost.s;
+                S.cut_t = lost.t;
+            }
+        } else {
+            Sums st{0.f, job.ref, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {  // in order
+                st.s += S.sums[job.list >> 1][w].x;
+                st.t += S.sums[job.list >> 1][w].y;
+            }
+            const uint64_t* sorted = list;
+            if (!job.ordered) {
+                if (uint32_t(count) > n) {
+                    Keys keys;
+                    take_keys(keys, list, count);
+                    const uint64_t least = select_warp(keys, n, n, true, order_of(job.bar));
+                    Sums lost;
+                    count = split_keys<kEntropy>(keys, least, list, q, lost);
+                    move(st, key_value(least), q.c);
+                    move(lost, st.ref, q.c);
+                    st.s += lost.s;
+                    st.t += lost.t;
+                }
+                sort_keys(list, count, S.sorted);
+                sorted = S.sorted;
+            }
+            RowJob h;
+            h.token = job.token;
+            h.x_t = job.x_t;
+            h.c = job.c;
+            h.c_hi = job.c_hi;
+            h.c_lo = job.c_lo;
+            h.inv_t = job.inv_t;
+            h.inv_t_lo = job.inv_t_lo;
+            close_row<kEntropy>(P, sorted, count, st, h, job.row);
+        }
+        __syncwarp();
+        if (lane == 0) {
+            if (job.kind == kClose) mbar_arrive(&S.closed[job.list >> 1]);
+            mbar_arrive(&S.ended[slot]);
+        }
+    }
+}
+
+// Whether job j has ended; a whole warp. (Job -1 and before: there is none. The job that has its place after it must not
+// have been asked for.)
+__device__ __forceinline__ bool wait_job(int j, uint64_t ns)
+{
+    return j < 0 || wait(&shared().ended[j % kJobs], uint32_t(j / kJobs) & 1u, ns);
+}
+
+// Asks for job j; a whole warp, of which lane 0 has it. False where a wait gave up.
+__device__ __forceinline__ bool post_job(int j, const Job& job, uint64_t ns)
+{
+    Shared& S = shared();
+    const bool ok = wait_job(j - kJobs, ns);
+    if (ok && (threadIdx.x & 31) == 0) {
+        S.jobs[j % kJobs] = job;
+        mbar_arrive(&S.ready[j % kJobs]);
+    }
+    __syncwarp();
+    return ok;
+}
+
+// The last part of a row joins them all: its largest keys, in order, are then in list `at` + 1, and the others' sums
+// thread 0's, in S.state. How many keys; -1: a part has failed; -2: it has a NaN or +inf.
+template <bool kEntropy>
+__device__ __noinline__ int join_parts(const TopParams& P, int64_t r, uint32_t at, float c, float c_hi, float c_lo)
 {
     Shared& S = shared();
     const int tid = threadIdx.x, parts = P.parts;
     const uint32_t n = uint32_t(P.top.top_n);
-    RowJob h;
-    h.token = token;
-    row_scale(h, P.rows, temperature);
-    h.x_t = x_t;
-    if (tid < 2) S.count[tid] = 0;
+    const Scale q{c, c_hi, c_lo};
+    if (tid < 2) S.count[at + tid] = 0;
     if (tid < parts) {
         const volatile TopPart& from = P.ws.parts[r * parts + tid];
         S.part_ref[tid] = from.ref;
@@ -727,37 +934,42 @@ __device__ __noinline__ uint32_t join_parts(const TopParams& P, int64_t r, int32
     for (int p = 0; p < parts; ++p) {
         const uint32_t c = uint32_t(S.part_count[p]);
         if (uint32_t(tid) < c)
-            S.list[0][count + tid] = __ldcg(reinterpret_cast<const unsigned long long*>(P.ws.keys + (r * parts + p) * kMost + tid));
+            S.list[at][count + tid] = __ldcg(reinterpret_cast<const unsigned long long*>(P.ws.keys + (r * parts + p) * kMost + tid));
         count += c;
         flags |= S.part_flags[p];
         st.ref = fmaxf(st.ref, S.part_ref[p]);
     }
     for (int p = 0; p < parts; ++p) {
         Sums one{0.f, S.part_ref[p], S.part_s[p], S.part_t[p]};
-        move(one, st.ref, h.c);
+        move(one, st.ref, c);
         st.s += tid == 0 ? one.s : 0.f;
         st.t += tid == 0 ? one.t : 0.f;
     }
     bar_sync();
-    if (flags & 2) {
-        write_none(P, r, SAMPLER_ROW_TIMEOUT);
-        return turn + 1;
-    }
-    uint32_t at = 0;
+    if (flags) return flags & 2 ? -1 : -2;
     if (count > uint32_t(kConsumers)) {
         S.state[tid] = make_float4(st.bar, st.ref, st.s, st.t);
-        at = cut_long<kEntropy>(0, count, n, n, h.c, h.c_hi, h.c_lo);
-        const float4 q = S.state[tid];
-        st = Sums{q.x, q.y, q.z, q.w};
+        cut_long<kEntropy>(at, count, n, n, c, c_hi, c_lo);
+        const float4 in = S.state[tid];
+        st = Sums{in.x, in.y, in.z, in.w};
         count = n;
+        // (back into the list that the ranking reads)
+        const uint64_t k = uint32_t(tid) < count ? S.list[at + 1][tid] : 0;
+        bar_sync();
+        if (uint32_t(tid) < count) S.list[at][tid] = k;
+        bar_sync();
     }
-    return hand_over<kEntropy>(P, S.list[at], count, st, h, temperature, flags & 1, r, turn) ? turn + 1 : 0;
+    rank<kEntropy>(S.list[at], count, n, S.list[at + 1], st, q);
+    S.state[tid] = make_float4(st.bar, st.ref, st.s, st.t);
+    bar_sync();
+    return int(min(count, n));
 }
 
 template <typename T, bool kEntropy>
 __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant__ TopParams P)
 {
     constexpr int kPer = Elems<T>::kPer;
+    constexpr int kLag = 2;  // chunks that the closer has for a cut
     unsigned char* ring = ring_of();
     Shared& S = shared();
     const sampler_rows_t& a = P.rows;
@@ -768,10 +980,11 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
             mbar_init(&S.full[i], 1);
             mbar_init(&S.empty[i], kWarps);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kJobs; ++i) {
             mbar_init(&S.ready[i], 1);
-            mbar_init(&S.written[i], 1);
+            mbar_init(&S.ended[i], 1);
         }
+        for (int i = 0; i < 2; ++i) mbar_init(&S.closed[i], 1);
         queue_open(S.queue, kWarps);
         S.lost_most = 0;
         fence_mbar_init();
@@ -808,27 +1021,17 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
     }
 
     if (warp == kCloser) {
-        // (the consumers give up before it does, and say so)
-        for (uint32_t turn = 0;; ++turn) {
-            const uint32_t slot = turn & 1;
-            if (!wait(&S.ready[slot], turn >> 1 & 1, 8 * kWaitNs)) return;
-            const Close row = S.close[slot];
-            if (row.row < 0) return;
-            RowJob h;
-            h.token = row.token;
-            row_scale(h, a, row.temperature);
-            h.x_t = row.x_t;
-            close_row<kEntropy>(P, S.sorted[slot], row.count, Sums{0.f, row.ref, row.s, row.t}, h, row.row);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&S.written[slot]);
-        }
+        run_closer<kEntropy>(P);
+        return;
     }
 
     const uint32_t n = uint32_t(P.top.top_n);
     const uint32_t trigger = n + 64, about = n + n / 4 + 8;
     RingPlace slot{0, 0};
     QueuePlace place{{0, 0}, 0};
-    uint32_t turn = 0;  // rows that have gone to the closer
+    int job = 0;                    // jobs that the closer has been asked for
+    uint32_t pair = 0;              // of lists that the row has: 0 or 2
+    uint32_t rows_of[2] = {0, 0};   // rows that have gone to the closer with either pair
     int64_t done = 0;   // rows that this CTA has ended with
     bool failed = false;
     for (;; ++done) {
@@ -848,8 +1051,17 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
         Sums st{-pos_inf(), -kFloatMax, 0.f, 0.f};
         bool has_n = false;
         uint32_t worst = Peak<T>::none();  // NaN, or +inf, where the row has one
-        uint32_t at = 0, count = 0;  // the list that is filled, and, at the end, the keys in it
-        if (tid < 2) S.count[tid] = 0;
+        uint32_t at = pair, count = 0;  // the list that is filled, and the keys in it
+        uint32_t kept = 0;              // keys that the list had before the present counter of S.pushed was begun
+        int cutting = -1, age = 0;      // the job that cuts the other one, which was filled before, and the chunks since
+        const Job job_of_row{kClose, 0, 0, 0, row.row, row.token, 0.f, 0.f, h.c, h.c_hi, h.c_lo, h.inv_t, h.inv_t_lo, h.x_t};
+        // the row's lists are the ones of two rows ago
+        const uint32_t gone = pair ? rows_of[1] : rows_of[0];
+        failed = bar_any(gone != 0 && !wait(&S.closed[pair >> 1], (gone - 1) & 1u, P.wait_ns));
+        if (failed) break;
+        if (tid < 2) S.count[pair + tid] = 0;
+        if (tid < 4) S.pushed[tid] = 0;
+        uint32_t counter = 0;
         bar_sync();
         for (int base = first; base < last; base += kChunkVecs) {
             const bool ok = wait(&S.full[slot.at], slot.phase, P.wait_ns);
@@ -902,43 +1114,115 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
 #pragma unroll
             for (int k = 0; k < kVecs; ++k)
                 if (Peak<T>::above(peaks[k], bar)) above |= take_above<T>(v[k], bar) << k * kPer;
-            while (above) {
+            uint32_t to = kCap;
+            if (above) {
+                const uint32_t want = uint32_t(__popc(above));
+                to = kept + next_places(&S.pushed[counter], want);
+                top = to + want;
+            }
+            add<T, kEntropy>(st, v, two(h.c, h.c));
+            for (; above && to < kCap; ++to, above &= above - 1) {
                 const int bit = __ffs(above) - 1, i = bit / kPer * kConsumers + tid, j = bit % kPer;
-                above &= above - 1;
-                const uint32_t to = next_place(&S.count[at]);
-                top = to + 1;
-                if (to < kCap)
-                    S.list[at][to] = key_of(load_logit(reinterpret_cast<const T*>(ring + chunk.at) + i * kPer + j),
-                                            (base + i) * kPer - span.head + j);
+                S.list[at][to] = key_of(load_logit(reinterpret_cast<const T*>(ring + chunk.at) + i * kPer + j),
+                                        (base + i) * kPer - span.head + j);
             }
             __syncwarp();
-            add<T, kEntropy>(st, v, two(h.c, h.c));
-            const bool any = bar_any(top >= (first_bar ? about : trigger) || !ok), end = base + kChunkVecs >= last;
-            if (any && bar_any(!ok)) {
+            const bool end = base + kChunkVecs >= last;
+            const bool joins = cutting >= 0 && (++age == kLag || end);  // what the closer has cut is wanted now
+            bool cut_ended = !joins || wait_job(cutting, P.wait_ns);
+            const bool any = bar_any(top >= (first_bar ? about : trigger) || !ok || !cut_ended);
+            if (any && bar_any(!ok || !cut_ended)) {
                 failed = true;
                 break;
             }
-            if (any || end) {
-                count = S.count[at];
-                if (count > uint32_t(kConsumers)) {
-                    const bool over = count > uint32_t(kCap);
-                    S.state[tid] = make_float4(st.bar, st.ref, over ? s_before : st.s, over ? t_before : st.t);
-                    at = over ? slow_chunk<T, kEntropy>(at, chunk.at, base, last, chunk.head, chunk.end, n, h.c, h.c_hi, h.c_lo)
+            if (any || end || joins) {
+                // (Nobody waits for anybody here, but where a function out of line or the closer takes over: counters are
+                // used in turn, and the one after the next is cleared.)
+                count = kept + S.pushed[counter];
+                bool over = count > uint32_t(kCap);
+                float bar_before = st.bar;  // of this chunk, should it be looked at again
+                // (with what the closer leaves, 256 at most, the other list's keys of the chunks before have to fit)
+                if (cutting >= 0 && (joins || count > uint32_t(kCap - kConsumers))) {
+                    if (!joins) {  // the cut is wanted early
+                        cut_ended = wait_job(cutting, P.wait_ns);
+                        failed = bar_any(!cut_ended);
+                        if (failed) break;
+                    }
+                    // what has been cut meanwhile, and, after it, what the chunks since have put into the other list
+                    const uint32_t left = S.cut_count, full = at ^ 1;
+                    const uint64_t least = S.cut_least;
+                    over |= left + count > uint32_t(kCap);
+                    if (over) {
+                        // this chunk's are taken again
+                        const int before = base * kPer - span.head;
+                        const uint32_t valid = min(count, uint32_t(kCap));
+                        if (tid == 0) S.count[full] = left;
+                        bar_sync();
+#pragma unroll 1
+                        for (uint32_t i0 = 0; i0 < valid; i0 += kConsumers) {
+                            const uint64_t k = i0 + tid < valid ? S.list[at][i0 + tid] : 0;
+                            const bool stays = k != 0 && key_token(k) < before;
+                            const uint32_t place = places(&S.count[full], stays);
+                            if (stays && place < kCap) S.list[full][place] = k;
+                        }
+                        bar_sync();
+                        count = min(S.count[full], uint32_t(kCap));
+                        st.s = s_before;
+                        st.t = t_before;
+                    } else {
+                        for (uint32_t i = tid; i < count; i += kConsumers) S.list[full][left + i] = S.list[at][i];
+                        count += left;
+                    }
+                    move(st, key_value(least), h.c);
+                    if (tid == 0) {
+                        Sums lost{0.f, S.cut_ref, S.cut_s, S.cut_t};
+                        move(lost, st.ref, h.c);
+                        st.s += lost.s;
+                        st.t += lost.t;
+                    }
+                    cutting = -1;
+                    at = full;
+                    bar_before = st.ref;
+                } else if (over) {  // (no cut is under way)
+                    st.s = s_before;
+                    st.t = t_before;
+                }
+                if (cutting >= 0) {
+                    kept = count;
+                } else if (over || count > uint32_t(kConsumers)) {
+                    if (tid == 0) S.count[at ^ 1] = 0;
+                    S.state[tid] = make_float4(bar_before, st.ref, st.s, st.t);
+                    bar_sync();
+                    at = over ? slow_chunk<T, kEntropy>(at, min(count, uint32_t(kCap)), chunk.at, base, last, chunk.head, chunk.end, n,
+                                                        h.c, h.c_hi, h.c_lo)
                               : cut_long<kEntropy>(at, count, n, about, h.c, h.c_hi, h.c_lo);
                     const float4 q = S.state[tid];
                     st = Sums{q.x, q.y, q.z, q.w};
                     count = S.count[at];
                     has_n = true;
-                } else if (any && !end) {
-                    rank<kEntropy>(S.list[at], count, n, S.list[at ^ 1], st, scale);
-                    if (tid == 0) {
-                        S.count[at] = 0;
-                        S.count[at ^ 1] = min(count, n);
+                    kept = count;
+                } else if (!end && count > (first_bar ? about : trigger - 1)) {
+                    // the closer cuts it, while the next chunks go into the other one
+                    has_n = true;
+                    cutting = job++;
+                    age = 0;
+                    bar_sync();
+                    if (warp == 0) {
+                        Job j = job_of_row;
+                        j.kind = kCut;
+                        j.list = int(at);
+                        j.count = int(count);
+                        j.bar = bar_before;
+                        post_job(cutting, j, P.wait_ns);  // (where that gives up, the wait for its end does)
                     }
                     at ^= 1;
-                    has_n |= count >= n;
+                    kept = 0;
+                } else {
+                    kept = count;
                 }
-                bar_sync();
+                counter = (counter + 1) & 3;
+                if (tid == 0) S.pushed[(counter + 1) & 3] = 0;
+                if (end) bar_sync();
             }
             if (has_n) st.bar = st.ref;  // later tokens lose ties
             if (lane == 0) mbar_arrive(&S.empty[slot.at]);
@@ -946,50 +1230,82 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
         }
         if (failed) break;
         const bool bad = bar_any(!(Peak<T>::value(worst) < pos_inf()));
-        if (P.parts == 1) {
-            failed = !hand_over<kEntropy>(P, S.list[at], count, st, h, row.temperature, bad, r, turn);
-            if (failed) break;
+        int status = h.bad_param ? SAMPLER_ROW_BAD_PARAM : bad ? SAMPLER_ROW_NONFINITE : SAMPLER_ROW_OK;
+        bool ordered = false;
+        if (P.parts > 1) {
+            // this part's n largest keys and sums go into the workspace, for the part of the row that ends last
+            rank<kEntropy>(S.list[at], count, n, S.list[at ^ 1], st, scale);
+            count = min(count, n);
+            float s = st.s, t = st.t;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+                if (kEntropy) t += __shfl_xor_sync(0xffffffffu, t, o);
+            }
+            if (lane == 0) S.sums[pair >> 1][warp] = make_float2(s, t);
+            if (uint32_t(tid) < count)
+                __stcg(reinterpret_cast<unsigned long long*>(P.ws.keys + (r * P.parts + part) * kMost + tid), S.list[at ^ 1][tid]);
+            bar_sync();
+            s = t = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                s += S.sums[pair >> 1][w].x;
+                t += S.sums[pair >> 1][w].y;
+            }
+            if (!leave(P, r, part, TopPart{st.ref, s, t, int(count), bad, 0})) continue;
+            const int joined = join_parts<kEntropy>(P, r, pair, h.c, h.c_hi, h.c_lo);
+            const float4 q = S.state[tid];
+            st = Sums{q.x, q.y, q.z, q.w};
+            count = uint32_t(max(joined, 0));
+            at = pair + 1;
+            ordered = true;
+            if (status == SAMPLER_ROW_OK && joined < 0) status = joined == -1 ? SAMPLER_ROW_TIMEOUT : SAMPLER_ROW_NONFINITE;
+            if (joined == -1) status = SAMPLER_ROW_TIMEOUT;
+        }
+        if (status == SAMPLER_ROW_OK && count == 0) status = SAMPLER_ROW_ALL_NEG_INF;
+        if (status != SAMPLER_ROW_OK) {
+            write_none(P, r, status);
+            bar_sync();
             continue;
         }
-        // this part's n largest keys and sums go into the workspace, for the part of the row that ends last
-        rank<kEntropy>(S.list[at], count, n, S.list[at ^ 1], st, scale);
-        count = min(count, n);
+        // the rest of the row's work is the closer's
         float s = st.s, t = st.t;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             s += __shfl_xor_sync(0xffffffffu, s, o);
             if (kEntropy) t += __shfl_xor_sync(0xffffffffu, t, o);
         }
-        if (lane == 0) S.sums[warp] = make_float2(s, t);
-        if (uint32_t(tid) < count)
-            __stcg(reinterpret_cast<unsigned long long*>(P.ws.keys + (r * P.parts + part) * kMost + tid), S.list[at ^ 1][tid]);
+        if (lane == 0) S.sums[pair >> 1][warp] = make_float2(s, t);
         bar_sync();
-        s = t = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            s += S.sums[w].x;
-            t += S.sums[w].y;
+        const int closing = job++;
+        if (pair)
+            ++rows_of[1];
+        else
+            ++rows_of[0];
+        pair ^= 2;
+        bool posted = true;
+        if (warp == 0) {
+            Job j = job_of_row;
+            j.list = int(at);
+            j.count = int(count);
+            j.ordered = ordered;
+            j.ref = st.ref;
+            j.bar = st.bar;
+            posted = post_job(closing, j, P.wait_ns);
         }
-        if (leave(P, r, part, TopPart{st.ref, s, t, int(count), bad, 0})) {
-            // (0: a wait gave up; a row with a status does not go to the closer)
-            const uint32_t to = join_parts<kEntropy>(P, r, row.token, row.temperature, row.x_t, turn);
-            if (to == 0) {
+        failed = bar_any(!posted);
+        if (failed) {
+            if (P.parts > 1) {  // the row's parts have all been counted
                 write_none(P, r, SAMPLER_ROW_TIMEOUT);
-                failed = true;
                 ++done;
-                break;
             }
-            turn = to - 1;
+            break;
         }
-        bar_sync();
     }
-    if (warp == 0) {  // the closer's last
-        const uint32_t to = turn & 1;
-        if (wait(&S.written[to], (turn >> 1 & 1) ^ 1u, kWaitNs) && lane == 0) {
-            S.close[to].row = -1;
-            mbar_arrive(&S.ready[to]);
-        }
-        __syncwarp();
+    if (warp == 0) {
+        Job j;
+        j.kind = kEnd;
+        post_job(job, j, kWaitNs);
     }
     if (!failed) return;
 

@@ -41,11 +41,13 @@ constexpr int kThreads = kConsumers + 64;
 constexpr int kVecs = 4;                        // of a chunk in each consumer
 constexpr int kChunkVecs = kConsumers * kVecs;
 constexpr int kChunkBytes = kChunkVecs * 16;
-constexpr int kSlots = 4;
+constexpr int kSlots = 5;
+constexpr int kLook = 4;                         // chunks that are looked at for a row's first bar
 constexpr int kJobs = 4;                         // of the closer
 constexpr int kLane = 8;                         // keys of a list in each of its lanes, at most
+constexpr int kClosable = 32 * kLane;            // keys of a list that it takes
 constexpr int kMost = SAMPLER_MAX_ALTERNATIVES;
-constexpr int kCap = 1024;                      // keys in a list
+constexpr int kCap = 512;                       // keys in a list
 constexpr int kMaxToken = 262143;
 constexpr int kMaxTopParts = 32;                // of a row: the lanes of a warp
 constexpr float kLostUnit = 1099511627776.f;    // 2^40
@@ -1026,7 +1028,7 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
     }
 
     const uint32_t n = uint32_t(P.top.top_n);
-    const uint32_t trigger = n + 64, about = n + n / 4 + 8;
+    const uint32_t trigger = min(n + 96, 208u), about = n + n / 4 + 8;
     RingPlace slot{0, 0};
     QueuePlace place{{0, 0}, 0};
     int job = 0;                    // jobs that the closer has been asked for
@@ -1062,7 +1064,54 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
         if (tid < 2) S.count[pair + tid] = 0;
         if (tid < 4) S.pushed[tid] = 0;
         uint32_t counter = 0;
-        bar_sync();
+        // The first bar: of the first chunks' largest in each thread, the n-th, rounded down to bf16 (two to an instruction,
+        // whose counts are exact in bf16 up to 256); where fewer threads have any, all are taken. (Of the first chunk
+        // alone: four times as many keys of the first quarter of a row, which cost more than this second look.)
+        const int looked = min(last, first + kLook * kChunkVecs);
+        {
+            uint32_t peaks = Peak<T>::none();
+            RingPlace ahead = slot;
+            bool ok = true;
+            for (int base = first; base < looked; base += kChunkVecs) {
+                ok = ok && wait(&S.full[ahead.at], ahead.phase, P.wait_ns);
+                uint4 v[kVecs];
+                load<T>(v, Chunk{int(ahead.at) * kChunkBytes, base, ok ? last : 0, span.head, span.head + int(a.vocab)});
+#pragma unroll
+                for (int k = 0; k < kVecs; ++k) peaks = Peak<T>::join(peaks, peak<T>(v[k]));
+                ahead.next(kSlots);
+            }
+            const float most = Peak<T>::value(peaks);
+            const uint32_t mine = packed_bar<uint16_t>(most);
+            S.largest[tid] = uint16_t(mine);
+            failed = bar_any(!ok);
+            if (failed) break;
+            uint32_t n0 = 0, n1 = 0;
+            const uint4* all = reinterpret_cast<const uint4*>(S.largest);
+#pragma unroll 8
+            for (int j = 0; j < kConsumers / 8; ++j) {
+                const uint4 o = all[j];
+                count_above(n0, o.x, mine);
+                count_above(n1, o.y, mine);
+                count_above(n0, o.z, mine);
+                count_above(n1, o.w, mine);
+            }
+            const float above = __uint_as_float(n0 << 16) + __uint_as_float(n0 & 0xffff0000u) + __uint_as_float(n1 << 16) +
+                                __uint_as_float(n1 & 0xffff0000u);
+            // (of equal ones all have the first's place: the least of those that come before the n-th or on it)
+            const bool within = above < float(n);
+            const uint32_t least = __reduce_min_sync(0xffffffffu, within ? order_of(__uint_as_float(mine << 16)) : 0xffffffffu);
+            if (lane == 0) S.tops[warp] = least;
+            has_n = bar_count(within && most >= -kFloatMax) >= n;
+            if (has_n) {
+                uint32_t lo = 0xffffffffu;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) lo = min(lo, S.tops[w]);
+                lo = max(lo, order_of(-kFloatMax));
+                st.ref = value_of(lo);
+                st.bar = below(lo);
+            }
+        }
+        bool loose = has_n;  // n of the looked at tokens, not of those that are in the list, are at the bar or above
         for (int base = first; base < last; base += kChunkVecs) {
             const bool ok = wait(&S.full[slot.at], slot.phase, P.wait_ns);
             const Chunk chunk{int(slot.at) * kChunkBytes, base, ok ? last : 0, span.head, span.head + int(a.vocab)};
@@ -1071,44 +1120,8 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
             uint32_t peaks[kVecs];
 #pragma unroll
             for (int k = 0; k < kVecs; ++k) peaks[k] = peak<T>(v[k]);
-            const uint32_t four = Peak<T>::join(Peak<T>::join(peaks[0], peaks[1]), Peak<T>::join(peaks[2], peaks[3]));
-            worst = Peak<T>::join(worst, four);
-            bool first_bar = false;
-            if (!has_n) {
-                // The n-th of the threads' largest, rounded down to bf16 (two to an instruction, whose counts are exact in
-                // bf16 up to 256); where fewer threads have any, all are taken.
-                const float most = Peak<T>::value(four);
-                const uint32_t mine = packed_bar<uint16_t>(most);
-                S.largest[tid] = uint16_t(mine);
-                bar_sync();
-                uint32_t n0 = 0, n1 = 0;
-                const uint4* all = reinterpret_cast<const uint4*>(S.largest);
-#pragma unroll 8
-                for (int j = 0; j < kConsumers / 8; ++j) {
-                    const uint4 o = all[j];
-                    count_above(n0, o.x, mine);
-                    count_above(n1, o.y, mine);
-                    count_above(n0, o.z, mine);
-                    count_above(n1, o.w, mine);
-                }
-                const float above = __uint_as_float(n0 << 16) + __uint_as_float(n0 & 0xffff0000u) + __uint_as_float(n1 << 16) +
-                                    __uint_as_float(n1 & 0xffff0000u);
-                // (of equal ones all have the first's place: the least of those that come before the n-th or on it)
-                const bool within = above < float(n);
-                const uint32_t order = order_of(__uint_as_float(mine << 16));
-                const uint32_t least = __reduce_min_sync(0xffffffffu, within ? order : 0xffffffffu);
-                if (lane == 0) S.tops[warp] = least;
-                first_bar = has_n = bar_count(within && most >= -kFloatMax) >= n;
-                if (has_n) {
-                    uint32_t lo = 0xffffffffu;
-#pragma unroll
-                    for (int w = 0; w < kWarps; ++w) lo = min(lo, S.tops[w]);
-                    lo = max(lo, order_of(-kFloatMax));
-                    move(st, value_of(lo), h.c);
-                    st.bar = below(lo);
-                }
-            }
-            const float s_before = st.s, t_before = st.t;
+            worst = Peak<T>::join(worst, Peak<T>::join(Peak<T>::join(peaks[0], peaks[1]), Peak<T>::join(peaks[2], peaks[3])));
+            const float s_before = st.s, t_before = st.t, ref_before = st.ref;
             uint32_t top = 0, above = 0;
             const uint32_t bar = packed_bar<T>(st.bar);
 #pragma unroll
@@ -1130,7 +1143,7 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
             const bool end = base + kChunkVecs >= last;
             const bool joins = cutting >= 0 && (++age == kLag || end);  // what the closer has cut is wanted now
             bool cut_ended = !joins || wait_job(cutting, P.wait_ns);
-            const bool any = bar_any(top >= (first_bar ? about : trigger) || !ok || !cut_ended);
+            const bool any = bar_any(top >= trigger || !ok || !cut_ended);
             if (any && bar_any(!ok || !cut_ended)) {
                 failed = true;
                 break;
@@ -1142,7 +1155,7 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
                 bool over = count > uint32_t(kCap);
                 float bar_before = st.bar;  // of this chunk, should it be looked at again
                 // (with what the closer leaves, 256 at most, the other list's keys of the chunks before have to fit)
-                if (cutting >= 0 && (joins || count > uint32_t(kCap - kConsumers))) {
+                if (cutting >= 0 && (joins || count > uint32_t(kCap - kClosable))) {
                     if (!joins) {  // the cut is wanted early
                         cut_ended = wait_job(cutting, P.wait_ns);
                         failed = bar_any(!cut_ended);
@@ -1189,7 +1202,7 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
                 }
                 if (cutting >= 0) {
                     kept = count;
-                } else if (over || count > uint32_t(kConsumers)) {
+                } else if (over || count > uint32_t(kClosable)) {
                     if (tid == 0) S.count[at ^ 1] = 0;
                     S.state[tid] = make_float4(bar_before, st.ref, st.s, st.t);
                     bar_sync();
@@ -1201,7 +1214,7 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
                     count = S.count[at];
                     has_n = true;
                     kept = count;
-                } else if (!end && count > (first_bar ? about : trigger - 1)) {
+                } else if (!end && count >= trigger) {
                     // the closer cuts it, while the next chunks go into the other one
                     has_n = true;
                     cutting = job++;
@@ -1224,7 +1237,8 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
                 if (tid == 0) S.pushed[(counter + 1) & 3] = 0;
                 if (end) bar_sync();
             }
-            if (has_n) st.bar = st.ref;  // later tokens lose ties
+            loose = loose && st.ref == ref_before && base + kChunkVecs < looked;
+            if (has_n && !loose) st.bar = st.ref;  // later tokens lose ties
             if (lane == 0) mbar_arrive(&S.empty[slot.at]);
             slot.next(kSlots);
         }

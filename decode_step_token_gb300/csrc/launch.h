@@ -218,7 +218,7 @@ int scaled_head_launch(const sampler_scaled_head_t& g, void* logits, int dtype, 
                        ScaledHeadGrants* grants, cudaStream_t stream);
 
 // ---------------------------------------------------------------- 4-bit LM head
-int micro_quantize_launch(const sampler_micro_t& q, cudaStream_t stream);
+int micro_quantize_launch(const sampler_micro_t& q, int sms, cudaStream_t stream);
 int micro_rows_launch(const sampler_micro_rows_t& q, cudaStream_t stream);
 
 // Whether a handle has granted the head's kernels their shared memory, by block size,

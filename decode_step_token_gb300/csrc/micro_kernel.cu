@@ -26,6 +26,7 @@ namespace micro {
 
 constexpr int kThreads = 256;
 constexpr int kPer = 16;                     // values of a thread
+constexpr int kVectors = 4;                  // of a thread of the rows read back
 constexpr float kLeast = 7.888609052e-31f;   // 2^-100: keeps a row's scale and its quotients normal
 constexpr uint32_t kInf = 0x7f800000u;
 
@@ -38,9 +39,12 @@ __device__ __forceinline__ int least_power(uint32_t m, uint32_t f)
     return int(m >> 23) - 127 + ((m & 0x7fffffu) > f ? 1 : 0);
 }
 
-// Eight values to eight codes, the first in the lowest four bits; ties to even, beyond 6 to 6.
-__device__ __forceinline__ uint32_t codes8(const float* x)
+// Eight values (four pairs) to eight codes, the first in the lowest four bits; ties to even, beyond 6 to 6.
+__device__ __forceinline__ uint32_t codes8(const unsigned long long* q)
 {
+    float x[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) asm("mov.b64 {%0, %1}, %2;" : "=f"(x[2 * j]), "=f"(x[2 * j + 1]) : "l"(q[j]));
     uint32_t r;
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
@@ -78,54 +82,80 @@ __device__ __forceinline__ float scale_value(uint32_t code)
     return code == 0u ? __int_as_float(0x00400000) : __int_as_float(code << 23);
 }
 
+// 16 values of a row as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load16(float (&x)[kPer], const T* p, int count, bool vec);
+struct Raw {
+    static constexpr int kWords = int(sizeof(T)) * kPer / 4;
+    uint32_t w[kWords];
+};
 
-template <>
-__device__ __forceinline__ void load16<float>(float (&x)[kPer], const float* p, int count, bool vec)
+template <typename T>
+__device__ __forceinline__ void load16(Raw<T>& x, const T* p, int count, bool vec)
 {
     if (vec && count == kPer) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p) + j);
-            x[4 * j] = v.x;
-            x[4 * j + 1] = v.y;
-            x[4 * j + 2] = v.z;
-            x[4 * j + 3] = v.w;
+        for (int j = 0; j < Raw<T>::kWords / 4; ++j) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + j);
+            x.w[4 * j] = v.x;
+            x.w[4 * j + 1] = v.y;
+            x.w[4 * j + 2] = v.z;
+            x.w[4 * j + 3] = v.w;
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) x[j] = j < count ? p[j] : 0.f;
-    }
-}
-
-template <>
-__device__ __forceinline__ void load16<uint16_t>(float (&x)[kPer], const uint16_t* p, int count, bool vec)
-{
-    if (vec && count == kPer) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + j);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[8 * j + 2 * k] = __uint_as_float(w[k] << 16);
-                x[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        for (int j = 0; j < Raw<T>::kWords; ++j) {
+            if (sizeof(T) == 4) {
+                x.w[j] = j < count ? reinterpret_cast<const uint32_t*>(p)[j] : 0u;
+            } else {
+                const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+                x.w[j] = (2 * j < count ? uint32_t(h[2 * j]) : 0u) | (2 * j + 1 < count ? uint32_t(h[2 * j + 1]) << 16 : 0u);
             }
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) x[j] = j < count ? __uint_as_float(uint32_t(p[j]) << 16) : 0.f;
     }
 }
 
-// The largest magnitude of 16 values as bits: kInf or more where one is not finite.
-__device__ __forceinline__ uint32_t largest(const float (&x)[kPer])
+// Two neighbouring values as a pair of fp32.
+using Two = unsigned long long;
+
+__device__ __forceinline__ Two two(uint32_t a, uint32_t b)
+{
+    Two y;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "r"(a), "r"(b));
+    return y;
+}
+
+__device__ __forceinline__ Two pair_at(const Raw<float>& x, int j) { return two(x.w[2 * j], x.w[2 * j + 1]); }
+__device__ __forceinline__ Two pair_at(const Raw<uint16_t>& x, int j) { return two(x.w[j] << 16, x.w[j] & 0xffff0000u); }
+
+__device__ __forceinline__ Two times(Two a, Two b)
+{
+    Two y;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(y) : "l"(a), "l"(b));
+    return y;
+}
+
+__device__ __forceinline__ Two times_add(Two a, Two b, Two c)
+{
+    Two y;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(y) : "l"(a), "l"(b), "l"(c));
+    return y;
+}
+
+// The largest magnitude of 16 values as fp32 bits: kInf or more where one is not finite.
+__device__ __forceinline__ uint32_t largest(const Raw<float>& x)
 {
     uint32_t m = 0u;
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) m = max(m, __float_as_uint(x[j]) & 0x7fffffffu);
+    for (int j = 0; j < 16; ++j) m = max(m, x.w[j] & 0x7fffffffu);
     return m;
+}
+
+__device__ __forceinline__ uint32_t largest(const Raw<uint16_t>& x)
+{
+    uint32_t m = x.w[0] & 0x7fff7fffu;
+#pragma unroll
+    for (int j = 1; j < 8; ++j) asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(x.w[j] & 0x7fff7fffu));
+    return max(m & 0xffff0000u, m << 16);
 }
 
 // What a call's shape makes of it. group: threads to a row.
@@ -137,31 +167,32 @@ struct Plan {
 
 // The codes of one chunk and its block's scale code, given the block's largest magnitude and (blocks of 16) the row's
 // scale 2^g.
-template <int kBlock>
-__device__ __forceinline__ uint2 encode(const float (&x)[kPer], uint32_t most, int g, uint32_t& code)
+template <typename T, int kBlock>
+__device__ __forceinline__ uint2 encode(const Raw<T>& x, uint32_t most, int g, uint32_t& code)
 {
-    float q[kPer];
+    Two q[kPer / 2];
     const bool finite = most < kInf;
     if (kBlock == 32) {
         const int e = max(least_power(most, 0x400000u) - 2, -127);  // m <= 1.5 * 4 * 2^e
         code = finite ? uint32_t(e + 127) : 0xffu;
-        const float up = power(-max(min(e, 126), -127));  // its reciprocal: a product with it is exact
+        const uint32_t up = __float_as_uint(power(-max(min(e, 126), -127)));  // its reciprocal: a product with it is exact
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) q[j] = x[j] * up;
+        for (int j = 0; j < kPer / 2; ++j) q[j] = times(pair_at(x, j), two(up, up));
     } else {
         code = finite ? e4m3_code(__fdiv_rn(__uint_as_float(most), 6.f) * power(-g)) : 0x7fu;
         const float unit = (finite ? e4m3_value(code) : 0.f) * power(g);
-        const float inv = unit > 0.f ? __fdiv_rn(1.f, unit) : 0.f;
+        const uint32_t i = __float_as_uint(unit > 0.f ? __fdiv_rn(1.f, unit) : 0.f), u = __float_as_uint(-unit);
+        const Two inv = two(i, i), less = two(u, u);
         // the quotient, correctly rounded: the product with the rounded reciprocal and one step on its remainder
         // (Markstein)
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-            const float y = x[j] * inv;
-            q[j] = fmaf(fmaf(-y, unit, x[j]), inv, y);
+        for (int j = 0; j < kPer / 2; ++j) {
+            const Two v = pair_at(x, j), y = times(v, inv);
+            q[j] = times_add(times_add(y, less, v), inv, y);
         }
     }
     const uint32_t keep = finite ? 0xffffffffu : 0u;
-    return make_uint2(codes8(q) & keep, codes8(q + 8) & keep);
+    return make_uint2(codes8(q) & keep, codes8(q + 4) & keep);
 }
 
 // Store a chunk's codes: 8 bytes where they lie so, else the `bytes` that belong to the row.
@@ -182,91 +213,111 @@ __device__ __forceinline__ int64_t scale_word(int64_t row, int tile, int tiles)
     return (row / 128 * tiles + tile) * 128 + (row % 32) * 4 + row / 32 % 4;
 }
 
-// kChunks: of a thread, in registers; 0: any number, read twice where blocks are of 16.
-template <typename T, int kBlock, int kChunks>
+// kChunks: of a row in a thread, in registers; 0: any number, read twice where blocks are of 16. kRows: that a group of
+// threads has in hand.
+template <typename T, int kBlock, int kChunks, int kRows>
 __global__ void __launch_bounds__(kThreads) quantize_kernel(const sampler_micro_t q, const Plan plan)
 {
     constexpr int kHeld = kChunks ? kChunks : 1;
     constexpr int kOfTile = 4 * kBlock / kPer;  // chunks that one word of scales belongs to
-    const int group = plan.group, t = threadIdx.x & (group - 1);
-    const int64_t row = int64_t(blockIdx.x) * (kThreads / group) + threadIdx.x / group;
-    const bool in = row < q.rows;
-    const T* src = static_cast<const T*>(q.src) + (in ? row * q.src_stride : 0);
+    const int group = plan.group, t = threadIdx.x & (group - 1), groups = kThreads / group;
+    const int64_t row0 = int64_t(blockIdx.x) * (groups * kRows) + threadIdx.x / group;  // rows of a group: `groups` apart
     uint32_t* words = static_cast<uint32_t*>(q.scales);
-    float x[kHeld][kPer];
-    auto load = [&](int k, int chunk) {
-        const int64_t left = in ? q.cols - int64_t(chunk) * kPer : 0;
-        load16<T>(x[k], src + int64_t(chunk) * kPer, int(max(int64_t(0), min(int64_t(kPer), left))), plan.vec_in);
+    Raw<T> x[kRows][kHeld];
+    auto load = [&](int r, int k, int chunk) {
+        const int64_t row = row0 + r * groups, left = row < q.rows ? q.cols - int64_t(chunk) * kPer : 0;
+        const T* src = static_cast<const T*>(q.src) + (row < q.rows ? row * q.src_stride : 0) + int64_t(chunk) * kPer;
+        load16<T>(x[r][k], src, int(max(int64_t(0), min(int64_t(kPer), left))), plan.vec_in);
     };
-    int g = 0;
-    uint32_t most[kHeld];
+    int g[kRows] = {};
+    uint32_t most[kRows][kHeld];
     if (kChunks) {
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) load(k, t + k * group);
+        for (int r = 0; r < kRows; ++r)
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) {
-            most[k] = largest(x[k]);
-            if (kBlock == 32) most[k] = max(most[k], __shfl_xor_sync(0xffffffffu, most[k], 1));
-        }
+            for (int k = 0; k < kHeld; ++k) load(r, k, t + k * group);
+#pragma unroll
+        for (int r = 0; r < kRows; ++r)
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) {
+                most[r][k] = largest(x[r][k]);
+                if (kBlock == 32) most[r][k] = max(most[r][k], __shfl_xor_sync(0xffffffffu, most[r][k], 1));
+            }
     }
     if (kBlock == 16) {
-        // the row's largest, of its blocks without a NaN or an infinity
-        __shared__ uint32_t part[kThreads / 32];
-        uint32_t m = __float_as_uint(kLeast);
-        if (kChunks) {
+        // each row's largest, of its blocks without a NaN or an infinity
+        __shared__ uint32_t part[kRows][kThreads / 32];
+        uint32_t m[kRows];
 #pragma unroll
-            for (int k = 0; k < kHeld; ++k) m = max(m, most[k] < kInf ? most[k] : 0u);
-        } else {
-            for (int chunk = t; chunk < plan.chunks; chunk += group) {
-                load(0, chunk);
-                const uint32_t n = largest(x[0]);
-                m = max(m, n < kInf ? n : 0u);
+        for (int r = 0; r < kRows; ++r) {
+            m[r] = __float_as_uint(kLeast);
+            if (kChunks) {
+#pragma unroll
+                for (int k = 0; k < kHeld; ++k) m[r] = max(m[r], most[r][k] < kInf ? most[r][k] : 0u);
+            } else {
+                for (int chunk = t; chunk < plan.chunks; chunk += group) {
+                    load(r, 0, chunk);
+                    const uint32_t n = largest(x[r][0]);
+                    m[r] = max(m[r], n < kInf ? n : 0u);
+                }
             }
+            if (group >= 32)
+                m[r] = __reduce_max_sync(0xffffffffu, m[r]);
+            else
+                for (int o = group / 2; o > 0; o >>= 1) m[r] = max(m[r], __shfl_xor_sync(0xffffffffu, m[r], o));
         }
-        for (int o = min(group, 32) / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
         if (group > 32) {
-            if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+            if ((threadIdx.x & 31) == 0)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) part[r][threadIdx.x >> 5] = m[r];
             __syncthreads();
             const int first = threadIdx.x / group * (group / 32);
-            for (int w = 0; w < group / 32; ++w) m = max(m, part[first + w]);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+                for (int w = 0; w < group / 32; ++w) m[r] = max(m[r], part[r][first + w]);
         }
-        g = least_power(m, 0x280000u) - 11;  // m <= 448 * 6 * 2^g = 1.3125 * 2^11 * 2^g
-        if (in && t == 0) q.row_scale[row] = power(g);
-    } else if (in && t == 0) {
-        q.row_scale[row] = 1.f;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) g[r] = least_power(m[r], 0x280000u) - 11;  // m <= 448 * 6 * 2^g = 1.3125 * 2^11 * 2^g
     }
-    auto finish = [&](int k, int chunk, uint32_t m) {
-        uint32_t code;
-        const uint2 c = encode<kBlock>(x[k], m, g, code);
-        const bool there = in && chunk < plan.chunks;
-        if (there) {
-            const int64_t bytes = (q.cols + 1) / 2 - int64_t(chunk) * 8;
-            put_codes(static_cast<uint8_t*>(q.values) + row * q.values_stride + int64_t(chunk) * 8, c,
-                      int(min(int64_t(8), bytes)), plan.vec_out);
-        }
-        // the word of a row's four blocks, from the threads that have them; scales that belong to no block are 0
-        uint32_t w = there ? code << 8 * (chunk * kPer / kBlock & 3) : 0u;
 #pragma unroll
-        for (int o = kOfTile / 2; o > 0; o >>= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
-        const int tile = chunk / kOfTile;
-        if (t % kOfTile == 0 && tile < plan.tiles && row < plan.padded) words[scale_word(row, tile, plan.tiles)] = w;
-    };
-    if (kChunks) {
+    for (int r = 0; r < kRows; ++r) {
+        const int64_t row = row0 + r * groups;
+        const bool in = row < q.rows;
+        if (in && t == 0) q.row_scale[row] = kBlock == 16 ? power(g[r]) : 1.f;
+        uint8_t* values = static_cast<uint8_t*>(q.values) + (in ? row * q.values_stride : 0);
+        uint32_t* to = words + scale_word(row, 0, plan.tiles);
+        auto finish = [&](int k, int chunk, uint32_t m) {
+            uint32_t code;
+            const uint2 c = encode<T, kBlock>(x[r][k], m, g[r], code);
+            const bool there = in && chunk < plan.chunks;
+            if (there) {
+                const int64_t bytes = (q.cols + 1) / 2 - int64_t(chunk) * 8;
+                put_codes(values + int64_t(chunk) * 8, c, int(min(int64_t(8), bytes)), plan.vec_out);
+            }
+            // the word of a row's four blocks, from the threads that have them; scales that belong to no block are 0
+            uint32_t w = there ? code << 8 * (chunk * kPer / kBlock & 3) : 0u;
 #pragma unroll
-        for (int k = 0; k < kHeld; ++k) finish(k, t + k * group, most[k]);
-    } else {
-        // all threads of a row (256) take as many turns
-        for (int first = 0; first < plan.chunks; first += group) {
-            load(0, first + t);
-            uint32_t m = largest(x[0]);
-            if (kBlock == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            finish(0, first + t, m);
+            for (int o = kOfTile / 2; o > 0; o >>= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
+            const int tile = chunk / kOfTile;
+            if (t % kOfTile == 0 && tile < plan.tiles && row < plan.padded) to[tile * 128] = w;
+        };
+        if (kChunks) {
+#pragma unroll
+            for (int k = 0; k < kHeld; ++k) finish(k, t + k * group, most[r][k]);
+        } else {
+            // all threads of a row (256) take as many turns
+            for (int first = 0; first < plan.chunks; first += group) {
+                load(r, 0, first + t);
+                uint32_t m = largest(x[r][0]);
+                if (kBlock == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                finish(0, first + t, m);
+            }
         }
     }
 }
 
 template <typename T, int kBlock>
-cudaError_t launch_quantize(const sampler_micro_t& q, cudaStream_t stream)
+cudaError_t launch_quantize(const sampler_micro_t& q, int sms, cudaStream_t stream)
 {
     Plan p;
     const int64_t chunks = (q.cols + kPer - 1) / kPer;
@@ -278,15 +329,18 @@ cudaError_t launch_quantize(const sampler_micro_t& q, cudaStream_t stream)
     p.group = 8;
     while (p.group < kThreads && p.group < chunks) p.group *= 2;
     const int held = chunks <= p.group ? 1 : chunks <= 2 * kThreads ? 2 : chunks <= 4 * kThreads ? 4 : 0;
-    const int64_t per = kThreads / p.group;
+    // two rows in hand where there are many, for the loads under way
+    const bool two_rows = held == 1 && p.padded * p.group > int64_t(sms) * 8 * kThreads;
+    const int64_t per = kThreads / p.group * (two_rows ? 2 : 1);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned((p.padded + per - 1) / per));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
-    const auto kernel = held == 1   ? quantize_kernel<T, kBlock, 1>
-                        : held == 2 ? quantize_kernel<T, kBlock, 2>
-                        : held == 4 ? quantize_kernel<T, kBlock, 4>
-                                    : quantize_kernel<T, kBlock, 0>;
+    const auto kernel = two_rows    ? quantize_kernel<T, kBlock, 1, 2>
+                        : held == 1 ? quantize_kernel<T, kBlock, 1, 1>
+                        : held == 2 ? quantize_kernel<T, kBlock, 2, 1>
+                        : held == 4 ? quantize_kernel<T, kBlock, 4, 1>
+                                    : quantize_kernel<T, kBlock, 0, 1>;
     return cudaLaunchKernelEx(&cfg, kernel, q, p);
 }
 
@@ -324,51 +378,61 @@ struct Out<uint16_t> {
     }
 };
 
-// One 16-byte vector of a row in each thread, `group` of them side by side.
+// kVectors 16-byte vectors of a row in each thread, `group` of them side by side.
 template <typename T, int kBlock>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const sampler_micro_rows_t q, int group, int vectors, int tiles,
                                                         bool vec_in, bool vec_out)
 {
     constexpr int kVec = Out<T>::kVec;
     const int64_t r = int64_t(blockIdx.x) * (kThreads / group) + threadIdx.x / group;
-    const int i = int(blockIdx.y) * group + (threadIdx.x & (group - 1));
-    if (r >= q.n || i >= vectors) return;
-    const int64_t row = q.ids ? int64_t(q.ids[r]) : r;
-    const int64_t col = int64_t(i) * kVec;
-    const int count = int(min(int64_t(kVec), q.cols - col));
-    float x[kVec];
-    if (row < 0 || row >= q.rows) {
+    const int first = int(blockIdx.y) * (group * kVectors) + (threadIdx.x & (group - 1));
+    if (r >= q.n || first >= vectors) return;
+    const int64_t row = q.ids ? int64_t(__ldg(q.ids + r)) : r;
+    const bool there = row >= 0 && row < q.rows;
+    const uint8_t* v = static_cast<const uint8_t*>(q.values) + (there ? row * q.values_stride : 0);
+    const uint8_t* s = static_cast<const uint8_t*>(q.scales) + (there ? scale_word(row, 0, tiles) * 4 : 0);
+    T* out = static_cast<T*>(q.out) + r * q.out_stride;
+    const float row_scale = !there ? __int_as_float(0x7fc00000) : q.row_scale ? __ldg(q.row_scale + row) : 1.f;
+    const int cols = int(q.cols);
+    uint32_t codes[kVectors], scale[kVectors];
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) x[j] = __int_as_float(0x7fc00000);
-    } else {
-        const uint8_t* v = static_cast<const uint8_t*>(q.values) + row * q.values_stride + col / 2;
-        uint32_t codes = 0u;
+    for (int k = 0; k < kVectors; ++k) {
+        const int i = first + k * group, col = i * kVec, count = min(kVec, cols - col);
+        codes[k] = scale[k] = 0u;
+        if (!there || count <= 0) continue;
+        const uint8_t* p = v + col / 2;
         if (vec_in && count == kVec) {
-            codes = kVec == 8 ? *reinterpret_cast<const uint32_t*>(v) : *reinterpret_cast<const uint16_t*>(v);
+            codes[k] = kVec == 8 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p)));
         } else {
 #pragma unroll
             for (int j = 0; j < kVec / 2; ++j)
-                if (2 * j < count) codes |= uint32_t(v[j]) << 8 * j;
+                if (2 * j < count) codes[k] |= uint32_t(p[j]) << 8 * j;
         }
-        const int b = int(col / kBlock);
-        const uint32_t code = static_cast<const uint8_t*>(q.scales)[scale_word(row, b / 4, tiles) * 4 + b % 4];
-        const float unit = scale_value<kBlock>(code) * (q.row_scale ? q.row_scale[row] : 1.f);
+        const int b = col / kBlock;
+        scale[k] = __ldg(s + (b / 4) * 512 + b % 4);
+    }
+#pragma unroll
+    for (int k = 0; k < kVectors; ++k) {
+        const int i = first + k * group, col = i * kVec, count = min(kVec, cols - col);
+        if (count <= 0) break;
+        const float unit = scale_value<kBlock>(scale[k]) * row_scale;
+        float x[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; j += 2) {
-            const float2 y = values2(codes >> 4 * j & 0xffu);
+            const float2 y = values2(codes[k] >> 4 * j & 0xffu);
             x[j] = y.x * unit;
             x[j + 1] = y.y * unit;
         }
-    }
-    T* to = static_cast<T*>(q.out) + r * q.out_stride + col;
-    const uint4 y = Out<T>::pack(x);
-    if (vec_out && count == kVec) {
-        *reinterpret_cast<uint4*>(to) = y;
-    } else {
-        const T* e = reinterpret_cast<const T*>(&y);
+        T* to = out + col;
+        const uint4 y = Out<T>::pack(x);
+        if (vec_out && count == kVec) {
+            __stcs(reinterpret_cast<uint4*>(to), y);
+        } else {
+            const T* e = reinterpret_cast<const T*>(&y);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-            if (j < count) to[j] = e[j];
+            for (int j = 0; j < kVec; ++j)
+                if (j < count) to[j] = e[j];
+        }
     }
 }
 
@@ -378,12 +442,12 @@ cudaError_t launch_rows(const sampler_micro_rows_t& q, cudaStream_t stream)
     constexpr int kVec = Out<T>::kVec;
     const int64_t vectors = (q.cols + kVec - 1) / kVec;
     int group = 8;
-    while (group < kThreads && group < vectors) group *= 2;
+    while (group < kThreads && group * kVectors < vectors) group *= 2;
     const bool vec_in = reinterpret_cast<uintptr_t>(q.values) % (kVec / 2) == 0 && q.values_stride % (kVec / 2) == 0;
     const bool vec_out = reinterpret_cast<uintptr_t>(q.out) % 16 == 0 && q.out_stride * int64_t(sizeof(T)) % 16 == 0;
     const int64_t per = kThreads / group;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(unsigned((q.n + per - 1) / per), unsigned((vectors + group - 1) / group));
+    cfg.gridDim = dim3(unsigned((q.n + per - 1) / per), unsigned((vectors + group * kVectors - 1) / (group * kVectors)));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     const int tiles = int(((q.cols + kBlock - 1) / kBlock + 3) / 4);
@@ -392,13 +456,13 @@ cudaError_t launch_rows(const sampler_micro_rows_t& q, cudaStream_t stream)
 
 }  // namespace micro
 
-int micro_quantize_launch(const sampler_micro_t& q, cudaStream_t stream)
+int micro_quantize_launch(const sampler_micro_t& q, int sms, cudaStream_t stream)
 {
     using namespace micro;
     const bool bf16 = q.dtype == SAMPLER_DTYPE_BF16;
-    const cudaError_t e = q.block == 16 ? bf16 ? launch_quantize<uint16_t, 16>(q, stream) : launch_quantize<float, 16>(q, stream)
-                          : bf16        ? launch_quantize<uint16_t, 32>(q, stream)
-                                        : launch_quantize<float, 32>(q, stream);
+    const cudaError_t e = q.block == 16 ? bf16 ? launch_quantize<uint16_t, 16>(q, sms, stream) : launch_quantize<float, 16>(q, sms, stream)
+                          : bf16        ? launch_quantize<uint16_t, 32>(q, sms, stream)
+                                        : launch_quantize<float, 32>(q, sms, stream);
     return e == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
 }
 

@@ -318,7 +318,7 @@ int sampler_quantize_micro(sampler_t h, const sampler_micro_t* q, sampler_stream
         return SAMPLER_ERR_BAD_SHAPE;
     DeviceGuard guard;
     if (cudaSetDevice(h->device) != cudaSuccess) return SAMPLER_ERR_CUDA;
-    return dst::micro_quantize_launch(*q, cuda_stream(stream));
+    return dst::micro_quantize_launch(*q, h->num_sms, cuda_stream(stream));
 }
 
 int sampler_micro_rows(sampler_t h, const sampler_micro_rows_t* q, sampler_stream_t stream)

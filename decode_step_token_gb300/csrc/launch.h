@@ -222,9 +222,9 @@ int micro_quantize_launch(const sampler_micro_t& q, int sms, cudaStream_t stream
 int micro_rows_launch(const sampler_micro_rows_t& q, cudaStream_t stream);
 
 // Whether a handle has granted the head's kernels their shared memory, by block size,
-// few or many rows and the logits' type.
+// the form of the tiles and the logits' type.
 struct MicroHeadGrants {
-    bool granted[2][2][2];
+    bool granted[2][3][2];
 };
 
 int micro_head_launch(const sampler_micro_head_t& g, void* logits, int dtype, int64_t ldl, int64_t rows, int64_t vocab,

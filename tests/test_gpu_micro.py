@@ -171,7 +171,9 @@ SHAPES = [(1, 1, 1), (1, 128, 64), (2, 129, 65), (3, 1000, 32), (16, 4096, 256),
           # few tiles with many stages of K
           (1, 1, 600), (16, 1000, 4096), (5, 4000, 2500), (40, 3000, 4100), (100, 500, 1900), (150, 130, 8200),
           # several tiles for each CTA, with more than one ring's stages
-          (140, 42000, 1300), (300, 42001, 2100), (600, 20003, 384), (40, 40011, 2100), (128, 40000, 700)]
+          (140, 42000, 1300), (300, 42001, 2100), (600, 20003, 384), (40, 40011, 2100), (128, 40000, 700),
+          # tiles of two CTAs: few, several for each pair, a last one whose second CTA has no rows
+          (256, 20000, 100), (511, 42001, 2100), (700, 30001, 64), (2600, 9003, 300)]
 
 
 @pytest.mark.parametrize("rows,V,K", SHAPES)
@@ -193,7 +195,7 @@ def test_product(sampler, rows, V, K, kind, block):
     _close(got[:, :V], want, mag, K, kind)
 
 
-@pytest.mark.parametrize("rows,V,K", [(200, 3000, 512), (300, 3008, 300), (129, 256, 64)])
+@pytest.mark.parametrize("rows,V,K", [(200, 3000, 512), (300, 3008, 300), (129, 256, 64), (2600, 9008, 320)])
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 def test_product_on_whole_vectors(sampler, rows, V, K, kind):
     """Logits that the TMA engine stores, with guards after the last row and beside."""

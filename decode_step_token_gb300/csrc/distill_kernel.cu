@@ -15,13 +15,18 @@
 // between the two passes, so that each logit is read once and each gradient written once. Here a part is one buffer,
 // of which a CTA has two to four. Warp roles of a CTA:
 //   producer   goes ahead over the cluster's rows and brings their parts in with bulk copies;
-//   closers    (two, a row each in turn) mark the list's tokens of a part in a map of bits, a byte for each vector, before pass 1; take their
-//              logits from the buffer and put their share of the list's sums into all CTAs of the cluster; combine what
-//              all have put, work out the row's factors, write the row's outputs, and put the list's own gradients
-//              into the buffer in their logits' place;
-//   consumers  (eight) pass 1: the running reference and sum of what is not marked; pass 2: the gradient, marked elements
-//              as they now are in the buffer. A row's pass 1 comes before the pass 2 of the row before it, so that the
-//              join and the closer's work run under it.
+//   closers    (two, a row each in turn) mark the list's tokens of a part in a map of bits, a byte for each vector,
+//              before pass 1; take their logits from the buffer and put their share of the list's sums into all CTAs of
+//              the cluster; combine what all have put, work out the row's factors, write the row's outputs, and put the
+//              list's own gradients into the buffer in their logits' place;
+//   consumers  (sixteen) pass 1: the running reference and sum of what is not marked; pass 2: the gradient, marked
+//              elements as they now are in the buffer. A row's pass 1 comes before the pass 2 of the row before it, so
+//              that the join and the closer's work run under it.
+//
+// One CTA an SM. 4096 x 128000 bf16 with gradient, lists of 64, 0.9 of the rows counted: 379 us, 0.78 of the copy rate
+// over what has to move. Two CTAs of eight consumers an SM, with parts of half the size and twice as many: 475 us (twice
+// the joins and closers' turns of a row). What bounds it now is the consumers' instructions, which take 0.68 of the issue
+// slots: an exponential and packed arithmetic around it for each element in each pass.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -50,7 +55,7 @@ constexpr int kMaxParts = 16;                // CTAs of a cluster
 constexpr int kMaps = 3;                     // rows whose tokens are marked
 constexpr int kSums = 4;                     // rows whose sums are in shared memory
 constexpr int kHeld = SAMPLER_MAX_ALTERNATIVES / 32;  // of a list in each of the closer's lanes
-constexpr int kSmemTwo = 113 * 1024, kSmemOne = 226 * 1024;  // of a CTA: two on an SM, and one
+constexpr int kSmem = 226 * 1024;           // of a CTA, one on an SM
 constexpr uint64_t kSettleNs = 100000;       // in which what is on its way to shared memory lands
 
 // What a CTA's closer puts into all CTAs: sums of the list's tokens in its part.
@@ -680,24 +685,22 @@ int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, 
     const bool bf16 = p.rows.dtype == SAMPLER_DTYPE_BF16, grad = p.rows.out_grad != nullptr;
     const int per = bf16 ? 8 : 4;
     const int64_t vecs = (p.rows.vocab + 2 * per - 2) / per;  // the most that a row touches, wherever it starts
-    // CTAs of a cluster: so many that two on an SM have three buffers each, and more where rows are few; one CTA on an SM
-    // where a row is too long for that
+    // CTAs of a cluster: so many that three buffers of a part fit (one is filled while two rows are in hand), and more,
+    // of 4 KB at least, where rows are too few for the SMs
     auto part_of = [&](int parts) { return int((vecs + parts - 1) / parts); };
-    auto fits = [&](int parts, int buffers, int smem) { return smem_of(part_of(parts), buffers, parts) <= smem; };
+    auto fits = [&](int parts, int buffers) { return smem_of(part_of(parts), buffers, parts) <= kSmem; };
     int parts = 1;
-    while (parts < kMaxParts && !fits(parts, 3, kSmemOne)) parts *= 2;
-    const bool two = false;
+    while (parts < kMaxParts && !fits(parts, 3)) parts *= 2;
     while (parts < kMaxParts && p.rows.n_rows * parts < sms && part_of(2 * parts) >= 256) parts *= 2;
-    const int budget = two ? kSmemTwo : kSmemOne;
     p.part_vecs = part_of(parts);
     p.buffers = 2;
-    while (p.buffers < kMaxBuffers && fits(parts, p.buffers + 1, budget)) ++p.buffers;
-    if (!fits(parts, 2, budget)) return SAMPLER_ERR_TOO_LARGE;  // (no row of the vocabularies that handles take)
+    while (p.buffers < kMaxBuffers && fits(parts, p.buffers + 1)) ++p.buffers;
+    if (!fits(parts, 2)) return SAMPLER_ERR_TOO_LARGE;  // (no row of the vocabularies that handles take)
     const auto kernel = bf16 ? grad ? distill_kernel<uint16_t, true> : distill_kernel<uint16_t, false>
                              : grad ? distill_kernel<float, true> : distill_kernel<float, false>;
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = size_t(budget);
+    cfg.dynamicSmemBytes = size_t(kSmem);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -705,10 +708,10 @@ int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, 
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const int size = parts == 1 ? 0 : parts == 2 ? 1 : parts == 4 ? 2 : parts == 8 ? 3 : 4;
-    int& resident = occ->clusters[bf16][grad][size][two];
+    int& resident = occ->clusters[bf16][grad][size];
     if (resident < 1) {  // once for each kernel and shape of the launch of a handle
         const void* k = reinterpret_cast<const void*>(kernel);
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemOne) != cudaSuccess ||
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
             (parts > 8 && cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
             return SAMPLER_ERR_CUDA;
         cfg.gridDim = dim3(unsigned(parts));

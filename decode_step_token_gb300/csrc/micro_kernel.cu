@@ -15,6 +15,13 @@
 // Scales are laid out as the tensor cores take them: 512 bytes for 128 rows by 4
 // blocks, (row % 32) * 16 + (row / 32 % 4) * 4 + block % 4. The four bytes of a
 // row are stored as one word.
+//
+// What bounds both ways is memory, for blocks of 16 the instructions too: 128000 x
+// 4096 bf16 takes 232 us with blocks of 32 and 318 of 16 (0.84 and 0.62 of the copy
+// rate), and 240 and 232 back (0.81 and 0.85). A value at a time as fp32, with one row
+// in hand, they were 287 and 423; a vector a thread back, 369 and 386. Rows of 1000
+// (20000 of them: 19 and 27 us, 0.39 and 0.28) leave half of a group's threads without
+// a chunk.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -89,27 +96,51 @@ struct Raw {
     uint32_t w[kWords];
 };
 
+// The first `count` of 16 values, zeros after them. Values that do not lie in whole vectors are cut out of the 16-byte
+// vectors that hold them, and never out of one that holds none (20000 rows of 1001 bf16: 25 us for 31 one by one; of
+// fp32 31 for 46, though 4001 of 5003 take 35 for 31).
 template <typename T>
 __device__ __forceinline__ void load16(Raw<T>& x, const T* p, int count, bool vec)
 {
+    constexpr int kWords = Raw<T>::kWords;
     if (vec && count == kPer) {
 #pragma unroll
-        for (int j = 0; j < Raw<T>::kWords / 4; ++j) {
+        for (int j = 0; j < kWords / 4; ++j) {
             const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + j);
             x.w[4 * j] = v.x;
             x.w[4 * j + 1] = v.y;
             x.w[4 * j + 2] = v.z;
             x.w[4 * j + 3] = v.w;
         }
-    } else {
+        return;
+    }
+    const uint32_t off = uint32_t(reinterpret_cast<uintptr_t>(p)) & 15u;
+    const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - off);
+    const int end = count > 0 ? int(off) + count * int(sizeof(T)) : 0;
+    uint32_t w[kWords + 4];
 #pragma unroll
-        for (int j = 0; j < Raw<T>::kWords; ++j) {
-            if (sizeof(T) == 4) {
-                x.w[j] = j < count ? reinterpret_cast<const uint32_t*>(p)[j] : 0u;
-            } else {
-                const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-                x.w[j] = (2 * j < count ? uint32_t(h[2 * j]) : 0u) | (2 * j + 1 < count ? uint32_t(h[2 * j + 1]) << 16 : 0u);
-            }
+    for (int j = 0; j <= kWords / 4; ++j) {
+        const uint4 v = 16 * j < end ? __ldg(from + j) : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * j] = v.x;
+        w[4 * j + 1] = v.y;
+        w[4 * j + 2] = v.z;
+        w[4 * j + 3] = v.w;
+    }
+    if (off & 8u) {
+#pragma unroll
+        for (int j = 0; j < kWords + 2; ++j) w[j] = w[j + 2];
+    }
+    if (off & 4u) {
+#pragma unroll
+        for (int j = 0; j < kWords + 1; ++j) w[j] = w[j + 1];
+    }
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) x.w[j] = sizeof(T) == 2 ? __funnelshift_r(w[j], w[j + 1], (off & 2u) * 8u) : w[j];
+    if (count < kPer) {
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+            const int left = count * int(sizeof(T)) / 2 - 2 * j;  // halves of the word
+            x.w[j] = left >= 2 ? x.w[j] : left == 1 ? x.w[j] & 0xffffu : 0u;
         }
     }
 }
@@ -329,7 +360,8 @@ cudaError_t launch_quantize(const sampler_micro_t& q, int sms, cudaStream_t stre
     p.group = 8;
     while (p.group < kThreads && p.group < chunks) p.group *= 2;
     const int held = chunks <= p.group ? 1 : chunks <= 2 * kThreads ? 2 : chunks <= 4 * kThreads ? 4 : 0;
-    // two rows in hand where there are many, for the loads under way
+    // two rows in hand where there are more than eight blocks' worth for each SM, for the loads under way: the same time
+    // for blocks of 32 as with one, a tenth less for blocks of 16; with fewer rows half of the blocks would not be there
     const bool two_rows = held == 1 && p.padded * p.group > int64_t(sms) * 8 * kThreads;
     const int64_t per = kThreads / p.group * (two_rows ? 2 : 1);
     cudaLaunchConfig_t cfg{};
@@ -378,8 +410,20 @@ struct Out<uint16_t> {
     }
 };
 
-// kVectors 16-byte vectors of a row in each thread, `group` of them side by side.
-template <typename T, int kBlock>
+// Eight codes of a row from column `col` on, in a word, as far as they lie in one of the row's `words` words of codes.
+__device__ __forceinline__ uint32_t codes_at(const uint8_t* row, int col, int words)
+{
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row);
+    const int i = col >> 3;  // (rounded down: columns before the first have codes 0)
+    const uint32_t a = i >= 0 ? __ldg(w + i) : 0u, b = i + 1 < words ? __ldg(w + i + 1) : 0u;
+    return __funnelshift_r(a, b, 4 * (col & 7));
+}
+
+// kVectors 16-byte vectors of the output in each thread, `group` of them side by side. kCut (bf16 whose rows begin within
+// a vector): the vectors are the output's, whose codes and scales are cut out of the row's, and not the row's, stored one
+// by one: 3000 x 15001 takes 48 us in place of 127. In fp32, with half as many values in a vector, it would be 36 in place
+// of 29 (20001 x 1001).
+template <typename T, int kBlock, bool kCut>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const sampler_micro_rows_t q, int group, int vectors, int tiles,
                                                         bool vec_in, bool vec_out)
 {
@@ -393,45 +437,59 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const sampler_micro_rows
     const uint8_t* s = static_cast<const uint8_t*>(q.scales) + (there ? scale_word(row, 0, tiles) * 4 : 0);
     T* out = static_cast<T*>(q.out) + r * q.out_stride;
     const float row_scale = !there ? __int_as_float(0x7fc00000) : q.row_scale ? __ldg(q.row_scale + row) : 1.f;
-    const int cols = int(q.cols);
-    uint32_t codes[kVectors], scale[kVectors];
+    const int cols = int(q.cols), bytes = (cols + 1) / 2;
+    const int head = kCut ? int(reinterpret_cast<uintptr_t>(out) & 15u) / int(sizeof(T)) : 0;  // columns of the first vector before the row
+    uint32_t codes[kVectors], scale[kVectors], next[kVectors];
 #pragma unroll
     for (int k = 0; k < kVectors; ++k) {
-        const int i = first + k * group, col = i * kVec, count = min(kVec, cols - col);
-        codes[k] = scale[k] = 0u;
-        if (!there || count <= 0) continue;
-        const uint8_t* p = v + col / 2;
-        if (vec_in && count == kVec) {
-            codes[k] = kVec == 8 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p)));
-        } else {
+        const int col = (first + k * group) * kVec - head;
+        codes[k] = scale[k] = next[k] = 0u;
+        if (!there || col >= cols) continue;
+        if (kCut) {
+            if (vec_in) {
+                codes[k] = codes_at(v, col, (bytes + 3) / 4);
+            } else {
 #pragma unroll
-            for (int j = 0; j < kVec / 2; ++j)
-                if (2 * j < count) codes[k] |= uint32_t(p[j]) << 8 * j;
+                for (int j = 0; j < kVec; ++j)
+                    if (col + j >= 0 && col + j < cols) codes[k] |= (uint32_t(v[(col + j) / 2]) >> 4 * ((col + j) & 1) & 15u) << 4 * j;
+            }
+            const int b0 = max(col, 0) / kBlock, b1 = min(col + kVec - 1, cols - 1) / kBlock;
+            scale[k] = __ldg(s + (b0 / 4) * 512 + b0 % 4);
+            next[k] = b1 == b0 ? scale[k] : __ldg(s + (b1 / 4) * 512 + b1 % 4);
+        } else {
+            const uint8_t* p = v + col / 2;
+            if (vec_in && col + kVec <= cols) {
+                codes[k] = kVec == 8 ? __ldg(reinterpret_cast<const uint32_t*>(p)) : uint32_t(__ldg(reinterpret_cast<const uint16_t*>(p)));
+            } else {
+#pragma unroll
+                for (int j = 0; j < kVec / 2; ++j)
+                    if (col + 2 * j < cols) codes[k] |= uint32_t(p[j]) << 8 * j;
+            }
+            const int b = col / kBlock;
+            scale[k] = __ldg(s + (b / 4) * 512 + b % 4);
         }
-        const int b = col / kBlock;
-        scale[k] = __ldg(s + (b / 4) * 512 + b % 4);
     }
 #pragma unroll
     for (int k = 0; k < kVectors; ++k) {
-        const int i = first + k * group, col = i * kVec, count = min(kVec, cols - col);
-        if (count <= 0) break;
-        const float unit = scale_value<kBlock>(scale[k]) * row_scale;
+        const int col = (first + k * group) * kVec - head;
+        if (col >= cols) break;
+        const float unit = scale_value<kBlock>(scale[k]) * row_scale, after = kCut ? scale_value<kBlock>(next[k]) * row_scale : unit;
+        const int change = kCut ? (max(col, 0) / kBlock + 1) * kBlock - col : kVec;  // from where on the next block's scale counts
         float x[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; j += 2) {
             const float2 y = values2(codes[k] >> 4 * j & 0xffu);
-            x[j] = y.x * unit;
-            x[j + 1] = y.y * unit;
+            x[j] = y.x * (kCut && j >= change ? after : unit);
+            x[j + 1] = y.y * (kCut && j + 1 >= change ? after : unit);
         }
-        T* to = out + col;
         const uint4 y = Out<T>::pack(x);
-        if (vec_out && count == kVec) {
-            __stcs(reinterpret_cast<uint4*>(to), y);
+        if (vec_out && (!kCut || col >= 0) && col + kVec <= cols) {
+            __stcs(reinterpret_cast<uint4*>(out + col), y);
         } else {
             const T* e = reinterpret_cast<const T*>(&y);
 #pragma unroll
             for (int j = 0; j < kVec; ++j)
-                if (j < count) to[j] = e[j];
+                if ((!kCut || col + j >= 0) && col + j < cols) out[col + j] = e[j];
         }
     }
 }
@@ -440,18 +498,20 @@ template <typename T, int kBlock>
 cudaError_t launch_rows(const sampler_micro_rows_t& q, cudaStream_t stream)
 {
     constexpr int kVec = Out<T>::kVec;
-    const int64_t vectors = (q.cols + kVec - 1) / kVec;
+    const bool vec_in = reinterpret_cast<uintptr_t>(q.values) % (kVec / 2) == 0 && q.values_stride % (kVec / 2) == 0;
+    const bool whole = reinterpret_cast<uintptr_t>(q.out) % 16 == 0 && q.out_stride * int64_t(sizeof(T)) % 16 == 0;
+    const bool cut = sizeof(T) == 2 && !whole;
+    const int64_t vectors = (q.cols + (cut ? 2 * kVec - 2 : kVec - 1)) / kVec;  // the most that a row touches
     int group = 8;
     while (group < kThreads && group * kVectors < vectors) group *= 2;
-    const bool vec_in = reinterpret_cast<uintptr_t>(q.values) % (kVec / 2) == 0 && q.values_stride % (kVec / 2) == 0;
-    const bool vec_out = reinterpret_cast<uintptr_t>(q.out) % 16 == 0 && q.out_stride * int64_t(sizeof(T)) % 16 == 0;
     const int64_t per = kThreads / group;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned((q.n + per - 1) / per), unsigned((vectors + group * kVectors - 1) / (group * kVectors)));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
     const int tiles = int(((q.cols + kBlock - 1) / kBlock + 3) / 4);
-    return cudaLaunchKernelEx(&cfg, rows_kernel<T, kBlock>, q, group, int(vectors), tiles, vec_in, vec_out);
+    const auto kernel = sizeof(T) == 2 && cut ? rows_kernel<T, kBlock, sizeof(T) == 2> : rows_kernel<T, kBlock, false>;
+    return cudaLaunchKernelEx(&cfg, kernel, q, group, int(vectors), tiles, vec_in, whole || cut);
 }
 
 }  // namespace micro

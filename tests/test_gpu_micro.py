@@ -122,6 +122,28 @@ def test_rows_by_id(sampler, cols, kind, block):
             assert np.isnan(out[i]).all()
 
 
+@pytest.mark.parametrize("cols", [1, 7, 31, 33, 97, 500])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [16, 32])
+def test_rows_to_anywhere(sampler, cols, kind, block):
+    """Rows back to outputs that begin at each place of a vector, with guards around."""
+    import torch
+
+    rng = np.random.default_rng(cols)
+    t, _ = _source(rng, 40, cols, "bf16")
+    got, scales, row_scale = _quantize(sampler, t.cuda(), block)
+    want = M.values(got.cpu().numpy(), scales.cpu().numpy(), row_scale.cpu().numpy(), cols, block)
+    dtype = torch.bfloat16 if kind == "bf16" else torch.float32
+    want = torch.from_numpy(want.astype(np.float32)).to(dtype).float().numpy()
+    for shift in range(8):
+        for gap in (0, 8 - cols % 8, 5):  # rows that begin one after the other, each at the same place, and elsewhere
+            flat = torch.full((40 * (cols + gap) + shift + 40,), -7.0, dtype=dtype, device="cuda:0")
+            view = flat[shift:shift + 40 * (cols + gap)].view(40, cols + gap)
+            sampler.micro_rows(values=got, scales=scales, row_scale=row_scale, block=block, out=view[:, :cols])
+            np.testing.assert_array_equal(view[:, :cols].float().cpu().numpy(), want)
+            assert (view[:, cols:] == -7).all() and (flat[:shift] == -7).all() and (flat[-40:] == -7).all()
+
+
 def _operand(rng, rows, K, block, row_scale=True):
     """Random codes and scales: every code, scales of all sizes with zeros among them."""
     half = (K + 1) // 2

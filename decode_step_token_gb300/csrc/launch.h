@@ -180,9 +180,9 @@ struct TopParams {
     uint64_t wait_ns;
 };
 
-// Whether a handle has granted the kernel its shared memory, by the logits' type and entropy.
+// Whether a handle has granted the kernels their shared memory, by the logits' type and entropy.
 struct TopGrants {
-    bool granted[2][2];
+    bool granted[2][2], short_granted[2][2];
 };
 
 int top_launch(const TopParams& params, int sms, TopGrants* grants, cudaStream_t stream);

@@ -616,21 +616,26 @@ __device__ __forceinline__ bool leave(const TopParams& P, int64_t r, uint32_t pa
 }
 
 // The outputs of a row that has no statistics: left out (zeros) or with a status (NaN).
-__device__ __forceinline__ void write_none(const TopParams& P, int64_t r, int status)
+__device__ __forceinline__ void write_none(const TopParams& P, int64_t r, int status, int thread, int threads)
 {
     const sampler_rows_t& a = P.rows;
     const float x = status == SAMPLER_ROW_OK ? 0.f : quiet_nan();
     const int n = P.top.top_n;
-    for (int j = threadIdx.x; j < n; j += kConsumers) {
+    for (int j = thread; j < n; j += threads) {
         P.top.out_top_ids[r * n + j] = -1;
         P.top.out_top_logprobs[r * n + j] = x;
     }
-    if (threadIdx.x == 0) {
+    if (thread == 0) {
         if (P.top.out_rest_logprob) P.top.out_rest_logprob[r] = x;
         if (a.out_logprob) a.out_logprob[r] = x;
         if (a.out_entropy) a.out_entropy[r] = x;
         if (a.out_status) a.out_status[r] = status;
     }
+}
+
+__device__ __forceinline__ void write_none(const TopParams& P, int64_t r, int status)
+{
+    write_none(P, r, status, int(threadIdx.x), kConsumers);
 }
 
 // The closer (a warp), with a row's `count` largest keys in order and the sums of the rest: its outputs.
@@ -833,6 +838,27 @@ __device__ __forceinline__ void sort_keys(const uint64_t* list, int count, uint6
     __syncwarp();
 }
 
+// A row that is done, of whose list (of 32 * kLane keys at most, none below `bar`) n at most are wanted; a whole warp.
+template <bool kEntropy>
+__device__ __forceinline__ void close_list(const TopParams& P, uint64_t* list, int count, uint64_t* sorted, float bar, Sums st,
+                                           const RowJob& h, int64_t r)
+{
+    const uint32_t n = uint32_t(P.top.top_n);
+    if (uint32_t(count) > n) {
+        Keys keys;
+        take_keys(keys, list, count);
+        const uint64_t least = select_warp(keys, n, n, true, order_of(bar));
+        Sums lost;
+        count = split_keys<kEntropy>(keys, least, list, Scale{h.c, h.c_hi, h.c_lo}, lost);
+        move(st, key_value(least), h.c);
+        move(lost, st.ref, h.c);
+        st.s += lost.s;
+        st.t += lost.t;
+    }
+    sort_keys(list, count, sorted);
+    close_row<kEntropy>(P, sorted, count, st, h, r);
+}
+
 template <bool kEntropy>
 __device__ __forceinline__ void run_closer(const TopParams& P)
 {
@@ -868,22 +894,6 @@ __device__ __forceinline__ void run_closer(const TopParams& P)
                 st.s += S.sums[job.list >> 1][w].x;
                 st.t += S.sums[job.list >> 1][w].y;
             }
-            const uint64_t* sorted = list;
-            if (!job.ordered) {
-                if (uint32_t(count) > n) {
-                    Keys keys;
-                    take_keys(keys, list, count);
-                    const uint64_t least = select_warp(keys, n, n, true, order_of(job.bar));
-                    Sums lost;
-                    count = split_keys<kEntropy>(keys, least, list, q, lost);
-                    move(st, key_value(least), q.c);
-                    move(lost, st.ref, q.c);
-                    st.s += lost.s;
-                    st.t += lost.t;
-                }
-                sort_keys(list, count, S.sorted);
-                sorted = S.sorted;
-            }
             RowJob h;
             h.token = job.token;
             h.x_t = job.x_t;
@@ -892,7 +902,10 @@ __device__ __forceinline__ void run_closer(const TopParams& P)
             h.c_lo = job.c_lo;
             h.inv_t = job.inv_t;
             h.inv_t_lo = job.inv_t_lo;
-            close_row<kEntropy>(P, sorted, count, st, h, job.row);
+            if (job.ordered)
+                close_row<kEntropy>(P, list, count, st, h, job.row);
+            else
+                close_list<kEntropy>(P, list, count, S.sorted, job.bar, st, h, job.row);
         }
         __syncwarp();
         if (lane == 0) {
@@ -962,15 +975,47 @@ __device__ __noinline__ int join_parts(const TopParams& P, int64_t r, uint32_t a
     bar_sync();
     if (flags) return flags & 2 ? -1 : -2;
     if (count > uint32_t(kConsumers)) {
-        S.state[tid] = make_float4(st.bar, st.ref, st.s, st.t);
-        cut_long<kEntropy>(at, count, n, n, c, c_hi, c_lo);
-        const float4 in = S.state[tid];
-        st = Sums{in.x, in.y, in.z, in.w};
-        count = n;
-        // (back into the list that the ranking reads)
-        const uint64_t k = uint32_t(tid) < count ? S.list[at + 1][tid] : 0;
+        // More than are ranked at once. A bar for them all: of the first of each part's (which are in order), as many as
+        // there are threads, the n-th. What does not reach it is lost. (6 rows of 157971 bf16 in 28 parts, n = 18: ? us in
+        // place of 31 by bisection.)
+        const uint32_t each = uint32_t(kConsumers / parts), p = uint32_t(tid) / each, i = uint32_t(tid) % each;
+        uint32_t before = 0;
+        for (uint32_t k = 0; k < p && k < uint32_t(parts); ++k) before += uint32_t(S.part_count[k]);
+        const bool there = p < uint32_t(parts) && i < uint32_t(S.part_count[p]);
+        const uint64_t mine = there ? S.list[at][before + i] : 0;
+        S.list[at + 1][tid] = mine;
+        if (tid == 0) S.cut_least = 0;
         bar_sync();
-        if (uint32_t(tid) < count) S.list[at][tid] = k;
+        uint32_t above = 0;
+        const ulonglong2* pairs = reinterpret_cast<const ulonglong2*>(S.list[at + 1]);
+#pragma unroll 8
+        for (int j = 0; j < kConsumers / 2; ++j) {
+            const ulonglong2 k = pairs[j];
+            above += k.x > mine;
+            above += k.y > mine;
+        }
+        if (there && above == n - 1) S.cut_least = mine;
+        bar_sync();
+        const uint64_t least = S.cut_least;
+        uint32_t from = at;
+        if (least != 0) {
+            cut<kEntropy>(at, count, least, st, q);
+            bar_sync();
+            count = S.count[at + 1];
+            from = at + 1;
+        }
+        if (count > uint32_t(kConsumers)) {
+            S.state[tid] = make_float4(st.bar, st.ref, st.s, st.t);
+            from = cut_long<kEntropy>(from, count, n, n, c, c_hi, c_lo);
+            const float4 in = S.state[tid];
+            st = Sums{in.x, in.y, in.z, in.w};
+            count = n;
+        }
+        if (from != at) {  // back into the list that the ranking reads
+            const uint64_t k = uint32_t(tid) < count ? S.list[from][tid] : 0;
+            bar_sync();
+            if (uint32_t(tid) < count) S.list[at][tid] = k;
+        }
         bar_sync();
     }
     rank<kEntropy>(S.list[at], count, n, S.list[at + 1], st, q);
@@ -1352,6 +1397,270 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
     }
 }
 
+// ---------------------------------------------------------------- short rows
+// A warp by itself takes a row of 16 KB at most, all of it in shared memory, with the next one on its way there while the
+// row's keys are put in order.
+constexpr int kShortWarps = 4;
+constexpr int kShortVecs = 1025;   // of a row
+constexpr int kShortResident = 5;  // CTAs of kShortWarps that an SM's registers hold
+constexpr int kGroups = 8;         // of a lane's vectors
+
+struct Short {
+    uint64_t list[kClosable];
+    uint64_t sorted[kMost];
+    uint32_t count;
+    uint32_t pad[3];
+};
+constexpr int kSmemOfSm = 228 * 1024;
+constexpr int kShortSmem = kShortWarps * (kShortVecs * 16 + int(sizeof(Short)));
+
+__device__ __forceinline__ void copy_vector(uint4* to, const uint4* from)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
+
+// The largest elements that a lane's groups have: of a group one in fp32, two in bf16 (of the even and the odd ones).
+template <typename T>
+struct Largest {
+    static constexpr int kCount = sizeof(T) == 2 ? 2 * kGroups : kGroups;
+    float x[kCount];
+};
+
+template <typename T>
+__device__ __forceinline__ Largest<T> largest_of(const uint32_t (&peaks)[kGroups])
+{
+    Largest<T> y;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        if (sizeof(T) == 2) {
+            y.x[2 * g] = __uint_as_float(peaks[g] << 16);
+            y.x[(2 * g + 1) % Largest<T>::kCount] = __uint_as_float(peaks[g] & 0xffff0000u);
+        } else {
+            y.x[g] = __uint_as_float(peaks[g]);
+        }
+    }
+    return y;
+}
+
+// The order of a value that n of the lanes' largest reach, and not many more than n; `top` is the largest's. The lowest
+// finite value's where there are fewer than n.
+template <typename T>
+__device__ __forceinline__ uint32_t first_bar(const Largest<T>& a, uint32_t n, uint32_t top)
+{
+    auto reach = [&](float b1, float b2, float b3) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < Largest<T>::kCount; ++i)
+            c += (a.x[i] >= b1 ? 1u : 0u) + (a.x[i] >= b2 ? 1u << 10 : 0u) + (a.x[i] >= b3 ? 1u << 20 : 0u);
+        return __reduce_add_sync(0xffffffffu, c);
+    };
+    uint32_t lo = order_of(-kFloatMax), hi = top + 1;
+#pragma unroll 1
+    while (hi - lo > 1) {
+        const uint32_t q = max((hi - lo) / 4, 1u), o1 = lo + q, o2 = min(o1 + q, hi), o3 = min(o2 + q, hi);
+        const uint32_t got = reach(value_of(o1), value_of(o2), value_of(o3)), c1 = got & 1023u, c2 = got >> 10 & 1023u,
+                       c3 = got >> 20;
+        uint32_t c;
+        if (c3 >= n) {
+            lo = o3;
+            c = c3;
+        } else if (c2 >= n) {
+            lo = o2;
+            hi = o3;
+            c = c2;
+        } else if (c1 >= n) {
+            lo = o1;
+            hi = o2;
+            c = c1;
+        } else {
+            hi = o1;
+            continue;
+        }
+        if (c <= n + n / 8) break;
+    }
+    return lo;
+}
+
+// The least key of those that n to kClosable of the row's reach; more than kClosable reach the value of order `lo`.
+template <typename T>
+__device__ __forceinline__ uint64_t least_of_row(const T* x, int vocab, uint32_t n, uint32_t lo, uint32_t top)
+{
+    const int lane = threadIdx.x & 31;
+    auto reach = [&](uint64_t key) {
+        uint32_t c = 0;
+        for (int j = lane; j < vocab; j += 32) c += key_of(load_logit(x + j), j) >= key;
+        return __reduce_add_sync(0xffffffffu, c);
+    };
+    uint64_t l = uint64_t(lo) << 32, h = (uint64_t(top) + 1) << 32;
+    for (int part = 0; part < 2; ++part) {
+        const uint64_t last = part == 0 ? 1ull << 32 : 1;
+#pragma unroll 1
+        while (h - l > last) {
+            const uint64_t mid = l + ((h - l) / 2 & ~(last - 1));
+            const uint32_t got = reach(mid);
+            if (got >= n) {
+                l = mid;
+                if (got <= uint32_t(kClosable)) return l;
+            } else {
+                h = mid;
+            }
+        }
+        if (part == 0) l |= uint32_t(~uint32_t(kMaxToken));  // the lowest key of the value
+    }
+    return l;
+}
+
+template <typename T, bool kEntropy>
+__global__ void __launch_bounds__(kShortWarps * 32, kShortResident) top_short_kernel(const __grid_constant__ TopParams P)
+{
+    constexpr int kPer = Elems<T>::kPer;
+    const sampler_rows_t& a = P.rows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, vocab = int(a.vocab);
+    unsigned char* mine = ring_of() + warp * (P.part_vecs * 16 + int(sizeof(Short)));
+    uint4* vecs = reinterpret_cast<uint4*>(mine);
+    Short& S = *reinterpret_cast<Short*>(mine + P.part_vecs * 16);
+    const uint32_t n = uint32_t(P.top.top_n);
+    const int64_t step = int64_t(gridDim.x) * (blockDim.x >> 5);
+
+    // What comes with a row, and its vectors where it counts.
+    struct Next {
+        float weight, temperature;
+        int token;
+    };
+    auto look = [&](int64_t r) {
+        Next y{0.f, 1.f, 0};
+        if (r >= a.n_rows) return y;
+        y.weight = a.weight ? a.weight[r] : 1.f;
+        if (a.temperature) y.temperature = a.temperature[r];
+        if (a.tokens) y.token = a.tokens[r];
+        return y;
+    };
+    auto fetch = [&](int64_t r) {
+        const T* x = static_cast<const T*>(a.logits) + r * a.row_stride;
+        const RowSpan span = row_span(x, a.vocab);
+        const uint4* from = reinterpret_cast<const uint4*>(x - span.head);
+        for (int i = lane; i < span.count; i += 32) copy_vector(vecs + i, from + i);
+    };
+
+    int64_t r = int64_t(blockIdx.x) + int64_t(gridDim.x) * warp;
+    Next now = look(r);
+    if (now.weight != 0.f) fetch(r);
+    for (; r < a.n_rows; r += step) {
+        const Next next = look(r + step);
+        // (the row's vectors have been read when this is called)
+        auto ahead = [&] {
+            __syncwarp();
+            if (next.weight != 0.f) fetch(r + step);
+        };
+        const Next given = now;
+        now = next;
+        if (given.weight == 0.f) {
+            write_none(P, r, SAMPLER_ROW_OK, lane, 32);
+            ahead();
+            continue;
+        }
+        RowJob h;
+        h.token = given.token;
+        row_scale(h, a, given.temperature);
+        const RowSpan span = row_span(static_cast<const T*>(a.logits) + r * a.row_stride, a.vocab);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        // what is not the row's becomes -inf
+        if (lane == 0) {
+            uint4 v = vecs[0];
+            Elems<T>::mask(v, span.head, span.head + vocab);
+            vecs[0] = v;
+            const int at = (span.count - 1) * kPer;
+            v = vecs[span.count - 1];
+            Elems<T>::mask(v, span.head - at, span.head + vocab - at);
+            vecs[span.count - 1] = v;
+            S.count = 0;
+        }
+        __syncwarp();
+        const T* x = reinterpret_cast<const T*>(vecs) + span.head;
+        h.x_t = a.out_logprob && !h.bad_param ? load_logit(x + h.token) : 0.f;
+
+        uint32_t peaks[kGroups];
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) peaks[g] = Peak<T>::none();
+        for (int base = 0; base < span.count; base += 32 * kGroups)
+#pragma unroll
+            for (int g = 0; g < kGroups; ++g) {
+                const int i = base + 32 * g + lane;
+                if (i < span.count) peaks[g] = Peak<T>::join(peaks[g], peak<T>(vecs[i]));
+            }
+        uint32_t most = peaks[0];
+#pragma unroll
+        for (int g = 1; g < kGroups; ++g) most = Peak<T>::join(most, peaks[g]);
+        const float largest = Peak<T>::value(most);
+        const bool bad = __any_sync(0xffffffffu, !(largest < pos_inf()));
+        const uint32_t top = __reduce_max_sync(0xffffffffu, order_of(largest));
+        const int status = h.bad_param            ? SAMPLER_ROW_BAD_PARAM
+                           : bad                  ? SAMPLER_ROW_NONFINITE
+                           : top < order_of(-kFloatMax) ? SAMPLER_ROW_ALL_NEG_INF
+                                                  : SAMPLER_ROW_OK;
+        if (status != SAMPLER_ROW_OK) {
+            write_none(P, r, status, lane, 32);
+            ahead();
+            continue;
+        }
+        const uint32_t lo = first_bar<T>(largest_of<T>(peaks), n, top);
+        Sums st{below(lo), value_of(lo), 0.f, 0.f};
+        const uint32_t bar = packed_bar<T>(st.bar);
+        for (int base = 0; base < span.count; base += 32 * kVecs) {
+            uint4 v[kVecs];
+            uint32_t above = 0;
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) {
+                const int i = base + 32 * k + lane;
+                v[k] = i < span.count ? vecs[i] : make_uint4(Peak<T>::none(), Peak<T>::none(), Peak<T>::none(), Peak<T>::none());
+                if (Peak<T>::above(peak<T>(v[k]), bar)) above |= take_above<T>(v[k], bar) << k * kPer;
+            }
+            if (above) {
+                uint32_t to = next_places(&S.count, uint32_t(__popc(above)));
+                for (; above && to < uint32_t(kClosable); ++to, above &= above - 1) {
+                    const int bit = __ffs(above) - 1, j = (base + 32 * (bit / kPer) + lane) * kPer + bit % kPer - span.head;
+                    S.list[to] = key_of(load_logit(x + j), j);
+                }
+            }
+            add<T, kEntropy>(st, v, two(h.c, h.c));
+        }
+        __syncwarp();
+        uint32_t count = S.count;
+        if (count > uint32_t(kClosable)) {
+            // ties, or a row whose largest are close together: a key for a bar, and all of it once more
+            const uint64_t least = least_of_row<T>(x, vocab, n, lo, top);
+            st = Sums{0.f, key_value(least), 0.f, 0.f};
+            st.bar = st.ref;
+            count = 0;
+            for (int base = 0; base < vocab; base += 32) {
+                const int j = base + lane;
+                const float y = j < vocab ? load_logit(x + j) : -pos_inf();
+                const uint64_t k = key_of(y, j);
+                const bool stays = j < vocab && k >= least;
+                const uint32_t lanes = __ballot_sync(0xffffffffu, stays);
+                if (stays) {
+                    S.list[count + __popc(lanes & ((1u << lane) - 1u))] = k;
+                } else {
+                    const float u = (y - st.ref) * h.c, f = exp2_fast(u);
+                    st.s += f;
+                    if (kEntropy) st.t = fmaf(f, fmaxf(u, kLowest), st.t);
+                }
+                count += uint32_t(__popc(lanes));
+            }
+        }
+        ahead();
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            st.s += __shfl_xor_sync(0xffffffffu, st.s, o);
+            if (kEntropy) st.t += __shfl_xor_sync(0xffffffffu, st.t, o);
+        }
+        st.bar = st.ref;
+        close_list<kEntropy>(P, S.list, int(count), S.sorted, st.ref, st, h, r);
+        __syncwarp();
+    }
+}
+
 }  // namespace top
 
 int top_launch(const TopParams& params, int sms, TopGrants* grants, cudaStream_t stream)
@@ -1361,6 +1670,27 @@ int top_launch(const TopParams& params, int sms, TopGrants* grants, cudaStream_t
     const bool bf16 = p.rows.dtype == SAMPLER_DTYPE_BF16, entropy = p.rows.out_entropy != nullptr;
     const int per = bf16 ? 8 : 4;
     const int64_t vecs = (p.rows.vocab + 2 * per - 2) / per;  // the most that a row touches, wherever it starts
+    if (vecs <= kShortVecs && p.wait_ns != 0) {  // (a handle whose waits all give up takes the kernel that waits)
+        const auto kernel = bf16 ? entropy ? top_short_kernel<uint16_t, true> : top_short_kernel<uint16_t, false>
+                                 : entropy ? top_short_kernel<float, true> : top_short_kernel<float, false>;
+        bool& granted = grants->short_granted[bf16][entropy];
+        if (!granted && cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kShortSmem) != cudaSuccess)
+            return SAMPLER_ERR_CUDA;
+        granted = true;
+        p.parts = 1;
+        p.part_vecs = int(vecs);
+        // rows on as many SMs as there are
+        const int64_t warps = std::min<int64_t>(kShortWarps, (p.rows.n_rows + sms - 1) / sms);
+        const int smem = int(warps) * (p.part_vecs * 16 + int(sizeof(Short)));
+        const int64_t resident = std::min<int64_t>(kShortResident * kShortWarps / warps, kSmemOfSm / (smem + 1024));
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(unsigned(std::min((p.rows.n_rows + warps - 1) / warps, resident * sms)));
+        cfg.blockDim = dim3(unsigned(warps) * 32);
+        cfg.dynamicSmemBytes = size_t(smem);
+        cfg.stream = stream;
+        return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
+    }
     const int64_t slots = 2 * int64_t(sms);
     // parts of a row: as many as give every place on the GPU one, where rows are few; not so small that their joining is
     // what takes the time, and so many that their keys fit the list

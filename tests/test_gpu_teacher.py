@@ -172,6 +172,43 @@ def test_top(sampler, shape):
     _check_top(got, x, n, tokens, T, weight)
 
 
+@pytest.mark.parametrize("V", [1, 2, 31, 127, 128, 257, 500, 1025, 4095, 4096, 4103, 8185, 8186, 8192, 8200])
+@pytest.mark.parametrize("n", [1, 8, 128])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_top_short_rows(sampler, V, n, kind):
+    """Rows that one warp takes, and a little longer ones; they begin anywhere, and some are flat, or nearly so."""
+    rng = np.random.default_rng(V + n)
+    rows = 1300 if V < 600 else 170
+    x = rng.standard_normal((rows, V)) * rng.choice([0.001, 1.0, 30.0], (rows, 1))
+    x[rng.random((rows, V)) < 0.02] = -np.inf
+    x[3], x[5, V // 2:], x[7] = 0.25, -np.inf, rng.integers(0, 2, V)
+    x = _round(x, kind)
+    weight = (rng.random(rows) < 0.9).astype(np.float32)
+    x[weight == 0] = np.nan
+    T = rng.uniform(0.5, 1.6, rows).astype(np.float32)
+    tokens = rng.integers(0, V, rows).astype(np.int32)
+    got = _run_top(sampler, x, kind, n, 1 + V % 2, V % 5, tokens, T, weight, n != 8)
+    some = np.concatenate([np.arange(min(rows, 160)), np.arange(rows - 10, rows)])
+    _check_top({k: v[some] for k, v in got.items()}, x[some], n, tokens[some], T[some], weight[some])
+
+
+# parts of rows that leave more keys than are ranked at once
+@pytest.mark.parametrize("rows,V,n", [(6, 157971, 18), (17, 60001, 99), (2, 262144, 128), (3, 100000, 12), (60, 50000, 65)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("order", ["random", "one part", "flat", "few"])
+def test_top_joined_parts(sampler, rows, V, n, kind, order):
+    rng = np.random.default_rng(V + n)
+    x = rng.standard_normal((rows, V))
+    if order == "one part":  # all that are wanted, and more, are next to each other
+        x[:, V // 3:V // 3 + 4 * n] += 20
+    elif order == "flat":
+        x = rng.integers(0, 2, (rows, V)) * 0.5
+    elif order == "few":  # parts with fewer than n
+        x = np.where(rng.random((rows, V)) < 300 / V, x, -np.inf)
+    x = _round(x, kind)
+    _check_top(_run_top(sampler, x, kind, n), x, n)
+
+
 @pytest.mark.parametrize("V,n", [(300, 128), (9000, 5), (40000, 128), (151936, 64)])
 @pytest.mark.parametrize("kind", ["bf16", "f32"])
 @pytest.mark.parametrize("rows", [6, 700])

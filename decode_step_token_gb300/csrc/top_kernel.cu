@@ -61,7 +61,7 @@ constexpr int kClosable = 32 * kLane;            // keys of a list that it takes
 constexpr int kMost = SAMPLER_MAX_ALTERNATIVES;
 constexpr int kCap = 512;                       // keys in a list
 constexpr int kMaxToken = 262143;
-constexpr int kMaxTopParts = 32;                // of a row: the lanes of a warp
+constexpr int kMaxTopParts = 8;                 // of a row
 constexpr float kLostUnit = 1099511627776.f;    // 2^40
 
 // What the closer is asked for: to cut a list down, to close a row, or to end.
@@ -976,8 +976,8 @@ __device__ __noinline__ int join_parts(const TopParams& P, int64_t r, uint32_t a
     if (flags) return flags & 2 ? -1 : -2;
     if (count > uint32_t(kConsumers)) {
         // More than are ranked at once. A bar for them all: of the first of each part's (which are in order), as many as
-        // there are threads, the n-th. What does not reach it is lost. (6 rows of 157971 bf16 in 28 parts, n = 18: ? us in
-        // place of 31 by bisection.)
+        // there are threads, the n-th. What does not reach it is lost. (17 rows of 18557 bf16 in five parts, n = 99: 18 us
+        // in place of 28 by bisection.)
         const uint32_t each = uint32_t(kConsumers / parts), p = uint32_t(tid) / each, i = uint32_t(tid) % each;
         uint32_t before = 0;
         for (uint32_t k = 0; k < p && k < uint32_t(parts); ++k) before += uint32_t(S.part_count[k]);
@@ -1692,10 +1692,11 @@ int top_launch(const TopParams& params, int sms, TopGrants* grants, cudaStream_t
         return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
     }
     const int64_t slots = 2 * int64_t(sms);
-    // parts of a row: as many as give every place on the GPU one, where rows are few; not so small that their joining is
-    // what takes the time, and so many that their keys fit the list
+    // parts of a row, where rows are few: eight at most, of two chunks at least, as their joining takes as long as some
+    // chunks do (32 of 4 KB, 32 x 151936 bf16 and n = 20: 18.2 for 16.4 us; 1 row: 21.2 for 15.1; 1 x 16384: 13.4 for 7.9
+    // in one part), and so many that their keys fit the list
     int64_t parts = std::max<int64_t>(1, slots / p.rows.n_rows);
-    parts = std::min({parts, int64_t(kMaxTopParts), int64_t(kCap / p.top.top_n), std::max<int64_t>(1, vecs / 256)});
+    parts = std::min({parts, int64_t(kMaxTopParts), int64_t(kCap / p.top.top_n), std::max<int64_t>(1, vecs / (2 * kChunkVecs))});
     if (p.rows.n_rows * parts > kTopUnits) parts = 1;
     p.part_vecs = int((vecs + parts - 1) / parts);
     p.parts = int((vecs + p.part_vecs - 1) / p.part_vecs);

@@ -685,12 +685,14 @@ int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, 
     const bool bf16 = p.rows.dtype == SAMPLER_DTYPE_BF16, grad = p.rows.out_grad != nullptr;
     const int per = bf16 ? 8 : 4;
     const int64_t vecs = (p.rows.vocab + 2 * per - 2) / per;  // the most that a row touches, wherever it starts
-    // CTAs of a cluster: so many that three buffers of a part fit (one is filled while two rows are in hand), and more,
-    // of 4 KB at least, where rows are too few for the SMs
+    // CTAs of a cluster: so many that two buffers of a part fit, in fp32 three (bf16, where the instructions bound it, loses
+    // more by smaller parts than it waits for its loads: 1000 x 151936 180 us with two of 76 KB, 208 with more of 38; fp32
+    // waits: 2000 x 40000 164 us with two of 80 KB, 144 with four of 40); and more, of 4 KB at least, where rows are too
+    // few for the SMs
     auto part_of = [&](int parts) { return int((vecs + parts - 1) / parts); };
     auto fits = [&](int parts, int buffers) { return smem_of(part_of(parts), buffers, parts) <= kSmem; };
     int parts = 1;
-    while (parts < kMaxParts && !fits(parts, 3)) parts *= 2;
+    while (parts < kMaxParts && !fits(parts, bf16 ? 2 : 3)) parts *= 2;
     while (parts < kMaxParts && p.rows.n_rows * parts < sms && part_of(2 * parts) >= 256) parts *= 2;
     p.part_vecs = part_of(parts);
     p.buffers = 2;

@@ -109,15 +109,16 @@ def _micro_types():
 
 def _scales(name: str, t, rows: int, cols: int, block: int, device: int) -> int:
     """Address of the scales of a matrix in 4 bits."""
-    need = sampler_micro_scale_bytes(rows, cols, block)
-    if need < 0:
+    if block != 16 and block != 32:
         raise ValueError(f"{name}: no scales for blocks of {block} in {rows} x {cols}")
+    # (sampler_micro_scale_bytes, without a call of the library, which checks the sizes itself)
+    need = (rows + 127) // 128 * (((cols + block - 1) // block + 3) // 4) * 512
+    if t.dtype in _micro_types()[1] and t.get_device() == device and t.numel() >= need and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype not in _micro_types()[1]:
         raise TypeError(f"{name} must be one of {_micro_types()[1]}, not {t.dtype}")
     _on_device(name, t, device)
-    if not t.is_contiguous() or t.numel() < need:
-        raise ValueError(f"{name} must be {need} contiguous bytes, not {tuple(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be {need} contiguous bytes, not {tuple(t.shape)}")
 
 
 def _vector(name: str, t, n: int, dtype, device: int) -> Optional[int]:

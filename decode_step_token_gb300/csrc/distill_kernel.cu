@@ -19,11 +19,11 @@
 //              before pass 1; take their logits from the buffer and put their share of the list's sums into all CTAs of
 //              the cluster; combine what all have put, work out the row's factors, write the row's outputs, and put the
 //              list's own gradients into the buffer in their logits' place;
-//   consumers  (sixteen) pass 1: the running reference and sum of what is not marked; pass 2: the gradient, marked
+//   consumers  (sixteen, of short rows four) pass 1: the running reference and sum of what is not marked; pass 2: the gradient, marked
 //              elements as they now are in the buffer. A row's pass 1 comes before the pass 2 of the row before it, so
 //              that the join and the closer's work run under it.
 //
-// One CTA an SM. 4096 x 128000 bf16 with gradient, lists of 64, 0.9 of the rows counted: 379 us, 0.78 of the copy rate
+// One CTA an SM (of short rows three). 4096 x 128000 bf16 with gradient, lists of 64, 0.9 of the rows counted: 379 us, 0.78 of the copy rate
 // over what has to move. Two CTAs of eight consumers an SM, with parts of half the size and twice as many: 475 us (twice
 // the joins and closers' turns of a row). What bounds it now is the consumers' instructions, which take 0.68 of the issue
 // slots: an exponential and packed arithmetic around it for each element in each pass.
@@ -43,19 +43,24 @@ namespace distill {
 
 using namespace rows;
 
-constexpr int kWarps = 16;
-constexpr int kConsumers = kWarps * 32;
-constexpr int kProducer = kWarps, kCloser = kWarps + 1;
-constexpr int kClosers = 2;                  // warps, of which each takes every other row
-constexpr int kThreads = kConsumers + 32 + 32 * kClosers;
+constexpr int kLongWarps = 16, kShortWarps = 4;  // consumers of a CTA, one or three on an SM
+constexpr int kClosers = 2;                      // warps, of which each takes every other row
 constexpr int kVecs = 4;                     // vectors that a consumer folds at once
-constexpr int kStep = kConsumers * kVecs;
 constexpr int kMaxBuffers = 4;
 constexpr int kMaxParts = 16;                // CTAs of a cluster
 constexpr int kMaps = 3;                     // rows whose tokens are marked
 constexpr int kSums = 4;                     // rows whose sums are in shared memory
 constexpr int kHeld = SAMPLER_MAX_ALTERNATIVES / 32;  // of a list in each of the closer's lanes
-constexpr int kSmem = 226 * 1024;           // of a CTA, one on an SM
+
+// What follows from a CTA's number of consumer warps.
+template <int kWarps>
+struct Shape {
+    static constexpr int kConsumers = kWarps * 32;
+    static constexpr int kThreads = kConsumers + 32 + 32 * kClosers;
+    static constexpr int kStep = kConsumers * kVecs;  // vectors that they take at once
+    static constexpr int kResident = kWarps == kShortWarps ? 3 : 1;
+    static constexpr int kSmem = (kResident == 1 ? 226 : 75) * 1024;
+};
 constexpr uint64_t kSettleNs = 100000;       // in which what is on its way to shared memory lands
 
 // What a CTA's closer puts into all CTAs: sums of the list's tokens in its part.
@@ -86,16 +91,23 @@ struct Shared {
     uint64_t join[kSums], closed[kSums];
     RowQueue queue;
     Factor factor[kSums];
-    double scratch[kThreads / 32];
+    double scratch[kLongWarps + 1 + kClosers];
     uint32_t flag, failed;  // failed: a wait of this cluster gave up
 };
 
 // The buffers, the consumers' sums [kSums][parts * kWarps], the closers' [kSums][parts], the maps [kMaps][part_vecs] and
 // Shared.
-__host__ __device__ constexpr int map_bytes(int part_vecs) { return (part_vecs + kStep - 1) / kStep * kStep; }
+template <int kWarps>
+__host__ __device__ constexpr int map_bytes(int part_vecs)
+{
+    constexpr int kStep = Shape<kWarps>::kStep;
+    return (part_vecs + kStep - 1) / kStep * kStep;
+}
+
+template <int kWarps>
 constexpr int smem_of(int part_vecs, int buffers, int parts)
 {
-    return buffers * part_vecs * 16 + kSums * parts * (kWarps * 16 + int(sizeof(ListSums))) + kMaps * map_bytes(part_vecs) +
+    return buffers * part_vecs * 16 + kSums * parts * (kWarps * 16 + int(sizeof(ListSums))) + kMaps * map_bytes<kWarps>(part_vecs) +
            int(sizeof(Shared));
 }
 
@@ -115,7 +127,7 @@ __device__ __forceinline__ void write_row(const DistillParams& P, int64_t r, flo
 
 // A wait of this cluster gave up. Which of its rows were done with is not known, so all of them are written again, by all
 // CTAs after the last of them has come to its end: those that count as TIMEOUT with NaN, the others as ever.
-template <typename T, bool kGrad>
+template <typename T, bool kGrad, int kThreads>
 __device__ __noinline__ void abandon(const DistillParams& P, uint32_t q, uint32_t n_clusters, uint32_t parts, uint32_t rank)
 {
     // copies, and sums put into this CTA, that nobody has waited for land before it may exit
@@ -168,7 +180,12 @@ __device__ __forceinline__ void pair_warp(Pair& a)
 }
 
 // Where the byte of a part's vector i is in a map: those of the vectors that a thread takes at once lie side by side.
-__device__ __forceinline__ int map_place(int i) { return (i & ~(kStep - 1)) | (i & (kConsumers - 1)) * kVecs | (i / kConsumers & (kVecs - 1)); }
+template <int kWarps>
+__device__ __forceinline__ int map_place(int i)
+{
+    constexpr int kStep = Shape<kWarps>::kStep, kConsumers = Shape<kWarps>::kConsumers;
+    return (i & ~(kStep - 1)) | (i & (kConsumers - 1)) * kVecs | (i / kConsumers & (kVecs - 1));
+}
 
 // Marked elements of a vector become -inf, or those of `from`.
 template <typename T>
@@ -194,10 +211,10 @@ __device__ __forceinline__ void blend<uint16_t>(uint4& v, const uint4& from, uin
     word(v.w, from.w, bits >> 6);
 }
 
-// Whether some of the kStep vectors from `at` on of a row's span are partly beside the row.
-__device__ __forceinline__ bool ragged(const RowSpan& span, int end, int at, int per)
+// Whether some of the `step` vectors from `at` on of a row's span are partly beside the row.
+__device__ __forceinline__ bool ragged(const RowSpan& span, int end, int at, int per, int step)
 {
-    return (at == 0 && span.head != 0) || (at + kStep >= span.count && end % per != 0);
+    return (at == 0 && span.head != 0) || (at + step >= span.count && end % per != 0);
 }
 
 template <typename T>
@@ -207,9 +224,12 @@ __device__ __forceinline__ uint4 nothing()
     return make_uint4(w, w, w, w);
 }
 
-template <typename T, bool kGrad>
-__global__ void __launch_bounds__(kThreads, 1) distill_kernel(const __grid_constant__ DistillParams P)
+template <typename T, bool kGrad, int kWarps>
+__global__ void __launch_bounds__(Shape<kWarps>::kThreads, Shape<kWarps>::kResident)
+    distill_kernel(const __grid_constant__ DistillParams P)
 {
+    constexpr int kConsumers = Shape<kWarps>::kConsumers, kThreads = Shape<kWarps>::kThreads, kStep = Shape<kWarps>::kStep;
+    constexpr int kProducer = kWarps, kCloser = kWarps + 1;
     constexpr int kPer = Elems<T>::kPer;
     extern __shared__ __align__(128) unsigned char smem[];
     const sampler_rows_t& a = P.rows;
@@ -222,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) distill_kernel(const __grid_const
     float4* sums = reinterpret_cast<float4*>(smem + buffers * buffer_bytes);
     ListSums* lists = reinterpret_cast<ListSums*>(sums + kSums * parts * kWarps);
     unsigned char* maps = reinterpret_cast<unsigned char*>(lists + kSums * parts);
-    Shared& S = *reinterpret_cast<Shared*>(maps + kMaps * map_bytes(P.part_vecs));
+    Shared& S = *reinterpret_cast<Shared*>(maps + kMaps * map_bytes<kWarps>(P.part_vecs));
 
     if (tid == 0) {
         for (int i = 0; i < kMaxBuffers; ++i) {
@@ -240,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) distill_kernel(const __grid_const
         S.failed = 0;
         fence_mbar_init();
     }
-    for (int i = tid; i < kMaps * map_bytes(P.part_vecs) / 4; i += kThreads) reinterpret_cast<uint32_t*>(maps)[i] = 0;
+    for (int i = tid; i < kMaps * map_bytes<kWarps>(P.part_vecs) / 4; i += kThreads) reinterpret_cast<uint32_t*>(maps)[i] = 0;
     cluster_sync();
 
     const int first_vec = int(rank) * P.part_vecs;
@@ -345,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1) distill_kernel(const __grid_const
             }
             __syncwarp();
             if (!wait(&S.unmarked[map.at], map.phase ^ 1u, P.wait_ns)) return false;
-            unsigned char* bits = maps + map.at * map_bytes(P.part_vecs);
+            unsigned char* bits = maps + map.at * map_bytes<kWarps>(P.part_vecs);
             for (int i = lane; i < o.count; i += 32) {
-                const int at = list[i].at, byte = map_place(at / kPer);
+                const int at = list[i].at, byte = map_place<kWarps>(at / kPer);
                 const uint32_t bit = 1u << (8 * (byte & 3) + at % kPer);
                 if (atomicOr(reinterpret_cast<uint32_t*>(bits) + byte / 4, bit) & bit) flags |= kBadList;  // twice
             }
@@ -554,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1) distill_kernel(const __grid_const
             const float c = item.c;
             if (!wait(&S.full[buf1.at], buf1.phase, P.wait_ns)) return -1;
             const uint4* in = reinterpret_cast<const uint4*>(smem + buf1.at * buffer_bytes);
-            unsigned char* bits = maps + map1.at * map_bytes(P.part_vecs);
+            unsigned char* bits = maps + map1.at * map_bytes<kWarps>(P.part_vecs);
             Stats st = stats_empty();
             bool bad = false;
             for (int i0 = 0; i0 < n; i0 += kStep) {
@@ -566,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) distill_kernel(const __grid_const
                     v[k] = nothing<T>();
                     if (i < n) v[k] = in[i];
                 }
-                if (ragged(span, end, first_vec + i0, kPer))
+                if (ragged(span, end, first_vec + i0, kPer, kStep))
 #pragma unroll
                     for (int k = 0; k < kVecs; ++k) {
                         const int at = (first_vec + i0 + k * kConsumers + tid) * kPer;
@@ -611,12 +631,12 @@ __global__ void __launch_bounds__(kThreads, 1) distill_kernel(const __grid_const
                 const bool whole = ((reinterpret_cast<uintptr_t>(g) - reinterpret_cast<uintptr_t>(x)) & 15u) == 0;
                 const int token_vec = f.token == kNoToken ? -1 : (f.token + span.head) / kPer - first_vec;
                 const uint4* in = reinterpret_cast<const uint4*>(smem + buf2.at * buffer_bytes);
-                unsigned char* bits = maps + map2.at * map_bytes(P.part_vecs);
+                unsigned char* bits = maps + map2.at * map_bytes<kWarps>(P.part_vecs);
                 const int end = span.head + vocab;
                 for (int i0 = 0; i0 < n; i0 += kStep) {
                     uint32_t* marks = reinterpret_cast<uint32_t*>(bits + i0) + tid;
                     const uint32_t marked = *marks;
-                    if (whole && !ragged(span, end, first_vec + i0, kPer) && !(token_vec >= i0 && token_vec < i0 + kStep)) {
+                    if (whole && !ragged(span, end, first_vec + i0, kPer, kStep) && !(token_vec >= i0 && token_vec < i0 + kStep)) {
                         uint4* to = reinterpret_cast<uint4*>(g - span.head) + first_vec + i0 + tid;
                         uint4 v[kVecs], y[kVecs];
 #pragma unroll
@@ -669,7 +689,7 @@ __global__ void __launch_bounds__(kThreads, 1) distill_kernel(const __grid_const
     }
     __syncwarp();
     cluster_sync();
-    if (S.failed) abandon<T, kGrad>(P, q, n_clusters, parts, rank);
+    if (S.failed) abandon<T, kGrad, kThreads>(P, q, n_clusters, parts, rank);
     if (rank == 0 && last_block(P.ws.ticket, n_clusters, &S.flag)) {
         const double loss = sum_terms<kThreads>(P.ws.terms, a.n_rows, S.scratch);
         if (tid == 0) D.out_loss[0] = float(loss);
@@ -678,10 +698,12 @@ __global__ void __launch_bounds__(kThreads, 1) distill_kernel(const __grid_const
 
 }  // namespace distill
 
-int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, cudaStream_t stream)
+namespace distill {
+
+template <int kWarps>
+int launch(DistillParams& p, int sms, DistillOccupancy* occ, cudaStream_t stream)
 {
-    using namespace distill;
-    DistillParams p = params;
+    using S = Shape<kWarps>;
     const bool bf16 = p.rows.dtype == SAMPLER_DTYPE_BF16, grad = p.rows.out_grad != nullptr;
     const int per = bf16 ? 8 : 4;
     const int64_t vecs = (p.rows.vocab + 2 * per - 2) / per;  // the most that a row touches, wherever it starts
@@ -690,19 +712,19 @@ int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, 
     // waits: 2000 x 40000 164 us with two of 80 KB, 144 with four of 40); and more, of 4 KB at least, where rows are too
     // few for the SMs
     auto part_of = [&](int parts) { return int((vecs + parts - 1) / parts); };
-    auto fits = [&](int parts, int buffers) { return smem_of(part_of(parts), buffers, parts) <= kSmem; };
+    auto fits = [&](int parts, int buffers) { return smem_of<kWarps>(part_of(parts), buffers, parts) <= S::kSmem; };
     int parts = 1;
-    while (parts < kMaxParts && !fits(parts, bf16 ? 2 : 3)) parts *= 2;
+    while (parts < kMaxParts && !fits(parts, bf16 || kWarps == kShortWarps ? 2 : 3)) parts *= 2;
     while (parts < kMaxParts && p.rows.n_rows * parts < sms && part_of(2 * parts) >= 256) parts *= 2;
     p.part_vecs = part_of(parts);
     p.buffers = 2;
     while (p.buffers < kMaxBuffers && fits(parts, p.buffers + 1)) ++p.buffers;
     if (!fits(parts, 2)) return SAMPLER_ERR_TOO_LARGE;  // (no row of the vocabularies that handles take)
-    const auto kernel = bf16 ? grad ? distill_kernel<uint16_t, true> : distill_kernel<uint16_t, false>
-                             : grad ? distill_kernel<float, true> : distill_kernel<float, false>;
+    const auto kernel = bf16 ? grad ? distill_kernel<uint16_t, true, kWarps> : distill_kernel<uint16_t, false, kWarps>
+                             : grad ? distill_kernel<float, true, kWarps> : distill_kernel<float, false, kWarps>;
     cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = size_t(kSmem);
+    cfg.blockDim = dim3(S::kThreads);
+    cfg.dynamicSmemBytes = size_t(S::kSmem);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -710,10 +732,10 @@ int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, 
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     const int size = parts == 1 ? 0 : parts == 2 ? 1 : parts == 4 ? 2 : parts == 8 ? 3 : 4;
-    int& resident = occ->clusters[bf16][grad][size];
+    int& resident = occ->clusters[kWarps == kShortWarps][bf16][grad][size];
     if (resident < 1) {  // once for each kernel and shape of the launch of a handle
         const void* k = reinterpret_cast<const void*>(kernel);
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) != cudaSuccess ||
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess ||
             (parts > 8 && cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
             return SAMPLER_ERR_CUDA;
         cfg.gridDim = dim3(unsigned(parts));
@@ -723,6 +745,20 @@ int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, 
     }
     cfg.gridDim = dim3(unsigned(std::min<int64_t>(p.rows.n_rows, resident) * parts));
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
+}
+
+}  // namespace distill
+
+int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, cudaStream_t stream)
+{
+    using namespace distill;
+    DistillParams p = params;
+    // Rows of 32 KB at most go to CTAs of four consumer warps, of which an SM holds three: a row's fixed work, the chain from
+    // its sums to its factors, is then under way for three times as many rows. With gradient, bf16, us by four and by sixteen
+    // warps: 4096 x 1000 52 and 84, 4096 x 8000 74 and 94, 4096 x 16000 99 and 104, 4096 x 24000 138 and 131; fp32:
+    // 4 x 1024 8.7 and 10.2, 4096 x 8000 80 and 90.
+    const int64_t bytes = p.rows.vocab * (p.rows.dtype == SAMPLER_DTYPE_BF16 ? 2 : 4);
+    return bytes <= 32 * 1024 ? launch<kShortWarps>(p, sms, occ, stream) : launch<kLongWarps>(p, sms, occ, stream);
 }
 
 }  // namespace dst

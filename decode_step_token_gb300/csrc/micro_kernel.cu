@@ -3,10 +3,10 @@
 //
 // Every step is exact or one rounding, so that the codes follow from the
 // definition bit for bit: the row's scale is a power of two, a block's scale has
-// at most four digits, and a quotient is the correctly rounded one. (A product
-// with the rounded reciprocal would put many of the quotients that lie halfway
-// between two codes on the wrong side: bf16 values over a scale of four digits
-// often do.)
+// at most four digits, and a quotient is on the exact one's side of every tie
+// between codes. (A product with the rounded reciprocal would put many of the
+// quotients that are such a tie on a side: bf16 values over a scale of four digits
+// often are.)
 //
 // A block's codes need the block's largest magnitude and, for blocks of 16, the
 // row's, so a row stays in registers: 16 neighbouring values in each thread, one
@@ -17,10 +17,10 @@
 // row are stored as one word.
 //
 // What bounds both ways is memory, for blocks of 16 the instructions too: 128000 x
-// 4096 bf16 takes 232 us with blocks of 32 and 318 of 16 (0.84 and 0.62 of the copy
+// 4096 bf16 takes 232 us with blocks of 32 and 302 of 16 (0.84 and 0.66 of the copy
 // rate), and 240 and 232 back (0.81 and 0.85). A value at a time as fp32, with one row
 // in hand, they were 287 and 423; a vector a thread back, 369 and 386. Rows of 1000
-// (20000 of them: 19 and 27 us, 0.39 and 0.28) leave half of a group's threads without
+// (20000 of them: 20 and 25 us, 0.37 and 0.30) leave half of a group's threads without
 // a chunk.
 #include <cuda_runtime.h>
 
@@ -189,6 +189,22 @@ __device__ __forceinline__ uint32_t largest(const Raw<uint16_t>& x)
     return max(m & 0xffff0000u, m << 16);
 }
 
+__device__ __forceinline__ float reciprocal(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// x / d by a reciprocal that may be a unit off, with one step on the remainder (Newton): off by 2^-45 before it is
+// rounded. What it is rounded to, a code of few digits, is then the exact quotient's: a tie between two codes comes out as
+// itself, and x and d, of 24 digits and of four, have quotients on either side of one that are 2^-25 of it away at least.
+__device__ __forceinline__ float quotient(float x, float d, float inv)
+{
+    const float y = x * inv;
+    return fmaf(fmaf(-d, y, x), inv, y);
+}
+
 // What a call's shape makes of it. group: threads to a row.
 struct Plan {
     int group, chunks, tiles;  // chunks of 16 values, and tiles of scales, in a row
@@ -210,12 +226,12 @@ __device__ __forceinline__ uint2 encode(const Raw<T>& x, uint32_t most, int g, u
 #pragma unroll
         for (int j = 0; j < kPer / 2; ++j) q[j] = times(pair_at(x, j), two(up, up));
     } else {
-        code = finite ? e4m3_code(__fdiv_rn(__uint_as_float(most), 6.f) * power(-g)) : 0x7fu;
+        // (m / 2^g, exact where it is not far below the least scale, over 6)
+        code = finite ? e4m3_code(quotient(__uint_as_float(most) * power(-g), 6.f, 1.f / 6.f)) : 0x7fu;
         const float unit = (finite ? e4m3_value(code) : 0.f) * power(g);
-        const uint32_t i = __float_as_uint(unit > 0.f ? __fdiv_rn(1.f, unit) : 0.f), u = __float_as_uint(-unit);
+        const uint32_t i = __float_as_uint(unit > 0.f ? reciprocal(unit) : 0.f), u = __float_as_uint(-unit);
         const Two inv = two(i, i), less = two(u, u);
-        // the quotient, correctly rounded: the product with the rounded reciprocal and one step on its remainder
-        // (Markstein)
+        // as quotient(), two at a time
 #pragma unroll
         for (int j = 0; j < kPer / 2; ++j) {
             const Two v = pair_at(x, j), y = times(v, inv);

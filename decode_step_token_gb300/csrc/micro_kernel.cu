@@ -17,7 +17,7 @@
 // row are stored as one word.
 //
 // What bounds both ways is memory, for blocks of 16 the instructions too: 128000 x
-// 4096 bf16 takes 232 us with blocks of 32 and 302 of 16 (0.84 and 0.66 of the copy
+// 4096 bf16 takes 220 us with blocks of 32 and 300 of 16 (0.89 and 0.66 of the copy
 // rate), and 240 and 232 back (0.81 and 0.85). A value at a time as fp32, with one row
 // in hand, they were 287 and 423; a vector a thread back, 369 and 386. Rows of 1000
 // (20000 of them: 20 and 25 us, 0.37 and 0.30) leave half of a group's threads without
@@ -376,15 +376,24 @@ cudaError_t launch_quantize(const sampler_micro_t& q, int sms, cudaStream_t stre
     p.group = 8;
     while (p.group < kThreads && p.group < chunks) p.group *= 2;
     const int held = chunks <= p.group ? 1 : chunks <= 2 * kThreads ? 2 : chunks <= 4 * kThreads ? 4 : 0;
-    // two rows in hand where there are more than eight blocks' worth for each SM, for the loads under way: the same time
-    // for blocks of 32 as with one, a tenth less for blocks of 16; with fewer rows half of the blocks would not be there
-    const bool two_rows = held == 1 && p.padded * p.group > int64_t(sms) * 8 * kThreads;
-    const int64_t per = kThreads / p.group * (two_rows ? 2 : 1);
+    // Rows in hand, for the loads under way: two where there are more than eight blocks' worth for each SM and they lie in
+    // whole vectors, four of bf16 whose blocks need no row's largest, where every thread has a chunk. Measured, us by one,
+    // two and four:
+    //   128000 x 4096 bf16    336  300  304, blocks of 32: 271  233  220
+    //   64000 x 4096 fp32     210  199  244, blocks of 32: 189  183  232
+    //   150000 x 1000 bf16    124  126  150, blocks of 32: 105   97  103
+    //   20001 x 1001 fp32      27   31   42
+    constexpr bool kFour = sizeof(T) == 2 && kBlock == 32;
+    const int rows = held != 1 || !p.vec_in || p.padded * p.group <= int64_t(sms) * 8 * kThreads ? 1
+                     : kFour && chunks == p.group                                               ? 4
+                                                                                                : 2;
+    const int64_t per = kThreads / p.group * rows;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(unsigned((p.padded + per - 1) / per));
     cfg.blockDim = dim3(kThreads);
     cfg.stream = stream;
-    const auto kernel = two_rows    ? quantize_kernel<T, kBlock, 1, 2>
+    const auto kernel = rows == 4   ? quantize_kernel<T, kBlock, 1, kFour ? 4 : 2>
+                        : rows == 2 ? quantize_kernel<T, kBlock, 1, 2>
                         : held == 1 ? quantize_kernel<T, kBlock, 1, 1>
                         : held == 2 ? quantize_kernel<T, kBlock, 2, 1>
                         : held == 4 ? quantize_kernel<T, kBlock, 4, 1>

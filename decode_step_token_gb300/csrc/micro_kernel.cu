@@ -18,7 +18,7 @@
 //
 // What bounds both ways is memory, for blocks of 16 the instructions too: 128000 x
 // 4096 bf16 takes 220 us with blocks of 32 and 300 of 16 (0.89 and 0.66 of the copy
-// rate), and 240 and 232 back (0.81 and 0.85). A value at a time as fp32, with one row
+// rate), and 222 back from either (0.88). A value at a time as fp32, with one row
 // in hand, they were 287 and 423; a vector a thread back, 369 and 386. Rows of 1000
 // (20000 of them: 20 and 25 us, 0.37 and 0.30) leave half of a group's threads without
 // a chunk.
@@ -85,8 +85,9 @@ template <int kBlock>
 __device__ __forceinline__ float scale_value(uint32_t code)
 {
     if (kBlock == 16) return e4m3_value(code);
-    if (code == 0xffu) return __int_as_float(0x7fc00000);
-    return code == 0u ? __int_as_float(0x00400000) : __int_as_float(code << 23);
+    uint32_t w;  // as bf16, which has all of them
+    asm("cvt.rn.bf16x2.ue8m0x2 %0, %1;" : "=r"(w) : "h"(uint16_t(code)));
+    return __uint_as_float(w << 16);
 }
 
 // 16 values of a row as they lie in memory.
@@ -504,8 +505,14 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const sampler_micro_rows
 #pragma unroll
         for (int j = 0; j < kVec; j += 2) {
             const float2 y = values2(codes[k] >> 4 * j & 0xffu);
-            x[j] = y.x * (kCut && j >= change ? after : unit);
-            x[j + 1] = y.y * (kCut && j + 1 >= change ? after : unit);
+            if (kCut) {
+                x[j] = y.x * (j >= change ? after : unit);
+                x[j + 1] = y.y * (j + 1 >= change ? after : unit);
+            } else {
+                const Two z = times(two(__float_as_uint(y.x), __float_as_uint(y.y)), two(__float_as_uint(unit), __float_as_uint(unit)));
+                x[j] = __uint_as_float(uint32_t(z));
+                x[j + 1] = __uint_as_float(uint32_t(z >> 32));
+            }
         }
         const uint4 y = Out<T>::pack(x);
         if (vec_out && (!kCut || col >= 0) && col + kVec <= cols) {

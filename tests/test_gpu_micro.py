@@ -344,6 +344,81 @@ def test_waits_that_give_up(rows):
         _close(out.double().cpu().numpy(), want, mag, 512, "f32")
 
 
+def _pair_case(sampler, block, nan=False):
+    """So much that pairs of CTAs take it, of 300 rows by 20000 tokens."""
+    import torch
+
+    rows, V, K = 300, 20000, 2048
+    gen = torch.Generator(device="cuda:0").manual_seed(block)
+    hidden = torch.randn((rows, K), generator=gen, device="cuda:0")
+    weight = torch.randn((V, K), generator=gen, device="cuda:0") / K ** 0.5
+    if nan:
+        hidden[2, 100], hidden[299, 2047], weight[300, 0], weight[19999, 319] = (float("nan"), float("inf"), float("-inf"),
+                                                                               float("nan"))
+    ops = dict(block=block)
+    for name, src in (("hidden", hidden), ("weight", weight)):
+        ops[name], ops[name + "_scale"], ops[name + "_row_scale"] = _quantize(sampler, src, block)
+    return ops, torch.empty((rows, V), device="cuda:0")
+
+
+@pytest.mark.parametrize("block", [16, 32])
+def test_pairs_of_ctas_leave_nan_in_its_rows(sampler, block):
+    import torch
+
+    ops, out = _pair_case(sampler, block, nan=True)
+    sampler.lm_head_micro(**ops, logits=out)
+    want = torch.zeros_like(out, dtype=torch.bool)
+    want[[2, 299]], want[:, [300, 19999]] = True, True
+    assert torch.equal(torch.isnan(out), want) and torch.isfinite(out[~want]).all()
+
+
+def test_pairs_of_ctas_again_and_in_a_graph(sampler):
+    """The same bits from every call, on two handles and streams at once, and from a graph, in which the sampler follows."""
+    import torch
+
+    import decode_step_token_gb300 as d
+
+    ops, out = _pair_case(sampler, 16)
+    sampler.lm_head_micro(**ops, logits=out)
+    first = out.clone()
+    with d.Sampler(max_rows=512, max_vocab=20000) as other:
+        outs = [torch.empty_like(out) for _ in range(2)]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for s, stream, to in zip((sampler, other), streams, outs):
+                with torch.cuda.stream(stream):
+                    s.lm_head_micro(**ops, logits=to)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], first) and torch.equal(outs[1], first)
+    small = {k: v if k.startswith("weight") or k == "block" else v[:256] if k != "hidden_scale" else v for k, v in ops.items()}
+    temperature = torch.full((256,), 0.8, device="cuda:0")
+    tokens = torch.empty(256, dtype=torch.int32, device="cuda:0")
+    args = sampler.make_args(logits=first[:256].contiguous(), temperature=temperature, out_tokens=tokens, global_seed=3)
+    sampler.sample_ex_args(args)
+    want = tokens.clone()
+    chained = torch.empty((256, 20000), device="cuda:0")
+    args = sampler.make_args(logits=chained, temperature=temperature, out_tokens=tokens, global_seed=3)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sampler.lm_head_micro_sample_args(args, **small)
+    for _ in range(3):
+        tokens.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(chained, first[:256]) and torch.equal(tokens, want)
+
+
+def test_pairs_of_ctas_whose_waits_give_up():
+    import decode_step_token_gb300 as d
+
+    with d.Sampler(max_rows=512, max_vocab=20000, short_waits=True) as s:
+        ops, out = _pair_case(s, 16)
+        out.fill_(-7.0)
+        s.lm_head_micro(**ops, logits=out)
+        assert s.stat(d.SAMPLER_STAT_LM_HEAD_TIMEOUTS) > 0 and (out == -7).all()
+
+
 def test_argument_checks(sampler):
     import torch
 

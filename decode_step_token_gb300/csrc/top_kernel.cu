@@ -23,7 +23,8 @@
 //   A row's end: the closer again, under the next row: the exact n, in order, their
 //   logprobs and the row's outputs.
 // Few rows are cut into parts, a CTA each, which leave their n keys and sums in the
-// workspace; the part that ends last joins them, parts in order.
+// workspace; the part that ends last joins them, parts in order. Short rows are a warp's
+// each, with a kernel of their own.
 //
 // Two CTAs an SM. 4096 x 128000 bf16, n = 64: 285 us, 0.49 of the copy rate; instructions
 // bound it (issue slots 0.56 busy, and where they are not, warps wait for the few of them
@@ -1398,10 +1399,11 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
 }
 
 // ---------------------------------------------------------------- short rows
-// A warp by itself takes a row of 16 KB at most, all of it in shared memory, with the next one on its way there while the
+// A warp by itself takes a row of 32 KB at most, all of it in shared memory, with the next one on its way there while the
 // row's keys are put in order.
 constexpr int kShortWarps = 4;
-constexpr int kShortVecs = 1025;   // of a row
+constexpr int kShortVecs = 2049;   // of a row, where rows are many
+constexpr int kShortFew = 513;     // where each has a place in the other kernel
 constexpr int kShortResident = 5;  // CTAs of kShortWarps that an SM's registers hold
 constexpr int kGroups = 8;         // of a lane's vectors
 
@@ -1670,7 +1672,15 @@ int top_launch(const TopParams& params, int sms, TopGrants* grants, cudaStream_t
     const bool bf16 = p.rows.dtype == SAMPLER_DTYPE_BF16, entropy = p.rows.out_entropy != nullptr;
     const int per = bf16 ? 8 : 4;
     const int64_t vecs = (p.rows.vocab + 2 * per - 2) / per;  // the most that a row touches, wherever it starts
-    if (vecs <= kShortVecs && p.wait_ns != 0) {  // (a handle whose waits all give up takes the kernel that waits)
+    // Rows of 8 KB at most, and of 32 KB where there are more than the other kernel holds at once, are a warp's each. Measured,
+    // us by chunks and by warps (bf16, n = 64; of one row n = 20):
+    //   1 x 1000       8.9   7.5      4096 x 4096   121   38
+    //   1 x 4096       9.1   8.0      4096 x 8186   121   65
+    //   1 x 8186       7.8  10.4      4096 x 12000  131   73
+    //   100 x 4096    13.0  12.9      4096 x 16000  132  120
+    //   100 x 8186    13.6  15.4      350 x 12000    23   18
+    // (A handle whose waits all give up takes the kernel that waits.)
+    if (vecs <= (p.rows.n_rows > 2 * sms ? kShortVecs : kShortFew) && p.wait_ns != 0) {
         const auto kernel = bf16 ? entropy ? top_short_kernel<uint16_t, true> : top_short_kernel<uint16_t, false>
                                  : entropy ? top_short_kernel<float, true> : top_short_kernel<float, false>;
         bool& granted = grants->short_granted[bf16][entropy];

@@ -192,6 +192,19 @@ def test_top_short_rows(sampler, V, n, kind):
     _check_top({k: v[some] for k, v in got.items()}, x[some], n, tokens[some], T[some], weight[some])
 
 
+@pytest.mark.parametrize("rows", [300, 700])
+@pytest.mark.parametrize("V", [4089, 12001, 16376, 16384, 16385, 16400])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_top_rows_of_warps_where_there_are_many(sampler, V, kind, rows):
+    rng = np.random.default_rng(V)
+    x = rng.standard_normal((rows, V if kind == "bf16" else V // 2))
+    x[2], x[4] = np.sort(x[2]), 1.0
+    x = _round(x, kind)
+    got = _run_top(sampler, x, kind, 64, V % 2, V % 3)
+    some = np.concatenate([np.arange(24), np.arange(rows - 8, rows)])
+    _check_top({k: v[some] for k, v in got.items()}, x[some], 64)
+
+
 # parts of rows that leave more keys than are ranked at once
 @pytest.mark.parametrize("rows,V,n", [(6, 157971, 18), (17, 60001, 99), (2, 262144, 128), (3, 100000, 12), (60, 50000, 65)])
 @pytest.mark.parametrize("kind", ["bf16", "f32"])

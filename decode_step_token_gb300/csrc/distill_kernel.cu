@@ -700,6 +700,57 @@ __global__ void __launch_bounds__(Shape<kWarps>::kThreads, Shape<kWarps>::kResid
 
 namespace distill {
 
+// Clusters of `parts` CTAs that the device holds at once (asked once for each kernel of a handle); 0: an error.
+template <int kWarps, typename Kernel>
+int resident(Kernel kernel, cudaLaunchConfig_t cfg, int parts, int& known)
+{
+    if (known > 0) return known;
+    const void* k = reinterpret_cast<const void*>(kernel);
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<kWarps>::kSmem) != cudaSuccess ||
+        (parts > 8 && cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
+        return 0;
+    cudaLaunchAttribute attr = *cfg.attrs;
+    attr.val.clusterDim = {unsigned(parts), 1u, 1u};
+    cfg.attrs = &attr;
+    cfg.gridDim = dim3(unsigned(parts));
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return 0;
+    return known = n;
+}
+
+// CTAs of a cluster: those for which the turns that the rows take on the clusters the device holds, each as long as a part
+// takes, are the shortest; of equal ones the most. A turn is about 2.2 us for a part of one step of the consumers'
+// (32 KB), 3.5 for two and 4.1 for a little more, and 7.5 where there is no room for three buffers (one is filled while two
+// rows are in hand). Parts have 4 KB at least. Measured with gradient, us by parts:
+//   1200 x 128000 bf16   3 (two buffers): 178   4: 127   5: 143   6: 169   8: 181
+//   1200 x 151936 bf16   4 (two buffers): 216   5: 152   6: 170   8: 245
+//   1200 x 65000 bf16    2: 75   3: 98   4: 95
+//   800 x 100000 fp32    5 (two buffers): 157   6: 118   7: 141   8: 132
+//   800 x 151936 fp32    8 (two buffers): 266   10: 168   16: 262
+template <int kWarps, typename Kernel>
+int parts_of(Kernel kernel, const cudaLaunchConfig_t& cfg, int64_t vecs, int64_t rows, int (&known)[kMaxParts])
+{
+    using S = Shape<kWarps>;
+    int best = 0;
+    double least = 0.;
+    for (int parts = 1; parts <= kMaxParts; ++parts) {
+        const int part_vecs = int((vecs + parts - 1) / parts);
+        if (smem_of<kWarps>(part_vecs, 2, parts) > S::kSmem || (parts > 1 && part_vecs < 256)) continue;
+        const int clusters = resident<kWarps>(kernel, cfg, parts, known[parts - 1]);
+        if (clusters < 1) continue;
+        const double turn = smem_of<kWarps>(part_vecs, 3, parts) > S::kSmem ? 7.5
+                            : part_vecs <= S::kStep                         ? 2.2
+                            : part_vecs <= 2 * S::kStep                     ? 3.5
+                                                                            : 4.1;
+        const double time = turn * double((rows + clusters - 1) / clusters);
+        if (best == 0 || time <= least) {
+            best = parts;
+            least = time;
+        }
+    }
+    return best;
+}
+
 template <int kWarps>
 int launch(DistillParams& p, int sms, DistillOccupancy* occ, cudaStream_t stream)
 {
@@ -707,43 +758,32 @@ int launch(DistillParams& p, int sms, DistillOccupancy* occ, cudaStream_t stream
     const bool bf16 = p.rows.dtype == SAMPLER_DTYPE_BF16, grad = p.rows.out_grad != nullptr;
     const int per = bf16 ? 8 : 4;
     const int64_t vecs = (p.rows.vocab + 2 * per - 2) / per;  // the most that a row touches, wherever it starts
-    // CTAs of a cluster: so many that two buffers of a part fit, in fp32 three (bf16, where the instructions bound it, loses
-    // more by smaller parts than it waits for its loads: 1000 x 151936 180 us with two of 76 KB, 208 with more of 38; fp32
-    // waits: 2000 x 40000 164 us with two of 80 KB, 144 with four of 40); and more, of 4 KB at least, where rows are too
-    // few for the SMs
-    auto part_of = [&](int parts) { return int((vecs + parts - 1) / parts); };
-    auto fits = [&](int parts, int buffers) { return smem_of<kWarps>(part_of(parts), buffers, parts) <= S::kSmem; };
-    int parts = 1;
-    while (parts < kMaxParts && !fits(parts, bf16 || kWarps == kShortWarps ? 2 : 3)) parts *= 2;
-    while (parts < kMaxParts && p.rows.n_rows * parts < sms && part_of(2 * parts) >= 256) parts *= 2;
-    p.part_vecs = part_of(parts);
-    p.buffers = 2;
-    while (p.buffers < kMaxBuffers && fits(parts, p.buffers + 1)) ++p.buffers;
-    if (!fits(parts, 2)) return SAMPLER_ERR_TOO_LARGE;  // (no row of the vocabularies that handles take)
     const auto kernel = bf16 ? grad ? distill_kernel<uint16_t, true, kWarps> : distill_kernel<uint16_t, false, kWarps>
                              : grad ? distill_kernel<float, true, kWarps> : distill_kernel<float, false, kWarps>;
+    int(&known)[kMaxParts] = occ->clusters[kWarps == kShortWarps][bf16][grad];
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3(S::kThreads);
     cfg.dynamicSmemBytes = size_t(S::kSmem);
     cfg.stream = stream;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim = {unsigned(parts), 1u, 1u};
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const int size = parts == 1 ? 0 : parts == 2 ? 1 : parts == 4 ? 2 : parts == 8 ? 3 : 4;
-    int& resident = occ->clusters[kWarps == kShortWarps][bf16][grad][size];
-    if (resident < 1) {  // once for each kernel and shape of the launch of a handle
-        const void* k = reinterpret_cast<const void*>(kernel);
-        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess ||
-            (parts > 8 && cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess))
-            return SAMPLER_ERR_CUDA;
-        cfg.gridDim = dim3(unsigned(parts));
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) return SAMPLER_ERR_CUDA;
-        resident = n;
+    int parts = 1;
+    if (kWarps == kShortWarps) {
+        // short rows: one, or as many as give each SM a part where rows are few
+        while (parts < kMaxParts && p.rows.n_rows * parts < sms && vecs / (2 * parts) >= 256) parts *= 2;
+    } else {
+        parts = parts_of<kWarps>(kernel, cfg, vecs, p.rows.n_rows, known);
     }
-    cfg.gridDim = dim3(unsigned(std::min<int64_t>(p.rows.n_rows, resident) * parts));
+    if (parts < 1) return SAMPLER_ERR_CUDA;
+    const int clusters = resident<kWarps>(kernel, cfg, parts, known[parts - 1]);
+    if (clusters < 1) return SAMPLER_ERR_CUDA;
+    p.part_vecs = int((vecs + parts - 1) / parts);
+    p.buffers = 2;
+    while (p.buffers < kMaxBuffers && smem_of<kWarps>(p.part_vecs, p.buffers + 1, parts) <= S::kSmem) ++p.buffers;
+    attr.val.clusterDim = {unsigned(parts), 1u, 1u};
+    cfg.gridDim = dim3(unsigned(std::min<int64_t>(p.rows.n_rows, clusters) * parts));
     return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? SAMPLER_OK : SAMPLER_ERR_CUDA;
 }
 

@@ -199,7 +199,7 @@ struct DistillParams {
 // Clusters that the device holds at once, by the kernel's form, the logits' type, gradient and size of the cluster; 0 = not
 // asked yet.
 struct DistillOccupancy {
-    int clusters[2][2][2][5];
+    int clusters[2][2][2][16];
 };
 
 int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, cudaStream_t stream);

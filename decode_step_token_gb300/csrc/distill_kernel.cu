@@ -781,6 +781,7 @@ int launch(DistillParams& p, int sms, DistillOccupancy* occ, cudaStream_t stream
     if (clusters < 1) return SAMPLER_ERR_CUDA;
     p.part_vecs = int((vecs + parts - 1) / parts);
     p.buffers = 2;
+    if (smem_of<kWarps>(p.part_vecs, p.buffers, parts) > S::kSmem) return SAMPLER_ERR_TOO_LARGE;  // (no vocabulary of a handle's)
     while (p.buffers < kMaxBuffers && smem_of<kWarps>(p.part_vecs, p.buffers + 1, parts) <= S::kSmem) ++p.buffers;
     attr.val.clusterDim = {unsigned(parts), 1u, 1u};
     cfg.gridDim = dim3(unsigned(std::min<int64_t>(p.rows.n_rows, clusters) * parts));
@@ -793,12 +794,15 @@ int distill_launch(const DistillParams& params, int sms, DistillOccupancy* occ, 
 {
     using namespace distill;
     DistillParams p = params;
-    // Rows of 32 KB at most go to CTAs of four consumer warps, of which an SM holds three: a row's fixed work, the chain from
+    // Rows of which the shared memory of a small CTA has room for two (32 KB at most) go to CTAs of four consumer warps, of
+    // which an SM holds three: a row's fixed work, the chain from
     // its sums to its factors, is then under way for three times as many rows. With gradient, bf16, us by four and by sixteen
     // warps: 4096 x 1000 52 and 84, 4096 x 8000 74 and 94, 4096 x 16000 99 and 104, 4096 x 24000 138 and 131; fp32:
     // 4 x 1024 8.7 and 10.2, 4096 x 8000 80 and 90.
-    const int64_t bytes = p.rows.vocab * (p.rows.dtype == SAMPLER_DTYPE_BF16 ? 2 : 4);
-    return bytes <= 32 * 1024 ? launch<kShortWarps>(p, sms, occ, stream) : launch<kLongWarps>(p, sms, occ, stream);
+    const int per = p.rows.dtype == SAMPLER_DTYPE_BF16 ? 8 : 4;
+    const int64_t vecs = (p.rows.vocab + 2 * per - 2) / per;
+    const bool small = vecs <= 2049 && smem_of<kShortWarps>(int(vecs), 2, 1) <= Shape<kShortWarps>::kSmem;
+    return small ? launch<kShortWarps>(p, sms, occ, stream) : launch<kLongWarps>(p, sms, occ, stream);
 }
 
 }  // namespace dst

@@ -407,6 +407,20 @@ DISTILS = [  # rows, vocabulary, list, type, pad, shift, heat, kept, tail, coef,
     (500, 20011, 128, "f32", 0, 0, True, 1.0, True, 0.0, 0.0)]
 
 
+@pytest.mark.parametrize("rows,V,kind", [(140, 80000, "f32"), (60, 151936, "bf16"), (100, 40961, "f32"), (50, 230001, "bf16"),
+                                         (90, 151936, "f32"), (40, 262144, "f32"), (500, 16385, "bf16"), (700, 8191, "f32")])
+def test_distill_on_clusters_of_all_sizes(sampler, rows, V, kind):
+    """More rows than there are clusters, of sizes that are no powers of two among them; the same bits again."""
+    import torch
+
+    b = Batch(V, rows, V, 33, kind, pad=V % 2, heat=True, coef=0.1, kept=0.9)
+    b.run(sampler).check()
+    grad, kl = b.grad.clone(), b.out["kl"].clone()
+    for _ in range(3):
+        b.call()
+    assert torch.equal(torch.nan_to_num(b.grad.float()), torch.nan_to_num(grad.float())) and torch.equal(b.out["kl"], kl)
+
+
 @pytest.mark.parametrize("shape", DISTILS)
 @pytest.mark.parametrize("grad", [True, False])
 def test_distill(sampler, shape, grad):

@@ -8,8 +8,8 @@
 //                        (W + h) p_j - q_j                inside,     and -h at the row's token.
 // The two sides of the list are kept apart from the start: the sums of the tokens outside have their own reference, so
 // that p_r is a sum and not a difference, however little it is, and an element outside is one exponential times one
-// factor of the row. The list's own terms are taken one by one, with the accurate exponential, and added up in double:
-// a divergence is a small difference of logprobs.
+// factor of the row. The list's own terms are taken one by one, with the accurate exponential, and added up as pairs
+// of fp32: a divergence is a small difference of logprobs.
 //
 // As in the other losses (row_loss_kernel.cu) a cluster of C CTAs takes a row, each CTA a part of it in shared memory
 // between the two passes, so that each logit is read once and each gradient written once. Here a part is one buffer,
@@ -19,12 +19,12 @@
 //              before pass 1; take their logits from the buffer and put their share of the list's sums into all CTAs of
 //              the cluster; combine what all have put, work out the row's factors, write the row's outputs, and put the
 //              list's own gradients into the buffer in their logits' place;
-//   consumers  (sixteen, of short rows four) pass 1: the running reference and sum of what is not marked; pass 2: the gradient, marked
-//              elements as they now are in the buffer. A row's pass 1 comes before the pass 2 of the row before it, so
-//              that the join and the closer's work run under it.
+//   consumers  (sixteen, of short rows four) pass 1: the running reference and sum of what is not marked; pass 2: the
+//              gradient, marked elements as they now are in the buffer. A row's pass 1 comes before the pass 2 of the row
+//              before it, so that the join and the closer's work run under it.
 //
-// One CTA an SM (of short rows three). 4096 x 128000 bf16 with gradient, lists of 64, 0.9 of the rows counted: 379 us, 0.78 of the copy rate
-// over what has to move. Two CTAs of eight consumers an SM, with parts of half the size and twice as many: 475 us (twice
+// One CTA an SM (of short rows three). 4096 x 128000 bf16 with gradient, lists of 64, 0.9 of the rows counted: 378 us, 0.78
+// of the copy rate over what has to move. Two CTAs of eight consumers an SM, with parts of half the size and twice as many: 475 us (twice
 // the joins and closers' turns of a row). What bounds it now is the consumers' instructions, which take 0.68 of the issue
 // slots: an exponential and packed arithmetic around it for each element in each pass.
 #include <cuda_runtime.h>

@@ -500,19 +500,16 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const sampler_micro_rows
         const int col = (first + k * group) * kVec - head;
         if (col >= cols) break;
         const float unit = scale_value<kBlock>(scale[k]) * row_scale, after = kCut ? scale_value<kBlock>(next[k]) * row_scale : unit;
-        const int change = kCut ? (max(col, 0) / kBlock + 1) * kBlock - col : kVec;  // from where on the next block's scale counts
         float x[kVec];
 #pragma unroll
         for (int j = 0; j < kVec; j += 2) {
             const float2 y = values2(codes[k] >> 4 * j & 0xffu);
-            if (kCut) {
-                x[j] = y.x * (j >= change ? after : unit);
-                x[j + 1] = y.y * (j + 1 >= change ? after : unit);
-            } else {
-                const Two z = times(two(__float_as_uint(y.x), __float_as_uint(y.y)), two(__float_as_uint(unit), __float_as_uint(unit)));
-                x[j] = __uint_as_float(uint32_t(z));
-                x[j + 1] = __uint_as_float(uint32_t(z >> 32));
-            }
+            // (a block that begins within the vector begins where the row's first column is in its own)
+            const Two u = kCut ? two(__float_as_uint(j >= head ? after : unit), __float_as_uint(j + 1 >= head ? after : unit))
+                               : two(__float_as_uint(unit), __float_as_uint(unit));
+            const Two z = times(two(__float_as_uint(y.x), __float_as_uint(y.y)), u);
+            x[j] = __uint_as_float(uint32_t(z));
+            x[j + 1] = __uint_as_float(uint32_t(z >> 32));
         }
         const uint4 y = Out<T>::pack(x);
         if (vec_out && (!kCut || col >= 0) && col + kVec <= cols) {

@@ -6,10 +6,10 @@
 // is not is added up, as 2^((x - ref) c) with ref the bar's value: no exponential is
 // above 1, the running maximum is not needed, and the mass outside the top n is a sum
 // of its own and not a difference that cancels.
-//   The first bar. Of the 256 threads' largest in the first four chunks, the n-th,
+//   The first bar. Of the 256 threads' largest in the first five chunks, the n-th,
 //   rounded down to bf16, by counts of two to an instruction. At least n logits reach
-//   it. (Of the first chunk alone: 349 us for 285 at 4096 x 128000 bf16, n = 64, as four
-//   times as many keys come in the first quarter of a row.)
+//   it. (Of the first chunk alone: 331 us for 281 at 4096 x 128000 bf16, n = 64, and 61 for
+//   46 at 517 x 40961 fp32, n = 128, for the many keys that come in a row's first part.)
 //   Later bars. A list of `trigger` keys or more goes to the closer, a warp that cuts it
 //   down to about n, whose least is the new bar, while the next chunks are read and put
 //   theirs into the row's other list; two chunks later what it has left comes back. What
@@ -26,7 +26,7 @@
 // workspace; the part that ends last joins them, parts in order. Short rows are a warp's
 // each, with a kernel of their own.
 //
-// Two CTAs an SM. 4096 x 128000 bf16, n = 64: 285 us, 0.49 of the copy rate; instructions
+// Two CTAs an SM. 4096 x 128000 bf16, n = 64: 281 us, 0.49 of the copy rate; instructions
 // bound it (issue slots 0.56 busy, and where they are not, warps wait for the few of them
 // that have keys to put): 51000 of a warp a row, of which exponentials and sums are 14000,
 // loads, peaks and comparisons with the bar 19000, keys and cuts 15000. Tried besides: one
@@ -55,7 +55,7 @@ constexpr int kVecs = 4;                        // of a chunk in each consumer
 constexpr int kChunkVecs = kConsumers * kVecs;
 constexpr int kChunkBytes = kChunkVecs * 16;
 constexpr int kSlots = 5;
-constexpr int kLook = 4;                         // chunks that are looked at for a row's first bar
+constexpr int kLook = kSlots;                    // chunks that are looked at for a row's first bar
 constexpr int kJobs = 4;                         // of the closer
 constexpr int kLane = 8;                         // keys of a list in each of its lanes, at most
 constexpr int kClosable = 32 * kLane;            // keys of a list that it takes

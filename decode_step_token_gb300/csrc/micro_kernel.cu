@@ -374,7 +374,7 @@ cudaError_t launch_quantize(const sampler_micro_t& q, int sms, cudaStream_t stre
     p.padded = (q.rows + 127) / 128 * 128;
     p.vec_in = reinterpret_cast<uintptr_t>(q.src) % 16 == 0 && q.src_stride * int64_t(sizeof(T)) % 16 == 0;
     p.vec_out = reinterpret_cast<uintptr_t>(q.values) % 8 == 0 && q.values_stride % 8 == 0;
-    p.group = 8;
+    p.group = 4 * kBlock / kPer;  // the threads that share a word of scales
     while (p.group < kThreads && p.group < chunks) p.group *= 2;
     const int held = chunks <= p.group ? 1 : chunks <= 2 * kThreads ? 2 : chunks <= 4 * kThreads ? 4 : 0;
     // Rows in hand, for the loads under way: two where there are more than eight blocks' worth for each SM and they lie in
@@ -436,18 +436,19 @@ struct Out<uint16_t> {
     }
 };
 
-// Eight codes of a row from column `col` on, in a word, as far as they lie in one of the row's `words` words of codes.
+// Eight codes of a row from column `col` on, in a word (of columns before the first, 0; `words` of codes are the row's). Both
+// words are read, so that nothing waits for a branch.
 __device__ __forceinline__ uint32_t codes_at(const uint8_t* row, int col, int words)
 {
     const uint32_t* w = reinterpret_cast<const uint32_t*>(row);
-    const int i = col >> 3;  // (rounded down: columns before the first have codes 0)
-    const uint32_t a = i >= 0 ? __ldg(w + i) : 0u, b = i + 1 < words ? __ldg(w + i + 1) : 0u;
-    return __funnelshift_r(a, b, 4 * (col & 7));
+    const int i = col >> 3;  // (rounded down)
+    const uint32_t a = __ldg(w + max(i, 0)), b = __ldg(w + min(i + 1, words - 1));
+    return __funnelshift_r(i < 0 ? 0u : a, b, 4 * (col & 7));
 }
 
 // kVectors 16-byte vectors of the output in each thread, `group` of them side by side. kCut (bf16 whose rows begin within
 // a vector): the vectors are the output's, whose codes and scales are cut out of the row's, and not the row's, stored one
-// by one: 3000 x 15001 takes 48 us in place of 127. In fp32, with half as many values in a vector, it would be 36 in place
+// by one: 3000 x 15001 takes 43 us in place of 127. In fp32, with half as many values in a vector, it would be 36 in place
 // of 29 (20001 x 1001).
 template <typename T, int kBlock, bool kCut>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const sampler_micro_rows_t q, int group, int vectors, int tiles,
@@ -468,10 +469,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const sampler_micro_rows
     uint32_t codes[kVectors], scale[kVectors], next[kVectors];
 #pragma unroll
     for (int k = 0; k < kVectors; ++k) {
-        const int col = (first + k * group) * kVec - head;
+        int col = (first + k * group) * kVec - head;
         codes[k] = scale[k] = next[k] = 0u;
-        if (!there || col >= cols) continue;
+        if (!there || (!kCut && col >= cols)) continue;
         if (kCut) {
+            col = min(col, cols - 1);  // (a vector that is not there reads what is not used)
             if (vec_in) {
                 codes[k] = codes_at(v, col, (bytes + 3) / 4);
             } else {
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const sampler_micro_rows
             }
             const int b0 = max(col, 0) / kBlock, b1 = min(col + kVec - 1, cols - 1) / kBlock;
             scale[k] = __ldg(s + (b0 / 4) * 512 + b0 % 4);
-            next[k] = b1 == b0 ? scale[k] : __ldg(s + (b1 / 4) * 512 + b1 % 4);
+            next[k] = __ldg(s + (b1 / 4) * 512 + b1 % 4);
         } else {
             const uint8_t* p = v + col / 2;
             if (vec_in && col + kVec <= cols) {
@@ -531,7 +533,7 @@ cudaError_t launch_rows(const sampler_micro_rows_t& q, cudaStream_t stream)
     const bool whole = reinterpret_cast<uintptr_t>(q.out) % 16 == 0 && q.out_stride * int64_t(sizeof(T)) % 16 == 0;
     const bool cut = sizeof(T) == 2 && !whole;
     const int64_t vectors = (q.cols + (cut ? 2 * kVec - 2 : kVec - 1)) / kVec;  // the most that a row touches
-    int group = 8;
+    int group = 2;
     while (group < kThreads && group * kVectors < vectors) group *= 2;
     const int64_t per = kThreads / group;
     cudaLaunchConfig_t cfg{};

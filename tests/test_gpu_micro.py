@@ -144,6 +144,33 @@ def test_rows_to_anywhere(sampler, cols, kind, block):
             assert (view[:, cols:] == -7).all() and (flat[:shift] == -7).all() and (flat[-40:] == -7).all()
 
 
+@pytest.mark.parametrize("cols,pad", [(64, 0), (128, 0), (33, 0), (256, 8), (1000, 0), (1024, 0), (1001, 1)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [16, 32])
+def test_many_rows_are_as_few(sampler, cols, pad, kind, block):
+    """So many rows that a thread has several in hand: the bytes of their first and last 1024 rows, quantised and read back
+    apart."""
+    import torch
+
+    rows, few = 45003, 1024
+    gen = torch.Generator(device="cuda:0").manual_seed(cols)
+    whole = torch.randn((rows, cols + pad), generator=gen, device="cuda:0").to(torch.bfloat16 if kind == "bf16" else torch.float32)
+    src = whole[:, :cols]
+    values, scales, row_scale = _quantize(sampler, src, block)
+    back = torch.full((rows, cols), -7.0, dtype=src.dtype, device="cuda:0")
+    sampler.micro_rows(values=values, scales=scales, row_scale=row_scale, out=back, block=block)
+    size = sampler.micro_scale_bytes(few, cols, block)
+    start = (rows - few) // 128 * 128
+    for at, n in ((0, few), (start, rows - start)):
+        v, s, r = _quantize(sampler, src[at:at + n], block)
+        assert torch.equal(values[at:at + n], v) and torch.equal(row_scale[at:at + n], r)
+        first = at // 128 * (size // (few // 128))
+        assert torch.equal(scales[first:first + s.numel()], s)
+        out = torch.empty((n, cols), dtype=src.dtype, device="cuda:0")
+        sampler.micro_rows(values=v, scales=s, row_scale=r, out=out, block=block)
+        assert torch.equal(back[at:at + n], out)
+
+
 def _operand(rng, rows, K, block, row_scale=True):
     """Random codes and scales: every code, scales of all sizes with zeros among them."""
     half = (K + 1) // 2
@@ -417,6 +444,39 @@ def test_pairs_of_ctas_whose_waits_give_up():
         out.fill_(-7.0)
         s.lm_head_micro(**ops, logits=out)
         assert s.stat(d.SAMPLER_STAT_LM_HEAD_TIMEOUTS) > 0 and (out == -7).all()
+
+
+@pytest.mark.parametrize("rows", [5, 140])
+def test_rows_far_apart(sampler, rows):
+    """Offsets beyond 32 bits: of the source, the values, what is read back and the logits."""
+    import torch
+
+    V, K = 700, 320
+    gen = torch.Generator(device="cuda:0").manual_seed(rows)
+    hidden = torch.randn((rows, K), generator=gen, device="cuda:0").to(torch.bfloat16)
+    weight = torch.randn((V, K), generator=gen, device="cuda:0").to(torch.bfloat16)
+
+    def far(n, cols, dtype, apart):
+        return torch.empty(n * apart, dtype=dtype, device="cuda:0").view(n, apart)[:, :cols]
+
+    apart = 16 * (2 ** 32 // 16 // (rows - 1) + 1)  # in bytes, and more of what is larger
+    src = far(rows, K, torch.bfloat16, apart)
+    src.copy_(hidden)
+    near = _quantize(sampler, hidden, 16)
+    values = far(rows, K // 2, torch.uint8, apart)
+    scales, row_scale = torch.empty_like(near[1]), torch.empty_like(near[2])
+    sampler.quantize_micro(src=src, out_values=values, out_scales=scales, out_row_scale=row_scale)
+    assert torch.equal(values, near[0]) and torch.equal(scales, near[1]) and torch.equal(row_scale, near[2])
+    back, want = far(rows, K, torch.bfloat16, apart), torch.empty_like(hidden)
+    sampler.micro_rows(values=near[0], scales=scales, row_scale=row_scale, out=want)
+    sampler.micro_rows(values=values, scales=scales, row_scale=row_scale, out=back)
+    assert torch.equal(back, want)
+    w = _quantize(sampler, weight, 16)
+    ops = dict(hidden_scale=scales, hidden_row_scale=row_scale, weight=w[0], weight_scale=w[1], weight_row_scale=w[2])
+    logits, want = far(rows, V, torch.bfloat16, apart), torch.empty((rows, V), dtype=torch.bfloat16, device="cuda:0")
+    sampler.lm_head_micro(hidden=near[0], logits=want, **ops)
+    sampler.lm_head_micro(hidden=values, logits=logits, **ops)
+    assert torch.equal(logits, want)
 
 
 def test_argument_checks(sampler):

@@ -585,6 +585,75 @@ def test_waits_that_give_up(kind, rows, V):
             _check_top(_run_top(s, b.x, kind, 9, weight=b.weight), b.x, 9, weight=b.weight)
 
 
+def test_two_graphs_share_a_workspace(sampler):
+    """Graphs of both operators on one handle, of rows in parts and whole ones, replayed in turn on inputs that change."""
+    import torch
+
+    gen = torch.Generator(device="cuda:0").manual_seed(11)
+    sets = []
+    for rows, V in ((3, 151936), (40, 100000), (400, 5000)):
+        x = torch.randn((rows, V), generator=gen, device="cuda:0")
+        o = dict(ids=torch.empty((rows, 20), dtype=torch.int32, device="cuda:0"), lps=torch.empty((rows, 20), device="cuda:0"),
+                 rest=torch.empty(rows, device="cuda:0"), loss=torch.empty(1, device="cuda:0"), grad=torch.empty_like(x))
+
+        def call(x=x, o=o):
+            sampler.score_top(logits=x, top_n=20, out_top_ids=o["ids"], out_top_logprobs=o["lps"], out_rest_logprob=o["rest"])
+            sampler.distill_loss(logits=0.7 * x, teacher_ids=o["ids"], teacher_logprobs=o["lps"], teacher_rest=o["rest"],
+                                 out_loss=o["loss"], out_grad=o["grad"])
+
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        sets.append((x, o, call, graph))
+    for turn in range(4):
+        for x, o, call, graph in sets:
+            x.copy_(torch.randn(x.shape, generator=gen, device="cuda:0"))
+        for x, o, call, graph in sets:
+            graph.replay()
+        torch.cuda.synchronize()
+        for x, o, call, graph in sets:
+            first = {k: v.clone() for k, v in o.items()}
+            call()
+            torch.cuda.synchronize()
+            assert all(torch.equal(first[k], o[k]) for k in o)
+
+
+@pytest.mark.parametrize("V", [700, 40000, 200001])
+def test_rows_far_apart(sampler, V):
+    """Offsets beyond 32 bits, of the logits and of the gradient, give what rows side by side give."""
+    import torch
+
+    rows, stride = 5, 600_000_001
+    gen = torch.Generator(device="cuda:0").manual_seed(V)
+    near = torch.randn((rows, V), generator=gen, device="cuda:0").to(torch.bfloat16)
+    far = torch.empty(rows * stride, dtype=torch.bfloat16, device="cuda:0").view(rows, stride)[:, :V]
+    far.copy_(near)
+    outs = []
+    for x in (near, far):
+        ids = torch.empty((rows, 30), dtype=torch.int32, device="cuda:0")
+        lps, rest = torch.empty((rows, 30), device="cuda:0"), torch.empty(rows, device="cuda:0")
+        sampler.score_top(logits=x, top_n=30, out_top_ids=ids, out_top_logprobs=lps, out_rest_logprob=rest)
+        outs.append((ids, lps, rest))
+    assert torch.equal(outs[0][0], outs[1][0])
+    # rows that begin elsewhere in a vector add up in another order: 4 sqrt(V / 256 + 64) roundings of 2^-24 for each
+    for a, b in zip(outs[0][1:], outs[1][1:]):
+        assert torch.allclose(a, b, rtol=0, atol=1e-5)
+    ids, lps, rest = outs[0]
+    loss, grads = [], []
+    wide = torch.empty(rows * stride, dtype=torch.bfloat16, device="cuda:0").view(rows, stride)[:, :V]
+    for x, g in ((near, torch.empty_like(near)), (far, wide)):
+        out = torch.empty(1, device="cuda:0")
+        sampler.distill_loss(logits=x, teacher_ids=ids, teacher_logprobs=lps + 0.1, teacher_rest=rest,
+                             out_loss=out, out_grad=g)
+        loss.append(out.item())
+        grads.append(g.float())
+    assert abs(loss[0] - loss[1]) <= 1e-5 * abs(loss[0])
+    # a bf16 rounding where the fp32 values differ in their last places
+    assert ((grads[0] - grads[1]).abs() <= 2.0 ** -7 * grads[0].abs() + 1e-12).all()
+
+
 def test_argument_checks(sampler):
     import torch
 

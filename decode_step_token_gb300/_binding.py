@@ -285,6 +285,8 @@ _lib = None
 def load_library(path: str = LIB):
     """Load libsampler.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):
@@ -444,11 +446,11 @@ def sampler_lm_head_scaled_sample(h, lm: sampler_scaled_head_t, args: sampler_ar
 
 
 def sampler_score_top(h, rows: sampler_rows_t, top: sampler_top_t, stream: int) -> int:
-    return load_library().sampler_score_top(h, ctypes.byref(rows), ctypes.byref(top), _P(stream))
+    return load_library().sampler_score_top(h, ctypes.byref(rows), ctypes.byref(top), stream)
 
 
 def sampler_distill_loss(h, rows: sampler_rows_t, distill: sampler_distill_t, stream: int) -> int:
-    return load_library().sampler_distill_loss(h, ctypes.byref(rows), ctypes.byref(distill), _P(stream))
+    return load_library().sampler_distill_loss(h, ctypes.byref(rows), ctypes.byref(distill), stream)
 
 
 def sampler_micro_scale_bytes(rows: int, cols: int, block: int) -> int:
@@ -456,17 +458,16 @@ def sampler_micro_scale_bytes(rows: int, cols: int, block: int) -> int:
 
 
 def sampler_quantize_micro(h, q: sampler_micro_t, stream: int) -> int:
-    return load_library().sampler_quantize_micro(h, ctypes.byref(q), _P(stream))
+    return load_library().sampler_quantize_micro(h, ctypes.byref(q), stream)
 
 
 def sampler_micro_rows(h, q: sampler_micro_rows_t, stream: int) -> int:
-    return load_library().sampler_micro_rows(h, ctypes.byref(q), _P(stream))
+    return load_library().sampler_micro_rows(h, ctypes.byref(q), stream)
 
 
 def sampler_lm_head_micro(h, lm: sampler_micro_head_t, logits: int, dtype: int, logits_stride: int, rows: int, vocab: int,
                           stream: int) -> int:
-    return load_library().sampler_lm_head_micro(h, ctypes.byref(lm), _P(logits), dtype, logits_stride, rows, vocab,
-                                                _P(stream))
+    return load_library().sampler_lm_head_micro(h, ctypes.byref(lm), logits, dtype, logits_stride, rows, vocab, stream)
 
 
 def sampler_lm_head_micro_sample(h, lm: sampler_micro_head_t, args: sampler_args_t, ext, stream: int) -> int:

@@ -570,7 +570,18 @@ __device__ __noinline__ uint32_t slow_chunk(uint32_t at, uint32_t valid, int chu
     uint64_t least = st.bar > -pos_inf() ? uint64_t(order_of(st.bar) + 1) << 32 : 0;  // (of the list, where it has n keys)
     const T* x = reinterpret_cast<const T*>(ring_of() + chunk_at);
 #pragma unroll 1
-    for (int e = 0; e < kVecs * kPer; ++e) {
+    for (int e = 0;; ++e) {
+        // Room for a key of each thread. (What was there before may leave none: the keys of a cut that has just come back, and
+        // those that were put in meanwhile, are up to kCap.) In the end the list is cut down in any case.
+        const bool end_of_chunk = e == kVecs * kPer;
+        const uint32_t count = S.count[at];
+        if (count > (end_of_chunk ? n : uint32_t(kCap - kConsumers))) {
+            least = select(S.list[at], count, n, n + n / 4 + 8 < count ? n + n / 4 + 8 : n);
+            cut<kEntropy>(at, count, least, st, q);
+            at ^= 1;
+        }
+        bar_sync();
+        if (end_of_chunk) break;
         const int i = e / kPer * kConsumers + tid, j = (base + i) * kPer + e % kPer;
         const bool there = base + i < last && j >= head && j < end;
         const float y = there ? load_logit(x + i * kPer + e % kPer) : -pos_inf();
@@ -583,13 +594,6 @@ __device__ __noinline__ uint32_t slow_chunk(uint32_t at, uint32_t valid, int chu
             const float u = (y - st.ref) * c, f = exp2_fast(u);
             st.s += f;
             if (kEntropy) st.t = fmaf(f, fmaxf(u, kLowest), st.t);
-        }
-        bar_sync();
-        const uint32_t count = S.count[at];
-        if (count >= uint32_t(kCap - kConsumers) || (e == kVecs * kPer - 1 && count > n)) {
-            least = select(S.list[at], count, n, n + n / 4 + 8 < count ? n + n / 4 + 8 : n);
-            cut<kEntropy>(at, count, least, st, q);
-            at ^= 1;
         }
         bar_sync();
     }

@@ -677,3 +677,54 @@ def test_argument_checks(sampler):
             continue
         with pytest.raises(error):
             sampler.distill_loss(**{**dis, **change})
+
+
+def _lists_under_way(rng, rows, V, chunk, first, kind):
+    """Rows whose list is cut while more keys come than a list of 512 holds with those of the next chunk: in chunk
+    `first` `second` values above all before, in the next `third` above those, and all of the one after above them."""
+    x = 0.01 * rng.standard_normal((rows, V))
+    for r in range(rows):
+        lanes, deep = rng.integers(1, 129), rng.integers(1, 6)  # of the first chunk, values that pass the first bar
+        x[r, rng.permutation(chunk)[:lanes * deep]] = 5 + 1e-4 * rng.random(lanes * deep)
+        second, third, at = rng.integers(40, 250), rng.integers(200, 257), first * chunk
+        x[r, at + rng.permutation(chunk)[:second]] = 6 + rng.random(second)
+        x[r, at + chunk + rng.permutation(chunk)[:third]] = 8 + rng.random(third)
+        x[r, at + 2 * chunk:at + 3 * chunk] = 10 + rng.random(chunk)
+        if r % 3 == 1:  # the last chunk in steps of its own
+            x[r, at + 2 * chunk:at + 3 * chunk] += 0.001 * np.arange(chunk)
+    return _round(x, kind)
+
+
+@pytest.mark.parametrize("n", [1, 8, 20, 64, 100, 128])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_top_chunk_over_a_list_that_a_cut_comes_back_to(sampler, kind, n):
+    """Several rows for each CTA, in either pair of its lists."""
+    rng = np.random.default_rng(n)
+    chunk = 8192 if kind == "bf16" else 4096
+    rows, V, kinds = 640, 9 * chunk, 40
+    x = np.concatenate([_lists_under_way(rng, kinds // 2, V, chunk, first, kind) for first in (5, 6)])
+    x = x[np.arange(rows) * 7 % kinds]
+    got = _run_top(sampler, x, kind, n, entropy=n in (8, 64))
+    for r in range(kinds, rows):  # the same rows have the same outputs, wherever they are
+        for k in got:
+            np.testing.assert_array_equal(got[k][r], got[k][r % kinds])
+    _check_top({k: v[:kinds] for k, v in got.items()}, x[:kinds], n)
+
+
+@pytest.mark.parametrize("n", [4, 20, 64])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_top_chunk_over_such_a_list_in_a_part(sampler, kind, n):
+    """The same in one of a row's eight parts."""
+    rng = np.random.default_rng(n)
+    V = 262144
+    chunk = 8192 if kind == "bf16" else 4096
+    part = V // 8
+    x = 0.01 * rng.standard_normal((6, V))
+    if part >= 8 * chunk:
+        for r in range(6):
+            x[r, r * part:(r + 1) * part] = _lists_under_way(rng, 1, part, chunk, 5, kind)[0]
+    else:  # parts of four chunks, which are all looked at for the first bar
+        for r in range(6):
+            x[r, r * part + 3 * chunk:r * part + 4 * chunk] = 10 + rng.random(chunk)
+    x = _round(x, kind)
+    _check_top(_run_top(sampler, x, kind, n), x, n)

@@ -728,3 +728,80 @@ def test_top_chunk_over_such_a_list_in_a_part(sampler, kind, n):
             x[r, r * part + 3 * chunk:r * part + 4 * chunk] = 10 + rng.random(chunk)
     x = _round(x, kind)
     _check_top(_run_top(sampler, x, kind, n), x, n)
+
+
+def _check_rest(got, x, n, T=None):
+    """The logprob of what is outside the lists, -inf exactly where that has no finite logit, else within the roundings of
+    its own sum (a warp's, of V / 32 in a lane, or of the row), of the row's, and of the distances between their largest."""
+    rows, V = x.shape
+    far = 0
+    for r in range(rows):
+        logp = x[r].astype(np.float64) / (1.0 if T is None or T[r] < np.float32(1e-5) else float(T[r]))
+        logp = logp - logp.max()
+        logp -= O.log_sum(logp)
+        ids = got["ids"][r][got["ids"][r] >= 0]
+        np.testing.assert_array_equal(ids, np.lexsort((np.arange(V), -x[r]))[:min(n, np.isfinite(logp).sum())])
+        out = np.delete(logp, ids)
+        if not np.isfinite(out).any():
+            assert got["rest"][r] == -np.inf, (r, got["rest"][r])
+            continue
+        want, depth = O.log_sum(out), _depths(out)
+        gap = min(logp[ids].min() - out.max(), 60.0)  # a sum relative to the list's least: 84 powers of two below it at most
+        far += logp[ids].min() - out.max() > 60
+        tol = (_sum_error(np.exp(logp), _depths(logp), V) + _sum_error(np.exp(out - out.max()), depth, 8 * V) + 3 * EPS * gap
+               + 4 * EPS + EPS * abs(want))
+        assert abs(got["rest"][r] - want) <= tol, (r, got["rest"][r], want, tol)
+    return far
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V", [(40, 200), (40, 4096), (40, 8000), (700, 16000), (40, 30011), (6, 151936), (170, 40000)])
+def test_top_rest_far_below_the_list(sampler, kind, rows, V):
+    """The mass of the others, however little it is: low temperatures, leads of some logits, tokens forbidden by a large
+    negative number or the type's lowest in place of -inf, all others at -inf, as many tokens as were asked for."""
+    rng = np.random.default_rng(V)
+    for n in (1, 20, 64):
+        x = rng.standard_normal((rows, V))
+        T = np.ones(rows, np.float32)
+        for r in range(rows):
+            some = rng.permutation(V)[:n + r % 2]  # n, or one more
+            if r % 7 == 0:
+                T[r] = rng.choice([0.02, 0.05, 0.1])
+                x[r, some] += 12
+            elif r % 7 == 1:
+                keep = x[r, some]
+                x[r] = -1e4 + x[r]
+                x[r, some] = keep
+            elif r % 7 == 2:
+                keep = x[r, some]
+                x[r] = -3.38e38
+                x[r, some] = keep
+            elif r % 7 == 3:
+                keep = x[r, some]
+                x[r] = -np.inf
+                x[r, some] = keep
+            elif r % 7 == 4:  # the list's own next keys are far below it, and the rest far below those
+                x[r] = -1500 - 500 * rng.random(V)
+                x[r, some] = 3 + 0.1 * rng.random(len(some))
+                x[r, rng.permutation(V)[:30]] = -700 - 100 * rng.random(30)
+            elif r % 7 == 5:  # all that is wanted in one place, and what comes next in another
+                x[r] = -300 + x[r]
+                x[r, V // 2:V // 2 + n] = 5
+                x[r, :3] = -200
+        x = _round(x, kind)
+        got = _run_top(sampler, x, kind, n, V % 3, V % 5, T=T, entropy=False)
+        some = np.arange(rows) if rows < 100 else np.concatenate([np.arange(28), np.arange(rows - 28, rows)])
+        far = _check_rest({k: v[some] for k, v in got.items()}, x[some], n, T[some])
+        assert far > len(some) // 4
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V,n", [(1, 1), (2, 1), (5, 5), (64, 64), (128, 128), (100, 128), (129, 128)])
+def test_top_rest_of_short_vocabularies(sampler, kind, V, n):
+    """All tokens listed, or all but one, which may be far below."""
+    rng = np.random.default_rng(V)
+    x = rng.standard_normal((60, V))
+    x[np.arange(60), rng.integers(0, V, 60)] -= rng.choice([0, 100, 1e4, 1e30], 60)
+    x = _round(x, kind)
+    got = _run_top(sampler, x, kind, n, V % 3, V % 5, entropy=False)
+    _check_rest(got, x, n)

@@ -73,7 +73,7 @@ struct Job {
     int row, token;
     float ref;    // of the sums of what is not in the list
     float bar;    // the list's keys have values of that or above
-    float c, c_hi, c_lo, inv_t, inv_t_lo, x_t;
+    float c_hi, c_lo, inv_t, inv_t_lo, x_t;
 };
 
 struct Shared {
@@ -261,9 +261,16 @@ struct Sums {
     float s, t;
 };
 
-// Add four vectors to the sums. (The rounded log2(e) / T alone: its error is that of the product after it. A row of
-// 128000 takes a tenth of its instructions more with the pair that the other losses take, whose logprobs are of sums
-// that are not.)
+// log2(e) / T as a pair, and as the float that is nearest to it.
+struct Scale {
+    float c_hi, c_lo;
+    __device__ __forceinline__ float nearest() const { return __fadd_rn(c_hi, c_lo); }
+};
+
+// Add four vectors to the sums. (By log2(e) / T as one float, c, the nearest. The pair takes 6 % longer: 4096 x 128000
+// bf16, n = 64, 324 us for 306 with a cold L2. Mean errors of 2048 logprobs of rows of 128000 bf16 whose mass is 8 nats
+// below one token: 0.8e-7 at T = 1.44, where the product of rounded log2(e) and 1 / T, 1.9 units of 2^-24 off, had -7.4e-7;
+// 0.7 and 7.5e-7 at T = 0.7195. sampler_score, which moves its sums by that product, has -7.2e-7 and 6.4e-7.)
 template <typename T, bool kEntropy>
 __device__ __forceinline__ void add(Sums& st, const uint4 (&v)[kVecs], Two c)
 {
@@ -290,13 +297,14 @@ __device__ __forceinline__ void add(Sums& st, const uint4 (&v)[kVecs], Two c)
     }
 }
 
-__device__ __forceinline__ void move(Sums& st, float ref, float c)
+// The sums relative to a reference that is at least their own. (By the pair: what moves is all that was added up before,
+// and an error in its exponent is one of all of that, the same way each time.)
+__device__ __forceinline__ void move(Sums& st, float ref, const Scale& q)
 {
-    Stats a{st.ref, st.s, st.t};
-    stats_move(a, ref, c);
-    st.ref = a.ref;
-    st.s = a.s;
-    st.t = a.t;
+    const float x = st.ref - ref, d = fmaxf(fmaf(x, q.c_hi, x * q.c_lo), kLowest), f = exp2_fast(d);
+    st.t = f * fmaf(st.s, d, st.t);
+    st.s *= f;
+    st.ref = ref;
 }
 
 // The sum of all consumers' counts; `turn` goes round the three tallies, of which the one that it starts from is 0.
@@ -360,11 +368,6 @@ __device__ __forceinline__ uint64_t select(const uint64_t* list, uint32_t count,
     return lo;
 }
 
-// log2(e) / T, rounded and as a pair, for keys one by one.
-struct Scale {
-    float c, c_hi, c_lo;
-};
-
 // The next `want` places in a list for a lane by itself. (Written so that the lanes that want some, a few of a warp, are
 // not put together first.)
 __device__ __forceinline__ uint32_t next_places(uint32_t* count, uint32_t want)
@@ -423,7 +426,7 @@ __device__ __forceinline__ void lose(const uint64_t* from, uint32_t count, Sums&
             t += S.lost_t[w];
         }
         Sums one{0.f, ref, __ull2float_rn(s) * (1.f / kLostUnit), __ll2float_rn(t) * (1.f / kLostUnit)};
-        move(one, st.ref, q.c);
+        move(one, st.ref, q);
         st.s += one.s;
         st.t += one.t;
         S.lost_most = 0;
@@ -457,7 +460,7 @@ __device__ __forceinline__ void rank(const uint64_t* from, uint32_t count, uint3
     bar_sync();
     if (count <= n) return;
     const uint64_t least = to[n - 1];
-    move(st, key_value(least), q.c);
+    move(st, key_value(least), q);
     st.bar = st.ref;
     lose<kEntropy>(from, count, st, q, [&](uint64_t k) { return k < least; });
 }
@@ -484,7 +487,7 @@ __device__ __forceinline__ void cut(uint32_t at, uint32_t count, uint64_t least,
     }
     most = __reduce_max_sync(0xffffffffu, most);
     if ((tid & 31) == 0 && most) atomicMax(&S.lost_most, most);
-    move(st, key_value(least), q.c);
+    move(st, key_value(least), q);
     st.bar = st.ref;
     bar_sync();
     lose<kEntropy>(from, count, st, q, [&](uint64_t k) { return k < least; });
@@ -494,13 +497,13 @@ __device__ __forceinline__ void cut(uint32_t at, uint32_t count, uint64_t least,
 // A list that is longer than there are threads is cut down to n to `most` keys. Sums come and go in S.state; the list that
 // is filled in the end is returned.
 template <bool kEntropy>
-__device__ __noinline__ uint32_t cut_long(uint32_t at, uint32_t count, uint32_t n, uint32_t most, float c, float c_hi, float c_lo)
+__device__ __noinline__ uint32_t cut_long(uint32_t at, uint32_t count, uint32_t n, uint32_t most, float c_hi, float c_lo)
 {
     Shared& S = shared();
     const float4 in = S.state[threadIdx.x];
     Sums st{in.x, in.y, in.z, in.w};
     const uint64_t least = select(S.list[at], count, n, most);
-    cut<kEntropy>(at, count, least, st, Scale{c, c_hi, c_lo});
+    cut<kEntropy>(at, count, least, st, Scale{c_hi, c_lo});
     S.state[threadIdx.x] = make_float4(st.bar, st.ref, st.s, st.t);
     bar_sync();
     return at ^ 1;
@@ -548,12 +551,12 @@ __device__ __forceinline__ void load(uint4 (&v)[kVecs], const Chunk& p)
 // in S.state (before the chunk; after it); the list that is filled in the end is returned.
 template <typename T, bool kEntropy>
 __device__ __noinline__ uint32_t slow_chunk(uint32_t at, uint32_t valid, int chunk_at, int base, int last, int head, int end,
-                                            uint32_t n, float c, float c_hi, float c_lo)
+                                            uint32_t n, float c_hi, float c_lo)
 {
     constexpr int kPer = Elems<T>::kPer;
     Shared& S = shared();
     const int tid = threadIdx.x, before = base * kPer - head;
-    const Scale q{c, c_hi, c_lo};
+    const Scale q{c_hi, c_lo};
     const float4 in = S.state[tid];
     Sums st{in.x, in.y, in.z, in.w};
     bar_sync();
@@ -591,7 +594,7 @@ __device__ __noinline__ uint32_t slow_chunk(uint32_t at, uint32_t valid, int chu
         if (wants) {
             S.list[at][to] = k;
         } else {
-            const float u = (y - st.ref) * c, f = exp2_fast(u);
+            const float d = y - st.ref, u = fmaf(d, q.c_hi, d * q.c_lo), f = exp2_fast(u);
             st.s += f;
             if (kEntropy) st.t = fmaf(f, fmaxf(u, kLowest), st.t);
         }
@@ -653,7 +656,7 @@ constexpr float kFaint = 5.169878828e-26f;  // 2^-84
 // with the key. Rows like that come with a low temperature and a short list, or where all tokens but a few are forbidden.
 // One of 151936 bf16 takes 49 us more; 4096 x 128000 bf16, n = 1, T = 0.05, all of them such: 703 us, without any 232.)
 template <typename T>
-__device__ __noinline__ float2 far_outside(const TopParams& P, int64_t r, uint64_t least, float c, float c_hi, float c_lo)
+__device__ __noinline__ float2 far_outside(const TopParams& P, int64_t r, uint64_t least, float c_hi, float c_lo)
 {
     constexpr int kPer = Elems<T>::kPer, kAhead = 8;
     const sampler_rows_t& a = P.rows;
@@ -662,6 +665,7 @@ __device__ __noinline__ float2 far_outside(const TopParams& P, int64_t r, uint64
     const uint4* from = reinterpret_cast<const uint4*>(x - span.head);
     const int lane = threadIdx.x & 31, end = span.head + int(a.vocab);
     const uint32_t none = Peak<T>::none(), bar = packed_bar<T>(below(uint32_t(least >> 32)));
+    const float c = Scale{c_hi, c_lo}.nearest();
     Stats st = stats_empty();
     bool bad = false;
     for (int base = lane; base < span.count; base += 32 * kAhead) {
@@ -703,8 +707,8 @@ __device__ __forceinline__ void close_row(const TopParams& P, const uint64_t* so
         if (kEntropy) t += __shfl_xor_sync(0xffffffffu, t, o);
     }
     float rest = st.s, ref = st.ref;
-    Stats outside{ref, st.s, st.t};
-    stats_move(outside, most, h.c);
+    Sums outside = st;
+    move(outside, most, Scale{h.c_hi, h.c_lo});
     const Stats all{most, s + outside.s, t + outside.t};
     Pair ln_s = log_of(all.s);
     ln_s.lo = fmaf(kExp2Short, __fdividef(outside.s, all.s), ln_s.lo);
@@ -716,7 +720,7 @@ __device__ __forceinline__ void close_row(const TopParams& P, const uint64_t* so
     }
     // (fewer keys than n: the row has no others above -inf)
     if (P.top.out_rest_logprob && rest < kFaint && count == n) {
-        const float2 far = far_outside<T>(P, r, sorted[n - 1], h.c, h.c_hi, h.c_lo);
+        const float2 far = far_outside<T>(P, r, sorted[n - 1], h.c_hi, h.c_lo);
         ref = far.x;
         rest = far.y;
     }
@@ -900,11 +904,12 @@ __device__ __forceinline__ void close_list(const TopParams& P, uint64_t* list, i
         take_keys(keys, list, count);
         const uint64_t least = select_warp(keys, n, n, true, order_of(bar));
         Sums lost;
-        count = split_keys<kEntropy>(keys, least, list, Scale{h.c, h.c_hi, h.c_lo}, lost);
+        const Scale q{h.c_hi, h.c_lo};
+        count = split_keys<kEntropy>(keys, least, list, q, lost);
         // (relative to the largest of both and not to the list's least, which may be far above)
         const float ref = fmaxf(st.ref, lost.ref);
-        move(st, ref, h.c);
-        move(lost, ref, h.c);
+        move(st, ref, q);
+        move(lost, ref, q);
         st.s += lost.s;
         st.t += lost.t;
     }
@@ -924,7 +929,7 @@ __device__ __forceinline__ void run_closer(const TopParams& P)
         if (!wait(&S.ready[slot], j / kJobs & 1u, 8 * kWaitNs)) return;
         const Job job = S.jobs[slot];
         if (job.kind == kEnd) return;
-        const Scale q{job.c, job.c_hi, job.c_lo};
+        const Scale q{job.c_hi, job.c_lo};
         uint64_t* list = S.list[job.list];
         int count = job.count;
         if (job.kind == kCut) {
@@ -950,7 +955,6 @@ __device__ __forceinline__ void run_closer(const TopParams& P)
             RowJob h;
             h.token = job.token;
             h.x_t = job.x_t;
-            h.c = job.c;
             h.c_hi = job.c_hi;
             h.c_lo = job.c_lo;
             h.inv_t = job.inv_t;
@@ -991,12 +995,12 @@ __device__ __forceinline__ bool post_job(int j, const Job& job, uint64_t ns)
 // The last part of a row joins them all: its largest keys, in order, are then in list `at` + 1, and the others' sums
 // thread 0's, in S.state. How many keys; -1: a part has failed; -2: it has a NaN or +inf.
 template <bool kEntropy>
-__device__ __noinline__ int join_parts(const TopParams& P, int64_t r, uint32_t at, float c, float c_hi, float c_lo)
+__device__ __noinline__ int join_parts(const TopParams& P, int64_t r, uint32_t at, float c_hi, float c_lo)
 {
     Shared& S = shared();
     const int tid = threadIdx.x, parts = P.parts;
     const uint32_t n = uint32_t(P.top.top_n);
-    const Scale q{c, c_hi, c_lo};
+    const Scale q{c_hi, c_lo};
     if (tid < 2) S.count[at + tid] = 0;
     // all that the parts have left at once: the keys' places, two a thread (kCap at most), before their numbers are known (32 x 151936 bf16
     // in eight parts, n = 20: 16.5 us; one part after the other 17.5)
@@ -1034,7 +1038,7 @@ __device__ __noinline__ int join_parts(const TopParams& P, int64_t r, uint32_t a
     }
     for (int p = 0; p < parts; ++p) {
         Sums one{0.f, S.part_ref[p], S.part_s[p], S.part_t[p]};
-        move(one, st.ref, c);
+        move(one, st.ref, q);
         st.s += tid == 0 ? one.s : 0.f;
         st.t += tid == 0 ? one.t : 0.f;
     }
@@ -1072,7 +1076,7 @@ __device__ __noinline__ int join_parts(const TopParams& P, int64_t r, uint32_t a
         }
         if (count > uint32_t(kConsumers)) {
             S.state[tid] = make_float4(st.bar, st.ref, st.s, st.t);
-            from = cut_long<kEntropy>(from, count, n, n, c, c_hi, c_lo);
+            from = cut_long<kEntropy>(from, count, n, n, c_hi, c_lo);
             const float4 in = S.state[tid];
             st = Sums{in.x, in.y, in.z, in.w};
             count = n;
@@ -1172,14 +1176,15 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
         const RowJob h = job_of(row);
         const RowSpan span{row.head, row.count};
         const int first = int(part) * P.part_vecs, last = min(first + P.part_vecs, span.count);
-        const Scale scale{h.c, h.c_hi, h.c_lo};
+        const Scale scale{h.c_hi, h.c_lo};
+        const Two c = two(scale.nearest(), scale.nearest());
         Sums st{-pos_inf(), -kFloatMax, 0.f, 0.f};
         bool has_n = false;
         uint32_t worst = Peak<T>::none();  // NaN, or +inf, where the row has one
         uint32_t at = pair, count = 0;  // the list that is filled, and the keys in it
         uint32_t kept = 0;              // keys that the list had before the present counter of S.pushed was begun
         int cutting = -1, age = 0;      // the job that cuts the other one, which was filled before, and the chunks since
-        const Job job_of_row{kClose, 0, 0, 0, row.row, row.token, 0.f, 0.f, h.c, h.c_hi, h.c_lo, h.inv_t, h.inv_t_lo, h.x_t};
+        const Job job_of_row{kClose, 0, 0, 0, row.row, row.token, 0.f, 0.f, h.c_hi, h.c_lo, h.inv_t, h.inv_t_lo, h.x_t};
         // the row's lists are the ones of two rows ago
         const uint32_t gone = pair ? rows_of[1] : rows_of[0];
         failed = bar_any(gone != 0 && !wait(&S.closed[pair >> 1], (gone - 1) & 1u, P.wait_ns));
@@ -1256,7 +1261,7 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
                 to = kept + next_places(&S.pushed[counter], want);
                 top = to + want;
             }
-            add<T, kEntropy>(st, v, two(h.c, h.c));
+            add<T, kEntropy>(st, v, c);
             for (; above && to < kCap; ++to, above &= above - 1) {
                 const int bit = __ffs(above) - 1, i = bit / kPer * kConsumers + tid, j = bit % kPer;
                 S.list[at][to] = key_of(load_logit(reinterpret_cast<const T*>(ring + chunk.at) + i * kPer + j),
@@ -1309,10 +1314,10 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
                         for (uint32_t i = tid; i < count; i += kConsumers) S.list[full][left + i] = S.list[at][i];
                         count += left;
                     }
-                    move(st, key_value(least), h.c);
+                    move(st, key_value(least), scale);
                     if (tid == 0) {
                         Sums lost{0.f, S.cut_ref, S.cut_s, S.cut_t};
-                        move(lost, st.ref, h.c);
+                        move(lost, st.ref, scale);
                         st.s += lost.s;
                         st.t += lost.t;
                     }
@@ -1330,8 +1335,8 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
                     S.state[tid] = make_float4(bar_before, st.ref, st.s, st.t);
                     bar_sync();
                     at = over ? slow_chunk<T, kEntropy>(at, min(count, uint32_t(kCap)), chunk.at, base, last, chunk.head, chunk.end, n,
-                                                        h.c, h.c_hi, h.c_lo)
-                              : cut_long<kEntropy>(at, count, n, about, h.c, h.c_hi, h.c_lo);
+                                                        h.c_hi, h.c_lo)
+                              : cut_long<kEntropy>(at, count, n, about, h.c_hi, h.c_lo);
                     const float4 q = S.state[tid];
                     st = Sums{q.x, q.y, q.z, q.w};
                     count = S.count[at];
@@ -1390,7 +1395,7 @@ __global__ void __launch_bounds__(kThreads, 2) top_kernel(const __grid_constant_
                 t += S.sums[pair >> 1][w].y;
             }
             if (!leave(P, r, part, TopPart{st.ref, s, t, int(count), bad, 0})) continue;
-            const int joined = join_parts<kEntropy>(P, r, pair, h.c, h.c_hi, h.c_lo);
+            const int joined = join_parts<kEntropy>(P, r, pair, h.c_hi, h.c_lo);
             const float4 q = S.state[tid];
             st = Sums{q.x, q.y, q.z, q.w};
             count = uint32_t(max(joined, 0));
@@ -1674,6 +1679,8 @@ __global__ void __launch_bounds__(kShortWarps * 32, kShortResident) top_short_ke
         const uint32_t lo = first_bar<T>(largest_of<T>(peaks), n, top);
         Sums st{below(lo), value_of(lo), 0.f, 0.f};
         const uint32_t bar = packed_bar<T>(st.bar);
+        const float nearest = Scale{h.c_hi, h.c_lo}.nearest();
+        const Two c = two(nearest, nearest);
         for (int base = 0; base < span.count; base += 32 * kVecs) {
             uint4 v[kVecs];
             uint32_t above = 0;
@@ -1690,7 +1697,7 @@ __global__ void __launch_bounds__(kShortWarps * 32, kShortResident) top_short_ke
                     S.list[to] = key_of(load_logit(x + j), j);
                 }
             }
-            add<T, kEntropy>(st, v, two(h.c, h.c));
+            add<T, kEntropy>(st, v, c);
         }
         __syncwarp();
         uint32_t count = S.count;
@@ -1709,7 +1716,7 @@ __global__ void __launch_bounds__(kShortWarps * 32, kShortResident) top_short_ke
                 if (stays) {
                     S.list[count + __popc(lanes & ((1u << lane) - 1u))] = k;
                 } else {
-                    const float u = (y - st.ref) * h.c, f = exp2_fast(u);
+                    const float d = y - st.ref, u = fmaf(d, h.c_hi, d * h.c_lo), f = exp2_fast(u);
                     st.s += f;
                     if (kEntropy) st.t = fmaf(f, fmaxf(u, kLowest), st.t);
                 }

@@ -805,3 +805,39 @@ def test_top_rest_of_short_vocabularies(sampler, kind, V, n):
     x = _round(x, kind)
     got = _run_top(sampler, x, kind, n, V % 3, V % 5, entropy=False)
     _check_rest(got, x, n)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V,n", [(4000, 1), (4000, 64), (40000, 1), (40000, 64)])
+def test_top_errors_do_not_go_one_way(sampler, kind, V, n):
+    """The mean error of many logprobs at a temperature whose log2(e) / T, as the product of two rounded numbers, is off by
+    1.9 EPS. All exponents take the float that is nearest to it, so that the error in all of them is of rel * depth, with
+    rel that float's own (0.1 EPS here); ex2.approx and the logarithm are off by 1.5e-8 and 3e-8 the same way at most. What
+    is left is at random: the output's rounding (uniform, of EPS |logprob|) and the sums' own, by four standard errors."""
+    import torch
+
+    rows, T = 2048, np.float32(1.4400320053)
+    exact = np.log2(np.e) / float(T)
+    rel = abs(float(np.float32(exact)) / exact - 1)
+    assert abs(float(np.float32(np.log2(np.e)) * (np.float32(1) / T)) / exact - 1) > 1.5 * EPS and rel < 0.2 * EPS
+    gen = torch.Generator(device="cuda:0").manual_seed(V)
+    x = 0.5 * torch.randn((rows, V), generator=gen, device="cuda:0")
+    x[:, V // 2] = 8 * float(T)  # far above all others, which have most of the mass
+    x = x.to(torch.bfloat16) if kind == "bf16" else x
+    tokens = torch.randint(0, V, (rows,), generator=gen, device="cuda:0", dtype=torch.int32)
+    ids = torch.empty((rows, n), dtype=torch.int32, device="cuda:0")
+    lps, lp, rest = torch.empty((rows, n), device="cuda:0"), torch.empty(rows, device="cuda:0"), torch.empty(rows, device="cuda:0")
+    sampler.score_top(logits=x, top_n=n, out_top_ids=ids, out_top_logprobs=lps, out_rest_logprob=rest, tokens=tokens,
+                      out_logprob=lp, temperature=torch.full((rows,), float(T), device="cuda:0"))
+    z = torch.log_softmax(x.double() / float(T), 1)
+    depth = (z.exp() * (z.amax(1, keepdim=True) - z)).sum(1).mean().item()
+    one_way = rel * depth + 1.5e-8 + 3e-8
+    at_random = 4 / rows ** 0.5 * (EXP + 4 * np.sqrt(V / 32 + 64) * EPS / 32 ** 0.5)
+    for got, want in ((lp, z.gather(1, tokens.long()[:, None])[:, 0]), (lps[:, -1], z.gather(1, ids[:, -1:].long())[:, 0]),
+                      (rest, torch.logsumexp(z.scatter(1, ids.long(), -torch.inf), 1))):
+        mean = (got.double() - want).mean().item()
+        size = want.abs().mean().item() if got is lp else 0.0
+        # (the outputs other than the drawn tokens' are close together: their roundings may go one way)
+        step = 0.0 if got is lp else EPS * want.abs().max().item()
+        tol = one_way + step + at_random + 4 / rows ** 0.5 * EPS * size / 3 ** 0.5
+        assert abs(mean) <= tol, (mean, tol)

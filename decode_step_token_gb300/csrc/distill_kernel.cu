@@ -426,6 +426,7 @@ __global__ void __launch_bounds__(Shape<kWarps>::kThreads, Shape<kWarps>::kResid
         auto close = [&](const Open& o) {
             if (!wait(&S.join[taken.at], taken.phase, P.wait_ns)) return false;
             const RowJob h = job_of(o.item);
+            const Scale by{h.c_hi, h.c_lo};
             // outside the list, and inside
             const float4* in = sums + taken.at * parts * kWarps;
             Stats out = stats_empty();
@@ -433,13 +434,13 @@ __global__ void __launch_bounds__(Shape<kWarps>::kThreads, Shape<kWarps>::kResid
             out.ref = max_warp(out.ref);
             for (uint32_t i = lane; i < parts * kWarps; i += 32) {
                 Stats p{in[i].x, in[i].y, 0.f};
-                stats_move(p, out.ref, h.c);
+                stats_move(p, out.ref, by);
                 out.s += p.s;
             }
             ListSums mine{-kFloatMax, 0.f, {0.f, 0.f}, {0.f, 0.f}, 0, 0};
             if (uint32_t(lane) < parts) mine = lists[taken.at * parts + lane];
             Stats inside{mine.ref, mine.s, 0.f};
-            stats_move(inside, max_warp(mine.ref), h.c);
+            stats_move(inside, max_warp(mine.ref), by);
             float q_list = mine.q.hi;
 #pragma unroll
             for (int i = 16; i > 0; i >>= 1) {
@@ -571,7 +572,7 @@ __global__ void __launch_bounds__(Shape<kWarps>::kThreads, Shape<kWarps>::kResid
             const int n = min(first_vec + P.part_vecs, span.count) - first_vec;
             const int end = span.head + vocab;
             const Two c_hi = two(item.c_hi, item.c_hi), c_lo = two(item.c_lo, item.c_lo);
-            const float c = item.c;
+            const Scale by{item.c_hi, item.c_lo};
             if (!wait(&S.full[buf1.at], buf1.phase, P.wait_ns)) return -1;
             const uint4* in = reinterpret_cast<const uint4*>(smem + buf1.at * buffer_bytes);
             unsigned char* bits = maps + map1.at * map_bytes<kWarps>(P.part_vecs);
@@ -598,10 +599,10 @@ __global__ void __launch_bounds__(Shape<kWarps>::kThreads, Shape<kWarps>::kResid
                         if (b >> 8 * k & 0xffu) blend<T>(v[k], nothing<T>(), b >> 8 * k & 0xffu);
                     if (!kGrad) *marks = 0;
                 }
-                fold<T, false, kVecs>(st, bad, v, c_hi, c_lo, c);
+                fold<T, false, kVecs>(st, bad, v, c_hi, c_lo, by);
             }
             if (bad) st.s = quiet_nan();
-            stats_warp<false>(st, c);
+            stats_warp<false>(st, by);
             // (A buffer of sums is written again four rows later: by then every closer of the cluster is done with it, as
             // each puts a row's list sums after closing the row two before, and a warp puts a row's after that two before
             // is closed.)

@@ -69,6 +69,22 @@ __device__ __forceinline__ void stats_move(Stats& a, float ref, float c)
     a.ref = ref;
 }
 
+// log2(e) / T as a pair (of RowJob), and as the float that is nearest to it.
+struct Scale {
+    float c_hi, c_lo;
+    __device__ __forceinline__ float nearest() const { return __fadd_rn(c_hi, c_lo); }
+};
+
+// The same by the pair. (What moves is all that was added up before: an error in its exponent is one of all of that, the
+// same way each time, and RowJob's c is up to 1.9 units of 2^-24 off.)
+__device__ __forceinline__ void stats_move(Stats& a, float ref, const Scale& q)
+{
+    const float x = a.ref - ref, d = fmaxf(fmaf(x, q.c_hi, x * q.c_lo), kLowest), f = exp2_fast(d);
+    a.t = f * fmaf(a.s, d, a.t);
+    a.s *= f;
+    a.ref = ref;
+}
+
 // The largest of all lanes' values, in every lane.
 __device__ __forceinline__ float max_warp(float x)
 {
@@ -88,8 +104,8 @@ __device__ __forceinline__ void sum_warp(Stats& a)
 }
 
 // The statistics of all lanes' parts, in every lane (t where kEntropy).
-template <bool kEntropy>
-__device__ __forceinline__ void stats_warp(Stats& a, float c)
+template <bool kEntropy, typename C>
+__device__ __forceinline__ void stats_warp(Stats& a, const C& c)
 {
     stats_move(a, max_warp(a.ref), c);
     sum_warp<kEntropy>(a);

@@ -87,7 +87,8 @@ struct RowItem {
     int32_t token, bad_param;
     float weight, temperature;
     float x_t;     // the token's logit (0 without one)
-    float c, c_hi, c_lo, inv_t, inv_t_lo;  // as in RowJob
+    float c;                               // the float nearest to c_hi + c_lo
+    float c_hi, c_lo, inv_t, inv_t_lo;     // as in RowJob
     int32_t head, count;                   // of its span of vectors
 };
 
@@ -165,7 +166,7 @@ __device__ __forceinline__ bool queue_fill(RowQueue& S, const sampler_rows_t& a,
             h.token = item.token;
             row_scale(h, a, item.temperature);
             item.bad_param = h.bad_param;
-            item.c = h.c;
+            item.c = Scale{h.c_hi, h.c_lo}.nearest();
             item.c_hi = h.c_hi;
             item.c_lo = h.c_lo;
             item.inv_t = h.inv_t;

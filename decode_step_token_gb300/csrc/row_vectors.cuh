@@ -162,9 +162,9 @@ __device__ __forceinline__ float max_nan(float a, float b)
 }
 
 // Pass 1 over N vectors. The reference moves only when one holds a larger
-// element, which is rare after the first few.
-template <typename T, bool kEntropy, int N>
-__device__ __forceinline__ void fold(Stats& st, bool& bad, const uint4 (&v)[N], Two c_hi, Two c_lo, float c)
+// element, which is rare after the first few; c is what stats_move takes.
+template <typename T, bool kEntropy, int N, typename C>
+__device__ __forceinline__ void fold(Stats& st, bool& bad, const uint4 (&v)[N], Two c_hi, Two c_lo, const C& c)
 {
     constexpr int kPer = Elems<T>::kPer;
     float m = Elems<T>::largest(v[0]);

@@ -261,12 +261,6 @@ struct Sums {
     float s, t;
 };
 
-// log2(e) / T as a pair, and as the float that is nearest to it.
-struct Scale {
-    float c_hi, c_lo;
-    __device__ __forceinline__ float nearest() const { return __fadd_rn(c_hi, c_lo); }
-};
-
 // Add four vectors to the sums. (By log2(e) / T as one float, c, the nearest. The pair takes 6 % longer: 4096 x 128000
 // bf16, n = 64, 324 us for 306 with a cold L2. Mean errors of 2048 logprobs of rows of 128000 bf16 whose mass is 8 nats
 // below one token: 0.8e-7 at T = 1.44, where the product of rounded log2(e) and 1 / T, 1.9 units of 2^-24 off, had -7.4e-7;
@@ -297,14 +291,14 @@ __device__ __forceinline__ void add(Sums& st, const uint4 (&v)[kVecs], Two c)
     }
 }
 
-// The sums relative to a reference that is at least their own. (By the pair: what moves is all that was added up before,
-// and an error in its exponent is one of all of that, the same way each time.)
+// The sums relative to a reference that is at least their own.
 __device__ __forceinline__ void move(Sums& st, float ref, const Scale& q)
 {
-    const float x = st.ref - ref, d = fmaxf(fmaf(x, q.c_hi, x * q.c_lo), kLowest), f = exp2_fast(d);
-    st.t = f * fmaf(st.s, d, st.t);
-    st.s *= f;
-    st.ref = ref;
+    Stats a{st.ref, st.s, st.t};
+    stats_move(a, ref, q);
+    st.ref = a.ref;
+    st.s = a.s;
+    st.t = a.t;
 }
 
 // The sum of all consumers' counts; `turn` goes round the three tallies, of which the one that it starts from is 0.
@@ -665,7 +659,7 @@ __device__ __noinline__ float2 far_outside(const TopParams& P, int64_t r, uint64
     const uint4* from = reinterpret_cast<const uint4*>(x - span.head);
     const int lane = threadIdx.x & 31, end = span.head + int(a.vocab);
     const uint32_t none = Peak<T>::none(), bar = packed_bar<T>(below(uint32_t(least >> 32)));
-    const float c = Scale{c_hi, c_lo}.nearest();
+    const Scale q{c_hi, c_lo};
     Stats st = stats_empty();
     bool bad = false;
     for (int base = lane; base < span.count; base += 32 * kAhead) {
@@ -681,9 +675,9 @@ __device__ __noinline__ float2 far_outside(const TopParams& P, int64_t r, uint64
             if (at < span.head || at + kPer > end) Elems<T>::mask(v[k], span.head - at, end - at);
             take_above<T>(v[k], bar);
         }
-        fold<T, false, kAhead>(st, bad, v, two(c_hi, c_hi), two(c_lo, c_lo), c);
+        fold<T, false, kAhead>(st, bad, v, two(c_hi, c_hi), two(c_lo, c_lo), q);
     }
-    stats_warp<false>(st, c);
+    stats_warp<false>(st, q);
     return make_float2(st.ref, st.s);
 }
 

@@ -841,3 +841,43 @@ def test_top_errors_do_not_go_one_way(sampler, kind, V, n):
         step = 0.0 if got is lp else EPS * want.abs().max().item()
         tol = one_way + step + at_random + 4 / rows ** 0.5 * EPS * size / 3 ** 0.5
         assert abs(mean) <= tol, (mean, tol)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [4000, 40000])
+def test_distill_errors_do_not_go_one_way(sampler, kind, V):
+    """As above, of divergences, logprobs and (fp32) the gradient outside the lists, W p_v: the mean of its errors relative to
+    itself. A gradient's exponential has its own mean error, 5e-8 at most."""
+    import torch
+
+    rows, T, k = 1024, float(np.float32(1.4400320053)), 4
+    exact = np.log2(np.e) / T
+    rel = abs(float(np.float32(exact)) / exact - 1)
+    gen = torch.Generator(device="cuda:0").manual_seed(V)
+    x = 0.5 * torch.randn((rows, V), generator=gen, device="cuda:0")
+    x[:, -2] = 8 * T  # comes last, and is outside the lists
+    x = x.to(torch.bfloat16) if kind == "bf16" else x
+    ids = torch.rand((rows, V - 2), generator=gen, device="cuda:0").argsort(1)[:, :k].to(torch.int32)
+    tokens = torch.randint(0, V, (rows,), generator=gen, device="cuda:0", dtype=torch.int32)
+    l = torch.log(torch.rand((rows, k), generator=gen, device="cuda:0") / k)
+    kl, lp, loss = torch.empty(rows, device="cuda:0"), torch.empty(rows, device="cuda:0"), torch.empty(1, device="cuda:0")
+    grad = torch.empty_like(x)
+    sampler.distill_loss(logits=x, teacher_ids=ids, teacher_logprobs=l, tokens=tokens, out_loss=loss, out_kl=kl, out_logprob=lp,
+                         temperature=torch.full((rows,), T, device="cuda:0"), out_grad=grad)
+    z = torch.log_softmax(x.double() / T, 1)
+    q = torch.exp(l.double())
+    depth = (z.exp() * (z.amax(1, keepdim=True) - z)).sum(1).mean().item()
+    one_way = rel * depth + 1.5e-8 + 3e-8
+    at_random = 4 / rows ** 0.5 * (EXP + 4 * np.sqrt(V / 256 + 64) * EPS / 32 ** 0.5)
+    for got, want in ((lp, z.gather(1, tokens.long()[:, None])[:, 0]), (kl, (q * (l.double() - z.gather(1, ids.long()))).sum(1))):
+        mean, size = (got.double() - want).mean().item(), want.abs().mean().item()
+        tol = one_way * q.sum(1).max().item() + at_random + 4 / rows ** 0.5 * EPS * (size + 4) / 3 ** 0.5
+        assert abs(mean) <= tol, (mean, tol)
+    if kind == "f32":
+        want = z.exp() * q.sum(1, keepdim=True) / T
+        off = (grad.double() - want) / want
+        off.scatter_(1, ids.long(), 0.0)
+        # (the largest, alone of its kind, is not among them; an element's own roundings are at random)
+        mean, far = off[:, :-2].mean().item(), (z[:, -2:-1] - z[:, :-2]).mean().item()
+        tol = rel * far + one_way + 5e-8 + 4 * EPS + at_random
+        assert abs(mean) <= tol, (mean, tol)

@@ -230,17 +230,17 @@ __device__ __forceinline__ uint2 encode(const Raw<T>& x, uint32_t most, int g, u
         // (m / 2^g, exact where it is not far below the least scale, over 6)
         code = finite ? e4m3_code(quotient(__uint_as_float(most) * power(-g), 6.f, 1.f / 6.f)) : 0x7fu;
         const float unit = (finite ? e4m3_value(code) : 0.f) * power(g);
-        const uint32_t i = __float_as_uint(unit > 0.f ? reciprocal(unit) : 0.f), u = __float_as_uint(-unit);
-        const Two inv = two(i, i), less = two(u, u);
-        // as quotient(), two at a time
+        const uint32_t i = __float_as_uint(unit > 0.f ? -reciprocal(unit) : -0.f), u = __float_as_uint(unit);
+        const Two less = two(i, i), d = two(u, u);
+        // as quotient(), two at a time, and with the other sign: the remainder of -0 is 0, which the last step adds as -0
 #pragma unroll
         for (int j = 0; j < kPer / 2; ++j) {
-            const Two v = pair_at(x, j), y = times(v, inv);
-            q[j] = times_add(times_add(y, less, v), inv, y);
+            const Two v = pair_at(x, j), y = times(v, less);
+            q[j] = times_add(times_add(y, d, v), less, y);
         }
     }
-    const uint32_t keep = finite ? 0xffffffffu : 0u;
-    return make_uint2(codes8(q) & keep, codes8(q + 4) & keep);
+    const uint32_t keep = finite ? 0xffffffffu : 0u, sign = kBlock == 16 ? 0x88888888u : 0u;
+    return make_uint2((codes8(q) ^ sign) & keep, (codes8(q + 4) ^ sign) & keep);
 }
 
 // Store a chunk's codes: 8 bytes where they lie so, else the `bytes` that belong to the row.

@@ -506,3 +506,42 @@ def test_argument_checks(sampler):
                            out_scales=q["out_scales"], out_row_scale=q["out_row_scale"])
     with pytest.raises(ValueError):
         sampler.micro_rows(values=q["out_values"], scales=q["out_scales"], out=torch.empty((8, 98), device="cuda:0"))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [16, 32])
+def test_quantize_at_the_ends_of_the_types(sampler, block, kind):
+    """The largest and the smallest values and scales, and largest values on the borders between two scales."""
+    import torch
+
+    rng = np.random.default_rng(block)
+    cols, largest = 192, 3.3895314e38 if kind == "bf16" else 3.4028235e38
+    up = np.float32(2.0 ** -7 if kind == "bf16" else 2.0 ** -23)
+    x = np.zeros((140, cols), np.float32)
+    x[0], x[1] = largest, -largest
+    x[2] = (largest * rng.uniform(-1, 1, cols)).astype(np.float32)
+    x[3], x[4] = 1.1754944e-38, 1e-45 if kind == "f32" else 9.2e-41  # least normal, least subnormal
+    x[5] = (1e-38 * rng.standard_normal(cols)).astype(np.float32)
+    x[6] = (1e-42 * rng.standard_normal(cols)).astype(np.float32)
+    x[7] = np.where(rng.random(cols) < 0.5, 3e38, 1e-38)
+    x[8] = np.where(np.arange(cols) < 64, largest, 1.0)
+    x[9] = np.where(np.arange(cols) < 64, 2.0 ** -100, 2.0 ** -112)
+    x[10] = 2.0 ** -100 * (1 + up)
+    x[11, 5] = np.float32(2.0 ** -126)
+    for r in range(12, 140):  # a largest value on a border of the scales, and one step on either side
+        e = float(rng.integers(-120, 120))
+        m = np.float32((1.3125 if r % 2 else 1.5) * 2.0 ** e) * (1 + up * np.float32(r % 3 - 1))
+        x[r] = (float(m) * rng.choice([1.0, 0.5, 0.25, 0.125, 0.375, 0.625, 1 / 12], cols)).astype(np.float32)
+        x[r, r] = m
+    t = torch.from_numpy(x).to(torch.bfloat16 if kind == "bf16" else torch.float32)
+    got, scales, row_scale = _quantize(sampler, t.to("cuda:0"), block)
+    codes, want_scales, want_row, values = M.quantize(t.float().numpy(), block)
+    np.testing.assert_array_equal(row_scale.cpu().numpy(), want_row)
+    np.testing.assert_array_equal(scales.cpu().numpy(), want_scales)
+    np.testing.assert_array_equal(got.cpu().numpy(), codes)
+    for out_kind in (torch.bfloat16, torch.float32):
+        out = torch.empty((140, cols), dtype=out_kind, device="cuda:0")
+        sampler.micro_rows(values=got, scales=scales, row_scale=row_scale, block=block, out=out)
+        with np.errstate(over="ignore"):  # the largest may be rounded up to 2^128
+            want = torch.from_numpy(values.astype(np.float32)).to(out_kind)
+        np.testing.assert_array_equal(out.float().cpu().numpy(), want.float().numpy())

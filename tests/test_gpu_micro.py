@@ -545,3 +545,56 @@ def test_quantize_at_the_ends_of_the_types(sampler, block, kind):
         with np.errstate(over="ignore"):  # the largest may be rounded up to 2^128
             want = torch.from_numpy(values.astype(np.float32)).to(out_kind)
         np.testing.assert_array_equal(out.float().cpu().numpy(), want.float().numpy())
+
+
+@pytest.mark.parametrize("rows", [9, 100, 300])
+@pytest.mark.parametrize("far", [30, 60, 90])
+@pytest.mark.parametrize("block", [16, 32])
+def test_product_of_large_and_small_operands(sampler, rows, far, block):
+    """Hidden rows of the size of 2^far by a weight of the size of 2^-far, and the other way round."""
+    import torch
+
+    V, K = 1300, 320
+    rng = np.random.default_rng(far)
+    for sign in (1, -1):
+        hidden = (rng.standard_normal((rows, K)) * 2.0 ** (sign * far)).astype(np.float32)
+        weight = (rng.standard_normal((V, K)) * 2.0 ** (-sign * far)).astype(np.float32)
+        ops, exact = {}, {}
+        for name, src in (("hidden", hidden), ("weight", weight)):
+            ops[name], ops[name + "_scale"], ops[name + "_row_scale"] = _quantize(sampler, torch.from_numpy(src).cuda(), block)
+            exact[name] = M.quantize(src, block)[3]
+        out = torch.empty((rows, V), device="cuda:0")
+        sampler.lm_head_micro(**ops, hidden_dim=K, block=block, logits=out)
+        want, mag = M.head(exact["hidden"], exact["weight"])
+        _close(out.double().cpu().numpy(), want, mag, K, "f32")
+
+
+@pytest.mark.parametrize("rows,V,K,block,kind", [(64, 128000, 4096, 16, "bf16"), (1, 151936, 2048, 32, "bf16"),
+                                                 (32, 32000, 4096, 32, "bf16"), (64, 32000, 4096, 16, "f32"),
+                                                 (200, 50257, 768, 16, "bf16")])
+def test_a_decode_step_of_full_size(sampler, rows, V, K, block, kind):
+    """The chained step's logits, tokens and logprobs are those of the head and the sampler one after the other."""
+    import torch
+
+    gen = torch.Generator(device="cuda:0").manual_seed(V)
+    ops = dict(block=block)
+    for name, n, size in (("hidden", rows, 1.0), ("weight", V, K ** -0.5)):
+        src = (size * torch.randn((n, K), generator=gen, device="cuda:0")).to(torch.bfloat16)
+        ops[name], ops[name + "_scale"], ops[name + "_row_scale"] = _quantize(sampler, src, block)
+    dt = torch.bfloat16 if kind == "bf16" else torch.float32
+    temperature = torch.full((rows,), 0.7, device="cuda:0")
+    got = []
+    for chained in (False, True):
+        logits = torch.full((rows, V), float("nan"), dtype=dt, device="cuda:0")
+        token, lp = torch.empty(rows, dtype=torch.int32, device="cuda:0"), torch.empty(rows, device="cuda:0")
+        args = sampler.make_args(logits=logits, temperature=temperature, out_tokens=token, global_seed=11,
+                                 top_k=torch.full((rows,), 50, dtype=torch.int32, device="cuda:0"))
+        if chained:
+            sampler.lm_head_micro_sample_args(args, out_token_logprob=lp, **ops)
+        else:
+            sampler.lm_head_micro(**ops, logits=logits)
+            sampler.sample_ex_args(args, out_token_logprob=lp)
+        assert torch.isfinite(logits).all() and (token >= 0).all() and (token < V).all()
+        got.append((logits, token, lp))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)

@@ -291,11 +291,13 @@ __device__ __forceinline__ void add(Sums& st, const uint4 (&v)[kVecs], Two c)
     }
 }
 
-// The sums relative to a reference that is at least their own.
+// The sums relative to a higher reference; a lower one is not taken. (A list's keys may be below the reference: what came in
+// before a cut ended, and what parts leave that are far below another. A key that some of those reach may be, too, and sums
+// relative to it beyond all numbers.)
 __device__ __forceinline__ void move(Sums& st, float ref, const Scale& q)
 {
     Stats a{st.ref, st.s, st.t};
-    stats_move(a, ref, q);
+    stats_move(a, fmaxf(ref, st.ref), q);
     st.ref = a.ref;
     st.s = a.s;
     st.t = a.t;

@@ -881,3 +881,42 @@ def test_distill_errors_do_not_go_one_way(sampler, kind, V):
         mean, far = off[:, :-2].mean().item(), (z[:, -2:-1] - z[:, :-2]).mean().item()
         tol = rel * far + one_way + 5e-8 + 4 * EPS + at_random
         assert abs(mean) <= tol, (mean, tol)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V", [(1, 151936), (8, 151936), (30, 65000), (5, 262144), (12, 40000)])
+@pytest.mark.parametrize("n", [1, 20, 64, 100, 128])
+def test_top_parts_far_below_each_other(sampler, kind, rows, V, n):
+    """Stretches of a row that are forbidden by a large negative number, beside others at -inf and ordinary ones."""
+    rng = np.random.default_rng(V + n)
+    x = rng.standard_normal((rows, V))
+    for r in range(rows):
+        for low in rng.permutation([-30.0, -1e4, -1e30, -3.38e38, -np.inf, -np.inf]):
+            at, much = rng.integers(0, V), rng.integers(1, V // 3)
+            x[r, at:at + much] = low + (rng.standard_normal(len(x[r, at:at + much])) if low == -1e4 else 0)
+        x[r, V // 40 * (r % 40):V // 40 * (r % 40) + 200] = rng.standard_normal(200)
+    x = _round(x, kind)
+    T = rng.choice([0.02, 0.9, 1.0, 1.5], rows).astype(np.float32)
+    T[0] = 1.0
+    got = _run_top(sampler, x, kind, n, T=T, entropy=False)
+    in_range = T >= 1
+    _check_top({k: v[in_range] for k, v in got.items()}, x[in_range], n, T=T[in_range])
+    assert not np.isnan(got["logprobs"]).any() and not np.isnan(got["rest"]).any()
+    assert (got["logprobs"][:, 0] > -20).all()
+
+
+@pytest.mark.parametrize("n", [1, 20, 64, 128])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_top_lists_at_low_temperatures(sampler, kind, n):
+    """Keys that came in before a cut ended, thousands of powers of two below the new reference."""
+    rng = np.random.default_rng(n)
+    chunk = 8192 if kind == "bf16" else 4096
+    rows, V, kinds = 640, 9 * chunk, 24
+    x = np.concatenate([_lists_under_way(rng, kinds // 2, V, chunk, first, kind) for first in (5, 6)])
+    x[::2, 7 * chunk:] = _round(0.01 * rng.standard_normal(x[::2, 7 * chunk:].shape), kind)  # the cut's list is the last
+    x = x[np.arange(rows) * 7 % kinds]
+    T = np.float32([0.003, 0.01])[np.arange(rows) // kinds % 2]
+    got = _run_top(sampler, x, kind, n, T=T, entropy=False)
+    few = {k: v[:2 * kinds] for k, v in got.items()}
+    _check_top(few, x[:2 * kinds], n, T=T[:2 * kinds])
+    assert not any(np.isnan(v).any() for v in got.values())

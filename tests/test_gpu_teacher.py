@@ -920,3 +920,47 @@ def test_top_lists_at_low_temperatures(sampler, kind, n):
     few = {k: v[:2 * kinds] for k, v in got.items()}
     _check_top(few, x[:2 * kinds], n, T=T[:2 * kinds])
     assert not any(np.isnan(v).any() for v in got.values())
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V", [(1, 151936), (8, 151936), (40, 65000), (20, 262144), (30, 40000)])
+@pytest.mark.parametrize("n", [1, 20, 64, 100, 128])
+def test_top_most_parts_far_below(sampler, kind, rows, V, n):
+    """All that is not forbidden is in one stretch of the row; other parts leave full lists of large negative numbers."""
+    rng = np.random.default_rng(V + n)
+    x = np.full((rows, V), -np.inf)
+    for r in range(rows):
+        ends = np.sort(rng.integers(0, V, 5))
+        for low, a, b in zip(rng.permutation([-1e4, -1e4, -1e3, -1e30, -np.inf, -3.38e38]), np.append(0, ends), np.append(ends, V)):
+            x[r, a:b] = low + (rng.standard_normal(b - a) if low == -1e4 else 0)
+        much, at = rng.integers(n, V // 20), rng.integers(0, V)
+        x[r, at:at + much] = rng.standard_normal(len(x[r, at:at + much]))
+        x[r, rng.integers(0, V)] = 1.0
+    x = _round(x, kind)
+    got = _run_top(sampler, x, kind, n)
+    _check_top(got, x, n)
+    _check_rest(got, x, n)
+
+
+@pytest.mark.parametrize("n", [20, 64, 100])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_top_keys_below_the_reference(sampler, kind, n):
+    """While a list is cut more keys come than are cut at once, above the old bar and below what the cut leaves, at temperatures
+    by which they are thousands of powers of two below that."""
+    rng = np.random.default_rng(n)
+    chunk = 8192 if kind == "bf16" else 4096
+    rows, V, kinds = 320, 9 * chunk, 32
+    x = 0.01 * rng.standard_normal((kinds, V))
+    for r in range(kinds):
+        first = 5 + r % 2
+        lanes, second, third = rng.integers(n // 2, n), rng.integers(n + 60, n + 140), rng.integers(150, 250)
+        x[r, rng.permutation(chunk)[:3 * lanes]] = 2 + 0.1 * rng.random(3 * lanes)
+        x[r, first * chunk + rng.permutation(chunk)[:second]] = 6 + 3 * rng.random(second)
+        x[r, (first + 1) * chunk + rng.permutation(chunk)[:third]] = 2.5 + 3 * rng.random(third)
+    x = _round(x, kind)[np.arange(rows) % kinds]
+    T = np.float32([0.002, 0.01])[np.arange(rows) // kinds % 2]
+    got = _run_top(sampler, x, kind, n, T=T, entropy=False)
+    assert not any(np.isnan(v).any() for v in got.values())
+    few = {k: v[:2 * kinds] for k, v in got.items()}
+    _check_top(few, x[:2 * kinds], n, T=T[:2 * kinds])
+    _check_rest(few, x[:2 * kinds], n, T[:2 * kinds])

@@ -726,7 +726,7 @@ __device__ __forceinline__ void close_row(const TopParams& P, const uint64_t* so
             if (rest > 0.f) {
                 const Pair q = logprob_of(h, all, ref, ln_s), l = log_of(rest);
                 const Pair z = two_sum(q.hi, l.hi);
-                y = z.hi + (z.lo + (q.lo + l.lo + kExp2Short));
+                if (q.hi >= -kFloatMax) y = z.hi + (z.lo + (q.lo + l.lo + kExp2Short));  // (else below fp32's range)
             }
             P.top.out_rest_logprob[r] = y;
         }

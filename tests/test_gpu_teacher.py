@@ -746,6 +746,9 @@ def _check_rest(got, x, n, T=None):
             assert got["rest"][r] == -np.inf, (r, got["rest"][r])
             continue
         want, depth = O.log_sum(out), _depths(out)
+        if want < -3.4028236e38:  # below fp32's range
+            assert got["rest"][r] == -np.inf, (r, got["rest"][r])
+            continue
         gap = min(logp[ids].min() - out.max(), 60.0)  # a sum relative to the list's least: 84 powers of two below it at most
         far += logp[ids].min() - out.max() > 60
         tol = (_sum_error(np.exp(logp), _depths(logp), V) + _sum_error(np.exp(out - out.max()), depth, 8 * V) + 3 * EPS * gap
@@ -964,3 +967,22 @@ def test_top_keys_below_the_reference(sampler, kind, n):
     few = {k: v[:2 * kinds] for k, v in got.items()}
     _check_top(few, x[:2 * kinds], n, T=T[:2 * kinds])
     _check_rest(few, x[:2 * kinds], n, T[:2 * kinds])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V", [(20, 300), (20, 9000), (8, 151936), (400, 6000)])
+def test_top_rest_below_the_range(sampler, kind, rows, V):
+    """Tokens forbidden by the type's lowest value, at temperatures by which their logprobs are below fp32's range or not."""
+    rng = np.random.default_rng(V)
+    x = rng.standard_normal((rows, V))
+    x[:, 3 * V // 4:] = -3.3895314e38 if kind == "bf16" else -3.4028235e38
+    x[::2, V // 40:3 * V // 4] = -np.inf
+    x[::4, :V // 40] = x[0, -1]
+    x[::4, 1] = 2.0
+    x = _round(x, kind)
+    T = rng.choice([0.3, 0.99, 1.0, 1.1, 3.0], rows).astype(np.float32)
+    for n in (1, V // 40, 128):
+        if n <= 128:
+            got = _run_top(sampler, x, kind, n, V % 3, V % 5, T=T, entropy=False)
+            _check_rest(got, x, n, T)
+            assert not np.isnan(got["logprobs"]).any()

@@ -269,7 +269,7 @@ template <typename T, bool kEntropy>
 __device__ __forceinline__ void add(Sums& st, const uint4 (&v)[kVecs], Two c)
 {
     const Two ref = two(-st.ref, -st.ref);
-    Two s = two(st.s, 0.f), t = two(st.t, 0.f);
+    Two s = two(0.f, 0.f), t = s;
 #pragma unroll
     for (int k = 0; k < kVecs; ++k) {
         Two x[Elems<T>::kPer / 2];
@@ -282,12 +282,13 @@ __device__ __forceinline__ void add(Sums& st, const uint4 (&v)[kVecs], Two c)
             if (kEntropy) t = fma2(e, clamp2(u), t);
         }
     }
+    // (four vectors by themselves first: the roundings of long sums of equal terms go one way)
     float a, b;
     split(s, a, b);
-    st.s = a + b;
+    st.s += a + b;
     if (kEntropy) {
         split(t, a, b);
-        st.t = a + b;
+        st.t += a + b;
     }
 }
 
@@ -1703,6 +1704,7 @@ __global__ void __launch_bounds__(kShortWarps * 32, kShortResident) top_short_ke
             st = Sums{0.f, key_value(least), 0.f, 0.f};
             st.bar = st.ref;
             count = 0;
+            Pair s{0.f, 0.f}, t{0.f, 0.f};  // (one after the other: 440 a lane, alike where there are ties)
             for (int base = 0; base < vocab; base += 32) {
                 const int j = base + lane;
                 const float y = j < vocab ? load_logit(x + j) : -pos_inf();
@@ -1713,11 +1715,17 @@ __global__ void __launch_bounds__(kShortWarps * 32, kShortResident) top_short_ke
                     S.list[count + __popc(lanes & ((1u << lane) - 1u))] = k;
                 } else {
                     const float d = y - st.ref, u = fmaf(d, h.c_hi, d * h.c_lo), f = exp2_fast(u);
-                    st.s += f;
-                    if (kEntropy) st.t = fmaf(f, fmaxf(u, kLowest), st.t);
+                    const Pair p = two_sum(s.hi, f);
+                    s = Pair{p.hi, s.lo + p.lo};
+                    if (kEntropy) {
+                        const Pair w = two_sum(t.hi, f * fmaxf(u, kLowest));
+                        t = Pair{w.hi, t.lo + w.lo};
+                    }
                 }
                 count += uint32_t(__popc(lanes));
             }
+            st.s = s.hi + s.lo;
+            st.t = t.hi + t.lo;
         }
         ahead();
 #pragma unroll

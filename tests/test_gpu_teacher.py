@@ -986,3 +986,26 @@ def test_top_rest_below_the_range(sampler, kind, rows, V):
             got = _run_top(sampler, x, kind, n, V % 3, V % 5, T=T, entropy=False)
             _check_rest(got, x, n, T)
             assert not np.isnan(got["logprobs"]).any()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V", [(320, 14000), (40, 3000), (320, 60000), (3, 262144)])
+@pytest.mark.parametrize("entropy", [True, False])
+def test_top_sums_of_few_different_values(sampler, kind, rows, V, entropy):
+    """Sums whose terms are alike, so that their roundings are."""
+    rng = np.random.default_rng(V)
+    V = V if kind == "bf16" else V // 2
+    kinds = 24
+    x = rng.integers(0, rng.integers(2, 8, (kinds, 1)), (kinds, V)) * rng.choice([0.3, 0.5, 0.7], (kinds, 1))
+    x[:, V // 3] = rng.uniform(4, 9, kinds)
+    for r in range(0, kinds, 2):  # two values, of which more have the larger one than a list holds
+        x[r] = 0
+        x[r, rng.permutation(V)[:rng.integers(300, 1200)]] = rng.choice([2.0, 4.0, 6.0, 7.0])
+    x[::4], x[::4, :1024] = 0, 6.0
+    x = _round(x, kind)[np.arange(rows) % kinds]
+    T = rng.choice([0.7, 0.9, 1.3], rows).astype(np.float32)
+    T[::4] = 1.0
+    for n in (1, 20):
+        got = _run_top(sampler, x, kind, n, T=T, entropy=entropy)
+        some = np.arange(min(rows, 48))
+        _check_top({k: v[some] for k, v in got.items()}, x[some], n, T=T[some])

@@ -502,7 +502,10 @@ __global__ void __launch_bounds__(Shape<kWarps>::kThreads, Shape<kWarps>::kResid
                 Pair kl{0.f, 0.f};
                 if (mine.q.hi > 0.f) {
                     const Pair y = scaled(h, most, mine.ref), z = pair_add(ln_s, y);
-                    kl = pair_add(mine.a, pair_add(pair_times(mine.q.hi, z), Pair{mine.q.lo * z.hi, 0.f}));
+                    // (a part without a finite logit has its reference at the lowest float, and y may be infinite)
+                    kl = mine.a.hi < pos_inf() && z.hi < pos_inf()
+                             ? pair_add(mine.a, pair_add(pair_times(mine.q.hi, z), Pair{mine.q.lo * z.hi, 0.f}))
+                             : Pair{pos_inf(), 0.f};
                 }
                 pair_warp(kl);
                 if (q_out > 0.f) {

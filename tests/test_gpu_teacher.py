@@ -1009,3 +1009,25 @@ def test_top_sums_of_few_different_values(sampler, kind, rows, V, entropy):
         got = _run_top(sampler, x, kind, n, T=T, entropy=entropy)
         some = np.arange(min(rows, 48))
         _check_top({k: v[some] for k, v in got.items()}, x[some], n, T=T[some])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [2, 400, 9000, 60000, 200000])
+def test_distill_infinite_divergences(sampler, kind, V):
+    """Lists of which the student forbids all tokens of a part of the row, or all, at temperatures below 1 and above."""
+    k = min(10, V)
+    for coef in (0.0, 0.3):
+        b = Batch(V, 12, V, k, kind, coef=coef)
+        b.T = np.float32([0.7, 0.9, 0.99, 1.0, 1.5, 30.0] * 2)
+        b.tokens[:] = b.ids[:, 0] if V > 2 else V - 1
+        if V > 2:
+            b.tokens[:] = np.array([np.setdiff1d(np.arange(40), b.ids[r])[0] for r in range(12)])
+        for r in range(12):
+            some = b.ids[r] if r < 6 and V > 2 else b.ids[r, -1:]
+            some = some[some != b.tokens[r]]
+            b.x[r, some] = -np.inf
+            b.x[r, b.tokens[r]] = 1.0
+        b.run(sampler, scale=0.7).check()
+        want = O.distill(b.x, b.ids, b.l, b.rest, b.tokens, coef, b.T, b.weight)
+        if V > 2:
+            assert np.isinf(want["kl"]).all() and np.isinf(want["loss"])

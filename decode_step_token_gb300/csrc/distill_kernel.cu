@@ -731,8 +731,17 @@ int resident(Kernel kernel, cudaLaunchConfig_t cfg, int parts, int& known)
 //   1200 x 65000 bf16    2: 75   3: 98   4: 95
 //   800 x 100000 fp32    5 (two buffers): 157   6: 118   7: 141   8: 132
 //   800 x 151936 fp32    8 (two buffers): 266   10: 168   16: 262
+// Without gradient a row leaves its buffer after its first pass: two are enough, and a turn is about 1.6 us for one step of
+// the consumers', 2.1 for two and 2.6 for three. Of 77 shapes (64 to 4096 rows of 20000 to 262144, both types, 1 to 16 parts,
+// a cold L2) what that chooses is 0.2 % off the best on average and 6 at most; the turns with gradient were up to 65 % off.
+// us by parts:
+//   4096 x 40000 bf16    1 (two buffers): 90    2: 133   3: 166   4: 199
+//   4096 x 200000 bf16   5 (two buffers): 377   6: 442   7: 569   8: 549
+//   800 x 200000 fp32    9 (two buffers): 123   10: 133  11: 205  16: 203
+//   1200 x 128000 fp32   6 (two buffers): 121   7: 168   8: 143   9: 147
+//   64 x 151936 fp32     7: 25   9: 25   10: 23   16: 29
 template <int kWarps, typename Kernel>
-int parts_of(Kernel kernel, const cudaLaunchConfig_t& cfg, int64_t vecs, int64_t rows, int (&known)[kMaxParts])
+int parts_of(Kernel kernel, const cudaLaunchConfig_t& cfg, int64_t vecs, int64_t rows, bool grad, int (&known)[kMaxParts])
 {
     using S = Shape<kWarps>;
     int best = 0;
@@ -742,10 +751,12 @@ int parts_of(Kernel kernel, const cudaLaunchConfig_t& cfg, int64_t vecs, int64_t
         if (smem_of<kWarps>(part_vecs, 2, parts) > S::kSmem || (parts > 1 && part_vecs < 256)) continue;
         const int clusters = resident<kWarps>(kernel, cfg, parts, known[parts - 1]);
         if (clusters < 1) continue;
-        const double turn = smem_of<kWarps>(part_vecs, 3, parts) > S::kSmem ? 7.5
-                            : part_vecs <= S::kStep                         ? 2.2
-                            : part_vecs <= 2 * S::kStep                     ? 3.5
-                                                                            : 4.1;
+        const int steps = part_vecs <= S::kStep ? 1 : part_vecs <= 2 * S::kStep ? 2 : 3;
+        const double turn = !grad                                             ? steps == 1 ? 1.6 : steps == 2 ? 2.1 : 2.6
+                            : smem_of<kWarps>(part_vecs, 3, parts) > S::kSmem ? 7.5
+                            : steps == 1                                      ? 2.2
+                            : steps == 2                                      ? 3.5
+                                                                              : 4.1;
         const double time = turn * double((rows + clusters - 1) / clusters);
         if (best == 0 || time <= least) {
             best = parts;
@@ -778,7 +789,7 @@ int launch(DistillParams& p, int sms, DistillOccupancy* occ, cudaStream_t stream
         // short rows: one, or as many as give each SM a part where rows are few
         while (parts < kMaxParts && p.rows.n_rows * parts < sms && vecs / (2 * parts) >= 256) parts *= 2;
     } else {
-        parts = parts_of<kWarps>(kernel, cfg, vecs, p.rows.n_rows, known);
+        parts = parts_of<kWarps>(kernel, cfg, vecs, p.rows.n_rows, grad, known);
     }
     if (parts < 1) return SAMPLER_ERR_CUDA;
     const int clusters = resident<kWarps>(kernel, cfg, parts, known[parts - 1]);

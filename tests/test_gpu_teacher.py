@@ -1031,3 +1031,11 @@ def test_distill_infinite_divergences(sampler, kind, V):
         want = O.distill(b.x, b.ids, b.l, b.rest, b.tokens, coef, b.T, b.weight)
         if V > 2:
             assert np.isinf(want["kl"]).all() and np.isinf(want["loss"])
+
+
+@pytest.mark.parametrize("rows,V,kind", [(170, 40000, "bf16"), (60, 100001, "f32"), (40, 200000, "f32"), (90, 151937, "bf16"),
+                                         (60, 128000, "f32"), (400, 20011, "f32"), (30, 262144, "bf16")])
+def test_distill_without_gradient_on_clusters_of_all_sizes(sampler, rows, V, kind):
+    """Parts of up to three steps in two buffers, several rows for each cluster."""
+    b = Batch(V, rows, V, 30, kind, pad=V % 3, shift=V % 5, heat=True, kept=0.9, coef=0.1, short=0.3)
+    b.run(sampler, grad=False).check()

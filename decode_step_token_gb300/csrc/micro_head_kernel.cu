@@ -21,8 +21,9 @@
 //          an SM takes 38 KB a stage from L2 in place of 54 and five stages fit in
 //          place of three. The first CTA's barriers count the copies of both, its
 //          thread issues for both, and its commits arrive in both. 4096 x 128000 x 4096
-//          bf16: 632 us (6.8 PFLOP/s, 0.89 of four times the measured bf16 rate) against
-//          879 of many.
+//          bf16, codes and scales at random: 655 us (6.6 PFLOP/s, 0.86 of four times the
+//          measured bf16 rate) against 890 of many; with scales that are all alike 639
+//          and 886. Power has its share in that.
 // Of many rows one accumulator and the scales leave no room for a second: the epilogue
 // reads it into registers first and gives it back, and scales, rounds and stores
 // (through shared memory and the TMA engine) under the next tile's products.
@@ -148,7 +149,7 @@ __device__ __forceinline__ void commit(uint64_t* bar)
 
 // Arrives on a barrier of the pair's first CTA. What the arrival hands over is tensor memory that completed loads have
 // read, ordered by the tcgen05 fences on both sides; no memory that a thread wrote, for which it would have to release at
-// the cluster's scope (that waits for the warp's stores of logits: 720 us in place of 632).
+// the cluster's scope (that waits for the warp's stores of logits: 720 us in place of 632, scales that are all alike).
 __device__ __forceinline__ void arrive_first(uint64_t* bar)
 {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(dsmem_map(smem_addr(bar), 0)) : "memory");
@@ -537,17 +538,27 @@ uint32_t stage_bytes(Form form, int NT)
 //   64 x 128000 x 4096            55.4  58.6   58.6     the weight's bytes
 //   32 x 32000 x 4096             16.3  17.6   21.5
 //   64 x 32000 x 4096             17.6  14.6   19.2     125 wide tiles are one turn of the SMs, 250 narrow ones two
-//   128 x 48000 x 2048            19.2  16.3   19.1     (two turns against three: left to few, 15.5 to 16.4 at 64 rows)
+//   128 x 48000 x 2048            19.2  16.3   19.1     (two turns against three: left to few, 15.5 to 16.4 at 64 rows, and
+//                                                        24.6 to 24.6 at 128 where the weight comes from HBM)
 //   300 x 42000 x 1024                  17.5   19.4     little to multiply: a pair starts and ends later
 //   300 x 42000 x 2112                  27.8   28.3
 //   512 x 32000 x 4096                  43.0   36.0
 //   4096 x 128000 x 1024               331    253
-//   4096 x 128000 x 4096               879    632
+//   4096 x 128000 x 4096               890    655      (codes and scales at random)
+// With the weight from HBM (the clock's step is 2 us):
+//   128 x 128000 x 1024           36.9  26.6   30.8     four stages of K: the logits' stores of a narrow tile, by element,
+//   96 x 100000 x 1024            28.7  22.5   26.6      take longer than its products
+//   128 x 42000 x 1024            20.5  16.4   18.4
+//   64 x 128000 x 1024            28.7  24.6   28.7     (left to few)
+//   128 x 16000 x 1024            12.3  12.3   12.3
+//   128 x 128000 x 2048           41.1  41.0   45.1
+//   128 x 128000 x 4096           67.6  69.6   69.7
 Form form_of(int64_t rows, int64_t vocab, int64_t hidden, int sms)
 {
     const auto up = [](int64_t a, int64_t b) { return (a + b - 1) / b; };
     if (rows <= kFewRows) {
         const int64_t narrow = up(up(vocab, kBM), sms), wide = up(up(vocab, kWideN), sms);  // turns
+        if (rows > kFewRows / 2 && hidden <= 4 * kBK && narrow > 1) return kMany;
         return rows > 32 && 2 * wide <= narrow && narrow <= 4 ? kMany : kFew;
     }
     const int64_t turns = up(up(rows, 2 * kBM) * up(vocab, kWideN), sms / 2);

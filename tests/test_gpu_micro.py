@@ -598,3 +598,11 @@ def test_a_decode_step_of_full_size(sampler, rows, V, K, block, kind):
         got.append((logits, token, lp))
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("rows,V,K", [(65, 30001, 96), (90, 25000, 1000), (128, 19600, 1024), (100, 41003, 33), (128, 40000, 1025)])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [16, 32])
+def test_product_of_short_hidden_rows(sampler, rows, V, K, kind, block):
+    """65 to 128 rows, which short hidden dimensions take as wide tiles."""
+    test_product(sampler, rows, V, K, kind, block)

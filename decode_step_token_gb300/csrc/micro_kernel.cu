@@ -6,7 +6,8 @@
 // at most four digits, and a quotient is on the exact one's side of every tie
 // between codes. (A product with the rounded reciprocal would put many of the
 // quotients that are such a tie on a side: bf16 values over a scale of four digits
-// often are.)
+// often are. For bf16, not for fp32, a product with the reciprocal rounded up, rounded
+// towards 0, has every code right; not built.)
 //
 // A block's codes need the block's largest magnitude and, for blocks of 16, the
 // row's, so a row stays in registers: 16 neighbouring values in each thread, one

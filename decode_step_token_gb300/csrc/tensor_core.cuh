@@ -1,6 +1,7 @@
-// tensor_core.cuh -- what the LM heads on the fifth-generation tensor cores share:
-// TMA loads and stores of tiles, tensor memory, the operands' descriptors, and the
-// encoder of tensor maps.
+// tensor_core.cuh -- what the LM heads in 8 and 4 bits share: TMA loads and stores of
+// tiles, tensor memory, the operands' descriptors, and the encoder of tensor maps. (The
+// bf16 head has its own. The stores of a warp's logits are the 4-bit head's: the 8-bit
+// one writes the same steps out, as calling them spills registers of its fp32 form.)
 #pragma once
 
 #include <cuda.h>

@@ -21,16 +21,18 @@
 //   Chunks that overflow the list (rows that ascend, ties in the first chunks) are looked
 //   at again, an element of each thread at a time, and cut by bisection over keys.
 //   A row's end: the closer again, under the next row: the exact n, in order, their
-//   logprobs and the row's outputs.
+//   logprobs and the row's outputs, and a second look where the others' mass is too little
+//   for sums relative to the list.
 // Few rows are cut into parts, a CTA each, which leave their n keys and sums in the
 // workspace; the part that ends last joins them, parts in order. Short rows are a warp's
 // each, with a kernel of their own.
 //
-// Two CTAs an SM. 4096 x 128000 bf16, n = 64: 281 us, 0.49 of the copy rate; instructions
-// bound it (issue slots 0.56 busy, and where they are not, warps wait for the few of them
-// that have keys to put): 51000 of a warp a row, of which exponentials and sums are 14000,
-// loads, peaks and comparisons with the bar 19000, keys and cuts 15000. Tried besides: one
-// CTA of sixteen warps (425 us), four of four (339), two chunks for each step (292).
+// Two CTAs an SM. 4096 x 128000 bf16, n = 64: 281 us, 0.49 of the copy rate. What bounds it
+// is the barrier for each chunk, at which all warps wait for the few that have keys to put:
+// issue slots are 0.56 busy, warps 0.28 active. (51000 instructions of a warp a row, of which
+// exponentials and sums are 14000, loads, peaks and comparisons with the bar 19000, keys and
+// cuts 15000.) Tried besides: one CTA of sixteen warps (425 us), four of four (339), two
+// chunks for each step (292).
 #include <cuda_runtime.h>
 
 #include <algorithm>

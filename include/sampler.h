@@ -516,6 +516,8 @@ int sampler_score_top(sampler_t h, const sampler_rows_t* rows, const sampler_top
  * NULL (SAMPLER_ERR_UNSUPPORTED).
  * A token that has no mass in the student gets the gradient of its logprob's limit,
  * as in sampler_score_grad; where the loss is infinite for that, it is reported so.
+ * (So it is where a logprob is below fp32's range, as logits of the type's lowest value
+ * can make it at temperatures below 1.)
  */
 typedef struct {
     int32_t top_n;                  /* 1 .. SAMPLER_MAX_ALTERNATIVES */
@@ -650,7 +652,8 @@ int sampler_micro_rows(sampler_t h, const sampler_micro_rows_t* q, sampler_strea
 
 /* logits[i, v] = hidden_row_scale[i] * weight_row_scale[v] * sum_k (code * block scale of hidden[i, k])
  *                                                               * (code * block scale of weight[v, k])
- * for i < rows, v < vocab, in fp32 sums, rounded once to `dtype`. Both operands
+ * for i < rows, v < vocab, in fp32 sums (times the hidden row's scale, then the
+ * weight row's), rounded once to `dtype`. Both operands
  * 16-byte aligned with strides multiples of 16 bytes and >= ceil(hidden_dim / 2),
  * else SAMPLER_ERR_BAD_SHAPE; where hidden_dim is odd the upper four bits of a row's
  * last byte are 0. vocab is at most the handle's max_vocab. Waits and
